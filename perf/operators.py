@@ -14,11 +14,6 @@ import torch
 
 own = False
 
-if own:
-    import context_ring_attention_fwd_gb300 as pkg
-else:
-    pkg = None
-
 EPS = 1e-6
 THETA = 500000.0
 
@@ -358,6 +353,7 @@ def plain_decode(st):
 def run(st):
     case = st["case"]
     if own:
+        import context_ring_attention_fwd_gb300 as pkg
         rope = {"interleaved": case.get("pairs", False), "eps": EPS}
         if case["op"] == "rope":
             return pkg.qk_norm_rope(st["q"], st["k"], st["q_weight"], st["k_weight"],
