@@ -22,6 +22,8 @@ from ._binding import (  # noqa: F401
     cp_ring_attn_fwd_rank, cp_ring_attn_fwd_host, cp_ring_attn_fwd_host_workspace_bytes,
     cp_ring_attn_fwd_noalloc,
     cp_lse_finalize, cp_lse_merge, cp_ring_attn_bwd, cp_ring_attn_bwd_workspace_bytes,
+    cp_paged_append,
+    cp_qk_norm_rope, cp_qk_norm_rope_bwd, cp_qk_norm_rope_bwd_workspace_bytes,
     cp_ring_attn_fwd, cp_ring_attn_fwd_emulated,
     cp_ring_attn_fwd_f32, cp_ring_attn_fwd_fp8,
     cp_ring_emulated_workspace_bytes, cp_ring_schedule, cp_ring_schedule_device, cp_ring_step,
@@ -37,6 +39,8 @@ __all__ = [
     "cp_ring_attn_fwd_host", "cp_ring_attn_fwd_noalloc",
     "cp_fp8_quantize", "cp_ring_attn_fwd_fp8", "fp8_quantize_qkv", "ring_attn_fwd_fp8",
     "cp_ring_attn_bwd", "ring_attn_bwd",
+    "cp_qk_norm_rope", "cp_qk_norm_rope_bwd", "qk_norm_rope", "qk_norm_rope_bwd",
+    "cp_paged_append", "paged_append",
     "CpError", "lib",
 ]
 
@@ -172,3 +176,47 @@ def ring_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.
     docs = doc_offsets_tensor(doc_offsets, q.device)
     cp_ring_attn_bwd(q, k, v, out, lse, dout, dq, dk, dv, n_shards, causal, docs, None, stream)
     return dq, dk, dv
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight=None, k_weight=None,
+                 inv_freq=None, positions=None, eps: float = 1e-6, interleaved: bool = False,
+                 stream=None):
+    """Per-head RMS norm of q [B,S,Hq,d] and k [B,S,Hk,d] and their rotation,
+    ready for ring_attn_fwd: allocates and returns contiguous (q_out, k_out) of
+    the inputs' type.  q and k may be strided views; k None gives (q_out, None)."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    cp_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps, interleaved,
+                    stream)
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: torch.Tensor,
+                     k: Optional[torch.Tensor], q_weight=None, k_weight=None, inv_freq=None,
+                     positions=None, eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """The backward of qk_norm_rope for the gradients of its outputs (those of
+    ring_attn_bwd): allocates and returns (dq, dk, dq_weight, dk_weight), the
+    first two contiguous and of the inputs' type, the others fp32 [d]; None
+    where the operand is None."""
+    def like(t):
+        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    dq, dk, dqw = like(q), like(k), like(q_weight)
+    dkw = like(k_weight) if k is not None else None
+    cp_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, dq, dk, dqw,
+                        dkw, eps, interleaved, None, stream)
+    return dq, dk, dqw, dkw
+
+
+def paged_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                 k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                 cache_lens: torch.Tensor, new_lens=None, q_weight=None, k_weight=None,
+                 inv_freq=None, eps: float = 1e-6, interleaved: bool = False, k_descale=None,
+                 v_descale=None, q_out=None, stream=None):
+    """Append k, v [B,S,Hk,d] to the paged caches, k normed and rotated by its
+    position, and return q normed and rotated likewise (in q_out, allocated if
+    None; its rows behind a sequence's new tokens are not written)."""
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens, q_weight, k_weight,
+                    inv_freq, q_out, eps, interleaved, k_descale, v_descale, stream)
+    return q_out if q is not None else None

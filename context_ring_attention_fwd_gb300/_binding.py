@@ -21,13 +21,14 @@ STATUS_NAMES = {
     0: "CP_OK", -1: "CP_ERR_NULL", -2: "CP_ERR_SHAPE", -3: "CP_ERR_UNSUPPORTED",
     -4: "CP_ERR_ALIGN", -5: "CP_ERR_CUDA", -6: "CP_ERR_BUFFER", -7: "CP_ERR_DOC_OFFSETS",
     -8: "CP_ERR_TIMEOUT", -9: "CP_ERR_DEVICE", -10: "CP_ERR_SCRATCH",
+    -11: "CP_ERR_CACHE",
 }
 STATUS_CODES = {v: k for k, v in STATUS_NAMES.items()}
 
 _lib = None
 _lock = threading.Lock()
 
-_vp, _i, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+_vp, _i, _i64, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 _SIGS = {
     "cp_ring_attn_fwd": [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp],
     "cp_ring_attn_fwd_noalloc": [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp],
@@ -61,7 +62,23 @@ _SIGS = {
                               _vp],
     "cp_ring_attn_fwd_host_f32": [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp,
                                   _i64, _vp],
+    "cp_qk_norm_rope": [_vp, _vp, _vp, _vp, _vp, _vp, _f, _vp, _i, _i, _vp, _vp, _vp, _i, _i, _i,
+                        _i, _i, _i, _vp],
+    "cp_qk_norm_rope_bwd_workspace_bytes": [_i, _i, _i, _i, _i],
+    "cp_qk_norm_rope_bwd": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f, _vp, _i, _i, _vp, _vp, _vp,
+                            _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp],
+    "cp_paged_append": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f, _vp, _i, _i,
+                        _vp, _i, _i, _i, _vp],
 }
+
+
+class PagedCacheStruct(ctypes.Structure):
+    """cp_paged_cache of include/cpring.h."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_strides", _i64 * 3), ("v_strides", _i64 * 3),
+                ("k_descale", _vp), ("v_descale", _vp), ("page_table", _vp),
+                ("table_stride", _i64), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("d", ctypes.c_int32), ("elem_bytes", ctypes.c_int32)]
 
 
 class CpError(RuntimeError):
@@ -92,6 +109,7 @@ def lib() -> ctypes.CDLL:
                     fn.restype = None
                 elif name in ("cp_ring_emulated_workspace_bytes", "cp_ulysses_workspace_bytes",
                               "cp_ring_attn_bwd_workspace_bytes",
+                              "cp_qk_norm_rope_bwd_workspace_bytes",
                               "cp_ring_attn_fwd_host_workspace_bytes"):
                     fn.restype = _i64
                 else:
@@ -139,6 +157,57 @@ def doc_offsets_tensor(doc_offsets, device) -> Optional[torch.Tensor]:
     else:
         t = torch.tensor([int(x) for x in doc_offsets], dtype=torch.int32, device=device)
     return t.contiguous()
+
+
+def _operand(t, name: str, dtype: torch.dtype, device, shape=None) -> None:
+    """t has this type, device and shape, and its last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must live on {device}, got {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _dense(t, name: str, dtype: torch.dtype, device, shape=None) -> None:
+    _operand(t, name, dtype, device, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _cuda_device(t, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    return t.device
+
+
+def _steps(t):
+    """The three leading strides of [a, b, c, d], None when contiguous.  The
+    stride of a dimension of one entry is never used and passed as 0."""
+    if t is None or t.is_contiguous():
+        return None
+    return (_i64 * 3)(*[st if n > 1 else 0 for st, n in zip(t.stride()[:3], t.shape)])
+
+
+def _call_on(name: str, device: torch.device, stream, *args) -> None:
+    """Run a library call with `device` current, on `stream` or, if None, on
+    that device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        _check(name, fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(name, fn(*args, _stream(stream)))
 
 
 # --------------------------------------------------------------------- C ABI
@@ -478,3 +547,153 @@ def launch_counts():
     buf = (ctypes.c_int64 * 4)()
     lib().cp_launch_counts(buf)
     return tuple(buf)
+
+
+# ------------------------------------------------- norm, rotation, paged cache
+def _rows4(t, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError(f"{name} must be a tensor of four dimensions")
+    return t.shape
+
+
+def _rotation(inv_freq, positions, device, tokens):
+    """rot_dim, after checking the two operands of the rotation."""
+    if inv_freq is not None:
+        _dense(inv_freq, "inv_freq", torch.float32, device, (inv_freq.numel(),))
+    if positions is not None:
+        _dense(positions, "positions", torch.int32, device, tokens)
+    return 0 if inv_freq is None else 2 * inv_freq.numel()
+
+
+def _weight(w, name: str, d: int, device):
+    if w is not None:
+        _dense(w, name, torch.float32, device, (d,))
+
+
+def cp_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out,
+                    eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """Per-head RMS norm and rotation of q [B,S,Hq,d] and k [B,S,Hk,d] (bf16 or
+    fp32, strided views allowed; k None: q only) into the contiguous q_out and
+    k_out.  Weights fp32 [d] (None: not normed), inv_freq fp32 [rot_dim / 2]
+    (None: not rotated), positions int32 [B,S] (None: the token's index)."""
+    B, S, Hq, d = _rows4(q, "q")
+    dev, dt = _cuda_device(q, "q"), q.dtype
+    if dt not in (torch.bfloat16, torch.float32):
+        raise TypeError("q must be bf16 or fp32")
+    Hk = 0 if k is None else _rows4(k, "k")[2]
+    _operand(q, "q", dt, dev)
+    _dense(q_out, "q_out", dt, dev, (B, S, Hq, d))
+    if k is not None:
+        _operand(k, "k", dt, dev, (B, S, Hk, d))
+        _dense(k_out, "k_out", dt, dev, (B, S, Hk, d))
+    _weight(q_weight, "q_weight", d, dev)
+    _weight(k_weight, "k_weight", d, dev)
+    rot = _rotation(inv_freq, positions, dev, (B, S))
+    _call_on("cp_qk_norm_rope", dev, stream, _ptr(q), _steps(q), _ptr(k), _steps(k),
+             _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(inv_freq), rot,
+             int(bool(interleaved)), _ptr(positions), _ptr(q_out),
+             _ptr(k_out) if k is not None else None, B, S, Hq, Hk, d, int(dt == torch.bfloat16))
+
+
+def cp_qk_norm_rope_bwd_workspace_bytes(B: int, S: int, Hq: int, Hk: int, d: int) -> int:
+    return int(lib().cp_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hk, d))
+
+
+def cp_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, dq, dk,
+                        dq_weight, dk_weight, eps: float = 1e-6, interleaved: bool = False,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Backward of cp_qk_norm_rope: from dq_out, dk_out (contiguous) and the
+    forward's inputs, writes dq, dk (the inputs' type, strided views allowed)
+    and the weights' gradients (fp32 [d], or None).  workspace: a uint8 device
+    tensor (allocated here if None)."""
+    B, S, Hq, d = _rows4(q, "q")
+    dev, dt = _cuda_device(q, "q"), q.dtype
+    if dt not in (torch.bfloat16, torch.float32):
+        raise TypeError("q must be bf16 or fp32")
+    Hk = 0 if k is None else _rows4(k, "k")[2]
+    for x, H, names in ((q, Hq, ("q", "dq", "dq_out")), (k, Hk, ("k", "dk", "dk_out"))):
+        if x is None:
+            continue
+        grad, given = (dq, dq_out) if x is q else (dk, dk_out)
+        _operand(x, names[0], dt, dev, (B, S, H, d))
+        _operand(grad, names[1], dt, dev, (B, S, H, d))
+        _dense(given, names[2], dt, dev, (B, S, H, d))
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight"), (dq_weight, "dq_weight"),
+                 (dk_weight, "dk_weight")):
+        _weight(w, n, d, dev)
+    rot = _rotation(inv_freq, positions, dev, (B, S))
+    if workspace is None:
+        need = cp_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hk, d)
+        if need < 0:
+            raise CpError("cp_qk_norm_rope_bwd_workspace_bytes", STATUS_CODES["CP_ERR_SHAPE"])
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _dense(workspace, "workspace", torch.uint8, dev)
+    has_k = k is not None
+    _call_on("cp_qk_norm_rope_bwd", dev, stream, _ptr(dq_out), _ptr(dk_out) if has_k else None,
+             _ptr(q), _steps(q), _ptr(k), _steps(k), _ptr(q_weight), _ptr(k_weight), float(eps),
+             _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(positions), _ptr(dq), _steps(dq),
+             _ptr(dk) if has_k else None, _steps(dk) if has_k else None, _ptr(dq_weight),
+             _ptr(dk_weight), B, S, Hq, Hk, d, int(dt == torch.bfloat16), _ptr(workspace),
+             int(workspace.numel()))
+
+
+def _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, dev) -> PagedCacheStruct:
+    """The cp_paged_cache of caches [pages, page_size, Hk, d] (bf16, or uint8
+    E4M3 codes with fp32 [Hk] descales) and an int32 table [B, max_pages]."""
+    dt = k_cache.dtype if isinstance(k_cache, torch.Tensor) else None
+    if dt not in (torch.bfloat16, torch.uint8):
+        raise TypeError("k_cache must be bf16 or uint8 (E4M3 codes)")
+    n_pages, page_size, Hk, d = _rows4(k_cache, "k_cache")
+    _operand(k_cache, "k_cache", dt, dev)
+    _operand(v_cache, "v_cache", dt, dev, k_cache.shape)
+    _operand(page_table, "page_table", torch.int32, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must have two dimensions")
+    for t, n in ((k_descale, "k_descale"), (v_descale, "v_descale")):
+        if dt == torch.uint8:
+            _dense(t, n, torch.float32, dev, (Hk,))
+        elif t is not None:
+            raise ValueError(f"{n} goes with an E4M3 cache")
+    sizes = k_cache.shape[:3]
+    row = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+    e4m3 = dt == torch.uint8
+    return PagedCacheStruct(
+        k_cache.data_ptr(), v_cache.data_ptr(),
+        (_i64 * 3)(*[s if n > 1 else 0 for s, n in zip(k_cache.stride(), sizes)]),
+        (_i64 * 3)(*[s if n > 1 else 0 for s, n in zip(v_cache.stride(), sizes)]),
+        k_descale.data_ptr() if e4m3 else None, v_descale.data_ptr() if e4m3 else None,
+        page_table.data_ptr(), row, n_pages, page_size, page_table.shape[1], Hk, d,
+        1 if e4m3 else 2)
+
+
+def cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens, q_weight,
+                    k_weight, inv_freq, q_out, eps: float = 1e-6, interleaved: bool = False,
+                    k_descale=None, v_descale=None, stream=None) -> None:
+    """Norm, rotate and append k, v [B,S,Hk,d] bf16 (strided views allowed) to
+    the paged caches [pages, page_size, Hk, d] at positions cache_lens[b] + s
+    (int32 [B]), for s < new_lens[b] (int32 [B], None: all S); q [B,S,Hq,d]
+    (None: keys and values only) is normed and rotated into q_out."""
+    B, S, Hk, d = _rows4(k, "k")
+    dev = _cuda_device(k, "k")
+    cache = _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, dev)
+    if page_table.shape[0] != B:
+        raise ValueError(f"page_table must have {B} rows, got {page_table.shape[0]}")
+    bf16 = torch.bfloat16
+    shape = (B, S, cache.Hk, cache.d)
+    _operand(k, "k", bf16, dev, shape)
+    _operand(v, "v", bf16, dev, shape)
+    Hq = 0
+    if q is not None:
+        Hq = _rows4(q, "q")[2]
+        _operand(q, "q", bf16, dev, (B, S, Hq, d))
+        _dense(q_out, "q_out", bf16, dev, (B, S, Hq, d))
+    _dense(cache_lens, "cache_lens", torch.int32, dev, (B,))
+    if new_lens is not None:
+        _dense(new_lens, "new_lens", torch.int32, dev, (B,))
+    _weight(q_weight, "q_weight", d, dev)
+    _weight(k_weight, "k_weight", d, dev)
+    rot = _rotation(inv_freq, None, dev, None)
+    _call_on("cp_paged_append", dev, stream, ctypes.byref(cache), _ptr(q), _steps(q), _ptr(k),
+             _steps(k), _ptr(v), _steps(v), _ptr(cache_lens), _ptr(new_lens), _ptr(q_weight),
+             _ptr(k_weight), float(eps), _ptr(inv_freq), rot, int(bool(interleaved)),
+             _ptr(q_out) if q is not None else None, B, S, Hq)

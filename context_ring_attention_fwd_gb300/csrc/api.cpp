@@ -391,6 +391,7 @@ cp_status cp_get_last_status(cudaStream_t stream) {
     if (cudaMemcpy(word, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
       return CP_ERR_CUDA;
   }
+  if (bits & cpring::kErrCache) return CP_ERR_CACHE;
   if (bits & cpring::kErrScratch) return CP_ERR_SCRATCH;
   if (bits & cpring::kErrTimeout) return CP_ERR_TIMEOUT;
   if (bits & cpring::kErrDocOffsets) return CP_ERR_DOC_OFFSETS;
@@ -410,6 +411,7 @@ const char* cp_status_string(cp_status s) {
     case CP_ERR_TIMEOUT: return "device wait timed out";
     case CP_ERR_DEVICE: return "device is not sm_103";
     case CP_ERR_SCRATCH: return "more documents than the fixed scratch of cp_ring_attn_fwd_noalloc holds";
+    case CP_ERR_CACHE: return "page number or length outside the paged cache";
     default: return "unknown status";
   }
 }

@@ -130,6 +130,7 @@ struct TraceRange {
 constexpr int kErrDocOffsets = 1;
 constexpr int kErrTimeout = 2;
 constexpr int kErrScratch = 4;  // raised only by cp_ring_attn_fwd_noalloc
+constexpr int kErrCache = 8;    // a page number or length outside a paged cache
 int* device_error_word();   // device address for the current device, or null
 
 // Launchers: return cudaSuccess or the launch error.
@@ -163,6 +164,15 @@ cudaError_t launch_finalize_strided(const float* o_acc, const float* m_acc, cons
 // tensor-core launches skips one tile load, and the wait limit in ns.
 int test_fault_drop();
 unsigned long long test_wait_limit_ns();
+
+// Caller-given strides (three, in elements, of the dimensions before the
+// contiguous last one; null = contiguous): each a non-negative multiple of 16
+// bytes; and, for written tensors, that no two elements share an address
+// (n0 x n1 x n2 rows of d elements).
+bool strides_ok(const int64_t* strides, int elem_bytes);
+bool strides_distinct(const int64_t* strides, int n0, int n1, int n2, int d);
+// The checks every entry point on a paged cache shares.
+cp_status check_cache(const cp_paged_cache* c);
 
 // Host launch counters (index: 0 tcgen05 attention, 1 fp32 attention,
 // 2 merge/finalize, 3 doc scan).

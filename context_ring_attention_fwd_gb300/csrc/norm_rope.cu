@@ -1,0 +1,391 @@
+// Per-head RMS norm of queries and keys with the position rotation in the
+// same pass, and its backward.
+//
+//   forward   r = (mean x^2 + eps)^(-1/2),  y = R(p) (x r w)
+//   backward  g = R(p)^T dy,  u = x r,  dw = sum over rows of g u,
+//             dx = r (g w - u mean(g w u))
+// R(p) rotates pairs of a row by p * inv_freq (rope.cuh).  Everything between
+// the load and the one rounding at the store is fp32; r is recomputed in the
+// backward, which reads x anyway, so the forward saves nothing for it.
+//
+// Bound by HBM: a forward moves 2 d elements per row, a backward 3 d.  Work
+// units of a warp are kUnroll * (rows per warp) heads of one token: all of a
+// unit's rows are loaded before the first is used (kUnroll x 1 KB in flight
+// per warp; the backward twice that), and one token's angles serve them all.
+// Units of q come first, then those of k, so a warp changes its gain (and, in
+// the backward, hands over its sums for the gain's gradient) once.
+//
+// The gain's gradient: each lane sums its columns over its rows in registers,
+// the block's warps are added in shared memory, and a second kernel adds the
+// blocks' sums in block order: no atomics, so it is the same in every run.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "internal.h"
+#include "rope.cuh"
+
+namespace cpring {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxBlocks = 1024;  // most blocks of a backward: sizes its workspace
+
+struct Rows {        // one of q and k
+  const void* x;     // read: [B, S, H, d] with the strides below (elements)
+  const void* dy;    // backward: read, contiguous
+  void* y;           // written: the rows (contiguous) or dx (with the strides below)
+  long long xb, xs, xh;
+  long long yb, ys, yh;
+  const float* w;    // [d] or null: rows are not normed
+  int H;
+  int chunks;        // units per token
+};
+
+struct RopeParams {
+  Rows t[2];
+  const float* inv_freq;
+  const int32_t* positions;  // [B, S], or null: position = index in the sequence
+  float* partial;            // backward: [blocks][2][d]
+  int S, rot, interleaved;
+  int units_q, units;
+  float eps;
+};
+
+template <typename T, int D, int kUnroll, bool kBwd>
+__global__ void __launch_bounds__(kThreads)
+    qk_norm_rope_kernel(const RopeParams p) {
+  using Lay = RowLayout<T, D>;
+  constexpr int NP = Lay::kPairs;
+  constexpr int kUnitRows = kUnroll * Lay::kRows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = lane % Lay::kLanes, g = lane / Lay::kLanes;
+  __shared__ float sums[kBwd ? 2 * kWarps * D : 1];
+
+  int lo, hi;
+  bool turned;
+  lane_columns<NP>(l, p.rot, p.interleaved != 0, lo, hi, turned);
+  uint64_t frac[Lay::kAngles];
+  load_fractions<Lay>(p.inv_freq, l, g, turned, frac);
+  float w[2 * NP], dw[2 * NP];
+#pragma unroll
+  for (int i = 0; i < 2 * NP; ++i) dw[i] = 0.f;
+
+  // Hand the sums for tensor `ti`'s gain to the block (its warp's own slot).
+  auto flush = [&](int ti) {
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) {
+      float v = dw[i];
+#pragma unroll
+      for (int o = Lay::kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (g == 0) sums[(ti * kWarps + warp) * D + (i < NP ? lo + i : hi + i - NP)] = v;
+      dw[i] = 0.f;
+    }
+  };
+
+  int cur = -1;
+  const unsigned stride = gridDim.x * kWarps;  // unsigned: the last step may pass 2^31
+  for (unsigned u = blockIdx.x * kWarps + warp; u < static_cast<unsigned>(p.units); u += stride) {
+    const int ti = u >= static_cast<unsigned>(p.units_q);
+    const Rows& t = p.t[ti];
+    const T* const xin = static_cast<const T*>(t.x);
+    const int local = static_cast<int>(u) - (ti ? p.units_q : 0);
+    const int tok = local / t.chunks;
+    const int h0 = (local - tok * t.chunks) * kUnitRows + g;
+    const int b = tok / p.S, s = tok - b * p.S;
+    uint4 raw[kUnroll][2], rawg[kBwd ? kUnroll : 1][2];
+    const T* const xrow = xin + b * t.xb + s * t.xs;
+    const long long flat = static_cast<long long>(tok) * t.H * D;  // contiguous [B, S, H, d]
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int h = h0 + i * Lay::kRows;
+      raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (kBwd) rawg[i][0] = rawg[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (h < t.H) {
+        const T* const src = xrow + h * t.xh;
+        raw[i][0] = *reinterpret_cast<const uint4*>(src + lo);
+        raw[i][1] = *reinterpret_cast<const uint4*>(src + hi);
+        if (kBwd) {
+          const T* const dy = static_cast<const T*>(t.dy) + flat + static_cast<long long>(h) * D;
+          rawg[i][0] = *reinterpret_cast<const uint4*>(dy + lo);
+          rawg[i][1] = *reinterpret_cast<const uint4*>(dy + hi);
+        }
+      }
+    }
+    if (ti != cur) {
+      if (kBwd && cur >= 0) flush(cur);
+      cur = ti;
+      if (t.w != nullptr) load_columns<NP>(t.w, lo, hi, w);
+    }
+    float c[NP], sn[NP];
+    if (p.rot > 0) row_angles<Lay>(p.positions ? __ldg(p.positions + tok) : s, frac, l, c, sn);
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int h = h0 + i * Lay::kRows;
+      if (h - g >= t.H) break;  // the same for the whole warp
+      float z[2 * NP];
+      unpack(raw[i][0], z, 0, T());
+      unpack(raw[i][1], z, NP, T());
+      if (!kBwd) {
+        if (t.w != nullptr) {
+          const float r = rsqrtf(row_sum<Lay::kLanes>(sum_squares(z)) * (1.f / D) + p.eps);
+#pragma unroll
+          for (int e = 0; e < 2 * NP; ++e) z[e] = z[e] * r * w[e];
+        }
+        if (turned) rotate<NP>(z, c, sn, p.interleaved != 0, 1.f);
+        if (h < t.H) {
+          T* const dst = static_cast<T*>(t.y) + flat + static_cast<long long>(h) * D;
+          *reinterpret_cast<uint4*>(dst + lo) = repack(z, 0, T());
+          *reinterpret_cast<uint4*>(dst + hi) = repack(z, NP, T());
+        }
+      } else {
+        float gr[2 * NP];
+        unpack(rawg[i][0], gr, 0, T());
+        unpack(rawg[i][1], gr, NP, T());
+        if (turned) rotate<NP>(gr, c, sn, p.interleaved != 0, -1.f);
+        if (t.w != nullptr) {
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < 2 * NP; ++e) dot = fmaf(gr[e] * w[e], z[e], dot);
+          const float r = rsqrtf(row_sum<Lay::kLanes>(sum_squares(z)) * (1.f / D) + p.eps);
+          const float m = row_sum<Lay::kLanes>(dot) * r * (1.f / D);
+          if (h < t.H) {
+#pragma unroll
+            for (int e = 0; e < 2 * NP; ++e) {
+              const float un = z[e] * r;
+              dw[e] = fmaf(gr[e], un, dw[e]);
+              gr[e] = r * (gr[e] * w[e] - un * m);
+            }
+          }
+        }
+        if (h < t.H) {
+          T* const dst = static_cast<T*>(t.y) + b * t.yb + s * t.ys + h * t.yh;
+          *reinterpret_cast<uint4*>(dst + lo) = repack(gr, 0, T());
+          *reinterpret_cast<uint4*>(dst + hi) = repack(gr, NP, T());
+        }
+      }
+    }
+  }
+  if (kBwd) {
+    // A warp writes the slots of tensors that it had no unit of as zeros.
+    for (int ti = 0; ti < 2; ++ti)
+      if (ti != cur && !(ti == 0 && cur == 1 && blockIdx.x * kWarps + warp < p.units_q))
+        for (int i = lane; i < D; i += 32) sums[(ti * kWarps + warp) * D + i] = 0.f;
+    if (cur >= 0) flush(cur);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+      const float* at = sums + (i / D) * kWarps * D + i % D;
+      float v = 0.f;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) v += at[x * D];
+      p.partial[static_cast<size_t>(blockIdx.x) * 2 * D + i] = v;
+    }
+  }
+}
+
+// dw[tensor][column] = sum over blocks, 32 columns a block of this kernel,
+// 32 threads a column; the order is fixed by the block count alone.
+__global__ void __launch_bounds__(1024)
+    gain_grad_kernel(const float* __restrict__ partial, int blocks, int d, float* dqw,
+                     float* dkw) {
+  __shared__ float part[32][33];
+  cudaGridDependencySynchronize();
+  const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 d
+  float v = 0.f;
+  for (int b = threadIdx.y; b < blocks; b += 32) v += partial[static_cast<size_t>(b) * 2 * d + col];
+  part[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y != 0) return;
+  v = 0.f;
+#pragma unroll
+  for (int y = 0; y < 32; ++y) v += part[y][threadIdx.x];
+  float* const out = col < d ? dqw : dkw;
+  if (out != nullptr) out[col < d ? col : col - d] = v;
+}
+
+template <typename T, int D, int kUnroll, bool kBwd>
+cudaError_t launch_rows(RopeParams p, int tokens, float* dqw, float* dkw, cudaStream_t stream) {
+  constexpr int kUnitRows = kUnroll * RowLayout<T, D>::kRows;
+  for (Rows& t : p.t) t.chunks = (t.H + kUnitRows - 1) / kUnitRows;
+  p.units_q = tokens * p.t[0].chunks;
+  p.units = p.units_q + tokens * p.t[1].chunks;
+  const int want = (p.units + kWarps - 1) / kWarps;
+  const int blocks = std::min(want, std::min(kMaxBlocks, sm_count() * (kBwd ? 2 : 3)));
+  qk_norm_rope_kernel<T, D, kUnroll, kBwd><<<blocks, kThreads, 0, stream>>>(p);
+  count_launch(2);
+  if (!kBwd || (!dqw && !dkw)) return cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * D / 32);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, gain_grad_kernel, static_cast<const float*>(p.partial), blocks, D,
+                         dqw, dkw);
+  count_launch(2);
+  return e;
+}
+
+// Heads per unit: as many as keep enough bytes in flight per warp, fewer when
+// the call is too small to give every warp of the grid such a unit.
+template <typename T, int D, bool kBwd>
+cudaError_t launch_sized(const RopeParams& p, int tokens, float* dqw, float* dkw,
+                         cudaStream_t stream) {
+  constexpr int kWide = kBwd ? 2 : 4;
+  const long long rows = static_cast<long long>(tokens) * (p.t[0].H + p.t[1].H);
+  const long long wide_units = rows / (kWide * RowLayout<T, D>::kRows);
+  if (wide_units >= 2LL * sm_count() * kWarps)
+    return launch_rows<T, D, kWide, kBwd>(p, tokens, dqw, dkw, stream);
+  return launch_rows<T, D, 1, kBwd>(p, tokens, dqw, dkw, stream);
+}
+
+template <bool kBwd>
+cudaError_t launch_any(const RopeParams& p, int tokens, int d, bool bf16, float* dqw, float* dkw,
+                       cudaStream_t stream) {
+  if (bf16)
+    return d == 128 ? launch_sized<__nv_bfloat16, 128, kBwd>(p, tokens, dqw, dkw, stream)
+                    : launch_sized<__nv_bfloat16, 64, kBwd>(p, tokens, dqw, dkw, stream);
+  return d == 128 ? launch_sized<float, 128, kBwd>(p, tokens, dqw, dkw, stream)
+                  : launch_sized<float, 64, kBwd>(p, tokens, dqw, dkw, stream);
+}
+
+// Strides of a [B, S, H, d] operand: the caller's, or contiguous.
+void set_strides(const int64_t* given, int S, int H, int d, long long& b, long long& s,
+                 long long& h) {
+  b = given ? given[0] : static_cast<long long>(S) * H * d;
+  s = given ? given[1] : static_cast<long long>(H) * d;
+  h = given ? given[2] : d;
+}
+
+cp_status check_rows(const void* q, const void* k, int B, int S, int Hq, int Hk, int d,
+                     const float* inv_freq, int rot_dim, int interleaved, float eps, int is_bf16) {
+  if (!q || (Hk > 0 && !k) || (rot_dim > 0 && !inv_freq)) return CP_ERR_NULL;
+  if (B < 1 || S < 1 || Hq < 1 || Hk < 0) return CP_ERR_SHAPE;
+  // every row's index, and so every unit's, is an int
+  if (static_cast<long long>(Hq) + Hk > 0x7fffffff ||
+      static_cast<long long>(B) * S > 0x7fffffff / (static_cast<long long>(Hq) + Hk))
+    return CP_ERR_SHAPE;
+  if (d != 64 && d != 128) return CP_ERR_UNSUPPORTED;
+  if (rot_dim < 0 || rot_dim > d) return CP_ERR_SHAPE;
+  if (rot_dim % 16 != 0) return CP_ERR_UNSUPPORTED;
+  if ((interleaved != 0 && interleaved != 1) || (is_bf16 != 0 && is_bf16 != 1))
+    return CP_ERR_SHAPE;
+  if (!(eps >= 0.f) || eps > 3.4e38f) return CP_ERR_SHAPE;
+  return CP_OK;
+}
+
+cp_status check_written(const void* y, const int64_t* ys, int B, int S, int H, int d, int esz) {
+  if (!strides_ok(ys, esz)) return CP_ERR_ALIGN;
+  return strides_distinct(ys, B, S, H, d) ? CP_OK : CP_ERR_SHAPE;
+}
+
+}  // namespace
+
+bool strides_ok(const int64_t* st, int elem_bytes) {
+  if (!st) return true;
+  for (int i = 0; i < 3; ++i)
+    if (st[i] < 0 || st[i] > (1LL << 40) || (st[i] * elem_bytes) % 16 != 0) return false;
+  return true;
+}
+
+bool strides_distinct(const int64_t* st, int n0, int n1, int n2, int d) {
+  if (!st) return true;
+  struct Dim { int64_t stride, n; } dim[3] = {{st[0], n0}, {st[1], n1}, {st[2], n2}};
+  std::sort(dim, dim + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  int64_t extent = d;
+  for (const Dim& x : dim) {
+    if (x.n <= 1) continue;
+    if (x.stride < extent) return false;
+    extent += x.stride * (x.n - 1);
+  }
+  return true;
+}
+
+}  // namespace cpring
+
+extern "C" {
+
+cp_status cp_qk_norm_rope(const void* q, const int64_t* q_strides, const void* k,
+                          const int64_t* k_strides, const float* q_weight, const float* k_weight,
+                          float eps, const float* inv_freq, int rot_dim, int interleaved,
+                          const int32_t* positions, void* q_out, void* k_out, int B, int S,
+                          int Hq, int Hk, int d, int is_bf16, cudaStream_t stream) {
+  cpring::TraceRange trace_("cp_qk_norm_rope");
+  using namespace cpring;
+  cp_status st = check_rows(q, k, B, S, Hq, Hk, d, inv_freq, rot_dim, interleaved, eps, is_bf16);
+  if (st != CP_OK) return st;
+  if (!q_out || (Hk > 0 && !k_out)) return CP_ERR_NULL;
+  const int esz = is_bf16 ? 2 : 4;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+      !aligned(q_weight, 4) || !aligned(k_weight, 4) || !aligned(inv_freq, 4) ||
+      !aligned(positions, 4) || !strides_ok(q_strides, esz) || !strides_ok(k_strides, esz))
+    return CP_ERR_ALIGN;
+  if (device_cc() != 103) return CP_ERR_DEVICE;
+  RopeParams p{};
+  p.t[0].x = q; p.t[0].y = q_out; p.t[0].w = q_weight; p.t[0].H = Hq;
+  p.t[1].x = k; p.t[1].y = k_out; p.t[1].w = k_weight; p.t[1].H = Hk;
+  set_strides(q_strides, S, Hq, d, p.t[0].xb, p.t[0].xs, p.t[0].xh);
+  set_strides(k_strides, S, Hk, d, p.t[1].xb, p.t[1].xs, p.t[1].xh);
+  p.inv_freq = inv_freq; p.positions = positions;
+  p.S = S; p.rot = rot_dim; p.interleaved = interleaved; p.eps = eps;
+  return launch_any<false>(p, B * S, d, is_bf16 != 0, nullptr, nullptr, stream) == cudaSuccess
+             ? CP_OK
+             : CP_ERR_CUDA;
+}
+
+int64_t cp_qk_norm_rope_bwd_workspace_bytes(int B, int S, int Hq, int Hk, int d) {
+  if (B < 1 || S < 1 || Hq < 1 || Hk < 0 || (d != 64 && d != 128)) return -1;
+  return static_cast<int64_t>(cpring::kMaxBlocks) * 2 * d * 4;
+}
+
+cp_status cp_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
+                              const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                              const float* q_weight, const float* k_weight, float eps,
+                              const float* inv_freq, int rot_dim, int interleaved,
+                              const int32_t* positions, void* dq, const int64_t* dq_strides,
+                              void* dk, const int64_t* dk_strides, float* dq_weight,
+                              float* dk_weight, int B, int S, int Hq, int Hk, int d, int is_bf16,
+                              void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
+  cpring::TraceRange trace_("cp_qk_norm_rope_bwd");
+  using namespace cpring;
+  cp_status st = check_rows(q, k, B, S, Hq, Hk, d, inv_freq, rot_dim, interleaved, eps, is_bf16);
+  if (st != CP_OK) return st;
+  if (!dq_out || !dq || !workspace || (Hk > 0 && (!dk_out || !dk))) return CP_ERR_NULL;
+  if ((dq_weight && !q_weight) || (dk_weight && !k_weight)) return CP_ERR_NULL;
+  const int esz = is_bf16 ? 2 : 4;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(dq_out, 16) || !aligned(dk_out, 16) ||
+      !aligned(dq, 16) || !aligned(dk, 16) || !aligned(q_weight, 4) || !aligned(k_weight, 4) ||
+      !aligned(dq_weight, 4) || !aligned(dk_weight, 4) || !aligned(inv_freq, 4) ||
+      !aligned(positions, 4) || !aligned(workspace, 16) || !strides_ok(q_strides, esz) ||
+      !strides_ok(k_strides, esz))
+    return CP_ERR_ALIGN;
+  st = check_written(dq, dq_strides, B, S, Hq, d, esz);
+  if (st == CP_OK && Hk > 0) st = check_written(dk, dk_strides, B, S, Hk, d, esz);
+  if (st != CP_OK) return st;
+  if (workspace_bytes < cp_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hk, d))
+    return CP_ERR_BUFFER;
+  if (device_cc() != 103) return CP_ERR_DEVICE;
+  RopeParams p{};
+  p.t[0].x = q; p.t[0].dy = dq_out; p.t[0].y = dq; p.t[0].w = q_weight; p.t[0].H = Hq;
+  p.t[1].x = k; p.t[1].dy = dk_out; p.t[1].y = dk; p.t[1].w = k_weight; p.t[1].H = Hk;
+  set_strides(q_strides, S, Hq, d, p.t[0].xb, p.t[0].xs, p.t[0].xh);
+  set_strides(k_strides, S, Hk, d, p.t[1].xb, p.t[1].xs, p.t[1].xh);
+  set_strides(dq_strides, S, Hq, d, p.t[0].yb, p.t[0].ys, p.t[0].yh);
+  set_strides(dk_strides, S, Hk, d, p.t[1].yb, p.t[1].ys, p.t[1].yh);
+  p.inv_freq = inv_freq; p.positions = positions;
+  p.partial = static_cast<float*>(workspace);
+  p.S = S; p.rot = rot_dim; p.interleaved = interleaved; p.eps = eps;
+  return launch_any<true>(p, B * S, d, is_bf16 != 0, dq_weight, dk_weight, stream) == cudaSuccess
+             ? CP_OK
+             : CP_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -46,8 +46,9 @@
  *              violation returns a negative cp_status and launches nothing.
  *              Faults found on the device (malformed doc_offsets, a wait
  *              that ran out) set a sticky device error word; the call that
- *              found them writes none of its outputs, and the error is
- *              reported by cp_get_last_status.
+ *              found them writes none of its outputs (the calls on a paged
+ *              cache: what each says), and the error is reported by
+ *              cp_get_last_status.
  *  Pointers    q/k/v/out/o_part: 16-byte aligned; lse/m/l: 4-byte aligned.
  */
 #ifndef CPRING_H
@@ -73,8 +74,10 @@ enum {
   CP_ERR_DOC_OFFSETS = -7,  /* doc_offsets not 0 < ... < S terminated by S      */
   CP_ERR_TIMEOUT = -8,      /* a bounded device wait ran out; outputs invalid   */
   CP_ERR_DEVICE = -9,       /* current device is not an sm_103 GPU              */
-  CP_ERR_SCRATCH = -10      /* problem too large for the fixed scratch of       */
+  CP_ERR_SCRATCH = -10,     /* problem too large for the fixed scratch of       */
                             /* cp_ring_attn_fwd_noalloc (more than 65,535 docs) */
+  CP_ERR_CACHE = -11        /* a page number or a length is outside the paged   */
+                            /* cache (found on the device)                      */
 };
 
 /*
@@ -299,8 +302,9 @@ cp_status cp_ring_traffic(int64_t B, int64_t S, int64_t H, int64_t d, int dtype_
 
 /*
  * Synchronise `stream`, then read and clear the sticky device error word of
- * the current device: CP_OK, CP_ERR_DOC_OFFSETS, CP_ERR_TIMEOUT or
- * CP_ERR_SCRATCH (the lowest code wins when several were raised);
+ * the current device: CP_OK, CP_ERR_DOC_OFFSETS, CP_ERR_TIMEOUT,
+ * CP_ERR_SCRATCH or CP_ERR_CACHE (the lowest code wins when several were
+ * raised);
  * CP_ERR_CUDA if the synchronisation itself failed.
  */
 cp_status cp_get_last_status(cudaStream_t stream);
@@ -371,8 +375,8 @@ cp_status cp_ulysses_attn_fwd(const void* q, const void* k, const void* v, void*
 void cp_test_set_wait_fault(int drop_first_k_tile, long long wait_limit_ns);
 
 /* Number of tcgen05 kernel launches, fp32 kernel launches, auxiliary
- * launches (merge, finalize, all-to-all permutation, FP8 quantisation) and
- * doc-scan launches made by this process so far (host-side counters, for
+ * launches (merge, finalize, all-to-all permutation, FP8 quantisation, norm
+ * and rotation, paged append) and doc-scan launches made by this process so far (host-side counters, for
  * launch accounting in benchmarks). */
 void cp_launch_counts(int64_t* counts4);
 
@@ -452,6 +456,120 @@ cp_status cp_ring_attn_fwd_fp8(const void* q8, const void* k8, const void* v8t,
                                const float* v_descale, void* out, float* lse, int B, int S, int H,
                                int d, int n_shards, int causal, const int32_t* doc_offsets,
                                cudaStream_t stream);
+
+/*
+ * Norm and rotation of queries and keys, per head, in one pass: what a layer
+ * does to q and k between its projection and the attention.  For each row x
+ * (one head of one token, d entries):
+ *   y = R(p) (x * (mean(x^2) + eps)^(-1/2) * weight)
+ * where R(p) turns the first rot_dim entries in pairs (a, b) by the angle
+ * t = p * inv_freq[c]:  (a cos t - b sin t, b cos t + a sin t).
+ *  q, k       device, [B,S,Hq,d] and [B,S,Hk,d], bf16 (is_bf16 = 1) or fp32
+ *             (0), read.  Hk = 0 with k, k_out NULL: queries only.
+ *  q_strides, k_strides   host, three strides in elements (batch row, token,
+ *             head; the d entries are contiguous), or NULL = contiguous:
+ *             q and k may be views of one projection's output.  Each a
+ *             multiple of 16 bytes, 0 allowed (CP_ERR_ALIGN otherwise).
+ *  q_weight, k_weight     device fp32 [d], or NULL: that tensor is not normed.
+ *  eps        >= 0, finite.
+ *  inv_freq   device fp32 [rot_dim / 2]; angles are the exact products
+ *             p * inv_freq modulo a turn, so far positions are as exact as
+ *             near ones.  rot_dim: 0 (no rotation; inv_freq may be NULL) to
+ *             d, a multiple of 16 (else CP_ERR_UNSUPPORTED).
+ *  interleaved  0: pairs (x[c], x[c + rot_dim / 2]); 1: (x[2c], x[2c + 1]).
+ *  positions  device int32 [B,S] (for packed documents they restart with
+ *             each), or NULL: a token's index in its row.
+ *  q_out, k_out   device, contiguous, the inputs' type, written.  May be the
+ *             inputs' own contiguous buffers.
+ *  d          64 or 128; B * S * (Hq + Hk) < 2^31.
+ *  Alignment  q, k, q_out, k_out 16 bytes; the others 4.
+ * Computed in fp32 and rounded once.  One launch; nothing is allocated.
+ */
+cp_status cp_qk_norm_rope(const void* q, const int64_t* q_strides, const void* k,
+                          const int64_t* k_strides, const float* q_weight, const float* k_weight,
+                          float eps, const float* inv_freq, int rot_dim, int interleaved,
+                          const int32_t* positions, void* q_out, void* k_out, int B, int S,
+                          int Hq, int Hk, int d, int is_bf16, cudaStream_t stream);
+
+/*
+ * Backward of cp_qk_norm_rope: from the gradients of its outputs (those that
+ * cp_ring_attn_bwd gives), the gradients of q, k and the two weights.
+ *  dq_out, dk_out   device, contiguous [B,S,H,d], read.
+ *  q, k, weights, eps, inv_freq, rot_dim, interleaved, positions   as given
+ *             to the forward (its inputs, not its outputs).
+ *  dq, dk     device, the inputs' type, written; dq_strides, dk_strides as the
+ *             inputs' strides (no two elements at one address, else
+ *             CP_ERR_SHAPE), so both may be views of the projection's gradient.
+ *             They may be dq_out / dk_out's own contiguous buffers.
+ *  dq_weight, dk_weight   device fp32 [d], written (summed over every row in
+ *             an order that the sizes alone fix), or NULL: not wanted.  Must
+ *             be NULL where the weight is (CP_ERR_NULL).
+ *  workspace  device, >= cp_qk_norm_rope_bwd_workspace_bytes(...) bytes,
+ *             16-byte aligned, caller-owned, contents undefined afterwards;
+ *             too small: CP_ERR_BUFFER.
+ * One launch, and a small one for the weights' sums.
+ */
+int64_t cp_qk_norm_rope_bwd_workspace_bytes(int B, int S, int Hq, int Hk, int d);
+cp_status cp_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
+                              const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                              const float* q_weight, const float* k_weight, float eps,
+                              const float* inv_freq, int rot_dim, int interleaved,
+                              const int32_t* positions, void* dq, const int64_t* dq_strides,
+                              void* dk, const int64_t* dk_strides, float* dq_weight,
+                              float* dk_weight, int B, int S, int Hq, int Hk, int d, int is_bf16,
+                              void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * A paged key/value cache: pages of page_size tokens, Hk heads of d entries
+ * each.  Token p of sequence b lies in slot p % page_size of page
+ * page_table[b * table_stride + p / page_size].  The struct is read during the
+ * call only.
+ */
+typedef struct cp_paged_cache {
+  void* k;                  /* device, 16-byte aligned                                 */
+  void* v;
+  int64_t k_strides[3];     /* elements between pages, tokens of a page, heads (each a */
+  int64_t v_strides[3];     /* multiple of 16 bytes; no two entries at one address)    */
+  const float* k_descale;   /* E4M3: device fp32 [Hk], value = code * descale[head];   */
+  const float* v_descale;   /* bf16: not read                                          */
+  const int32_t* page_table;  /* device, rows of max_pages entries                     */
+  int64_t table_stride;     /* entries between its rows, >= max_pages                  */
+  int32_t n_pages;          /* pages of k and v                                        */
+  int32_t page_size;        /* >= 1; max_pages * page_size < 2^31                      */
+  int32_t max_pages;
+  int32_t Hk;               /* 1 .. 65535                                              */
+  int32_t d;                /* 64 or 128                                               */
+  int32_t elem_bytes;       /* 2: bf16, 1: E4M3 (codes as cp_fp8_quantize writes)      */
+} cp_paged_cache;
+
+/*
+ * Append new tokens' keys and values to a paged cache, with the norm and
+ * rotation of cp_qk_norm_rope on the way.  Token s of sequence b (s <
+ * new_lens[b]) has the position p = cache_lens[b] + s: its key, normed and
+ * rotated by p, and its value are written to the cache's slot of p, rounded
+ * once to the cache's type (E4M3: the code of x / descale[head], saturated).
+ * Its query row, normed and rotated likewise, goes to q_out.
+ *  q, k, v    device, bf16 [B,S,Hq,d], [B,S,Hk,d], [B,S,Hk,d] with strides as
+ *             for cp_qk_norm_rope.  Hq = 0 with q, q_out NULL: keys and
+ *             values only.
+ *  cache_lens device int32 [B]: tokens that each sequence holds already.
+ *  new_lens   device int32 [B], in [0, S]: its new tokens, or NULL = S for all.
+ *             Rows behind them are neither written to the cache nor to q_out.
+ *  weights, eps, inv_freq, rot_dim, interleaved   as for cp_qk_norm_rope.
+ *  q_out      device, bf16 [B,S,Hq,d] contiguous, written (may be q).
+ *  B * S * (Hq + 2 Hk) < 2^31.
+ * A token whose position or page is outside the table or the cache is not
+ * written to it; others are, and cp_get_last_status reports CP_ERR_CACHE (as it
+ * does for a new_lens outside [0, S], which counts as the nearer of the two).
+ * Two tokens of a call that the table sends to one slot race.  One launch;
+ * nothing is allocated; the caller advances cache_lens.
+ */
+cp_status cp_paged_append(const cp_paged_cache* cache, const void* q, const int64_t* q_strides,
+                          const void* k, const int64_t* k_strides, const void* v,
+                          const int64_t* v_strides, const int32_t* cache_lens,
+                          const int32_t* new_lens, const float* q_weight, const float* k_weight,
+                          float eps, const float* inv_freq, int rot_dim, int interleaved,
+                          void* q_out, int B, int S, int Hq, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
