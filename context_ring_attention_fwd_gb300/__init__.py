@@ -22,7 +22,7 @@ from ._binding import (  # noqa: F401
     cp_ring_attn_fwd_rank, cp_ring_attn_fwd_host, cp_ring_attn_fwd_host_workspace_bytes,
     cp_ring_attn_fwd_noalloc,
     cp_lse_finalize, cp_lse_merge, cp_ring_attn_bwd, cp_ring_attn_bwd_workspace_bytes,
-    cp_paged_append,
+    cp_paged_append, cp_paged_attn_decode, cp_paged_attn_decode_workspace_bytes,
     cp_qk_norm_rope, cp_qk_norm_rope_bwd, cp_qk_norm_rope_bwd_workspace_bytes,
     cp_ring_attn_fwd, cp_ring_attn_fwd_emulated,
     cp_ring_attn_fwd_f32, cp_ring_attn_fwd_fp8,
@@ -40,7 +40,7 @@ __all__ = [
     "cp_fp8_quantize", "cp_ring_attn_fwd_fp8", "fp8_quantize_qkv", "ring_attn_fwd_fp8",
     "cp_ring_attn_bwd", "ring_attn_bwd",
     "cp_qk_norm_rope", "cp_qk_norm_rope_bwd", "qk_norm_rope", "qk_norm_rope_bwd",
-    "cp_paged_append", "paged_append",
+    "cp_paged_append", "paged_append", "cp_paged_attn_decode", "paged_attn_decode",
     "CpError", "lib",
 ]
 
@@ -220,3 +220,18 @@ def paged_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens, q_weight, k_weight,
                     inv_freq, q_out, eps, interleaved, k_descale, v_descale, stream)
     return q_out if q is not None else None
+
+
+def paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      page_table: torch.Tensor, seq_lens: torch.Tensor, prefix_pages=None,
+                      prefix_len: int = 0, k_descale=None, v_descale=None, workspace=None,
+                      stream=None):
+    """Decode attention over the paged caches, the shared prefix attended once
+    for the whole batch: allocates and returns (out [B,n_q,Hq,d] bf16, lse
+    [B,Hq,n_q] fp32)."""
+    B, n_q, Hq, d = q.shape
+    out = torch.empty((B, n_q, Hq, d), dtype=q.dtype, device=q.device)
+    lse = torch.empty((B, Hq, n_q), dtype=torch.float32, device=q.device)
+    cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out, lse, prefix_pages,
+                         prefix_len, k_descale, v_descale, workspace, stream)
+    return out, lse

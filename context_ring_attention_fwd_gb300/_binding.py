@@ -69,6 +69,8 @@ _SIGS = {
                             _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp],
     "cp_paged_append": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f, _vp, _i, _i,
                         _vp, _i, _i, _i, _vp],
+    "cp_paged_attn_decode_workspace_bytes": [_i, _i, _i, _i, _i, _i],
+    "cp_paged_attn_decode": [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _i64, _vp],
 }
 
 
@@ -110,6 +112,7 @@ def lib() -> ctypes.CDLL:
                 elif name in ("cp_ring_emulated_workspace_bytes", "cp_ulysses_workspace_bytes",
                               "cp_ring_attn_bwd_workspace_bytes",
                               "cp_qk_norm_rope_bwd_workspace_bytes",
+                              "cp_paged_attn_decode_workspace_bytes",
                               "cp_ring_attn_fwd_host_workspace_bytes"):
                     fn.restype = _i64
                 else:
@@ -697,3 +700,42 @@ def cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens,
              _steps(k), _ptr(v), _steps(v), _ptr(cache_lens), _ptr(new_lens), _ptr(q_weight),
              _ptr(k_weight), float(eps), _ptr(inv_freq), rot, int(bool(interleaved)),
              _ptr(q_out) if q is not None else None, B, S, Hq)
+
+
+def cp_paged_attn_decode_workspace_bytes(B: int, n_q: int, Hq: int, Hk: int, d: int,
+                                         prefix_len: int = 0) -> int:
+    return int(lib().cp_paged_attn_decode_workspace_bytes(B, n_q, Hq, Hk, d, prefix_len))
+
+
+def cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out, lse, prefix_pages=None,
+                         prefix_len: int = 0, k_descale=None, v_descale=None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Decode attention of q [B,n_q,Hq,d] bf16 (strided views allowed), the
+    last n_q tokens of each sequence of seq_lens (int32 [B], 0 = unused row),
+    over the paged caches of cp_paged_append; the keys of positions below
+    prefix_len are read through prefix_pages (int32) once for the whole batch.
+    out [B,n_q,Hq,d] bf16, lse [B,Hq,n_q] fp32; workspace a uint8 device
+    tensor (allocated here if None)."""
+    B, n_q, Hq, d = _rows4(q, "q")
+    dev = _cuda_device(q, "q")
+    cache = _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, dev)
+    if page_table.shape[0] != B:
+        raise ValueError(f"page_table must have {B} rows, got {page_table.shape[0]}")
+    _operand(q, "q", torch.bfloat16, dev, (B, n_q, Hq, cache.d))
+    _dense(out, "out", torch.bfloat16, dev, (B, n_q, Hq, d))
+    _dense(lse, "lse", torch.float32, dev, (B, Hq, n_q))
+    _dense(seq_lens, "seq_lens", torch.int32, dev, (B,))
+    prefix_len = int(prefix_len)
+    if prefix_pages is not None:
+        _dense(prefix_pages, "prefix_pages", torch.int32, dev, (prefix_pages.numel(),))
+        if prefix_pages.numel() * cache.page_size < prefix_len:
+            raise ValueError("prefix_pages holds fewer tokens than prefix_len")
+    if workspace is None:
+        need = cp_paged_attn_decode_workspace_bytes(B, n_q, Hq, cache.Hk, d, prefix_len)
+        if need < 0:
+            raise CpError("cp_paged_attn_decode_workspace_bytes", STATUS_CODES["CP_ERR_SHAPE"])
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _dense(workspace, "workspace", torch.uint8, dev)
+    _call_on("cp_paged_attn_decode", dev, stream, ctypes.byref(cache), _ptr(q), _steps(q),
+             _ptr(seq_lens), _ptr(prefix_pages), prefix_len, _ptr(out), _ptr(lse), B, n_q, Hq,
+             _ptr(workspace), int(workspace.numel()))

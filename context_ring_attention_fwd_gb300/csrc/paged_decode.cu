@@ -1,0 +1,913 @@
+// Decode attention over a paged key/value cache for a batch whose sequences
+// may share a prefix.
+//
+// Row (b, i, h) - query i of sequence b, head h - sees the prefix's keys
+// [0, P) and its own [P, len - n_q + i].  softmax(q k / sqrt d) v over them is
+// built from partial states (O, m, l) over parts of the keys, O = sum
+// 2^(s - m) v and l = sum 2^(s - m) with s in units of log2, joined by the
+// online-softmax merge ("上下文並行（Context Parallelism, CP）",
+// compassingai.com, section 線上 Softmax):
+//   M = max m_x,  O = sum 2^(m_x - M) O_x,  l = sum 2^(m_x - M) l_x,
+//   out = O / l,  lse = (M + log2 l) ln 2.
+//
+// paged_decode_kernel.  The n_q * G rows that share a key head (G = Hq / Hk)
+// are one item per sequence, in tiles of 16 rows; all of them see the keys
+// [P, len - n_q], so an item needs no mask but its end.  (The up to n_q - 1
+// later keys, which query i sees i of, are left to the join.)  Items of the
+// prefix hold the rows of the whole batch.  Bound by HBM: each key and value
+// is read once per item and serves 16 rows, 32 FLOP per byte in bf16, which
+// mma.sync delivers several times over, so the work is in keeping loads in
+// flight.  A warp owns 16 keys of each 64-key tile, with its own cp.async ring
+// and its own running (O, m, l): no two warps meet until the item ends, where
+// the four states are joined in shared memory.  cp.async takes any page size,
+// page order and stride, and fills what lies behind the last key with zeros.
+//
+// Split: the items' tiles are laid end to end (prefix, then sequence by
+// sequence) and every CTA of a fixed grid takes an equal stretch, so a batch of
+// ragged lengths, one long sequence and many short ones all fill the GPU.
+// The stretch is found on the device from the lengths, which lets a captured
+// graph follow them.  An item inside one stretch is finished by its CTA;
+// a cut item leaves its parts in the CTAs' slots (one for a stretch's first
+// item, one for its last).
+//
+// decode_join_kernel, one CTA per row, joins the parts and the later keys of
+// an n_q > 1 call, in a fixed order.
+//
+// E4M3 caches: codes are exact in fp16, so both products run as fp16 MMAs.
+// Q is scaled per row by a power of two into fp16's range (exact but for
+// entries 2^-28 below the row's largest), P by 2^15 so that what fp16 flushes
+// is below 2^-39 of the row's largest; the descales go to the softmax scale
+// and the output.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace cpring {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kWarpKeys = 16;                    // keys of a tile that a warp owns
+constexpr int kTileKeys = kWarps * kWarpKeys;    // 64
+constexpr int kRows = 16;                        // rows of an item
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxGrid = 320;                    // bounds the slots of the workspace
+constexpr int kMaxBatch = 4096;
+constexpr int kMaxQueries = 16;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// One warp's part of a pipeline stage: 16 rows of K, then 16 of V, as 16-byte
+// chunks; chunk c of row r at c ^ (r mod 8) (mod 4 for rows of 64 bytes), so
+// that both ldmatrix and the row-wise reads of codes are conflict-free.
+template <int D, bool kE4M3>
+struct Stage {
+  static constexpr int kRowBytes = D * (kE4M3 ? 1 : 2);
+  static constexpr int kChunks = kRowBytes / 16;
+  static constexpr int kBytes = 2 * kWarpKeys * kRowBytes;
+  static constexpr int kCount = kBytes >= 8192 ? 3 : 6;
+  static constexpr int kRing = kCount * kBytes;  // per warp
+  static constexpr int kSwz = kChunks >= 8 ? 7 : 3;
+  __device__ static uint32_t at(uint32_t base, int row, int chunk) {
+    return base + row * kRowBytes + ((chunk ^ (row & kSwz)) << 4);
+  }
+};
+
+struct DecodeParams {
+  const __nv_bfloat16* q;
+  const uint8_t* cache[2];  // k, v
+  long long cs[2][3];       // their strides in bytes: page, token, head
+  const float* descale[2];
+  const int32_t* table;
+  const int32_t* seq_lens;
+  const int32_t* prefix_pages;
+  __nv_bfloat16* out;
+  float* lse;
+  int* err;
+  // workspace
+  unsigned* starts;  // [B + 1] first own tile of each sequence's items
+  float* slot_o;     // [grid][2][16][d]
+  float* slot_ml;    // [grid][2][16][2]
+  float* whole_o;    // [2][rows][d]: items finished by one CTA but owed a join (own, prefix)
+  float* whole_ml;   // [2][rows][2]
+  long long qb, qs, qh;
+  long long table_stride;
+  float scale;  // log2(e) / sqrt(d)
+  int B, n_q, Hq, Hk, G, R;  // R = n_q * G rows of an item before tiling
+  int own_tiles_of_rows, prefix_tiles_of_rows;  // 16-row tiles of an own and of a prefix item
+  int P, prefix_tiles;       // key tiles of the prefix
+  int n_pages, page_size;
+  long long capacity;        // max_pages * page_size
+};
+
+// Keys of sequence b that all of its queries see behind the prefix; -1 if its
+// length is out of range.
+__device__ __forceinline__ int common_keys(const DecodeParams& p, int len) {
+  if (len == 0) return 0;
+  if (len < p.P || len > p.capacity) return -1;
+  return max(0, len - (p.n_q - 1) - p.P);
+}
+
+__device__ __forceinline__ unsigned own_tiles(const DecodeParams& p, int b) {
+  const int n = common_keys(p, __ldg(p.seq_lens + b));
+  return n <= 0 ? 0u
+                : static_cast<unsigned>((n + kTileKeys - 1) / kTileKeys) *
+                      static_cast<unsigned>(p.Hk * p.own_tiles_of_rows);
+}
+
+__device__ __forceinline__ unsigned prefix_work(const DecodeParams& p) {
+  return static_cast<unsigned>(p.prefix_tiles) *
+         static_cast<unsigned>(p.Hk * p.prefix_tiles_of_rows);
+}
+
+// CTA c's stretch of W tiles over g CTAs starts at c W / g; the CTA whose
+// stretch holds tile w.
+__device__ __forceinline__ unsigned stretch(unsigned c, unsigned W, unsigned g) {
+  return static_cast<unsigned>(static_cast<unsigned long long>(c) * W / g);
+}
+__device__ __forceinline__ unsigned holder(unsigned w, unsigned W, unsigned g) {
+  return static_cast<unsigned>((static_cast<unsigned long long>(w + 1) * g - 1) / W);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+template <bool kF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if (kF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two E4M3 codes (16 bits) to two fp16 values, exactly.
+__device__ __forceinline__ uint32_t half2_of_codes(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+// Row r of an item: its place in q, and its index (b, i, h) in [B, n_q, Hq].
+struct RowOf {
+  int b, i, h;
+  __device__ RowOf(const DecodeParams& p, int b0, int hk, int r) {
+    b = b0 + r / p.R;  // own items: r < R, so b = b0; prefix items: b0 = 0
+    const int rem = r % p.R;
+    i = rem / p.G;
+    h = hk * p.G + rem % p.G;
+  }
+  __device__ long long index(const DecodeParams& p) const {
+    return (static_cast<long long>(b) * p.n_q + i) * p.Hq + h;
+  }
+  __device__ const __nv_bfloat16* query(const DecodeParams& p) const {
+    return p.q + b * p.qb + i * p.qs + h * p.qh;
+  }
+};
+
+template <int D, bool kE4M3>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const DecodeParams p) {
+  using St = Stage<D, kE4M3>;
+  constexpr int kK = D / 16;   // k-steps of S = Q K^T
+  constexpr int kN = D / 8;    // 8-column tiles of O
+  constexpr float kShift = kE4M3 ? 15.f : 0.f;  // P is held times 2^kShift
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ unsigned scan[kWarps];
+  __shared__ float merge_ml[kWarps][kRows][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = lane >> 2, c4 = lane & 3;
+  const uint32_t ring = ptx::smem_u32(smem) + warp * St::kRing;
+
+  // ---- the sequences' first tiles (every CTA scans the lengths; CTA 0 keeps
+  // the result for the join) and this CTA's stretch
+  const unsigned prefix_all = prefix_work(p);
+  unsigned* const starts = reinterpret_cast<unsigned*>(smem + kWarps * St::kRing);
+  unsigned run = prefix_all;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    const unsigned n = b < p.B ? own_tiles(p, b) : 0u;
+    unsigned x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    unsigned base = run;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) base += scan[w];
+      run += scan[w];
+    }
+    if (b < p.B) {
+      starts[b] = base + x - n;
+      if (blockIdx.x == 0) p.starts[b] = base + x - n;
+    }
+    __syncthreads();
+  }
+  const unsigned W = run;
+  if (threadIdx.x == 0) {
+    starts[p.B] = W;
+    if (blockIdx.x == 0) p.starts[p.B] = W;
+  }
+  __syncthreads();
+  const unsigned g = min(gridDim.x, W);
+  if (blockIdx.x >= g) return;
+  unsigned w = stretch(blockIdx.x, W, g);
+  const unsigned w_end = stretch(blockIdx.x + 1, W, g);
+
+  while (w < w_end) {
+    // ---- the item that holds tile w
+    bool prefix;
+    int b0, hk, row0, rows, n_keys, base_pos, t0;
+    unsigned n_tiles;
+    const int32_t* pages;
+    if (w < prefix_all) {
+      prefix = true;
+      n_tiles = p.prefix_tiles;
+      const unsigned item = w / n_tiles;
+      t0 = static_cast<int>(w - item * n_tiles);
+      hk = static_cast<int>(item) / p.prefix_tiles_of_rows;
+      row0 = (static_cast<int>(item) - hk * p.prefix_tiles_of_rows) * kRows;
+      rows = min(kRows, p.B * p.R - row0);
+      b0 = 0;
+      n_keys = p.P;
+      base_pos = 0;
+      pages = p.prefix_pages;
+    } else {
+      prefix = false;
+      int lo = 0, hi = p.B;  // the last b with starts[b] <= w; empty sequences in between skip
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (starts[mid] <= w) lo = mid; else hi = mid;
+      }
+      b0 = lo;
+      n_keys = common_keys(p, __ldg(p.seq_lens + b0));
+      n_tiles = (n_keys + kTileKeys - 1) / kTileKeys;
+      const unsigned local = w - starts[b0];
+      const unsigned item = local / n_tiles;
+      t0 = static_cast<int>(local - item * n_tiles);
+      hk = static_cast<int>(item) / p.own_tiles_of_rows;
+      row0 = (static_cast<int>(item) - hk * p.own_tiles_of_rows) * kRows;
+      rows = min(kRows, p.R - row0);
+      base_pos = p.P;
+      pages = p.table + b0 * p.table_stride;
+    }
+    const int t1 = static_cast<int>(min(n_tiles, static_cast<unsigned>(t0) + (w_end - w)));
+
+    // ---- this warp's loads of tile t: 16 keys, whose pages were looked up
+    // one tile earlier
+    int next_page = -1, next_slot = 0;
+    bool bad = false;
+    auto look_up = [&](int t) {
+      const int key = t * kTileKeys + warp * kWarpKeys + lane;
+      next_page = -1;
+      if (lane < kWarpKeys && t < t1 && key < n_keys) {
+        const int at = (base_pos + key) / p.page_size;
+        next_slot = base_pos + key - at * p.page_size;
+        next_page = __ldg(pages + at);
+        if (next_page < 0 || next_page >= p.n_pages) {
+          next_page = -1;
+          bad = true;
+        }
+      }
+    };
+    auto load = [&](int t, int stage) {
+      if (t < t1) {
+        const uint32_t dst = ring + stage * St::kBytes;
+        const bool have = next_page >= 0;
+        long long off[2] = {0, 0};
+        if (have) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            off[x] = next_page * p.cs[x][0] + next_slot * p.cs[x][1] + hk * p.cs[x][2];
+        }
+        constexpr int kPerStep = 32 / St::kChunks;  // keys per warp-wide access
+        const int chunk = lane % St::kChunks;
+        const unsigned held = __ballot_sync(0xffffffffu, have);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int i = 0; i < kWarpKeys / kPerStep; ++i) {
+            const int key = i * kPerStep + lane / St::kChunks;
+            const long long o = __shfl_sync(0xffffffffu, off[x], key);
+            cp_async16(St::at(dst + x * (St::kBytes / 2), key, chunk),
+                       p.cache[x] + o + chunk * 16, (held >> key & 1u) ? 16 : 0);
+          }
+        }
+        look_up(t + 1);
+      }
+      cp_commit();
+    };
+    look_up(t0);
+#pragma unroll
+    for (int i = 0; i < St::kCount - 1; ++i) load(t0 + i, i);
+
+    // ---- Q fragments: rows quad and quad + 8 of the item
+    uint32_t qf[kK][4];
+    float sc0 = p.scale, sc1 = p.scale;
+    {
+      const RowOf r0(p, b0, hk, min(row0 + quad, row0 + rows - 1));
+      const RowOf r1(p, b0, hk, min(row0 + quad + 8, row0 + rows - 1));
+      const __nv_bfloat16* const q0 = r0.query(p);
+      const __nv_bfloat16* const q1 = r1.query(p);
+      if (!kE4M3) {
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          qf[k][0] = *reinterpret_cast<const uint32_t*>(q0 + k * 16 + c4 * 2);
+          qf[k][1] = *reinterpret_cast<const uint32_t*>(q1 + k * 16 + c4 * 2);
+          qf[k][2] = *reinterpret_cast<const uint32_t*>(q0 + k * 16 + c4 * 2 + 8);
+          qf[k][3] = *reinterpret_cast<const uint32_t*>(q1 + k * 16 + c4 * 2 + 8);
+        }
+      } else {
+        // The order of a dot product's terms is free: lane c4 takes the D / 4
+        // neighbouring columns from c4 * D / 4 on, in Q as in the codes of K.
+        const float desc = __ldg(p.descale[0] + hk);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint4* const src =
+              reinterpret_cast<const uint4*>((x ? q1 : q0) + c4 * (D / 4));
+          float z[D / 4];
+          float top = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const uint4 v = src[i];
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              z[8 * i + 2 * e] = __uint_as_float(u[e] << 16);
+              z[8 * i + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+              top = fmaxf(top, fmaxf(fabsf(z[8 * i + 2 * e]), fabsf(z[8 * i + 2 * e + 1])));
+            }
+          }
+          top = quad_max(top);
+          // 2^e <= top < 2^(e + 1) is brought to [2^14, 2^15)
+          const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+          const int e = (ex == 0 || ex == 255) ? 0 : max(ex - 127 - 14, -112);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          (x ? sc1 : sc0) = p.scale * desc * down;
+#pragma unroll
+          for (int k = 0; k < kK; ++k) {
+            qf[k][x] = pack_f16(z[4 * k] * up, z[4 * k + 1] * up);
+            qf[k][2 + x] = pack_f16(z[4 * k + 2] * up, z[4 * k + 3] * up);
+          }
+        }
+      }
+    }
+    float o[kN][4];
+#pragma unroll
+    for (int n = 0; n < kN; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    int stage = 0;
+    for (int t = t0; t < t1; ++t) {
+      cp_wait<St::kCount - 2>();
+      __syncwarp();
+      load(t + St::kCount - 1, stage == 0 ? St::kCount - 1 : stage - 1);
+      const uint32_t ks = ring + stage * St::kBytes;
+      const uint32_t vs = ks + St::kBytes / 2;
+      if (++stage == St::kCount) stage = 0;
+      // ---- S: two 8-key tiles
+      float s[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      if (!kE4M3) {
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          uint32_t b[4];
+          ldsm4(St::at(ks, (lane >> 4) * 8 + (lane & 7), 2 * k + ((lane >> 3) & 1)), b);
+          mma16816<false>(s[0], qf[k], b[0], b[1]);
+          mma16816<false>(s[1], qf[k], b[2], b[3]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          constexpr int kVecs = D / 64;  // 16-byte vectors of codes per lane and row
+#pragma unroll
+          for (int x = 0; x < kVecs; ++x) {
+            const uint32_t addr = St::at(ks, j * 8 + quad, c4 * kVecs + x);
+            uint32_t u[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                         : "r"(addr));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mma16816<true>(s[j], qf[4 * x + e], half2_of_codes(u[e] & 0xffffu),
+                             half2_of_codes(u[e] >> 16));
+          }
+        }
+      }
+      // ---- mask, running maximum, P
+      const int left = n_keys - (t * kTileKeys + warp * kWarpKeys);  // keys of mine that exist
+      if (left < kWarpKeys) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j * 8 + c4 * 2 + (e & 1) >= left) s[j][e] = -INFINITY;
+      }
+      const float x0 = quad_max(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])) * sc0);
+      const float x1 = quad_max(fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3])) * sc1);
+      if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
+        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+        const float a0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - n0);
+        const float a1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          o[n][0] *= a0;
+          o[n][1] *= a0;
+          o[n][2] *= a1;
+          o[n][3] *= a1;
+        }
+      }
+      const float r0 = (m0 == -INFINITY ? 0.f : m0) - kShift;
+      const float r1 = (m1 == -INFINITY ? 0.f : m1) - kShift;
+      float pr[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        pr[j][0] = ptx::ex2(fmaf(s[j][0], sc0, -r0));
+        pr[j][1] = ptx::ex2(fmaf(s[j][1], sc0, -r0));
+        pr[j][2] = ptx::ex2(fmaf(s[j][2], sc1, -r1));
+        pr[j][3] = ptx::ex2(fmaf(s[j][3], sc1, -r1));
+        l0 += pr[j][0] + pr[j][1];
+        l1 += pr[j][2] + pr[j][3];
+      }
+      uint32_t pf[4];
+      if (kE4M3) {
+        pf[0] = pack_f16(pr[0][0], pr[0][1]);
+        pf[1] = pack_f16(pr[0][2], pr[0][3]);
+        pf[2] = pack_f16(pr[1][0], pr[1][1]);
+        pf[3] = pack_f16(pr[1][2], pr[1][3]);
+      } else {
+        pf[0] = ptx::pack_bf16(pr[0][0], pr[0][1]);
+        pf[1] = ptx::pack_bf16(pr[0][2], pr[0][3]);
+        pf[2] = ptx::pack_bf16(pr[1][0], pr[1][1]);
+        pf[3] = ptx::pack_bf16(pr[1][2], pr[1][3]);
+      }
+      // ---- O += P V
+#pragma unroll
+      for (int ch = 0; ch < St::kChunks; ch += 2) {
+        uint32_t b[4];
+        ldsm4_t(St::at(vs, ((lane >> 3) & 1) * 8 + (lane & 7), ch + (lane >> 4)), b);
+        if (!kE4M3) {
+          mma16816<false>(o[ch], pf, b[0], b[1]);
+          mma16816<false>(o[ch + 1], pf, b[2], b[3]);
+        } else {
+          // A 16-bit element is two neighbouring columns: the even ones make
+          // one 8-column tile, the odd ones another.
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t k_lo = __byte_perm(b[2 * x], 0, 0x3120);
+            const uint32_t k_hi = __byte_perm(b[2 * x + 1], 0, 0x3120);
+            mma16816<true>(o[2 * (ch + x)], pf, half2_of_codes(k_lo & 0xffffu),
+                           half2_of_codes(k_hi & 0xffffu));
+            mma16816<true>(o[2 * (ch + x) + 1], pf, half2_of_codes(k_lo >> 16),
+                           half2_of_codes(k_hi >> 16));
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+
+    // ---- join the four warps' states; a bad page makes the item's l NaN
+    l0 = quad_sum(l0);
+    l1 = quad_sum(l1);
+    const bool any_bad = __syncthreads_or(bad);  // also: every warp is done with its ring
+    if (c4 == 0) {
+      merge_ml[warp][quad][0] = m0;
+      merge_ml[warp][quad][1] = l0;
+      merge_ml[warp][quad + 8][0] = m1;
+      merge_ml[warp][quad + 8][1] = l1;
+    }
+    __syncthreads();
+    constexpr int kPitch = D + 8;  // floats; staggers the rows over the banks
+    float* const mo = reinterpret_cast<float*>(smem);
+    {
+      float big0 = -INFINITY, big1 = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) {
+        big0 = fmaxf(big0, merge_ml[x][quad][0]);
+        big1 = fmaxf(big1, merge_ml[x][quad + 8][0]);
+      }
+      const float f0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - big0);
+      const float f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - big1);
+      float* const w0 = mo + (warp * kRows + quad) * kPitch;
+      float* const w1 = w0 + 8 * kPitch;
+      if (!kE4M3) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          *reinterpret_cast<float2*>(w0 + n * 8 + c4 * 2) = make_float2(o[n][0] * f0, o[n][1] * f0);
+          *reinterpret_cast<float2*>(w1 + n * 8 + c4 * 2) = make_float2(o[n][2] * f1, o[n][3] * f1);
+        }
+      } else {
+#pragma unroll
+        for (int ch = 0; ch < kN / 2; ++ch) {
+          const float(&ev)[4] = o[2 * ch];
+          const float(&od)[4] = o[2 * ch + 1];
+          *reinterpret_cast<float4*>(w0 + ch * 16 + c4 * 4) =
+              make_float4(ev[0] * f0, od[0] * f0, ev[1] * f0, od[1] * f0);
+          *reinterpret_cast<float4*>(w1 + ch * 16 + c4 * 4) =
+              make_float4(ev[2] * f1, od[2] * f1, ev[3] * f1, od[3] * f1);
+        }
+      }
+    }
+    __syncthreads();
+    const bool complete = t0 == 0 && static_cast<unsigned>(t1) == n_tiles;
+    const bool direct = complete && !prefix && p.P == 0 && p.n_q == 1;
+    const float vd = kE4M3 ? __ldg(p.descale[1] + hk) : 1.f;
+    constexpr int kVecs = D / 4;  // 4-column vectors of a row
+    for (int x = threadIdx.x; x < rows * kVecs; x += kThreads) {
+      const int r = x / kVecs, col = (x % kVecs) * 4;
+      float big = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int y = 0; y < kWarps; ++y) big = fmaxf(big, merge_ml[y][r][0]);
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < kWarps; ++y) {
+        const float my = merge_ml[y][r][0];
+        // an empty state's l is 0, or NaN where its scores were
+        l += merge_ml[y][r][1] * (my == -INFINITY ? 1.f : ptx::ex2(my - big));
+        const float4 a = *reinterpret_cast<const float4*>(mo + (y * kRows + r) * kPitch + col);
+        sum.x += a.x;
+        sum.y += a.y;
+        sum.z += a.z;
+        sum.w += a.w;
+      }
+      if (any_bad) l = NAN;
+      const RowOf row(p, b0, hk, row0 + r);
+      if (direct) {
+        const float inv = l == 0.f ? 0.f : vd / l;
+        uint2 v;
+        v.x = ptx::pack_bf16(sum.x * inv, sum.y * inv);
+        v.y = ptx::pack_bf16(sum.z * inv, sum.w * inv);
+        *reinterpret_cast<uint2*>(p.out + row.index(p) * D + col) = v;
+        if (col == 0)
+          p.lse[(static_cast<long long>(row.b) * p.Hq + row.h) * p.n_q + row.i] =
+              (big - kShift + log2f(l)) * kLn2;
+        continue;
+      }
+      float *to, *ml;
+      if (complete) {
+        const long long at = (prefix ? static_cast<long long>(p.B) * p.n_q * p.Hq : 0) +
+                             row.index(p);
+        to = p.whole_o + at * D;
+        ml = p.whole_ml + at * 2;
+      } else {
+        const long long at = (static_cast<long long>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0)) * kRows + r;
+        to = p.slot_o + at * D;
+        ml = p.slot_ml + at * 2;
+      }
+      *reinterpret_cast<float4*>(to + col) = make_float4(sum.x * vd, sum.y * vd, sum.z * vd,
+                                                         sum.w * vd);
+      if (col == 0) *reinterpret_cast<float2*>(ml) = make_float2(big - kShift, l);
+    }
+    if (any_bad && threadIdx.x == 0) atomicOr(p.err, kErrCache);
+    __syncthreads();  // the ring is free again
+    w += static_cast<unsigned>(t1 - t0);
+  }
+}
+
+// The parts of one row's item whose tiles are [first, first + n) of W: where
+// the x-th lies.
+struct Parts {
+  unsigned c0, count;
+  bool whole;
+  __device__ Parts(unsigned first, unsigned n, unsigned W, unsigned g) {
+    c0 = holder(first, W, g);
+    const unsigned c1 = holder(first + n - 1, W, g);
+    whole = c0 == c1;
+    count = c1 - c0 + 1;
+  }
+};
+
+template <int D, bool kE4M3>
+__global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParams p, unsigned grid) {
+  constexpr int kCols = D / 32;  // columns per lane
+  __shared__ float part_m[kWarps], part_l[kWarps];
+  __shared__ float part_o[kWarps][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  cudaGridDependencySynchronize();
+  const long long rid = blockIdx.x;  // (b, i, h)
+  const int h = static_cast<int>(rid % p.Hq);
+  const long long bi = rid / p.Hq;
+  const int i = static_cast<int>(bi % p.n_q), b = static_cast<int>(bi / p.n_q);
+  const int hk = h / p.G;
+  const int len = __ldg(p.seq_lens + b);
+  const int common = common_keys(p, len);
+  const long long lse_at = (static_cast<long long>(b) * p.Hq + h) * p.n_q + i;
+  __nv_bfloat16* const out = p.out + rid * D;
+  if (len == 0 || common < 0) {
+    const float v = len == 0 ? 0.f : NAN;
+    for (int x = threadIdx.x; x < D; x += kThreads) out[x] = __float2bfloat16_rn(v);
+    if (threadIdx.x == 0) {
+      p.lse[lse_at] = len == 0 ? -INFINITY : NAN;
+      if (common < 0) atomicOr(p.err, kErrCache);
+    }
+    return;
+  }
+  const unsigned W = p.starts[p.B];
+  const unsigned g = min(grid, W);
+  const unsigned n_own = static_cast<unsigned>((common + kTileKeys - 1) / kTileKeys);
+  const int r_own = i * p.G + h % p.G;
+  const long long r_prefix = static_cast<long long>(b) * p.R + r_own;
+  float m = -INFINITY, l = 0.f;
+  float o[kCols];
+#pragma unroll
+  for (int x = 0; x < kCols; ++x) o[x] = 0.f;
+  auto add = [&](float mx, float lx, const float (&ox)[kCols]) {
+    const float big = fmaxf(m, mx);
+    const float a = m == -INFINITY ? 0.f : ptx::ex2(m - big);
+    const float c = mx == -INFINITY ? 0.f : ptx::ex2(mx - big);
+    l = l * a + (mx == -INFINITY ? lx : lx * c);  // an empty part's l is 0, or NaN
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) o[x] = o[x] * a + ox[x] * c;
+    m = big;
+  };
+  auto take = [&](const float* from, const float* ml) {
+    const float2 v = *reinterpret_cast<const float2*>(ml);
+    float ox[kCols];
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) ox[x] = from[lane * kCols + x];
+    add(v.x, v.y, ox);
+  };
+  // the parts of this row's two items, dealt to the warps
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {  // own, prefix
+    const unsigned n = kind ? static_cast<unsigned>(p.prefix_tiles) : n_own;
+    if (n == 0) continue;
+    unsigned item;
+    int r;
+    if (kind) {
+      item = static_cast<unsigned>(hk * p.prefix_tiles_of_rows + r_prefix / kRows);
+      r = static_cast<int>(r_prefix % kRows);
+    } else {
+      item = static_cast<unsigned>(hk * p.own_tiles_of_rows + r_own / kRows);
+      r = r_own % kRows;
+    }
+    const unsigned first = (kind ? 0u : p.starts[b]) + item * n;
+    const Parts parts(first, n, W, g);
+    if (parts.whole) {
+      if (!kind && p.P == 0 && p.n_q == 1) return;  // written by the item's CTA
+      if (warp == 0) {
+        const long long at = (kind ? static_cast<long long>(p.B) * p.n_q * p.Hq : 0) + rid;
+        take(p.whole_o + at * D, p.whole_ml + at * 2);
+      }
+      continue;
+    }
+    for (unsigned x = warp; x < parts.count; x += kWarps) {
+      const long long at =
+          (static_cast<long long>(parts.c0 + x) * 2 + (x == 0 ? 1 : 0)) * kRows + r;
+      take(p.slot_o + at * D, p.slot_ml + at * 2);
+    }
+  }
+  // the keys behind the common ones that this query sees, one per warp at a time
+  const int pos0 = max(len - p.n_q + 1, p.P);
+  const int pos1 = len - p.n_q + i;
+  bool bad = false;
+  if (pos0 <= pos1) {
+    float q[kCols];
+    const __nv_bfloat16* const src = p.q + b * p.qb + i * p.qs + h * p.qh + lane * kCols;
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) q[x] = __bfloat162float(src[x]);
+    for (int pos = pos0 + warp; pos <= pos1; pos += kWarps) {
+      const int at = pos / p.page_size;
+      const int page = __ldg(p.table + b * p.table_stride + at);
+      if (page < 0 || page >= p.n_pages) {
+        bad = true;
+        continue;
+      }
+      float kv[2][kCols];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint8_t* const row = p.cache[x] + page * p.cs[x][0] +
+                                   (pos - at * p.page_size) * p.cs[x][1] + hk * p.cs[x][2];
+#pragma unroll
+        for (int y = 0; y < kCols; ++y) {
+          if (kE4M3) {
+            const uint32_t hh = half2_of_codes(row[lane * kCols + y]);
+            kv[x][y] = __half2float(__ushort_as_half(static_cast<unsigned short>(hh & 0xffffu))) *
+                       __ldg(p.descale[x] + hk);
+          } else {
+            kv[x][y] = __bfloat162float(
+                reinterpret_cast<const __nv_bfloat16*>(row)[lane * kCols + y]);
+          }
+        }
+      }
+      float dot = 0.f;
+#pragma unroll
+      for (int y = 0; y < kCols; ++y) dot = fmaf(q[y], kv[0][y], dot);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+      add(dot * p.scale, 1.f, kv[1]);
+    }
+  }
+  if (lane == 0) {
+    part_m[warp] = m;
+    part_l[warp] = bad ? NAN : l;
+    if (bad) atomicOr(p.err, kErrCache);
+  }
+#pragma unroll
+  for (int x = 0; x < kCols; ++x) part_o[warp][lane * kCols + x] = o[x];
+  __syncthreads();
+  float big = -INFINITY;
+#pragma unroll
+  for (int y = 0; y < kWarps; ++y) big = fmaxf(big, part_m[y]);
+  float total = 0.f, f[kWarps];
+#pragma unroll
+  for (int y = 0; y < kWarps; ++y) {
+    f[y] = part_m[y] == -INFINITY ? 0.f : ptx::ex2(part_m[y] - big);
+    total += part_m[y] == -INFINITY ? part_l[y] : part_l[y] * f[y];
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  for (int x = threadIdx.x; x < D; x += kThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int y = 0; y < kWarps; ++y) v += part_o[y][x] * f[y];
+    out[x] = __float2bfloat16_rn(v * inv);
+  }
+  if (threadIdx.x == 0) p.lse[lse_at] = total == 0.f ? -INFINITY : (big + log2f(total)) * kLn2;
+}
+
+long long align256(long long n) { return (n + 255) / 256 * 256; }
+
+// Byte offsets of the workspace's parts.
+struct Space {
+  long long starts, slot_o, slot_ml, whole_o, whole_ml, total;
+  Space(int B, int n_q, int Hq, int d, int prefix_len) {
+    const long long rows = static_cast<long long>(B) * n_q * Hq;
+    const long long slots = 2LL * kMaxGrid * kRows;
+    const long long whole = prefix_len > 0 ? 2 * rows : n_q > 1 ? rows : 0;
+    starts = 0;
+    slot_o = align256(4LL * (B + 1));
+    slot_ml = slot_o + align256(slots * d * 4);
+    whole_o = slot_ml + align256(slots * 8);
+    whole_ml = whole_o + align256(whole * d * 4);
+    total = whole_ml + align256(whole * 8);
+  }
+};
+
+template <int D, bool kE4M3>
+cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
+  using St = Stage<D, kE4M3>;
+  static_assert(kWarps * St::kRing >= kWarps * kRows * (D + 8) * 4, "the join fits the ring");
+  const int smem = kWarps * St::kRing + 4 * (p.B + 1);
+  const int most = kWarps * St::kRing + 4 * (kMaxBatch + 1);
+  cudaError_t e = ensure_smem_limit(
+      reinterpret_cast<const void*>(&paged_decode_kernel<D, kE4M3>), most);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(std::min(kMaxGrid, kCtasPerSm * sm_count()));
+  paged_decode_kernel<D, kE4M3><<<grid, kThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  count_launch(2);
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.n_q * p.Hq);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, decode_join_kernel<D, kE4M3>, p, grid);
+  count_launch(2);
+  return e;
+}
+
+bool sizes_ok(int B, int n_q, int Hq, int Hk, int prefix_len) {
+  return B >= 1 && B <= kMaxBatch && n_q >= 1 && n_q <= kMaxQueries && Hq >= 1 && Hk >= 1 &&
+         Hq % Hk == 0 && prefix_len >= 0 &&
+         static_cast<long long>(B) * n_q * Hq <= (1LL << 24);
+}
+
+}  // namespace
+}  // namespace cpring
+
+extern "C" {
+
+int64_t cp_paged_attn_decode_workspace_bytes(int B, int n_q, int Hq, int Hk, int d,
+                                             int prefix_len) {
+  if (!cpring::sizes_ok(B, n_q, Hq, Hk, prefix_len) || (d != 64 && d != 128)) return -1;
+  return cpring::Space(B, n_q, Hq, d, prefix_len).total;
+}
+
+cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
+                               const int64_t* q_strides, const int32_t* seq_lens,
+                               const int32_t* prefix_pages, int prefix_len, void* out, float* lse,
+                               int B, int n_q, int Hq, void* workspace, int64_t workspace_bytes,
+                               cudaStream_t stream) {
+  cpring::TraceRange trace_("cp_paged_attn_decode");
+  using namespace cpring;
+  if (!q || !seq_lens || !out || !lse || !workspace || (prefix_len > 0 && !prefix_pages))
+    return CP_ERR_NULL;
+  cp_status st = check_cache(cache);
+  if (st != CP_OK) return st;
+  const int Hk = cache->Hk, d = cache->d;
+  if (!sizes_ok(B, n_q, Hq, Hk, prefix_len)) return CP_ERR_SHAPE;
+  const long long capacity = static_cast<long long>(cache->max_pages) * cache->page_size;
+  if (prefix_len > capacity) return CP_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(seq_lens, 4) ||
+      !aligned(prefix_pages, 4) || !aligned(workspace, 256) || !strides_ok(q_strides, 2))
+    return CP_ERR_ALIGN;
+  if (workspace_bytes < cp_paged_attn_decode_workspace_bytes(B, n_q, Hq, Hk, d, prefix_len))
+    return CP_ERR_BUFFER;
+  // the tiles of a call are counted in 32 bits
+  const long long G = Hq / Hk, R = G * n_q;
+  const long long own_rt = (R + kRows - 1) / kRows, prefix_rt = (B * R + kRows - 1) / kRows;
+  const long long most_tiles = (capacity + kTileKeys - 1) / kTileKeys;
+  const long long prefix_tiles = (static_cast<long long>(prefix_len) + kTileKeys - 1) / kTileKeys;
+  if ((prefix_tiles * prefix_rt + most_tiles * own_rt * B) * Hk > 0xffffffffLL)
+    return CP_ERR_SHAPE;
+  if (device_cc() != 103) return CP_ERR_DEVICE;
+  DecodeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.cache[0] = static_cast<const uint8_t*>(cache->k);
+  p.cache[1] = static_cast<const uint8_t*>(cache->v);
+  for (int i = 0; i < 3; ++i) {
+    p.cs[0][i] = cache->k_strides[i] * cache->elem_bytes;
+    p.cs[1][i] = cache->v_strides[i] * cache->elem_bytes;
+  }
+  p.descale[0] = cache->k_descale;
+  p.descale[1] = cache->v_descale;
+  p.table = cache->page_table;
+  p.table_stride = cache->table_stride;
+  p.seq_lens = seq_lens;
+  p.prefix_pages = prefix_pages;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.err = device_error_word();
+  if (!p.err) return CP_ERR_CUDA;
+  const Space sp(B, n_q, Hq, d, prefix_len);
+  char* const ws = static_cast<char*>(workspace);
+  p.starts = reinterpret_cast<unsigned*>(ws + sp.starts);
+  p.slot_o = reinterpret_cast<float*>(ws + sp.slot_o);
+  p.slot_ml = reinterpret_cast<float*>(ws + sp.slot_ml);
+  p.whole_o = reinterpret_cast<float*>(ws + sp.whole_o);
+  p.whole_ml = reinterpret_cast<float*>(ws + sp.whole_ml);
+  p.qb = q_strides ? q_strides[0] : static_cast<long long>(n_q) * Hq * d;
+  p.qs = q_strides ? q_strides[1] : static_cast<long long>(Hq) * d;
+  p.qh = q_strides ? q_strides[2] : d;
+  p.scale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
+  p.B = B; p.n_q = n_q; p.Hq = Hq; p.Hk = Hk;
+  p.G = static_cast<int>(G); p.R = static_cast<int>(R);
+  p.own_tiles_of_rows = static_cast<int>(own_rt);
+  p.prefix_tiles_of_rows = static_cast<int>(prefix_rt);
+  p.P = prefix_len;
+  p.prefix_tiles = static_cast<int>(prefix_tiles);
+  p.n_pages = cache->n_pages; p.page_size = cache->page_size;
+  p.capacity = capacity;
+  const bool e4m3 = cache->elem_bytes == 1;
+  const cudaError_t e = d == 128 ? (e4m3 ? launch_decode<128, true>(p, stream)
+                                         : launch_decode<128, false>(p, stream))
+                                 : (e4m3 ? launch_decode<64, true>(p, stream)
+                                         : launch_decode<64, false>(p, stream));
+  return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+}  // extern "C"

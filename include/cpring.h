@@ -376,7 +376,7 @@ void cp_test_set_wait_fault(int drop_first_k_tile, long long wait_limit_ns);
 
 /* Number of tcgen05 kernel launches, fp32 kernel launches, auxiliary
  * launches (merge, finalize, all-to-all permutation, FP8 quantisation, norm
- * and rotation, paged append) and doc-scan launches made by this process so far (host-side counters, for
+ * and rotation, paged append and decode) and doc-scan launches made by this process so far (host-side counters, for
  * launch accounting in benchmarks). */
 void cp_launch_counts(int64_t* counts4);
 
@@ -570,6 +570,45 @@ cp_status cp_paged_append(const cp_paged_cache* cache, const void* q, const int6
                           const int32_t* new_lens, const float* q_weight, const float* k_weight,
                           float eps, const float* inv_freq, int rot_dim, int interleaved,
                           void* q_out, int B, int S, int Hq, cudaStream_t stream);
+
+/*
+ * Decode attention over a paged cache for a batch whose sequences share a
+ * prefix, which is attended once for the whole batch: every sequence's
+ * partial state over the prefix and over its own keys are joined by the
+ * online merge of cp_lse_merge ("上下文並行", section 線上 Softmax).
+ * Sequence b has seq_lens[b] tokens in the cache, the n_q last of them its
+ * queries: query i is at position seq_lens[b] - n_q + i.  It sees the keys of
+ * positions [0, prefix_len), read through prefix_pages, and those of positions
+ * [prefix_len, seq_lens[b] - n_q + i], read through row b of the page table.
+ *  q          device, bf16 [B,n_q,Hq,d], strides as for cp_qk_norm_rope; head h
+ *             reads key head h / (Hq / Hk); Hq % Hk must be 0.
+ *  seq_lens   device int32 [B]: 0 for an unused row of the batch, otherwise
+ *             >= prefix_len and <= max_pages * page_size.
+ *  prefix_pages  device int32 [ceil(prefix_len / page_size)], or NULL with
+ *             prefix_len = 0 (no shared prefix).
+ *  out        device, bf16 [B,n_q,Hq,d] contiguous, written.
+ *  lse        device, fp32 [B,Hq,n_q], written (natural log).
+ *  B          1 .. 4096;  n_q  1 .. 16;  B * n_q * Hq <= 2^24.
+ *  workspace  device, >= cp_paged_attn_decode_workspace_bytes(...) bytes,
+ *             256-byte aligned, caller-owned, contents undefined afterwards
+ *             (calls that can overlap, two captured graphs' among them, need
+ *             one each); too small: CP_ERR_BUFFER.
+ * Rows that see no key (an unused batch row, a query before its sequence's
+ * start) get out = 0, lse = -inf.  What the cache holds in slots that no query
+ * sees is never used, whatever it is.  A sequence with a length outside its
+ * range, or a page outside the cache among those it reads, gets NaN in its
+ * rows of out and lse (a bad prefix page: every used row), the others are
+ * computed as usual, and cp_get_last_status reports CP_ERR_CACHE.
+ * Nothing is allocated; lengths are read on the device, so a captured call
+ * follows them when it is replayed.
+ */
+int64_t cp_paged_attn_decode_workspace_bytes(int B, int n_q, int Hq, int Hk, int d,
+                                             int prefix_len);
+cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
+                               const int64_t* q_strides, const int32_t* seq_lens,
+                               const int32_t* prefix_pages, int prefix_len, void* out, float* lse,
+                               int B, int n_q, int Hq, void* workspace, int64_t workspace_bytes,
+                               cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -166,3 +166,56 @@ def test_append_refuses_bad_caches(lib, cache, want):
 def test_append_refuses_before_any_launch(lib, change, want):
     assert lib.cp_paged_append(*append_args(**change)) == want
     assert lib.cp_paged_append(None, *append_args(**change)[1:]) == -1
+
+
+def test_paged_decode_is_attention_over_the_gathered_keys():
+    """The decode oracle on an identity table equals the forward's causal oracle on its last
+    rows, whatever part of the keys is called the prefix."""
+    from oracle import ref
+    rng = np.random.default_rng(9)
+    L, H, d, ps, n = 23, 2, 16, 4, 3
+    q, k, v = rng.standard_normal((3, 1, L, H, d))
+    want, wantl = ref.attention(q, k, v, True)
+    pages = -(-L // ps)
+    kc, vc = np.zeros((2, pages, ps, H, d))
+    kc.reshape(-1, H, d)[:L], vc.reshape(-1, H, d)[:L] = k[0], v[0]
+    table = np.arange(pages)[None]
+    for prefix in (0, 7, 20):
+        out, lse = serving.paged_decode(q[:, L - n:], kc, vc, table, [L], table[0], prefix)
+        assert np.abs(out - want[:, L - n:]).max() < 1e-12
+        assert np.abs(lse - wantl[:, :, L - n:]).max() < 1e-12
+    out, lse = serving.paged_decode(q[:, :3], kc, vc, table, [0])
+    assert (out == 0).all() and np.isneginf(lse).all()
+
+
+def decode_args(cache=None, **kw):
+    a = dict(q=FAKE, qs=None, lens=FAKE, pages=None, P=0, out=FAKE, lse=FAKE, B=2, n_q=1, Hq=4,
+             ws=FAKE, n=1 << 40, stream=None)
+    a.update(kw)
+    return [ctypes.byref(cache_struct(**(cache or {})))] + list(a.values())
+
+
+@pytest.mark.parametrize("cache,want", BAD_CACHES)
+def test_decode_refuses_bad_caches(lib, cache, want):
+    assert lib.cp_paged_attn_decode(*decode_args(cache)) == want
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(q=None), -1), (dict(lens=None), -1), (dict(out=None), -1), (dict(lse=None), -1),
+    (dict(ws=None), -1), (dict(P=5), -1), (dict(B=0), -2), (dict(B=4097), -2), (dict(n_q=0), -2),
+    (dict(n_q=17), -2), (dict(Hq=3), -2), (dict(Hq=0), -2), (dict(P=-1), -2),
+    (dict(P=129, pages=FAKE), -2),                        # more than max_pages * page_size
+    (dict(q=ODD), -4), (dict(out=ODD), -4), (dict(ws=V(0x10010)), -4), (dict(lens=ODD), -4),
+    (dict(qs=strides(0, 0, 60)), -4), (dict(n=1000), -6),
+])
+def test_decode_refuses_before_any_launch(lib, change, want):
+    assert lib.cp_paged_attn_decode(*decode_args(**change)) == want
+    assert lib.cp_paged_attn_decode(None, *decode_args(**change)[1:]) == -1
+
+
+def test_decode_workspace(lib):
+    f = pkg.cp_paged_attn_decode_workspace_bytes
+    assert 0 < f(1, 1, 1, 1, 64) <= f(64, 4, 32, 8, 128) < f(64, 4, 32, 8, 128, 1000)
+    for bad in [(0, 1, 1, 1, 64), (1, 17, 1, 1, 64), (1, 1, 3, 2, 64), (1, 1, 2, 2, 80),
+                (4097, 1, 1, 1, 64)]:
+        assert f(*bad) == -1
