@@ -21,8 +21,8 @@ LIB = os.path.join(LIBDIR, "libcpring.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["attn_sm103.cu", "attn_f32.cu", "merge.cu", "noalloc.cu", "ring_emulation.cpp",
-           "ulysses.cu", "fp8.cu", "attn_bwd_sm103.cu", "norm_rope.cu", "paged_append.cu", "paged_decode.cu",
-           "api.cpp", "scratch.cpp", "host_path.cpp"]
+           "ulysses.cu", "fp8.cu", "attn_bwd_sm103.cu", "norm_rope.cu", "paged_append.cu",
+           "paged_decode.cu", "prefix_sm103.cu", "api.cpp", "scratch.cpp", "host_path.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -37,7 +37,8 @@ def _nvcc() -> str:
 # setmaxnreg; the split is sized for exactly this many registers per thread at
 # launch, so a build that comes out different is refused (the split would not
 # fit and the kernel would stall).
-SPLIT_KERNELS = ("ring_attn_bf16_kernel", "ring_attn_fp8_kernel", "ring_attn_bwd_kernel")
+SPLIT_KERNELS = ("ring_attn_bf16_kernel", "ring_attn_fp8_kernel", "ring_attn_bwd_kernel",
+                 "prefix_attn_kernel")
 SPLIT_LAUNCH_REGS = 168
 
 

@@ -47,6 +47,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "paged_decode.h"
 #include "ptx.cuh"
 
 namespace cpring {
@@ -79,33 +80,6 @@ struct Stage {
   }
 };
 
-struct DecodeParams {
-  const __nv_bfloat16* q;
-  const uint8_t* cache[2];  // k, v
-  long long cs[2][3];       // their strides in bytes: page, token, head
-  const float* descale[2];
-  const int32_t* table;
-  const int32_t* seq_lens;
-  const int32_t* prefix_pages;
-  __nv_bfloat16* out;
-  float* lse;
-  int* err;
-  // workspace
-  unsigned* starts;  // [B + 1] first own tile of each sequence's items
-  float* slot_o;     // [grid][2][16][d]
-  float* slot_ml;    // [grid][2][16][2]
-  float* whole_o;    // [2][rows][d]: items finished by one CTA but owed a join (own, prefix)
-  float* whole_ml;   // [2][rows][2]
-  long long qb, qs, qh;
-  long long table_stride;
-  float scale;  // log2(e) / sqrt(d)
-  int B, n_q, Hq, Hk, G, R;  // R = n_q * G rows of an item before tiling
-  int own_tiles_of_rows, prefix_tiles_of_rows;  // 16-row tiles of an own and of a prefix item
-  int P, prefix_tiles;       // key tiles of the prefix
-  int n_pages, page_size;
-  long long capacity;        // max_pages * page_size
-};
-
 // Keys of sequence b that all of its queries see behind the prefix; -1 if its
 // length is out of range.
 __device__ __forceinline__ int common_keys(const DecodeParams& p, int len) {
@@ -121,18 +95,11 @@ __device__ __forceinline__ unsigned own_tiles(const DecodeParams& p, int b) {
                       static_cast<unsigned>(p.Hk * p.own_tiles_of_rows);
 }
 
+// Tiles of the prefix in this kernel's own list.
 __device__ __forceinline__ unsigned prefix_work(const DecodeParams& p) {
-  return static_cast<unsigned>(p.prefix_tiles) *
-         static_cast<unsigned>(p.Hk * p.prefix_tiles_of_rows);
-}
-
-// CTA c's stretch of W tiles over g CTAs starts at c W / g; the CTA whose
-// stretch holds tile w.
-__device__ __forceinline__ unsigned stretch(unsigned c, unsigned W, unsigned g) {
-  return static_cast<unsigned>(static_cast<unsigned long long>(c) * W / g);
-}
-__device__ __forceinline__ unsigned holder(unsigned w, unsigned W, unsigned g) {
-  return static_cast<unsigned>((static_cast<unsigned long long>(w + 1) * g - 1) / W);
+  return p.prefix_grid > 0 ? 0u
+                           : static_cast<unsigned>(p.prefix_tiles) *
+                                 static_cast<unsigned>(p.Hk * p.prefix_row_tiles);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -188,23 +155,6 @@ __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
-
-// Row r of an item: its place in q, and its index (b, i, h) in [B, n_q, Hq].
-struct RowOf {
-  int b, i, h;
-  __device__ RowOf(const DecodeParams& p, int b0, int hk, int r) {
-    b = b0 + r / p.R;  // own items: r < R, so b = b0; prefix items: b0 = 0
-    const int rem = r % p.R;
-    i = rem / p.G;
-    h = hk * p.G + rem % p.G;
-  }
-  __device__ long long index(const DecodeParams& p) const {
-    return (static_cast<long long>(b) * p.n_q + i) * p.Hq + h;
-  }
-  __device__ const __nv_bfloat16* query(const DecodeParams& p) const {
-    return p.q + b * p.qb + i * p.qs + h * p.qh;
-  }
-};
 
 template <int D, bool kE4M3>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const DecodeParams p) {
@@ -268,8 +218,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       n_tiles = p.prefix_tiles;
       const unsigned item = w / n_tiles;
       t0 = static_cast<int>(w - item * n_tiles);
-      hk = static_cast<int>(item) / p.prefix_tiles_of_rows;
-      row0 = (static_cast<int>(item) - hk * p.prefix_tiles_of_rows) * kRows;
+      hk = static_cast<int>(item) / p.prefix_row_tiles;
+      row0 = (static_cast<int>(item) - hk * p.prefix_row_tiles) * kRows;
       rows = min(kRows, p.B * p.R - row0);
       b0 = 0;
       n_keys = p.P;
@@ -382,11 +332,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
             }
           }
           top = quad_max(top);
-          // 2^e <= top < 2^(e + 1) is brought to [2^14, 2^15)
-          const int ex = static_cast<int>(__float_as_uint(top) >> 23);
-          const int e = (ex == 0 || ex == 255) ? 0 : max(ex - 127 - 14, -112);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          const float down = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          float up, down;
+          fp16_row_scale(top, up, down);
           (x ? sc1 : sc0) = p.scale * desc * down;
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
@@ -681,17 +628,16 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
   for (int kind = 0; kind < 2; ++kind) {  // own, prefix
     const unsigned n = kind ? static_cast<unsigned>(p.prefix_tiles) : n_own;
     if (n == 0) continue;
-    unsigned item;
-    int r;
-    if (kind) {
-      item = static_cast<unsigned>(hk * p.prefix_tiles_of_rows + r_prefix / kRows);
-      r = static_cast<int>(r_prefix % kRows);
-    } else {
-      item = static_cast<unsigned>(hk * p.own_tiles_of_rows + r_own / kRows);
-      r = r_own % kRows;
-    }
-    const unsigned first = (kind ? 0u : p.starts[b]) + item * n;
-    const Parts parts(first, n, W, g);
+    const bool wide = kind && p.prefix_grid > 0;  // prefix_attn_kernel's parts
+    const int item_rows = kind ? p.prefix_rows : kRows;
+    const long long row = kind ? r_prefix : r_own;
+    const unsigned item = static_cast<unsigned>(
+        hk * (kind ? p.prefix_row_tiles : p.own_tiles_of_rows) + row / item_rows);
+    const int r = static_cast<int>(row % item_rows);
+    const unsigned all =
+        wide ? n * static_cast<unsigned>(p.Hk * p.prefix_row_tiles) : W;
+    const Parts parts((kind ? 0u : p.starts[b]) + item * n, n, all,
+                      wide ? static_cast<unsigned>(p.prefix_grid) : g);
     if (parts.whole) {
       if (!kind && p.P == 0 && p.n_q == 1) return;  // written by the item's CTA
       if (warp == 0) {
@@ -700,10 +646,12 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
       }
       continue;
     }
+    const float* const slots_o = wide ? p.pslot_o : p.slot_o;
+    const float* const slots_ml = wide ? p.pslot_ml : p.slot_ml;
     for (unsigned x = warp; x < parts.count; x += kWarps) {
       const long long at =
-          (static_cast<long long>(parts.c0 + x) * 2 + (x == 0 ? 1 : 0)) * kRows + r;
-      take(p.slot_o + at * D, p.slot_ml + at * 2);
+          (static_cast<long long>(parts.c0 + x) * 2 + (x == 0 ? 1 : 0)) * item_rows + r;
+      take(slots_o + at * D, slots_ml + at * 2);
     }
   }
   // the keys behind the common ones that this query sees, one per warp at a time
@@ -776,25 +724,36 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
 
 long long align256(long long n) { return (n + 255) / 256 * 256; }
 
+// Whether the prefix's rows per key head go to prefix_attn_kernel.
+bool wide_prefix(long long rows, int prefix_len) { return prefix_len > 0 && rows > 32; }
+
 // Byte offsets of the workspace's parts.
 struct Space {
-  long long starts, slot_o, slot_ml, whole_o, whole_ml, total;
-  Space(int B, int n_q, int Hq, int d, int prefix_len) {
+  long long starts, slot_o, slot_ml, whole_o, whole_ml, pslot_o, pslot_ml, total;
+  Space(int B, int n_q, int Hq, int Hk, int d, int prefix_len) {
     const long long rows = static_cast<long long>(B) * n_q * Hq;
     const long long slots = 2LL * kMaxGrid * kRows;
     const long long whole = prefix_len > 0 ? 2 * rows : n_q > 1 ? rows : 0;
+    const long long pslots =
+        wide_prefix(rows / Hk, prefix_len) ? 2LL * kMaxPrefixGrid * kPrefixRows : 0;
     starts = 0;
     slot_o = align256(4LL * (B + 1));
     slot_ml = slot_o + align256(slots * d * 4);
     whole_o = slot_ml + align256(slots * 8);
     whole_ml = whole_o + align256(whole * d * 4);
-    total = whole_ml + align256(whole * 8);
+    pslot_o = whole_ml + align256(whole * 8);
+    pslot_ml = pslot_o + align256(pslots * d * 4);
+    total = pslot_ml + align256(pslots * 8);
   }
 };
 
 template <int D, bool kE4M3>
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   using St = Stage<D, kE4M3>;
+  if (p.prefix_grid > 0) {
+    const cudaError_t e = launch_prefix_attn(p, D, kE4M3, stream);
+    if (e != cudaSuccess) return e;
+  }
   static_assert(kWarps * St::kRing >= kWarps * kRows * (D + 8) * 4, "the join fits the ring");
   const int smem = kWarps * St::kRing + 4 * (p.B + 1);
   const int most = kWarps * St::kRing + 4 * (kMaxBatch + 1);
@@ -834,7 +793,7 @@ extern "C" {
 int64_t cp_paged_attn_decode_workspace_bytes(int B, int n_q, int Hq, int Hk, int d,
                                              int prefix_len) {
   if (!cpring::sizes_ok(B, n_q, Hq, Hk, prefix_len) || (d != 64 && d != 128)) return -1;
-  return cpring::Space(B, n_q, Hq, d, prefix_len).total;
+  return cpring::Space(B, n_q, Hq, Hk, d, prefix_len).total;
 }
 
 cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
@@ -859,9 +818,13 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
     return CP_ERR_BUFFER;
   // the tiles of a call are counted in 32 bits
   const long long G = Hq / Hk, R = G * n_q;
-  const long long own_rt = (R + kRows - 1) / kRows, prefix_rt = (B * R + kRows - 1) / kRows;
+  const bool wide = wide_prefix(B * R, prefix_len);
+  const int prefix_rows = wide ? kPrefixRows : kRows, prefix_keys = wide ? kPrefixKeys : kTileKeys;
+  const long long own_rt = (R + kRows - 1) / kRows;
+  const long long prefix_rt = (B * R + prefix_rows - 1) / prefix_rows;
   const long long most_tiles = (capacity + kTileKeys - 1) / kTileKeys;
-  const long long prefix_tiles = (static_cast<long long>(prefix_len) + kTileKeys - 1) / kTileKeys;
+  const long long prefix_tiles =
+      (static_cast<long long>(prefix_len) + prefix_keys - 1) / prefix_keys;
   if ((prefix_tiles * prefix_rt + most_tiles * own_rt * B) * Hk > 0xffffffffLL)
     return CP_ERR_SHAPE;
   if (device_cc() != 103) return CP_ERR_DEVICE;
@@ -883,13 +846,15 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
   p.lse = lse;
   p.err = device_error_word();
   if (!p.err) return CP_ERR_CUDA;
-  const Space sp(B, n_q, Hq, d, prefix_len);
+  const Space sp(B, n_q, Hq, Hk, d, prefix_len);
   char* const ws = static_cast<char*>(workspace);
   p.starts = reinterpret_cast<unsigned*>(ws + sp.starts);
   p.slot_o = reinterpret_cast<float*>(ws + sp.slot_o);
   p.slot_ml = reinterpret_cast<float*>(ws + sp.slot_ml);
   p.whole_o = reinterpret_cast<float*>(ws + sp.whole_o);
   p.whole_ml = reinterpret_cast<float*>(ws + sp.whole_ml);
+  p.pslot_o = reinterpret_cast<float*>(ws + sp.pslot_o);
+  p.pslot_ml = reinterpret_cast<float*>(ws + sp.pslot_ml);
   p.qb = q_strides ? q_strides[0] : static_cast<long long>(n_q) * Hq * d;
   p.qs = q_strides ? q_strides[1] : static_cast<long long>(Hq) * d;
   p.qh = q_strides ? q_strides[2] : d;
@@ -897,9 +862,15 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
   p.B = B; p.n_q = n_q; p.Hq = Hq; p.Hk = Hk;
   p.G = static_cast<int>(G); p.R = static_cast<int>(R);
   p.own_tiles_of_rows = static_cast<int>(own_rt);
-  p.prefix_tiles_of_rows = static_cast<int>(prefix_rt);
+  p.prefix_rows = prefix_rows;
+  p.prefix_row_tiles = static_cast<int>(prefix_rt);
   p.P = prefix_len;
   p.prefix_tiles = static_cast<int>(prefix_tiles);
+  if (wide)
+    p.prefix_grid = static_cast<int>(std::min<long long>(
+        std::min(kMaxPrefixGrid, sm_count()), prefix_tiles * prefix_rt * Hk));
+  p.timeout_ns = test_wait_limit_ns();
+  p.fault_drop_k = test_fault_drop();
   p.n_pages = cache->n_pages; p.page_size = cache->page_size;
   p.capacity = capacity;
   const bool e4m3 = cache->elem_bytes == 1;

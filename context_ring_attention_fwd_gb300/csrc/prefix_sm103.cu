@@ -1,0 +1,653 @@
+// The shared prefix of the decode attention on tcgen05: partial states of the
+// whole batch's rows over the prefix's keys.
+//
+// With B n_q G rows per key head, reading K and V once leaves the two
+// products, 4 d FLOP per row and key: from about 300 rows on the tensor pipe
+// bounds it, HBM below.  An item is 256 rows of one key head (two tiles of 128, the TMEM
+// lanes) over the prefix's 128-key tiles; the items' tiles are laid end to end
+// and every CTA of one per SM takes an equal stretch, so any number of rows
+// and heads fills the GPU.  An item cut between CTAs leaves its parts in their slots; the
+// join of paged_decode.cu merges them with the sequences' own keys.
+//
+// Roles (384 threads): two softmax warpgroups, one per row tile, a thread a
+// row; in the third, one warp that issues the MMAs and three that load K and V.
+//   S_t = Q_t K^T (both in shared memory), P_t back into S's TMEM columns in two
+//   halves of 64 keys, O_t += P_t V (P from TMEM), as in the ring forward
+//   (attn_sm103.cu); no row max on the way: P is taken against a reference
+//   that moves only when a row runs 2^64 (fp16 P: 2^8) past it.
+// The loader uses cp.async with the 128-byte swizzle written by address, so
+// pages of any size, order and stride cost the same; each thread orders its
+// finished copies before the tensor core's reads with a proxy fence and then
+// arrives.  E4M3 codes go through a second ring of 16 KB and are widened to
+// fp16 (exactly) on the way to the operand tile; Q is scaled per row and P by
+// 2^7 into fp16's range, as in paged_decode.cu.
+//
+// Registers: launched at 168 per thread; the third warpgroup drops to 104 and
+// the softmax warpgroups rise to 200 (the build checks the launch's count).  A
+// fourth warp per scheduler would cap the launch at 128.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "attn_common.cuh"
+#include "internal.h"
+#include "paged_decode.h"
+#include "ptx.cuh"
+
+namespace cpring {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8;
+constexpr int kLoadWarp0 = 9;
+constexpr int kLoadWarps = 3;
+constexpr int kLaunchRegs = 168;  // registers per thread at launch (checked by the build)
+constexpr int kSoftmaxRegs = 200;
+constexpr int kControlRegs = 104;
+static_assert(2 * kSoftmaxRegs + kControlRegs <= 3 * kLaunchRegs,
+              "the register split fits the launch");
+constexpr int kStages = 2;
+constexpr int kTmemCols = 512;  // S0 | S1 | O0 | O1
+
+template <int D, bool kE4M3>
+struct Lay {
+  static constexpr int kPanel = 128 * 128;           // 128 rows x 128 bytes
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTile = kPanels * kPanel;     // 128 rows of D 16-bit values
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + 2 * kTile;
+  static constexpr int kV = kK + kStages * kTile;
+  static constexpr int kCodes = kV + kStages * kTile;
+  static constexpr int kCodeTile = kE4M3 ? 128 * D : 0;
+  static constexpr int kBars = kCodes + 2 * kCodeTile;
+  static constexpr int kBytes = kBars + 256;
+  static constexpr int kAlloc = kBytes + 1024;       // room to align the base to 1024 B
+  static_assert(kAlloc <= 232448, "shared memory budget");
+};
+
+enum Bar : int {
+  kQFull = 0,    // + row tile
+  kKFull = 2,    // + stage
+  kVFull = 4,
+  kKEmpty = 6,
+  kVEmpty = 8,
+  kSFull = 10,   // + row tile
+  kPReady = 12,  // + row tile: keys 0-63 of P stored
+  kPReadyB = 14, // + row tile: keys 64-127
+  kOFull = 16,   // + row tile: the segment's last P V done
+  kDrain = 18,
+  kNumBars = 19
+};
+constexpr int kTmemSlot = kNumBars * 8;
+constexpr int kAbortSlot = kTmemSlot + 4;
+constexpr int kBadSlot = kTmemSlot + 8;
+static_assert(kBadSlot + 4 <= 256, "the barrier block");
+
+// A CTA's k-th segment: tiles [t0, t1) of an item.
+struct Segment {
+  int hk, row0, rows, t0, t1;
+  bool whole;
+};
+
+__device__ __forceinline__ bool segment_at(const DecodeParams& p, unsigned& w, unsigned w_end,
+                                           Segment& s) {
+  if (w >= w_end) return false;
+  const unsigned n = p.prefix_tiles;
+  const unsigned item = w / n;
+  s.t0 = static_cast<int>(w - item * n);
+  s.t1 = static_cast<int>(min(n, static_cast<unsigned>(s.t0) + (w_end - w)));
+  s.hk = static_cast<int>(item) / p.prefix_row_tiles;
+  s.row0 = (static_cast<int>(item) - s.hk * p.prefix_row_tiles) * kPrefixRows;
+  s.rows = min(kPrefixRows, p.B * p.R - s.row0);
+  s.whole = s.t0 == 0 && s.t1 == static_cast<int>(n);
+  w += static_cast<unsigned>(s.t1 - s.t0);
+  return true;
+}
+
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((static_cast<uint32_t>(N) >> 3) << 17) |
+         ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Four E4M3 codes to four fp16 values, exactly.
+__device__ __forceinline__ void widen(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(codes)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(codes >> 16)));
+}
+
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Largest of the scores of keys 64 * half .. + 63.
+__device__ __forceinline__ float half_max(const uint32_t (&sv)[4][32], int half) {
+  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+  for (int x = 0; x < 32; x += 2) {
+    m0 = max3f(m0, __uint_as_float(sv[2 * half][x]), __uint_as_float(sv[2 * half][x + 1]));
+    m1 = max3f(m1, __uint_as_float(sv[2 * half + 1][x]), __uint_as_float(sv[2 * half + 1][x + 1]));
+  }
+  return fmaxf(m0, m1);
+}
+// P = 2^(s sc - base) of those keys as 16-bit pairs, and its sum.
+template <bool kF16>
+__device__ __forceinline__ float exp_half(const uint32_t (&sv)[4][32], int half, float sc,
+                                          float base, uint32_t (&pk)[32]) {
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+  for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      float e0, e1;
+      ptx::fma_f32x2(e0, e1, __uint_as_float(sv[2 * half + cc][2 * x]),
+                     __uint_as_float(sv[2 * half + cc][2 * x + 1]), sc, sc, -base, -base);
+      const float p0 = ptx::ex2(e0), p1 = ptx::ex2(e1);
+      asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%0, %1};\n\tmov.b64 rb, {%2, %3};\n\t"
+          "add.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+          : "+f"(s0), "+f"(s1)
+          : "f"(p0), "f"(p1));
+      pk[cc * 16 + x] = kF16 ? pack_f16(p0, p1) : ptx::pack_bf16(p0, p1);
+    }
+  return s0 + s1;
+}
+
+template <int D, bool kE4M3>
+__global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const DecodeParams p) {
+  using L = Lay<D, kE4M3>;
+  constexpr float kShift = kE4M3 ? 7.f : 0.f;           // P is held times 2^kShift
+  constexpr float kGuardLog2 = kE4M3 ? 8.f : 64.f;      // P / 2^kShift stays below 2^kGuardLog2
+  constexpr float kGuard = kE4M3 ? 32768.f : 18446744073709551616.f;  // 2^(kGuardLog2 + kShift)
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = ptx::smem_u32(smem);
+  auto bar = [&](int i) -> uint32_t { return sbase + L::kBars + 8u * static_cast<uint32_t>(i); };
+  volatile uint32_t* const abort_flag =
+      reinterpret_cast<volatile uint32_t*>(smem + L::kBars + kAbortSlot);
+  volatile uint32_t* const bad_flag =
+      reinterpret_cast<volatile uint32_t*>(smem + L::kBars + kBadSlot);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBars + kTmemSlot);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(bar(kQFull + t), 128);
+      ptx::mbar_init(bar(kKFull + t), 32 * kLoadWarps);
+      ptx::mbar_init(bar(kVFull + t), 32 * kLoadWarps);
+      ptx::mbar_init(bar(kKEmpty + t), 1);
+      ptx::mbar_init(bar(kVEmpty + t), 1);
+      ptx::mbar_init(bar(kSFull + t), 1);
+      ptx::mbar_init(bar(kPReady + t), 128);
+      ptx::mbar_init(bar(kPReadyB + t), 128);
+      ptx::mbar_init(bar(kOFull + t), 1);
+    }
+    ptx::mbar_init(bar(kDrain), 1);
+    *abort_flag = 0u;
+    *bad_flag = 0u;
+    ptx::fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const unsigned W = static_cast<unsigned>(p.prefix_tiles) *
+                     static_cast<unsigned>(p.Hk * p.prefix_row_tiles);
+  unsigned w = stretch(blockIdx.x, W, gridDim.x);
+  const unsigned w_end = stretch(blockIdx.x + 1, W, gridDim.x);
+  Segment s;
+
+  if (warp >= kMmaWarp) ptx::setmaxnreg_dec<kControlRegs>();  // the whole third warpgroup
+  if (warp >= kLoadWarp0) {
+    // ------------------------------------------------------------ K and V
+    // One copy of a warp moves kRowsPer rows; the tile's copies are dealt to
+    // the three warps in turn.
+    const int lw = warp - kLoadWarp0;
+    constexpr int kRowChunks = D * (kE4M3 ? 1 : 2) / 16;  // 16-byte chunks of a cached row
+    constexpr int kRowsPer = 32 / kRowChunks;
+    constexpr int kAll = kPrefixKeys / kRowsPer;          // copies of a tile
+    constexpr int kCopies = (kAll + kLoadWarps - 1) / kLoadWarps;
+    static_assert(kCopies * kRowsPer <= 64, "two rows' places per lane");
+    const int chunk = lane % kRowChunks, sub = lane / kRowChunks;
+    bool ok = true;
+    // The places of the warp's rows of the next tile to be copied: its q-th
+    // row (of copy q / kRowsPer) in lane q % 32.
+    int page[2] = {-1, -1}, slot[2] = {0, 0};
+    auto look_up = [&](int tile, int t1) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int q = j * 32 + lane;
+        const int row = (lw + kLoadWarps * (q / kRowsPer)) * kRowsPer + q % kRowsPer;
+        const int key = tile * kPrefixKeys + row;
+        page[j] = -1;
+        if (tile < t1 && row < kPrefixKeys && key < p.P) {
+          const int at = key / p.page_size;
+          slot[j] = key - at * p.page_size;
+          page[j] = __ldg(p.prefix_pages + at);
+          if (page[j] < 0 || page[j] >= p.n_pages) {
+            page[j] = -1;
+            *bad_flag = 1u;
+          }
+        }
+      }
+    };
+    auto copy = [&](int x, int hk, uint32_t dst) {  // the warp's rows of K (0) or V (1)
+      long long off[2];
+      unsigned held[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        off[j] = page[j] >= 0 ? page[j] * p.cs[x][0] + slot[j] * p.cs[x][1] + hk * p.cs[x][2] : 0;
+        held[j] = __ballot_sync(0xffffffffu, page[j] >= 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        const int q = i * kRowsPer + sub;
+        constexpr int kHalf = 32 / kRowsPer;  // copies whose rows' places are the lanes' first
+        const long long o = __shfl_sync(0xffffffffu, off[i >= kHalf], q & 31);
+        const unsigned have = held[i >= kHalf] >> (q & 31) & 1u;
+        const int c = lw + kLoadWarps * i;    // of the tile's copies
+        if (c < kAll) {
+          const int row = c * kRowsPer + sub;
+          const uint32_t at = kE4M3 ? dst + (c * 32 + lane) * 16
+                                    : dst + (chunk >> 3) * L::kPanel + row * 128 +
+                                          (((chunk & 7) ^ (row & 7)) << 4);
+          cp_async16(at, p.cache[x] + o + chunk * 16, have ? 16 : 0);
+        }
+      }
+    };
+    // Step n copies K (n even) or V (n odd) of the CTA's tile n / 2, into stage
+    // (n / 2) % 2; its use of that buffer is number n / 4.
+    auto full = [&](unsigned n) { return bar((n & 1 ? kVFull : kKFull) + ((n >> 1) & 1)); };
+    auto empty = [&](unsigned n) { return bar((n & 1 ? kVEmpty : kKEmpty) + ((n >> 1) & 1)); };
+    auto buffer = [&](unsigned n) {
+      return sbase + (n & 1 ? L::kV : L::kK) + ((n >> 1) & 1) * L::kTile;
+    };
+    auto announce = [&](unsigned n) {
+      ptx::fence_proxy_async_shared();
+      // Test hook: the first K tile of CTA 0 is never announced.
+      if (!(p.fault_drop_k && blockIdx.x == 0 && n == 0)) ptx::mbar_arrive(full(n));
+    };
+    if (!kE4M3) {
+      unsigned n = 0, told = 0;  // steps copied, steps announced
+      while (ok && segment_at(p, w, w_end, s)) {
+        look_up(s.t0, s.t1);
+        for (int f = s.t0; ok && f < s.t1; ++f) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (n >= 4 &&
+                !__all_sync(0xffffffffu, ptx::mbar_try_wait(empty(n), ((n >> 2) - 1) & 1u))) {
+              // The buffer is still in use: announce what is under way first.
+              cp_wait<0>();
+              for (; told < n; ++told) announce(told);
+              if (!wait_warp(empty(n), ((n >> 2) - 1) & 1u, abort_flag, p)) {
+                ok = false;
+                break;
+              }
+            }
+            copy(x, s.hk, buffer(n));
+            if (x == 1) look_up(f + 1, s.t1);
+            cp_commit();
+            ++n;
+            if (n - told > 2) {
+              cp_wait<2>();
+              announce(told++);
+            }
+          }
+        }
+      }
+      cp_wait<0>();
+      if (ok)
+        for (; told < n; ++told) announce(told);
+    } else {
+      // Codes run two steps ahead through their own ring; a thread widens
+      // the chunks that it copied itself.
+      unsigned w2 = w;           // the copying walk
+      Segment c{};
+      int cf = 0;
+      unsigned copied = 0;
+      bool more = segment_at(p, w2, w_end, c);
+      if (more) {
+        cf = c.t0;
+        look_up(cf, c.t1);
+      }
+      auto copy_step = [&]() {
+        if (more) {
+          const int x = copied & 1;
+          copy(x, c.hk, sbase + L::kCodes + x * L::kCodeTile);
+          ++copied;
+          if (x == 1 && ++cf == c.t1) {
+            more = segment_at(p, w2, w_end, c);
+            if (more) {
+              cf = c.t0;
+              look_up(cf, c.t1);
+            }
+          } else if (x == 1) {
+            look_up(cf, c.t1);
+          }
+        }
+        cp_commit();
+      };
+      copy_step();
+      copy_step();
+      unsigned n = 0;
+      while (ok && segment_at(p, w, w_end, s)) {
+        for (int f = s.t0; ok && f < s.t1; ++f) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x, ++n) {
+            if (n >= 4 && !wait_warp(empty(n), ((n >> 2) - 1) & 1u, abort_flag, p)) {
+              ok = false;
+              break;
+            }
+            cp_wait<1>();
+            const uint32_t src = sbase + L::kCodes + x * L::kCodeTile + lane * 16;
+            const uint32_t dst = buffer(n);
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+              const int c = lw + kLoadWarps * i;
+              if (c >= kAll) break;
+              const int row = c * kRowsPer + sub;
+              uint32_t u[4], h[8];
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                           : "r"(src + c * 32 * 16));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) widen(u[e], h[2 * e], h[2 * e + 1]);
+              // 16 codes are two chunks; lanes of the row's second panel write
+              // theirs in the other order, so that eight lanes meet eight banks
+              const int c0 = 2 * chunk;
+              const uint32_t line = dst + (c0 >> 3) * L::kPanel + row * 128;
+              const bool swap = chunk & 4;
+              const uint32_t a0 = line + ((((c0 + swap) & 7) ^ (row & 7)) << 4);
+              const uint32_t a1 = line + ((((c0 + !swap) & 7) ^ (row & 7)) << 4);
+              ptx::st_shared_v4(a0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2],
+                                swap ? h[7] : h[3]);
+              ptx::st_shared_v4(a1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6],
+                                swap ? h[3] : h[7]);
+            }
+            announce(n);
+            copy_step();
+          }
+        }
+      }
+      cp_wait<0>();
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMAs
+    constexpr uint32_t kIdescQK =
+        kE4M3 ? idesc_f16_f32(128, 128, false) : ptx::idesc_bf16_f32(128, 128, false);
+    constexpr uint32_t kIdescPV =
+        kE4M3 ? idesc_f16_f32(128, D, true) : ptx::idesc_bf16_f32(128, D, true);
+    const uint64_t d_qk = ptx::smem_desc_sw128(sbase, 16, 1024);
+    const uint64_t d_v = ptx::smem_desc_sw128(sbase, L::kPanel, 1024);
+    uint32_t p_cnt[2] = {0, 0};
+    uint32_t it = 0, segs0 = 0, segs1 = 0;
+    bool ok = true;
+    auto issue_s = [&](int t, uint32_t st) {
+      const uint64_t dq = d_qk + ((L::kQ + t * L::kTile) >> 4);
+      const uint64_t dk = d_qk + ((L::kK + st * L::kTile) >> 4);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t step = static_cast<uint64_t>(((k >> 2) * L::kPanel + (k & 3) * 32) >> 4);
+        ptx::mma_ss_w(tmem + t * 128, dq + step, dk + step, kIdescQK, k > 0 ? 1u : 0u);
+      }
+      ptx::mma_commit_w(bar(kSFull + t));
+    };
+    while (ok && segment_at(p, w, w_end, s)) {
+      const bool two = s.rows > 128;
+      if (!wait_warp(bar(kQFull), segs0++ & 1u, abort_flag, p)) { ok = false; break; }
+      if (two && !wait_warp(bar(kQFull + 1), segs1++ & 1u, abort_flag, p)) { ok = false; break; }
+      ptx::tc_fence_after();
+      uint32_t prev_st = 0, prev_ph = 0;
+      bool v_ready = false;
+      // O_t (+)= P_t V of the previous key tile, each half once its P is there.
+      auto flush = [&](int t, bool first, bool last) -> bool {
+        if (!v_ready) {
+          if (!wait_warp(bar(kVFull + prev_st), prev_ph, abort_flag, p)) return false;
+          v_ready = true;
+        }
+        const uint64_t dv = d_v + ((L::kV + prev_st * L::kTile) >> 4);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!wait_warp(bar((half ? kPReadyB : kPReady) + t), p_cnt[t] & 1u, abort_flag, p))
+            return false;
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int k = half * 4; k < half * 4 + 4; ++k)
+            ptx::mma_ts_w(tmem + 256 + t * D, tmem + t * 128 + k * 8,
+                          dv + static_cast<uint64_t>((k * 16 * 128) >> 4), kIdescPV,
+                          (first && k == 0) ? 0u : 1u);
+        }
+        ++p_cnt[t];
+        if (last) ptx::mma_commit_w(bar(kOFull + t));
+        return true;
+      };
+      for (int f = s.t0; f < s.t1; ++f) {
+        const uint32_t st = it & 1u, ph = (it >> 1) & 1u;
+        if (f > s.t0 && !flush(0, f == s.t0 + 1, false)) { ok = false; break; }
+        if (!wait_warp(bar(kKFull + st), ph, abort_flag, p)) { ok = false; break; }
+        ptx::tc_fence_after();
+        issue_s(0, st);
+        if (two) {
+          if (f > s.t0 && !flush(1, f == s.t0 + 1, false)) { ok = false; break; }
+          issue_s(1, st);
+        }
+        ptx::mma_commit_w(bar(kKEmpty + st));
+        if (f > s.t0) ptx::mma_commit_w(bar(kVEmpty + prev_st));
+        prev_st = st;
+        prev_ph = ph;
+        v_ready = false;
+        ++it;
+      }
+      if (!ok) break;
+      const bool only = s.t1 == s.t0 + 1;
+      if (!flush(0, only, true) || (two && !flush(1, only, true))) { ok = false; break; }
+      ptx::mma_commit_w(bar(kVEmpty + prev_st));
+    }
+    ptx::mma_commit_w(bar(kDrain));
+    wait_warp(bar(kDrain), 0u, abort_flag, p, false);
+  } else {
+    // ------------------------------------------------------------ softmax
+    ptx::setmaxnreg_inc<kSoftmaxRegs>();
+    const int t = warp >> 2;                    // row tile
+    const int row_in_tile = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + static_cast<uint32_t>(t * 128);
+    const uint32_t tO = tmem + lane_off + 256u + static_cast<uint32_t>(t * D);
+    uint32_t s_cnt = 0, o_cnt = 0;
+    bool ok = true;
+    while (segment_at(p, w, w_end, s)) {
+      if (t * 128 >= s.rows) continue;
+      const int r = t * 128 + row_in_tile;      // of the item
+      const bool valid = r < s.rows;
+      const RowOf row(p, 0, s.hk, s.row0 + min(r, s.rows - 1));
+      float sc = p.scale;
+      if (ok) {
+        // ---- this row of Q into its place of the swizzled tile (every MMA on the
+        // previous segment's has finished: its last S or P V was waited for)
+        const uint4* const src = reinterpret_cast<const uint4*>(row.query(p));
+        uint4 v[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) v[i] = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        float up = 1.f;
+        if (kE4M3) {
+          float top = 0.f, down;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[e] << 16)),
+                                     fabsf(__uint_as_float(u[e] & 0xffff0000u))));
+          }
+          fp16_row_scale(top, up, down);
+          sc = p.scale * __ldg(p.descale[0] + s.hk) * down;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          if (kE4M3) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              u[e] = pack_f16(__uint_as_float(u[e] << 16) * up,
+                              __uint_as_float(u[e] & 0xffff0000u) * up);
+          }
+          ptx::st_shared_v4(sbase + L::kQ + t * L::kTile + (i >> 3) * L::kPanel +
+                                row_in_tile * 128 + (((i & 7) ^ (row_in_tile & 7)) << 4),
+                            u[0], u[1], u[2], u[3]);
+        }
+        ptx::fence_proxy_async_shared();
+        ptx::mbar_arrive(bar(kQFull + t));
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int f = s.t0; ok && f < s.t1; ++f) {
+        if (!wait_warp(bar(kSFull + t), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
+        ++s_cnt;
+        ptx::tc_fence_after();
+        uint32_t sv[4][32], pk[32];
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tS + ch * 32, sv[ch]);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) ptx::reg_fence(sv[ch]);
+        const int left = p.P - f * kPrefixKeys;  // keys of this tile that exist
+        if (left < kPrefixKeys) {
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (ch * 32 + x >= left) sv[ch][x] = __float_as_uint(-INFINITY);
+        }
+        bool fast = false;
+        if (f > s.t0) {
+          // P against the reference so far, its first half stored and signalled
+          // before the second is computed, if neither runs past the guard.
+          const float l1 = exp_half<kE4M3>(sv, 0, sc, m - kShift, pk);
+          const bool in_range = (l1 <= kGuard) &
+                                (half_max(sv, 1) * sc <= m + kGuardLog2);
+          fast = __all_sync(0xffffffffu, in_range);
+          if (fast) l += l1;
+        }
+        if (!fast) {
+          // A segment's first tile, or a row past the guard: the reference
+          // moves to this tile's maximum and O with it.
+          const float top = fmaxf(half_max(sv, 0), half_max(sv, 1)) * sc;
+          const bool move = f == s.t0 || top > m;
+          const float alpha = (f == s.t0 || !move) ? 1.f : ptx::ex2(m - top);
+          if (move) m = top == -INFINITY ? 0.f : top;
+          l *= alpha;
+          if (f > s.t0) {
+            // O_t holds the sum up to the previous tile: the MMA warp issued
+            // that P V before this tile's S, whose commit was waited for.
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ++ch) {
+              uint32_t ov[32];
+              ptx::tmem_ld32(tO + ch * 32, ov);
+              ptx::tmem_wait_ld();
+              ptx::reg_fence(ov);
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
+              ptx::tmem_st32(tO + ch * 32, ov);
+            }
+          }
+          l += exp_half<kE4M3>(sv, 0, sc, m - kShift, pk);
+        }
+        ptx::tmem_st32(tS, pk);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(kPReady + t));
+        l += exp_half<kE4M3>(sv, 1, sc, m - kShift, pk);
+        ptx::tmem_st32(tS + 32, pk);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(kPReadyB + t));
+      }
+      // ---- the segment's part: O, its reference and its sum
+      if (ok && !wait_warp(bar(kOFull + t), o_cnt & 1u, abort_flag, p)) ok = false;
+      ++o_cnt;
+      ptx::tc_fence_after();
+      const bool nan = !ok || *bad_flag != 0u;  // the part is marked, not left as it was
+      float *to, *ml;
+      if (s.whole) {
+        const long long at = static_cast<long long>(p.B) * p.n_q * p.Hq + row.index(p);
+        to = p.whole_o + at * D;
+        ml = p.whole_ml + at * 2;
+      } else {
+        const long long at =
+            (static_cast<long long>(blockIdx.x) * 2 + (s.t0 == 0 ? 1 : 0)) * kPrefixRows + r;
+        to = p.pslot_o + at * D;
+        ml = p.pslot_ml + at * 2;
+      }
+      if (ok) {
+        const float vd = kE4M3 ? __ldg(p.descale[1] + s.hk) : 1.f;
+#pragma unroll
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t ov[32];
+          ptx::tmem_ld32(tO + ch * 32, ov);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence(ov);
+          if (valid) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<float4*>(to + ch * 32 + 4 * x) = make_float4(
+                  __uint_as_float(ov[4 * x]) * vd, __uint_as_float(ov[4 * x + 1]) * vd,
+                  __uint_as_float(ov[4 * x + 2]) * vd, __uint_as_float(ov[4 * x + 3]) * vd);
+          }
+        }
+        ptx::tc_fence_before();
+      }
+      if (valid) *reinterpret_cast<float2*>(ml) = make_float2(m - kShift, nan ? NAN : l);
+    }
+    if (threadIdx.x == 0 && *bad_flag != 0u) atomicOr(p.err, kErrCache);
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool kE4M3>
+cudaError_t launch_t(const DecodeParams& p, cudaStream_t stream) {
+  using L = Lay<D, kE4M3>;
+  const cudaError_t e = ensure_smem_limit(
+      reinterpret_cast<const void*>(&prefix_attn_kernel<D, kE4M3>), L::kAlloc);
+  if (e != cudaSuccess) return e;
+  prefix_attn_kernel<D, kE4M3><<<p.prefix_grid, kThreads, L::kAlloc, stream>>>(p);
+  count_launch(0);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_attn(const DecodeParams& p, int d, bool e4m3, cudaStream_t stream) {
+  if (d == 128) return e4m3 ? launch_t<128, true>(p, stream) : launch_t<128, false>(p, stream);
+  return e4m3 ? launch_t<64, true>(p, stream) : launch_t<64, false>(p, stream);
+}
+
+}  // namespace cpring
