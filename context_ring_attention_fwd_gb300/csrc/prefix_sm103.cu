@@ -15,12 +15,21 @@
 //   halves of 64 keys, O_t += P_t V (P from TMEM), as in the ring forward
 //   (attn_sm103.cu); no row max on the way: P is taken against a reference
 //   that moves only when a row runs 2^64 (fp16 P: 2^8) past it.
-// The loader uses cp.async with the 128-byte swizzle written by address, so
-// pages of any size, order and stride cost the same; each thread orders its
-// finished copies before the tensor core's reads with a proxy fence and then
-// arrives.  E4M3 codes go through a second ring of 16 KB and are widened to
-// fp16 (exactly) on the way to the operand tile; Q is scaled per row and P by
-// 2^7 into fp16's range, as in paged_decode.cu.
+// Loading.  Pages whose size is a multiple of 8 come by TMA, one box per page
+// (or per largest power of two of rows that divides it) and 128-byte panel;
+// the rows of V behind the prefix's end are zeroed, whatever the page holds there.  Other
+// page sizes and stride orders that no tensor map describes come by cp.async
+// with the swizzle written by address, each thread ordering its finished copies
+// before the tensor core's reads with a proxy fence.
+//
+// E4M3, d = 128, by TMA: K's codes are the operand themselves.  A bf16 q has 8
+// significant bits, so it is the sum of two E4M3 values (exactly, but for
+// entries 2^-10 below the row's largest, which lose at most 2^-18 of that), and
+// S = q_hi K^T + q_lo K^T takes as long as one product in 16 bits.  P would
+// lose what lies 2^-18 below its reference in such a pair, so P V runs in fp16:
+// two warps widen V's codes on their way from a ring of 16 KB to the operand
+// tile, and P is held times 2^7, which leaves it 2^31 of range.  The
+// cp.async path widens K and V both.
 //
 // Registers: launched at 168 per thread; the third warpgroup drops to 104 and
 // the softmax warpgroups rise to 200 (the build checks the launch's count).  A
@@ -29,8 +38,10 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "attn_common.cuh"
 #include "internal.h"
@@ -42,7 +53,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8;
-constexpr int kLoadWarp0 = 9;
+constexpr int kLoadWarp0 = 9;     // by TMA: this warp loads, the next two widen V's codes
 constexpr int kLoadWarps = 3;
 constexpr int kLaunchRegs = 168;  // registers per thread at launch (checked by the build)
 constexpr int kSoftmaxRegs = 200;
@@ -52,34 +63,41 @@ static_assert(2 * kSoftmaxRegs + kControlRegs <= 3 * kLaunchRegs,
 constexpr int kStages = 2;
 constexpr int kTmemCols = 512;  // S0 | S1 | O0 | O1
 
-template <int D, bool kE4M3>
+template <int D, bool kE4M3, bool kTma>
 struct Lay {
+  static constexpr bool kCodesK = kE4M3 && kTma;     // S from E4M3 operands
   static constexpr int kPanel = 128 * 128;           // 128 rows x 128 bytes
   static constexpr int kPanels = D / 64;
   static constexpr int kTile = kPanels * kPanel;     // 128 rows of D 16-bit values
-  static constexpr int kQ = 0;
+  static constexpr int kKTile = kCodesK ? kPanel : kTile;
+  static constexpr int kKStages = kCodesK ? 4 : 2;
+  static constexpr int kQ = 0;                       // + row tile (codes: hi, then lo)
   static constexpr int kK = kQ + 2 * kTile;
-  static constexpr int kV = kK + kStages * kTile;
+  static constexpr int kV = kK + kKStages * kKTile;
   static constexpr int kCodes = kV + kStages * kTile;
   static constexpr int kCodeTile = kE4M3 ? 128 * D : 0;
   static constexpr int kBars = kCodes + 2 * kCodeTile;
   static constexpr int kBytes = kBars + 256;
   static constexpr int kAlloc = kBytes + 1024;       // room to align the base to 1024 B
   static_assert(kAlloc <= 232448, "shared memory budget");
+  static_assert(!kCodesK || D == 128, "one 128-byte panel of codes");
 };
 
 enum Bar : int {
-  kQFull = 0,    // + row tile
-  kKFull = 2,    // + stage
-  kVFull = 4,
-  kKEmpty = 6,
-  kVEmpty = 8,
-  kSFull = 10,   // + row tile
-  kPReady = 12,  // + row tile: keys 0-63 of P stored
-  kPReadyB = 14, // + row tile: keys 64-127
-  kOFull = 16,   // + row tile: the segment's last P V done
-  kDrain = 18,
-  kNumBars = 19
+  kQFull = 0,     // + row tile
+  kKFull = 2,     // + stage (4)
+  kKEmpty = 6,    // + stage (4)
+  kVFull = 10,    // + stage
+  kVEmpty = 12,
+  kSFull = 14,    // + row tile
+  kPReady = 16,   // + row tile: keys 0-63 of P stored
+  kPReadyB = 18,  // + row tile: keys 64-127
+  kOFull = 20,    // + row tile: the segment's last P V done
+  kCFull = 22,    // + buffer: V's codes landed
+  kCEmpty = 24,   // + buffer: widened
+  kTail = 26,     // V of the prefix's last tile landed
+  kDrain = 27,
+  kNumBars = 28
 };
 constexpr int kTmemSlot = kNumBars * 8;
 constexpr int kAbortSlot = kTmemSlot + 4;
@@ -132,6 +150,22 @@ __device__ __forceinline__ void widen(uint32_t codes, uint32_t& lo, uint32_t& hi
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(codes >> 16)));
 }
 
+// Stores 16 widened codes: chunks 2 c and 2 c + 1 of a row of the operand tile.
+// Lanes of a row's second panel write theirs in the other order, so that
+// eight lanes meet eight banks.
+__device__ __forceinline__ void store_widened(uint32_t tile, int panel, int row, int c,
+                                              const uint32_t (&h)[8]) {
+  const int c0 = 2 * c;
+  const uint32_t line = tile + (c0 >> 3) * panel + row * 128;
+  const bool swap = c & 4;
+  const uint32_t a0 = line + ((((c0 + swap) & 7) ^ (row & 7)) << 4);
+  const uint32_t a1 = line + ((((c0 + !swap) & 7) ^ (row & 7)) << 4);
+  ptx::st_shared_v4(a0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2],
+                    swap ? h[7] : h[3]);
+  ptx::st_shared_v4(a1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6],
+                    swap ? h[3] : h[7]);
+}
+
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -169,9 +203,17 @@ __device__ __forceinline__ float exp_half(const uint32_t (&sv)[4][32], int half,
   return s0 + s1;
 }
 
-template <int D, bool kE4M3>
-__global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const DecodeParams p) {
-  using L = Lay<D, kE4M3>;
+// How the TMA path finds a tile's rows: boxes of `rows` rows; the tensor maps'
+// dimensions are (d, head, token, page), or (d, token, head, page).
+struct Boxes {
+  int rows, token_first;
+};
+
+template <int D, bool kE4M3, bool kTma>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const Boxes boxes) {
+  using L = Lay<D, kE4M3, kTma>;
   constexpr float kShift = kE4M3 ? 7.f : 0.f;           // P is held times 2^kShift
   constexpr float kGuardLog2 = kE4M3 ? 8.f : 64.f;      // P / 2^kShift stays below 2^kGuardLog2
   constexpr float kGuard = kE4M3 ? 32768.f : 18446744073709551616.f;  // 2^(kGuardLog2 + kShift)
@@ -188,17 +230,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const DecodePa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    for (int t = 0; t < L::kKStages; ++t) {
+      ptx::mbar_init(bar(kKFull + t), kTma ? 1 : 32 * kLoadWarps);
+      ptx::mbar_init(bar(kKEmpty + t), 1);
+    }
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(bar(kQFull + t), 128);
-      ptx::mbar_init(bar(kKFull + t), 32 * kLoadWarps);
-      ptx::mbar_init(bar(kVFull + t), 32 * kLoadWarps);
-      ptx::mbar_init(bar(kKEmpty + t), 1);
+      ptx::mbar_init(bar(kVFull + t), !kTma ? 32 * kLoadWarps : kE4M3 ? 64 : 1);
       ptx::mbar_init(bar(kVEmpty + t), 1);
+      ptx::mbar_init(bar(kCFull + t), 1);
+      ptx::mbar_init(bar(kCEmpty + t), 64);
       ptx::mbar_init(bar(kSFull + t), 1);
       ptx::mbar_init(bar(kPReady + t), 128);
       ptx::mbar_init(bar(kPReadyB + t), 128);
       ptx::mbar_init(bar(kOFull + t), 1);
     }
+    ptx::mbar_init(bar(kTail), 1);
     ptx::mbar_init(bar(kDrain), 1);
     *abort_flag = 0u;
     *bad_flag = 0u;
@@ -220,8 +267,139 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const DecodePa
   Segment s;
 
   if (warp >= kMmaWarp) ptx::setmaxnreg_dec<kControlRegs>();  // the whole third warpgroup
-  if (warp >= kLoadWarp0) {
-    // ------------------------------------------------------------ K and V
+  if (kTma && warp == kLoadWarp0) {
+    // ------------------------------------------------------------ K and V by TMA
+    // Lane j brings box j of a tile: its page was looked up a tile earlier.
+    const int n_boxes = kPrefixKeys / boxes.rows;
+    int page = -1, slot = 0;
+    auto look_up = [&](int tile, int t1) {
+      const int key = tile * kPrefixKeys + lane * boxes.rows;
+      page = -1;
+      if (tile < t1 && lane < n_boxes && key < p.P) {
+        const int at = key / p.page_size;
+        slot = key - at * p.page_size;
+        page = __ldg(p.prefix_pages + at);
+        if (page < 0 || page >= p.n_pages) {
+          page = -1;
+          *bad_flag = 1u;
+        }
+      }
+    };
+    constexpr int kBoxCols = kE4M3 ? 128 : 64;  // of a panel
+    constexpr int kBoxPanels = kE4M3 ? 1 : L::kPanels;
+    auto bring = [&](const CUtensorMap* map, int hk, uint32_t dst, uint32_t full) {
+      const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
+      if (lane == 0)
+        ptx::mbar_arrive_expect_tx(
+            full, static_cast<uint32_t>(__popc(have) * boxes.rows * 128 * kBoxPanels));
+      __syncwarp();
+      if (page >= 0) {
+#pragma unroll
+        for (int pn = 0; pn < kBoxPanels; ++pn)
+          ptx::tma_load_4d(dst + pn * L::kPanel + lane * boxes.rows * 128, map, full,
+                           pn * kBoxCols, boxes.token_first ? slot : hk,
+                           boxes.token_first ? hk : slot, page);
+      }
+      __syncwarp();
+    };
+    uint32_t n = 0, nk = 0, nv = 0, tails = 0;  // tiles; K, V and last tiles under way
+    bool ok = true;
+    while (ok && segment_at(p, w, w_end, s)) {
+      look_up(s.t0, s.t1);
+      for (int f = s.t0; f < s.t1; ++f, ++n) {
+        const uint32_t ks = n % L::kKStages, ku = n / L::kKStages;
+        const uint32_t vs = n & 1u, vu = n >> 1;
+        if (ku > 0 && !wait_warp(bar(kKEmpty + ks), (ku - 1) & 1u, abort_flag, p)) {
+          ok = false;
+          break;
+        }
+        if (!(p.fault_drop_k && blockIdx.x == 0 && n == 0)) {  // test hook: one tile never comes
+          bring(&map_k, s.hk, sbase + L::kK + ks * L::kKTile, bar(kKFull + ks));
+          nk = n + 1;
+        }
+        const uint32_t v_empty = bar((kE4M3 ? kCEmpty : kVEmpty) + vs);
+        if (vu > 0 && !wait_warp(v_empty, (vu - 1) & 1u, abort_flag, p)) {
+          ok = false;
+          break;
+        }
+        const int left = p.P - f * kPrefixKeys;
+        if (kE4M3) {
+          bring(&map_v, s.hk, sbase + L::kCodes + vs * L::kCodeTile, bar(kCFull + vs));
+        } else if (left >= kPrefixKeys) {
+          bring(&map_v, s.hk, sbase + L::kV + vs * L::kTile, bar(kVFull + vs));
+        } else {
+          // The prefix ends in this tile: what its last page holds behind the
+          // end, and what no box brought, becomes zeros.
+          const uint32_t dst = sbase + L::kV + vs * L::kTile;
+          bring(&map_v, s.hk, dst, bar(kTail));
+          ++tails;
+          if (!wait_warp(bar(kTail), (tails - 1) & 1u, abort_flag, p)) {
+            ok = false;
+            break;
+          }
+          for (int x = left * 8 * L::kPanels + lane; x < kPrefixKeys * 8 * L::kPanels; x += 32) {
+            const int row = x / (8 * L::kPanels), c = x % (8 * L::kPanels);
+            ptx::st_shared_v4(dst + (c >> 3) * L::kPanel + row * 128 + (c & 7) * 16, 0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(kVFull + vs));
+        }
+        nv = n + 1;
+        look_up(f + 1, s.t1);
+      }
+    }
+    // Every copy under way lands before the CTA can exit: the last use of
+    // each buffer, of which the dropped tile was none.
+    for (uint32_t x = 0; x < L::kKStages; ++x) {
+      const uint32_t uses = nk > x ? (nk - x + L::kKStages - 1) / L::kKStages : 0u;
+      if (uses > 0 && !(p.fault_drop_k && blockIdx.x == 0 && x == 0))
+        wait_warp(bar(kKFull + x), (uses - 1) & 1u, abort_flag, p, false);
+    }
+    for (uint32_t x = 0; x < 2; ++x) {
+      const uint32_t uses = nv > x ? (nv - x + 1) / 2 : 0u;
+      if (uses > 0)
+        wait_warp(bar((kE4M3 ? kCFull : kVFull) + x), (uses - 1) & 1u, abort_flag, p, false);
+    }
+    if (tails > 0) wait_warp(bar(kTail), (tails - 1) & 1u, abort_flag, p, false);
+  } else if (kTma && warp > kLoadWarp0) {
+    // ------------------------------------------------------------ V's codes to fp16
+    if (kE4M3) {
+      const int tid = (warp - kLoadWarp0 - 1) * 32 + lane;
+      constexpr int kRowChunks = D / 16;
+      bool ok = true;
+      uint32_t n = 0;
+      while (ok && segment_at(p, w, w_end, s)) {
+        for (int f = s.t0; f < s.t1; ++f, ++n) {
+          const uint32_t vs = n & 1u, vu = n >> 1;
+          if (!wait_warp(bar(kCFull + vs), vu & 1u, abort_flag, p) ||
+              (vu > 0 && !wait_warp(bar(kVEmpty + vs), (vu - 1) & 1u, abort_flag, p))) {
+            ok = false;
+            break;
+          }
+          const int left = p.P - f * kPrefixKeys;
+          const uint32_t src = sbase + L::kCodes + vs * L::kCodeTile;
+          const uint32_t dst = sbase + L::kV + vs * L::kTile;
+          const int chunk = tid % kRowChunks;
+#pragma unroll 8
+          for (int i = 0; i < 128 * kRowChunks / 64; ++i) {
+            const int row = (i * 64 + tid) / kRowChunks;
+            uint32_t u[4], h[8];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                         : "r"(src + (i * 64 + tid) * 16));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) widen(row < left ? u[e] : 0u, h[2 * e], h[2 * e + 1]);
+            store_widened(dst, L::kPanel, row, chunk, h);
+          }
+          ptx::fence_proxy_async_shared();
+          ptx::mbar_arrive(bar(kVFull + vs));
+          ptx::mbar_arrive(bar(kCEmpty + vs));
+        }
+      }
+    }
+  } else if (!kTma && warp >= kLoadWarp0) {
+    // ------------------------------------------------------------ K and V by cp.async
     // One copy of a warp moves kRowsPer rows; the tile's copies are dealt to
     // the three warps in turn.
     const int lw = warp - kLoadWarp0;
@@ -374,17 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const DecodePa
                            : "r"(src + c * 32 * 16));
 #pragma unroll
               for (int e = 0; e < 4; ++e) widen(u[e], h[2 * e], h[2 * e + 1]);
-              // 16 codes are two chunks; lanes of the row's second panel write
-              // theirs in the other order, so that eight lanes meet eight banks
-              const int c0 = 2 * chunk;
-              const uint32_t line = dst + (c0 >> 3) * L::kPanel + row * 128;
-              const bool swap = chunk & 4;
-              const uint32_t a0 = line + ((((c0 + swap) & 7) ^ (row & 7)) << 4);
-              const uint32_t a1 = line + ((((c0 + !swap) & 7) ^ (row & 7)) << 4);
-              ptx::st_shared_v4(a0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2],
-                                swap ? h[7] : h[3]);
-              ptx::st_shared_v4(a1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6],
-                                swap ? h[3] : h[7]);
+              store_widened(dst, L::kPanel, row, chunk, h);
             }
             announce(n);
             copy_step();
@@ -395,8 +563,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const DecodePa
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
-    constexpr uint32_t kIdescQK =
-        kE4M3 ? idesc_f16_f32(128, 128, false) : ptx::idesc_bf16_f32(128, 128, false);
+    constexpr uint32_t kIdescQK = L::kCodesK ? ptx::idesc_e4m3_f32(128, 128)
+                                  : kE4M3    ? idesc_f16_f32(128, 128, false)
+                                             : ptx::idesc_bf16_f32(128, 128, false);
     constexpr uint32_t kIdescPV =
         kE4M3 ? idesc_f16_f32(128, D, true) : ptx::idesc_bf16_f32(128, D, true);
     const uint64_t d_qk = ptx::smem_desc_sw128(sbase, 16, 1024);
@@ -406,11 +575,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const DecodePa
     bool ok = true;
     auto issue_s = [&](int t, uint32_t st) {
       const uint64_t dq = d_qk + ((L::kQ + t * L::kTile) >> 4);
-      const uint64_t dk = d_qk + ((L::kK + st * L::kTile) >> 4);
+      const uint64_t dk = d_qk + ((L::kK + st * L::kKTile) >> 4);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint64_t step = static_cast<uint64_t>(((k >> 2) * L::kPanel + (k & 3) * 32) >> 4);
-        ptx::mma_ss_w(tmem + t * 128, dq + step, dk + step, kIdescQK, k > 0 ? 1u : 0u);
+        if (L::kCodesK)  // k-steps of 32 codes: the low parts' panel follows the high ones'
+          ptx::mma_ss_f8_w(tmem + t * 128, dq + step,
+                           dk + static_cast<uint64_t>(((k & 3) * 32) >> 4), kIdescQK,
+                           k > 0 ? 1u : 0u);
+        else
+          ptx::mma_ss_w(tmem + t * 128, dq + step, dk + step, kIdescQK, k > 0 ? 1u : 0u);
       }
       ptx::mma_commit_w(bar(kSFull + t));
     };
@@ -444,16 +618,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const DecodePa
         return true;
       };
       for (int f = s.t0; f < s.t1; ++f) {
-        const uint32_t st = it & 1u, ph = (it >> 1) & 1u;
+        const uint32_t st = it & 1u, ph = (it >> 1) & 1u;  // V's
+        const uint32_t kst = it % L::kKStages, kph = (it / L::kKStages) & 1u;
         if (f > s.t0 && !flush(0, f == s.t0 + 1, false)) { ok = false; break; }
-        if (!wait_warp(bar(kKFull + st), ph, abort_flag, p)) { ok = false; break; }
+        if (!wait_warp(bar(kKFull + kst), kph, abort_flag, p)) { ok = false; break; }
         ptx::tc_fence_after();
-        issue_s(0, st);
+        issue_s(0, kst);
         if (two) {
           if (f > s.t0 && !flush(1, f == s.t0 + 1, false)) { ok = false; break; }
-          issue_s(1, st);
+          issue_s(1, kst);
         }
-        ptx::mma_commit_w(bar(kKEmpty + st));
+        ptx::mma_commit_w(bar(kKEmpty + kst));
         if (f > s.t0) ptx::mma_commit_w(bar(kVEmpty + prev_st));
         prev_st = st;
         prev_ph = ph;
@@ -503,19 +678,50 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const DecodePa
           }
           fp16_row_scale(top, up, down);
           sc = p.scale * __ldg(p.descale[0] + s.hk) * down;
-        }
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          if (kE4M3) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              u[e] = pack_f16(__uint_as_float(u[e] << 16) * up,
-                              __uint_as_float(u[e] & 0xffff0000u) * up);
+          if (L::kCodesK) {  // to [2^7, 2^8): the pair saturates at 448
+            up *= 0x1p-7f;
+            sc *= 0x1p+7f;
+            if (!(top < INFINITY)) sc = NAN;  // nor has it an infinity
           }
-          ptx::st_shared_v4(sbase + L::kQ + t * L::kTile + (i >> 3) * L::kPanel +
-                                row_in_tile * 128 + (((i & 7) ^ (row_in_tile & 7)) << 4),
-                            u[0], u[1], u[2], u[3]);
+        }
+        if (L::kCodesK) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4& x = v[2 * i + (e >> 1)];
+              const uint32_t u0 = (e & 1) ? x.z : x.x, u1 = (e & 1) ? x.w : x.y;
+              const float z0 = __uint_as_float(u0 << 16) * up;
+              const float z1 = __uint_as_float(u0 & 0xffff0000u) * up;
+              const float z2 = __uint_as_float(u1 << 16) * up;
+              const float z3 = __uint_as_float(u1 & 0xffff0000u) * up;
+              hi[e] = ptx::pack_e4m3x4(z0, z1, z2, z3);
+              uint32_t h01, h23;
+              widen(hi[e], h01, h23);
+              const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+              const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+              lo[e] = ptx::pack_e4m3x4(z0 - a.x, z1 - a.y, z2 - b.x, z3 - b.y);
+            }
+            const uint32_t at = sbase + L::kQ + t * L::kTile + row_in_tile * 128 +
+                                ((i ^ (row_in_tile & 7)) << 4);
+            ptx::st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+            ptx::st_shared_v4(at + L::kPanel, lo[0], lo[1], lo[2], lo[3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            if (kE4M3) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                u[e] = pack_f16(__uint_as_float(u[e] << 16) * up,
+                                __uint_as_float(u[e] & 0xffff0000u) * up);
+            }
+            ptx::st_shared_v4(sbase + L::kQ + t * L::kTile + (i >> 3) * L::kPanel +
+                                  row_in_tile * 128 + (((i & 7) ^ (row_in_tile & 7)) << 4),
+                              u[0], u[1], u[2], u[3]);
+          }
         }
         ptx::fence_proxy_async_shared();
         ptx::mbar_arrive(bar(kQFull + t));
@@ -632,13 +838,47 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const DecodePa
   }
 }
 
-template <int D, bool kE4M3>
-cudaError_t launch_t(const DecodeParams& p, cudaStream_t stream) {
-  using L = Lay<D, kE4M3>;
+// K or V as (d, head, token, page) or (d, token, head, page), the smaller
+// stride first; a box is one panel of `rows` tokens of a head.  False where the
+// strides are not multiples of one another in that order.
+bool make_page_map(CUtensorMap* m, const DecodeParams& p, int x, int d, bool e4m3, bool swizzled,
+                   const Boxes& boxes) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t e = e4m3 ? 1 : 2;
+  struct Dim { cuuint64_t n, stride; cuuint32_t box; };
+  Dim dim[3] = {{static_cast<cuuint64_t>(p.Hk), static_cast<cuuint64_t>(p.cs[x][2]), 1},
+                {static_cast<cuuint64_t>(p.page_size), static_cast<cuuint64_t>(p.cs[x][1]),
+                 static_cast<cuuint32_t>(boxes.rows)},
+                {static_cast<cuuint64_t>(p.n_pages), static_cast<cuuint64_t>(p.cs[x][0]), 1}};
+  if (boxes.token_first) std::swap(dim[0], dim[1]);
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d)}, strides[3], inner = d * e;
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / e)};
+  for (int i = 0; i < 3; ++i) {
+    if (dim[i].n == 1) dim[i].stride = inner;  // never used
+    if (dim[i].stride % inner != 0) return false;
+    inner = strides[i] = dim[i].stride;
+    dims[i + 1] = dim[i].n;
+    box[i + 1] = dim[i].box;
+  }
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<uint8_t*>(p.cache[x]), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kE4M3, bool kTma>
+cudaError_t launch_t(const DecodeParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
+                     const Boxes& boxes, cudaStream_t stream) {
+  using L = Lay<D, kE4M3, kTma>;
   const cudaError_t e = ensure_smem_limit(
-      reinterpret_cast<const void*>(&prefix_attn_kernel<D, kE4M3>), L::kAlloc);
+      reinterpret_cast<const void*>(&prefix_attn_kernel<D, kE4M3, kTma>), L::kAlloc);
   if (e != cudaSuccess) return e;
-  prefix_attn_kernel<D, kE4M3><<<p.prefix_grid, kThreads, L::kAlloc, stream>>>(p);
+  prefix_attn_kernel<D, kE4M3, kTma>
+      <<<p.prefix_grid, kThreads, L::kAlloc, stream>>>(p, mk, mv, boxes);
   count_launch(0);
   return cudaGetLastError();
 }
@@ -646,8 +886,26 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_prefix_attn(const DecodeParams& p, int d, bool e4m3, cudaStream_t stream) {
-  if (d == 128) return e4m3 ? launch_t<128, true>(p, stream) : launch_t<128, false>(p, stream);
-  return e4m3 ? launch_t<64, true>(p, stream) : launch_t<64, false>(p, stream);
+  CUtensorMap mk{}, mv{};
+  Boxes boxes{p.page_size & -p.page_size, 0};
+  boxes.rows = std::min(boxes.rows, kPrefixKeys);
+  // TMA needs boxes of whole 8-row swizzle groups, one order of strides for K and V,
+  // and a 128-byte panel of codes.
+  const bool hnd = p.page_size > 1 && p.Hk > 1 && p.cs[0][1] < p.cs[0][2];
+  boxes.token_first = hnd;
+  const bool tma = boxes.rows >= 8 && !(e4m3 && d == 64) &&
+                   make_page_map(&mk, p, 0, d, e4m3, true, boxes) &&
+                   make_page_map(&mv, p, 1, d, e4m3, !e4m3, boxes);
+  if (d == 128) {
+    if (e4m3)
+      return tma ? launch_t<128, true, true>(p, mk, mv, boxes, stream)
+                 : launch_t<128, true, false>(p, mk, mv, boxes, stream);
+    return tma ? launch_t<128, false, true>(p, mk, mv, boxes, stream)
+               : launch_t<128, false, false>(p, mk, mv, boxes, stream);
+  }
+  if (e4m3) return launch_t<64, true, false>(p, mk, mv, boxes, stream);
+  return tma ? launch_t<64, false, true>(p, mk, mv, boxes, stream)
+             : launch_t<64, false, false>(p, mk, mv, boxes, stream);
 }
 
 }  // namespace cpring
