@@ -61,6 +61,7 @@ constexpr int kRows = 16;                        // rows of an item
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxGrid = 320;                    // bounds the slots of the workspace
 constexpr int kMaxBatch = 4096;
+constexpr int kMaxParts = 2 * kMaxGrid;          // of a row: its own item's and the prefix's
 constexpr int kMaxQueries = 16;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -88,18 +89,20 @@ __device__ __forceinline__ int common_keys(const DecodeParams& p, int len) {
   return max(0, len - (p.n_q - 1) - p.P);
 }
 
-__device__ __forceinline__ unsigned own_tiles(const DecodeParams& p, int b) {
+// Units of sequence b's items.
+__device__ __forceinline__ unsigned own_units(const DecodeParams& p, int b) {
   const int n = common_keys(p, __ldg(p.seq_lens + b));
   return n <= 0 ? 0u
-                : static_cast<unsigned>((n + kTileKeys - 1) / kTileKeys) *
+                : (static_cast<unsigned>((n + kTileKeys - 1) / kTileKeys) + kItemCost) *
                       static_cast<unsigned>(p.Hk * p.own_tiles_of_rows);
 }
 
-// Tiles of the prefix in this kernel's own list.
-__device__ __forceinline__ unsigned prefix_work(const DecodeParams& p) {
-  return p.prefix_grid > 0 ? 0u
-                           : static_cast<unsigned>(p.prefix_tiles) *
-                                 static_cast<unsigned>(p.Hk * p.prefix_row_tiles);
+// Units of the prefix in this kernel's own list.
+__device__ __forceinline__ unsigned prefix_units(const DecodeParams& p) {
+  return p.prefix_grid > 0 || p.P == 0
+             ? 0u
+             : (static_cast<unsigned>(p.prefix_tiles) + kItemCost) *
+                   static_cast<unsigned>(p.Hk * p.prefix_row_tiles);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -169,14 +172,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   const int quad = lane >> 2, c4 = lane & 3;
   const uint32_t ring = ptx::smem_u32(smem) + warp * St::kRing;
 
-  // ---- the sequences' first tiles (every CTA scans the lengths; CTA 0 keeps
+  cudaTriggerProgrammaticLaunchCompletion();  // the next kernel's blocks may line up
+  // ---- the sequences' first units (every CTA scans the lengths; CTA 0 keeps
   // the result for the join) and this CTA's stretch
-  const unsigned prefix_all = prefix_work(p);
+  const unsigned prefix_all = prefix_units(p);
   unsigned* const starts = reinterpret_cast<unsigned*>(smem + kWarps * St::kRing);
   unsigned run = prefix_all;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    const unsigned n = b < p.B ? own_tiles(p, b) : 0u;
+    const unsigned n = b < p.B ? own_units(p, b) : 0u;
     unsigned x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -208,16 +212,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
   const unsigned w_end = stretch(blockIdx.x + 1, W, g);
 
   while (w < w_end) {
-    // ---- the item that holds tile w
+    // ---- the item that holds unit w
     bool prefix;
-    int b0, hk, row0, rows, n_keys, base_pos, t0;
-    unsigned n_tiles;
+    int b0, hk, row0, rows, n_keys, base_pos;
+    unsigned n_tiles, u0;
     const int32_t* pages;
     if (w < prefix_all) {
       prefix = true;
       n_tiles = p.prefix_tiles;
-      const unsigned item = w / n_tiles;
-      t0 = static_cast<int>(w - item * n_tiles);
+      const unsigned item = w / (n_tiles + kItemCost);
+      u0 = w - item * (n_tiles + kItemCost);
       hk = static_cast<int>(item) / p.prefix_row_tiles;
       row0 = (static_cast<int>(item) - hk * p.prefix_row_tiles) * kRows;
       rows = min(kRows, p.B * p.R - row0);
@@ -236,42 +240,46 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       n_keys = common_keys(p, __ldg(p.seq_lens + b0));
       n_tiles = (n_keys + kTileKeys - 1) / kTileKeys;
       const unsigned local = w - starts[b0];
-      const unsigned item = local / n_tiles;
-      t0 = static_cast<int>(local - item * n_tiles);
+      const unsigned item = local / (n_tiles + kItemCost);
+      u0 = local - item * (n_tiles + kItemCost);
       hk = static_cast<int>(item) / p.own_tiles_of_rows;
       row0 = (static_cast<int>(item) - hk * p.own_tiles_of_rows) * kRows;
       rows = min(kRows, p.R - row0);
       base_pos = p.P;
       pages = p.table + b0 * p.table_stride;
     }
-    const int t1 = static_cast<int>(min(n_tiles, static_cast<unsigned>(t0) + (w_end - w)));
+    const unsigned u1 = min(n_tiles + kItemCost, u0 + (w_end - w));
+    const int t0 = tile_of_unit(u0), t1 = tile_of_unit(u1);
+    w += u1 - u0;
+    if (t0 >= t1) continue;
 
-    // ---- this warp's loads of tile t: 16 keys, whose pages were looked up
-    // one tile earlier
-    int next_page = -1, next_slot = 0;
+    // ---- this warp's loads of tile t: 16 keys, whose pages are looked up
+    // before (the first tiles' together, later ones' one tile ahead)
+    struct Place {
+      int page, slot;
+    };
     bool bad = false;
     auto look_up = [&](int t) {
+      Place at{-1, 0};
       const int key = t * kTileKeys + warp * kWarpKeys + lane;
-      next_page = -1;
       if (lane < kWarpKeys && t < t1 && key < n_keys) {
-        const int at = (base_pos + key) / p.page_size;
-        next_slot = base_pos + key - at * p.page_size;
-        next_page = __ldg(pages + at);
-        if (next_page < 0 || next_page >= p.n_pages) {
-          next_page = -1;
-          bad = true;
-        }
+        const int x = (base_pos + key) / p.page_size;
+        at.slot = base_pos + key - x * p.page_size;
+        at.page = __ldg(pages + x);
       }
+      return at;
     };
-    auto load = [&](int t, int stage) {
+    auto load = [&](int t, int stage, Place at) {
       if (t < t1) {
         const uint32_t dst = ring + stage * St::kBytes;
-        const bool have = next_page >= 0;
+        const bool have = at.page >= 0 && at.page < p.n_pages;
+        if (!have && lane < kWarpKeys && t * kTileKeys + warp * kWarpKeys + lane < n_keys)
+          bad = true;
         long long off[2] = {0, 0};
         if (have) {
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            off[x] = next_page * p.cs[x][0] + next_slot * p.cs[x][1] + hk * p.cs[x][2];
+            off[x] = at.page * p.cs[x][0] + at.slot * p.cs[x][1] + hk * p.cs[x][2];
         }
         constexpr int kPerStep = 32 / St::kChunks;  // keys per warp-wide access
         const int chunk = lane % St::kChunks;
@@ -286,14 +294,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
                        p.cache[x] + o + chunk * 16, (held >> key & 1u) ? 16 : 0);
           }
         }
-        look_up(t + 1);
       }
       cp_commit();
     };
-    look_up(t0);
+    Place next;
+    {
+      Place first[St::kCount];
 #pragma unroll
-    for (int i = 0; i < St::kCount - 1; ++i) load(t0 + i, i);
-
+      for (int i = 0; i < St::kCount; ++i) first[i] = look_up(t0 + i);
+#pragma unroll
+      for (int i = 0; i < St::kCount - 1; ++i) load(t0 + i, i, first[i]);
+      next = first[St::kCount - 1];
+    }
     // ---- Q fragments: rows quad and quad + 8 of the item
     uint32_t qf[kK][4];
     float sc0 = p.scale, sc1 = p.scale;
@@ -352,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     for (int t = t0; t < t1; ++t) {
       cp_wait<St::kCount - 2>();
       __syncwarp();
-      load(t + St::kCount - 1, stage == 0 ? St::kCount - 1 : stage - 1);
+      load(t + St::kCount - 1, stage == 0 ? St::kCount - 1 : stage - 1, next);
+      next = look_up(t + St::kCount);
       const uint32_t ks = ring + stage * St::kBytes;
       const uint32_t vs = ks + St::kBytes / 2;
       if (++stage == St::kCount) stage = 0;
@@ -556,20 +569,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     }
     if (any_bad && threadIdx.x == 0) atomicOr(p.err, kErrCache);
     __syncthreads();  // the ring is free again
-    w += static_cast<unsigned>(t1 - t0);
   }
 }
 
-// The parts of one row's item whose tiles are [first, first + n) of W: where
-// the x-th lies.
+// Where the parts of one row of an item lie: `count` of them, the x-th in
+// the slots of CTA c0 + x, or the one in the array of finished items.
 struct Parts {
+  const float* o;
+  const float* ml;
   unsigned c0, count;
-  bool whole;
-  __device__ Parts(unsigned first, unsigned n, unsigned W, unsigned g) {
-    c0 = holder(first, W, g);
-    const unsigned c1 = holder(first + n - 1, W, g);
-    whole = c0 == c1;
-    count = c1 - c0 + 1;
+  int rows, r;  // a slot's rows; this row
+  // n > 0 tiles, the item's first unit of W over g CTAs.
+  __device__ void find(unsigned first, unsigned n, unsigned W, unsigned g) {
+    c0 = holder(first + kItemCost, W, g);
+    count = holder(first + kItemCost + n - 1, W, g) - c0 + 1;
+  }
+  __device__ long long at(unsigned x) const {
+    return rows == 0 ? r : (static_cast<long long>(c0 + x) * 2 + (x == 0 ? 1 : 0)) * rows + r;
   }
 };
 
@@ -578,6 +594,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
   constexpr int kCols = D / 32;  // columns per lane
   __shared__ float part_m[kWarps], part_l[kWarps];
   __shared__ float part_o[kWarps][D];
+  __shared__ float weight[kMaxParts];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   cudaGridDependencySynchronize();
   const long long rid = blockIdx.x;  // (b, i, h)
@@ -585,6 +602,8 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
   const long long bi = rid / p.Hq;
   const int i = static_cast<int>(bi % p.n_q), b = static_cast<int>(bi / p.n_q);
   const int hk = h / p.G;
+  const unsigned W = p.starts[p.B];
+  const unsigned first_own = p.starts[b];
   const int len = __ldg(p.seq_lens + b);
   const int common = common_keys(p, len);
   const long long lse_at = (static_cast<long long>(b) * p.Hq + h) * p.n_q + i;
@@ -598,62 +617,91 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
     }
     return;
   }
-  const unsigned W = p.starts[p.B];
   const unsigned g = min(grid, W);
-  const unsigned n_own = static_cast<unsigned>((common + kTileKeys - 1) / kTileKeys);
+  const long long all_rows = static_cast<long long>(p.B) * p.n_q * p.Hq;
   const int r_own = i * p.G + h % p.G;
-  const long long r_prefix = static_cast<long long>(b) * p.R + r_own;
-  float m = -INFINITY, l = 0.f;
+  Parts own{p.slot_o, p.slot_ml, 0, 0, kRows, r_own % kRows};
+  if (common > 0) {
+    const unsigned n = static_cast<unsigned>((common + kTileKeys - 1) / kTileKeys);
+    own.find(first_own + (hk * p.own_tiles_of_rows + r_own / kRows) * (n + kItemCost), n, W, g);
+    if (own.count == 1) {
+      if (p.P == 0 && p.n_q == 1) return;  // written by the item's CTA
+      own = Parts{p.whole_o + rid * D, p.whole_ml + rid * 2, 0, 1, 0, 0};
+    }
+  }
+  Parts pre{p.slot_o, p.slot_ml, 0, 0, p.prefix_rows, 0};
+  if (p.P > 0) {
+    const bool wide = p.prefix_grid > 0;  // prefix_attn_kernel's parts
+    const int row = b * p.R + r_own;
+    const unsigned n = static_cast<unsigned>(p.prefix_tiles), units = n + kItemCost;
+    if (wide) {
+      pre.o = p.pslot_o;
+      pre.ml = p.pslot_ml;
+    }
+    pre.r = row % p.prefix_rows;
+    pre.find((hk * p.prefix_row_tiles + row / p.prefix_rows) * units, n,
+             wide ? units * static_cast<unsigned>(p.Hk * p.prefix_row_tiles) : W,
+             wide ? static_cast<unsigned>(p.prefix_grid) : g);
+    if (pre.count == 1)
+      pre = Parts{p.whole_o + (all_rows + rid) * D, p.whole_ml + (all_rows + rid) * 2, 0, 1, 0, 0};
+  }
+  // ---- the parts' weights against their common maximum: one thread a part
+  const int n_parts = static_cast<int>(own.count + pre.count);
+  float m_here = -INFINITY;
+  for (int x = threadIdx.x; x < n_parts; x += kThreads) {
+    const bool o = x < static_cast<int>(own.count);
+    const float* const ml = o ? own.ml + own.at(x) * 2 : pre.ml + pre.at(x - own.count) * 2;
+    m_here = fmaxf(m_here, __ldcg(ml));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m_here = fmaxf(m_here, __shfl_xor_sync(0xffffffffu, m_here, o));
+  if (lane == 0) part_m[warp] = m_here;
+  __syncthreads();
+  float m = fmaxf(fmaxf(part_m[0], part_m[1]), fmaxf(part_m[2], part_m[3]));
+  float l = 0.f;
+  for (int x = threadIdx.x; x < n_parts; x += kThreads) {
+    const bool o = x < static_cast<int>(own.count);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(
+        o ? own.ml + own.at(x) * 2 : pre.ml + pre.at(x - own.count) * 2));
+    const bool empty = ml.x == -INFINITY;  // its l is 0, or NaN
+    const float f = empty ? 0.f : ptx::ex2(ml.x - m);
+    weight[x] = f;
+    l += empty ? ml.y : ml.y * f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  __syncthreads();
+  // ---- the parts' O, dealt to the warps
   float o[kCols];
 #pragma unroll
   for (int x = 0; x < kCols; ++x) o[x] = 0.f;
+#pragma unroll 4
+  for (int x = warp; x < n_parts; x += kWarps) {
+    const bool from_own = x < static_cast<int>(own.count);
+    const float* const src =
+        (from_own ? own.o + own.at(x) * D : pre.o + pre.at(x - own.count) * D) + lane * kCols;
+    const float f = weight[x];
+    if (kCols == 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+      o[0] = fmaf(v.x, f, o[0]);
+      o[1] = fmaf(v.y, f, o[1]);
+      o[kCols - 2] = fmaf(v.z, f, o[kCols - 2]);
+      o[kCols - 1] = fmaf(v.w, f, o[kCols - 1]);
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+      o[0] = fmaf(v.x, f, o[0]);
+      o[1] = fmaf(v.y, f, o[1]);
+    }
+  }
   auto add = [&](float mx, float lx, const float (&ox)[kCols]) {
     const float big = fmaxf(m, mx);
     const float a = m == -INFINITY ? 0.f : ptx::ex2(m - big);
     const float c = mx == -INFINITY ? 0.f : ptx::ex2(mx - big);
-    l = l * a + (mx == -INFINITY ? lx : lx * c);  // an empty part's l is 0, or NaN
+    l = (m == -INFINITY ? l : l * a) + (mx == -INFINITY ? lx : lx * c);
 #pragma unroll
     for (int x = 0; x < kCols; ++x) o[x] = o[x] * a + ox[x] * c;
     m = big;
   };
-  auto take = [&](const float* from, const float* ml) {
-    const float2 v = *reinterpret_cast<const float2*>(ml);
-    float ox[kCols];
-#pragma unroll
-    for (int x = 0; x < kCols; ++x) ox[x] = from[lane * kCols + x];
-    add(v.x, v.y, ox);
-  };
-  // the parts of this row's two items, dealt to the warps
-#pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {  // own, prefix
-    const unsigned n = kind ? static_cast<unsigned>(p.prefix_tiles) : n_own;
-    if (n == 0) continue;
-    const bool wide = kind && p.prefix_grid > 0;  // prefix_attn_kernel's parts
-    const int item_rows = kind ? p.prefix_rows : kRows;
-    const long long row = kind ? r_prefix : r_own;
-    const unsigned item = static_cast<unsigned>(
-        hk * (kind ? p.prefix_row_tiles : p.own_tiles_of_rows) + row / item_rows);
-    const int r = static_cast<int>(row % item_rows);
-    const unsigned all =
-        wide ? n * static_cast<unsigned>(p.Hk * p.prefix_row_tiles) : W;
-    const Parts parts((kind ? 0u : p.starts[b]) + item * n, n, all,
-                      wide ? static_cast<unsigned>(p.prefix_grid) : g);
-    if (parts.whole) {
-      if (!kind && p.P == 0 && p.n_q == 1) return;  // written by the item's CTA
-      if (warp == 0) {
-        const long long at = (kind ? static_cast<long long>(p.B) * p.n_q * p.Hq : 0) + rid;
-        take(p.whole_o + at * D, p.whole_ml + at * 2);
-      }
-      continue;
-    }
-    const float* const slots_o = wide ? p.pslot_o : p.slot_o;
-    const float* const slots_ml = wide ? p.pslot_ml : p.slot_ml;
-    for (unsigned x = warp; x < parts.count; x += kWarps) {
-      const long long at =
-          (static_cast<long long>(parts.c0 + x) * 2 + (x == 0 ? 1 : 0)) * item_rows + r;
-      take(slots_o + at * D, slots_ml + at * 2);
-    }
-  }
   // the keys behind the common ones that this query sees, one per warp at a time
   const int pos0 = max(len - p.n_q + 1, p.P);
   const int pos1 = len - p.n_q + i;
@@ -695,6 +743,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
       add(dot * p.scale, 1.f, kv[1]);
     }
   }
+  __syncthreads();  // part_m has been read
   if (lane == 0) {
     part_m[warp] = m;
     part_l[warp] = bad ? NAN : l;
@@ -750,10 +799,6 @@ struct Space {
 template <int D, bool kE4M3>
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   using St = Stage<D, kE4M3>;
-  if (p.prefix_grid > 0) {
-    const cudaError_t e = launch_prefix_attn(p, D, kE4M3, stream);
-    if (e != cudaSuccess) return e;
-  }
   static_assert(kWarps * St::kRing >= kWarps * kRows * (D + 8) * 4, "the join fits the ring");
   const int smem = kWarps * St::kRing + 4 * (p.B + 1);
   const int most = kWarps * St::kRing + 4 * (kMaxBatch + 1);
@@ -765,6 +810,10 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   count_launch(2);
+  if (p.prefix_grid > 0) {
+    e = launch_prefix_attn(p, D, kE4M3, stream);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
@@ -816,7 +865,7 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
     return CP_ERR_ALIGN;
   if (workspace_bytes < cp_paged_attn_decode_workspace_bytes(B, n_q, Hq, Hk, d, prefix_len))
     return CP_ERR_BUFFER;
-  // the tiles of a call are counted in 32 bits
+  // the units of a call are counted in 32 bits
   const long long G = Hq / Hk, R = G * n_q;
   const bool wide = wide_prefix(B * R, prefix_len);
   const int prefix_rows = wide ? kPrefixRows : kRows, prefix_keys = wide ? kPrefixKeys : kTileKeys;
@@ -825,7 +874,8 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
   const long long most_tiles = (capacity + kTileKeys - 1) / kTileKeys;
   const long long prefix_tiles =
       (static_cast<long long>(prefix_len) + prefix_keys - 1) / prefix_keys;
-  if ((prefix_tiles * prefix_rt + most_tiles * own_rt * B) * Hk > 0xffffffffLL)
+  if (((prefix_tiles + kItemCost) * prefix_rt + (most_tiles + kItemCost) * own_rt * B) * Hk >
+      0xffffffffLL)
     return CP_ERR_SHAPE;
   if (device_cc() != 103) return CP_ERR_DEVICE;
   DecodeParams p{};

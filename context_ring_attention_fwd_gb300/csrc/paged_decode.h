@@ -23,7 +23,7 @@ struct DecodeParams {
   unsigned long long timeout_ns;
   int fault_drop_k;
   // workspace
-  unsigned* starts;  // [B + 1] first own tile of each sequence's items
+  unsigned* starts;  // [B + 1] first unit of each sequence's items
   float* slot_o;     // [grid][2][16][d]
   float* slot_ml;    // [grid][2][16][2]
   float* whole_o;    // [2][rows][d]: items finished by one CTA but owed a join (own, prefix)
@@ -45,13 +45,23 @@ struct DecodeParams {
   long long capacity;        // max_pages * page_size
 };
 
-// CTA c's stretch of W tiles over g CTAs starts at c W / g; the CTA whose
-// stretch holds tile w.
+// Both kernels lay their items end to end in units, kItemCost of them for
+// starting and ending an item and one for each of its key tiles, and give every
+// CTA c of g an equal stretch of the W units, from c W / g on.  An item's cost
+// units come first; the CTA that holds only those has no part of it.
+// (Measured: an item's loads of pages and queries, its pipeline's filling and
+// its state's writing take about as long as that many tiles.)
+constexpr unsigned kItemCost = 2;
 __device__ __forceinline__ unsigned stretch(unsigned c, unsigned W, unsigned g) {
   return static_cast<unsigned>(static_cast<unsigned long long>(c) * W / g);
 }
+// The CTA whose stretch holds unit w.
 __device__ __forceinline__ unsigned holder(unsigned w, unsigned W, unsigned g) {
   return static_cast<unsigned>((static_cast<unsigned long long>(w + 1ull) * g - 1) / W);
+}
+// Tiles [t0, t1) of an item for units [u0, u1) of it.
+__device__ __forceinline__ int tile_of_unit(unsigned u) {
+  return u > kItemCost ? static_cast<int>(u - kItemCost) : 0;
 }
 
 // Row r of an item: its place in q, and its index (b, i, h) in [B, n_q, Hq].

@@ -104,7 +104,7 @@ constexpr int kAbortSlot = kTmemSlot + 4;
 constexpr int kBadSlot = kTmemSlot + 8;
 static_assert(kBadSlot + 4 <= 256, "the barrier block");
 
-// A CTA's k-th segment: tiles [t0, t1) of an item.
+// A CTA's next segment: tiles [t0, t1) of an item.
 struct Segment {
   int hk, row0, rows, t0, t1;
   bool whole;
@@ -112,16 +112,20 @@ struct Segment {
 
 __device__ __forceinline__ bool segment_at(const DecodeParams& p, unsigned& w, unsigned w_end,
                                            Segment& s) {
-  if (w >= w_end) return false;
-  const unsigned n = p.prefix_tiles;
-  const unsigned item = w / n;
-  s.t0 = static_cast<int>(w - item * n);
-  s.t1 = static_cast<int>(min(n, static_cast<unsigned>(s.t0) + (w_end - w)));
-  s.hk = static_cast<int>(item) / p.prefix_row_tiles;
-  s.row0 = (static_cast<int>(item) - s.hk * p.prefix_row_tiles) * kPrefixRows;
+  const unsigned n = static_cast<unsigned>(p.prefix_tiles) + kItemCost;
+  do {
+    if (w >= w_end) return false;
+    const unsigned item = w / n;
+    const unsigned u0 = w - item * n;
+    const unsigned u1 = min(n, u0 + (w_end - w));
+    s.t0 = tile_of_unit(u0);
+    s.t1 = tile_of_unit(u1);
+    s.hk = static_cast<int>(item) / p.prefix_row_tiles;
+    s.row0 = (static_cast<int>(item) - s.hk * p.prefix_row_tiles) * kPrefixRows;
+    w += u1 - u0;
+  } while (s.t0 >= s.t1);
   s.rows = min(kPrefixRows, p.B * p.R - s.row0);
-  s.whole = s.t0 == 0 && s.t1 == static_cast<int>(n);
-  w += static_cast<unsigned>(s.t1 - s.t0);
+  s.whole = s.t0 == 0 && s.t1 == p.prefix_tiles;
   return true;
 }
 
@@ -148,6 +152,25 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ void widen(uint32_t codes, uint32_t& lo, uint32_t& hi) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(codes)));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(codes >> 16)));
+}
+
+// Four bf16 values times `up` as E4M3 codes and the codes of what those leave.
+// fp16 holds the scaled values, and the differences, exactly.
+__device__ __forceinline__ void split4(uint32_t x01, uint32_t x23, float up, uint32_t& hi,
+                                       uint32_t& lo) {
+  uint32_t z[2], back[2];
+  uint16_t h[2], r[2];
+  z[0] = pack_f16(__uint_as_float(x01 << 16) * up, __uint_as_float(x01 & 0xffff0000u) * up);
+  z[1] = pack_f16(__uint_as_float(x23 << 16) * up, __uint_as_float(x23 & 0xffff0000u) * up);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h[i]) : "r"(z[i]));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back[i]) : "h"(h[i]));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(z[i]) : "r"(back[i]));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r[i]) : "r"(z[i]));
+  }
+  hi = static_cast<uint32_t>(h[0]) | (static_cast<uint32_t>(h[1]) << 16);
+  lo = static_cast<uint32_t>(r[0]) | (static_cast<uint32_t>(r[1]) << 16);
 }
 
 // Stores 16 widened codes: chunks 2 c and 2 c + 1 of a row of the operand tile.
@@ -185,22 +208,49 @@ __device__ __forceinline__ float half_max(const uint32_t (&sv)[4][32], int half)
 template <bool kF16>
 __device__ __forceinline__ float exp_half(const uint32_t (&sv)[4][32], int half, float sc,
                                           float base, uint32_t (&pk)[32]) {
-  float s0 = 0.f, s1 = 0.f;
+  uint64_t acc = 0;  // two fp32 sums
 #pragma unroll
   for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
     for (int x = 0; x < 16; ++x) {
       float e0, e1;
-      ptx::fma_f32x2(e0, e1, __uint_as_float(sv[2 * half + cc][2 * x]),
-                     __uint_as_float(sv[2 * half + cc][2 * x + 1]), sc, sc, -base, -base);
+      asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+          "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
+          "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+          : "=f"(e0), "=f"(e1)
+          : "f"(__uint_as_float(sv[2 * half + cc][2 * x])),
+            "f"(__uint_as_float(sv[2 * half + cc][2 * x + 1])), "f"(sc), "f"(-base));
       const float p0 = ptx::ex2(e0), p1 = ptx::ex2(e1);
-      asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%0, %1};\n\tmov.b64 rb, {%2, %3};\n\t"
-          "add.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
-          : "+f"(s0), "+f"(s1)
+      asm("{\n\t.reg .b64 rp;\n\tmov.b64 rp, {%1, %2};\n\tadd.rn.f32x2 %0, %0, rp;\n\t}"
+          : "+l"(acc)
           : "f"(p0), "f"(p1));
       pk[cc * 16 + x] = kF16 ? pack_f16(p0, p1) : ptx::pack_bf16(p0, p1);
     }
-  return s0 + s1;
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(acc));
+  return lo + hi;
+}
+
+// Eight TMEM columns of this lane times alpha.
+__device__ __forceinline__ void scale8(uint32_t taddr, float alpha) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+  ptx::tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    asm volatile("" : "+r"(r[i]));
+    r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+  }
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::
+                   "r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
 }
 
 // How the TMA path finds a tile's rows: boxes of `rows` rows; the tensor maps'
@@ -260,10 +310,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const unsigned W = static_cast<unsigned>(p.prefix_tiles) *
+  cudaTriggerProgrammaticLaunchCompletion();  // the join's blocks may line up
+  const unsigned W = (static_cast<unsigned>(p.prefix_tiles) + kItemCost) *
                      static_cast<unsigned>(p.Hk * p.prefix_row_tiles);
   unsigned w = stretch(blockIdx.x, W, gridDim.x);
   const unsigned w_end = stretch(blockIdx.x + 1, W, gridDim.x);
+  // Test hook: the launch's first K tile never comes.
+  const bool drop = p.fault_drop_k && blockIdx.x == holder(kItemCost, W, gridDim.x);
   Segment s;
 
   if (warp >= kMmaWarp) ptx::setmaxnreg_dec<kControlRegs>();  // the whole third warpgroup
@@ -313,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        if (!(p.fault_drop_k && blockIdx.x == 0 && n == 0)) {  // test hook: one tile never comes
+        if (!(drop && n == 0)) {
           bring(&map_k, s.hk, sbase + L::kK + ks * L::kKTile, bar(kKFull + ks));
           nk = n + 1;
         }
@@ -353,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // each buffer, of which the dropped tile was none.
     for (uint32_t x = 0; x < L::kKStages; ++x) {
       const uint32_t uses = nk > x ? (nk - x + L::kKStages - 1) / L::kKStages : 0u;
-      if (uses > 0 && !(p.fault_drop_k && blockIdx.x == 0 && x == 0))
+      if (uses > 0 && !(drop && x == 0))
         wait_warp(bar(kKFull + x), (uses - 1) & 1u, abort_flag, p, false);
     }
     for (uint32_t x = 0; x < 2; ++x) {
@@ -464,8 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto announce = [&](unsigned n) {
       ptx::fence_proxy_async_shared();
-      // Test hook: the first K tile of CTA 0 is never announced.
-      if (!(p.fault_drop_k && blockIdx.x == 0 && n == 0)) ptx::mbar_arrive(full(n));
+      if (!(drop && n == 0)) ptx::mbar_arrive(full(n));
     };
     if (!kE4M3) {
       unsigned n = 0, told = 0;  // steps copied, steps announced
@@ -652,13 +704,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_off + 256u + static_cast<uint32_t>(t * D);
     uint32_t s_cnt = 0, o_cnt = 0;
     bool ok = true;
+    unsigned w_seg = w;
     while (segment_at(p, w, w_end, s)) {
-      if (t * 128 >= s.rows) continue;
-      const int r = t * 128 + row_in_tile;      // of the item
-      const bool valid = r < s.rows;
-      const RowOf row(p, 0, s.hk, s.row0 + min(r, s.rows - 1));
+      if (t * 128 >= s.rows) { w_seg = w; continue; }
       float sc = p.scale;
       if (ok) {
+        const int r = t * 128 + row_in_tile;    // of the item
+        const bool valid = r < s.rows;
+        const RowOf row(p, 0, s.hk, s.row0 + min(r, s.rows - 1));
         // ---- this row of Q into its place of the swizzled tile (every MMA on the
         // previous segment's has finished: its last S or P V was waited for)
         const uint4* const src = reinterpret_cast<const uint4*>(row.query(p));
@@ -691,17 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint4& x = v[2 * i + (e >> 1)];
-              const uint32_t u0 = (e & 1) ? x.z : x.x, u1 = (e & 1) ? x.w : x.y;
-              const float z0 = __uint_as_float(u0 << 16) * up;
-              const float z1 = __uint_as_float(u0 & 0xffff0000u) * up;
-              const float z2 = __uint_as_float(u1 << 16) * up;
-              const float z3 = __uint_as_float(u1 & 0xffff0000u) * up;
-              hi[e] = ptx::pack_e4m3x4(z0, z1, z2, z3);
-              uint32_t h01, h23;
-              widen(hi[e], h01, h23);
-              const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h01));
-              const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h23));
-              lo[e] = ptx::pack_e4m3x4(z0 - a.x, z1 - a.y, z2 - b.x, z3 - b.y);
+              split4((e & 1) ? x.z : x.x, (e & 1) ? x.w : x.y, up, hi[e], lo[e]);
             }
             const uint32_t at = sbase + L::kQ + t * L::kTile + row_in_tile * 128 +
                                 ((i ^ (row_in_tile & 7)) << 4);
@@ -727,7 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_arrive(bar(kQFull + t));
       }
       float m = -INFINITY, l = 0.f;
-      for (int f = s.t0; ok && f < s.t1; ++f) {
+      const int first = s.t0, end = s.t1;
+      for (int f = first; ok && f < end; ++f) {
         if (!wait_warp(bar(kSFull + t), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
         ++s_cnt;
         ptx::tc_fence_after();
@@ -745,82 +789,114 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 32; ++x)
               if (ch * 32 + x >= left) sv[ch][x] = __float_as_uint(-INFINITY);
         }
-        bool fast = false;
-        if (f > s.t0) {
+        const float ref = m - kShift;
+        bool in_range = false;
+        if (f > first) {
           // P against the reference so far, its first half stored and signalled
           // before the second is computed, if neither runs past the guard.
-          const float l1 = exp_half<kE4M3>(sv, 0, sc, m - kShift, pk);
-          const bool in_range = (l1 <= kGuard) &
-                                (half_max(sv, 1) * sc <= m + kGuardLog2);
-          fast = __all_sync(0xffffffffu, in_range);
-          if (fast) l += l1;
-        }
-        if (!fast) {
-          // A segment's first tile, or a row past the guard: the reference
-          // moves to this tile's maximum and O with it.
-          const float top = fmaxf(half_max(sv, 0), half_max(sv, 1)) * sc;
-          const bool move = f == s.t0 || top > m;
-          const float alpha = (f == s.t0 || !move) ? 1.f : ptx::ex2(m - top);
-          if (move) m = top == -INFINITY ? 0.f : top;
-          l *= alpha;
-          if (f > s.t0) {
-            // O_t holds the sum up to the previous tile: the MMA warp issued
-            // that P V before this tile's S, whose commit was waited for.
-#pragma unroll
-            for (int ch = 0; ch < D / 32; ++ch) {
-              uint32_t ov[32];
-              ptx::tmem_ld32(tO + ch * 32, ov);
-              ptx::tmem_wait_ld();
-              ptx::reg_fence(ov);
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
-              ptx::tmem_st32(tO + ch * 32, ov);
-            }
+          const float l1 = exp_half<kE4M3>(sv, 0, sc, ref, pk);
+          in_range = (l1 <= kGuard) & (half_max(sv, 1) * sc <= m + kGuardLog2);
+          if (__all_sync(0xffffffffu, in_range)) {
+            ptx::tmem_st32(tS, pk);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(kPReady + t));
+            l += l1 + exp_half<kE4M3>(sv, 1, sc, ref, pk);
+            ptx::tmem_st32(tS + 32, pk);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(kPReadyB + t));
+            continue;
           }
-          l += exp_half<kE4M3>(sv, 0, sc, m - kShift, pk);
         }
-        ptx::tmem_st32(tS, pk);
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(bar(kPReady + t));
-        l += exp_half<kE4M3>(sv, 1, sc, m - kShift, pk);
-        ptx::tmem_st32(tS + 32, pk);
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(bar(kPReadyB + t));
+        // A segment's first tile, or a row of this warp past the guard: such a
+        // row's reference moves to this tile's maximum and O with it; the other
+        // rows get what they had above.
+        const float top = fmaxf(half_max(sv, 0), half_max(sv, 1)) * sc;
+        const bool move = f == first || (!in_range && top > m);
+        const float alpha = (f == first || !move) ? 1.f : ptx::ex2(m - top);
+        if (move) m = top == -INFINITY ? 0.f : top;
+        l *= alpha;
+        if (f > first) {
+          // O_t holds the sum up to the previous tile: the MMA warp issued
+          // that P V before this tile's S, whose commit was waited for.
+          // Eight columns at a time: the scores stay in registers.
+#pragma unroll 1
+          for (int ch = 0; ch < D / 8; ++ch) scale8(tO + ch * 8, alpha);
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          sum += exp_half<kE4M3>(sv, half, sc, m - kShift, pk);
+          ptx::tmem_st32(tS + 32 * half, pk);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar((half ? kPReadyB : kPReady) + t));
+        }
+        l += sum;
       }
-      // ---- the segment's part: O, its reference and its sum
+      // ---- the segment's part: O, its reference and its sum.  Where it goes is
+      // worked out again, so that the loop above holds no registers for it.
+      asm volatile("" : "+r"(w_seg));
+      segment_at(p, w_seg, w_end, s);
+      const int r = t * 128 + row_in_tile;
+      const bool valid = r < s.rows;
       if (ok && !wait_warp(bar(kOFull + t), o_cnt & 1u, abort_flag, p)) ok = false;
       ++o_cnt;
       ptx::tc_fence_after();
       const bool nan = !ok || *bad_flag != 0u;  // the part is marked, not left as it was
+      long long at;
       float *to, *ml;
       if (s.whole) {
-        const long long at = static_cast<long long>(p.B) * p.n_q * p.Hq + row.index(p);
+        const RowOf row(p, 0, s.hk, s.row0 + min(r, s.rows - 1));
+        at = static_cast<long long>(p.B) * p.n_q * p.Hq + row.index(p);
         to = p.whole_o + at * D;
         ml = p.whole_ml + at * 2;
       } else {
-        const long long at =
-            (static_cast<long long>(blockIdx.x) * 2 + (s.t0 == 0 ? 1 : 0)) * kPrefixRows + r;
+        at = (static_cast<long long>(blockIdx.x) * 2 + (s.t0 == 0 ? 1 : 0)) * kPrefixRows + r;
         to = p.pslot_o + at * D;
         ml = p.pslot_ml + at * 2;
       }
       if (ok) {
+        // Through this warp's rows of the Q tile, which nothing reads any more:
+        // half a row per round and lane goes in, whole lines come out.
         const float vd = kE4M3 ? __ldg(p.descale[1] + s.hk) : 1.f;
+        constexpr int kCols = 32 * L::kPanels;       // columns of a round
+        constexpr int kLineChunks = kCols / 4;       // 16-byte chunks of a row's round
+        const uint32_t mine = sbase + L::kQ + t * L::kTile + (warp & 3) * 32 * 128;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += kCols) {
 #pragma unroll
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t ov[32];
-          ptx::tmem_ld32(tO + ch * 32, ov);
-          ptx::tmem_wait_ld();
-          ptx::reg_fence(ov);
-          if (valid) {
+          for (int pn = 0; pn < L::kPanels; ++pn) {
+            uint32_t ov[32];
+            ptx::tmem_ld32(tO + c0 + pn * 32, ov);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence(ov);
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-              *reinterpret_cast<float4*>(to + ch * 32 + 4 * x) = make_float4(
-                  __uint_as_float(ov[4 * x]) * vd, __uint_as_float(ov[4 * x + 1]) * vd,
-                  __uint_as_float(ov[4 * x + 2]) * vd, __uint_as_float(ov[4 * x + 3]) * vd);
+              ptx::st_shared_v4(mine + pn * L::kPanel + lane * 128 + ((x ^ (lane & 7)) << 4),
+                                __float_as_uint(__uint_as_float(ov[4 * x]) * vd),
+                                __float_as_uint(__uint_as_float(ov[4 * x + 1]) * vd),
+                                __float_as_uint(__uint_as_float(ov[4 * x + 2]) * vd),
+                                __float_as_uint(__uint_as_float(ov[4 * x + 3]) * vd));
           }
+          __syncwarp();
+          constexpr int kRowsPer = 32 / kLineChunks;
+          const int chunk = lane % kLineChunks;
+#pragma unroll 4
+          for (int i = 0; i < kLineChunks; ++i) {
+            const int row = i * kRowsPer + lane / kLineChunks;
+            float* const dst = reinterpret_cast<float*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), row));
+            uint32_t u[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                         : "r"(mine + (chunk >> 3) * L::kPanel + row * 128 +
+                               (((chunk & 7) ^ (row & 7)) << 4)));
+            if (t * 128 + (warp & 3) * 32 + row < s.rows)
+              *reinterpret_cast<uint4*>(dst + c0 + chunk * 4) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          __syncwarp();
         }
         ptx::tc_fence_before();
       }
@@ -829,6 +905,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *bad_flag != 0u) atomicOr(p.err, kErrCache);
   }
 
+  // The join waits for this kernel alone, so this kernel ends after the one
+  // before it (the sequences' own keys), next to which it runs.
+  if (threadIdx.x == 0) cudaGridDependencySynchronize();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -877,10 +956,18 @@ cudaError_t launch_t(const DecodeParams& p, const CUtensorMap& mk, const CUtenso
   const cudaError_t e = ensure_smem_limit(
       reinterpret_cast<const void*>(&prefix_attn_kernel<D, kE4M3, kTma>), L::kAlloc);
   if (e != cudaSuccess) return e;
-  prefix_attn_kernel<D, kE4M3, kTma>
-      <<<p.prefix_grid, kThreads, L::kAlloc, stream>>>(p, mk, mv, boxes);
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.prefix_grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kAlloc;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
   count_launch(0);
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, prefix_attn_kernel<D, kE4M3, kTma>, p, mk, mv, boxes);
 }
 
 }  // namespace
