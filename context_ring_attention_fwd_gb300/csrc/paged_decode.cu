@@ -61,7 +61,6 @@ constexpr int kRows = 16;                        // rows of an item
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxGrid = 320;                    // bounds the slots of the workspace
 constexpr int kMaxBatch = 4096;
-constexpr int kMaxParts = 2 * kMaxGrid;          // of a row: its own item's and the prefix's
 constexpr int kMaxQueries = 16;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -594,20 +593,18 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
   constexpr int kCols = D / 32;  // columns per lane
   __shared__ float part_m[kWarps], part_l[kWarps];
   __shared__ float part_o[kWarps][D];
-  __shared__ float weight[kMaxParts];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   cudaGridDependencySynchronize();
-  const long long rid = blockIdx.x;  // (b, i, h)
-  const int h = static_cast<int>(rid % p.Hq);
-  const long long bi = rid / p.Hq;
-  const int i = static_cast<int>(bi % p.n_q), b = static_cast<int>(bi / p.n_q);
+  const int rid = static_cast<int>(blockIdx.x);  // (b, i, h), below 2^24
+  const int bi = rid / p.Hq, h = rid - bi * p.Hq;
+  const int b = bi / p.n_q, i = bi - b * p.n_q;
   const int hk = h / p.G;
   const unsigned W = p.starts[p.B];
   const unsigned first_own = p.starts[b];
   const int len = __ldg(p.seq_lens + b);
   const int common = common_keys(p, len);
   const long long lse_at = (static_cast<long long>(b) * p.Hq + h) * p.n_q + i;
-  __nv_bfloat16* const out = p.out + rid * D;
+  __nv_bfloat16* const out = p.out + static_cast<long long>(rid) * D;
   if (len == 0 || common < 0) {
     const float v = len == 0 ? 0.f : NAN;
     for (int x = threadIdx.x; x < D; x += kThreads) out[x] = __float2bfloat16_rn(v);
@@ -618,7 +615,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
     return;
   }
   const unsigned g = min(grid, W);
-  const long long all_rows = static_cast<long long>(p.B) * p.n_q * p.Hq;
+  const long long whole = rid, whole_pre = static_cast<long long>(p.B) * p.n_q * p.Hq + rid;
   const int r_own = i * p.G + h % p.G;
   Parts own{p.slot_o, p.slot_ml, 0, 0, kRows, r_own % kRows};
   if (common > 0) {
@@ -626,7 +623,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
     own.find(first_own + (hk * p.own_tiles_of_rows + r_own / kRows) * (n + kItemCost), n, W, g);
     if (own.count == 1) {
       if (p.P == 0 && p.n_q == 1) return;  // written by the item's CTA
-      own = Parts{p.whole_o + rid * D, p.whole_ml + rid * 2, 0, 1, 0, 0};
+      own = Parts{p.whole_o + whole * D, p.whole_ml + whole * 2, 0, 1, 0, 0};
     }
   }
   Parts pre{p.slot_o, p.slot_ml, 0, 0, p.prefix_rows, 0};
@@ -643,55 +640,55 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
              wide ? units * static_cast<unsigned>(p.Hk * p.prefix_row_tiles) : W,
              wide ? static_cast<unsigned>(p.prefix_grid) : g);
     if (pre.count == 1)
-      pre = Parts{p.whole_o + (all_rows + rid) * D, p.whole_ml + (all_rows + rid) * 2, 0, 1, 0, 0};
+      pre = Parts{p.whole_o + whole_pre * D, p.whole_ml + whole_pre * 2, 0, 1, 0, 0};
   }
-  // ---- the parts' weights against their common maximum: one thread a part
-  const int n_parts = static_cast<int>(own.count + pre.count);
-  float m_here = -INFINITY;
-  for (int x = threadIdx.x; x < n_parts; x += kThreads) {
-    const bool o = x < static_cast<int>(own.count);
-    const float* const ml = o ? own.ml + own.at(x) * 2 : pre.ml + pre.at(x - own.count) * 2;
-    m_here = fmaxf(m_here, __ldcg(ml));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m_here = fmaxf(m_here, __shfl_xor_sync(0xffffffffu, m_here, o));
-  if (lane == 0) part_m[warp] = m_here;
-  __syncthreads();
-  float m = fmaxf(fmaxf(part_m[0], part_m[1]), fmaxf(part_m[2], part_m[3]));
-  float l = 0.f;
-  for (int x = threadIdx.x; x < n_parts; x += kThreads) {
-    const bool o = x < static_cast<int>(own.count);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(
-        o ? own.ml + own.at(x) * 2 : pre.ml + pre.at(x - own.count) * 2));
-    const bool empty = ml.x == -INFINITY;  // its l is 0, or NaN
-    const float f = empty ? 0.f : ptx::ex2(ml.x - m);
-    weight[x] = f;
-    l += empty ? ml.y : ml.y * f;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  __syncthreads();
-  // ---- the parts' O, dealt to the warps
+  // ---- the parts, dealt to the warps: kBatch of a warp's are loaded before the
+  // first is used
+  constexpr int kBatch = 6;
+  const int n_own = static_cast<int>(own.count), n_parts = n_own + static_cast<int>(pre.count);
+  float m = -INFINITY, l = 0.f;
   float o[kCols];
 #pragma unroll
   for (int x = 0; x < kCols; ++x) o[x] = 0.f;
-#pragma unroll 4
-  for (int x = warp; x < n_parts; x += kWarps) {
-    const bool from_own = x < static_cast<int>(own.count);
-    const float* const src =
-        (from_own ? own.o + own.at(x) * D : pre.o + pre.at(x - own.count) * D) + lane * kCols;
-    const float f = weight[x];
-    if (kCols == 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-      o[0] = fmaf(v.x, f, o[0]);
-      o[1] = fmaf(v.y, f, o[1]);
-      o[kCols - 2] = fmaf(v.z, f, o[kCols - 2]);
-      o[kCols - 1] = fmaf(v.w, f, o[kCols - 1]);
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-      o[0] = fmaf(v.x, f, o[0]);
-      o[1] = fmaf(v.y, f, o[1]);
+  for (int x0 = warp; x0 < n_parts; x0 += kWarps * kBatch) {
+    float2 ml[kBatch];
+    float v[kBatch][kCols];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int x = x0 + k * kWarps;
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int y = 0; y < kCols; ++y) v[k][y] = 0.f;
+      if (x < n_parts) {
+        const Parts& from = x < n_own ? own : pre;
+        const long long at = from.at(x < n_own ? x : x - n_own);
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(from.ml + at * 2));
+        const float* const src = from.o + at * D + lane * kCols;
+        if (kCols == 4) {
+          const float4 u = __ldcg(reinterpret_cast<const float4*>(src));
+          v[k][0] = u.x, v[k][1] = u.y, v[k][kCols - 2] = u.z, v[k][kCols - 1] = u.w;
+        } else {
+          const float2 u = __ldcg(reinterpret_cast<const float2*>(src));
+          v[k][0] = u.x, v[k][1] = u.y;
+        }
+      }
     }
+    float big = m;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) big = fmaxf(big, ml[k].x);
+    const float a = m == -INFINITY ? 0.f : ptx::ex2(m - big);
+    l = m == -INFINITY ? l : l * a;  // an empty state's l is 0, or NaN
+#pragma unroll
+    for (int y = 0; y < kCols; ++y) o[y] *= a;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const bool empty = ml[k].x == -INFINITY;
+      const float f = empty ? 0.f : ptx::ex2(ml[k].x - big);
+      l += empty ? ml[k].y : ml[k].y * f;
+#pragma unroll
+      for (int y = 0; y < kCols; ++y) o[y] = fmaf(v[k][y], f, o[y]);
+    }
+    m = big;
   }
   auto add = [&](float mx, float lx, const float (&ox)[kCols]) {
     const float big = fmaxf(m, mx);
@@ -743,7 +740,6 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
       add(dot * p.scale, 1.f, kv[1]);
     }
   }
-  __syncthreads();  // part_m has been read
   if (lane == 0) {
     part_m[warp] = m;
     part_l[warp] = bad ? NAN : l;
