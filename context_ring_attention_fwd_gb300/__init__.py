@@ -178,14 +178,18 @@ def ring_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.
     return dq, dk, dv
 
 
+def _like(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """A contiguous tensor of t's shape, type and device (None for None)."""
+    return None if t is None else t.new_empty(t.shape)
+
+
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight=None, k_weight=None,
                  inv_freq=None, positions=None, eps: float = 1e-6, interleaved: bool = False,
                  stream=None):
     """Per-head RMS norm of q [B,S,Hq,d] and k [B,S,Hk,d] and their rotation,
     ready for ring_attn_fwd: allocates and returns contiguous (q_out, k_out) of
     the inputs' type.  q and k may be strided views; k None gives (q_out, None)."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    q_out, k_out = _like(q), _like(k)
     cp_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps, interleaved,
                     stream)
     return q_out, k_out
@@ -198,10 +202,8 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: to
     ring_attn_bwd): allocates and returns (dq, dk, dq_weight, dk_weight), the
     first two contiguous and of the inputs' type, the others fp32 [d]; None
     where the operand is None."""
-    def like(t):
-        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    dq, dk, dqw = like(q), like(k), like(q_weight)
-    dkw = like(k_weight) if k is not None else None
+    dq, dk, dqw = _like(q), _like(k), _like(q_weight)
+    dkw = _like(k_weight) if k is not None else None
     cp_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, dq, dk, dqw,
                         dkw, eps, interleaved, None, stream)
     return dq, dk, dqw, dkw
@@ -216,7 +218,7 @@ def paged_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     position, and return q normed and rotated likewise (in q_out, allocated if
     None; its rows behind a sequence's new tokens are not written)."""
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _like(q)
     cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens, q_weight, k_weight,
                     inv_freq, q_out, eps, interleaved, k_descale, v_descale, stream)
     return q_out if q is not None else None
@@ -230,8 +232,8 @@ def paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     for the whole batch: allocates and returns (out [B,n_q,Hq,d] bf16, lse
     [B,Hq,n_q] fp32)."""
     B, n_q, Hq, d = q.shape
-    out = torch.empty((B, n_q, Hq, d), dtype=q.dtype, device=q.device)
-    lse = torch.empty((B, Hq, n_q), dtype=torch.float32, device=q.device)
+    out = _like(q)
+    lse = q.new_empty((B, Hq, n_q), dtype=torch.float32)
     cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out, lse, prefix_pages,
                          prefix_len, k_descale, v_descale, workspace, stream)
     return out, lse

@@ -162,32 +162,46 @@ def doc_offsets_tensor(doc_offsets, device) -> Optional[torch.Tensor]:
     return t.contiguous()
 
 
-def _operand(t, name: str, dtype: torch.dtype, device, shape=None) -> None:
-    """t has this type, device and shape, and its last dimension is contiguous."""
+# The calls around the attention are short enough on the device for their host side to
+# count: the checks below read each property of a tensor once, and pointers travel as plain
+# integers.
+def _operand(t, name: str, dtype: torch.dtype, index: int, shape=None) -> int:
+    """t's address, after checking its type, device, shape and that its last
+    dimension is contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must live on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must live on cuda:{index}, got {t.device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if not t.is_contiguous() and t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.data_ptr()
 
 
-def _dense(t, name: str, dtype: torch.dtype, device, shape=None) -> None:
-    _operand(t, name, dtype, device, shape)
+def _dense(t, name: str, dtype: torch.dtype, index: int, shape=None) -> int:
+    at = _operand(t, name, dtype, index, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return at
 
 
-def _cuda_device(t, name: str) -> torch.device:
+def _optional(t, name: str, dtype: torch.dtype, index: int, shape=None):
+    return None if t is None else _dense(t, name, dtype, index, shape)
+
+
+def _cuda_index(t, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must live on a CUDA device")
-    return t.device
+    return index
+
+
+_Steps = _i64 * 3
 
 
 def _steps(t):
@@ -195,22 +209,30 @@ def _steps(t):
     stride of a dimension of one entry is never used and passed as 0."""
     if t is None or t.is_contiguous():
         return None
-    return (_i64 * 3)(*[st if n > 1 else 0 for st, n in zip(t.stride()[:3], t.shape)])
+    a, b, c, _ = t.stride()
+    n = t.shape
+    return _Steps(a if n[0] > 1 else 0, b if n[1] > 1 else 0, c if n[2] > 1 else 0)
 
 
-def _call_on(name: str, device: torch.device, stream, *args) -> None:
-    """Run a library call with `device` current, on `stream` or, if None, on
-    that device's current stream."""
+def _call_on(name: str, index: int, stream, *args) -> None:
+    """Run a library call with device `index` current, on `stream` or, if
+    None, on that device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif isinstance(stream, torch.cuda.Stream) and stream.device != device:
-        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
-        _check(name, fn(*args, _stream(stream)))
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != index:
+            raise ValueError(f"stream belongs to {stream.device}, the tensors to cuda:{index}")
+        raw = stream.cuda_stream
     else:
-        with torch.cuda.device(device):
-            _check(name, fn(*args, _stream(stream)))
+        raw = int(stream)
+    fn = getattr(_lib or lib(), name)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, raw)
+    if st != CP_OK:
+        raise CpError(name, st)
 
 
 # --------------------------------------------------------------------- C ABI
@@ -559,43 +581,30 @@ def _rows4(t, name: str):
     return t.shape
 
 
-def _rotation(inv_freq, positions, device, tokens):
-    """rot_dim, after checking the two operands of the rotation."""
-    if inv_freq is not None:
-        _dense(inv_freq, "inv_freq", torch.float32, device, (inv_freq.numel(),))
-    if positions is not None:
-        _dense(positions, "positions", torch.int32, device, tokens)
-    return 0 if inv_freq is None else 2 * inv_freq.numel()
-
-
-def _weight(w, name: str, d: int, device):
-    if w is not None:
-        _dense(w, name, torch.float32, device, (d,))
-
-
 def cp_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out,
                     eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
     """Per-head RMS norm and rotation of q [B,S,Hq,d] and k [B,S,Hk,d] (bf16 or
     fp32, strided views allowed; k None: q only) into the contiguous q_out and
     k_out.  Weights fp32 [d] (None: not normed), inv_freq fp32 [rot_dim / 2]
     (None: not rotated), positions int32 [B,S] (None: the token's index)."""
-    B, S, Hq, d = _rows4(q, "q")
-    dev, dt = _cuda_device(q, "q"), q.dtype
-    if dt not in (torch.bfloat16, torch.float32):
+    shape = _rows4(q, "q")
+    B, S, Hq, d = shape
+    dev, dt, f32 = _cuda_index(q, "q"), q.dtype, torch.float32
+    if dt is not torch.bfloat16 and dt is not f32:
         raise TypeError("q must be bf16 or fp32")
-    Hk = 0 if k is None else _rows4(k, "k")[2]
-    _operand(q, "q", dt, dev)
-    _dense(q_out, "q_out", dt, dev, (B, S, Hq, d))
+    q_at, qo_at = _operand(q, "q", dt, dev), _dense(q_out, "q_out", dt, dev, shape)
+    Hk, k_at, ko_at = 0, None, None
     if k is not None:
-        _operand(k, "k", dt, dev, (B, S, Hk, d))
-        _dense(k_out, "k_out", dt, dev, (B, S, Hk, d))
-    _weight(q_weight, "q_weight", d, dev)
-    _weight(k_weight, "k_weight", d, dev)
-    rot = _rotation(inv_freq, positions, dev, (B, S))
-    _call_on("cp_qk_norm_rope", dev, stream, _ptr(q), _steps(q), _ptr(k), _steps(k),
-             _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(inv_freq), rot,
-             int(bool(interleaved)), _ptr(positions), _ptr(q_out),
-             _ptr(k_out) if k is not None else None, B, S, Hq, Hk, d, int(dt == torch.bfloat16))
+        Hk = _rows4(k, "k")[2]
+        k_at = _operand(k, "k", dt, dev, (B, S, Hk, d))
+        ko_at = _dense(k_out, "k_out", dt, dev, (B, S, Hk, d))
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    _call_on("cp_qk_norm_rope", dev, stream, q_at, _steps(q), k_at, _steps(k),
+             _optional(q_weight, "q_weight", f32, dev, (d,)),
+             _optional(k_weight, "k_weight", f32, dev, (d,)), eps,
+             _optional(inv_freq, "inv_freq", f32, dev, (rot // 2,)), rot, bool(interleaved),
+             _optional(positions, "positions", torch.int32, dev, (B, S)), qo_at, ko_at, B, S, Hq,
+             Hk, d, dt is not f32)
 
 
 def cp_qk_norm_rope_bwd_workspace_bytes(B: int, S: int, Hq: int, Hk: int, d: int) -> int:
@@ -609,64 +618,69 @@ def cp_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, posi
     forward's inputs, writes dq, dk (the inputs' type, strided views allowed)
     and the weights' gradients (fp32 [d], or None).  workspace: a uint8 device
     tensor (allocated here if None)."""
-    B, S, Hq, d = _rows4(q, "q")
-    dev, dt = _cuda_device(q, "q"), q.dtype
-    if dt not in (torch.bfloat16, torch.float32):
+    shape = _rows4(q, "q")
+    B, S, Hq, d = shape
+    dev, dt, f32 = _cuda_index(q, "q"), q.dtype, torch.float32
+    if dt is not torch.bfloat16 and dt is not f32:
         raise TypeError("q must be bf16 or fp32")
-    Hk = 0 if k is None else _rows4(k, "k")[2]
-    for x, H, names in ((q, Hq, ("q", "dq", "dq_out")), (k, Hk, ("k", "dk", "dk_out"))):
-        if x is None:
-            continue
-        grad, given = (dq, dq_out) if x is q else (dk, dk_out)
-        _operand(x, names[0], dt, dev, (B, S, H, d))
-        _operand(grad, names[1], dt, dev, (B, S, H, d))
-        _dense(given, names[2], dt, dev, (B, S, H, d))
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight"), (dq_weight, "dq_weight"),
-                 (dk_weight, "dk_weight")):
-        _weight(w, n, d, dev)
-    rot = _rotation(inv_freq, positions, dev, (B, S))
+    q_at, dq_at = _operand(q, "q", dt, dev), _operand(dq, "dq", dt, dev, shape)
+    dqo_at = _dense(dq_out, "dq_out", dt, dev, shape)
+    Hk, k_at, dk_at, dko_at, dk_steps = 0, None, None, None, None
+    if k is not None:
+        Hk = _rows4(k, "k")[2]
+        k_at = _operand(k, "k", dt, dev, (B, S, Hk, d))
+        dk_at = _operand(dk, "dk", dt, dev, (B, S, Hk, d))
+        dko_at = _dense(dk_out, "dk_out", dt, dev, (B, S, Hk, d))
+        dk_steps = _steps(dk)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     if workspace is None:
         need = cp_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hk, d)
         if need < 0:
             raise CpError("cp_qk_norm_rope_bwd_workspace_bytes", STATUS_CODES["CP_ERR_SHAPE"])
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _dense(workspace, "workspace", torch.uint8, dev)
-    has_k = k is not None
-    _call_on("cp_qk_norm_rope_bwd", dev, stream, _ptr(dq_out), _ptr(dk_out) if has_k else None,
-             _ptr(q), _steps(q), _ptr(k), _steps(k), _ptr(q_weight), _ptr(k_weight), float(eps),
-             _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(positions), _ptr(dq), _steps(dq),
-             _ptr(dk) if has_k else None, _steps(dk) if has_k else None, _ptr(dq_weight),
-             _ptr(dk_weight), B, S, Hq, Hk, d, int(dt == torch.bfloat16), _ptr(workspace),
-             int(workspace.numel()))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _call_on("cp_qk_norm_rope_bwd", dev, stream, dqo_at, dko_at, q_at, _steps(q), k_at, _steps(k),
+             _optional(q_weight, "q_weight", f32, dev, (d,)),
+             _optional(k_weight, "k_weight", f32, dev, (d,)), eps,
+             _optional(inv_freq, "inv_freq", f32, dev, (rot // 2,)), rot, bool(interleaved),
+             _optional(positions, "positions", torch.int32, dev, (B, S)), dq_at, _steps(dq), dk_at,
+             dk_steps, _optional(dq_weight, "dq_weight", f32, dev, (d,)),
+             _optional(dk_weight, "dk_weight", f32, dev, (d,)), B, S, Hq, Hk, d, dt is not f32,
+             _dense(workspace, "workspace", torch.uint8, dev), workspace.numel())
 
 
-def _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, dev) -> PagedCacheStruct:
+def _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, B: int,
+                  dev: int) -> PagedCacheStruct:
     """The cp_paged_cache of caches [pages, page_size, Hk, d] (bf16, or uint8
     E4M3 codes with fp32 [Hk] descales) and an int32 table [B, max_pages]."""
     dt = k_cache.dtype if isinstance(k_cache, torch.Tensor) else None
-    if dt not in (torch.bfloat16, torch.uint8):
+    e4m3 = dt is torch.uint8
+    if not e4m3 and dt is not torch.bfloat16:
         raise TypeError("k_cache must be bf16 or uint8 (E4M3 codes)")
-    n_pages, page_size, Hk, d = _rows4(k_cache, "k_cache")
-    _operand(k_cache, "k_cache", dt, dev)
-    _operand(v_cache, "v_cache", dt, dev, k_cache.shape)
-    _operand(page_table, "page_table", torch.int32, dev)
+    shape = _rows4(k_cache, "k_cache")
+    n_pages, page_size, Hk, d = shape
+    k_at = _operand(k_cache, "k_cache", dt, dev)
+    v_at = _operand(v_cache, "v_cache", dt, dev, shape)
+    table_at = _operand(page_table, "page_table", torch.int32, dev)
     if page_table.dim() != 2:
         raise ValueError("page_table must have two dimensions")
-    for t, n in ((k_descale, "k_descale"), (v_descale, "v_descale")):
-        if dt == torch.uint8:
-            _dense(t, n, torch.float32, dev, (Hk,))
-        elif t is not None:
-            raise ValueError(f"{n} goes with an E4M3 cache")
-    sizes = k_cache.shape[:3]
-    row = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
-    e4m3 = dt == torch.uint8
-    return PagedCacheStruct(
-        k_cache.data_ptr(), v_cache.data_ptr(),
-        (_i64 * 3)(*[s if n > 1 else 0 for s, n in zip(k_cache.stride(), sizes)]),
-        (_i64 * 3)(*[s if n > 1 else 0 for s, n in zip(v_cache.stride(), sizes)]),
-        k_descale.data_ptr() if e4m3 else None, v_descale.data_ptr() if e4m3 else None,
-        page_table.data_ptr(), row, n_pages, page_size, page_table.shape[1], Hk, d,
-        1 if e4m3 else 2)
+    rows, max_pages = page_table.shape
+    if rows != B:
+        raise ValueError(f"page_table must have {B} rows, got {rows}")
+    if e4m3:
+        kd_at = _dense(k_descale, "k_descale", torch.float32, dev, (Hk,))
+        vd_at = _dense(v_descale, "v_descale", torch.float32, dev, (Hk,))
+    elif k_descale is None and v_descale is None:
+        kd_at = vd_at = None
+    else:
+        raise ValueError("k_descale and v_descale go with an E4M3 cache")
+    ks = v_s = _Steps(page_size * Hk * d, Hk * d, d)
+    if not k_cache.is_contiguous():
+        ks = _steps(k_cache)
+    if not v_cache.is_contiguous():
+        v_s = _steps(v_cache)
+    return PagedCacheStruct(k_at, v_at, ks, v_s, kd_at, vd_at, table_at,
+                            page_table.stride(0) if rows > 1 else max_pages, n_pages, page_size,
+                            max_pages, Hk, d, 1 if e4m3 else 2)
 
 
 def cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens, q_weight,
@@ -677,29 +691,23 @@ def cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens,
     (int32 [B]), for s < new_lens[b] (int32 [B], None: all S); q [B,S,Hq,d]
     (None: keys and values only) is normed and rotated into q_out."""
     B, S, Hk, d = _rows4(k, "k")
-    dev = _cuda_device(k, "k")
-    cache = _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, dev)
-    if page_table.shape[0] != B:
-        raise ValueError(f"page_table must have {B} rows, got {page_table.shape[0]}")
-    bf16 = torch.bfloat16
+    dev, bf16, i32, f32 = _cuda_index(k, "k"), torch.bfloat16, torch.int32, torch.float32
+    cache = _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, B, dev)
     shape = (B, S, cache.Hk, cache.d)
-    _operand(k, "k", bf16, dev, shape)
-    _operand(v, "v", bf16, dev, shape)
-    Hq = 0
+    k_at, v_at = _operand(k, "k", bf16, dev, shape), _operand(v, "v", bf16, dev, shape)
+    Hq, q_at, qo_at = 0, None, None
     if q is not None:
         Hq = _rows4(q, "q")[2]
-        _operand(q, "q", bf16, dev, (B, S, Hq, d))
-        _dense(q_out, "q_out", bf16, dev, (B, S, Hq, d))
-    _dense(cache_lens, "cache_lens", torch.int32, dev, (B,))
-    if new_lens is not None:
-        _dense(new_lens, "new_lens", torch.int32, dev, (B,))
-    _weight(q_weight, "q_weight", d, dev)
-    _weight(k_weight, "k_weight", d, dev)
-    rot = _rotation(inv_freq, None, dev, None)
-    _call_on("cp_paged_append", dev, stream, ctypes.byref(cache), _ptr(q), _steps(q), _ptr(k),
-             _steps(k), _ptr(v), _steps(v), _ptr(cache_lens), _ptr(new_lens), _ptr(q_weight),
-             _ptr(k_weight), float(eps), _ptr(inv_freq), rot, int(bool(interleaved)),
-             _ptr(q_out) if q is not None else None, B, S, Hq)
+        q_at = _operand(q, "q", bf16, dev, (B, S, Hq, d))
+        qo_at = _dense(q_out, "q_out", bf16, dev, (B, S, Hq, d))
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    _call_on("cp_paged_append", dev, stream, ctypes.byref(cache), q_at, _steps(q), k_at, _steps(k),
+             v_at, _steps(v), _dense(cache_lens, "cache_lens", i32, dev, (B,)),
+             _optional(new_lens, "new_lens", i32, dev, (B,)),
+             _optional(q_weight, "q_weight", f32, dev, (d,)),
+             _optional(k_weight, "k_weight", f32, dev, (d,)), eps,
+             _optional(inv_freq, "inv_freq", f32, dev, (rot // 2,)), rot, bool(interleaved), qo_at,
+             B, S, Hq)
 
 
 def cp_paged_attn_decode_workspace_bytes(B: int, n_q: int, Hq: int, Hk: int, d: int,
@@ -717,25 +725,21 @@ def cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out, lse, pr
     out [B,n_q,Hq,d] bf16, lse [B,Hq,n_q] fp32; workspace a uint8 device
     tensor (allocated here if None)."""
     B, n_q, Hq, d = _rows4(q, "q")
-    dev = _cuda_device(q, "q")
-    cache = _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, dev)
-    if page_table.shape[0] != B:
-        raise ValueError(f"page_table must have {B} rows, got {page_table.shape[0]}")
-    _operand(q, "q", torch.bfloat16, dev, (B, n_q, Hq, cache.d))
-    _dense(out, "out", torch.bfloat16, dev, (B, n_q, Hq, d))
-    _dense(lse, "lse", torch.float32, dev, (B, Hq, n_q))
-    _dense(seq_lens, "seq_lens", torch.int32, dev, (B,))
-    prefix_len = int(prefix_len)
+    dev, bf16, i32 = _cuda_index(q, "q"), torch.bfloat16, torch.int32
+    cache = _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, B, dev)
+    shape = (B, n_q, Hq, cache.d)
+    q_at, out_at = _operand(q, "q", bf16, dev, shape), _dense(out, "out", bf16, dev, shape)
+    lse_at = _dense(lse, "lse", torch.float32, dev, (B, Hq, n_q))
+    prefix_len, pages_at = int(prefix_len), None
     if prefix_pages is not None:
-        _dense(prefix_pages, "prefix_pages", torch.int32, dev, (prefix_pages.numel(),))
+        pages_at = _dense(prefix_pages, "prefix_pages", i32, dev, (prefix_pages.numel(),))
         if prefix_pages.numel() * cache.page_size < prefix_len:
             raise ValueError("prefix_pages holds fewer tokens than prefix_len")
     if workspace is None:
         need = cp_paged_attn_decode_workspace_bytes(B, n_q, Hq, cache.Hk, d, prefix_len)
         if need < 0:
             raise CpError("cp_paged_attn_decode_workspace_bytes", STATUS_CODES["CP_ERR_SHAPE"])
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _dense(workspace, "workspace", torch.uint8, dev)
-    _call_on("cp_paged_attn_decode", dev, stream, ctypes.byref(cache), _ptr(q), _steps(q),
-             _ptr(seq_lens), _ptr(prefix_pages), prefix_len, _ptr(out), _ptr(lse), B, n_q, Hq,
-             _ptr(workspace), int(workspace.numel()))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _call_on("cp_paged_attn_decode", dev, stream, ctypes.byref(cache), q_at, _steps(q),
+             _dense(seq_lens, "seq_lens", i32, dev, (B,)), pages_at, prefix_len, out_at, lse_at, B,
+             n_q, Hq, _dense(workspace, "workspace", torch.uint8, dev), workspace.numel())

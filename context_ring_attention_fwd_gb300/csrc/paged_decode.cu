@@ -58,8 +58,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kWarpKeys = 16;                    // keys of a tile that a warp owns
 constexpr int kTileKeys = kWarps * kWarpKeys;    // 64
 constexpr int kRows = 16;                        // rows of an item
-constexpr int kCtasPerSm = 2;
-constexpr int kMaxGrid = 320;                    // bounds the slots of the workspace
+constexpr int kCtasPerSm = 3;
+constexpr int kMaxGrid = 480;                    // bounds the slots of the workspace
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxQueries = 16;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -72,7 +72,7 @@ struct Stage {
   static constexpr int kRowBytes = D * (kE4M3 ? 1 : 2);
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kBytes = 2 * kWarpKeys * kRowBytes;
-  static constexpr int kCount = kBytes >= 8192 ? 3 : 6;
+  static constexpr int kCount = kBytes >= 8192 ? 2 : 4;
   static constexpr int kRing = kCount * kBytes;  // per warp
   static constexpr int kSwz = kChunks >= 8 ? 7 : 3;
   __device__ static uint32_t at(uint32_t base, int row, int chunk) {

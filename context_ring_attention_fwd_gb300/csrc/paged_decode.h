@@ -51,7 +51,7 @@ struct DecodeParams {
 // units come first; the CTA that holds only those has no part of it.
 // (Measured: an item's loads of pages and queries, its pipeline's filling and
 // its state's writing take about as long as that many tiles.)
-constexpr unsigned kItemCost = 2;
+constexpr unsigned kItemCost = 3;
 __device__ __forceinline__ unsigned stretch(unsigned c, unsigned W, unsigned g) {
   return static_cast<unsigned>(static_cast<unsigned long long>(c) * W / g);
 }
