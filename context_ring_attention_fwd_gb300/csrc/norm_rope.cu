@@ -55,116 +55,171 @@ struct RopeParams {
   float eps;
 };
 
-template <typename T, int D, int kUnroll, bool kBwd>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int D, int kUnroll, bool kBwd, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, 2)
     qk_norm_rope_kernel(const RopeParams p) {
   using Lay = RowLayout<T, D>;
   constexpr int NP = Lay::kPairs;
   constexpr int kUnitRows = kUnroll * Lay::kRows;
+  constexpr int kRowVecs = kBwd ? 4 : 2;  // a lane's vectors of a row: x, and dy
+  using R = Ring<kUnroll * kRowVecs>;
+  extern __shared__ __align__(16) uint8_t rings[];
+  __shared__ float sums[kBwd ? 2 * kWarps * D : 1];
+  __shared__ __align__(16) float gain[2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % Lay::kLanes, g = lane / Lay::kLanes;
-  __shared__ float sums[kBwd ? 2 * kWarps * D : 1];
+  const R ring{static_cast<uint32_t>(__cvta_generic_to_shared(rings)) + warp * R::kBytes +
+               lane * 16};
 
   int lo, hi;
   bool turned;
-  lane_columns<NP>(l, p.rot, p.interleaved != 0, lo, hi, turned);
+  lane_columns<NP>(l, p.rot, kInterleaved, lo, hi, turned);
+
+  struct Unit {
+    int ti, tok, b, s, h0;
+  };
+  auto unit_at = [&](unsigned u) {
+    Unit x;
+    x.ti = u >= static_cast<unsigned>(p.units_q);
+    const int local = static_cast<int>(u) - (x.ti ? p.units_q : 0);
+    x.tok = local / p.t[x.ti].chunks;
+    x.h0 = (local - x.tok * p.t[x.ti].chunks) * kUnitRows + g;
+    x.b = x.tok / p.S;
+    x.s = x.tok - x.b * p.S;
+    return x;
+  };
+  auto fetch = [&](const Unit& x, int stage) {
+    const Rows& t = p.t[x.ti];
+    const T* const xrow = static_cast<const T*>(t.x) + x.b * t.xb + x.s * t.xs;
+    const T* const dy = static_cast<const T*>(t.dy) + static_cast<long long>(x.tok) * t.H * D;
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int h = x.h0 + i * Lay::kRows;
+      const bool there = h < t.H;
+      const T* const src = xrow + (there ? h : 0) * t.xh;
+      ring.copy(stage, i * kRowVecs, src + lo, there);
+      ring.copy(stage, i * kRowVecs + 1, src + hi, there);
+      if (kBwd) {
+        const T* const gsrc = dy + static_cast<long long>(there ? h : 0) * D;
+        ring.copy(stage, i * kRowVecs + 2, gsrc + lo, there);
+        ring.copy(stage, i * kRowVecs + 3, gsrc + hi, there);
+      }
+    }
+  };
+  const unsigned stride = gridDim.x * kWarps;  // unsigned: the last step may pass 2^31
+  const unsigned units = static_cast<unsigned>(p.units);
+  unsigned u = blockIdx.x * kWarps + warp;
+  Unit next{};
+  if (u < units) {
+    next = unit_at(u);
+    fetch(next, 0);
+  }
+  copies_commit();
+
   uint64_t frac[Lay::kAngles];
   load_fractions<Lay>(p.inv_freq, l, g, turned, frac);
-  float w[2 * NP], dw[2 * NP];
+  stage_gain(gain[0], p.t[0].w, D);
+  stage_gain(gain[1], p.t[1].w, D);
+  __syncthreads();
+  f32x2 dw[kBwd ? NP : 1];
 #pragma unroll
-  for (int i = 0; i < 2 * NP; ++i) dw[i] = 0.f;
+  for (int i = 0; i < (kBwd ? NP : 1); ++i) dw[i] = 0ull;
 
   // Hand the sums for tensor `ti`'s gain to the block (its warp's own slot).
   auto flush = [&](int ti) {
 #pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) {
-      float v = dw[i];
+    for (int i = 0; i < (kBwd ? NP : 1); ++i) {
+      float v[2];
+      unpack2(dw[i], v[0], v[1]);
 #pragma unroll
-      for (int o = Lay::kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (g == 0) sums[(ti * kWarps + warp) * D + (i < NP ? lo + i : hi + i - NP)] = v;
-      dw[i] = 0.f;
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = Lay::kLanes; o < 32; o <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+        const int col = i < NP / 2 ? lo + 2 * i + e : hi + 2 * i - NP + e;
+        if (g == 0) sums[(ti * kWarps + warp) * D + col] = v[e];
+      }
+      dw[i] = 0ull;
     }
   };
 
   int cur = -1;
-  const unsigned stride = gridDim.x * kWarps;  // unsigned: the last step may pass 2^31
-  for (unsigned u = blockIdx.x * kWarps + warp; u < static_cast<unsigned>(p.units); u += stride) {
-    const int ti = u >= static_cast<unsigned>(p.units_q);
-    const Rows& t = p.t[ti];
-    const T* const xin = static_cast<const T*>(t.x);
-    const int local = static_cast<int>(u) - (ti ? p.units_q : 0);
-    const int tok = local / t.chunks;
-    const int h0 = (local - tok * t.chunks) * kUnitRows + g;
-    const int b = tok / p.S, s = tok - b * p.S;
-    uint4 raw[kUnroll][2], rawg[kBwd ? kUnroll : 1][2];
-    const T* const xrow = xin + b * t.xb + s * t.xs;
-    const long long flat = static_cast<long long>(tok) * t.H * D;  // contiguous [B, S, H, d]
+  for (int stage = 0; u < units; u += stride, stage ^= 1) {
+    const Unit x = next;
+    if (u + stride < units && u + stride > u) {
+      next = unit_at(u + stride);
+      fetch(next, stage ^ 1);
+    }
+    copies_commit();
+    const Rows& t = p.t[x.ti];
+    const long long flat = static_cast<long long>(x.tok) * t.H * D;  // contiguous [B, S, H, d]
+    if (kBwd && x.ti != cur && cur >= 0) flush(cur);
+    cur = x.ti;
+    // The factors of this token's turn; the forward's carry the gain too:
+    // y[i] = own w[i] x[i] + other w[partner] x[partner], times r.
+    f32x2 own[NP], other[NP], w[NP];
+    load_gain<NP>(gain[x.ti], lo, hi, w);
+    if (p.rot > 0) {
+      float c[NP], sn[NP];
+      row_angles<Lay>(p.positions ? __ldg(p.positions + x.tok) : x.s, frac, l, c, sn);
+      turn_factors<NP, kInterleaved>(c, sn, kBwd ? -1.f : 1.f, own, other);
+      if (!kBwd) {
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int h = h0 + i * Lay::kRows;
-      raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (kBwd) rawg[i][0] = rawg[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < t.H) {
-        const T* const src = xrow + h * t.xh;
-        raw[i][0] = *reinterpret_cast<const uint4*>(src + lo);
-        raw[i][1] = *reinterpret_cast<const uint4*>(src + hi);
-        if (kBwd) {
-          const T* const dy = static_cast<const T*>(t.dy) + flat + static_cast<long long>(h) * D;
-          rawg[i][0] = *reinterpret_cast<const uint4*>(dy + lo);
-          rawg[i][1] = *reinterpret_cast<const uint4*>(dy + hi);
+        for (int i = 0; i < NP; ++i) {
+          own[i] = mul2(own[i], w[i]);
+          other[i] = mul2(other[i], partner<NP, kInterleaved>(w, i));
         }
       }
     }
-    if (ti != cur) {
-      if (kBwd && cur >= 0) flush(cur);
-      cur = ti;
-      if (t.w != nullptr) load_columns<NP>(t.w, lo, hi, w);
-    }
-    float c[NP], sn[NP];
-    if (p.rot > 0) row_angles<Lay>(p.positions ? __ldg(p.positions + tok) : s, frac, l, c, sn);
+    copies_wait_all_but_last();
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int h = h0 + i * Lay::kRows;
+      const int h = x.h0 + i * Lay::kRows;
       if (h - g >= t.H) break;  // the same for the whole warp
-      float z[2 * NP];
-      unpack(raw[i][0], z, 0, T());
-      unpack(raw[i][1], z, NP, T());
+      f32x2 z[NP];
+      unpack<NP>(ring.read(stage, i * kRowVecs), z, 0, T());
+      unpack<NP>(ring.read(stage, i * kRowVecs + 1), z, NP / 2, T());
+      float r = 1.f;
+      if (t.w != nullptr)
+        r = rsqrtf(row_sum<Lay::kLanes>(dot<NP>(z, z)) * (1.f / D) + p.eps);
+      const f32x2 r2 = pack2(r, r);
       if (!kBwd) {
-        if (t.w != nullptr) {
-          const float r = rsqrtf(row_sum<Lay::kLanes>(sum_squares(z)) * (1.f / D) + p.eps);
+        if (turned) {
+          turn<NP, kInterleaved>(z, own, other);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 2 * NP; ++e) z[e] = z[e] * r * w[e];
+          for (int e = 0; e < NP; ++e) z[e] = mul2(z[e], w[e]);
         }
-        if (turned) rotate<NP>(z, c, sn, p.interleaved != 0, 1.f);
+#pragma unroll
+        for (int e = 0; e < NP; ++e) z[e] = mul2(z[e], r2);
         if (h < t.H) {
           T* const dst = static_cast<T*>(t.y) + flat + static_cast<long long>(h) * D;
-          *reinterpret_cast<uint4*>(dst + lo) = repack(z, 0, T());
-          *reinterpret_cast<uint4*>(dst + hi) = repack(z, NP, T());
+          *reinterpret_cast<uint4*>(dst + lo) = repack<NP>(z, 0, T());
+          *reinterpret_cast<uint4*>(dst + hi) = repack<NP>(z, NP / 2, T());
         }
       } else {
-        float gr[2 * NP];
-        unpack(rawg[i][0], gr, 0, T());
-        unpack(rawg[i][1], gr, NP, T());
-        if (turned) rotate<NP>(gr, c, sn, p.interleaved != 0, -1.f);
+        f32x2 gr[NP];
+        unpack<NP>(ring.read(stage, i * kRowVecs + 2), gr, 0, T());
+        unpack<NP>(ring.read(stage, i * kRowVecs + 3), gr, NP / 2, T());
+        if (turned) turn<NP, kInterleaved>(gr, own, other);
         if (t.w != nullptr) {
-          float dot = 0.f;
+          f32x2 gw[NP];
 #pragma unroll
-          for (int e = 0; e < 2 * NP; ++e) dot = fmaf(gr[e] * w[e], z[e], dot);
-          const float r = rsqrtf(row_sum<Lay::kLanes>(sum_squares(z)) * (1.f / D) + p.eps);
-          const float m = row_sum<Lay::kLanes>(dot) * r * (1.f / D);
+          for (int e = 0; e < NP; ++e) gw[e] = mul2(gr[e], w[e]);
+          const float m = row_sum<Lay::kLanes>(dot<NP>(gw, z)) * r * (1.f / D);
           if (h < t.H) {
+            const f32x2 m2 = pack2(-m, -m);
 #pragma unroll
-            for (int e = 0; e < 2 * NP; ++e) {
-              const float un = z[e] * r;
-              dw[e] = fmaf(gr[e], un, dw[e]);
-              gr[e] = r * (gr[e] * w[e] - un * m);
+            for (int e = 0; e < NP; ++e) {
+              const f32x2 un = mul2(z[e], r2);
+              dw[e] = fma2(gr[e], un, dw[e]);
+              gr[e] = mul2(r2, fma2(un, m2, gw[e]));
             }
           }
         }
         if (h < t.H) {
-          T* const dst = static_cast<T*>(t.y) + b * t.yb + s * t.ys + h * t.yh;
-          *reinterpret_cast<uint4*>(dst + lo) = repack(gr, 0, T());
-          *reinterpret_cast<uint4*>(dst + hi) = repack(gr, NP, T());
+          T* const dst = static_cast<T*>(t.y) + x.b * t.yb + x.s * t.ys + h * t.yh;
+          *reinterpret_cast<uint4*>(dst + lo) = repack<NP>(gr, 0, T());
+          *reinterpret_cast<uint4*>(dst + hi) = repack<NP>(gr, NP / 2, T());
         }
       }
     }
@@ -206,18 +261,22 @@ __global__ void __launch_bounds__(1024)
   if (out != nullptr) out[col < d ? col : col - d] = v;
 }
 
-template <typename T, int D, int kUnroll, bool kBwd>
+template <typename T, int D, int kUnroll, bool kBwd, bool kInterleaved>
 cudaError_t launch_rows(RopeParams p, int tokens, float* dqw, float* dkw, cudaStream_t stream) {
   constexpr int kUnitRows = kUnroll * RowLayout<T, D>::kRows;
   for (Rows& t : p.t) t.chunks = (t.H + kUnitRows - 1) / kUnitRows;
   p.units_q = tokens * p.t[0].chunks;
   p.units = p.units_q + tokens * p.t[1].chunks;
   const int want = (p.units + kWarps - 1) / kWarps;
-  const int blocks = std::min(want, std::min(kMaxBlocks, sm_count() * (kBwd ? 2 : 3)));
-  qk_norm_rope_kernel<T, D, kUnroll, kBwd><<<blocks, kThreads, 0, stream>>>(p);
+  const int blocks = std::min(want, std::min(kMaxBlocks, 2 * sm_count()));
+  constexpr int kSmem = kWarps * Ring<kUnroll * (kBwd ? 4 : 2)>::kBytes;
+  const auto kern = qk_norm_rope_kernel<T, D, kUnroll, kBwd, kInterleaved>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<blocks, kThreads, kSmem, stream>>>(p);
   count_launch(2);
   if (!kBwd || (!dqw && !dkw)) return cudaGetLastError();
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -241,10 +300,12 @@ cudaError_t launch_sized(const RopeParams& p, int tokens, float* dqw, float* dkw
                          cudaStream_t stream) {
   constexpr int kWide = kBwd ? 2 : 4;
   const long long rows = static_cast<long long>(tokens) * (p.t[0].H + p.t[1].H);
-  const long long wide_units = rows / (kWide * RowLayout<T, D>::kRows);
-  if (wide_units >= 2LL * sm_count() * kWarps)
-    return launch_rows<T, D, kWide, kBwd>(p, tokens, dqw, dkw, stream);
-  return launch_rows<T, D, 1, kBwd>(p, tokens, dqw, dkw, stream);
+  const bool wide = rows / (kWide * RowLayout<T, D>::kRows) >= 2LL * sm_count() * kWarps;
+  if (p.interleaved)
+    return wide ? launch_rows<T, D, kWide, kBwd, true>(p, tokens, dqw, dkw, stream)
+                : launch_rows<T, D, 1, kBwd, true>(p, tokens, dqw, dkw, stream);
+  return wide ? launch_rows<T, D, kWide, kBwd, false>(p, tokens, dqw, dkw, stream)
+              : launch_rows<T, D, 1, kBwd, false>(p, tokens, dqw, dkw, stream);
 }
 
 template <bool kBwd>

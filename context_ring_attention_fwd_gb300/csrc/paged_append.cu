@@ -5,7 +5,8 @@
 // Token s of sequence b has the position p = cache_lens[b] + s and goes to
 // slot p % page_size of page page_table[b][p / page_size].  K is normed and
 // rotated in fp32 (rope.cuh) and rounded once, to what the cache holds: bf16,
-// or the E4M3 code of x / descale[head].
+// or the E4M3 code of x times the reciprocal of descale[head] (in fp32, as
+// cp_fp8_quantize multiplies by its inverse scale).
 //
 // Bound by HBM for prefill chunks and by launch latency for single tokens.  A
 // warp's unit is a few heads of one token of q, k or v; rows are 16-byte
@@ -46,133 +47,232 @@ struct AppendParams {
   int* err;
   long long table_stride;
   int n_pages, page_size, max_pages;
-  int S, rot, interleaved;
-  int units_q, units_qk, units;
+  int B, S, rot, interleaved;
+  int compact;  // units are laid over the new tokens alone (B <= kMaxScan)
+  int tokens;   // B * S
   float eps;
 };
 
-__device__ __forceinline__ uint2 codes8(const float (&z)[16], int at, float scale) {
+// A chunk's padding is left out of the work's layout, so that every warp gets an
+// equal share of the tokens that are there: each block sums the lengths once, for
+// batches of up to this many rows (a chunk of 8192 rows, half of them padding:
+// 31.8 -> 29.9 us with the launch).  Calls of one token a row, and larger
+// batches, walk the padding.
+constexpr int kMaxScan = 256;
+
+template <int NP>
+__device__ __forceinline__ uint2 codes8(const f32x2 (&z)[NP], int at, f32x2 inv) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack2(mul2(z[at + i], inv), lo, hi);
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(r)
-        : "f"(__fdiv_rn(z[at + 2 * i + 1], scale)), "f"(__fdiv_rn(z[at + 2 * i], scale)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     w[i] = r;
   }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-template <int D, int kUnroll, bool kE4M3>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendParams p) {
+template <int D, int kUnroll, bool kE4M3, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, 2) paged_append_kernel(const AppendParams p) {
   using T = __nv_bfloat16;
   using Lay = RowLayout<T, D>;
   constexpr int NP = Lay::kPairs;
   constexpr int kUnitRows = kUnroll * Lay::kRows;
-  const int lane = threadIdx.x & 31;
+  using R = Ring<kUnroll * 2>;
+  extern __shared__ __align__(16) uint8_t rings[];
+  __shared__ __align__(16) float gain[2][D];
+  __shared__ int starts[kMaxScan + 1];
+  __shared__ int warp_sum[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % Lay::kLanes, g = lane / Lay::kLanes;
+  const R ring{static_cast<uint32_t>(__cvta_generic_to_shared(rings)) + warp * R::kBytes +
+               lane * 16};
   int lo, hi;
   bool turned;
-  lane_columns<NP>(l, p.rot, p.interleaved != 0, lo, hi, turned);
+  lane_columns<NP>(l, p.rot, kInterleaved, lo, hi, turned);
+
+  auto new_len = [&](int b) {
+    const int n = p.new_lens ? __ldg(p.new_lens + b) : p.S;
+    if ((n < 0 || n > p.S) && blockIdx.x == 0) atomicOr(p.err, kErrCache);
+    return max(0, min(n, p.S));
+  };
+  int tokens = p.tokens;
+  if (p.compact) {
+    static_assert(kMaxScan == kThreads, "one thread a row");
+    const int n = threadIdx.x < p.B ? new_len(threadIdx.x) : 0;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int before = x - n;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    starts[threadIdx.x] = before;
+    if (threadIdx.x == kThreads - 1) starts[kMaxScan] = before + n;
+    __syncthreads();
+    tokens = starts[kMaxScan];
+  }
+  const unsigned units_q = static_cast<unsigned>(tokens) * p.t[0].chunks;
+  const unsigned units_qk = units_q + static_cast<unsigned>(tokens) * p.t[1].chunks;
+  const unsigned units = units_qk + static_cast<unsigned>(tokens) * p.t[2].chunks;
+
+  struct Unit {
+    int kind, tok, h0;  // 0 q, 1 k, 2 v; token (b, s)
+    int b, s;
+    int pos, page, slot;  // page -1: no place (or none needed), -2: padding
+  };
+  auto unit_at = [&](unsigned u) {
+    Unit x;
+    x.kind = (u >= units_q) + (u >= units_qk);
+    const int local = static_cast<int>(u - (x.kind == 0 ? 0u : x.kind == 1 ? units_q : units_qk));
+    const int tok = local / p.t[x.kind].chunks;
+    x.h0 = (local - tok * p.t[x.kind].chunks) * kUnitRows + g;
+    if (p.compact) {
+      int a = 0, z = p.B;  // the last row that starts at or before tok
+      while (z - a > 1) {
+        const int mid = (a + z) >> 1;
+        if (starts[mid] <= tok) a = mid; else z = mid;
+      }
+      x.b = a;
+      x.s = tok - starts[a];
+    } else {
+      x.b = tok / p.S;
+      x.s = tok - x.b * p.S;
+    }
+    x.tok = x.b * p.S + x.s;
+    return x;
+  };
+  // Starts the loads of a unit's rows, and finds its token's place meanwhile.
+  auto fetch = [&](Unit& x, int stage) {
+    const NewRows& t = p.t[x.kind];
+    const int b = x.b, s = x.s;
+    const int held = __ldg(p.cache_lens + b);
+    x.page = -2;
+    if (!p.compact && s >= new_len(b)) return;  // padding behind the new tokens: not touched
+    const T* const xrow = static_cast<const T*>(t.x) + b * t.xb + s * t.xs;
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int h = x.h0 + i * Lay::kRows;
+      const bool there = h < t.H;
+      const T* const src = xrow + (there ? h : 0) * t.xh;
+      ring.copy(stage, 2 * i, src + lo, there);
+      ring.copy(stage, 2 * i + 1, src + hi, there);
+    }
+    const long long pos = static_cast<long long>(held) + s;
+    x.pos = static_cast<int>(pos);
+    x.page = -1;
+    x.slot = 0;
+    if (x.kind != 0 && held >= 0 && pos < static_cast<long long>(p.max_pages) * p.page_size) {
+      const int at = x.pos / p.page_size;
+      x.slot = x.pos - at * p.page_size;
+      x.page = __ldg(p.table + b * p.table_stride + at);
+      if (x.page < 0 || x.page >= p.n_pages) x.page = -1;
+    }
+  };
+  const unsigned stride = gridDim.x * kWarps;  // unsigned: the last step may pass 2^31
+  unsigned u = blockIdx.x * kWarps + warp;
+  Unit next{};
+  if (u < units) {
+    next = unit_at(u);
+    fetch(next, 0);
+  }
+  copies_commit();
+
   uint64_t frac[Lay::kAngles];
   load_fractions<Lay>(p.inv_freq, l, g, turned, frac);
-  float w[2 * NP];
-  int cur = -1;
-  const unsigned stride = gridDim.x * kWarps;  // unsigned: the last step may pass 2^31
-  for (unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5);
-       u < static_cast<unsigned>(p.units); u += stride) {
-    const int kind = (u >= static_cast<unsigned>(p.units_q)) +
-                     (u >= static_cast<unsigned>(p.units_qk));  // 0 q, 1 k, 2 v
-    const NewRows& t = p.t[kind];
-    const int local =
-        static_cast<int>(u) - (kind == 0 ? 0 : kind == 1 ? p.units_q : p.units_qk);
-    const int tok = local / t.chunks;
-    const int h0 = (local - tok * t.chunks) * kUnitRows + g;
-    const int b = tok / p.S, s = tok - b * p.S;
-    const int held = __ldg(p.cache_lens + b);
-    const int n_new = p.new_lens ? __ldg(p.new_lens + b) : p.S;
-    const T* const xrow = static_cast<const T*>(t.x) + b * t.xb + s * t.xs;
-    uint4 raw[kUnroll][2];
+  stage_gain(gain[0], p.t[0].w, D);
+  stage_gain(gain[1], p.t[1].w, D);
+  __syncthreads();
+  for (int stage = 0; u < units; u += stride, stage ^= 1) {
+    const Unit x = next;
+    if (u + stride < units && u + stride > u) {
+      next = unit_at(u + stride);
+      fetch(next, stage ^ 1);
+    }
+    copies_commit();
+    if (x.page == -2) continue;
+    if (x.kind != 0 && x.page < 0) {  // no place in the cache: the token is not written
+      if (lane == 0) atomicOr(p.err, kErrCache);
+      continue;
+    }
+    const NewRows& t = p.t[x.kind];
+    f32x2 own[NP], other[NP], w[NP];
+    if (x.kind != 2) {  // the gain goes with the turn: see norm_rope.cu
+      load_gain<NP>(gain[x.kind], lo, hi, w);
+      if (p.rot > 0) {
+        float c[NP], sn[NP];
+        row_angles<Lay>(x.pos, frac, l, c, sn);
+        turn_factors<NP, kInterleaved>(c, sn, 1.f, own, other);
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int h = h0 + i * Lay::kRows;
-      raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < t.H) {
-        raw[i][0] = *reinterpret_cast<const uint4*>(xrow + h * t.xh + lo);
-        raw[i][1] = *reinterpret_cast<const uint4*>(xrow + h * t.xh + hi);
-      }
-    }
-    if (n_new < 0 || n_new > p.S) {
-      if (lane == 0 && kind == 1) atomicOr(p.err, kErrCache);
-    }
-    if (s >= n_new) continue;  // padding behind the sequence's new tokens: nothing is written
-    const long long pos = static_cast<long long>(held) + s;
-    int page = -1, slot = 0;  // this token's place
-    if (kind != 0) {
-      if (held >= 0 && pos < static_cast<long long>(p.max_pages) * p.page_size) {
-        const int at = static_cast<int>(pos / p.page_size);
-        slot = static_cast<int>(pos - static_cast<long long>(at) * p.page_size);
-        page = __ldg(p.table + b * p.table_stride + at);
-      }
-      if (page < 0 || page >= p.n_pages) {  // no place in the cache: the token is not written
-        if (lane == 0) atomicOr(p.err, kErrCache);
-        continue;
-      }
-    }
-    if (kind != cur) {
-      cur = kind;
-      if (t.w != nullptr) load_columns<NP>(t.w, lo, hi, w);
-    }
-    float c[NP], sn[NP];
-    if (kind != 2 && p.rot > 0) row_angles<Lay>(static_cast<int>(pos), frac, l, c, sn);
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int h = h0 + i * Lay::kRows;
-      if (h - g >= t.H) break;  // the same for the whole warp
-      float z[2 * NP];
-      unpack(raw[i][0], z, 0, T());
-      unpack(raw[i][1], z, NP, T());
-      if (kind != 2) {
-        if (t.w != nullptr) {
-          const float r = rsqrtf(row_sum<Lay::kLanes>(sum_squares(z)) * (1.f / D) + p.eps);
-#pragma unroll
-          for (int e = 0; e < 2 * NP; ++e) z[e] = z[e] * r * w[e];
+        for (int i = 0; i < NP; ++i) {
+          own[i] = mul2(own[i], w[i]);
+          other[i] = mul2(other[i], partner<NP, kInterleaved>(w, i));
         }
-        if (turned) rotate<NP>(z, c, sn, p.interleaved != 0, 1.f);
+      }
+    }
+    copies_wait_all_but_last();
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int h = x.h0 + i * Lay::kRows;
+      if (h - g >= t.H) break;  // the same for the whole warp
+      f32x2 z[NP];
+      unpack<NP>(ring.read(stage, 2 * i), z, 0, T());
+      unpack<NP>(ring.read(stage, 2 * i + 1), z, NP / 2, T());
+      if (x.kind != 2) {
+        float r = 1.f;
+        if (t.w != nullptr)
+          r = rsqrtf(row_sum<Lay::kLanes>(dot<NP>(z, z)) * (1.f / D) + p.eps);
+        if (turned) {
+          turn<NP, kInterleaved>(z, own, other);
+        } else {
+#pragma unroll
+          for (int e = 0; e < NP; ++e) z[e] = mul2(z[e], w[e]);
+        }
+        const f32x2 r2 = pack2(r, r);
+#pragma unroll
+        for (int e = 0; e < NP; ++e) z[e] = mul2(z[e], r2);
       }
       if (h >= t.H) continue;
-      if (kind == 0) {
-        T* const dst = p.q_out + (static_cast<long long>(tok) * t.H + h) * D;
-        *reinterpret_cast<uint4*>(dst + lo) = repack(z, 0, T());
-        *reinterpret_cast<uint4*>(dst + hi) = repack(z, NP, T());
+      if (x.kind == 0) {
+        T* const dst = p.q_out + (static_cast<long long>(x.tok) * t.H + h) * D;
+        *reinterpret_cast<uint4*>(dst + lo) = repack<NP>(z, 0, T());
+        *reinterpret_cast<uint4*>(dst + hi) = repack<NP>(z, NP / 2, T());
         continue;
       }
-      const int w_kv = kind - 1;
-      const long long off = page * p.cs[w_kv][0] + slot * p.cs[w_kv][1] + h * p.cs[w_kv][2];
+      const int kv = x.kind - 1;
+      const long long off = x.page * p.cs[kv][0] + x.slot * p.cs[kv][1] + h * p.cs[kv][2];
       if (kE4M3) {
-        uint8_t* const dst = static_cast<uint8_t*>(p.cache[w_kv]) + off;
-        const float scale = __ldg(p.descale[w_kv] + h);
-        *reinterpret_cast<uint2*>(dst + lo) = codes8(z, 0, scale);
-        *reinterpret_cast<uint2*>(dst + hi) = codes8(z, NP, scale);
+        uint8_t* const dst = static_cast<uint8_t*>(p.cache[kv]) + off;
+        const float inv = __frcp_rn(__ldg(p.descale[kv] + h));
+        *reinterpret_cast<uint2*>(dst + lo) = codes8<NP>(z, 0, pack2(inv, inv));
+        *reinterpret_cast<uint2*>(dst + hi) = codes8<NP>(z, NP / 2, pack2(inv, inv));
       } else {
-        T* const dst = static_cast<T*>(p.cache[w_kv]) + off;
-        *reinterpret_cast<uint4*>(dst + lo) = repack(z, 0, T());
-        *reinterpret_cast<uint4*>(dst + hi) = repack(z, NP, T());
+        T* const dst = static_cast<T*>(p.cache[kv]) + off;
+        *reinterpret_cast<uint4*>(dst + lo) = repack<NP>(z, 0, T());
+        *reinterpret_cast<uint4*>(dst + hi) = repack<NP>(z, NP / 2, T());
       }
     }
   }
 }
 
-template <int D, int kUnroll, bool kE4M3>
+template <int D, int kUnroll, bool kE4M3, bool kInterleaved>
 cudaError_t launch_append(AppendParams p, int tokens, cudaStream_t stream) {
   constexpr int kUnitRows = kUnroll * RowLayout<__nv_bfloat16, D>::kRows;
   for (NewRows& t : p.t) t.chunks = (t.H + kUnitRows - 1) / kUnitRows;
-  p.units_q = tokens * p.t[0].chunks;
-  p.units_qk = p.units_q + tokens * p.t[1].chunks;
-  p.units = p.units_qk + tokens * p.t[2].chunks;
-  const int blocks = std::min((p.units + kWarps - 1) / kWarps, 3 * sm_count());
-  paged_append_kernel<D, kUnroll, kE4M3><<<blocks, kThreads, 0, stream>>>(p);
+  p.tokens = tokens;
+  p.compact = p.new_lens != nullptr && p.S > 1 && p.B <= kMaxScan;
+  const int units = tokens * (p.t[0].chunks + p.t[1].chunks + p.t[2].chunks);
+  const int blocks = std::min((units + kWarps - 1) / kWarps, 2 * sm_count());
+  constexpr int kSmem = kWarps * Ring<kUnroll * 2>::kBytes;
+  const auto kern = paged_append_kernel<D, kUnroll, kE4M3, kInterleaved>;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<blocks, kThreads, kSmem, stream>>>(p);
   count_launch(2);
   return cudaGetLastError();
 }
@@ -182,9 +282,13 @@ cudaError_t launch_append(AppendParams p, int tokens, cudaStream_t stream) {
 template <int D, bool kE4M3>
 cudaError_t launch_sized(const AppendParams& p, int tokens, cudaStream_t stream) {
   const long long rows = static_cast<long long>(tokens) * (p.t[0].H + 2LL * p.t[1].H);
-  if (rows / (4 * RowLayout<__nv_bfloat16, D>::kRows) >= 2LL * sm_count() * kWarps)
-    return launch_append<D, 4, kE4M3>(p, tokens, stream);
-  return launch_append<D, 1, kE4M3>(p, tokens, stream);
+  const bool wide =
+      rows / (4 * RowLayout<__nv_bfloat16, D>::kRows) >= 2LL * sm_count() * kWarps;
+  if (p.interleaved)
+    return wide ? launch_append<D, 4, kE4M3, true>(p, tokens, stream)
+                : launch_append<D, 1, kE4M3, true>(p, tokens, stream);
+  return wide ? launch_append<D, 4, kE4M3, false>(p, tokens, stream)
+              : launch_append<D, 1, kE4M3, false>(p, tokens, stream);
 }
 
 void take_strides(const int64_t* given, int S, int H, int d, NewRows& t) {
@@ -265,7 +369,7 @@ extern "C" cp_status cp_paged_append(const cp_paged_cache* cache, const void* q,
   p.err = device_error_word();
   if (!p.err) return CP_ERR_CUDA;
   p.n_pages = cache->n_pages; p.page_size = cache->page_size; p.max_pages = cache->max_pages;
-  p.S = S; p.rot = rot_dim; p.interleaved = interleaved; p.eps = eps;
+  p.B = B; p.S = S; p.rot = rot_dim; p.interleaved = interleaved; p.eps = eps;
   const bool e4m3 = cache->elem_bytes == 1;
   const cudaError_t e =
       d == 128 ? (e4m3 ? launch_sized<128, true>(p, B * S, stream)

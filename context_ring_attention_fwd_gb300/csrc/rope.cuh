@@ -104,54 +104,139 @@ __device__ __forceinline__ void row_angles(int position, const uint64_t (&f)[Lay
   }
 }
 
-// One 16-byte vector as fp32 values and back (each value rounded to nearest).
-__device__ __forceinline__ void unpack(const uint4& v, float (&z)[16], int at, __nv_bfloat16) {
+// The arithmetic is on pairs of neighbouring fp32 values, two to an
+// instruction (fma / mul / add.rn.f32x2, each value rounded to nearest): these
+// kernels issue about as many instructions as the bytes they move leave time for.
+typedef uint64_t f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 neg2(f32x2 v) { return v ^ 0x8000000080000000ull; }
+__device__ __forceinline__ f32x2 swap2(f32x2 v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return pack2(hi, lo);
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return lo + hi;
+}
+
+// One 16-byte vector as pairs of fp32 values and back (rounded to nearest).
+// A lane's two vectors are z[0 .. NP / 2) and z[NP / 2 .. NP).
+template <int NP>
+__device__ __forceinline__ void unpack(const uint4& v, f32x2 (&z)[NP], int at, __nv_bfloat16) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    z[at + 2 * i] = __uint_as_float(w[i] << 16);
-    z[at + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    z[at + i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-__device__ __forceinline__ void unpack(const uint4& v, float (&z)[8], int at, float) {
-  z[at] = __uint_as_float(v.x);
-  z[at + 1] = __uint_as_float(v.y);
-  z[at + 2] = __uint_as_float(v.z);
-  z[at + 3] = __uint_as_float(v.w);
+template <int NP>
+__device__ __forceinline__ void unpack(const uint4& v, f32x2 (&z)[NP], int at, float) {
+  z[at] = pack2(__uint_as_float(v.x), __uint_as_float(v.y));
+  z[at + 1] = pack2(__uint_as_float(v.z), __uint_as_float(v.w));
 }
-__device__ __forceinline__ uint4 repack(const float (&z)[16], int at, __nv_bfloat16) {
+template <int NP>
+__device__ __forceinline__ uint4 repack(const f32x2 (&z)[NP], int at, __nv_bfloat16) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(z[at + 2 * i], z[at + 2 * i + 1]);
+    float lo, hi;
+    unpack2(z[at + i], lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint4 repack(const float (&z)[8], int at, float) {
-  return make_uint4(__float_as_uint(z[at]), __float_as_uint(z[at + 1]), __float_as_uint(z[at + 2]),
-                    __float_as_uint(z[at + 3]));
+template <int NP>
+__device__ __forceinline__ uint4 repack(const f32x2 (&z)[NP], int at, float) {
+  float f[4];
+  unpack2(z[at], f[0], f[1]);
+  unpack2(z[at + 1], f[2], f[3]);
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                    __float_as_uint(f[3]));
 }
 
-// Rotate the lane's pairs in place (sign -1 turns back).
-template <int NP>
-__device__ __forceinline__ void rotate(float (&z)[2 * NP], const float (&c)[NP],
-                                       const float (&s)[NP], bool interleaved, float sign) {
-  if (interleaved) {
+// cos and sin of the lane's NP angles as the pairs that its entries meet:
+// entry pair z[i] turns to own[i] * z[i] + other[i] * partner, where the partner
+// is z[i +- NP / 2], or z[i] with its entries exchanged in the interleaved form.
+// sign -1 turns back.
+template <int NP, bool kInterleaved>
+__device__ __forceinline__ void turn_factors(const float (&c)[NP], const float (&s)[NP],
+                                             float sign, f32x2 (&own)[NP], f32x2 (&other)[NP]) {
 #pragma unroll
-    for (int e = 0; e < NP; ++e) {
-      const float a = z[2 * e], b = z[2 * e + 1], t = sign * s[e];
-      z[2 * e] = a * c[e] - b * t;
-      z[2 * e + 1] = b * c[e] + a * t;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < NP; ++e) {
-      const float a = z[e], b = z[e + NP], t = sign * s[e];
-      z[e] = a * c[e] - b * t;
-      z[e + NP] = b * c[e] + a * t;
+  for (int i = 0; i < NP; ++i) {
+    if (kInterleaved) {
+      own[i] = pack2(c[i], c[i]);
+      other[i] = pack2(-sign * s[i], sign * s[i]);
+    } else {
+      const int e = (2 * i) % NP;
+      const float t = i < NP / 2 ? -sign : sign;
+      own[i] = pack2(c[e], c[e + 1]);
+      other[i] = pack2(t * s[e], t * s[e + 1]);
     }
   }
+}
+template <int NP, bool kInterleaved>
+__device__ __forceinline__ f32x2 partner(const f32x2 (&z)[NP], int i) {
+  return kInterleaved ? swap2(z[i]) : z[(i + NP / 2) % NP];
+}
+// The lane's entries turned.
+template <int NP, bool kInterleaved>
+__device__ __forceinline__ void turn(f32x2 (&z)[NP], const f32x2 (&own)[NP],
+                                     const f32x2 (&other)[NP]) {
+  f32x2 y[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    y[i] = fma2(z[i], own[i], mul2(partner<NP, kInterleaved>(z, i), other[i]));
+#pragma unroll
+  for (int i = 0; i < NP; ++i) z[i] = y[i];
+}
+
+// A warp's ring of two stages of kVecs 16-byte vectors per lane.  A lane copies
+// what it will read itself, so nothing is ordered but its own copies: the next
+// unit of work is under way while one is computed, without registers for it.
+template <int kVecs>
+struct Ring {
+  static constexpr int kBytes = 2 * kVecs * 512;  // per warp
+  uint32_t base;
+  __device__ uint32_t at(int stage, int v) const { return base + (stage * kVecs + v) * 512; }
+  __device__ void copy(int stage, int v, const void* src, bool there) const {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(stage, v)), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+  }
+  __device__ uint4 read(int stage, int v) const {
+    uint4 u;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "r"(at(stage, v))
+                 : "memory");
+    return u;
+  }
+};
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the last committed group have landed.
+__device__ __forceinline__ void copies_wait_all_but_last() {
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
 
 // Sum over the lanes of one row.
@@ -162,25 +247,33 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-template <int N>
-__device__ __forceinline__ float sum_squares(const float (&z)[N]) {
-  float a = 0.f, b = 0.f;
+// Sum over the lane's entries of a * b.
+template <int NP>
+__device__ __forceinline__ float dot(const f32x2 (&a)[NP], const f32x2 (&b)[NP]) {
+  f32x2 x = mul2(a[0], b[0]), y = mul2(a[1], b[1]);
 #pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    a = fmaf(z[i], z[i], a);
-    b = fmaf(z[i + 1], z[i + 1], b);
+  for (int i = 2; i < NP; i += 2) {
+    x = fma2(a[i], b[i], x);
+    y = fma2(a[i + 1], b[i + 1], y);
   }
-  return a + b;
+  return sum2(x) + sum2(y);
 }
 
-// The lane's columns of an fp32 vector of length d.
+// A gain vector laid out for a row's lanes: the block copies it to shared memory
+// once (ones where it is null), lanes read their columns as pairs.
+__device__ __forceinline__ void stage_gain(float* to, const float* __restrict__ w, int d) {
+  for (int i = threadIdx.x; i < d; i += blockDim.x) to[i] = w != nullptr ? __ldg(w + i) : 1.f;
+}
 template <int NP>
-__device__ __forceinline__ void load_columns(const float* __restrict__ w, int lo, int hi,
-                                             float (&z)[2 * NP]) {
+__device__ __forceinline__ void load_gain(const float* w, int lo, int hi, f32x2 (&z)[NP]) {
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    z[i] = __ldg(w + lo + i);
-    z[NP + i] = __ldg(w + hi + i);
+  for (int i = 0; i < NP / 2; i += 2) {
+    const float4 a = *reinterpret_cast<const float4*>(w + lo + 2 * i);
+    const float4 b = *reinterpret_cast<const float4*>(w + hi + 2 * i);
+    z[i] = pack2(a.x, a.y);
+    z[i + 1] = pack2(a.z, a.w);
+    z[NP / 2 + i] = pack2(b.x, b.y);
+    z[NP / 2 + i + 1] = pack2(b.z, b.w);
   }
 }
 

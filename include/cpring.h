@@ -547,7 +547,8 @@ typedef struct cp_paged_cache {
  * rotation of cp_qk_norm_rope on the way.  Token s of sequence b (s <
  * new_lens[b]) has the position p = cache_lens[b] + s: its key, normed and
  * rotated by p, and its value are written to the cache's slot of p, rounded
- * once to the cache's type (E4M3: the code of x / descale[head], saturated).
+ * once to the cache's type (E4M3: the code of x * (1 / descale[head]), both
+ * fp32 operations rounded to nearest, saturated).
  * Its query row, normed and rotated likewise, goes to q_out.
  *  q, k, v    device, bf16 [B,S,Hq,d], [B,S,Hk,d], [B,S,Hk,d] with strides as
  *             for cp_qk_norm_rope.  Hq = 0 with q, q_out NULL: keys and
