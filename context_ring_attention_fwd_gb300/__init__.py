@@ -29,7 +29,7 @@ from ._binding import (  # noqa: F401
     cp_ring_emulated_workspace_bytes, cp_ring_schedule, cp_ring_schedule_device, cp_ring_step,
     cp_ulysses_attn_fwd,
     cp_ulysses_workspace_bytes,
-    cp_ring_traffic, cp_status_string, doc_offsets_tensor, launch_counts, lib,
+    cp_ring_traffic, cp_status_string, doc_offsets_tensor, launch_counts, lib, native,
     test_set_wait_fault)
 
 __all__ = [
@@ -178,21 +178,14 @@ def ring_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.
     return dq, dk, dv
 
 
-def _like(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    """A contiguous tensor of t's shape, type and device (None for None)."""
-    return None if t is None else t.new_empty(t.shape)
-
-
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight=None, k_weight=None,
                  inv_freq=None, positions=None, eps: float = 1e-6, interleaved: bool = False,
                  stream=None):
     """Per-head RMS norm of q [B,S,Hq,d] and k [B,S,Hk,d] and their rotation,
     ready for ring_attn_fwd: allocates and returns contiguous (q_out, k_out) of
     the inputs' type.  q and k may be strided views; k None gives (q_out, None)."""
-    q_out, k_out = _like(q), _like(k)
-    cp_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps, interleaved,
-                    stream)
-    return q_out, k_out
+    return cp_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, None, None, eps,
+                           interleaved, stream)
 
 
 def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: torch.Tensor,
@@ -202,11 +195,8 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: to
     ring_attn_bwd): allocates and returns (dq, dk, dq_weight, dk_weight), the
     first two contiguous and of the inputs' type, the others fp32 [d]; None
     where the operand is None."""
-    dq, dk, dqw = _like(q), _like(k), _like(q_weight)
-    dkw = _like(k_weight) if k is not None else None
-    cp_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, dq, dk, dqw,
-                        dkw, eps, interleaved, None, stream)
-    return dq, dk, dqw, dkw
+    return native().qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions,
+                                     None, None, None, None, eps, interleaved, None, stream, True)
 
 
 def paged_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
@@ -217,11 +207,9 @@ def paged_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     """Append k, v [B,S,Hk,d] to the paged caches, k normed and rotated by its
     position, and return q normed and rotated likewise (in q_out, allocated if
     None; its rows behind a sequence's new tokens are not written)."""
-    if q is not None and q_out is None:
-        q_out = _like(q)
-    cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens, q_weight, k_weight,
-                    inv_freq, q_out, eps, interleaved, k_descale, v_descale, stream)
-    return q_out if q is not None else None
+    return cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens, q_weight,
+                           k_weight, inv_freq, q_out, eps, interleaved, k_descale, v_descale,
+                           stream)
 
 
 def paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -231,9 +219,5 @@ def paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     """Decode attention over the paged caches, the shared prefix attended once
     for the whole batch: allocates and returns (out [B,n_q,Hq,d] bf16, lse
     [B,Hq,n_q] fp32)."""
-    B, n_q, Hq, d = q.shape
-    out = _like(q)
-    lse = q.new_empty((B, Hq, n_q), dtype=torch.float32)
-    cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out, lse, prefix_pages,
-                         prefix_len, k_descale, v_descale, workspace, stream)
-    return out, lse
+    return cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, None, None,
+                                prefix_pages, prefix_len, k_descale, v_descale, workspace, stream)

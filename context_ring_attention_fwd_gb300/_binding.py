@@ -1,4 +1,5 @@
-"""ctypes binding of libcpring.so: argument marshalling only.
+"""Binding of libcpring.so: argument marshalling only, through ctypes or, for
+the calls of a few microseconds, the extension of csrc/torch_calls.cpp.
 
 Every computation runs in the library's CUDA kernels; torch supplies device
 memory and streams.  If the library is missing the calls raise instead of
@@ -7,6 +8,7 @@ falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from typing import Optional, Sequence
@@ -15,6 +17,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libcpring.so")
+EXT_PATH = os.path.join(_PKG, "_lib", "cpring_torch.so")
 
 CP_OK = 0
 STATUS_NAMES = {
@@ -162,77 +165,28 @@ def doc_offsets_tensor(doc_offsets, device) -> Optional[torch.Tensor]:
     return t.contiguous()
 
 
-# The calls around the attention are short enough on the device for their host side to
-# count: the checks below read each property of a tensor once, and pointers travel as plain
-# integers.
-def _operand(t, name: str, dtype: torch.dtype, index: int, shape=None) -> int:
-    """t's address, after checking its type, device, shape and that its last
-    dimension is contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must live on cuda:{index}, got {t.device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t.data_ptr()
+_ext = None
 
 
-def _dense(t, name: str, dtype: torch.dtype, index: int, shape=None) -> int:
-    at = _operand(t, name, dtype, index, shape)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return at
-
-
-def _optional(t, name: str, dtype: torch.dtype, index: int, shape=None):
-    return None if t is None else _dense(t, name, dtype, index, shape)
-
-
-def _cuda_index(t, name: str) -> int:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{name} must live on a CUDA device")
-    return index
-
-
-_Steps = _i64 * 3
-
-
-def _steps(t):
-    """The three leading strides of [a, b, c, d], None when contiguous.  The
-    stride of a dimension of one entry is never used and passed as 0."""
-    if t is None or t.is_contiguous():
-        return None
-    a, b, c, _ = t.stride()
-    n = t.shape
-    return _Steps(a if n[0] > 1 else 0, b if n[1] > 1 else 0, c if n[2] > 1 else 0)
-
-
-def _call_on(name: str, index: int, stream, *args) -> None:
-    """Run a library call with device `index` current, on `stream` or, if
-    None, on that device's current stream."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)
-    elif isinstance(stream, torch.cuda.Stream):
-        if stream.device.index != index:
-            raise ValueError(f"stream belongs to {stream.device}, the tensors to cuda:{index}")
-        raw = stream.cuda_stream
-    else:
-        raw = int(stream)
-    fn = getattr(_lib or lib(), name)
-    if torch._C._cuda_getDevice() == index:
-        st = fn(*args, raw)
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args, raw)
-    if st != CP_OK:
-        raise CpError(name, st)
+def native():
+    """The extension that checks torch tensors and calls the library for the
+    operators of a few microseconds (loaded once).  Raises if it has not been
+    built."""
+    global _ext
+    if _ext is None:
+        lib()
+        with _lock:
+            if _ext is None:
+                if not os.path.exists(EXT_PATH):
+                    raise RuntimeError(
+                        f"{EXT_PATH} is missing: build it with "
+                        "`python -c 'import __graft_entry__ as g; g.build()'`")
+                spec = importlib.util.spec_from_file_location("cpring_torch", EXT_PATH)
+                ext = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(ext)
+                ext.set_error(CpError)
+                _ext = ext
+    return _ext
 
 
 # --------------------------------------------------------------------- C ABI
@@ -575,36 +529,15 @@ def launch_counts():
 
 
 # ------------------------------------------------- norm, rotation, paged cache
-def _rows4(t, name: str):
-    if not isinstance(t, torch.Tensor) or t.dim() != 4:
-        raise ValueError(f"{name} must be a tensor of four dimensions")
-    return t.shape
-
-
 def cp_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out,
-                    eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+                    eps: float = 1e-6, interleaved: bool = False, stream=None):
     """Per-head RMS norm and rotation of q [B,S,Hq,d] and k [B,S,Hk,d] (bf16 or
     fp32, strided views allowed; k None: q only) into the contiguous q_out and
-    k_out.  Weights fp32 [d] (None: not normed), inv_freq fp32 [rot_dim / 2]
-    (None: not rotated), positions int32 [B,S] (None: the token's index)."""
-    shape = _rows4(q, "q")
-    B, S, Hq, d = shape
-    dev, dt, f32 = _cuda_index(q, "q"), q.dtype, torch.float32
-    if dt is not torch.bfloat16 and dt is not f32:
-        raise TypeError("q must be bf16 or fp32")
-    q_at, qo_at = _operand(q, "q", dt, dev), _dense(q_out, "q_out", dt, dev, shape)
-    Hk, k_at, ko_at = 0, None, None
-    if k is not None:
-        Hk = _rows4(k, "k")[2]
-        k_at = _operand(k, "k", dt, dev, (B, S, Hk, d))
-        ko_at = _dense(k_out, "k_out", dt, dev, (B, S, Hk, d))
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _call_on("cp_qk_norm_rope", dev, stream, q_at, _steps(q), k_at, _steps(k),
-             _optional(q_weight, "q_weight", f32, dev, (d,)),
-             _optional(k_weight, "k_weight", f32, dev, (d,)), eps,
-             _optional(inv_freq, "inv_freq", f32, dev, (rot // 2,)), rot, bool(interleaved),
-             _optional(positions, "positions", torch.int32, dev, (B, S)), qo_at, ko_at, B, S, Hq,
-             Hk, d, dt is not f32)
+    k_out (allocated if None), which it returns.  Weights fp32 [d] (None: not
+    normed), inv_freq fp32 [rot_dim / 2] (None: not rotated), positions int32
+    [B,S] (None: the token's index)."""
+    return (_ext or native()).qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, q_out,
+                                           k_out, eps, interleaved, stream)
 
 
 def cp_qk_norm_rope_bwd_workspace_bytes(B: int, S: int, Hq: int, Hk: int, d: int) -> int:
@@ -616,98 +549,25 @@ def cp_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, posi
                         workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Backward of cp_qk_norm_rope: from dq_out, dk_out (contiguous) and the
     forward's inputs, writes dq, dk (the inputs' type, strided views allowed)
-    and the weights' gradients (fp32 [d], or None).  workspace: a uint8 device
-    tensor (allocated here if None)."""
-    shape = _rows4(q, "q")
-    B, S, Hq, d = shape
-    dev, dt, f32 = _cuda_index(q, "q"), q.dtype, torch.float32
-    if dt is not torch.bfloat16 and dt is not f32:
-        raise TypeError("q must be bf16 or fp32")
-    q_at, dq_at = _operand(q, "q", dt, dev), _operand(dq, "dq", dt, dev, shape)
-    dqo_at = _dense(dq_out, "dq_out", dt, dev, shape)
-    Hk, k_at, dk_at, dko_at, dk_steps = 0, None, None, None, None
-    if k is not None:
-        Hk = _rows4(k, "k")[2]
-        k_at = _operand(k, "k", dt, dev, (B, S, Hk, d))
-        dk_at = _operand(dk, "dk", dt, dev, (B, S, Hk, d))
-        dko_at = _dense(dk_out, "dk_out", dt, dev, (B, S, Hk, d))
-        dk_steps = _steps(dk)
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    if workspace is None:
-        need = cp_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hk, d)
-        if need < 0:
-            raise CpError("cp_qk_norm_rope_bwd_workspace_bytes", STATUS_CODES["CP_ERR_SHAPE"])
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _call_on("cp_qk_norm_rope_bwd", dev, stream, dqo_at, dko_at, q_at, _steps(q), k_at, _steps(k),
-             _optional(q_weight, "q_weight", f32, dev, (d,)),
-             _optional(k_weight, "k_weight", f32, dev, (d,)), eps,
-             _optional(inv_freq, "inv_freq", f32, dev, (rot // 2,)), rot, bool(interleaved),
-             _optional(positions, "positions", torch.int32, dev, (B, S)), dq_at, _steps(dq), dk_at,
-             dk_steps, _optional(dq_weight, "dq_weight", f32, dev, (d,)),
-             _optional(dk_weight, "dk_weight", f32, dev, (d,)), B, S, Hq, Hk, d, dt is not f32,
-             _dense(workspace, "workspace", torch.uint8, dev), workspace.numel())
-
-
-def _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, B: int,
-                  dev: int) -> PagedCacheStruct:
-    """The cp_paged_cache of caches [pages, page_size, Hk, d] (bf16, or uint8
-    E4M3 codes with fp32 [Hk] descales) and an int32 table [B, max_pages]."""
-    dt = k_cache.dtype if isinstance(k_cache, torch.Tensor) else None
-    e4m3 = dt is torch.uint8
-    if not e4m3 and dt is not torch.bfloat16:
-        raise TypeError("k_cache must be bf16 or uint8 (E4M3 codes)")
-    shape = _rows4(k_cache, "k_cache")
-    n_pages, page_size, Hk, d = shape
-    k_at = _operand(k_cache, "k_cache", dt, dev)
-    v_at = _operand(v_cache, "v_cache", dt, dev, shape)
-    table_at = _operand(page_table, "page_table", torch.int32, dev)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must have two dimensions")
-    rows, max_pages = page_table.shape
-    if rows != B:
-        raise ValueError(f"page_table must have {B} rows, got {rows}")
-    if e4m3:
-        kd_at = _dense(k_descale, "k_descale", torch.float32, dev, (Hk,))
-        vd_at = _dense(v_descale, "v_descale", torch.float32, dev, (Hk,))
-    elif k_descale is None and v_descale is None:
-        kd_at = vd_at = None
-    else:
-        raise ValueError("k_descale and v_descale go with an E4M3 cache")
-    ks = v_s = _Steps(page_size * Hk * d, Hk * d, d)
-    if not k_cache.is_contiguous():
-        ks = _steps(k_cache)
-    if not v_cache.is_contiguous():
-        v_s = _steps(v_cache)
-    return PagedCacheStruct(k_at, v_at, ks, v_s, kd_at, vd_at, table_at,
-                            page_table.stride(0) if rows > 1 else max_pages, n_pages, page_size,
-                            max_pages, Hk, d, 1 if e4m3 else 2)
+    and the weights' gradients (fp32 [d], or None: not wanted).  workspace: a
+    uint8 device tensor (allocated here if None)."""
+    (_ext or native()).qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq,
+                                        positions, dq, dk, dq_weight, dk_weight, eps, interleaved,
+                                        workspace, stream, False)
 
 
 def cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens, q_weight,
                     k_weight, inv_freq, q_out, eps: float = 1e-6, interleaved: bool = False,
-                    k_descale=None, v_descale=None, stream=None) -> None:
+                    k_descale=None, v_descale=None, stream=None):
     """Norm, rotate and append k, v [B,S,Hk,d] bf16 (strided views allowed) to
-    the paged caches [pages, page_size, Hk, d] at positions cache_lens[b] + s
-    (int32 [B]), for s < new_lens[b] (int32 [B], None: all S); q [B,S,Hq,d]
-    (None: keys and values only) is normed and rotated into q_out."""
-    B, S, Hk, d = _rows4(k, "k")
-    dev, bf16, i32, f32 = _cuda_index(k, "k"), torch.bfloat16, torch.int32, torch.float32
-    cache = _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, B, dev)
-    shape = (B, S, cache.Hk, cache.d)
-    k_at, v_at = _operand(k, "k", bf16, dev, shape), _operand(v, "v", bf16, dev, shape)
-    Hq, q_at, qo_at = 0, None, None
-    if q is not None:
-        Hq = _rows4(q, "q")[2]
-        q_at = _operand(q, "q", bf16, dev, (B, S, Hq, d))
-        qo_at = _dense(q_out, "q_out", bf16, dev, (B, S, Hq, d))
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _call_on("cp_paged_append", dev, stream, ctypes.byref(cache), q_at, _steps(q), k_at, _steps(k),
-             v_at, _steps(v), _dense(cache_lens, "cache_lens", i32, dev, (B,)),
-             _optional(new_lens, "new_lens", i32, dev, (B,)),
-             _optional(q_weight, "q_weight", f32, dev, (d,)),
-             _optional(k_weight, "k_weight", f32, dev, (d,)), eps,
-             _optional(inv_freq, "inv_freq", f32, dev, (rot // 2,)), rot, bool(interleaved), qo_at,
-             B, S, Hq)
+    the paged caches [pages, page_size, Hk, d] (bf16, or uint8 E4M3 codes with
+    fp32 [Hk] descales) at positions cache_lens[b] + s (int32 [B]) of the table
+    int32 [B, max_pages], for s < new_lens[b] (int32 [B], None: all S); q
+    [B,S,Hq,d] (None: keys and values only) is normed and rotated into q_out
+    (allocated if None), which it returns."""
+    return (_ext or native()).paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens,
+                                           new_lens, q_weight, k_weight, inv_freq, q_out, eps,
+                                           interleaved, k_descale, v_descale, stream)
 
 
 def cp_paged_attn_decode_workspace_bytes(B: int, n_q: int, Hq: int, Hk: int, d: int,
@@ -717,29 +577,13 @@ def cp_paged_attn_decode_workspace_bytes(B: int, n_q: int, Hq: int, Hk: int, d: 
 
 def cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out, lse, prefix_pages=None,
                          prefix_len: int = 0, k_descale=None, v_descale=None,
-                         workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+                         workspace: Optional[torch.Tensor] = None, stream=None):
     """Decode attention of q [B,n_q,Hq,d] bf16 (strided views allowed), the
     last n_q tokens of each sequence of seq_lens (int32 [B], 0 = unused row),
     over the paged caches of cp_paged_append; the keys of positions below
     prefix_len are read through prefix_pages (int32) once for the whole batch.
-    out [B,n_q,Hq,d] bf16, lse [B,Hq,n_q] fp32; workspace a uint8 device
-    tensor (allocated here if None)."""
-    B, n_q, Hq, d = _rows4(q, "q")
-    dev, bf16, i32 = _cuda_index(q, "q"), torch.bfloat16, torch.int32
-    cache = _cache_struct(k_cache, v_cache, page_table, k_descale, v_descale, B, dev)
-    shape = (B, n_q, Hq, cache.d)
-    q_at, out_at = _operand(q, "q", bf16, dev, shape), _dense(out, "out", bf16, dev, shape)
-    lse_at = _dense(lse, "lse", torch.float32, dev, (B, Hq, n_q))
-    prefix_len, pages_at = int(prefix_len), None
-    if prefix_pages is not None:
-        pages_at = _dense(prefix_pages, "prefix_pages", i32, dev, (prefix_pages.numel(),))
-        if prefix_pages.numel() * cache.page_size < prefix_len:
-            raise ValueError("prefix_pages holds fewer tokens than prefix_len")
-    if workspace is None:
-        need = cp_paged_attn_decode_workspace_bytes(B, n_q, Hq, cache.Hk, d, prefix_len)
-        if need < 0:
-            raise CpError("cp_paged_attn_decode_workspace_bytes", STATUS_CODES["CP_ERR_SHAPE"])
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _call_on("cp_paged_attn_decode", dev, stream, ctypes.byref(cache), q_at, _steps(q),
-             _dense(seq_lens, "seq_lens", i32, dev, (B,)), pages_at, prefix_len, out_at, lse_at, B,
-             n_q, Hq, _dense(workspace, "workspace", torch.uint8, dev), workspace.numel())
+    out [B,n_q,Hq,d] bf16 and lse [B,Hq,n_q] fp32 (allocated if None) are
+    returned; workspace a uint8 device tensor (allocated here if None)."""
+    return (_ext or native()).paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out,
+                                                lse, prefix_pages, prefix_len, k_descale,
+                                                v_descale, workspace, stream)

@@ -1,7 +1,8 @@
-"""Build libcpring.so in-tree with nvcc for sm_103a.
+"""Build libcpring.so in-tree with nvcc for sm_103a, and the Python extension
+that calls it on torch tensors (cpring_torch.so, host code only).
 
-Sources are compiled in parallel (one nvcc process per translation unit)
-and linked into context_ring_attention_fwd_gb300/_lib/libcpring.so.  Object
+Sources are compiled in parallel (one nvcc or g++ process per translation unit)
+and linked into context_ring_attention_fwd_gb300/_lib/.  Object
 files go to context_ring_attention_fwd_gb300/_lib/obj/.  Nothing here needs a
 GPU: nvcc cross-compiles.
 """
@@ -12,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "_lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "libcpring.so")
+EXT = os.path.join(LIBDIR, "cpring_torch.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["attn_sm103.cu", "attn_f32.cu", "merge.cu", "noalloc.cu", "ring_emulation.cpp",
@@ -72,17 +75,47 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _run(cmd, what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_ext() -> str:
+    obj = os.path.join(OBJDIR, "torch_calls.o")
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], cuda]
+    _run(["g++", "-std=c++17", "-O2", "-fPIC", *(f"-I{d}" for d in dirs), "-c",
+          os.path.join(CSRC, "torch_calls.cpp"), "-o", obj], "g++ torch_calls.cpp")
+    return obj
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libcpring.so; returns its path."""
+    """Compile every source, link libcpring.so and the Python extension;
+    returns the library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext = ex.submit(_compile_ext)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        ext_obj = ext.result()
     tmp = LIB + ".tmp"
     cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = EXT + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, ext_obj, "-L" + LIBDIR, "-lcpring",
+          "-L" + os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+          "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of cpring_torch.so")
+    os.replace(tmp, EXT)
     return LIB
 
 
