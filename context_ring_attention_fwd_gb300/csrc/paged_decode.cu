@@ -45,6 +45,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "paged_decode.h"
@@ -61,6 +62,7 @@ constexpr int kRows = 16;                        // rows of an item
 constexpr int kCtasPerSm = 3;
 constexpr int kMaxGrid = 480;                    // bounds the slots of the workspace
 constexpr int kMaxBatch = 4096;
+constexpr unsigned kManyRows = 1024;             // joined by a warp each, fewer by four
 constexpr int kMaxQueries = 16;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -588,14 +590,51 @@ struct Parts {
   }
 };
 
-template <int D, bool kE4M3>
+// A lane's kCols columns of a cached row.
+template <int kCols, bool kE4M3>
+__device__ __forceinline__ void load_columns(const uint8_t* row, int lane, float (&v)[kCols]) {
+  if (kE4M3) {
+    uint32_t u;
+    if (kCols == 4)
+      u = __ldg(reinterpret_cast<const unsigned*>(row) + lane);
+    else
+      u = __ldg(reinterpret_cast<const unsigned short*>(row) + lane);
+#pragma unroll
+    for (int x = 0; x < kCols; x += 2) {
+      const uint32_t h = half2_of_codes((u >> (8 * x)) & 0xffffu);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      v[x] = f.x;
+      v[x + 1] = f.y;
+    }
+  } else {
+    uint32_t u[2];
+    if (kCols == 4) {
+      const uint2 t = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+      u[0] = t.x, u[1] = t.y;
+    } else {
+      u[0] = __ldg(reinterpret_cast<const unsigned*>(row) + lane);
+    }
+#pragma unroll
+    for (int x = 0; x < kCols; x += 2) {
+      v[x] = __uint_as_float(u[x / 2] << 16);
+      v[x + 1] = __uint_as_float(u[x / 2] & 0xffff0000u);
+    }
+  }
+}
+
+// kRowWarps warps join a row: four where rows are few (their parts' loads run side
+// by side), one where there are enough rows to fill the GPU.
+template <int D, bool kE4M3, int kRowWarps>
 __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParams p, unsigned grid) {
   constexpr int kCols = D / 32;  // columns per lane
   __shared__ float part_m[kWarps], part_l[kWarps];
-  __shared__ float part_o[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float part_o[kRowWarps > 1 ? kWarps : 1][D];
+  const int lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) % kRowWarps;  // of the row's
   cudaGridDependencySynchronize();
-  const int rid = static_cast<int>(blockIdx.x);  // (b, i, h), below 2^24
+  const int rid = static_cast<int>(blockIdx.x) * (kWarps / kRowWarps) +
+                  static_cast<int>(threadIdx.x >> 5) / kRowWarps;  // (b, i, h), below 2^24
+  if (rid >= p.B * p.n_q * p.Hq) return;  // whole warps, and only with one to a row
   const int bi = rid / p.Hq, h = rid - bi * p.Hq;
   const int b = bi / p.n_q, i = bi - b * p.n_q;
   const int hk = h / p.G;
@@ -606,9 +645,10 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
   const long long lse_at = (static_cast<long long>(b) * p.Hq + h) * p.n_q + i;
   __nv_bfloat16* const out = p.out + static_cast<long long>(rid) * D;
   if (len == 0 || common < 0) {
+    if (warp != 0) return;
     const float v = len == 0 ? 0.f : NAN;
-    for (int x = threadIdx.x; x < D; x += kThreads) out[x] = __float2bfloat16_rn(v);
-    if (threadIdx.x == 0) {
+    for (int x = lane; x < D; x += 32) out[x] = __float2bfloat16_rn(v);
+    if (lane == 0) {
       p.lse[lse_at] = len == 0 ? -INFINITY : NAN;
       if (common < 0) atomicOr(p.err, kErrCache);
     }
@@ -642,20 +682,40 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
     if (pre.count == 1)
       pre = Parts{p.whole_o + whole_pre * D, p.whole_ml + whole_pre * 2, 0, 1, 0, 0};
   }
-  // ---- the parts, dealt to the warps: kBatch of a warp's are loaded before the
-  // first is used
-  constexpr int kBatch = 6;
-  const int n_own = static_cast<int>(own.count), n_parts = n_own + static_cast<int>(pre.count);
+  // ---- the parts, dealt to the warps, kBatch of a warp's loaded before the first
+  // is used; behind them the keys that this query sees beyond the common ones,
+  // each a part with m = its score, l = 1, O = its value
+  constexpr int kBatch = 6, kKeys = 4;
   float m = -INFINITY, l = 0.f;
   float o[kCols];
 #pragma unroll
   for (int x = 0; x < kCols; ++x) o[x] = 0.f;
-  for (int x0 = warp; x0 < n_parts; x0 += kWarps * kBatch) {
+  auto fold = [&](const auto& ml, const auto& v, auto count) {
+    constexpr int kN = decltype(count)::value;
+    float big = m;
+#pragma unroll
+    for (int k = 0; k < kN; ++k) big = fmaxf(big, ml[k].x);
+    const float a = m == -INFINITY ? 0.f : ptx::ex2(m - big);
+    l = m == -INFINITY ? l : l * a;  // an empty state's l is 0, or NaN
+#pragma unroll
+    for (int y = 0; y < kCols; ++y) o[y] *= a;
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const bool empty = ml[k].x == -INFINITY;
+      const float f = empty ? 0.f : ptx::ex2(ml[k].x - big);
+      l += empty ? ml[k].y : ml[k].y * f;
+#pragma unroll
+      for (int y = 0; y < kCols; ++y) o[y] = fmaf(v[k][y], f, o[y]);
+    }
+    m = big;
+  };
+  const int n_own = static_cast<int>(own.count), n_parts = n_own + static_cast<int>(pre.count);
+  for (int x0 = warp; x0 < n_parts; x0 += kRowWarps * kBatch) {
     float2 ml[kBatch];
     float v[kBatch][kCols];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int x = x0 + k * kWarps;
+      const int x = x0 + k * kRowWarps;
       ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int y = 0; y < kCols; ++y) v[k][y] = 0.f;
@@ -673,87 +733,88 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
         }
       }
     }
-    float big = m;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) big = fmaxf(big, ml[k].x);
-    const float a = m == -INFINITY ? 0.f : ptx::ex2(m - big);
-    l = m == -INFINITY ? l : l * a;  // an empty state's l is 0, or NaN
-#pragma unroll
-    for (int y = 0; y < kCols; ++y) o[y] *= a;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const bool empty = ml[k].x == -INFINITY;
-      const float f = empty ? 0.f : ptx::ex2(ml[k].x - big);
-      l += empty ? ml[k].y : ml[k].y * f;
-#pragma unroll
-      for (int y = 0; y < kCols; ++y) o[y] = fmaf(v[k][y], f, o[y]);
-    }
-    m = big;
+    fold(ml, v, std::integral_constant<int, kBatch>());
   }
-  auto add = [&](float mx, float lx, const float (&ox)[kCols]) {
-    const float big = fmaxf(m, mx);
-    const float a = m == -INFINITY ? 0.f : ptx::ex2(m - big);
-    const float c = mx == -INFINITY ? 0.f : ptx::ex2(mx - big);
-    l = (m == -INFINITY ? l : l * a) + (mx == -INFINITY ? lx : lx * c);
-#pragma unroll
-    for (int x = 0; x < kCols; ++x) o[x] = o[x] * a + ox[x] * c;
-    m = big;
-  };
-  // the keys behind the common ones that this query sees, one per warp at a time
   const int pos0 = max(len - p.n_q + 1, p.P);
   const int pos1 = len - p.n_q + i;
   bool bad = false;
   if (pos0 <= pos1) {
     float q[kCols];
-    const __nv_bfloat16* const src = p.q + b * p.qb + i * p.qs + h * p.qh + lane * kCols;
+    load_columns<kCols, false>(
+        reinterpret_cast<const uint8_t*>(p.q + b * p.qb + i * p.qs + h * p.qh), lane, q);
+    const float kd = kE4M3 ? __ldg(p.descale[0] + hk) * p.scale : p.scale;
+    const float vd = kE4M3 ? __ldg(p.descale[1] + hk) : 1.f;
+    for (int first = pos0 + warp; first <= pos1; first += kRowWarps * kKeys) {
+      int page[kKeys], slot[kKeys];
 #pragma unroll
-    for (int x = 0; x < kCols; ++x) q[x] = __bfloat162float(src[x]);
-    for (int pos = pos0 + warp; pos <= pos1; pos += kWarps) {
-      const int at = pos / p.page_size;
-      const int page = __ldg(p.table + b * p.table_stride + at);
-      if (page < 0 || page >= p.n_pages) {
-        bad = true;
-        continue;
-      }
-      float kv[2][kCols];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint8_t* const row = p.cache[x] + page * p.cs[x][0] +
-                                   (pos - at * p.page_size) * p.cs[x][1] + hk * p.cs[x][2];
-#pragma unroll
-        for (int y = 0; y < kCols; ++y) {
-          if (kE4M3) {
-            const uint32_t hh = half2_of_codes(row[lane * kCols + y]);
-            kv[x][y] = __half2float(__ushort_as_half(static_cast<unsigned short>(hh & 0xffffu))) *
-                       __ldg(p.descale[x] + hk);
-          } else {
-            kv[x][y] = __bfloat162float(
-                reinterpret_cast<const __nv_bfloat16*>(row)[lane * kCols + y]);
+      for (int k = 0; k < kKeys; ++k) {
+        const int pos = first + k * kRowWarps;
+        page[k] = -1;
+        slot[k] = 0;
+        if (pos <= pos1) {
+          const int at = pos / p.page_size;
+          slot[k] = pos - at * p.page_size;
+          page[k] = __ldg(p.table + b * p.table_stride + at);
+          if (page[k] < 0 || page[k] >= p.n_pages) {
+            page[k] = -1;
+            bad = true;
           }
         }
       }
-      float dot = 0.f;
+      float key[kKeys][kCols], value[kKeys][kCols];
 #pragma unroll
-      for (int y = 0; y < kCols; ++y) dot = fmaf(q[y], kv[0][y], dot);
+      for (int k = 0; k < kKeys; ++k) {
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-      add(dot * p.scale, 1.f, kv[1]);
+        for (int y = 0; y < kCols; ++y) key[k][y] = value[k][y] = 0.f;
+        if (page[k] >= 0) {
+          load_columns<kCols, kE4M3>(p.cache[0] + page[k] * p.cs[0][0] + slot[k] * p.cs[0][1] +
+                                         hk * p.cs[0][2], lane, key[k]);
+          load_columns<kCols, kE4M3>(p.cache[1] + page[k] * p.cs[1][0] + slot[k] * p.cs[1][1] +
+                                         hk * p.cs[1][2], lane, value[k]);
+        }
+      }
+      float2 ml[kKeys];
+#pragma unroll
+      for (int k = 0; k < kKeys; ++k) {
+        float dot = 0.f;
+#pragma unroll
+        for (int y = 0; y < kCols; ++y) dot = fmaf(q[y], key[k][y], dot);
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+        ml[k] = page[k] >= 0 ? make_float2(dot * kd, 1.f) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int y = 0; y < kCols; ++y) value[k][y] *= vd;
+      }
+      fold(ml, value, std::integral_constant<int, kKeys>());
     }
+  }
+  if (bad) {
+    l = NAN;
+    if (lane == 0) atomicOr(p.err, kErrCache);
+  }
+  if (kRowWarps == 1) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (kCols == 4)
+      reinterpret_cast<uint2*>(out)[lane] = make_uint2(
+          ptx::pack_bf16(o[0] * inv, o[1] * inv), ptx::pack_bf16(o[kCols - 2] * inv, o[kCols - 1] * inv));
+    else
+      reinterpret_cast<uint32_t*>(out)[lane] = ptx::pack_bf16(o[0] * inv, o[1] * inv);
+    if (lane == 0) p.lse[lse_at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    return;
   }
   if (lane == 0) {
     part_m[warp] = m;
-    part_l[warp] = bad ? NAN : l;
-    if (bad) atomicOr(p.err, kErrCache);
+    part_l[warp] = l;
   }
 #pragma unroll
-  for (int x = 0; x < kCols; ++x) part_o[warp][lane * kCols + x] = o[x];
+  for (int x = 0; x < kCols; ++x) part_o[kRowWarps > 1 ? warp : 0][lane * kCols + x] = o[x];
   __syncthreads();
   float big = -INFINITY;
 #pragma unroll
-  for (int y = 0; y < kWarps; ++y) big = fmaxf(big, part_m[y]);
-  float total = 0.f, f[kWarps];
+  for (int y = 0; y < kRowWarps; ++y) big = fmaxf(big, part_m[y]);
+  float total = 0.f, f[kRowWarps];
 #pragma unroll
-  for (int y = 0; y < kWarps; ++y) {
+  for (int y = 0; y < kRowWarps; ++y) {
     f[y] = part_m[y] == -INFINITY ? 0.f : ptx::ex2(part_m[y] - big);
     total += part_m[y] == -INFINITY ? part_l[y] : part_l[y] * f[y];
   }
@@ -761,7 +822,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
   for (int x = threadIdx.x; x < D; x += kThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int y = 0; y < kWarps; ++y) v += part_o[y][x] * f[y];
+    for (int y = 0; y < kRowWarps; ++y) v += part_o[kRowWarps > 1 ? y : 0][x] * f[y];
     out[x] = __float2bfloat16_rn(v * inv);
   }
   if (threadIdx.x == 0) p.lse[lse_at] = total == 0.f ? -INFINITY : (big + log2f(total)) * kLn2;
@@ -814,12 +875,15 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.n_q * p.Hq);
+  const unsigned rows = static_cast<unsigned>(p.B) * p.n_q * p.Hq;
+  const bool many = rows >= kManyRows;
+  cfg.gridDim = dim3(many ? (rows + kWarps - 1) / kWarps : rows);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, decode_join_kernel<D, kE4M3>, p, grid);
+  e = many ? cudaLaunchKernelEx(&cfg, decode_join_kernel<D, kE4M3, 1>, p, grid)
+           : cudaLaunchKernelEx(&cfg, decode_join_kernel<D, kE4M3, kWarps>, p, grid);
   count_launch(2);
   return e;
 }
