@@ -709,62 +709,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t * 128 >= s.rows) { w_seg = w; continue; }
       float sc = p.scale;
       if (ok) {
-        const int r = t * 128 + row_in_tile;    // of the item
-        const bool valid = r < s.rows;
-        const RowOf row(p, 0, s.hk, s.row0 + min(r, s.rows - 1));
-        // ---- this row of Q into its place of the swizzled tile (every MMA on the
-        // previous segment's has finished: its last S or P V was waited for)
-        const uint4* const src = reinterpret_cast<const uint4*>(row.query(p));
-        uint4 v[D / 8];
+        // ---- this warp's 32 rows of Q into the swizzled tile (every MMA on the
+        // previous segment's has finished: its last P V was waited for).  D / 8
+        // lanes read a row, kPer rows a step; all steps' loads are under way
+        // before the first is used.
+        constexpr int kRowLanes = D / 8, kPer = 32 / kRowLanes, kSteps = kRowLanes;
+        const int c = lane % kRowLanes, sub = lane / kRowLanes;
+        uint4 v[kSteps];
+        {
+          const int r = t * 128 + row_in_tile;  // this lane's own row of the item
+          const RowOf row(p, 0, s.hk, s.row0 + min(r, s.rows - 1));
+          const unsigned long long mine = reinterpret_cast<unsigned long long>(row.query(p));
+          const unsigned there = __ballot_sync(0xffffffffu, r < s.rows);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) v[i] = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        float up = 1.f;
-        if (kE4M3) {
-          float top = 0.f, down;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[e] << 16)),
-                                     fabsf(__uint_as_float(u[e] & 0xffff0000u))));
-          }
-          fp16_row_scale(top, up, down);
-          sc = p.scale * __ldg(p.descale[0] + s.hk) * down;
-          if (L::kCodesK) {  // to [2^7, 2^8): the pair saturates at 448
-            up *= 0x1p-7f;
-            sc *= 0x1p+7f;
-            if (!(top < INFINITY)) sc = NAN;  // nor has it an infinity
+          for (int x = 0; x < kSteps; ++x) {
+            const int at = x * kPer + sub;
+            const uint4* const src = reinterpret_cast<const uint4*>(
+                __shfl_sync(0xffffffffu, mine, at));
+            v[x] = (there >> at & 1u) ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        if (L::kCodesK) {
+        const float desc = kE4M3 ? __ldg(p.descale[0] + s.hk) : 1.f;
+        // Four steps a turn, the later ones moved down behind them: unrolled whole,
+        // fetching this code took longer than running it.
+#pragma unroll 1
+        for (int x0 = 0; x0 < kSteps; x0 += 4) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint4& x = v[2 * i + (e >> 1)];
-              split4((e & 1) ? x.z : x.x, (e & 1) ? x.w : x.y, up, hi[e], lo[e]);
-            }
-            const uint32_t at = sbase + L::kQ + t * L::kTile + row_in_tile * 128 +
-                                ((i ^ (row_in_tile & 7)) << 4);
-            ptx::st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-            ptx::st_shared_v4(at + L::kPanel, lo[0], lo[1], lo[2], lo[3]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          for (int x = 0; x < 4; ++x) {
+            const int row = (warp & 3) * 32 + (x0 + x) * kPer + sub;  // of the tile
+            uint32_t u[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+            float up = 1.f;
             if (kE4M3) {
+              // magnitudes order like their bits, two to a comparison
+              uint32_t big = 0;
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                u[e] = pack_f16(__uint_as_float(u[e] << 16) * up,
-                                __uint_as_float(u[e] & 0xffff0000u) * up);
+                asm("max.u16x2 %0, %0, %1;" : "+r"(big) : "r"(u[e] & 0x7fff7fffu));
+#pragma unroll
+              for (int o = 1; o < kRowLanes; o <<= 1)
+                asm("max.u16x2 %0, %0, %1;"
+                    : "+r"(big)
+                    : "r"(__shfl_xor_sync(0xffffffffu, big, o)));
+              const float top = __uint_as_float(max(big << 16, big & 0xffff0000u));
+              float down;
+              fp16_row_scale(top, up, down);
+              if (L::kCodesK) {  // to [2^7, 2^8): the pair saturates at 448
+                up *= 0x1p-7f;
+                down *= 0x1p+7f;
+                if (!(top < INFINITY)) down = NAN;  // nor has it an infinity
+              }
+              // the row's own thread keeps what undoes its scale
+              const float its = __shfl_sync(0xffffffffu, down, (lane % kPer) * kRowLanes);
+              if (lane / kPer == x0 + x) sc = p.scale * desc * its;
             }
-            ptx::st_shared_v4(sbase + L::kQ + t * L::kTile + (i >> 3) * L::kPanel +
-                                  row_in_tile * 128 + (((i & 7) ^ (row_in_tile & 7)) << 4),
-                              u[0], u[1], u[2], u[3]);
+            const uint32_t line = sbase + L::kQ + t * L::kTile + row * 128;
+            if (L::kCodesK) {
+              uint32_t hi[2], lo[2];
+              split4(u[0], u[1], up, hi[0], lo[0]);
+              split4(u[2], u[3], up, hi[1], lo[1]);
+              const uint32_t at = line + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8;
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1])
+                           : "memory");
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + L::kPanel), "r"(lo[0]),
+                           "r"(lo[1])
+                           : "memory");
+            } else {
+              if (kE4M3) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  u[e] = pack_f16(__uint_as_float(u[e] << 16) * up,
+                                  __uint_as_float(u[e] & 0xffff0000u) * up);
+              }
+              ptx::st_shared_v4(line + (c >> 3) * L::kPanel + (((c & 7) ^ (row & 7)) << 4), u[0],
+                                u[1], u[2], u[3]);
+            }
           }
+#pragma unroll
+          for (int x = 0; x + 4 < kSteps; ++x) v[x] = v[x + 4];
         }
         ptx::fence_proxy_async_shared();
         ptx::mbar_arrive(bar(kQFull + t));
