@@ -86,9 +86,8 @@ struct Lay {
 enum Bar : int {
   kQFull = 0,     // + row tile
   kKFull = 2,     // + stage (4)
-  kKEmpty = 6,    // + stage (4)
+  kDone = 6,      // + parity of the tile: its S and the P V before it done
   kVFull = 10,    // + stage
-  kVEmpty = 12,
   kSFull = 14,    // + row tile
   kPReady = 16,   // + row tile: keys 0-63 of P stored
   kPReadyB = 18,  // + row tile: keys 64-127
@@ -282,12 +281,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int t = 0; t < L::kKStages; ++t) {
       ptx::mbar_init(bar(kKFull + t), kTma ? 1 : 32 * kLoadWarps);
-      ptx::mbar_init(bar(kKEmpty + t), 1);
     }
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(bar(kQFull + t), 128);
       ptx::mbar_init(bar(kVFull + t), !kTma ? 32 * kLoadWarps : kE4M3 ? 64 : 1);
-      ptx::mbar_init(bar(kVEmpty + t), 1);
+      ptx::mbar_init(bar(kDone + t), 1);
       ptx::mbar_init(bar(kCFull + t), 1);
       ptx::mbar_init(bar(kCEmpty + t), 64);
       ptx::mbar_init(bar(kSFull + t), 1);
@@ -319,6 +317,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool drop = p.fault_drop_k && blockIdx.x == holder(kItemCost, W, gridDim.x);
   Segment s;
 
+  // The CTA's tile n is done (two barriers in turn: the next tile of the same
+  // parity needs what waits for this one).
+  auto tile_done = [&](uint32_t n) {
+    return wait_warp(bar(kDone + (n & 1u)), (n >> 1) & 1u, abort_flag, p);
+  };
   if (warp >= kMmaWarp) ptx::setmaxnreg_dec<kControlRegs>();  // the whole third warpgroup
   if (kTma && warp == kLoadWarp0) {
     // ------------------------------------------------------------ K and V by TMA
@@ -360,18 +363,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && segment_at(p, w, w_end, s)) {
       look_up(s.t0, s.t1);
       for (int f = s.t0; f < s.t1; ++f, ++n) {
-        const uint32_t ks = n % L::kKStages, ku = n / L::kKStages;
-        const uint32_t vs = n & 1u, vu = n >> 1;
-        if (ku > 0 && !wait_warp(bar(kKEmpty + ks), (ku - 1) & 1u, abort_flag, p)) {
-          ok = false;
-          break;
-        }
+        // K of tile n may be overwritten once tile n - kKStages is done, V once
+        // tile n - 1 is (its P V comes one tile later): the wait for V of the
+        // tile before has covered K's (for codes, the wait for their buffer: the
+        // widening warps had waited for tile n - 4).
+        const uint32_t ks = n % L::kKStages;
+        const uint32_t vs = n & 1u;
         if (!(drop && n == 0)) {
           bring(&map_k, s.hk, sbase + L::kK + ks * L::kKTile, bar(kKFull + ks));
           nk = n + 1;
         }
-        const uint32_t v_empty = bar((kE4M3 ? kCEmpty : kVEmpty) + vs);
-        if (vu > 0 && !wait_warp(v_empty, (vu - 1) & 1u, abort_flag, p)) {
+        if (kE4M3 ? n >= 2 && !wait_warp(bar(kCEmpty + vs), ((n >> 1) - 1) & 1u, abort_flag, p)
+                  : n >= 1 && !tile_done(n - 1)) {
           ok = false;
           break;
         }
@@ -424,9 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 0;
       while (ok && segment_at(p, w, w_end, s)) {
         for (int f = s.t0; f < s.t1; ++f, ++n) {
-          const uint32_t vs = n & 1u, vu = n >> 1;
-          if (!wait_warp(bar(kCFull + vs), vu & 1u, abort_flag, p) ||
-              (vu > 0 && !wait_warp(bar(kVEmpty + vs), (vu - 1) & 1u, abort_flag, p))) {
+          const uint32_t vs = n & 1u;
+          if (!wait_warp(bar(kCFull + vs), (n >> 1) & 1u, abort_flag, p) ||
+              (n >= 1 && !tile_done(n - 1))) {
             ok = false;
             break;
           }
@@ -509,9 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     // Step n copies K (n even) or V (n odd) of the CTA's tile n / 2, into stage
-    // (n / 2) % 2; its use of that buffer is number n / 4.
+    // (n / 2) % 2, which V finds free once tile n / 2 - 1 is done and K then has been.
     auto full = [&](unsigned n) { return bar((n & 1 ? kVFull : kKFull) + ((n >> 1) & 1)); };
-    auto empty = [&](unsigned n) { return bar((n & 1 ? kVEmpty : kKEmpty) + ((n >> 1) & 1)); };
     auto buffer = [&](unsigned n) {
       return sbase + (n & 1 ? L::kV : L::kK) + ((n >> 1) & 1) * L::kTile;
     };
@@ -526,12 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int f = s.t0; ok && f < s.t1; ++f) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (n >= 4 &&
-                !__all_sync(0xffffffffu, ptx::mbar_try_wait(empty(n), ((n >> 2) - 1) & 1u))) {
+            const unsigned tile = n >> 1;
+            if (x == 1 && tile >= 1 &&
+                !__all_sync(0xffffffffu, ptx::mbar_try_wait(bar(kDone + ((tile - 1) & 1)),
+                                                            ((tile - 1) >> 1) & 1u))) {
               // The buffer is still in use: announce what is under way first.
               cp_wait<0>();
               for (; told < n; ++told) announce(told);
-              if (!wait_warp(empty(n), ((n >> 2) - 1) & 1u, abort_flag, p)) {
+              if (!tile_done(tile - 1)) {
                 ok = false;
                 break;
               }
@@ -586,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int f = s.t0; ok && f < s.t1; ++f) {
 #pragma unroll
           for (int x = 0; x < 2; ++x, ++n) {
-            if (n >= 4 && !wait_warp(empty(n), ((n >> 2) - 1) & 1u, abort_flag, p)) {
+            if (x == 1 && n >= 2 && !tile_done((n >> 1) - 1)) {
               ok = false;
               break;
             }
@@ -646,13 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (two && !wait_warp(bar(kQFull + 1), segs1++ & 1u, abort_flag, p)) { ok = false; break; }
       ptx::tc_fence_after();
       uint32_t prev_st = 0, prev_ph = 0;
-      bool v_ready = false;
       // O_t (+)= P_t V of the previous key tile, each half once its P is there.
       auto flush = [&](int t, bool first, bool last) -> bool {
-        if (!v_ready) {
-          if (!wait_warp(bar(kVFull + prev_st), prev_ph, abort_flag, p)) return false;
-          v_ready = true;
-        }
+        if (t == 0 && !wait_warp(bar(kVFull + prev_st), prev_ph, abort_flag, p)) return false;
         const uint64_t dv = d_v + ((L::kV + prev_st * L::kTile) >> 4);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -680,17 +680,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (f > s.t0 && !flush(1, f == s.t0 + 1, false)) { ok = false; break; }
           issue_s(1, kst);
         }
-        ptx::mma_commit_w(bar(kKEmpty + kst));
-        if (f > s.t0) ptx::mma_commit_w(bar(kVEmpty + prev_st));
+        ptx::mma_commit_w(bar(kDone + st));
         prev_st = st;
         prev_ph = ph;
-        v_ready = false;
         ++it;
       }
       if (!ok) break;
       const bool only = s.t1 == s.t0 + 1;
       if (!flush(0, only, true) || (two && !flush(1, only, true))) { ok = false; break; }
-      ptx::mma_commit_w(bar(kVEmpty + prev_st));
     }
     ptx::mma_commit_w(bar(kDrain));
     wait_warp(bar(kDrain), 0u, abort_flag, p, false);
