@@ -30,7 +30,7 @@ from ._binding import (  # noqa: F401
     cp_ulysses_attn_fwd,
     cp_ulysses_workspace_bytes,
     cp_ring_traffic, cp_status_string, doc_offsets_tensor, launch_counts, lib, native,
-    test_set_wait_fault)
+    test_set_prefix_path, test_set_wait_fault)
 
 __all__ = [
     "cp_ring_attn_fwd", "cp_ring_attn_fwd_f32", "cp_ring_step", "cp_lse_merge",

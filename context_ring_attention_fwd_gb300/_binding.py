@@ -73,6 +73,7 @@ _SIGS = {
     "cp_paged_append": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f, _vp, _i, _i,
                         _vp, _i, _i, _i, _vp],
     "cp_paged_attn_decode_workspace_bytes": [_i, _i, _i, _i, _i, _i],
+    "cp_test_set_prefix_path": [_i],
     "cp_paged_attn_decode": [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _i64, _vp],
 }
 
@@ -110,7 +111,8 @@ def lib() -> ctypes.CDLL:
                 fn.argtypes = argtypes
                 if name == "cp_status_string":
                     fn.restype = ctypes.c_char_p
-                elif name in ("cp_launch_counts", "cp_test_set_wait_fault"):
+                elif name in ("cp_launch_counts", "cp_test_set_wait_fault",
+                              "cp_test_set_prefix_path"):
                     fn.restype = None
                 elif name in ("cp_ring_emulated_workspace_bytes", "cp_ulysses_workspace_bytes",
                               "cp_ring_attn_bwd_workspace_bytes",
@@ -519,6 +521,12 @@ def test_set_wait_fault(drop_first_k_tile: bool, wait_limit_ns: int = 0) -> None
     """Test hook: make CTA 0 of later tensor-core launches skip its first K
     tile so that a bounded device wait runs out (see include/cpring.h)."""
     lib().cp_test_set_wait_fault(int(bool(drop_first_k_tile)), int(wait_limit_ns))
+
+
+def test_set_prefix_path(path: int = -1) -> None:
+    """Test hook: the kernel that attends a shared prefix (0: 16-row items, 1:
+    tcgen05, -1: by the sizes; see include/cpring.h)."""
+    lib().cp_test_set_prefix_path(int(path))
 
 
 def launch_counts():

@@ -43,6 +43,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -830,8 +831,25 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
 
 long long align256(long long n) { return (n + 255) / 256 * 256; }
 
-// Whether the prefix's rows per key head go to prefix_attn_kernel.
-bool wide_prefix(long long rows, int prefix_len) { return prefix_len > 0 && rows > 32; }
+// Test hook (cp_test_set_prefix_path): -1 the rule below, 0 or 1 its answer.
+std::atomic<int> g_prefix_path{-1};
+
+// Whether the prefix goes to prefix_attn_kernel.  The 16-row items of
+// paged_decode_kernel read the prefix's keys and values once per 16 rows of the
+// batch, from L2 but for the first time; prefix_attn_kernel reads them once per
+// 256 and takes about 10 us longer to start and to join.  They meet where the
+// former reads about 120 MB.  Measured (us, 16-row items / prefix_attn_kernel, 8 key
+// heads, 64 more keys a sequence): bf16, d = 128, 32K prefix: 46 / 50 at 16 rows, 56 / 50
+// at 32, 124 / 58 at 128; 8K: 30 / 30 at 48, 46 / 38 at 128; 2K: 28 / 32 at 128; E4M3,
+// 32K: 44 / 48 at 32, 65 / 48 at 64; bf16, d = 64, 32K: 36 / 40 at 32, 77 / 48 at 128.
+bool wide_prefix(long long rows, int prefix_len, int Hk, int d, int elem_bytes) {
+  if (prefix_len <= 0) return false;
+  const int forced = g_prefix_path.load(std::memory_order_relaxed);
+  if (forced >= 0) return forced != 0;
+  const double read = static_cast<double>((rows + kRows - 1) / kRows) * prefix_len * Hk * 2.0 *
+                      d * elem_bytes;
+  return rows > kRows && read > 120e6;
+}
 
 // Byte offsets of the workspace's parts.
 struct Space {
@@ -840,8 +858,8 @@ struct Space {
     const long long rows = static_cast<long long>(B) * n_q * Hq;
     const long long slots = 2LL * kMaxGrid * kRows;
     const long long whole = prefix_len > 0 ? 2 * rows : n_q > 1 ? rows : 0;
-    const long long pslots =
-        wide_prefix(rows / Hk, prefix_len) ? 2LL * kMaxPrefixGrid * kPrefixRows : 0;
+    const long long pslots =  // for bf16, which takes prefix_attn_kernel no later than E4M3
+        wide_prefix(rows / Hk, prefix_len, Hk, d, 2) ? 2LL * kMaxPrefixGrid * kPrefixRows : 0;
     starts = 0;
     slot_o = align256(4LL * (B + 1));
     slot_ml = slot_o + align256(slots * d * 4);
@@ -899,6 +917,10 @@ bool sizes_ok(int B, int n_q, int Hq, int Hk, int prefix_len) {
 
 extern "C" {
 
+void cp_test_set_prefix_path(int path) {
+  cpring::g_prefix_path.store(path < 0 ? -1 : path != 0, std::memory_order_relaxed);
+}
+
 int64_t cp_paged_attn_decode_workspace_bytes(int B, int n_q, int Hq, int Hk, int d,
                                              int prefix_len) {
   if (!cpring::sizes_ok(B, n_q, Hq, Hk, prefix_len) || (d != 64 && d != 128)) return -1;
@@ -927,7 +949,7 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
     return CP_ERR_BUFFER;
   // the units of a call are counted in 32 bits
   const long long G = Hq / Hk, R = G * n_q;
-  const bool wide = wide_prefix(B * R, prefix_len);
+  const bool wide = wide_prefix(B * R, prefix_len, Hk, d, cache->elem_bytes);
   const int prefix_rows = wide ? kPrefixRows : kRows, prefix_keys = wide ? kPrefixKeys : kTileKeys;
   const long long own_rt = (R + kRows - 1) / kRows;
   const long long prefix_rt = (B * R + prefix_rows - 1) / prefix_rows;

@@ -611,6 +611,14 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
                                int B, int n_q, int Hq, void* workspace, int64_t workspace_bytes,
                                cudaStream_t stream);
 
+/*
+ * TEST HOOK.  Later cp_paged_attn_decode calls (and their workspace sizes)
+ * attend the prefix with the 16-row items of the decode kernel (path 0) or with
+ * the tcgen05 kernel (path 1), whatever their sizes; -1 returns to the rule.
+ * Process-wide; for tests only.
+ */
+void cp_test_set_prefix_path(int path);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,5 +1,4 @@
-"""cp_paged_attn_decode where many rows share the prefix, so that its tcgen05
-kernel runs: row counts around its 128- and 256-row tiles, prefixes around its
+"""cp_paged_attn_decode with the prefix on its tcgen05 kernel: row counts around its 128- and 256-row tiles, prefixes around its
 128-key tiles, items cut between CTAs and whole ones, against attention in 64
 bits on the GPU.  Tolerances as derived in test_gpu_paged_decode.py, with the
 largest product of norms in place of the largest sum of magnitudes (Cauchy's
@@ -26,7 +25,9 @@ def _lib():
         _build.build()
     pkg.lib()
     torch.cuda.set_device(0)
+    pkg.test_set_prefix_path(1)
     yield
+    pkg.test_set_prefix_path(-1)
     assert pkg.cp_get_last_status() == 0
 
 
@@ -215,3 +216,24 @@ def test_replayed_in_a_graph_with_other_lengths():
     t.lens[5] = 0
     graph.replay()
     t.check(out, lse)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_both_kernels_give_the_same_attention(e4m3):
+    """The 16-row items and the tcgen05 kernel on one batch, and the rule's own choice on
+    either side of its threshold."""
+    t = Case(48, 1, 8, 4, 128, 16, 3000, 100, e4m3, 12)
+    got = []
+    for path in (0, 1):
+        pkg.test_set_prefix_path(path)
+        got.append(t.run())
+        t.check(*got[-1])
+    pkg.test_set_prefix_path(-1)
+    before = pkg.launch_counts()[0]
+    t.run()                                     # 6 * 3000 keys * 4 heads: 37 or 18 MB
+    assert pkg.launch_counts()[0] == before
+    big = Case(40, 1, 64, 8, 128, 64, 4000, 5, e4m3, 13)
+    out = big.run()                             # 20 * 4000 keys * 8 heads: 328 or 164 MB
+    assert pkg.launch_counts()[0] == before + 1
+    big.check(*out)
+    pkg.test_set_prefix_path(1)
