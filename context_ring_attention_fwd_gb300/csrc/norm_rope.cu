@@ -8,12 +8,14 @@
 // the load and the one rounding at the store is fp32; r is recomputed in the
 // backward, which reads x anyway, so the forward saves nothing for it.
 //
-// Bound by HBM: a forward moves 2 d elements per row, a backward 3 d.  Work
-// units of a warp are kUnroll * (rows per warp) heads of one token: all of a
-// unit's rows are loaded before the first is used (kUnroll x 1 KB in flight
-// per warp; the backward twice that), and one token's angles serve them all.
-// Units of q come first, then those of k, so a warp changes its gain (and, in
-// the backward, hands over its sums for the gain's gradient) once.
+// Bound by HBM: a forward moves 2 d elements per row, a backward 3 d.  A warp's
+// unit of work is kUnroll * (rows per warp) heads of one token; while it works
+// on one, the next one's rows are on their way to its ring in shared memory
+// (kUnroll x 1 KB, the backward twice that, on top of the unit at hand).  A
+// warp takes several units of a token in a row where there are enough, and works
+// out the token's angles once for them.  Units of q come first, then those of k,
+// so a warp changes its gain (and, in the backward, hands over its sums for the
+// gain's gradient) once.
 //
 // The gain's gradient: each lane sums its columns over its rows in registers,
 // the block's warps are added in shared memory, and a second kernel adds the
@@ -43,6 +45,7 @@ struct Rows {        // one of q and k
   const float* w;    // [d] or null: rows are not normed
   int H;
   int chunks;        // units per token
+  int per, groups;   // of which `per` in a row are one warp's; groups of them per token
 };
 
 struct RopeParams {
@@ -51,7 +54,7 @@ struct RopeParams {
   const int32_t* positions;  // [B, S], or null: position = index in the sequence
   float* partial;            // backward: [blocks][2][d]
   int S, rot, interleaved;
-  int units_q, units;
+  int groups_q, groups;  // of q; of both
   float eps;
 };
 
@@ -76,14 +79,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   lane_columns<NP>(l, p.rot, kInterleaved, lo, hi, turned);
 
   struct Unit {
-    int ti, tok, b, s, h0;
+    int ti, tok, b, s;
+    int chunk, end;  // this unit, and the last one but one of the warp's group
   };
-  auto unit_at = [&](unsigned u) {
+  auto group_at = [&](unsigned u) {
     Unit x;
-    x.ti = u >= static_cast<unsigned>(p.units_q);
-    const int local = static_cast<int>(u) - (x.ti ? p.units_q : 0);
-    x.tok = local / p.t[x.ti].chunks;
-    x.h0 = (local - x.tok * p.t[x.ti].chunks) * kUnitRows + g;
+    x.ti = u >= static_cast<unsigned>(p.groups_q);
+    const Rows& t = p.t[x.ti];
+    const int local = static_cast<int>(u) - (x.ti ? p.groups_q : 0);
+    x.tok = local / t.groups;
+    x.chunk = (local - x.tok * t.groups) * t.per;
+    x.end = min(x.chunk + t.per, t.chunks);
     x.b = x.tok / p.S;
     x.s = x.tok - x.b * p.S;
     return x;
@@ -94,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const T* const dy = static_cast<const T*>(t.dy) + static_cast<long long>(x.tok) * t.H * D;
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int h = x.h0 + i * Lay::kRows;
+      const int h = x.chunk * kUnitRows + g + i * Lay::kRows;
       const bool there = h < t.H;
       const T* const src = xrow + (there ? h : 0) * t.xh;
       ring.copy(stage, i * kRowVecs, src + lo, there);
@@ -107,11 +113,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   };
   const unsigned stride = gridDim.x * kWarps;  // unsigned: the last step may pass 2^31
-  const unsigned units = static_cast<unsigned>(p.units);
+  const unsigned groups = static_cast<unsigned>(p.groups);
   unsigned u = blockIdx.x * kWarps + warp;
+  const bool any_q = u < static_cast<unsigned>(p.groups_q);  // the warp has work on q
   Unit next{};
-  if (u < units) {
-    next = unit_at(u);
+  bool more = u < groups;
+  if (more) {
+    next = group_at(u);
     fetch(next, 0);
   }
   copies_commit();
@@ -143,37 +151,46 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
 
   int cur = -1;
-  for (int stage = 0; u < units; u += stride, stage ^= 1) {
+  bool fresh = true;  // a new group: another token, or another tensor
+  // The factors of the token's turn; the forward's carry the gain too:
+  // y[i] = own w[i] x[i] + other w[partner] x[partner], times r.
+  f32x2 own[NP], other[NP], w[NP];
+  for (int stage = 0; more; stage ^= 1) {
     const Unit x = next;
-    if (u + stride < units && u + stride > u) {
-      next = unit_at(u + stride);
-      fetch(next, stage ^ 1);
+    const bool renew = fresh;
+    if (++next.chunk < next.end) {
+      fresh = false;
+    } else {
+      fresh = true;
+      more = u + stride < groups && u + stride > u;
+      u += stride;
+      if (more) next = group_at(u);
     }
+    if (more) fetch(next, stage ^ 1);
     copies_commit();
     const Rows& t = p.t[x.ti];
     const long long flat = static_cast<long long>(x.tok) * t.H * D;  // contiguous [B, S, H, d]
-    if (kBwd && x.ti != cur && cur >= 0) flush(cur);
-    cur = x.ti;
-    // The factors of this token's turn; the forward's carry the gain too:
-    // y[i] = own w[i] x[i] + other w[partner] x[partner], times r.
-    f32x2 own[NP], other[NP], w[NP];
-    load_gain<NP>(gain[x.ti], lo, hi, w);
-    if (p.rot > 0) {
-      float c[NP], sn[NP];
-      row_angles<Lay>(p.positions ? __ldg(p.positions + x.tok) : x.s, frac, l, c, sn);
-      turn_factors<NP, kInterleaved>(c, sn, kBwd ? -1.f : 1.f, own, other);
-      if (!kBwd) {
+    if (renew) {
+      if (kBwd && x.ti != cur && cur >= 0) flush(cur);
+      cur = x.ti;
+      load_gain<NP>(gain[x.ti], lo, hi, w);
+      if (p.rot > 0) {
+        float c[NP], sn[NP];
+        row_angles<Lay>(p.positions ? __ldg(p.positions + x.tok) : x.s, frac, l, c, sn);
+        turn_factors<NP, kInterleaved>(c, sn, kBwd ? -1.f : 1.f, own, other);
+        if (!kBwd) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          own[i] = mul2(own[i], w[i]);
-          other[i] = mul2(other[i], partner<NP, kInterleaved>(w, i));
+          for (int i = 0; i < NP; ++i) {
+            own[i] = mul2(own[i], w[i]);
+            other[i] = mul2(other[i], partner<NP, kInterleaved>(w, i));
+          }
         }
       }
     }
     copies_wait_all_but_last();
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int h = x.h0 + i * Lay::kRows;
+      const int h = x.chunk * kUnitRows + g + i * Lay::kRows;
       if (h - g >= t.H) break;  // the same for the whole warp
       f32x2 z[NP];
       unpack<NP>(ring.read(stage, i * kRowVecs), z, 0, T());
@@ -227,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (kBwd) {
     // A warp writes the slots of tensors that it had no unit of as zeros.
     for (int ti = 0; ti < 2; ++ti)
-      if (ti != cur && !(ti == 0 && cur == 1 && blockIdx.x * kWarps + warp < p.units_q))
+      if (ti != cur && !(ti == 0 && cur == 1 && any_q))
         for (int i = lane; i < D; i += 32) sums[(ti * kWarps + warp) * D + i] = 0.f;
     if (cur >= 0) flush(cur);
     __syncthreads();
@@ -264,11 +281,20 @@ __global__ void __launch_bounds__(1024)
 template <typename T, int D, int kUnroll, bool kBwd, bool kInterleaved>
 cudaError_t launch_rows(RopeParams p, int tokens, float* dqw, float* dkw, cudaStream_t stream) {
   constexpr int kUnitRows = kUnroll * RowLayout<T, D>::kRows;
-  for (Rows& t : p.t) t.chunks = (t.H + kUnitRows - 1) / kUnitRows;
-  p.units_q = tokens * p.t[0].chunks;
-  p.units = p.units_q + tokens * p.t[1].chunks;
-  const int want = (p.units + kWarps - 1) / kWarps;
-  const int blocks = std::min(want, std::min(kMaxBlocks, 2 * sm_count()));
+  // A warp takes a token's units in a row, whose angles it then works out once,
+  // as many as still leave every warp of the grid a few such groups.
+  const int most = 2 * sm_count();
+  for (int per = 8;; per /= 2) {
+    for (Rows& t : p.t) {
+      t.chunks = (t.H + kUnitRows - 1) / kUnitRows;
+      t.per = std::max(1, std::min(per, t.chunks));
+      t.groups = (t.chunks + t.per - 1) / t.per;
+    }
+    p.groups_q = tokens * p.t[0].groups;
+    p.groups = p.groups_q + tokens * p.t[1].groups;
+    if (per == 1 || p.groups >= 4 * most * kWarps) break;
+  }
+  const int blocks = std::min((p.groups + kWarps - 1) / kWarps, std::min(kMaxBlocks, most));
   constexpr int kSmem = kWarps * Ring<kUnroll * (kBwd ? 4 : 2)>::kBytes;
   const auto kern = qk_norm_rope_kernel<T, D, kUnroll, kBwd, kInterleaved>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kSmem);
