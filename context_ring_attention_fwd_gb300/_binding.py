@@ -568,8 +568,8 @@ def cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens,
                     k_weight, inv_freq, q_out, eps: float = 1e-6, interleaved: bool = False,
                     k_descale=None, v_descale=None, stream=None):
     """Norm, rotate and append k, v [B,S,Hk,d] bf16 (strided views allowed) to
-    the paged caches [pages, page_size, Hk, d] (bf16, or uint8 E4M3 codes with
-    fp32 [Hk] descales) at positions cache_lens[b] + s (int32 [B]) of the table
+    the paged caches [pages, page_size, Hk, d] (bf16, or float8_e4m3fn or its
+    codes as uint8 with fp32 [Hk] descales) at positions cache_lens[b] + s (int32 [B]) of the table
     int32 [B, max_pages], for s < new_lens[b] (int32 [B], None: all S); q
     [B,S,Hq,d] (None: keys and values only) is normed and rotated into q_out
     (allocated if None), which it returns."""

@@ -307,8 +307,8 @@ cp_status check_cache(const cp_paged_cache* c) {
   if (c->n_pages < 1 || c->page_size < 1 || c->max_pages < 1 || c->Hk < 1 || c->Hk > 65535 ||
       c->table_stride < c->max_pages || c->table_stride > (1LL << 31))
     return CP_ERR_SHAPE;
-  // positions are int32
-  if (static_cast<long long>(c->max_pages) * c->page_size > 0x7fffffffLL) return CP_ERR_SHAPE;
+  // positions, and those up to a tile behind the last, are int32
+  if (static_cast<long long>(c->max_pages) * c->page_size > (1LL << 30)) return CP_ERR_SHAPE;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4) ||
       !aligned(c->k_descale, 4) || !aligned(c->v_descale, 4) ||
       !strides_ok(c->k_strides, c->elem_bytes) || !strides_ok(c->v_strides, c->elem_bytes))

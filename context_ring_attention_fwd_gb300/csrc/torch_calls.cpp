@@ -2,8 +2,8 @@
 // (cp_qk_norm_rope, cp_qk_norm_rope_bwd, cp_paged_append,
 // cp_paged_attn_decode): a Python extension that checks torch tensors, allocates
 // outputs where none are given, and calls the C ABI.  It computes nothing.
-// Measured against the same checks in Python over ctypes, a call's host side
-// falls from 22-36 us to 6-10 us.
+// Against the same checks in Python over ctypes a call's host side fell from
+// 26 to 6 us (norm and rotation), 22 to 4 (append) and 36 to 10 (decode).
 #include <ATen/ATen.h>
 #include <Python.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -286,14 +286,15 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// The cache of caches [pages, page_size, Hk, d] (bf16, or uint8 E4M3 codes with
-// fp32 [Hk] descales) and an int32 table [B, max_pages].
+// The cache of caches [pages, page_size, Hk, d] (bf16, or E4M3 with fp32 [Hk]
+// descales) and an int32 table [B, max_pages].
 cp_paged_cache cache_of(PyObject* ko, PyObject* vo, PyObject* to, PyObject* kdo, PyObject* vdo,
                         int64_t B, int dev) {
   const Tensor& k = rows4(ko, "k_cache");
   const at::ScalarType type = k.scalar_type();
-  const bool e4m3 = type == at::kByte;
-  TORCH_CHECK_TYPE(e4m3 || type == at::kBFloat16, "k_cache must be bf16 or uint8 (E4M3 codes)");
+  const bool e4m3 = type == at::kByte || type == at::kFloat8_e4m3fn;
+  TORCH_CHECK_TYPE(e4m3 || type == at::kBFloat16,
+                   "k_cache must be bf16, or E4M3 (float8_e4m3fn, or its codes as uint8)");
   const Tensor& v = needed(vo, "v_cache");
   const Tensor& table = needed(to, "page_table");
   cp_paged_cache c{};

@@ -530,12 +530,12 @@ typedef struct cp_paged_cache {
   void* v;
   int64_t k_strides[3];     /* elements between pages, tokens of a page, heads (each a */
   int64_t v_strides[3];     /* multiple of 16 bytes; no two entries at one address)    */
-  const float* k_descale;   /* E4M3: device fp32 [Hk], value = code * descale[head];   */
-  const float* v_descale;   /* bf16: not read                                          */
+  const float* k_descale;   /* E4M3: device fp32 [Hk], > 0, value = code *             */
+  const float* v_descale;   /* descale[head]; bf16: not read                           */
   const int32_t* page_table;  /* device, rows of max_pages entries                     */
   int64_t table_stride;     /* entries between its rows, >= max_pages                  */
   int32_t n_pages;          /* pages of k and v                                        */
-  int32_t page_size;        /* >= 1; max_pages * page_size < 2^31                      */
+  int32_t page_size;        /* >= 1; max_pages * page_size <= 2^30                     */
   int32_t max_pages;
   int32_t Hk;               /* 1 .. 65535                                              */
   int32_t d;                /* 64 or 128                                               */
@@ -589,7 +589,9 @@ cp_status cp_paged_append(const cp_paged_cache* cache, const void* q, const int6
  *             prefix_len = 0 (no shared prefix).
  *  out        device, bf16 [B,n_q,Hq,d] contiguous, written.
  *  lse        device, fp32 [B,Hq,n_q], written (natural log).
- *  B          1 .. 4096;  n_q  1 .. 16;  B * n_q * Hq <= 2^24.
+ *  B          1 .. 4096;  n_q  1 .. 16;  B * n_q * Hq <= 2^24; the work at the
+ *             table's full length, B * Hk * ceil(n_q (Hq / Hk) / 16) *
+ *             max_pages * page_size / 64 and the prefix's likewise, below 2^32.
  *  workspace  device, >= cp_paged_attn_decode_workspace_bytes(...) bytes,
  *             256-byte aligned, caller-owned, contents undefined afterwards
  *             (calls that can overlap, two captured graphs' among them, need

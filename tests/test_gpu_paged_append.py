@@ -221,3 +221,17 @@ def test_binding_refusals():
     with pytest.raises(TypeError):                # E4M3 codes need their descales
         pkg.paged_append(q, k, v, kc.view(torch.uint8)[..., :64].contiguous(),
                          vc.view(torch.uint8)[..., :64].contiguous(), table, lens)
+
+
+def test_a_cache_of_float8_tensors_is_that_of_its_codes():
+    q, k, v, (kc, vc), table, lens, (qw, kw), (kd, vd) = setup(2, 3, 4, 2, 64, 8, True, 8)
+    f = freqs(64).to(DEV)
+    k8, v8 = kc.clone().view(torch.float8_e4m3fn), vc.clone().view(torch.float8_e4m3fn)
+    a = pkg.paged_append(q, k, v, kc, vc, table, lens, None, qw, kw, f, k_descale=kd, v_descale=vd)
+    pkg.paged_append(q, k, v, k8, v8, table, lens, None, qw, kw, f, k_descale=kd, v_descale=vd)
+    assert torch.equal(k8.view(torch.uint8), kc) and torch.equal(v8.view(torch.uint8), vc)
+    want = pkg.paged_attn_decode(a, kc, vc, table, lens + 3, k_descale=kd, v_descale=vd)
+    got = pkg.paged_attn_decode(a, k8, v8, table, lens + 3, k_descale=kd, v_descale=vd)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(TypeError):
+        pkg.paged_attn_decode(a, k8, vc, table, lens + 3, k_descale=kd, v_descale=vd)
