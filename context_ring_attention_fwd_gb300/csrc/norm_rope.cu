@@ -8,7 +8,9 @@
 // the load and the one rounding at the store is fp32; r is recomputed in the
 // backward, which reads x anyway, so the forward saves nothing for it.
 //
-// Bound by HBM: a forward moves 2 d elements per row, a backward 3 d.  A warp's
+// Bound by HBM (bf16, d = 128: 2 x 32K tokens x 32 heads backward 244 us, 97 % of the
+// copy rate; 64K x 32 forward 163 us, 97 %; 8K x 64 forward 38.5 us and backward
+// 63.5 us): a forward moves 2 d elements per row, a backward 3 d.  A warp's
 // unit of work is kUnroll * (rows per warp) heads of one token; while it works
 // on one, the next one's rows are on their way to its ring in shared memory
 // (kUnroll x 1 KB, the backward twice that, on top of the unit at hand).  A
@@ -282,7 +284,8 @@ template <typename T, int D, int kUnroll, bool kBwd, bool kInterleaved>
 cudaError_t launch_rows(RopeParams p, int tokens, float* dqw, float* dkw, cudaStream_t stream) {
   constexpr int kUnitRows = kUnroll * RowLayout<T, D>::kRows;
   // A warp takes a token's units in a row, whose angles it then works out once,
-  // as many as still leave every warp of the grid a few such groups.
+  // as many as still leave every warp of the grid a few such groups (backward of
+  // 8192 tokens x 64 heads: 73.2 us one by one, 63.5 so).
   const int most = 2 * sm_count();
   for (int per = 8;; per /= 2) {
     for (Rows& t : p.t) {
@@ -319,8 +322,10 @@ cudaError_t launch_rows(RopeParams p, int tokens, float* dqw, float* dkw, cudaSt
   return e;
 }
 
-// Heads per unit: as many as keep enough bytes in flight per warp, fewer when
-// the call is too small to give every warp of the grid such a unit.
+// Rows per unit: as many as keep enough bytes in flight per warp, one row group
+// when the call is too small to give every warp of the grid more.  Measured, one
+// group / kWide (us in the kernel): forward 16 tokens x 40 heads 4.4 / 6.2, 8192 x 64
+// 45.6 / 39.3; backward 8192 x 64 67.3 / 64.1; fp32 backward 3074 x 16 13.7 / 14.1.
 template <typename T, int D, bool kBwd>
 cudaError_t launch_sized(const RopeParams& p, int tokens, float* dqw, float* dkw,
                          cudaStream_t stream) {

@@ -8,10 +8,13 @@
 // or the E4M3 code of x times the reciprocal of descale[head] (in fp32, as
 // cp_fp8_quantize multiplies by its inverse scale).
 //
-// Bound by HBM for prefill chunks and by launch latency for single tokens.  A
+// Bound by instructions for prefill chunks (3842 tokens of 32 + 8 + 8 heads to E4M3:
+// 24 us, half the copy rate; the issue slots are 40 % used with the 16 warps that the
+// registers allow) and by launch latency for single tokens (64 of them: 5.4 us).  A
 // warp's unit is a few heads of one token of q, k or v; rows are 16-byte
 // vectors of 8 (d = 128) or 4 lanes, so any page size, head order and page
-// stride costs the same.
+// stride costs the same; the next unit's rows are on their way meanwhile
+// (norm_rope.cu).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -278,7 +281,8 @@ cudaError_t launch_append(AppendParams p, int tokens, cudaStream_t stream) {
 }
 
 // Four row groups of a token per unit once that still fills the grid; one
-// otherwise (single tokens: more warps, each with less to wait for).
+// otherwise (single tokens: more warps, each with less to wait for).  Measured, one /
+// four (us in the kernel): 64 tokens of 48 heads 5.4 / 6.9, 3842 tokens 32.8 / 24.2.
 template <int D, bool kE4M3>
 cudaError_t launch_sized(const AppendParams& p, int tokens, cudaStream_t stream) {
   const long long rows = static_cast<long long>(tokens) * (p.t[0].H + 2LL * p.t[1].H);

@@ -30,8 +30,12 @@
 // a cut item leaves its parts in the CTAs' slots (one for a stretch's first
 // item, one for its last).
 //
-// decode_join_kernel, one CTA per row, joins the parts and the later keys of
-// an n_q > 1 call, in a fixed order.
+// Measured (bf16, d = 128, pages of 16): 32 sequences of up to 16K keys, 728 MB, 110 us
+// in the kernel, 98 % of the copy rate; E4M3, 364 MB, 70 us (77 %; the widening of
+// codes leaves each warp waiting for its own instructions).
+//
+// decode_join_kernel joins a row's parts and the later keys of an n_q > 1
+// call, in a fixed order.
 //
 // E4M3 caches: codes are exact in fp16, so both products run as fp16 MMAs.
 // Q is scaled per row by a power of two into fp16's range (exact but for
@@ -63,7 +67,10 @@ constexpr int kRows = 16;                        // rows of an item
 constexpr int kCtasPerSm = 3;
 constexpr int kMaxGrid = 480;                    // bounds the slots of the workspace
 constexpr int kMaxBatch = 4096;
-constexpr unsigned kManyRows = 1024;             // joined by a warp each, fewer by four
+// From this many rows on a warp joins a row, four below.  Measured, one / four (us in
+// the kernel): 32 rows of 11 parts 5.3 / 4.4; 2048 rows of 21 parts 9.5 / 11.1;
+// 4096 rows of 11 parts and up to three later keys 14.3 / 22.1.
+constexpr unsigned kManyRows = 1024;
 constexpr int kMaxQueries = 16;
 constexpr float kLn2 = 0.69314718055994531f;
 
