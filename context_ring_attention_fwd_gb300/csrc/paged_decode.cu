@@ -30,8 +30,8 @@
 // a cut item leaves its parts in the CTAs' slots (one for a stretch's first
 // item, one for its last).
 //
-// Measured (bf16, d = 128, pages of 16): 32 sequences of up to 16K keys, 728 MB, 110 us
-// in the kernel, 98 % of the copy rate; E4M3, 364 MB, 70 us (77 %; the widening of
+// Measured (bf16, d = 128, pages of 16): 32 sequences of up to 16K keys, 728 MB, 113 us
+// in the kernel, 95 % of the copy rate; E4M3, 364 MB, 70 us (77 %; the widening of
 // codes leaves each warp waiting for its own instructions).
 //
 // decode_join_kernel joins a row's parts and the later keys of an n_q > 1

@@ -27,7 +27,7 @@
 //
 // Bound by shared memory and the tensor pipe alike: of a pair of 128 x 128 tiles, the
 // products take 2048 clocks, and the operands that they read (A and B of S, V) and the
-// copies that fill them 2048 clocks at 128 bytes each; a pair takes about 2800.  512 rows
+// copies that fill them 2048 clocks at 128 bytes each; a pair takes about 2900.  512 rows
 // x 8 heads under a 128K prefix: 189 us, 1450 TFLOP/s.
 //
 // E4M3, d = 128, by TMA: K's codes are the operand themselves.  A bf16 q has 8
