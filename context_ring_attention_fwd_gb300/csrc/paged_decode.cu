@@ -684,7 +684,9 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
       pre.ml = p.pslot_ml;
     }
     pre.r = row % p.prefix_rows;
-    pre.find((hk * p.prefix_row_tiles + row / p.prefix_rows) * units, n,
+    const int tile = row / p.prefix_rows;
+    const int item = wide ? prefix_item<kE4M3>(p, hk, tile) : hk * p.prefix_row_tiles + tile;
+    pre.find(item * units, n,
              wide ? units * static_cast<unsigned>(p.Hk * p.prefix_row_tiles) : W,
              wide ? static_cast<unsigned>(p.prefix_grid) : g);
     if (pre.count == 1)

@@ -117,6 +117,7 @@ struct Segment {
   bool whole;
 };
 
+template <bool kE4M3>
 __device__ __forceinline__ bool segment_at(const DecodeParams& p, unsigned& w, unsigned w_end,
                                            Segment& s) {
   const unsigned n = static_cast<unsigned>(p.prefix_tiles) + kItemCost;
@@ -127,8 +128,9 @@ __device__ __forceinline__ bool segment_at(const DecodeParams& p, unsigned& w, u
     const unsigned u1 = min(n, u0 + (w_end - w));
     s.t0 = tile_of_unit(u0);
     s.t1 = tile_of_unit(u1);
-    s.hk = static_cast<int>(item) / p.prefix_row_tiles;
-    s.row0 = (static_cast<int>(item) - s.hk * p.prefix_row_tiles) * kPrefixRows;
+    int t;
+    prefix_item_at<kE4M3>(p, static_cast<int>(item), s.hk, t);
+    s.row0 = t * kPrefixRows;
     w += u1 - u0;
   } while (s.t0 >= s.t1);
   s.rows = min(kPrefixRows, p.B * p.R - s.row0);
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t n = 0, nk = 0, nv = 0, tails = 0;  // tiles; K, V and last tiles under way
     bool ok = true;
-    while (ok && segment_at(p, w, w_end, s)) {
+    while (ok && segment_at<kE4M3>(p, w, w_end, s)) {
       look_up(s.t0, s.t1);
       for (int f = s.t0; f < s.t1; ++f, ++n) {
         // K of tile n may be overwritten once tile n - kKStages is done, V once
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kRowChunks = D / 16;
       bool ok = true;
       uint32_t n = 0;
-      while (ok && segment_at(p, w, w_end, s)) {
+      while (ok && segment_at<kE4M3>(p, w, w_end, s)) {
         for (int f = s.t0; f < s.t1; ++f, ++n) {
           const uint32_t vs = n & 1u;
           if (!wait_warp(bar(kCFull + vs), (n >> 1) & 1u, abort_flag, p) ||
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (!kE4M3) {
       unsigned n = 0, told = 0;  // steps copied, steps announced
-      while (ok && segment_at(p, w, w_end, s)) {
+      while (ok && segment_at<kE4M3>(p, w, w_end, s)) {
         look_up(s.t0, s.t1);
         for (int f = s.t0; ok && f < s.t1; ++f) {
 #pragma unroll
@@ -569,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Segment c{};
       int cf = 0;
       unsigned copied = 0;
-      bool more = segment_at(p, w2, w_end, c);
+      bool more = segment_at<kE4M3>(p, w2, w_end, c);
       if (more) {
         cf = c.t0;
         look_up(cf, c.t1);
@@ -580,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           copy(x, c.hk, sbase + L::kCodes + x * L::kCodeTile);
           ++copied;
           if (x == 1 && ++cf == c.t1) {
-            more = segment_at(p, w2, w_end, c);
+            more = segment_at<kE4M3>(p, w2, w_end, c);
             if (more) {
               cf = c.t0;
               look_up(cf, c.t1);
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       copy_step();
       copy_step();
       unsigned n = 0;
-      while (ok && segment_at(p, w, w_end, s)) {
+      while (ok && segment_at<kE4M3>(p, w, w_end, s)) {
         for (int f = s.t0; ok && f < s.t1; ++f) {
 #pragma unroll
           for (int x = 0; x < 2; ++x, ++n) {
@@ -652,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::mma_commit_w(bar(kSFull + t));
     };
-    while (ok && segment_at(p, w, w_end, s)) {
+    while (ok && segment_at<kE4M3>(p, w, w_end, s)) {
       const bool two = s.rows > 128;
       if (!wait_warp(bar(kQFull), segs0++ & 1u, abort_flag, p)) { ok = false; break; }
       if (two && !wait_warp(bar(kQFull + 1), segs1++ & 1u, abort_flag, p)) { ok = false; break; }
@@ -710,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s_cnt = 0, o_cnt = 0;
     bool ok = true;
     unsigned w_seg = w;
-    while (segment_at(p, w, w_end, s)) {
+    while (segment_at<kE4M3>(p, w, w_end, s)) {
       if (t * 128 >= s.rows) { w_seg = w; continue; }
       float sc = p.scale;
       if (ok) {
@@ -864,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the segment's part: O, its reference and its sum.  Where it goes is
       // worked out again, so that the loop above holds no registers for it.
       asm volatile("" : "+r"(w_seg));
-      segment_at(p, w_seg, w_end, s);
+      segment_at<kE4M3>(p, w_seg, w_end, s);
       const int r = t * 128 + row_in_tile;
       const bool valid = r < s.rows;
       if (ok && !wait_warp(bar(kOFull + t), o_cnt & 1u, abort_flag, p)) ok = false;
