@@ -200,6 +200,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_append_kernel(const AppendP
     copies_commit();
     if (x.page == -2) continue;
     if (x.kind != 0 && x.page < 0) {  // no place in the cache: the token is not written
+      // Its rows are on their way all the same: they land before the stage is filled
+      // again (two copies to one address have no order), or the block ends.
+      copies_wait_all_but_last();
       if (lane == 0) atomicOr(p.err, kErrCache);
       continue;
     }

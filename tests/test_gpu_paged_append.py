@@ -235,3 +235,32 @@ def test_a_cache_of_float8_tensors_is_that_of_its_codes():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     with pytest.raises(TypeError):
         pkg.paged_attn_decode(a, k8, vc, table, lens + 3, k_descale=kd, v_descale=vd)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B,S", [(4096, 1), (40, 100), (40, 700)])
+def test_tokens_left_out_do_not_disturb_the_others(B, S, e4m3):
+    """Thousands of tokens, several units a warp, a third of them on pages outside the cache, in
+    runs and alone: every other slot and every query row is, bit for bit, that of a call whose
+    table is sound."""
+    q, k, v, (kc, vc), table, lens, (qw, kw), (kd, vd) = setup(B, S, 4, 4, 128, 8, e4m3, B, held=30)
+    f = freqs(128).to(DEV)
+    k0, v0, bad = kc.clone(), vc.clone(), table.clone()
+    out = torch.rand(table.shape, generator=torch.Generator().manual_seed(S)) < 1 / 3
+    out[::7] = True                                 # whole rows among them
+    out = out.to(DEV)
+    bad[out] = torch.where(torch.arange(B, device=DEV)[:, None] % 2 == 0, -1,
+                           kc.shape[0]).expand_as(bad)[out].to(torch.int32)
+    run = lambda t, a, b: pkg.paged_append(q, k, v, a, b, t, lens, None, qw, kw, f,  # noqa: E731
+                                           k_descale=kd, v_descale=vd)
+    want = run(table, kc, vc)
+    assert pkg.cp_get_last_status() == 0
+    lost = torch.zeros(kc.shape[0], dtype=torch.bool, device=DEV)
+    lost[table.long()[out]] = True
+    for _ in range(5):
+        ka, va = k0.clone(), v0.clone()
+        got = run(bad, ka, va)
+        assert pkg.cp_get_last_status() == pkg.STATUS_CODES["CP_ERR_CACHE"]
+        assert torch.equal(got, want)
+        for a, whole, before in ((ka, kc, k0), (va, vc, v0)):
+            assert torch.equal(a[~lost], whole[~lost]) and torch.equal(a[lost], before[lost])
