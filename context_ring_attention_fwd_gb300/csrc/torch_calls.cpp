@@ -136,6 +136,34 @@ void arity(Py_ssize_t n, Py_ssize_t want) {
   TORCH_CHECK_TYPE(n == want, "expected ", want, " arguments, got ", n);
 }
 
+// The stream that a call runs on, made torch's current one while the call's own
+// tensors are made: the allocator hands a block to the stream that it was made for,
+// and takes it back in that stream's order.  On another stream a workspace that
+// the call drops could be given away while the kernels still use it, and an output
+// be a block that the other stream's work still writes.
+class Home {
+ public:
+  Home(PyObject* o, int dev)
+      : caller_(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev))),
+        stream_(stream_of(o, dev)) {
+    if (stream_ == caller_.stream()) return;
+    // The handle 1 is the default stream under another name; torch knows it as 0.
+    const cudaStream_t known = stream_ == cudaStreamLegacy ? nullptr : stream_;
+    guard_.reset_stream(
+        c10::cuda::getStreamFromExternal(known, static_cast<c10::DeviceIndex>(dev)));
+  }
+  cudaStream_t get() const { return stream_; }
+  // An output made here goes to the caller, whose current stream may use it too.
+  void hand_over(const Tensor& t, bool made) const {
+    if (made && t.defined() && guard_.current_stream()) t.record_stream(caller_.unwrap());
+  }
+
+ private:
+  c10::cuda::CUDAStream caller_;
+  cudaStream_t stream_;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+};
+
 template <class F>
 void run(const char* name, int dev, F&& call) {
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
@@ -185,6 +213,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   arity(n, 11);
   const Tensor& q = rows4(a[0], "q");
   const int dev = device_of(q, "q");
+  const Home home(a[10], dev);
   const at::ScalarType type = rows_type(q);
   const int B = to_int(q.size(0), "q"), S = to_int(q.size(1), "q"), Hq = to_int(q.size(2), "q"),
             d = to_int(q.size(3), "q");
@@ -208,12 +237,13 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t* const pos = dense_or_null<int32_t>(a[5], "positions", at::kInt, dev, {B, S});
   const float eps = to_float(a[8]);
   const bool pairs = to_bool(a[9]);
-  const cudaStream_t st = stream_of(a[10], dev);
   const Steps qs(&q), ks(k);
   run("cp_qk_norm_rope", dev, [&] {
     return cp_qk_norm_rope(q_at, qs.get(), k_at, ks.get(), qw, kw, eps, freq, rot, pairs, pos,
-                           qo_at, ko_at, B, S, Hq, Hk, d, type == at::kBFloat16, st);
+                           qo_at, ko_at, B, S, Hq, Hk, d, type == at::kBFloat16, home.get());
   });
+  home.hand_over(q_out, a[6] == Py_None);
+  home.hand_over(k_out, a[7] == Py_None);
   return tuple_of({&q_out, &k_out});
   END_HANDLE_TH_ERRORS
 }
@@ -226,6 +256,7 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   arity(n, 17);
   const Tensor& q = rows4(a[2], "q");
   const int dev = device_of(q, "q");
+  const Home home(a[15], dev);
   const at::ScalarType type = rows_type(q);
   const int B = to_int(q.size(0), "q"), S = to_int(q.size(1), "q"), Hq = to_int(q.size(2), "q"),
             d = to_int(q.size(3), "q");
@@ -274,14 +305,16 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ws = at::empty({need}, q.options().dtype(at::kByte));
   }
   void* const ws_at = dense(ws, "workspace", at::kByte, dev, ws.sizes());
-  const cudaStream_t st = stream_of(a[15], dev);
   const Steps qs(&q), ks(k), dqs(&dq), dks(k ? &dk : nullptr);
   run("cp_qk_norm_rope_bwd", dev, [&] {
     return cp_qk_norm_rope_bwd(dqo_at, dko_at, q_at, qs.get(), k_at, ks.get(), qw, kw, eps, freq,
                                rot, pairs, pos, dq_at, dqs.get(), dk_at, dks.get(), dw_at[0],
                                dw_at[1], B, S, Hq, Hk, d, type == at::kBFloat16, ws_at,
-                               ws.numel(), st);
+                               ws.numel(), home.get());
   });
+  home.hand_over(dq, a[8] == Py_None);
+  home.hand_over(dk, a[9] == Py_None);
+  for (int i = 0; i < 2; ++i) home.hand_over(dw[i], a[10 + i] == Py_None);
   return tuple_of({&dq, &dk, &dw[0], &dw[1]});
   END_HANDLE_TH_ERRORS
 }
@@ -334,6 +367,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   arity(n, 17);
   const Tensor& k = rows4(a[1], "k");
   const int dev = device_of(k, "k");
+  const Home home(a[16], dev);
   const int B = to_int(k.size(0), "k"), S = to_int(k.size(1), "k");
   const cp_paged_cache cache = cache_of(a[3], a[4], a[5], a[14], a[15], B, dev);
   const int64_t shape[4] = {B, S, cache.Hk, cache.d};
@@ -360,12 +394,12 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float* const freq = floats(a[10], "inv_freq", dev, rot / 2);
   const float eps = to_float(a[12]);
   const bool pairs = to_bool(a[13]);
-  const cudaStream_t st = stream_of(a[16], dev);
   const Steps qs(q), ks(&k), vs(&v);
   run("cp_paged_append", dev, [&] {
     return cp_paged_append(&cache, q_at, qs.get(), k_at, ks.get(), v_at, vs.get(), lens, fresh, qw,
-                           kw, eps, freq, rot, pairs, qo_at, B, S, Hq, st);
+                           kw, eps, freq, rot, pairs, qo_at, B, S, Hq, home.get());
   });
+  home.hand_over(q_out, a[11] == Py_None);
   return wrap(&q_out);
   END_HANDLE_TH_ERRORS
 }
@@ -377,6 +411,7 @@ PyObject* paged_attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   arity(n, 13);
   const Tensor& q = rows4(a[0], "q");
   const int dev = device_of(q, "q");
+  const Home home(a[12], dev);
   const int B = to_int(q.size(0), "q"), n_q = to_int(q.size(1), "q"), Hq = to_int(q.size(2), "q");
   const cp_paged_cache cache = cache_of(a[1], a[2], a[3], a[9], a[10], B, dev);
   const void* const q_at = operand(q, "q", at::kBFloat16, dev, {B, n_q, Hq, cache.d});
@@ -411,12 +446,13 @@ PyObject* paged_attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ws = at::empty({need}, q.options().dtype(at::kByte));
   }
   void* const ws_at = dense(ws, "workspace", at::kByte, dev, ws.sizes());
-  const cudaStream_t st = stream_of(a[12], dev);
   const Steps qs(&q);
   run("cp_paged_attn_decode", dev, [&] {
     return cp_paged_attn_decode(&cache, q_at, qs.get(), lens, pages_at, prefix_len, out_at, lse_at,
-                                B, n_q, Hq, ws_at, ws.numel(), st);
+                                B, n_q, Hq, ws_at, ws.numel(), home.get());
   });
+  home.hand_over(out, a[5] == Py_None);
+  home.hand_over(lse, a[6] == Py_None);
   return tuple_of({&out, &lse});
   END_HANDLE_TH_ERRORS
 }

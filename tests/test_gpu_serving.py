@@ -328,3 +328,90 @@ def test_two_threads_and_two_graphs():
     finally:
         pkg.test_set_prefix_path(-1)
     assert pkg.cp_get_last_status() == 0
+
+
+def some_calls():
+    """The four calls with small and large workspaces: (name, call, bytes of its workspace)."""
+    g = torch.Generator().manual_seed(7)
+    lens = [700 + int(x) for x in torch.randint(1, 90, (9,), generator=g)]
+    q, table, seq, prefix = filled(g, lens, 16, 4, 64, 16, 300, 700, n_q=2)
+    k, v = normal(g, 300, 16, 4, 64), normal(g, 300, 16, 4, 64)
+    x, y = normal(g, 1, 900, 16, 128), normal(g, 1, 900, 4, 128)
+    w, f = torch.ones(128, device=DEV), freqs(128)
+    dx, dy = normal(g, *x.shape), normal(g, *y.shape)
+    new = normal(g, 9, 2, 24, 64)
+    need = pkg.cp_paged_attn_decode_workspace_bytes(9, 2, 16, 4, 64, 700)
+    return [
+        ("decode", lambda **s: pkg.paged_attn_decode(q, k, v, table, seq, prefix, 700, **s), need),
+        ("forward", lambda **s: pkg.qk_norm_rope(x, y, w, w, f, **s), 1 << 16),
+        ("backward", lambda **s: pkg.qk_norm_rope_bwd(dx, dy, x, y, w, w, f, **s),
+         pkg.cp_qk_norm_rope_bwd_workspace_bytes(1, 900, 16, 4, 128)),
+        ("append", lambda **s: (pkg.paged_append(new[:, :, :16], new[:, :, 16:20], new[:, :, 20:],
+                                                 k, v, table, seq - 2, **s),), 1 << 16)]
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("path", [0, 1])
+def test_a_call_on_another_stream_keeps_its_memory_to_itself(path, raw):
+    """A call with stream= while that stream is behind, and while the current one is: neither
+    its workspace nor its outputs are memory that the other stream's work holds."""
+    side = torch.cuda.Stream()
+    given = side.cuda_stream if raw else side
+    pkg.test_set_prefix_path(path)
+    try:
+        for name, call, need in some_calls():
+            want = call()
+            torch.cuda.synchronize()
+            # the side stream is behind: what the current one allocates now is its own
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)
+            got = call(stream=given)
+            sizes = {need} | {t.numel() * t.element_size() for t in got}
+            fills = [torch.full((n,), 0xA5, dtype=torch.uint8, device=DEV)
+                     for n in sizes for _ in range(3)]
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+            assert all((t == 0xA5).all() for t in fills), name
+            # the current stream is behind: its dropped blocks are not the call's yet
+            del got, fills
+            torch.cuda.synchronize()
+            torch.cuda._sleep(20_000_000)
+            for n in sizes:
+                for _ in range(3):
+                    torch.full((n,), 0x5A, dtype=torch.uint8, device=DEV)
+            got = call(stream=given)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+            # the outputs, used here and dropped, are not the side stream's again until then
+            torch.cuda._sleep(20_000_000)
+            kept = [t.clone() for t in got]
+            sizes = [t.numel() * t.element_size() for t in got]
+            del got
+            with torch.cuda.stream(side):
+                for n in sizes:
+                    for _ in range(3):
+                        torch.full((n,), 0x5A, dtype=torch.uint8, device=DEV)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(kept, want)), name
+    finally:
+        pkg.test_set_prefix_path(-1)
+
+
+def test_a_call_captured_beside_the_current_stream():
+    """A capture whose calls are given a forked stream: replayed, it gives the single results."""
+    calls = some_calls()[:3]
+    want = [call() for _, call, _ in calls]
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = [call(stream=side) for _, call, _ in calls]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for r in got:
+            for t in r:
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
