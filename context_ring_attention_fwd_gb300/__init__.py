@@ -18,6 +18,7 @@ from typing import Optional, Sequence
 import torch
 
 from ._binding import (  # noqa: F401
+    _hand_over, _on,
     CP_OK, STATUS_CODES, STATUS_NAMES, CpError, LIB_PATH, cp_fp8_quantize, cp_get_last_status,
     cp_ring_attn_fwd_rank, cp_ring_attn_fwd_host, cp_ring_attn_fwd_host_workspace_bytes,
     cp_ring_attn_fwd_noalloc,
@@ -50,15 +51,17 @@ def ring_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_shards: i
     """Allocate out [B,S,H,d] (q's dtype) and lse [B,H,S] fp32 on q's device
     and run the fused forward (bf16 on tensor cores, fp32 on CUDA cores)."""
     B, S, H, d = q.shape
-    out = torch.empty_like(q)
-    lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device)
-    docs = doc_offsets_tensor(doc_offsets, q.device)
+    with _on(stream):
+        out = torch.empty_like(q)
+        lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device)
+        docs = doc_offsets_tensor(doc_offsets, q.device)
     if q.dtype == torch.bfloat16:
         cp_ring_attn_fwd(q, k, v, out, lse, n_shards, causal, docs, stream)
     elif q.dtype == torch.float32:
         cp_ring_attn_fwd_f32(q, k, v, out, lse, n_shards, causal, docs, stream)
     else:
         raise TypeError("q must be bf16 or fp32")
+    _hand_over(stream, out, lse)
     return out, lse
 
 
@@ -78,15 +81,17 @@ def ring_attn_fwd_host(q_host: torch.Tensor, k_host: torch.Tensor, v_host: torch
         need = cp_ring_attn_fwd_host_workspace_bytes(B, S, H, d, int(n_shards), esz)
         if need < 0:
             raise CpError("cp_ring_attn_fwd_host_workspace_bytes", STATUS_CODES["CP_ERR_SHAPE"])
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        with _on(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
         hout = torch.empty(q_host.shape, dtype=q_host.dtype, pin_memory=True)
         hlse = torch.empty((B, H, S), dtype=torch.float32, pin_memory=True)
     else:
         ws, hout, hlse = buffers
-    docs = doc_offsets_tensor(doc_offsets, ws.device)
-    st = stream if stream is not None else torch.cuda.current_stream(ws.device)
-    cp_ring_attn_fwd_host(q_host, k_host, v_host, hout, hlse, n_shards, causal, docs, ws, st)
-    st.synchronize()
+    with _on(stream):
+        docs = doc_offsets_tensor(doc_offsets, ws.device)
+        st = torch.cuda.current_stream(ws.device)
+        cp_ring_attn_fwd_host(q_host, k_host, v_host, hout, hlse, n_shards, causal, docs, ws, st)
+        st.synchronize()
     return hout, hlse
 
 
@@ -104,37 +109,39 @@ def ring_attn_composed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_shar
     N = int(n_shards)
     L = S // N
     dev = q.device
-    docs = doc_offsets_tensor(doc_offsets, dev)
-    out = torch.empty_like(q)
-    lse = torch.empty((B, H, S), dtype=torch.float32, device=dev)
-    o_acc = torch.empty((B, L, H, d), dtype=torch.float32, device=dev)
-    m_acc = torch.empty((B, H, L), dtype=torch.float32, device=dev)
-    l_acc = torch.empty((B, H, L), dtype=torch.float32, device=dev)
-    o_p = torch.empty_like(o_acc)
-    m_p = torch.empty_like(m_acc)
-    l_p = torch.empty_like(l_acc)
-    o_fin = torch.empty((B, L, H, d), dtype=q.dtype, device=dev)
-    lse_fin = torch.empty((B, H, L), dtype=torch.float32, device=dev)
-    for i in range(N):
-        if order == "ascending" or order is None:
-            js = list(range(N))
-        elif order == "ring":
-            js = [(i - t) % N for t in range(N)]
-        else:
-            js = [int(x) for x in order]
-        first = True
-        for j in js:
-            if skip_masked and causal and doc_offsets is None and j > i:
-                continue
-            if first:  # the first visited step initialises the running state
-                cp_ring_step(q, k, v, o_acc, m_acc, l_acc, N, i, j, causal, docs, stream)
-                first = False
-                continue
-            cp_ring_step(q, k, v, o_p, m_p, l_p, N, i, j, causal, docs, stream)
-            cp_lse_merge(o_acc, m_acc, l_acc, o_p, m_p, l_p, stream)
-        cp_lse_finalize(o_acc, m_acc, l_acc, o_fin, lse_fin, stream)
-        out[:, i * L:(i + 1) * L].copy_(o_fin)
-        lse[:, :, i * L:(i + 1) * L].copy_(lse_fin)
+    with _on(stream):  # the copies into out and lse among them
+        docs = doc_offsets_tensor(doc_offsets, dev)
+        out = torch.empty_like(q)
+        lse = torch.empty((B, H, S), dtype=torch.float32, device=dev)
+        o_acc = torch.empty((B, L, H, d), dtype=torch.float32, device=dev)
+        m_acc = torch.empty((B, H, L), dtype=torch.float32, device=dev)
+        l_acc = torch.empty((B, H, L), dtype=torch.float32, device=dev)
+        o_p = torch.empty_like(o_acc)
+        m_p = torch.empty_like(m_acc)
+        l_p = torch.empty_like(l_acc)
+        o_fin = torch.empty((B, L, H, d), dtype=q.dtype, device=dev)
+        lse_fin = torch.empty((B, H, L), dtype=torch.float32, device=dev)
+        for i in range(N):
+            if order == "ascending" or order is None:
+                js = list(range(N))
+            elif order == "ring":
+                js = [(i - t) % N for t in range(N)]
+            else:
+                js = [int(x) for x in order]
+            first = True
+            for j in js:
+                if skip_masked and causal and doc_offsets is None and j > i:
+                    continue
+                if first:  # the first visited step initialises the running state
+                    cp_ring_step(q, k, v, o_acc, m_acc, l_acc, N, i, j, causal, docs, stream)
+                    first = False
+                    continue
+                cp_ring_step(q, k, v, o_p, m_p, l_p, N, i, j, causal, docs, stream)
+                cp_lse_merge(o_acc, m_acc, l_acc, o_p, m_p, l_p, stream)
+            cp_lse_finalize(o_acc, m_acc, l_acc, o_fin, lse_fin, stream)
+            out[:, i * L:(i + 1) * L].copy_(o_fin)
+            lse[:, :, i * L:(i + 1) * L].copy_(lse_fin)
+    _hand_over(stream, out, lse)
     return out, lse
 
 
@@ -144,13 +151,15 @@ def fp8_quantize_qkv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=N
     descales [B,H] fp32."""
     B, S, H, d = q.shape
     dev = q.device
-    q8 = torch.empty((B, S, H, d), dtype=torch.uint8, device=dev)
-    k8 = torch.empty_like(q8)
-    v8t = torch.empty((B, H, d, S), dtype=torch.uint8, device=dev)
-    desc = [torch.empty((B, H), dtype=torch.float32, device=dev) for _ in range(3)]
+    with _on(stream):
+        q8 = torch.empty((B, S, H, d), dtype=torch.uint8, device=dev)
+        k8 = torch.empty_like(q8)
+        v8t = torch.empty((B, H, d, S), dtype=torch.uint8, device=dev)
+        desc = [torch.empty((B, H), dtype=torch.float32, device=dev) for _ in range(3)]
     cp_fp8_quantize(q, q8, desc[0], False, stream)
     cp_fp8_quantize(k, k8, desc[1], False, stream)
     cp_fp8_quantize(v, v8t, desc[2], True, stream)
+    _hand_over(stream, q8, k8, v8t, *desc)
     return q8, k8, v8t, desc[0], desc[1], desc[2]
 
 
@@ -160,10 +169,12 @@ def ring_attn_fwd_fp8(fp8_inputs, n_shards: int = 1, causal: bool = True, doc_of
     returns (out [B,S,H,d] bf16, lse [B,H,S] fp32)."""
     q8, k8, v8t, qd, kd, vd = fp8_inputs
     B, S, H, d = q8.shape
-    out = torch.empty((B, S, H, d), dtype=torch.bfloat16, device=q8.device)
-    lse = torch.empty((B, H, S), dtype=torch.float32, device=q8.device)
-    docs = doc_offsets_tensor(doc_offsets, q8.device)
+    with _on(stream):
+        out = torch.empty((B, S, H, d), dtype=torch.bfloat16, device=q8.device)
+        lse = torch.empty((B, H, S), dtype=torch.float32, device=q8.device)
+        docs = doc_offsets_tensor(doc_offsets, q8.device)
     cp_ring_attn_fwd_fp8(q8, k8, v8t, qd, kd, vd, out, lse, n_shards, causal, docs, stream)
+    _hand_over(stream, out, lse)
     return out, lse
 
 
@@ -172,9 +183,11 @@ def ring_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.
                   doc_offsets=None, stream=None):
     """The bf16 backward for the forward's (out, lse): allocates and returns
     (dq, dk, dv) [B,S,H,d] bf16."""
-    dq, dk, dv = (torch.empty_like(q) for _ in range(3))
-    docs = doc_offsets_tensor(doc_offsets, q.device)
+    with _on(stream):
+        dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+        docs = doc_offsets_tensor(doc_offsets, q.device)
     cp_ring_attn_bwd(q, k, v, out, lse, dout, dq, dk, dv, n_shards, causal, docs, None, stream)
+    _hand_over(stream, dq, dk, dv)
     return dq, dk, dv
 
 

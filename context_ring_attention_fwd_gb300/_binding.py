@@ -7,6 +7,7 @@ falling back to anything else.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.util
 import os
@@ -143,6 +144,29 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _on(stream):
+    """Context in which `stream` (None: nothing changes) is torch's current one, for
+    the tensors that a call makes itself.  The allocator hands a block to the stream
+    it was made for and takes it back in that stream's order: made for another, a
+    workspace could be given away while the call's kernels still use it, and an
+    output be a block that the other stream's work still writes."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        # 0 and 1 are the default stream's handles; an ExternalStream of 0 is a new stream
+        handle = int(stream)
+        stream = (torch.cuda.ExternalStream(handle) if handle > 1
+                  else torch.cuda.default_stream())
+    return torch.cuda.stream(stream)
+
+
+def _hand_over(stream, *tensors) -> None:
+    """Outputs made under _on(stream) go to the caller, whose current stream may use them."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(t.device))
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -259,7 +283,8 @@ def cp_ring_attn_bwd(q, k, v, out, lse, dout, dq, dk, dv, n_shards: int, causal:
     if need < 0:
         raise CpError("cp_ring_attn_bwd_workspace_bytes", STATUS_CODES["CP_ERR_SHAPE"])
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _check("cp_ring_attn_bwd", lib().cp_ring_attn_bwd(
         _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
         _ptr(dv), B, S, H, d, int(n_shards), int(bool(causal)), _ptr(doc_offsets),
@@ -360,7 +385,8 @@ def cp_ring_attn_fwd_emulated(q, k, v, out, lse, n_shards: int, causal: bool = T
     if need < 0:
         raise CpError("cp_ring_emulated_workspace_bytes", STATUS_CODES["CP_ERR_SHAPE"])
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     recv = (ctypes.c_int64 * int(n_shards))()
     cs = None if copy_stream is None else _stream(copy_stream)
     _check("cp_ring_attn_fwd_emulated", lib().cp_ring_attn_fwd_emulated(
@@ -385,7 +411,8 @@ def cp_ulysses_attn_fwd(q, k, v, out, lse, n_shards: int, causal: bool = True,
     if need < 0:
         raise CpError("cp_ulysses_workspace_bytes", STATUS_CODES["CP_ERR_SHAPE"])
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     moved = ctypes.c_int64(0)
     _check("cp_ulysses_attn_fwd", lib().cp_ulysses_attn_fwd(
         _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, S, H, d, int(n_shards),
@@ -491,11 +518,13 @@ def cp_ring_schedule_device(S: int, n_shards: int, causal: bool = True,
     device: int32 [n_tiles, 2] (first, last flat key tile)."""
     L = S // n_shards
     n_tiles = n_shards * ((L + 127) // 128)
-    out = torch.full((n_tiles, 2), -7, dtype=torch.int32, device=device)
+    with _on(stream):
+        out = torch.full((n_tiles, 2), -7, dtype=torch.int32, device=device)
     if doc_offsets is not None:
         _need(doc_offsets, "doc_offsets", torch.int32)
     _check("cp_ring_schedule_device", lib().cp_ring_schedule_device(
         S, n_shards, int(bool(causal)), _ptr(doc_offsets), _ptr(out), _stream(stream)))
+    _hand_over(stream, out)
     return out
 
 

@@ -82,3 +82,64 @@ def test_two_threads_share_the_library_state():
             assert got is not None, (i, rep)
             for a, b in zip(got, alone[i]):
                 assert torch.equal(a, b), (i, rep)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_given_stream_owns_what_the_call_allocates(raw):
+    """stream= while that stream is behind: neither the outputs nor the workspaces and document
+    offsets that a call makes itself are memory that the current stream can take meanwhile."""
+    c = _case(83, 1024, [0, 300, 301, 1024])
+    q, k, v, N, docs, dout = c["q"], c["k"], c["v"], c["N"], c["docs"], c["dout"]
+    B, S, H, d = q.shape
+    out, lse = pkg.ring_attn_fwd(q, k, v, N, True, docs)
+    codes = pkg.fp8_quantize_qkv(q, k, v)
+    docs_t = pkg.doc_offsets_tensor(docs, q.device)
+    need = {"bwd": pkg.cp_ring_attn_bwd_workspace_bytes(B, S, H, d, N),
+            "ring": pkg.cp_ring_emulated_workspace_bytes(B, S, H, d, 2),
+            "all-to-all": pkg.cp_ulysses_workspace_bytes(B, S, H, d, 2)}
+
+    def into(fn):
+        def call(**s):
+            o, l = torch.empty_like(out), torch.empty_like(lse)
+            torch.cuda.synchronize()
+            if s:
+                with torch.cuda.stream(side):
+                    torch.cuda._sleep(20_000_000)
+            fn(q, k, v, o, l, 2, True, **s)
+            return o, l
+        return call
+
+    side = torch.cuda.Stream()
+    given = side.cuda_stream if raw else side
+    calls = {"fwd": lambda **s: pkg.ring_attn_fwd(q, k, v, N, True, docs, **s),
+             "bwd": lambda **s: pkg.ring_attn_bwd(q, k, v, out, lse, dout, N, True, docs, **s),
+             "steps": lambda **s: pkg.ring_attn_composed(q, k, v, N, True, **s),
+             "codes": lambda **s: pkg.fp8_quantize_qkv(q, k, v, **s),
+             "fp8": lambda **s: pkg.ring_attn_fwd_fp8(codes, N, True, docs, **s),
+             "schedule": lambda **s: (pkg.cp_ring_schedule_device(S, N, True, docs_t, **s),),
+             "ring": into(pkg.cp_ring_attn_fwd_emulated),
+             "all-to-all": into(pkg.cp_ulysses_attn_fwd)}
+    for name, call in calls.items():
+        want = call()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = call(stream=given)
+        sizes = {need.get(name, 1024)} | {t.numel() * t.element_size() for t in got}
+        fills = [torch.full((n,), 0xA5, dtype=torch.uint8, device=DEV) for n in sizes
+                 for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+        assert all((t == 0xA5).all() for t in fills), name
+        del got, fills
+        torch.cuda.synchronize()
+        if name in ("ring", "all-to-all"):
+            continue                                   # their outputs are the caller's
+        torch.cuda._sleep(20_000_000)
+        for n in sizes:
+            for _ in range(4):
+                torch.full((n,), 0x5A, dtype=torch.uint8, device=DEV)
+        got = call(stream=given)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+    assert pkg.cp_get_last_status() == 0
