@@ -96,15 +96,16 @@ __global__ void __launch_bounds__(kThreads, 2) paged_append_kernel(const AppendP
   bool turned;
   lane_columns<NP>(l, p.rot, kInterleaved, lo, hi, turned);
 
-  auto new_len = [&](int b) {
+  // `tells`: this call reports a length that is out of range (some call of each row's does).
+  auto new_len = [&](int b, bool tells) {
     const int n = p.new_lens ? __ldg(p.new_lens + b) : p.S;
-    if ((n < 0 || n > p.S) && blockIdx.x == 0) atomicOr(p.err, kErrCache);
+    if ((n < 0 || n > p.S) && tells) atomicOr(p.err, kErrCache);
     return max(0, min(n, p.S));
   };
   int tokens = p.tokens;
   if (p.compact) {
     static_assert(kMaxScan == kThreads, "one thread a row");
-    const int n = threadIdx.x < p.B ? new_len(threadIdx.x) : 0;
+    const int n = threadIdx.x < p.B ? new_len(threadIdx.x, blockIdx.x == 0) : 0;
     int x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -156,7 +157,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_append_kernel(const AppendP
     const int b = x.b, s = x.s;
     const int held = __ldg(p.cache_lens + b);
     x.page = -2;
-    if (!p.compact && s >= new_len(b)) return;  // padding behind the new tokens: not touched
+    // Every row has a unit of its first token's values.
+    const bool tells = x.kind == 2 && s == 0 && lane == 0;
+    if (!p.compact && s >= new_len(b, tells)) return;  // padding behind the new tokens: not touched
     const T* const xrow = static_cast<const T*>(t.x) + b * t.xb + s * t.xs;
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {

@@ -264,3 +264,20 @@ def test_tokens_left_out_do_not_disturb_the_others(B, S, e4m3):
         assert torch.equal(got, want)
         for a, whole, before in ((ka, kc, k0), (va, vc, v0)):
             assert torch.equal(a[~lost], whole[~lost]) and torch.equal(a[lost], before[lost])
+
+
+@pytest.mark.parametrize("B,S", [(64, 1), (300, 2)])
+@pytest.mark.parametrize("bad", [-2, 7])
+def test_a_new_length_out_of_range_is_reported_for_any_row(B, S, bad):
+    """The calls whose padding is walked: single tokens, and more rows than one scan takes."""
+    q, k, v, (kc, vc), table, lens, (qw, kw), _ = setup(B, S, 32, 8, 128, 16, False, B)
+    new = torch.full((B,), S, dtype=torch.int32, device=DEV)
+    pkg.paged_append(q, k, v, kc, vc, table, lens, new, qw, kw)
+    assert pkg.cp_get_last_status() == 0
+    for row in (0, 1, B // 2, B - 1):
+        new[:] = S
+        new[row] = bad
+        ka, va = kc.clone(), vc.clone()
+        pkg.paged_append(q, k, v, ka, va, table, lens, new, qw, kw)
+        assert pkg.cp_get_last_status() == pkg.STATUS_CODES["CP_ERR_CACHE"], row
+        assert torch.equal(ka, kc) and torch.equal(va, vc)     # the nearer of 0 and S
