@@ -843,7 +843,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float top = fmaxf(half_max(sv, 0), half_max(sv, 1)) * sc;
         const bool move = f == first || (!in_range && top > m);
         const float alpha = (f == first || !move) ? 1.f : ptx::ex2(m - top);
-        if (move) m = top == -INFINITY ? 0.f : top;
+        if (move) m = top;
+        // A row that has met scores of -inf alone keeps the reference -inf: its state is
+        // empty, and no later tile is in range of it, so the first with a score sets it.
+        const float base = (m == -INFINITY ? 0.f : m) - kShift;
         l *= alpha;
         if (f > first) {
           // O_t holds the sum up to the previous tile: the MMA warp issued
@@ -855,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sum = 0.f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          sum += exp_half<kE4M3>(sv, half, sc, m - kShift, pk);
+          sum += exp_half<kE4M3>(sv, half, sc, base, pk);
           ptx::tmem_st32(tS + 32 * half, pk);
           ptx::tmem_wait_st();
           ptx::tc_fence_before();

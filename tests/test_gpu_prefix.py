@@ -237,3 +237,37 @@ def test_both_kernels_give_the_same_attention(e4m3):
     assert pkg.launch_counts()[0] == before + 1
     big.check(*out)
     pkg.test_set_prefix_path(1)
+
+
+@pytest.mark.parametrize("path", [0, 1])
+@pytest.mark.parametrize("far", [-300.0, -20.0, 50.0])
+def test_keys_that_score_minus_infinity_leave_the_others(path, far):
+    """Keys of infinite entries lead the prefix over whole tiles and whole CTAs' shares of it:
+    the heads that score them -inf attend the others, whatever those score, and the head that
+    scores them +inf is NaN."""
+    t = Case(40, 1, 4, 1, 128, 16, 20000, 4, False, 14)
+    t.q[:, :, :, 0] = torch.tensor([-1.0, -2.0, 1.0, -0.5], device=DEV)
+    t.q[:, :, :, 1] = 64.0
+    pos = torch.arange(t.P, device=DEV)
+    rows = t.k[t.prefix.long()[pos // 16], pos % 16]
+    rows[:, 0, 0] = 0.0
+    rows[:, 0, 1] = far * 128 ** 0.5 / 64.0            # moves every finite score by `far`
+    rows[pos < 16992, 0, 0] = float("inf")
+    t.k[t.prefix.long()[pos // 16], pos % 16] = rows
+    own = t.k[:, :, :, 1]
+    own[~own.isnan()] = far * 128 ** 0.5 / 64.0
+    pkg.test_set_prefix_path(path)
+    try:
+        out, lse = t.run()
+    finally:
+        pkg.test_set_prefix_path(1)
+    assert out[:, :, 2].isnan().all() and lse[:, 2].isnan().all()
+    live = [0, 1, 3]
+    t.q = t.q[:, :, live].contiguous()
+    # the same attention without the keys that nobody sees, 1062 whole pages
+    cut = Case.__new__(Case)
+    cut.kd = cut.vd = None
+    cut.q, cut.k, cut.v = t.q, t.k, t.v
+    cut.prefix, cut.table = t.prefix[1062:].contiguous(), t.table[:, 1062:].contiguous()
+    cut.P, cut.lens = t.P - 16992, t.lens - 16992
+    cut.check(out[:, :, live], lse[:, live])
