@@ -581,6 +581,9 @@ cp_status cp_paged_append(const cp_paged_cache* cache, const void* q, const int6
  * queries: query i is at position seq_lens[b] - n_q + i.  It sees the keys of
  * positions [0, prefix_len), read through prefix_pages, and those of positions
  * [prefix_len, seq_lens[b] - n_q + i], read through row b of the page table.
+ * The prefix is not masked: a query whose position lies inside it (seq_lens[b] <
+ * prefix_len + n_q - 1) sees the later positions of the prefix too.  For causal
+ * queries, prefix_len must not exceed the first query's position + 1.
  *  q          device, bf16 [B,n_q,Hq,d], strides as for cp_qk_norm_rope; head h
  *             reads key head h / (Hq / Hk); Hq % Hk must be 0.
  *  seq_lens   device int32 [B]: 0 for an unused row of the batch, otherwise
@@ -599,8 +602,9 @@ cp_status cp_paged_append(const cp_paged_cache* cache, const void* q, const int6
  * Rows that see no key (an unused batch row, a query before its sequence's
  * start) get out = 0, lse = -inf.  What the cache holds in slots that no query
  * sees is never used, whatever it is.  A sequence with a length outside its
- * range, or a page outside the cache among those it reads, gets NaN in its
- * rows of out and lse (a bad prefix page: every used row), the others are
+ * range gets NaN in its rows of out and lse, and so does every row that sees a
+ * key on a page outside the cache (a prefix page: every used row; a page of the
+ * last n_q - 1 keys alone: the queries from its first key on); the others are
  * computed as usual, and cp_get_last_status reports CP_ERR_CACHE.
  * Nothing is allocated; lengths are read on the device, so a captured call
  * follows them when it is replayed.

@@ -288,3 +288,19 @@ def test_binding_refusals():
     assert e.value.name == "CP_ERR_BUFFER"
     with pytest.raises(pkg.CpError):
         pkg.paged_attn_decode(t.q[:, :, :3], *args[1:])
+
+
+@pytest.mark.parametrize("P,e4m3", [(0, False), (0, True), (20, False)])
+def test_a_bad_page_of_the_last_keys_marks_the_queries_that_see_it(P, e4m3):
+    """The last two of four queries' keys begin a page: the first two queries see none of it."""
+    t = Batch([34, 50, 3], 4, 4, 2, 64, 16, 0, e4m3, seed=12) if not P else \
+        Batch([34, 50], 4, 4, 2, 64, 16, P, e4m3, seed=12)
+    want, wantl = t.run()
+    assert pkg.cp_get_last_status() == 0
+    for bad in (-1, t.k.shape[0]):
+        t.table[0, 2] = bad                              # positions 32, 33 of 34
+        got, gotl = t.run()
+        assert pkg.cp_get_last_status() == pkg.STATUS_CODES["CP_ERR_CACHE"]
+        assert got[0, 2:].isnan().all() and gotl[0, :, 2:].isnan().all()
+        assert torch.equal(got[0, :2], want[0, :2]) and torch.equal(gotl[0, :, :2], wantl[0, :, :2])
+        assert torch.equal(got[1:], want[1:]) and torch.equal(gotl[1:], wantl[1:])
