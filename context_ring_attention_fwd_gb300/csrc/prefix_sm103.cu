@@ -25,6 +25,13 @@
 // before the tensor core's reads with a proxy fence.  (64 sequences under a 32K prefix,
 // bf16: 37 us by TMA, 54 by cp.async; 512 rows under 128K, E4M3: 189 and 327.)
 //
+// P in 16 bits, as the ring forward holds it, while l sums it in fp32.  In bf16 that
+// costs as much as the output's own rounding: against 64 bits, relative in the norm,
+// 2.3e-3 for 64 sequences under a 32K prefix, where the output's rounding alone makes
+// 1.66e-3.  A second product for what the rounding leaves, as the 16-row items of
+// paged_decode.cu take, would put 1024 more tensor clocks on a pair of tiles that has
+// 2048, in a kernel that the tensor pipe bounds; those items are bound by HBM.
+//
 // Bound by shared memory and the tensor pipe alike: of a pair of 128 x 128 tiles, the
 // products take 2048 clocks, and the operands that they read (A and B of S, V) and the
 // copies that fill them 2048 clocks at 128 bytes each; a pair takes about 2900.  512 rows

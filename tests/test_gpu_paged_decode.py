@@ -304,3 +304,45 @@ def test_a_bad_page_of_the_last_keys_marks_the_queries_that_see_it(P, e4m3):
         assert got[0, 2:].isnan().all() and gotl[0, :, 2:].isnan().all()
         assert torch.equal(got[0, :2], want[0, :2]) and torch.equal(gotl[0, :, :2], wantl[0, :, :2])
         assert torch.equal(got[1:], want[1:]) and torch.equal(gotl[1:], wantl[1:])
+
+
+@pytest.mark.parametrize("P", [0, 5])
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_weights_keep_more_than_their_rounding_to_bf16(d, P):
+    """Few keys of nearly equal small scores and values of either sign.  P is held as its upper
+    half and a bf16 rounding of the rest, which is below 2^-7 of P: off by 2^-15 of P, and 2^-20
+    for the bit that keeps the rest from 0.  With the scores' part and the output's own rounding
+    that is all; P rounded once would be off by up to 2^-8 of sum p |v|."""
+    lens = [P + 2 + b % 9 for b in range(60)]
+    t = Batch(lens, 1, 8, 2, d, 16, P, seed=20 + P, scale=0.25)
+    pkg.test_set_prefix_path(0)
+    try:
+        out, _ = t.run()
+    finally:
+        pkg.test_set_prefix_path(-1)
+    q, k, v = _np(t.q), _np(t.k), _np(t.v)
+    args = (t.table.cpu().numpy(), lens, () if t.prefix is None else t.prefix.cpu().numpy(), P)
+    want, _ = serving.paged_decode(q, k, v, *args)
+    size, _ = serving.paged_decode(q, k, np.abs(v), *args)
+    A = np.linalg.norm(q, axis=-1).max() * np.nanmax(np.linalg.norm(k, axis=-1)) / np.sqrt(d)
+    tol = (2.0 ** -15 + 2.0 ** -20 + 2.0 ** -15 * (A + 1)) * size + 2.0 ** -8 * np.abs(want)
+    assert np.all(np.abs(_np(out) - want) <= tol)
+
+
+@pytest.mark.parametrize("n", [1, 40, 700])
+def test_infinite_values_of_seen_keys_stay_infinite(n):
+    """out = sum p v with p > 0: +inf, -inf, or NaN where both meet, and no other column."""
+    t = Batch([n, n], 1, 4, 2, 64, 16, 0, seed=13)
+    want, wantl = t.run()
+    inf = float("inf")
+    at = [(int(t.table[0, p // 16]), p % 16) for p in sorted({0, n // 2, n - 1})]
+    t.v[at[0][0], at[0][1], :, 3] = inf
+    t.v[at[-1][0], at[-1][1], :, 9] = -inf
+    t.v[at[0][0], at[0][1], :, 20] = inf
+    t.v[at[-1][0], at[-1][1], :, 20] = inf if n == 1 else -inf
+    got, gotl = t.run()
+    assert torch.equal(gotl, wantl) and torch.equal(got[1], want[1])
+    assert (got[0, :, :, 3] == inf).all() and (got[0, :, :, 9] == -inf).all()
+    assert (got[0, :, :, 20] == inf).all() if n == 1 else got[0, :, :, 20].isnan().all()
+    keep = [c for c in range(64) if c not in (3, 9, 20)]
+    assert torch.equal(got[0][..., keep], want[0][..., keep])
