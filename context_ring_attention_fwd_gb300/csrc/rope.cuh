@@ -71,11 +71,19 @@ __device__ __forceinline__ uint64_t turn_fraction(float inv_freq) {
 }
 
 // cos and sin of position * inv_freq, from the fraction of a turn.  The top
-// 32 bits of the 64-bit product, read as signed, are the angle in units of
-// 2^-31 half turns.
+// 32 bits of the 64-bit product are the angle in units of 2^-31 half turns: the
+// nearest quarter turn (the top two bits, rounded) is taken off before the rest,
+// an eighth of a turn at most, is rounded to fp32.  So the angle is off by 2^-27
+// half turns, 2.3e-8, where half a turn rounded whole would be off by 9.4e-8.
 __device__ __forceinline__ void angle_of(int position, uint64_t fraction, float& c, float& s) {
   const uint64_t turns = static_cast<uint64_t>(static_cast<int64_t>(position)) * fraction;
-  sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f, &s, &c);
+  const uint32_t u = static_cast<uint32_t>(turns >> 32);
+  const uint32_t quarter = (u + 0x20000000u) >> 30;
+  float sn, cs;
+  sincospif(static_cast<float>(static_cast<int32_t>(u - (quarter << 30))) * 0x1p-31f, &sn, &cs);
+  const bool odd = quarter & 1u;
+  c = __uint_as_float(__float_as_uint(odd ? sn : cs) ^ (((quarter + 1u) & 2u) << 30));
+  s = __uint_as_float(__float_as_uint(odd ? cs : sn) ^ ((quarter & 2u) << 30));
 }
 
 // The fractions of the angles that this lane computes (kAngles of its row

@@ -256,3 +256,32 @@ def test_binding_refusals():
         pkg.qk_norm_rope(q.transpose(2, 3), k, qw, kw, f)
     with pytest.raises(pkg.CpError):
         pkg.qk_norm_rope(q, k, qw, kw, f[:4])      # rot_dim 8
+
+
+@pytest.mark.parametrize("il", [False, True])
+def test_cosines_and_sines_are_those_of_the_exact_angle(il):
+    """Rows of (1, 0) pairs, not normed, turn to the cosines and sines themselves.  The angle is
+    off by 2^-27 pi from its rounding and 2^-32 pi from the position's product, cosine and sine by
+    1 ulp (2^-24 below 1): 2.4e-8 + 6.0e-8."""
+    d, S = 64, 20000
+    g = torch.Generator().manual_seed(41)
+    pos = torch.cat([torch.arange(S // 2), torch.randint(-2 ** 31, 2 ** 31 - 1, (S - S // 2,),
+                                                         generator=g)])[None]
+    pos = pos.to(torch.int32)
+    x = torch.zeros((1, S, 1, d))
+    x[..., slice(0, d, 2) if il else slice(0, d // 2)] = 1.0
+    f = freqs(d)
+    y, _ = pkg.qk_norm_rope(x.to(DEV), None, None, None, f.to(DEV), pos.to(DEV), interleaved=il)
+    y = _np(y)[0, :, 0]
+    c, s = (y[:, 0::2], y[:, 1::2]) if il else (y[:, :d // 2], y[:, d // 2:])
+    angle = serving.angles(pos.numpy(), f.numpy())[0]
+    bound = np.pi * (2.0 ** -27 + 2.0 ** -32) + 2.0 ** -24
+    assert np.abs(c - np.cos(angle)).max() <= bound and np.abs(s - np.sin(angle)).max() <= bound
+    # the quarter turns themselves: fp32 pi / 2 is 4.4e-8 from it, four of them 1.75e-7
+    quarter = torch.tensor([np.pi / 2] * (d // 2), dtype=torch.float32)
+    y, _ = pkg.qk_norm_rope(x[:, :9].to(DEV).contiguous(), None, None, None, quarter.to(DEV),
+                            torch.arange(-4, 5, dtype=torch.int32, device=DEV)[None], interleaved=il)
+    y = _np(y)[0, :, 0]
+    c, s = (y[:, 0], y[:, 1]) if il else (y[:, 0], y[:, d // 2])
+    assert np.abs(c - np.array([1, 0, -1, 0, 1, 0, -1, 0, 1])).max() <= 2e-7
+    assert np.abs(s - np.array([0, 1, 0, -1, 0, 1, 0, -1, 0])).max() <= 2e-7
