@@ -862,19 +862,24 @@ std::atomic<int> g_prefix_path{-1};
 
 // Whether the prefix goes to prefix_attn_kernel.  The 16-row items of
 // paged_decode_kernel read the prefix's keys and values once per 16 rows of the
-// batch, from L2 but for the first time; prefix_attn_kernel reads them once per
-// 256 and takes about 10 us longer to start and to join.  They meet where the
-// former reads about 120 MB.  Measured (us, 16-row items / prefix_attn_kernel, 8 key
-// heads, 64 more keys a sequence): bf16, d = 128, 32K prefix: 46 / 50 at 16 rows, 56 / 50
-// at 32, 124 / 58 at 128; 8K: 30 / 30 at 48, 46 / 38 at 128; 2K: 28 / 32 at 128; E4M3,
-// 32K: 44 / 48 at 32, 65 / 48 at 64; bf16, d = 64, 32K: 36 / 40 at 32, 77 / 48 at 128.
+// batch, from L2 but for the first time, as fast as they compute: 0.10 to 0.19 us per
+// MB.  prefix_attn_kernel takes about 8 us longer to start and to join (80 MB of such
+// reads), and then its time is that of the prefix's own bytes: 1.4 times what
+// 16-row items take for them, 3.3 times for E4M3 at d = 64, which has no TMA path.
+// Up to 16 rows both read the prefix once.  Measured over 16 to 512 rows, 2 and 8 key
+// heads, 2K to 128K prefixes and pages of 64 tokens, the choice is the faster one or within
+// 2.5 us of it (16 rows under 128K, 2 key heads: 45 for 41).  Some points (us a call, items / prefix_attn_kernel, 8 key heads, 64 more
+// keys a sequence): bf16, d = 128: 32K 41 / 37 at 32 rows; 8K 21 / 22 at 32, 27 / 23 at 64;
+// 2K 20 / 22 at 128, 26 / 25 at 192.  bf16, d = 64: 32K 28 / 29 at 32, 34 / 29 at 48.
+// E4M3, d = 128: 32K 33 / 38 at 32, 44 / 39 at 48; 8K 23 / 27 at 64, 36 / 30 at 128.  E4M3,
+// d = 64: 32K 37 / 42 at 64, 50 / 43 at 96; 128K 96 / 111 at 48, 140 / 111 at 64.
 bool wide_prefix(long long rows, int prefix_len, int Hk, int d, int elem_bytes) {
   if (prefix_len <= 0) return false;
   const int forced = g_prefix_path.load(std::memory_order_relaxed);
   if (forced >= 0) return forced != 0;
-  const double read = static_cast<double>((rows + kRows - 1) / kRows) * prefix_len * Hk * 2.0 *
-                      d * elem_bytes;
-  return rows > kRows && read > 120e6;
+  const double once = 2.0 * prefix_len * Hk * d * elem_bytes;
+  const double read = static_cast<double>((rows + kRows - 1) / kRows) * once;
+  return rows > kRows && read > 80e6 + (elem_bytes == 1 && d == 64 ? 3.3 : 1.4) * once;
 }
 
 // Byte offsets of the workspace's parts.
@@ -884,7 +889,7 @@ struct Space {
     const long long rows = static_cast<long long>(B) * n_q * Hq;
     const long long slots = 2LL * kMaxGrid * kRows;
     const long long whole = prefix_len > 0 ? 2 * rows : n_q > 1 ? rows : 0;
-    const long long pslots =  // for bf16, which takes prefix_attn_kernel no later than E4M3
+    const long long pslots =  // for bf16, which takes prefix_attn_kernel wherever E4M3 does
         wide_prefix(rows / Hk, prefix_len, Hk, d, 2) ? 2LL * kMaxPrefixGrid * kPrefixRows : 0;
     starts = 0;
     slot_o = align256(4LL * (B + 1));

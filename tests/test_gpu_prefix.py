@@ -271,3 +271,19 @@ def test_keys_that_score_minus_infinity_leave_the_others(path, far):
     cut.prefix, cut.table = t.prefix[1062:].contiguous(), t.table[:, 1062:].contiguous()
     cut.P, cut.lens = t.P - 16992, t.lens - 16992
     cut.check(out[:, :, live], lse[:, live])
+
+
+@pytest.mark.parametrize("e4m3,d,rows,wide", [
+    (False, 128, 16, False), (False, 128, 32, True), (False, 64, 32, False), (False, 64, 48, True),
+    (True, 128, 32, False), (True, 128, 48, True), (True, 64, 64, False), (True, 64, 96, True)])
+def test_the_rule_takes_the_kernel_that_measured_faster(e4m3, d, rows, wide):
+    """8 key heads under a 32K prefix, on both sides of the rule for each type and size of head."""
+    t = Case(rows // 4, 1, 32, 8, d, 64, 32768, 30, e4m3, rows)
+    pkg.test_set_prefix_path(-1)
+    try:
+        before = pkg.launch_counts()[0]
+        out = t.run()
+        assert pkg.launch_counts()[0] - before == int(wide)
+    finally:
+        pkg.test_set_prefix_path(1)
+    t.check(*out)
