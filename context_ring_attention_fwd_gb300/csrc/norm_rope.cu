@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   struct Unit {
     int ti, tok, b, s;
-    int chunk, end;  // this unit, and the last one but one of the warp's group
+    int chunk, end;  // this unit, and the one behind the last of the warp's group
   };
   auto group_at = [&](unsigned u) {
     Unit x;
@@ -322,16 +322,21 @@ cudaError_t launch_rows(RopeParams p, int tokens, float* dqw, float* dkw, cudaSt
   return e;
 }
 
-// Rows per unit: as many as keep enough bytes in flight per warp, one row group
-// when the call is too small to give every warp of the grid more.  Measured, one
-// group / kWide (us in the kernel): forward 16 tokens x 40 heads 4.4 / 6.2, 8192 x 64
-// 45.6 / 39.3; backward 8192 x 64 67.3 / 64.1; fp32 backward 3074 x 16 13.7 / 14.1.
+// Rows per unit: one row group of a token, or kWide of them, which keeps more bytes in
+// flight, where those give half of the grid's warps one.  Measured at 203 points (256 to
+// 16K tokens, 16 to 64 heads, both types, head sizes and directions) the choice takes 0.9 %
+// more than the faster form on average and never 16 %; from one unit a warp on, 2.4 % and
+// 30 %.  One group / kWide (us a call): forward, bf16, d = 128: 512 tokens x 16 heads 4.1 /
+// 4.4, x 40 6.0 / 5.1, 4096 x 64 27.1 / 22.6; backward, bf16, d = 128: 512 x 16 6.8 / 7.6,
+// 256 x 64 9.1 / 7.8, 8192 x 64 69.7 / 67.9; backward, fp32, d = 64: 512 x 16 5.8 / 6.6,
+// 512 x 64 9.6 / 8.7, 3000 x 16 11.3 / 11.5.  The longest fp32 calls lose by it: backward,
+// d = 128, 4096 x 64 65.1 / 68.7.
 template <typename T, int D, bool kBwd>
 cudaError_t launch_sized(const RopeParams& p, int tokens, float* dqw, float* dkw,
                          cudaStream_t stream) {
   constexpr int kWide = kBwd ? 2 : 4;
   const long long rows = static_cast<long long>(tokens) * (p.t[0].H + p.t[1].H);
-  const bool wide = rows / (kWide * RowLayout<T, D>::kRows) >= 2LL * sm_count() * kWarps;
+  const bool wide = rows / (kWide * RowLayout<T, D>::kRows) >= 1LL * sm_count() * kWarps;
   if (p.interleaved)
     return wide ? launch_rows<T, D, kWide, kBwd, true>(p, tokens, dqw, dkw, stream)
                 : launch_rows<T, D, 1, kBwd, true>(p, tokens, dqw, dkw, stream);
