@@ -98,19 +98,19 @@ def _compile_ext() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source, link libcpring.so and the Python extension;
-    returns the library's path."""
+    """Compile every source and link libcpring.so, then the Python extension;
+    returns the library's path.  The library needs nvcc alone: it is there
+    when the extension fails to build, whose error is raised last."""
     os.makedirs(OBJDIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         ext = ex.submit(_compile_ext)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        tmp = LIB + ".tmp"
+        _run([_nvcc(), *ARCH, "-shared", "-o", tmp, *objs], "link of libcpring.so")
+        if os.path.exists(EXT):
+            os.remove(EXT)  # an older library's
+        os.replace(tmp, LIB)
         ext_obj = ext.result()
-    tmp = LIB + ".tmp"
-    cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
     tmp = EXT + ".tmp"
     _run(["g++", "-shared", "-o", tmp, ext_obj, "-L" + LIBDIR, "-lcpring",
           "-L" + os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",

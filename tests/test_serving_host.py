@@ -219,3 +219,25 @@ def test_decode_workspace(lib):
     for bad in [(0, 1, 1, 1, 64), (1, 17, 1, 1, 64), (1, 1, 3, 2, 64), (1, 1, 2, 2, 80),
                 (4097, 1, 1, 1, 64)]:
         assert f(*bad) == -1
+
+
+def test_the_library_is_built_where_the_extension_is_not(tmp_path, monkeypatch):
+    """A failing extension leaves a linked libcpring.so behind, and its error is raised."""
+    from context_ring_attention_fwd_gb300 import _build
+    obj = tmp_path / "obj"
+    src = tmp_path / "one.cpp"
+    src.write_text('extern "C" int cp_one() { return 1; }\n')
+    for name, value in (("OBJDIR", str(obj)), ("LIBDIR", str(tmp_path)), ("CSRC", str(tmp_path)),
+                        ("LIB", str(tmp_path / "libcpring.so")), ("SOURCES", ["one.cpp"]),
+                        ("EXT", str(tmp_path / "cpring_torch.so"))):
+        monkeypatch.setattr(_build, name, value)
+
+    (tmp_path / "cpring_torch.so").write_text("an older build's")
+
+    def fails():
+        raise RuntimeError("no headers")
+    monkeypatch.setattr(_build, "_compile_ext", fails)
+    with pytest.raises(RuntimeError, match="no headers"):
+        _build.build()
+    assert ctypes.CDLL(str(tmp_path / "libcpring.so")).cp_one() == 1
+    assert not os.path.exists(tmp_path / "cpring_torch.so")
