@@ -315,7 +315,7 @@ cp_status check_cache(const cp_paged_cache* c) {
   if (c->elem_bytes == 1 && (!c->k_descale || !c->v_descale)) return CP_ERR_NULL;
   if (c->d != 64 && c->d != 128) return CP_ERR_UNSUPPORTED;
   if (c->n_pages < 1 || c->page_size < 1 || c->max_pages < 1 || c->Hk < 1 || c->Hk > 65535 ||
-      c->table_stride < c->max_pages || c->table_stride > (1LL << 31))
+      (c->table_stride != 0 && c->table_stride < c->max_pages) || c->table_stride > (1LL << 31))
     return CP_ERR_SHAPE;
   // positions, and those up to a tile behind the last, are int32
   if (static_cast<long long>(c->max_pages) * c->page_size > (1LL << 30)) return CP_ERR_SHAPE;

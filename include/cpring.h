@@ -533,7 +533,8 @@ typedef struct cp_paged_cache {
   const float* k_descale;   /* E4M3: device fp32 [Hk], > 0, value = code *             */
   const float* v_descale;   /* descale[head]; bf16: not read                           */
   const int32_t* page_table;  /* device, rows of max_pages entries                     */
-  int64_t table_stride;     /* entries between its rows, >= max_pages                  */
+  int64_t table_stride;     /* entries between its rows, >= max_pages; 0: one row that */
+                            /* every sequence uses                                     */
   int32_t n_pages;          /* pages of k and v                                        */
   int32_t page_size;        /* >= 1; max_pages * page_size <= 2^30                     */
   int32_t max_pages;

@@ -415,3 +415,29 @@ def test_a_call_captured_beside_the_current_stream():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("path", [0, 1])
+def test_an_expanded_page_table(path):
+    """Sequences that share every page through one row of the table, as its copies give it."""
+    g = torch.Generator().manual_seed(8)
+    P = 100
+    q, table, seq, prefix = filled(g, [P + 90], 8, 2, 64, 16, 20, P)
+    k, v = normal(g, 20, 16, 2, 64), normal(g, 20, 16, 2, 64)
+    q = normal(g, 40, 1, 8, 64)
+    lens = (P + 1 + torch.arange(40, dtype=torch.int32, device=DEV) * 2).contiguous()
+    wide = table.expand(40, table.shape[1])
+    assert wide.stride(0) == 0
+    pkg.test_set_prefix_path(path)
+    try:
+        want = pkg.paged_attn_decode(q, k, v, wide.contiguous(), lens, prefix, P)
+        got = pkg.paged_attn_decode(q, k, v, wide, lens, prefix, P)
+    finally:
+        pkg.test_set_prefix_path(-1)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    new = normal(g, 40, 1, 4, 64)                    # to 40 slots of the shared pages
+    ka, va = k.clone(), v.clone()
+    pkg.paged_append(None, new[:, :, :2], new[:, :, 2:], k, v, wide, lens - 1)
+    pkg.paged_append(None, new[:, :, :2], new[:, :, 2:], ka, va, wide.contiguous(), lens - 1)
+    assert torch.equal(k, ka) and torch.equal(v, va)
+    assert pkg.cp_get_last_status() == 0

@@ -241,3 +241,13 @@ def test_the_library_is_built_where_the_extension_is_not(tmp_path, monkeypatch):
         _build.build()
     assert ctypes.CDLL(str(tmp_path / "libcpring.so")).cp_one() == 1
     assert not os.path.exists(tmp_path / "cpring_torch.so")
+
+
+def test_one_row_of_pages_for_every_sequence_is_allowed(lib):
+    """A row stride of 0 passes the cache's checks: what fails next is the workspace's size, and
+    the append's heads."""
+    assert lib.cp_paged_attn_decode(*decode_args(dict(table_stride=0), n=1000)) == -6
+    assert lib.cp_paged_append(*append_args(dict(table_stride=0), Hq=-1)) == -2
+    assert lib.cp_paged_append(*append_args(dict(table_stride=0), rot=8)) == -3
+    for bad in (-1, 7):
+        assert lib.cp_paged_attn_decode(*decode_args(dict(table_stride=bad), n=1000)) == -2
