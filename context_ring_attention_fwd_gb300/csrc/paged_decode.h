@@ -1,8 +1,10 @@
 // What the two kernels of the decode attention (paged_decode.cu,
-// prefix_sm103.cu) share: the launch's parameters and the split of work.
+// prefix_sm103.cu) share: the launch's parameters, the split of work, and copies and
+// conversions of cached rows.
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -44,6 +46,27 @@ struct DecodeParams {
   int n_pages, page_size;
   long long capacity;        // max_pages * page_size
 };
+
+// 16 bytes to shared memory, the first `bytes` (0 or 16) of them copied, the rest zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Two E4M3 codes (16 bits) to two fp16 values, exactly.
+__device__ __forceinline__ uint32_t half2_of_codes(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 
 // Both kernels lay their items end to end in units, kItemCost of them for
 // starting and ending an item and one for each of its key tiles, and give every
