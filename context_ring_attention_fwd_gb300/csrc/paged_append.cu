@@ -8,9 +8,10 @@
 // or the E4M3 code of x times the reciprocal of descale[head] (in fp32, as
 // cp_fp8_quantize multiplies by its inverse scale).
 //
-// Bound by instructions for prefill chunks (3842 tokens of 32 + 8 + 8 heads to E4M3:
-// 24 us, half the copy rate; the issue slots are 40 % used with the 16 warps that the
-// registers allow) and by launch latency for single tokens (64 of them: 5.4 us).  A
+// Bound by latency.  Single tokens (64 of them: 4.3 us a call) by the launch; prefill
+// chunks (3842 tokens of 32 + 8 + 8 heads: 25.7 us in the kernel to E4M3, 25.0 to bf16,
+// half the copy rate) by how much 16 warps an SM, which is what the registers allow, keep
+// under way with one unit each ahead: DRAM is 23 % used, the issue slots 40 %.  A
 // warp's unit is a few heads of one token of q, k or v; rows are 16-byte
 // vectors of 8 (d = 128) or 4 lanes, so any page size, head order and page
 // stride costs the same; the next unit's rows are on their way meanwhile
@@ -59,7 +60,7 @@ struct AppendParams {
 // A chunk's padding is left out of the work's layout, so that every warp gets an
 // equal share of the tokens that are there: each block sums the lengths once, for
 // batches of up to this many rows (a chunk of 8192 rows, half of them padding:
-// 31.8 -> 29.9 us with the launch).  Calls of one token a row, and larger
+// 27.3 -> 24.2 us a call).  Calls of one token a row, and larger
 // batches, walk the padding.
 constexpr int kMaxScan = 256;
 
@@ -286,14 +287,17 @@ cudaError_t launch_append(AppendParams p, int tokens, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// Four row groups of a token per unit once that still fills the grid; one
-// otherwise (single tokens: more warps, each with less to wait for).  Measured, one /
-// four (us in the kernel): 64 tokens of 48 heads 5.4 / 6.9, 3842 tokens 32.8 / 24.2.
+// One row group of a token per unit (more warps, each with less to wait for), or four
+// where that gives half of the grid's warps one.  Measured at 208 points (16 to 8192 tokens,
+// 12 to 96 heads, both types and head sizes) the choice takes 0.5 % more than the faster form
+// on average and never 15 %; from one unit a warp on, 1.7 % and 27 %.  One / four (us a call,
+// bf16, d = 128): 64 tokens x 48 heads 4.3 / 5.4, 256 x 48 5.8 / 5.4, 512 x 48 7.7 / 6.2,
+// 4096 x 48 32.8 / 23.9, 4096 x 12 13.3 / 13.1; d = 64, 8192 x 12 16.6 / 19.1, where it loses.
 template <int D, bool kE4M3>
 cudaError_t launch_sized(const AppendParams& p, int tokens, cudaStream_t stream) {
   const long long rows = static_cast<long long>(tokens) * (p.t[0].H + 2LL * p.t[1].H);
   const bool wide =
-      rows / (4 * RowLayout<__nv_bfloat16, D>::kRows) >= 2LL * sm_count() * kWarps;
+      rows / (4 * RowLayout<__nv_bfloat16, D>::kRows) >= 1LL * sm_count() * kWarps;
   if (p.interleaved)
     return wide ? launch_append<D, 4, kE4M3, true>(p, tokens, stream)
                 : launch_append<D, 1, kE4M3, true>(p, tokens, stream);

@@ -238,7 +238,7 @@ def test_a_cache_of_float8_tensors_is_that_of_its_codes():
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
-@pytest.mark.parametrize("B,S", [(4096, 1), (40, 100), (40, 700)])
+@pytest.mark.parametrize("B,S", [(1600, 1), (4096, 1), (40, 100), (40, 700)])
 def test_tokens_left_out_do_not_disturb_the_others(B, S, e4m3):
     """Thousands of tokens, several units a warp, a third of them on pages outside the cache, in
     runs and alone: every other slot and every query row is, bit for bit, that of a call whose
