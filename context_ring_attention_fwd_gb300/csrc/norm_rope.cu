@@ -8,9 +8,10 @@
 // the load and the one rounding at the store is fp32; r is recomputed in the
 // backward, which reads x anyway, so the forward saves nothing for it.
 //
-// Bound by HBM (bf16, d = 128: 2 x 32K tokens x 32 heads backward 244 us, 97 % of the
-// copy rate; 64K x 32 forward 163 us, 97 %; 8K x 64 forward 38.5 us and backward
-// 63.5 us): a forward moves 2 d elements per row, a backward 3 d.  A warp's
+// Bound by HBM (d = 128, in the kernel: bf16, 64K tokens x 32 heads forward 164 us, 97 % of
+// the copy rate, 8K x 64 forward 41 us and backward 66 us; fp32, 8K x 32 forward 40 us; a
+// whole backward of 2 x 32K x 32 in bf16 249 us, 95 %): a forward moves 2 d elements per
+// row, a backward 3 d.  A warp's
 // unit of work is kUnroll * (rows per warp) heads of one token; while it works
 // on one, the next one's rows are on their way to its ring in shared memory
 // (kUnroll x 1 KB, the backward twice that, on top of the unit at hand).  A
@@ -21,7 +22,8 @@
 //
 // The gain's gradient: each lane sums its columns over its rows in registers,
 // the block's warps are added in shared memory, and a second kernel adds the
-// blocks' sums in block order: no atomics, so it is the same in every run.
+// blocks' sums in block order: no atomics, so it is the same in every run.  It starts
+// when the first one's last block has left (no block lets it line up earlier): 6 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -285,7 +287,7 @@ cudaError_t launch_rows(RopeParams p, int tokens, float* dqw, float* dkw, cudaSt
   constexpr int kUnitRows = kUnroll * RowLayout<T, D>::kRows;
   // A warp takes a token's units in a row, whose angles it then works out once,
   // as many as still leave every warp of the grid a few such groups (backward of
-  // 8192 tokens x 64 heads: 73.2 us one by one, 63.5 so).
+  // 8192 tokens x 64 heads: 77.4 us a call one by one, 68.2 so).
   const int most = 2 * sm_count();
   for (int per = 8;; per /= 2) {
     for (Rows& t : p.t) {

@@ -30,8 +30,8 @@
 // a cut item leaves its parts in the CTAs' slots (one for a stretch's first
 // item, one for its last).
 //
-// Measured (bf16, d = 128, pages of 16): 32 sequences of up to 16K keys, 728 MB, 113 us
-// in the kernel, 95 % of the copy rate; E4M3, 364 MB, 70 us (77 %; the widening of
+// Measured (bf16, d = 128, pages of 16): 32 sequences of up to 16K keys, 728 MB, 112 us
+// in the kernel, 96 % of the copy rate; E4M3, 364 MB, 69 us (77 %; the widening of
 // codes leaves each warp waiting for its own instructions).
 //
 // decode_join_kernel joins a row's parts and the later keys of an n_q > 1
@@ -42,8 +42,9 @@
 // in the norm: 1.77e-3 for 32 sequences of up to 16K keys, where the output's rounding
 // alone makes 1.65e-3), so what the rounding left goes through a second product in bf16:
 // the sum holds 15 bits of P (measured: 114.5 / 114.7 us a call with one / both products,
-// 91.2 / 91.6 at 128 sequences of up to 3100 keys, 70.1 / 70.8 at d = 64).  Over E4M3 caches P is fp16 alone:
-// 2^-11 of each term, an eighth of the output's rounding (1.67e-3 against 1.66e-3).
+// 91.2 / 91.6 at 128 sequences of up to 3100 keys, 70.1 / 70.8 at d = 64).  Over E4M3
+// caches P is fp16 alone: 2^-11 of each term, an eighth of the output's rounding (1.67e-3
+// against 1.66e-3).
 //
 // E4M3 caches: codes are exact in fp16, so both products run as fp16 MMAs.
 // Q is scaled per row by a power of two into fp16's range (exact but for
@@ -849,8 +850,8 @@ std::atomic<int> g_prefix_path{-1};
 // 16-row items take for them, 3.3 times for E4M3 at d = 64, which has no TMA path.
 // Up to 16 rows both read the prefix once.  Measured over 16 to 512 rows, 2 and 8 key
 // heads, 2K to 128K prefixes and pages of 64 tokens, the choice is the faster one or within
-// 2.5 us of it (16 rows under 128K, 2 key heads: 45 for 41).  Some points (us a call, items / prefix_attn_kernel, 8 key heads, 64 more
-// keys a sequence): bf16, d = 128: 32K 41 / 37 at 32 rows; 8K 21 / 22 at 32, 27 / 23 at 64;
+// 2.5 us of it (16 rows under 128K, 2 key heads: 45 for 41).  Some points (us a call,
+// items / prefix_attn_kernel, 8 key heads, 64 more keys a sequence): bf16, d = 128: 32K 41 / 37 at 32 rows; 8K 21 / 22 at 32, 27 / 23 at 64;
 // 2K 20 / 22 at 128, 26 / 25 at 192.  bf16, d = 64: 32K 28 / 29 at 32, 34 / 29 at 48.
 // E4M3, d = 128: 32K 33 / 38 at 32, 44 / 39 at 48; 8K 23 / 27 at 64, 36 / 30 at 128.  E4M3,
 // d = 64: 32K 37 / 42 at 64, 50 / 43 at 96; 128K 96 / 111 at 48, 140 / 111 at 64.

@@ -22,8 +22,9 @@
 // the rows of V behind the prefix's end are zeroed, whatever the page holds there.  Other
 // page sizes and stride orders that no tensor map describes come by cp.async
 // with the swizzle written by address, each thread ordering its finished copies
-// before the tensor core's reads with a proxy fence.  (64 sequences under a 32K prefix,
-// bf16: 37 us by TMA, 54 by cp.async; 512 rows under 128K, E4M3: 189 and 327.)
+// before the tensor core's reads with a proxy fence.  (us a call with pages of 64
+// and of 60 tokens, by TMA and by cp.async: 64 sequences under a 32K prefix, bf16, 56 and
+// 68; 512 rows under 128K, E4M3, 216 and 315.)
 //
 // P in 16 bits, as the ring forward holds it, while l sums it in fp32.  In bf16 that
 // costs as much as the output's own rounding: against 64 bits, relative in the norm,
@@ -35,7 +36,7 @@
 // Bound by shared memory and the tensor pipe alike: of a pair of 128 x 128 tiles, the
 // products take 2048 clocks, and the operands that they read (A and B of S, V) and the
 // copies that fill them 2048 clocks at 128 bytes each; a pair takes about 2900.  512 rows
-// x 8 heads under a 128K prefix: 189 us, 1450 TFLOP/s.
+// x 8 heads under a 128K prefix: 192 us, 1430 TFLOP/s.
 //
 // E4M3, d = 128, by TMA: K's codes are the operand themselves.  A bf16 q has 8
 // significant bits, so it is the sum of two E4M3 values (exactly, but for
@@ -44,7 +45,9 @@
 // lose what lies 2^-18 below its reference in such a pair, so P V runs in fp16:
 // two warps widen V's codes on their way from a ring of 16 KB to the operand
 // tile, and P is held times 2^7, which leaves it 2^31 of range.  The
-// cp.async path widens K and V both.
+// cp.async path widens K and V both and holds Q in fp16, exactly but for entries 2^-28
+// below the row's largest: the page size decides which of the two a call gets, and either
+// is within the 2^-17 of sum |q k| that a score's fp32 sum may be off by.
 //
 // Registers: launched at 168 per thread; the third warpgroup drops to 104 and
 // the softmax warpgroups rise to 200 (the build checks the launch's count).  A

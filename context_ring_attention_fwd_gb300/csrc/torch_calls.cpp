@@ -3,7 +3,8 @@
 // cp_paged_attn_decode): a Python extension that checks torch tensors, allocates
 // outputs where none are given, and calls the C ABI.  It computes nothing.
 // Against the same checks in Python over ctypes a call's host side fell from
-// 27 to 7 us (norm and rotation), 22 to 4 (append) and 41 to 10 (decode).
+// 24 to 6.5 us (norm and rotation), 41 to 12.5 (its backward), 21 to 4.3 (append) and 33
+// to 10 (decode).
 #include <ATen/ATen.h>
 #include <Python.h>
 #include <c10/cuda/CUDAGuard.h>

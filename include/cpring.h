@@ -472,7 +472,7 @@ cp_status cp_ring_attn_fwd_fp8(const void* q8, const void* k8, const void* v8t,
  *             multiple of 16 bytes, 0 allowed (CP_ERR_ALIGN otherwise).
  *  q_weight, k_weight     device fp32 [d], or NULL: that tensor is not normed.
  *  eps        >= 0, finite.
- *  inv_freq   device fp32 [rot_dim / 2]; angles are the exact products
+ *  inv_freq   device fp32 [rot_dim / 2], finite; angles are the exact products
  *             p * inv_freq modulo a turn, so far positions are as exact as
  *             near ones.  rot_dim: 0 (no rotation; inv_freq may be NULL) to
  *             d, a multiple of 16 (else CP_ERR_UNSUPPORTED).
