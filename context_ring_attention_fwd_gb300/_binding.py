@@ -3,7 +3,8 @@ the calls of a few microseconds, the extension of csrc/torch_calls.cpp.
 
 Every computation runs in the library's CUDA kernels; torch supplies device
 memory and streams.  If the library is missing the calls raise instead of
-falling back to anything else.
+falling back to anything else.  A call that is given a stream makes its own
+outputs and workspaces on it; the tensors it is given must be ready there.
 """
 from __future__ import annotations
 
