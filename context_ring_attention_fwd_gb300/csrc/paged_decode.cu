@@ -846,22 +846,26 @@ std::atomic<int> g_prefix_path{-1};
 // paged_decode_kernel read the prefix's keys and values once per 16 rows of the
 // batch, from L2 but for the first time, as fast as they compute: 0.10 to 0.19 us per
 // MB.  prefix_attn_kernel takes about 8 us longer to start and to join (80 MB of such
-// reads), and then its time is that of the prefix's own bytes: 1.4 times what
-// 16-row items take for them, 3.3 times for E4M3 at d = 64, which has no TMA path.
-// Up to 16 rows both read the prefix once.  Measured over 16 to 512 rows, 2 and 8 key
-// heads, 2K to 128K prefixes and pages of 64 tokens, the choice is the faster one or within
-// 2.5 us of it (16 rows under 128K, 2 key heads: 45 for 41).  Some points (us a call,
-// items / prefix_attn_kernel, 8 key heads, 64 more keys a sequence): bf16, d = 128: 32K 41 / 37 at 32 rows; 8K 21 / 22 at 32, 27 / 23 at 64;
-// 2K 20 / 22 at 128, 26 / 25 at 192.  bf16, d = 64: 32K 28 / 29 at 32, 34 / 29 at 48.
-// E4M3, d = 128: 32K 33 / 38 at 32, 44 / 39 at 48; 8K 23 / 27 at 64, 36 / 30 at 128.  E4M3,
-// d = 64: 32K 37 / 42 at 64, 50 / 43 at 96; 128K 96 / 111 at 48, 140 / 111 at 64.
-bool wide_prefix(long long rows, int prefix_len, int Hk, int d, int elem_bytes) {
+// reads), and then its time is that of the prefix's own bytes, as many of which by TMA
+// weigh 1.4 such reads, by cp.async 2.2 (bf16) or 3.0 (E4M3, which is widened on the
+// way; stride orders that no tensor map describes count as TMA here).  Up to 16 rows both read the prefix once.  Measured over 16 to 512 rows, 2 and 8 key
+// heads, 2K to 128K prefixes and pages of 64 (TMA) and 60 tokens (cp.async), the choice is
+// the faster one or within 3.5 us of it (16 rows under 128K, 2 key heads: 45 for 41).  Some
+// points (us a call, items / prefix_attn_kernel, 8 key heads, 64 more keys a sequence):
+//   bf16, d = 128    32K 41 / 37 at 32 rows; 8K 21 / 22 at 32, 27 / 23 at 64;
+//                    2K 20 / 22 at 128, 26 / 25 at 192; cp.async 32K 41 / 45 at 32, 55 / 46 at 48
+//   bf16, d = 64     32K 28 / 29 at 32, 34 / 29 at 48; cp.async 34 / 37 at 48, 42 / 37 at 64
+//   E4M3, d = 128    32K 33 / 38 at 32, 44 / 39 at 48; 8K 23 / 27 at 64, 36 / 30 at 128;
+//                    cp.async 32K 44 / 53 at 48, 54 / 54 at 64; 128K 133 / 150 at 48
+//   E4M3, d = 64     32K 37 / 42 at 64, 50 / 43 at 96; 128K 96 / 111 at 48, 140 / 111 at 64
+bool wide_prefix(long long rows, int prefix_len, int Hk, int d, int elem_bytes, int page_size) {
   if (prefix_len <= 0) return false;
   const int forced = g_prefix_path.load(std::memory_order_relaxed);
   if (forced >= 0) return forced != 0;
+  const bool tma = page_size % 8 == 0 && !(elem_bytes == 1 && d == 64);
   const double once = 2.0 * prefix_len * Hk * d * elem_bytes;
   const double read = static_cast<double>((rows + kRows - 1) / kRows) * once;
-  return rows > kRows && read > 80e6 + (elem_bytes == 1 && d == 64 ? 3.3 : 1.4) * once;
+  return rows > kRows && read > 80e6 + (tma ? 1.4 : elem_bytes == 2 ? 2.2 : 3.0) * once;
 }
 
 // Byte offsets of the workspace's parts.
@@ -871,8 +875,8 @@ struct Space {
     const long long rows = static_cast<long long>(B) * n_q * Hq;
     const long long slots = 2LL * kMaxGrid * kRows;
     const long long whole = prefix_len > 0 ? 2 * rows : n_q > 1 ? rows : 0;
-    const long long pslots =  // for bf16, which takes prefix_attn_kernel wherever E4M3 does
-        wide_prefix(rows / Hk, prefix_len, Hk, d, 2) ? 2LL * kMaxPrefixGrid * kPrefixRows : 0;
+    const long long pslots =  // bf16 by TMA takes prefix_attn_kernel wherever another form does
+        wide_prefix(rows / Hk, prefix_len, Hk, d, 2, 8) ? 2LL * kMaxPrefixGrid * kPrefixRows : 0;
     starts = 0;
     slot_o = align256(4LL * (B + 1));
     slot_ml = slot_o + align256(slots * d * 4);
@@ -962,7 +966,8 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
     return CP_ERR_BUFFER;
   // the units of a call are counted in 32 bits
   const long long G = Hq / Hk, R = G * n_q;
-  const bool wide = wide_prefix(B * R, prefix_len, Hk, d, cache->elem_bytes);
+  const bool wide =
+      wide_prefix(B * R, prefix_len, Hk, d, cache->elem_bytes, cache->page_size);
   const int prefix_rows = wide ? kPrefixRows : kRows, prefix_keys = wide ? kPrefixKeys : kTileKeys;
   const long long own_rt = (R + kRows - 1) / kRows;
   const long long prefix_rt = (B * R + prefix_rows - 1) / prefix_rows;

@@ -273,12 +273,16 @@ def test_keys_that_score_minus_infinity_leave_the_others(path, far):
     cut.check(out[:, :, live], lse[:, live])
 
 
-@pytest.mark.parametrize("e4m3,d,rows,wide", [
-    (False, 128, 16, False), (False, 128, 32, True), (False, 64, 32, False), (False, 64, 48, True),
-    (True, 128, 32, False), (True, 128, 48, True), (True, 64, 64, False), (True, 64, 96, True)])
-def test_the_rule_takes_the_kernel_that_measured_faster(e4m3, d, rows, wide):
-    """8 key heads under a 32K prefix, on both sides of the rule for each type and size of head."""
-    t = Case(rows // 4, 1, 32, 8, d, 64, 32768, 30, e4m3, rows)
+@pytest.mark.parametrize("e4m3,d,rows,page,wide", [
+    (False, 128, 16, 64, False), (False, 128, 32, 64, True), (False, 64, 32, 64, False),
+    (False, 64, 48, 64, True), (True, 128, 32, 64, False), (True, 128, 48, 64, True),
+    (True, 64, 64, 64, False), (True, 64, 96, 64, True), (False, 128, 32, 60, False),
+    (False, 128, 48, 60, True), (False, 64, 48, 60, False), (False, 64, 64, 60, True),
+    (True, 128, 48, 60, False), (True, 128, 96, 60, True)])
+def test_the_rule_takes_the_kernel_that_measured_faster(e4m3, d, rows, page, wide):
+    """8 key heads under a 32K prefix, on both sides of the rule for each type and size of head,
+    by TMA and by cp.async."""
+    t = Case(rows // 4, 1, 32, 8, d, page, 32768, 30, e4m3, rows)
     pkg.test_set_prefix_path(-1)
     try:
         before = pkg.launch_counts()[0]
