@@ -848,10 +848,11 @@ std::atomic<int> g_prefix_path{-1};
 // MB.  prefix_attn_kernel takes about 8 us longer to start and to join (80 MB of such
 // reads), and then its time is that of the prefix's own bytes, as many of which by TMA
 // weigh 1.4 such reads, by cp.async 2.2 (bf16) or 3.0 (E4M3, which is widened on the
-// way; stride orders that no tensor map describes count as TMA here).  Up to 16 rows both read the prefix once.  Measured over 16 to 512 rows, 2 and 8 key
-// heads, 2K to 128K prefixes and pages of 64 (TMA) and 60 tokens (cp.async), the choice is
-// the faster one or within 3.5 us of it (16 rows under 128K, 2 key heads: 45 for 41).  Some
-// points (us a call, items / prefix_attn_kernel, 8 key heads, 64 more keys a sequence):
+// way; stride orders that no tensor map describes count as TMA here).  Up to 16 rows both
+// read the prefix once.  Measured over 16 to 512 rows, 2 and 8 key heads, 2K to 128K
+// prefixes and pages of 64 (TMA) and 60 tokens (cp.async), the choice is the faster one or
+// within 3.5 us of it (16 rows under 128K, 2 key heads: 45 for 41).  Some points (us a call,
+// items / prefix_attn_kernel, 8 key heads, 64 more keys a sequence):
 //   bf16, d = 128    32K 41 / 37 at 32 rows; 8K 21 / 22 at 32, 27 / 23 at 64;
 //                    2K 20 / 22 at 128, 26 / 25 at 192; cp.async 32K 41 / 45 at 32, 55 / 46 at 48
 //   bf16, d = 64     32K 28 / 29 at 32, 34 / 29 at 48; cp.async 34 / 37 at 48, 42 / 37 at 64
