@@ -963,11 +963,12 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(seq_lens, 4) ||
       !aligned(prefix_pages, 4) || !aligned(workspace, 256) || !strides_ok(q_strides, 2))
     return CP_ERR_ALIGN;
-  if (workspace_bytes < cp_paged_attn_decode_workspace_bytes(B, n_q, Hq, Hk, d, prefix_len))
-    return CP_ERR_BUFFER;
+  const Space sp(B, n_q, Hq, Hk, d, prefix_len);
+  if (workspace_bytes < sp.total) return CP_ERR_BUFFER;
   // the units of a call are counted in 32 bits
   const long long G = Hq / Hk, R = G * n_q;
-  const bool wide =
+  const bool wide =  // and never without the space for its parts
+      sp.pslot_ml > sp.pslot_o &&
       wide_prefix(B * R, prefix_len, Hk, d, cache->elem_bytes, cache->page_size);
   const int prefix_rows = wide ? kPrefixRows : kRows, prefix_keys = wide ? kPrefixKeys : kTileKeys;
   const long long own_rt = (R + kRows - 1) / kRows;
@@ -997,7 +998,6 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
   p.lse = lse;
   p.err = device_error_word();
   if (!p.err) return CP_ERR_CUDA;
-  const Space sp(B, n_q, Hq, Hk, d, prefix_len);
   char* const ws = static_cast<char*>(workspace);
   p.starts = reinterpret_cast<unsigned*>(ws + sp.starts);
   p.slot_o = reinterpret_cast<float*>(ws + sp.slot_o);
