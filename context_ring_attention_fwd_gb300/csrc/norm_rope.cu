@@ -402,7 +402,7 @@ bool strides_distinct(const int64_t* st, int n0, int n1, int n2, int d) {
   int64_t extent = d;
   for (const Dim& x : dim) {
     if (x.n <= 1) continue;
-    if (x.stride < extent) return false;
+    if (x.stride < extent || x.stride > (1LL << 61) / x.n) return false;  // extents stay in 64 bits
     extent += x.stride * (x.n - 1);
   }
   return true;

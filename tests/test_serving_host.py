@@ -251,3 +251,12 @@ def test_one_row_of_pages_for_every_sequence_is_allowed(lib):
     assert lib.cp_paged_append(*append_args(dict(table_stride=0), rot=8)) == -3
     for bad in (-1, 7):
         assert lib.cp_paged_attn_decode(*decode_args(dict(table_stride=bad), n=1000)) == -2
+
+
+def test_strides_whose_extent_passes_64_bits_are_refused(lib):
+    """2^40 entries between 2^31 - 1 pages, and the like for a gradient's rows."""
+    far = dict(k_strides=(1 << 40, 2 * 64, 64), n_pages=0x7fffffff)
+    assert lib.cp_paged_attn_decode(*decode_args(far, n=1000)) == -2
+    assert lib.cp_paged_append(*append_args(far)) == -2
+    assert lib.cp_qk_norm_rope_bwd(*bwd_args(dqs=strides(1 << 40, 256, 64), B=1 << 23, S=16, Hq=4,
+                                             Hk=2, n=16)) == -2
