@@ -216,21 +216,23 @@ def paged_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
                  k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
                  cache_lens: torch.Tensor, new_lens=None, q_weight=None, k_weight=None,
                  inv_freq=None, eps: float = 1e-6, interleaved: bool = False, k_descale=None,
-                 v_descale=None, q_out=None, stream=None):
+                 v_descale=None, q_out=None, stream=None, k_scale=None, v_scale=None):
     """Append k, v [B,S,Hk,d] to the paged caches, k normed and rotated by its
     position, and return q normed and rotated likewise (in q_out, allocated if
-    None; its rows behind a sequence's new tokens are not written)."""
+    None; its rows behind a sequence's new tokens are not written).  With k_scale
+    and v_scale the caches hold 4 bits (see cp_paged_append)."""
     return cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens, q_weight,
                            k_weight, inv_freq, q_out, eps, interleaved, k_descale, v_descale,
-                           stream)
+                           stream, k_scale, v_scale)
 
 
 def paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                       page_table: torch.Tensor, seq_lens: torch.Tensor, prefix_pages=None,
                       prefix_len: int = 0, k_descale=None, v_descale=None, workspace=None,
-                      stream=None):
+                      stream=None, k_scale=None, v_scale=None):
     """Decode attention over the paged caches, the shared prefix attended once
     for the whole batch: allocates and returns (out [B,n_q,Hq,d] bf16, lse
-    [B,Hq,n_q] fp32)."""
+    [B,Hq,n_q] fp32).  With k_scale and v_scale the caches hold 4 bits."""
     return cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, None, None,
-                                prefix_pages, prefix_len, k_descale, v_descale, workspace, stream)
+                                prefix_pages, prefix_len, k_descale, v_descale, workspace, stream,
+                                k_scale, v_scale)

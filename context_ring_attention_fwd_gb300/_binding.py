@@ -86,7 +86,9 @@ class PagedCacheStruct(ctypes.Structure):
                 ("k_descale", _vp), ("v_descale", _vp), ("page_table", _vp),
                 ("table_stride", _i64), ("n_pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
-                ("Hk", ctypes.c_int32), ("d", ctypes.c_int32), ("elem_bytes", ctypes.c_int32)]
+                ("Hk", ctypes.c_int32), ("d", ctypes.c_int32), ("elem_bytes", ctypes.c_int32),
+                ("k_scale", _vp), ("v_scale", _vp), ("k_scale_strides", _i64 * 3),
+                ("v_scale_strides", _i64 * 3)]
 
 
 class CpError(RuntimeError):
@@ -596,16 +598,19 @@ def cp_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, posi
 
 def cp_paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens, q_weight,
                     k_weight, inv_freq, q_out, eps: float = 1e-6, interleaved: bool = False,
-                    k_descale=None, v_descale=None, stream=None):
+                    k_descale=None, v_descale=None, stream=None, k_scale=None, v_scale=None):
     """Norm, rotate and append k, v [B,S,Hk,d] bf16 (strided views allowed) to
     the paged caches [pages, page_size, Hk, d] (bf16, or float8_e4m3fn or its
     codes as uint8 with fp32 [Hk] descales) at positions cache_lens[b] + s (int32 [B]) of the table
     int32 [B, max_pages], for s < new_lens[b] (int32 [B], None: all S); q
     [B,S,Hq,d] (None: keys and values only) is normed and rotated into q_out
-    (allocated if None), which it returns."""
+    (allocated if None), which it returns.  With k_scale and v_scale [pages,
+    page_size, Hk, d / 16] (float8_e4m3fn or uint8) the caches hold 4 bits: uint8
+    [pages, page_size, Hk, d / 2], two codes a byte (the descales: ones if None)."""
     return (_ext or native()).paged_append(q, k, v, k_cache, v_cache, page_table, cache_lens,
                                            new_lens, q_weight, k_weight, inv_freq, q_out, eps,
-                                           interleaved, k_descale, v_descale, stream)
+                                           interleaved, k_descale, v_descale, stream, k_scale,
+                                           v_scale)
 
 
 def cp_paged_attn_decode_workspace_bytes(B: int, n_q: int, Hq: int, Hk: int, d: int,
@@ -615,7 +620,8 @@ def cp_paged_attn_decode_workspace_bytes(B: int, n_q: int, Hq: int, Hk: int, d: 
 
 def cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out, lse, prefix_pages=None,
                          prefix_len: int = 0, k_descale=None, v_descale=None,
-                         workspace: Optional[torch.Tensor] = None, stream=None):
+                         workspace: Optional[torch.Tensor] = None, stream=None, k_scale=None,
+                         v_scale=None):
     """Decode attention of q [B,n_q,Hq,d] bf16 (strided views allowed), the
     last n_q tokens of each sequence of seq_lens (int32 [B], 0 = unused row),
     over the paged caches of cp_paged_append; the keys of positions below
@@ -624,4 +630,4 @@ def cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out, lse, pr
     returned; workspace a uint8 device tensor (allocated here if None)."""
     return (_ext or native()).paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out,
                                                 lse, prefix_pages, prefix_len, k_descale,
-                                                v_descale, workspace, stream)
+                                                v_descale, workspace, stream, k_scale, v_scale)

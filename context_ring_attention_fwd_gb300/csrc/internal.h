@@ -165,6 +165,13 @@ cudaError_t launch_finalize_strided(const float* o_acc, const float* m_acc, cons
 int test_fault_drop();
 unsigned long long test_wait_limit_ns();
 
+// What a paged cache holds.
+enum class Held { kBf16, kE4M3, kInt4 };
+inline Held held_by(const cp_paged_cache* c) {
+  return c->elem_bytes == 2 ? Held::kBf16 : c->elem_bytes == 1 ? Held::kE4M3 : Held::kInt4;
+}
+constexpr int kBlock = 16;  // entries of a 4-bit row that share a scale
+
 // Caller-given strides (three, in elements, of the dimensions before the
 // contiguous last one; null = contiguous): each a non-negative multiple of 16
 // bytes; and, for written tensors, that no two elements share an address

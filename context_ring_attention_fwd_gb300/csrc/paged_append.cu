@@ -5,8 +5,9 @@
 // Token s of sequence b has the position p = cache_lens[b] + s and goes to
 // slot p % page_size of page page_table[b][p / page_size].  K is normed and
 // rotated in fp32 (rope.cuh) and rounded once, to what the cache holds: bf16,
-// or the E4M3 code of x times the reciprocal of descale[head] (in fp32, as
-// cp_fp8_quantize multiplies by its inverse scale).
+// the E4M3 code of x times the reciprocal of descale[head] (in fp32, as
+// cp_fp8_quantize multiplies by its inverse scale), or codes in 4 bits with an
+// E4M3 scale to each 16 entries (codes4).
 //
 // Bound by latency.  Single tokens (64 of them: 4.3 us a call) by the launch; prefill
 // chunks (3842 tokens of 32 + 8 + 8 heads: 25.7 us in the kernel to E4M3, 25.0 to bf16,
@@ -17,10 +18,12 @@
 // stride costs the same; the next unit's rows are on their way meanwhile
 // (norm_rope.cu).
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "rope.cuh"
@@ -43,7 +46,9 @@ struct AppendParams {
   __nv_bfloat16* q_out;
   void* cache[2];            // k, v
   long long cs[2][3];        // their strides: page, token, head
-  const float* descale[2];   // [Hk], E4M3 caches
+  const float* descale[2];   // [Hk], E4M3 caches; 4 bits: or null (ones)
+  uint8_t* scales[2];        // 4 bits
+  long long ss[2][3];        // their strides: page, token, head
   const int32_t* table;
   const int32_t* cache_lens;
   const int32_t* new_lens;
@@ -78,7 +83,60 @@ __device__ __forceinline__ uint2 codes8(const f32x2 (&z)[NP], int at, f32x2 inv)
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-template <int D, int kUnroll, bool kE4M3, bool kInterleaved>
+// ---- 4 bits.  The 16 entries of a block are two of a row's 8-entry vectors, 2 x and
+// 2 x + 1.  A lane holds two vectors: neighbours, or, where a pair's halves are rotated
+// together, two that lie rot / 2 apart; then a block's vectors meet by shuffles.
+
+// The lane of a row and the slot (0 lo, 1 hi) that hold vector v.
+__device__ __forceinline__ void holder_of(int v, int rot, bool interleaved, int& lane, int& slot) {
+  const bool apart = !interleaved && v * 8 < rot;
+  const int half = rot / 16;
+  slot = apart ? v >= half : v & 1;
+  lane = apart ? v - slot * half : v / 2;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+template <int NP>
+__device__ __forceinline__ float largest8(const f32x2 (&y)[NP], int at) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack2(y[at + i], lo, hi);
+    m = max_nan(m, max_nan(fabsf(lo), fabsf(hi)));
+  }
+  return m;
+}
+
+// The codes of 8 entries for a block's scale s, r = 1 / s rounded to nearest (0 for s = 0):
+// round(y / s) + 8.  |y| is brought to 7 s first; then q = y r, corrected once by its
+// remainder, is the quotient rounded to nearest (Markstein, IBM J. Res. Dev. 34, 1990: for
+// a correctly rounded r), so ties are those of y / s.  Adding 1.5 2^23 + 8 rounds q to a whole
+// number (ties to even) and leaves q + 8 in the sum's low bits.
+template <int NP>
+__device__ __forceinline__ uint32_t codes4(const f32x2 (&y)[NP], int at, float s, float r) {
+  const float most = 7.f * s;
+  const f32x2 minus_s = pack2(-s, -s), r2 = pack2(r, r);
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack2(y[at + i], lo, hi);
+    const f32x2 x = pack2(fminf(fmaxf(lo, -most), most), fminf(fmaxf(hi, -most), most));
+    const f32x2 q = mul2(x, r2);
+    unpack2(fma2(fma2(q, minus_s, x), r2, q), lo, hi);
+    w |= (__float_as_uint(lo + 12582920.f) & 15u) << (8 * i);
+    w |= (__float_as_uint(hi + 12582920.f) & 15u) << (8 * i + 4);
+  }
+  return w;
+}
+
+template <int D, int kUnroll, Held kHeld, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, 2) paged_append_kernel(const AppendParams p) {
   using T = __nv_bfloat16;
   using Lay = RowLayout<T, D>;
@@ -96,6 +154,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_append_kernel(const AppendP
   int lo, hi;
   bool turned;
   lane_columns<NP>(l, p.rot, kInterleaved, lo, hi, turned);
+  // 4 bits: where the other vectors of the lane's two blocks are
+  int mate[2] = {0, 0}, mate_slot[2] = {0, 0};
+  if (kHeld == Held::kInt4) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      holder_of(((e ? hi : lo) / 8) ^ 1, p.rot, kInterleaved, mate[e], mate_slot[e]);
+      mate[e] += g * Lay::kLanes;
+    }
+  }
 
   // `tells`: this call reports a length that is out of range (some call of each row's does).
   auto new_len = [&](int b, bool tells) {
@@ -247,6 +314,22 @@ __global__ void __launch_bounds__(kThreads, 2) paged_append_kernel(const AppendP
 #pragma unroll
         for (int e = 0; e < NP; ++e) z[e] = mul2(z[e], r2);
       }
+      const int kv = x.kind - 1;
+      float s4[2];  // the scales of the lane's two blocks
+      if (kHeld == Held::kInt4 && x.kind != 0) {
+        if (p.descale[kv] != nullptr) {
+          const float inv = __frcp_rn(__ldg(p.descale[kv] + min(h, t.H - 1)));
+#pragma unroll
+          for (int e = 0; e < NP; ++e) z[e] = mul2(z[e], pack2(inv, inv));
+        }
+        const float m[2] = {largest8<NP>(z, 0), largest8<NP>(z, NP / 2)};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float a = __shfl_sync(0xffffffffu, m[0], mate[e]);
+          const float b = __shfl_sync(0xffffffffu, m[1], mate[e]);
+          s4[e] = max_nan(m[e], mate_slot[e] ? b : a) * (1.f / 7.f);
+        }
+      }
       if (h >= t.H) continue;
       if (x.kind == 0) {
         T* const dst = p.q_out + (static_cast<long long>(x.tok) * t.H + h) * D;
@@ -254,9 +337,24 @@ __global__ void __launch_bounds__(kThreads, 2) paged_append_kernel(const AppendP
         *reinterpret_cast<uint4*>(dst + hi) = repack<NP>(z, NP / 2, T());
         continue;
       }
-      const int kv = x.kind - 1;
       const long long off = x.page * p.cs[kv][0] + x.slot * p.cs[kv][1] + h * p.cs[kv][2];
-      if (kE4M3) {
+      if (kHeld == Held::kInt4) {
+        uint8_t* const dst = static_cast<uint8_t*>(p.cache[kv]) + off;
+        uint8_t* const sdst =
+            p.scales[kv] + x.page * p.ss[kv][0] + x.slot * p.ss[kv][1] + h * p.ss[kv][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = e ? hi : lo;
+          uint16_t code;
+          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(code) : "f"(0.f), "f"(s4[e]));
+          uint32_t half2;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(code));
+          const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(half2)));
+          const uint32_t w = codes4<NP>(z, e * (NP / 2), s, s > 0.f ? __frcp_rn(s) : 0.f);
+          *reinterpret_cast<uint32_t*>(dst + col / 2) = w;
+          if (col % kBlock == 0) sdst[col / kBlock] = static_cast<uint8_t>(code);
+        }
+      } else if (kHeld == Held::kE4M3) {
         uint8_t* const dst = static_cast<uint8_t*>(p.cache[kv]) + off;
         const float inv = __frcp_rn(__ldg(p.descale[kv] + h));
         *reinterpret_cast<uint2*>(dst + lo) = codes8<NP>(z, 0, pack2(inv, inv));
@@ -270,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_append_kernel(const AppendP
   }
 }
 
-template <int D, int kUnroll, bool kE4M3, bool kInterleaved>
+template <int D, int kUnroll, Held kHeld, bool kInterleaved>
 cudaError_t launch_append(AppendParams p, int tokens, cudaStream_t stream) {
   constexpr int kUnitRows = kUnroll * RowLayout<__nv_bfloat16, D>::kRows;
   for (NewRows& t : p.t) t.chunks = (t.H + kUnitRows - 1) / kUnitRows;
@@ -279,7 +377,7 @@ cudaError_t launch_append(AppendParams p, int tokens, cudaStream_t stream) {
   const int units = tokens * (p.t[0].chunks + p.t[1].chunks + p.t[2].chunks);
   const int blocks = std::min((units + kWarps - 1) / kWarps, 2 * sm_count());
   constexpr int kSmem = kWarps * Ring<kUnroll * 2>::kBytes;
-  const auto kern = paged_append_kernel<D, kUnroll, kE4M3, kInterleaved>;
+  const auto kern = paged_append_kernel<D, kUnroll, kHeld, kInterleaved>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kSmem);
   if (e != cudaSuccess) return e;
   kern<<<blocks, kThreads, kSmem, stream>>>(p);
@@ -293,16 +391,16 @@ cudaError_t launch_append(AppendParams p, int tokens, cudaStream_t stream) {
 // on average and never 15 %; from one unit a warp on, 1.7 % and 27 %.  One / four (us a call,
 // bf16, d = 128): 64 tokens x 48 heads 4.3 / 5.4, 256 x 48 5.8 / 5.4, 512 x 48 7.7 / 6.2,
 // 4096 x 48 32.8 / 23.9, 4096 x 12 13.3 / 13.1; d = 64, 8192 x 12 16.6 / 19.1, where it loses.
-template <int D, bool kE4M3>
+template <int D, Held kHeld>
 cudaError_t launch_sized(const AppendParams& p, int tokens, cudaStream_t stream) {
   const long long rows = static_cast<long long>(tokens) * (p.t[0].H + 2LL * p.t[1].H);
   const bool wide =
       rows / (4 * RowLayout<__nv_bfloat16, D>::kRows) >= 1LL * sm_count() * kWarps;
   if (p.interleaved)
-    return wide ? launch_append<D, 4, kE4M3, true>(p, tokens, stream)
-                : launch_append<D, 1, kE4M3, true>(p, tokens, stream);
-  return wide ? launch_append<D, 4, kE4M3, false>(p, tokens, stream)
-              : launch_append<D, 1, kE4M3, false>(p, tokens, stream);
+    return wide ? launch_append<D, 4, kHeld, true>(p, tokens, stream)
+                : launch_append<D, 1, kHeld, true>(p, tokens, stream);
+  return wide ? launch_append<D, 4, kHeld, false>(p, tokens, stream)
+              : launch_append<D, 1, kHeld, false>(p, tokens, stream);
 }
 
 void take_strides(const int64_t* given, int S, int H, int d, NewRows& t) {
@@ -315,7 +413,9 @@ void take_strides(const int64_t* given, int S, int H, int d, NewRows& t) {
 
 cp_status check_cache(const cp_paged_cache* c) {
   if (!c || !c->k || !c->v || !c->page_table) return CP_ERR_NULL;
-  if (c->elem_bytes != 1 && c->elem_bytes != 2) return CP_ERR_UNSUPPORTED;
+  if (c->elem_bytes != 1 && c->elem_bytes != 2 && c->elem_bytes != -2) return CP_ERR_UNSUPPORTED;
+  const bool int4 = held_by(c) == Held::kInt4;
+  if (int4 && (!c->k_scale || !c->v_scale)) return CP_ERR_NULL;
   if (c->elem_bytes == 1 && (!c->k_descale || !c->v_descale)) return CP_ERR_NULL;
   if (c->d != 64 && c->d != 128) return CP_ERR_UNSUPPORTED;
   if (c->n_pages < 1 || c->page_size < 1 || c->max_pages < 1 || c->Hk < 1 || c->Hk > 65535 ||
@@ -325,11 +425,21 @@ cp_status check_cache(const cp_paged_cache* c) {
   if (static_cast<long long>(c->max_pages) * c->page_size > (1LL << 30)) return CP_ERR_SHAPE;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4) ||
       !aligned(c->k_descale, 4) || !aligned(c->v_descale, 4) ||
-      !strides_ok(c->k_strides, c->elem_bytes) || !strides_ok(c->v_strides, c->elem_bytes))
+      !strides_ok(c->k_strides, int4 ? 1 : c->elem_bytes) ||
+      !strides_ok(c->v_strides, int4 ? 1 : c->elem_bytes))
     return CP_ERR_ALIGN;
-  if (!strides_distinct(c->k_strides, c->n_pages, c->page_size, c->Hk, c->d) ||
-      !strides_distinct(c->v_strides, c->n_pages, c->page_size, c->Hk, c->d))
+  const int row = int4 ? c->d / 2 : c->d;  // in the strides' units
+  if (!strides_distinct(c->k_strides, c->n_pages, c->page_size, c->Hk, row) ||
+      !strides_distinct(c->v_strides, c->n_pages, c->page_size, c->Hk, row))
     return CP_ERR_SHAPE;
+  if (!int4) return CP_OK;
+  const int scales = c->d / kBlock;
+  if (!aligned(c->k_scale, 8) || !aligned(c->v_scale, 8)) return CP_ERR_ALIGN;
+  for (const int64_t* st : {c->k_scale_strides, c->v_scale_strides}) {
+    for (int i = 0; i < 3; ++i)
+      if (st[i] < 0 || st[i] > (1LL << 40) || st[i] % scales != 0) return CP_ERR_ALIGN;
+    if (!strides_distinct(st, c->n_pages, c->page_size, c->Hk, scales)) return CP_ERR_SHAPE;
+  }
   return CP_OK;
 }
 
@@ -378,17 +488,28 @@ extern "C" cp_status cp_paged_append(const cp_paged_cache* cache, const void* q,
     p.cs[1][i] = cache->v_strides[i];
   }
   p.descale[0] = cache->k_descale; p.descale[1] = cache->v_descale;
+  const Held held = held_by(cache);
+  if (held == Held::kInt4) {
+    p.scales[0] = static_cast<uint8_t*>(cache->k_scale);
+    p.scales[1] = static_cast<uint8_t*>(cache->v_scale);
+    for (int i = 0; i < 3; ++i) {
+      p.ss[0][i] = cache->k_scale_strides[i];
+      p.ss[1][i] = cache->v_scale_strides[i];
+    }
+  }
   p.table = cache->page_table; p.table_stride = cache->table_stride;
   p.cache_lens = cache_lens; p.new_lens = new_lens; p.inv_freq = inv_freq;
   p.err = device_error_word();
   if (!p.err) return CP_ERR_CUDA;
   p.n_pages = cache->n_pages; p.page_size = cache->page_size; p.max_pages = cache->max_pages;
   p.B = B; p.S = S; p.rot = rot_dim; p.interleaved = interleaved; p.eps = eps;
-  const bool e4m3 = cache->elem_bytes == 1;
-  const cudaError_t e =
-      d == 128 ? (e4m3 ? launch_sized<128, true>(p, B * S, stream)
-                       : launch_sized<128, false>(p, B * S, stream))
-               : (e4m3 ? launch_sized<64, true>(p, B * S, stream)
-                       : launch_sized<64, false>(p, B * S, stream));
+  auto launch = [&](auto dim) {
+    constexpr int kD = decltype(dim)::value;
+    return held == Held::kBf16   ? launch_sized<kD, Held::kBf16>(p, B * S, stream)
+           : held == Held::kE4M3 ? launch_sized<kD, Held::kE4M3>(p, B * S, stream)
+                                 : launch_sized<kD, Held::kInt4>(p, B * S, stream);
+  };
+  const cudaError_t e = d == 128 ? launch(std::integral_constant<int, 128>())
+                                 : launch(std::integral_constant<int, 64>());
   return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }

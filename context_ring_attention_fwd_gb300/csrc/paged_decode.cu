@@ -85,17 +85,23 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 // One warp's part of a pipeline stage: 16 rows of K, then 16 of V, as 16-byte
 // chunks; chunk c of row r at c ^ (r mod 8) (mod 4 for rows of 64 bytes), so
-// that both ldmatrix and the row-wise reads of codes are conflict-free.
-template <int D, bool kE4M3>
+// that both ldmatrix and the row-wise reads of codes are conflict-free.  Rows in 4 bits
+// (64 or 32 bytes, two or four to a line of the banks) move their chunks every second or
+// fourth row, and the 16 rows' scales of K, then of V, lie behind them.
+template <int D, Held kHeld>
 struct Stage {
-  static constexpr int kRowBytes = D * (kE4M3 ? 1 : 2);
+  static constexpr int kRowBytes = kHeld == Held::kBf16 ? 2 * D : kHeld == Held::kE4M3 ? D : D / 2;
+  static constexpr int kScaleBytes = D / kBlock;  // of a row in 4 bits
   static constexpr int kChunks = kRowBytes / 16;
-  static constexpr int kBytes = 2 * kWarpKeys * kRowBytes;
+  static constexpr int kV = kWarpKeys * kRowBytes;  // where V starts
+  static constexpr int kScales = 2 * kV;            // and the scales
+  static constexpr int kBytes = kScales + (kHeld == Held::kInt4 ? 2 * kWarpKeys * kScaleBytes : 0);
   static constexpr int kCount = kBytes >= 8192 ? 2 : 4;
   static constexpr int kRing = kCount * kBytes;  // per warp
-  static constexpr int kSwz = kChunks >= 8 ? 7 : 3;
+  static constexpr int kSwz = kHeld == Held::kInt4 ? kChunks - 1 : kChunks >= 8 ? 7 : 3;
+  static constexpr int kSwzRows = kHeld == Held::kInt4 ? 8 / kChunks : 1;
   __device__ static uint32_t at(uint32_t base, int row, int chunk) {
-    return base + row * kRowBytes + ((chunk ^ (row & kSwz)) << 4);
+    return base + row * kRowBytes + ((chunk ^ (row / kSwzRows & kSwz)) << 4);
   }
 };
 
@@ -158,12 +164,29 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-template <int D, bool kE4M3>
+// What a head's codes are multiplied by (x: 0 K, 1 V).
+template <Held kHeld>
+__device__ __forceinline__ float head_descale(const DecodeParams& p, int x, int hk) {
+  if (kHeld == Held::kBf16 || (kHeld == Held::kInt4 && p.descale[x] == nullptr)) return 1.f;
+  return __ldg(p.descale[x] + hk);
+}
+
+// kBytes (4 or 8) to shared memory, or zeros.
+template <int kBytes>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? kBytes : 0), "n"(kBytes)
+               : "memory");
+}
+
+template <int D, Held kHeld>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const DecodeParams p) {
-  using St = Stage<D, kE4M3>;
+  using St = Stage<D, kHeld>;
+  constexpr bool kE4M3 = kHeld == Held::kE4M3, kInt4 = kHeld == Held::kInt4;
   constexpr int kK = D / 16;   // k-steps of S = Q K^T
   constexpr int kN = D / 8;    // 8-column tiles of O
-  constexpr float kShift = kE4M3 ? 15.f : 0.f;  // P is held times 2^kShift
+  constexpr bool kF16 = kE4M3 || kInt4;         // both products in fp16
+  constexpr float kShift = kF16 ? 15.f : 0.f;   // P is held times 2^kShift
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ unsigned scan[kWarps];
   __shared__ float merge_ml[kWarps][kRows][2];
@@ -289,9 +312,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
           for (int i = 0; i < kWarpKeys / kPerStep; ++i) {
             const int key = i * kPerStep + lane / St::kChunks;
             const long long o = __shfl_sync(0xffffffffu, off[x], key);
-            cp_async16(St::at(dst + x * (St::kBytes / 2), key, chunk),
+            cp_async16(St::at(dst + x * St::kV, key, chunk),
                        p.cache[x] + o + chunk * 16, (held >> key & 1u) ? 16 : 0);
           }
+        }
+        if (kInt4) {  // lane l: the scales of key l % 16, of K or of V
+          const int key = lane % kWarpKeys, x = lane / kWarpKeys;
+          const int page = __shfl_sync(0xffffffffu, at.page, key);
+          const int slot = __shfl_sync(0xffffffffu, at.slot, key);
+          const bool there = held >> key & 1u;
+          const long long o = there ? page * p.ss[x][0] + slot * p.ss[x][1] + hk * p.ss[x][2] : 0;
+          cp_async_small<St::kScaleBytes>(
+              dst + St::kScales + (x * kWarpKeys + key) * St::kScaleBytes, p.scales[x] + o, there);
         }
       }
       cp_commit();
@@ -313,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       const RowOf r1(p, b0, hk, min(row0 + quad + 8, row0 + rows - 1));
       const __nv_bfloat16* const q0 = r0.query(p);
       const __nv_bfloat16* const q1 = r1.query(p);
-      if (!kE4M3) {
+      if (!kF16) {
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
           qf[k][0] = *reinterpret_cast<const uint32_t*>(q0 + k * 16 + c4 * 2);
@@ -324,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       } else {
         // The order of a dot product's terms is free: lane c4 takes the D / 4
         // neighbouring columns from c4 * D / 4 on, in Q as in the codes of K.
-        const float desc = __ldg(p.descale[0] + hk);
+        const float desc = head_descale<kHeld>(p, 0, hk);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const uint4* const src =
@@ -348,8 +380,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
           (x ? sc1 : sc0) = p.scale * desc * down;
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
-            qf[k][x] = pack_f16(z[4 * k] * up, z[4 * k + 1] * up);
-            qf[k][2 + x] = pack_f16(z[4 * k + 2] * up, z[4 * k + 3] * up);
+            // 4 bits: a word's codes i and i + 4 come as a pair
+            const int at = kInt4 ? 8 * (k / 2) + 2 * (k % 2) : 4 * k;
+            constexpr int kNext = kInt4 ? 4 : 1, kSecond = kInt4 ? 1 : 2;
+            qf[k][x] = pack_f16(z[at] * up, z[at + kNext] * up);
+            qf[k][2 + x] = pack_f16(z[at + kSecond] * up, z[at + kSecond + kNext] * up);
           }
         }
       }
@@ -366,13 +401,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       load(t + St::kCount - 1, stage == 0 ? St::kCount - 1 : stage - 1, next);
       next = look_up(t + St::kCount);
       const uint32_t ks = ring + stage * St::kBytes;
-      const uint32_t vs = ks + St::kBytes / 2;
+      const uint32_t vs = ks + St::kV;
       if (++stage == St::kCount) stage = 0;
       // ---- S: two 8-key tiles
       float s[2][4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-      if (!kE4M3) {
+      if (kInt4) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int row = j * 8 + quad;
+          uint32_t u[D / 32], two;  // the lane's quarter of the row, and its scales
+          if constexpr (D == 128)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                         : "r"(St::at(ks, row, c4)));
+          else
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                         : "=r"(u[0]), "=r"(u[1])
+                         : "r"(St::at(ks, row, c4 / 2) + c4 % 2 * 8));
+          const uint32_t at = ks + St::kScales + row * St::kScaleBytes;
+          if constexpr (D == 128)
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(two) : "r"(at + 2 * c4));
+          else
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(two) : "r"(at + c4));
+          two = half2_of_codes(two);
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {  // two words to a block of 16
+            const uint32_t sc = __byte_perm(two, 0, x < 2 ? 0x1010 : 0x3232);
+            uint32_t v[4];
+            widen4(u[x], sc, scale_offset(sc), v);
+            mma16816<true>(s[j], qf[2 * x], v[0], v[1]);
+            mma16816<true>(s[j], qf[2 * x + 1], v[2], v[3]);
+          }
+        }
+      } else if (!kE4M3) {
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
           uint32_t b[4];
@@ -439,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       }
       uint32_t pf[4];
       uint32_t pe[4];  // bf16: what the upper half of P leaves
-      if (kE4M3) {
+      if (kF16) {
         pf[0] = pack_f16(pr[0][0], pr[0][1]);
         pf[1] = pack_f16(pr[0][2], pr[0][3]);
         pf[2] = pack_f16(pr[1][0], pr[1][1]);
@@ -457,11 +520,46 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
         }
       }
       // ---- O += P V
+      uint32_t vsc[kInt4 ? D / 64 : 1][4];  // scales as half pairs of keys: chunks 2 x (lo, hi), 2 x + 1
+      if constexpr (kInt4) {
+        // the words of this lane's keys 2 c4 and 2 c4 + 1 (y = 0), and of the two 8 further (1)
+        constexpr int kWords = D / 64;
+        const uint32_t pick = 0x6240u + 0x1111u * (quad >> 2);  // a chunk's columns 16 on: the odd
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t at = ks + St::kScales + (kWarpKeys + 8 * y + 2 * c4) * St::kScaleBytes;
+          uint32_t r[2 * kWords];
+          if constexpr (D == 128)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                         : "r"(at));
+          else
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at));
+#pragma unroll
+          for (int x = 0; x < kWords; ++x) {
+            const uint32_t c = __byte_perm(r[x], r[kWords + x], pick);
+            vsc[x][y] = half2_of_codes(c & 0xffffu);
+            vsc[x][2 + y] = half2_of_codes(c >> 16);
+          }
+        }
+      }
 #pragma unroll
       for (int ch = 0; ch < St::kChunks; ch += 2) {
         uint32_t b[4];
         ldsm4_t(St::at(vs, ((lane >> 3) & 1) * 8 + (lane & 7), ch + (lane >> 4)), b);
-        if (!kE4M3) {
+        if constexpr (kInt4) {
+          // A 16-bit element is four neighbouring columns: code i of each makes an
+          // 8-column tile.
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t lo[4], hi[4];
+            const uint32_t s0 = vsc[ch / 2][2 * x], s1 = vsc[ch / 2][2 * x + 1];
+            widen4(b[2 * x], s0, scale_offset(s0), lo);
+            widen4(b[2 * x + 1], s1, scale_offset(s1), hi);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma16816<true>(o[4 * (ch + x) + i], pf, lo[i], hi[i]);
+          }
+        } else if (!kE4M3) {
           mma16816<false>(o[ch], pf, b[0], b[1]);
           mma16816<false>(o[ch + 1], pf, b[2], b[3]);
           mma16816<false>(o[ch], pe, b[0], b[1]);
@@ -507,7 +605,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       const float f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - big1);
       float* const w0 = mo + (warp * kRows + quad) * kPitch;
       float* const w1 = w0 + 8 * kPitch;
-      if (!kE4M3) {
+      if (kInt4) {
+#pragma unroll
+        for (int ch = 0; ch < kN / 4; ++ch)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float(&a)[4] = o[4 * ch], (&b)[4] = o[4 * ch + 1], (&c)[4] = o[4 * ch + 2],
+                       (&d)[4] = o[4 * ch + 3];
+            const int col = ch * 32 + c4 * 8 + e * 4;
+            *reinterpret_cast<float4*>(w0 + col) =
+                make_float4(a[e] * f0, b[e] * f0, c[e] * f0, d[e] * f0);
+            *reinterpret_cast<float4*>(w1 + col) =
+                make_float4(a[2 + e] * f1, b[2 + e] * f1, c[2 + e] * f1, d[2 + e] * f1);
+          }
+      } else if (!kE4M3) {
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
           *reinterpret_cast<float2*>(w0 + n * 8 + c4 * 2) = make_float2(o[n][0] * f0, o[n][1] * f0);
@@ -528,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     __syncthreads();
     const bool complete = t0 == 0 && static_cast<unsigned>(t1) == n_tiles;
     const bool direct = complete && !prefix && p.P == 0 && p.n_q == 1;
-    const float vd = kE4M3 ? __ldg(p.descale[1] + hk) : 1.f;
+    const float vd = head_descale<kHeld>(p, 1, hk);
     constexpr int kVecs = D / 4;  // 4-column vectors of a row
     for (int x = threadIdx.x; x < rows * kVecs; x += kThreads) {
       const int r = x / kVecs, col = (x % kVecs) * 4;
@@ -597,10 +708,19 @@ struct Parts {
   }
 };
 
-// A lane's kCols columns of a cached row.
-template <int kCols, bool kE4M3>
-__device__ __forceinline__ void load_columns(const uint8_t* row, int lane, float (&v)[kCols]) {
-  if (kE4M3) {
+// A lane's kCols columns of a cached row (in 4 bits: and its row of scales).
+template <int kCols, Held kHeld>
+__device__ __forceinline__ void load_columns(const uint8_t* row, const uint8_t* scales, int lane,
+                                             float (&v)[kCols]) {
+  if (kHeld == Held::kInt4) {
+    const uint32_t u = kCols == 4 ? __ldg(reinterpret_cast<const unsigned short*>(row) + lane)
+                                  : __ldg(row + lane);
+    const uint32_t h = half2_of_codes(__ldg(scales + lane * kCols / kBlock));
+    const float s = __low2float(*reinterpret_cast<const __half2*>(&h));
+#pragma unroll
+    for (int x = 0; x < kCols; ++x)
+      v[x] = static_cast<float>(static_cast<int>(u >> (4 * x) & 15u) - 8) * s;
+  } else if (kHeld == Held::kE4M3) {
     uint32_t u;
     if (kCols == 4)
       u = __ldg(reinterpret_cast<const unsigned*>(row) + lane);
@@ -631,7 +751,7 @@ __device__ __forceinline__ void load_columns(const uint8_t* row, int lane, float
 
 // kRowWarps warps join a row: four where rows are few (their parts' loads run side
 // by side), one where there are enough rows to fill the GPU.
-template <int D, bool kE4M3, int kRowWarps>
+template <int D, Held kHeld, int kRowWarps>
 __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParams p, unsigned grid) {
   constexpr int kCols = D / 32;  // columns per lane
   __shared__ float part_m[kWarps], part_l[kWarps];
@@ -684,7 +804,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
     }
     pre.r = row % p.prefix_rows;
     const int tile = row / p.prefix_rows;
-    const int item = wide ? prefix_item<kE4M3>(p, hk, tile) : hk * p.prefix_row_tiles + tile;
+    const int item = wide ? prefix_item<kHeld == Held::kE4M3>(p, hk, tile) : hk * p.prefix_row_tiles + tile;
     pre.find(item * units, n,
              wide ? units * static_cast<unsigned>(p.Hk * p.prefix_row_tiles) : W,
              wide ? static_cast<unsigned>(p.prefix_grid) : g);
@@ -749,10 +869,10 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
   bool bad = false;
   if (pos0 <= pos1) {
     float q[kCols];
-    load_columns<kCols, false>(
-        reinterpret_cast<const uint8_t*>(p.q + b * p.qb + i * p.qs + h * p.qh), lane, q);
-    const float kd = kE4M3 ? __ldg(p.descale[0] + hk) * p.scale : p.scale;
-    const float vd = kE4M3 ? __ldg(p.descale[1] + hk) : 1.f;
+    load_columns<kCols, Held::kBf16>(
+        reinterpret_cast<const uint8_t*>(p.q + b * p.qb + i * p.qs + h * p.qh), nullptr, lane, q);
+    const float kd = head_descale<kHeld>(p, 0, hk) * p.scale;
+    const float vd = head_descale<kHeld>(p, 1, hk);
     for (int first = pos0 + warp; first <= pos1; first += kRowWarps * kKeys) {
       int page[kKeys], slot[kKeys];
 #pragma unroll
@@ -776,10 +896,12 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
 #pragma unroll
         for (int y = 0; y < kCols; ++y) key[k][y] = value[k][y] = 0.f;
         if (page[k] >= 0) {
-          load_columns<kCols, kE4M3>(p.cache[0] + page[k] * p.cs[0][0] + slot[k] * p.cs[0][1] +
-                                         hk * p.cs[0][2], lane, key[k]);
-          load_columns<kCols, kE4M3>(p.cache[1] + page[k] * p.cs[1][0] + slot[k] * p.cs[1][1] +
-                                         hk * p.cs[1][2], lane, value[k]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            load_columns<kCols, kHeld>(
+                p.cache[x] + page[k] * p.cs[x][0] + slot[k] * p.cs[x][1] + hk * p.cs[x][2],
+                p.scales[x] + page[k] * p.ss[x][0] + slot[k] * p.ss[x][1] + hk * p.ss[x][2], lane,
+                x ? value[k] : key[k]);
         }
       }
       float2 ml[kKeys];
@@ -889,22 +1011,22 @@ struct Space {
   }
 };
 
-template <int D, bool kE4M3>
+template <int D, Held kHeld>
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
-  using St = Stage<D, kE4M3>;
+  using St = Stage<D, kHeld>;
   static_assert(kWarps * St::kRing >= kWarps * kRows * (D + 8) * 4, "the join fits the ring");
   const int smem = kWarps * St::kRing + 4 * (p.B + 1);
   const int most = kWarps * St::kRing + 4 * (kMaxBatch + 1);
   cudaError_t e = ensure_smem_limit(
-      reinterpret_cast<const void*>(&paged_decode_kernel<D, kE4M3>), most);
+      reinterpret_cast<const void*>(&paged_decode_kernel<D, kHeld>), most);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(std::min(kMaxGrid, kCtasPerSm * sm_count()));
-  paged_decode_kernel<D, kE4M3><<<grid, kThreads, smem, stream>>>(p);
+  paged_decode_kernel<D, kHeld><<<grid, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   count_launch(2);
   if (p.prefix_grid > 0) {
-    e = launch_prefix_attn(p, D, kE4M3, stream);
+    e = launch_prefix_attn(p, D, kHeld == Held::kE4M3, stream);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute at{};
@@ -918,8 +1040,8 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  e = many ? cudaLaunchKernelEx(&cfg, decode_join_kernel<D, kE4M3, 1>, p, grid)
-           : cudaLaunchKernelEx(&cfg, decode_join_kernel<D, kE4M3, kWarps>, p, grid);
+  e = many ? cudaLaunchKernelEx(&cfg, decode_join_kernel<D, kHeld, 1>, p, grid)
+           : cudaLaunchKernelEx(&cfg, decode_join_kernel<D, kHeld, kWarps>, p, grid);
   count_launch(2);
   return e;
 }
@@ -968,7 +1090,7 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
   // the units of a call are counted in 32 bits
   const long long G = Hq / Hk, R = G * n_q;
   const bool wide =  // and never without the space for its parts
-      sp.pslot_ml > sp.pslot_o &&
+      cache->elem_bytes > 0 && sp.pslot_ml > sp.pslot_o &&
       wide_prefix(B * R, prefix_len, Hk, d, cache->elem_bytes, cache->page_size);
   const int prefix_rows = wide ? kPrefixRows : kRows, prefix_keys = wide ? kPrefixKeys : kTileKeys;
   const long long own_rt = (R + kRows - 1) / kRows;
@@ -984,9 +1106,18 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.cache[0] = static_cast<const uint8_t*>(cache->k);
   p.cache[1] = static_cast<const uint8_t*>(cache->v);
-  for (int i = 0; i < 3; ++i) {
-    p.cs[0][i] = cache->k_strides[i] * cache->elem_bytes;
-    p.cs[1][i] = cache->v_strides[i] * cache->elem_bytes;
+  const Held held = held_by(cache);
+  for (int i = 0; i < 3; ++i) {  // in bytes
+    const int unit = held == Held::kBf16 ? 2 : 1;
+    p.cs[0][i] = cache->k_strides[i] * unit;
+    p.cs[1][i] = cache->v_strides[i] * unit;
+    if (held != Held::kInt4) continue;
+    p.ss[0][i] = cache->k_scale_strides[i];
+    p.ss[1][i] = cache->v_scale_strides[i];
+  }
+  if (held == Held::kInt4) {
+    p.scales[0] = static_cast<const uint8_t*>(cache->k_scale);
+    p.scales[1] = static_cast<const uint8_t*>(cache->v_scale);
   }
   p.descale[0] = cache->k_descale;
   p.descale[1] = cache->v_descale;
@@ -1024,11 +1155,14 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
   p.fault_drop_k = test_fault_drop();
   p.n_pages = cache->n_pages; p.page_size = cache->page_size;
   p.capacity = capacity;
-  const bool e4m3 = cache->elem_bytes == 1;
-  const cudaError_t e = d == 128 ? (e4m3 ? launch_decode<128, true>(p, stream)
-                                         : launch_decode<128, false>(p, stream))
-                                 : (e4m3 ? launch_decode<64, true>(p, stream)
-                                         : launch_decode<64, false>(p, stream));
+  auto launch = [&](auto dim) {
+    constexpr int kD = decltype(dim)::value;
+    return held == Held::kBf16   ? launch_decode<kD, Held::kBf16>(p, stream)
+           : held == Held::kE4M3 ? launch_decode<kD, Held::kE4M3>(p, stream)
+                                 : launch_decode<kD, Held::kInt4>(p, stream);
+  };
+  const cudaError_t e = d == 128 ? launch(std::integral_constant<int, 128>())
+                                 : launch(std::integral_constant<int, 64>());
   return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 

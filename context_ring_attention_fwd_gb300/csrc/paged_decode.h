@@ -9,13 +9,17 @@
 
 #include <cstdint>
 
+#include "internal.h"
+
 namespace cpring {
 
 struct DecodeParams {
   const __nv_bfloat16* q;
   const uint8_t* cache[2];  // k, v
   long long cs[2][3];       // their strides in bytes: page, token, head
-  const float* descale[2];
+  const float* descale[2];  // 4 bits: may be null (ones)
+  const uint8_t* scales[2];  // 4 bits: E4M3, one of kBlock entries
+  long long ss[2][3];        // their strides in bytes: page, token, head
   const int32_t* table;
   const int32_t* seq_lens;
   const int32_t* prefix_pages;
@@ -62,6 +66,26 @@ __device__ __forceinline__ uint32_t half2_of_codes(uint32_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
   return h;
+}
+// Entries in 4 bits.  Entry i of a row is code (byte i / 2, the low half for even i) minus 8,
+// times its block's E4M3 scale, times the head's descale.  A code in bits 4 to 7 of a half word
+// below the fp16 exponent of 64 reads 64 + code, so one fused multiply-add, (64 + code) s -
+// 72 s, gives (code - 8) s: the sums and products of a code's 4 and a scale's 4 bits fit
+// fp16's 11, so the value is exact.
+// The four pairs of a word: half2 i holds the codes i and i + 4 (in two half words: code i of
+// each), times the scales of the halves of `s`; ms = scale_offset(s).
+__device__ __forceinline__ uint32_t scale_offset(uint32_t s) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(0xd480d480u));  // -72
+  return r;
+}
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t s, uint32_t ms, uint32_t (&v)[4]) {
+  const uint32_t t[4] = {w << 4, w, w >> 4, w >> 8};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t n = (t[i] & 0x00f000f0u) | 0x54005400u;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(n), "r"(s), "r"(ms));
+  }
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);

@@ -320,15 +320,26 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// The strides of a cache tensor's pages, tokens and heads, in its elements.
+void cache_strides(const Tensor& t, int64_t (&to)[3]) {
+  for (int i = 0; i < 3; ++i) to[i] = t.size(i) > 1 ? t.stride(i) : 0;
+}
+
 // The cache of caches [pages, page_size, Hk, d] (bf16, or E4M3 with fp32 [Hk]
-// descales) and an int32 table [B, max_pages].
+// descales; with scales [pages, page_size, Hk, d / 16], codes in 4 bits [pages,
+// page_size, Hk, d / 2]) and an int32 table [B, max_pages].
 cp_paged_cache cache_of(PyObject* ko, PyObject* vo, PyObject* to, PyObject* kdo, PyObject* vdo,
-                        int64_t B, int dev) {
+                        PyObject* kso, PyObject* vso, int64_t B, int dev) {
   const Tensor& k = rows4(ko, "k_cache");
   const at::ScalarType type = k.scalar_type();
-  const bool e4m3 = type == at::kByte || type == at::kFloat8_e4m3fn;
-  TORCH_CHECK_TYPE(e4m3 || type == at::kBFloat16,
-                   "k_cache must be bf16, or E4M3 (float8_e4m3fn, or its codes as uint8)");
+  const bool int4 = kso != Py_None || vso != Py_None;
+  const bool e4m3 = !int4 && (type == at::kByte || type == at::kFloat8_e4m3fn);
+  if (int4) {
+    TORCH_CHECK_TYPE(type == at::kByte, "k_cache must be uint8 (two codes a byte) with k_scale");
+  } else {
+    TORCH_CHECK_TYPE(e4m3 || type == at::kBFloat16,
+                     "k_cache must be bf16, or E4M3 (float8_e4m3fn, or its codes as uint8)");
+  }
   const Tensor& v = needed(vo, "v_cache");
   const Tensor& table = needed(to, "page_table");
   cp_paged_cache c{};
@@ -341,11 +352,23 @@ cp_paged_cache cache_of(PyObject* ko, PyObject* vo, PyObject* to, PyObject* kdo,
   c.n_pages = to_int(k.size(0), "k_cache");
   c.page_size = to_int(k.size(1), "k_cache");
   c.Hk = to_int(k.size(2), "k_cache");
-  c.d = to_int(k.size(3), "k_cache");
+  c.d = to_int(int4 ? 2 * k.size(3) : k.size(3), "k_cache");
   c.max_pages = to_int(table.size(1), "page_table");
   c.table_stride = B > 1 ? table.stride(0) : c.max_pages;
-  c.elem_bytes = e4m3 ? 1 : 2;
-  if (e4m3) {
+  c.elem_bytes = int4 ? -2 : e4m3 ? 1 : 2;
+  if (int4) {
+    const int64_t shape[4] = {c.n_pages, c.page_size, c.Hk, c.d / 16};
+    const Tensor* const scale[2] = {&needed(kso, "k_scale"), &needed(vso, "v_scale")};
+    const at::ScalarType of = scale[0]->scalar_type();
+    TORCH_CHECK_TYPE(of == at::kByte || of == at::kFloat8_e4m3fn,
+                     "k_scale must be float8_e4m3fn, or its codes as uint8");
+    c.k_scale = operand(*scale[0], "k_scale", of, dev, shape);
+    c.v_scale = operand(*scale[1], "v_scale", of, dev, shape);
+    cache_strides(*scale[0], c.k_scale_strides);
+    cache_strides(*scale[1], c.v_scale_strides);
+    c.k_descale = floats(kdo, "k_descale", dev, c.Hk);
+    c.v_descale = floats(vdo, "v_descale", dev, c.Hk);
+  } else if (e4m3) {
     c.k_descale = static_cast<const float*>(
         dense(needed(kdo, "k_descale"), "k_descale", at::kFloat, dev, {c.Hk}));
     c.v_descale = static_cast<const float*>(
@@ -354,23 +377,21 @@ cp_paged_cache cache_of(PyObject* ko, PyObject* vo, PyObject* to, PyObject* kdo,
     TORCH_CHECK_VALUE(kdo == Py_None && vdo == Py_None,
                       "k_descale and v_descale go with an E4M3 cache");
   }
-  for (int i = 0; i < 3; ++i) {
-    c.k_strides[i] = k.size(i) > 1 ? k.stride(i) : 0;
-    c.v_strides[i] = v.size(i) > 1 ? v.stride(i) : 0;
-  }
+  cache_strides(k, c.k_strides);
+  cache_strides(v, c.v_strides);
   return c;
 }
 
 // (q, k, v, k_cache, v_cache, page_table, cache_lens, new_lens, q_weight, k_weight, inv_freq,
-//  q_out, eps, interleaved, k_descale, v_descale, stream) -> q_out
+//  q_out, eps, interleaved, k_descale, v_descale, stream, k_scale, v_scale) -> q_out
 PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arity(n, 17);
+  arity(n, 19);
   const Tensor& k = rows4(a[1], "k");
   const int dev = device_of(k, "k");
   const Home home(a[16], dev);
   const int B = to_int(k.size(0), "k"), S = to_int(k.size(1), "k");
-  const cp_paged_cache cache = cache_of(a[3], a[4], a[5], a[14], a[15], B, dev);
+  const cp_paged_cache cache = cache_of(a[3], a[4], a[5], a[14], a[15], a[17], a[18], B, dev);
   const int64_t shape[4] = {B, S, cache.Hk, cache.d};
   const void* const k_at = operand(k, "k", at::kBFloat16, dev, shape);
   const Tensor& v = needed(a[2], "v");
@@ -406,15 +427,15 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (q, k_cache, v_cache, page_table, seq_lens, out, lse, prefix_pages, prefix_len, k_descale,
-//  v_descale, workspace, stream) -> (out, lse)
+//  v_descale, workspace, stream, k_scale, v_scale) -> (out, lse)
 PyObject* paged_attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arity(n, 13);
+  arity(n, 15);
   const Tensor& q = rows4(a[0], "q");
   const int dev = device_of(q, "q");
   const Home home(a[12], dev);
   const int B = to_int(q.size(0), "q"), n_q = to_int(q.size(1), "q"), Hq = to_int(q.size(2), "q");
-  const cp_paged_cache cache = cache_of(a[1], a[2], a[3], a[9], a[10], B, dev);
+  const cp_paged_cache cache = cache_of(a[1], a[2], a[3], a[9], a[10], a[13], a[14], B, dev);
   const void* const q_at = operand(q, "q", at::kBFloat16, dev, {B, n_q, Hq, cache.d});
   const Tensor out = output(a[5], "out", q);
   void* const out_at = dense(out, "out", at::kBFloat16, dev, q.sizes());

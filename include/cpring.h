@@ -531,7 +531,7 @@ typedef struct cp_paged_cache {
   int64_t k_strides[3];     /* elements between pages, tokens of a page, heads (each a */
   int64_t v_strides[3];     /* multiple of 16 bytes; no two entries at one address)    */
   const float* k_descale;   /* E4M3: device fp32 [Hk], > 0, value = code *             */
-  const float* v_descale;   /* descale[head]; bf16: not read                           */
+  const float* v_descale;   /* descale[head]; bf16: not read; 4 bits: NULL = ones      */
   const int32_t* page_table;  /* device, rows of max_pages entries                     */
   int64_t table_stride;     /* entries between its rows, >= max_pages; 0: one row that */
                             /* every sequence uses                                     */
@@ -540,8 +540,25 @@ typedef struct cp_paged_cache {
   int32_t max_pages;
   int32_t Hk;               /* 1 .. 65535                                              */
   int32_t d;                /* 64 or 128                                               */
-  int32_t elem_bytes;       /* 2: bf16, 1: E4M3 (codes as cp_fp8_quantize writes)      */
+  int32_t elem_bytes;       /* 2: bf16, 1: E4M3 (codes as cp_fp8_quantize writes),     */
+                            /* -2: 4 bits, two entries a byte (below)                  */
+  void* k_scale;            /* 4 bits only (otherwise not read): device, E4M3, d / 16  */
+  void* v_scale;            /* a row, 8-byte aligned                                   */
+  int64_t k_scale_strides[3];  /* bytes between pages, tokens of a page, heads (each a */
+  int64_t v_scale_strides[3];  /* multiple of a row's d / 16)                          */
 } cp_paged_cache;
+
+/*
+ * A cache in 4 bits.  A row (one head of one token) is d / 2 bytes of codes, entry i
+ * in byte i / 2 (the low half for even i), and d / 16 scales:
+ *   value[i] = (code[i] - 8) * scale[i / 16] * descale[head],  code in 0 .. 15.
+ * k_strides and v_strides are in bytes, each a multiple of 16.  A row x is written as
+ *   y = x * (1 / descale[head]);  scale = E4M3(max |y| over its 16 entries * (1 / 7));
+ *   code = round(y / scale) clamped to +-7, plus 8
+ * (each an fp32 operation rounded to nearest, ties to even; scale saturated at 448,
+ * and where it is 0 the code is 8), so that while max |y| < 3328 an entry y is off by
+ * scale / 2 or, where that is more, 7 / 1024.  A NaN makes its 16 entries NaN.
+ */
 
 /*
  * Append new tokens' keys and values to a paged cache, with the norm and

@@ -1,6 +1,6 @@
 """fp64 numpy oracle of the operators around the attention: the per-head norm
 and rotation of queries and keys with its gradient, the append to a paged
-cache, and decode attention over such a cache.  Written row by row from the
+cache, decode attention over such a cache, and what a cache in 4 bits holds.  Written row by row from the
 definitions; shares no code with the CUDA library."""
 from __future__ import annotations
 
@@ -83,3 +83,44 @@ def paged_decode(q, k_cache, v_cache, table, seq_lens, prefix_pages=(), prefix_l
                 out[b, i, h] = (e / e.sum()) @ v_cache[pg, sl, hk].astype(np.float64)
                 lse[b, h, i] = m + np.log(e.sum())
     return out, lse
+
+
+def e4m3_values():
+    """The values of the E4M3 codes 0 .. 0x7E (a sign bit of 0; 0x7F is NaN), ascending."""
+    return np.array([(m / 8 * 2.0 ** -6) if e == 0 else (1 + m / 8) * 2.0 ** (e - 7)
+                     for e in range(16) for m in range(8)][:127])
+
+
+def e4m3_codes(x):
+    """Codes of the nearest E4M3 values of x >= 0, ties to the even code, saturated at 448."""
+    v = e4m3_values()
+    up = np.clip(np.searchsorted(v, x), 1, 126)
+    lo, hi = v[up - 1], v[up]
+    even = np.where(up % 2 == 0, up, up - 1)
+    code = np.where(x - lo < hi - x, up - 1, np.where(x - lo > hi - x, up, even))
+    return np.where(x >= 448, 126, code).astype(np.uint8)
+
+
+def quantise4(x, descale=None):
+    """Rows x [..., Hk, d] as a cache in 4 bits holds them: codes [..., Hk, d / 2] (two to a byte,
+    the low half first) and E4M3 scale codes [..., Hk, d / 16].  The products with 1 / descale and
+    1 / 7 are fp32 operations by definition; the quotient's rounding is the same from fp32 and
+    from fp64 but for ties that fp32 makes, which no bf16 row without a descale has."""
+    f = np.float32
+    y = np.asarray(x, dtype=f)
+    if descale is not None:
+        y = y * (f(1) / np.asarray(descale, dtype=f))[:, None]
+    y = y.reshape(*y.shape[:-1], -1, 16)
+    scales = e4m3_codes((np.abs(y).max(-1) * (f(1) / f(7))).astype(np.float64))
+    s = e4m3_values()[scales][..., None]
+    q = np.divide(y, s.astype(f), out=np.zeros_like(y), where=s > 0)
+    n = (np.clip(np.rint(np.nan_to_num(q, nan=0.0, posinf=7, neginf=-7)), -7, 7) + 8).astype(np.uint8).reshape(*y.shape[:-2], -1)
+    return n[..., ::2] | n[..., 1::2] << 4, scales
+
+
+def values4(codes, scales, descale=None):
+    """What codes [..., Hk, d / 2] with scale codes [..., Hk, d / 16] stand for, in 64 bits."""
+    n = np.stack([codes & 15, codes >> 4], -1).reshape(*codes.shape[:-1], -1).astype(np.float64) - 8
+    s = np.append(e4m3_values(), np.nan)[scales & 0x7F] * np.where(scales >> 7, -1.0, 1.0)
+    v = (n.reshape(*n.shape[:-1], -1, 16) * s[..., None]).reshape(n.shape)
+    return v if descale is None else v * np.asarray(descale, dtype=np.float64)[:, None]
