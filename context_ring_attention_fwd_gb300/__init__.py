@@ -25,6 +25,8 @@ from ._binding import (  # noqa: F401
     cp_lse_finalize, cp_lse_merge, cp_ring_attn_bwd, cp_ring_attn_bwd_workspace_bytes,
     cp_paged_append, cp_paged_attn_decode, cp_paged_attn_decode_workspace_bytes,
     cp_qk_norm_rope, cp_qk_norm_rope_bwd, cp_qk_norm_rope_bwd_workspace_bytes,
+    cp_packed_attn_bwd, cp_packed_attn_bwd_workspace_bytes, cp_packed_attn_fwd,
+    cp_packed_attn_fwd_workspace_bytes,
     cp_ring_attn_fwd, cp_ring_attn_fwd_emulated,
     cp_ring_attn_fwd_f32, cp_ring_attn_fwd_fp8,
     cp_ring_emulated_workspace_bytes, cp_ring_schedule, cp_ring_schedule_device, cp_ring_step,
@@ -42,6 +44,7 @@ __all__ = [
     "cp_ring_attn_bwd", "ring_attn_bwd",
     "cp_qk_norm_rope", "cp_qk_norm_rope_bwd", "qk_norm_rope", "qk_norm_rope_bwd",
     "cp_paged_append", "paged_append", "cp_paged_attn_decode", "paged_attn_decode",
+    "cp_packed_attn_fwd", "packed_attn_fwd", "cp_packed_attn_bwd", "packed_attn_bwd",
     "CpError", "lib",
 ]
 
@@ -236,3 +239,22 @@ def paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     return cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, None, None,
                                 prefix_pages, prefix_len, k_descale, v_descale, workspace, stream,
                                 k_scale, v_scale)
+
+
+def packed_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_offsets: torch.Tensor,
+                    causal: bool = True, out=None, lse=None, workspace=None, stream=None):
+    """Attention over packed prompts with grouped heads: q [T,Hq,d], k, v [T,Hk,d] bf16 (strided
+    views allowed), sequence s the rows [seq_offsets[s], seq_offsets[s + 1]) (int32 on the device).
+    Returns (out [T,Hq,d] bf16, lse [Hq,T] fp32); rows of no sequence are left as they were in
+    those that are given and are zero in those that are allocated."""
+    return cp_packed_attn_fwd(q, k, v, seq_offsets, out, lse, causal, workspace, stream)
+
+
+def packed_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                    lse: torch.Tensor, dout: torch.Tensor, seq_offsets: torch.Tensor,
+                    causal: bool = True, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """The backward of packed_attn_fwd for its (out, lse): returns (dq [T,Hq,d], dk, dv [T,Hk,d])
+    bf16, a shared key head's gradients summed over its query heads.  dq, dk and dv may be views
+    of the projection's gradient; rows of no sequence as in packed_attn_fwd."""
+    return cp_packed_attn_bwd(q, k, v, out, lse, dout, seq_offsets, dq, dk, dv, causal, workspace,
+                              stream)

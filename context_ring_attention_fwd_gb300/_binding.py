@@ -75,6 +75,12 @@ _SIGS = {
     "cp_paged_append": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f, _vp, _i, _i,
                         _vp, _i, _i, _i, _vp],
     "cp_paged_attn_decode_workspace_bytes": [_i, _i, _i, _i, _i, _i],
+    "cp_packed_attn_fwd_workspace_bytes": [_i, _i, _i, _i, _i],
+    "cp_packed_attn_fwd": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                           _vp, _i64, _vp],
+    "cp_packed_attn_bwd_workspace_bytes": [_i, _i, _i, _i, _i],
+    "cp_packed_attn_bwd": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                           _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp],
     "cp_test_set_prefix_path": [_i],
     "cp_paged_attn_decode": [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _i64, _vp],
 }
@@ -122,6 +128,8 @@ def lib() -> ctypes.CDLL:
                               "cp_ring_attn_bwd_workspace_bytes",
                               "cp_qk_norm_rope_bwd_workspace_bytes",
                               "cp_paged_attn_decode_workspace_bytes",
+                              "cp_packed_attn_fwd_workspace_bytes",
+                              "cp_packed_attn_bwd_workspace_bytes",
                               "cp_ring_attn_fwd_host_workspace_bytes"):
                     fn.restype = _i64
                 else:
@@ -631,3 +639,31 @@ def cp_paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out, lse, pr
     return (_ext or native()).paged_attn_decode(q, k_cache, v_cache, page_table, seq_lens, out,
                                                 lse, prefix_pages, prefix_len, k_descale,
                                                 v_descale, workspace, stream, k_scale, v_scale)
+
+
+# ------------------------------------------------- packed prompts, grouped heads
+def cp_packed_attn_fwd_workspace_bytes(T: int, n_seqs: int, Hq: int, Hk: int, d: int) -> int:
+    return int(lib().cp_packed_attn_fwd_workspace_bytes(T, n_seqs, Hq, Hk, d))
+
+
+def cp_packed_attn_fwd(q, k, v, seq_offsets, out, lse, causal: bool = True,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of q [T,Hq,d] over k, v [T,Hk,d] (bf16, strided views allowed) packed from
+    sequences of the rows [seq_offsets[s], seq_offsets[s + 1]) (int32 [n + 1] on the device).
+    out [T,Hq,d] bf16 and lse [Hq,T] fp32 are returned (allocated, as zeros, if None); rows of
+    no sequence are not written.  workspace: a uint8 device tensor (allocated here if None)."""
+    return (_ext or native()).packed_attn_fwd(q, k, v, seq_offsets, causal, out, lse, workspace,
+                                              stream)
+
+
+def cp_packed_attn_bwd_workspace_bytes(T: int, n_seqs: int, Hq: int, Hk: int, d: int) -> int:
+    return int(lib().cp_packed_attn_bwd_workspace_bytes(T, n_seqs, Hq, Hk, d))
+
+
+def cp_packed_attn_bwd(q, k, v, out, lse, dout, seq_offsets, dq, dk, dv, causal: bool = True,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of sum(out * dout) for cp_packed_attn_fwd's out and lse (contiguous, as dout):
+    dq [T,Hq,d], dk, dv [T,Hk,d] bf16 (strided views allowed; allocated, as zeros, if None), which
+    are returned; rows of no sequence are not written."""
+    return (_ext or native()).packed_attn_bwd(q, k, v, out, lse, dout, seq_offsets, causal, dq, dk,
+                                              dv, workspace, stream)

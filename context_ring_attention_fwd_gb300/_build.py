@@ -25,7 +25,8 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["attn_sm103.cu", "attn_f32.cu", "merge.cu", "noalloc.cu", "ring_emulation.cpp",
            "ulysses.cu", "fp8.cu", "attn_bwd_sm103.cu", "norm_rope.cu", "paged_append.cu",
-           "paged_decode.cu", "prefix_sm103.cu", "api.cpp", "scratch.cpp", "host_path.cpp"]
+           "paged_decode.cu", "prefix_sm103.cu", "packed_plan.cu", "packed_fwd_sm103.cu",
+           "packed_bwd_sm103.cu", "api.cpp", "scratch.cpp", "host_path.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -41,7 +42,7 @@ def _nvcc() -> str:
 # launch, so a build that comes out different is refused (the split would not
 # fit and the kernel would stall).
 SPLIT_KERNELS = ("ring_attn_bf16_kernel", "ring_attn_fp8_kernel", "ring_attn_bwd_kernel",
-                 "prefix_attn_kernel")
+                 "prefix_attn_kernel", "packed_fwd_kernel", "packed_bwd_kernel")
 SPLIT_LAUNCH_REGS = 168
 
 

@@ -843,15 +843,6 @@ struct BwdSideStream {
 constexpr int kMaxBwdDevices = 64;
 BwdSideStream g_bwd_side[kMaxBwdDevices];
 
-cudaStream_t bwd_side_stream() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxBwdDevices) return nullptr;
-  BwdSideStream& b = g_bwd_side[dev];
-  std::lock_guard<std::mutex> lock(b.mu);
-  if (!b.s && cudaStreamCreateWithFlags(&b.s, cudaStreamNonBlocking) != cudaSuccess) b.s = nullptr;
-  return b.s;
-}
-
 // dK/dV on `stream`, dQ beside it; both after everything already on `stream`.
 template <int D>
 cudaError_t launch_bwd_pair(const BwdArgs& a, cudaStream_t stream) {
@@ -879,6 +870,15 @@ cudaError_t launch_bwd_pair(const BwdArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaStream_t bwd_side_stream() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxBwdDevices) return nullptr;
+  BwdSideStream& b = g_bwd_side[dev];
+  std::lock_guard<std::mutex> lock(b.mu);
+  if (!b.s && cudaStreamCreateWithFlags(&b.s, cudaStreamNonBlocking) != cudaSuccess) b.s = nullptr;
+  return b.s;
+}
 
 cudaError_t launch_attn_bwd(const BwdArgs& a, cudaStream_t stream) {
   {

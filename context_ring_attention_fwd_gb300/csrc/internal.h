@@ -145,6 +145,9 @@ cudaError_t launch_schedule_probe(const AttnArgs& a, int32_t* ranges, cudaStream
 // Backward: the row sums D, then the dK/dV kernel and the dQ kernel (bf16,
 // d in {64, 128}).
 cudaError_t launch_attn_bwd(const BwdArgs& a, cudaStream_t stream);
+// The library's second stream for the backward's dQ on the current device (null: none could
+// be made).
+cudaStream_t bwd_side_stream();
 cudaError_t launch_doc_scan(const int32_t* doc_offsets, int S, int32_t* doc_info,
                             cudaStream_t stream);
 cudaError_t launch_merge(float* o_acc, float* m_acc, float* l_acc, const float* o_part,

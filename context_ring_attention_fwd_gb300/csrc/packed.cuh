@@ -1,0 +1,160 @@
+// What the kernels of the attention over packed prompts share (packed_plan.cu,
+// packed_fwd_sm103.cu, packed_bwd_sm103.cu): the list of work items that the plan
+// makes of the sequences' lengths, and packed tiles of query rows.
+//
+// Query rows.  The G = Hq / Hk query heads that read one key head are attended
+// together: a 128-row tile holds tq = 128 / G (rounded down) tokens of all of them, row
+// r being head r % G of token r / G.  So a key tile is loaded once for G heads, a tile's
+// rows span few tokens (less of the causal diagonal is computed in vain), and the
+// gradients of a shared key head sum up in the products themselves.  In [T, Hq, d]
+// the G heads of a token lie side by side, so a tile is one TMA box of G x tq rows.
+// Rows behind tq G, and those of tokens behind a sequence's end, are not stored; where
+// they are summed over they are zeroed in shared memory, since what lies there may be
+// infinite or NaN.
+//
+// Items.  The lengths are on the device, so a captured call follows them: the
+// plan's kernel lists every sequence's tiles, the most expensive first, and the
+// attention's CTAs claim (tile, key head) pairs in that order.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "attn_common.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace cpring {
+
+constexpr int kCostUnit = 128;  // tokens that an item's cost is counted in
+
+// A list in the caller's workspace.  The attention's kernels, which may start before the plan
+// is done and wait for it, read it (and D) with plain loads: a read-only load (__ldg) promises
+// that nothing writes during the kernel, and the compiler may move it before the wait.
+struct PackedList {
+  int* head;        // [0] items of a key head (0 where the offsets are malformed), [1] next claim
+  int4* items;      // {first row of the sequence, its length, the tile's index, 0}
+  int* starts;      // [n] items before each sequence (scratch)
+  int* buckets;     // [n_buckets] (scratch)
+  int tokens;       // of a tile
+  int of_keys;      // tiles of keys: their cost is the queries that see them
+};
+
+struct PackedPlan {
+  PackedList list[2];
+  int lists;
+  const int32_t* offsets;
+  int n, T, causal, n_buckets;
+  int* err;
+  // the backward: delta[row] = sum of out * dout over a row's d entries (rows T * Hq)
+  const void* out;
+  const void* dout;
+  float* delta;
+  long long rows;
+  int d;
+};
+
+// A call's tensors: [T, H, d] with strides (token, head) in elements.
+struct PackedArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t qs[2], ks[2], vs[2];
+  int T, Hq, Hk;
+};
+
+constexpr int kMaxPacked = 1 << 20;  // sequences of a call
+
+// The checks that the forward and the backward share, and a tensor's strides (as given,
+// or contiguous; false if a tensor map cannot have them).
+cp_status check_packed(int T, int n, int Hq, int Hk, int d, int causal);
+bool packed_strides(const int64_t* given, int H, int d, int64_t (&to)[2]);
+
+cudaError_t launch_packed_plan(const PackedPlan& p, cudaStream_t stream);
+
+// Byte sizes and places of a list of tiles of `tokens` tokens.
+inline long long packed_items(int T, int n, int tokens) {
+  return static_cast<long long>(T) / tokens + n;
+}
+inline int packed_buckets(int T) { return T / kCostUnit + 2; }
+inline long long packed_list_bytes(int T, int n, int tokens) {
+  return 256 + 16 * packed_items(T, n, tokens) + 4LL * n + 4LL * packed_buckets(T);
+}
+inline PackedList packed_list(char* at, int T, int n, int tokens, bool of_keys) {
+  PackedList l{};
+  l.head = reinterpret_cast<int*>(at);
+  l.items = reinterpret_cast<int4*>(at + 256);
+  l.starts = reinterpret_cast<int*>(at + 256 + 16 * packed_items(T, n, tokens));
+  l.buckets = l.starts + n;
+  l.tokens = tokens;
+  l.of_keys = of_keys;
+  return l;
+}
+
+namespace {
+
+// The (tile, key head) pair of item w: groups of `hg` heads, in a group the list's order.
+// A long list walks few heads at a time, whose keys then come from L2: the smallest group
+// whose items fill the grid once; a short one (under 16 rounds of the grid) is one pool, so
+// that its cheapest items come last.
+struct PackedOrder {
+  int items, heads, group, n;
+  __device__ PackedOrder(int items_, int heads_, int grid) : items(items_), heads(heads_) {
+    n = items * heads;
+    group = heads;
+    if (n >= 16LL * grid) group = max(1, min(heads, (grid + items - 1) / items));
+  }
+  __device__ void at(int w, int& tile, int& head) const {
+    const int g = w / (group * items), r = w - g * group * items;
+    const int in_group = min(group, heads - g * group);
+    tile = r / in_group;
+    head = g * group + r - tile * in_group;
+  }
+};
+
+// One CTA's claims of a list: its first item is its own index, later ones come from the
+// list's counter (which the plan clears at every call, so a replayed graph starts afresh).
+__device__ __forceinline__ int packed_claim(int* head, int grid) {
+  return grid + atomicAdd(head + 1, 1);
+}
+
+// Zeroes the bytes [from, to) of shared memory (multiples of 16) with the lanes of a warp.
+__device__ __forceinline__ void zero_shared(uint32_t from, uint32_t to) {
+  for (uint32_t at = from + (threadIdx.x & 31) * 16; at < to; at += 512)
+    ptx::st_shared_v4(at, 0u, 0u, 0u, 0u);
+}
+// Rows [first, end) of every 128-byte panel of a 128-row tile (the swizzle moves
+// chunks within a row only).
+template <int kPanels>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int end) {
+#pragma unroll
+  for (int pn = 0; pn < kPanels; ++pn)
+    zero_shared(tile + pn * kTileRows * 128 + first * 128, tile + pn * kTileRows * 128 + end * 128);
+}
+
+// [T, H, d] with strides (token, head) in elements as (d, H, T); box = one 128-byte panel x
+// `heads` x `tokens`.  Strides as packed_strides_ok accepts them.
+bool packed_map(CUtensorMap* m, const void* base, int T, int H, int d, long long ts, long long hs,
+                int heads, int tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  if (H == 1) hs = d;        // a dimension of one entry: the stride is never used
+  if (T == 1) ts = hs * H;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H),
+                              static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hs) * 2, static_cast<cuuint64_t>(ts) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+}  // namespace cpring

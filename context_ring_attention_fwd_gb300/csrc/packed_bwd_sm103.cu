@@ -1,0 +1,887 @@
+// Gradients of the attention over packed prompts with grouped heads (packed_fwd_sm103.cu), on
+// sm_103a tensor cores (tcgen05), bf16.
+//
+// For L = sum(out * dout), row by row with P = exp(s - lse):
+//   D = rowsum(dO * O);  dP = dO V^T;  dS = P * (dP - D);
+//   dV = P^T dO;  dK = dS^T Q / sqrt(d);  dQ = dS K / sqrt(d)
+// ("上下文並行（Context Parallelism, CP）", compassingai.com, section 反向傳播), the sums of a key
+// head's dK and dV running over the G query heads that read it.  Two kernels as in
+// attn_bwd_sm103.cu, where the CTA's roles and its use of TMEM are described:
+//   kDKDV  a CTA owns a 128-key tile of one key head and walks the packed query tiles
+//          (packed.cuh) that see it: G heads' rows are neighbours in the products' inner
+//          dimension, so a shared head's gradients are summed in the accumulators.
+//   kDQ    a CTA owns a packed query tile and walks the key tiles it sees.
+// Every output is finished by one CTA: no atomics.
+//
+// Rows that are not there (behind a sequence, behind tq G) may hold anything.  Where they are
+// summed over - Q and dO in kDKDV, K in kDQ - they are zeroed in shared memory up to the next
+// multiple of 16, where the product ends; P and dS of masked pairs are replaced by zeros, not
+// multiplied.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "attn_common.cuh"
+#include "internal.h"
+#include "packed.cuh"
+#include "ptx.cuh"
+
+namespace cpring {
+namespace {
+
+constexpr int kT = kTileRows;       // rows of every tile
+constexpr int kThreads = 384;        // three warpgroups (warps 10, 11 idle)
+constexpr int kLaunchRegs = 168;     // registers per thread at launch (checked by the build)
+constexpr int kSoftmaxRegs = 200;    // softmax warpgroups after setmaxnreg.inc
+constexpr int kControlRegs = 104;    // producer / MMA warpgroup after setmaxnreg.dec
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= kThreads * kLaunchRegs,
+              "register split exceeds the launch's register pool");
+constexpr int kSoftmaxThreads = 256;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Streamed tiles run in two rings of single-tile slots: X0 (K for kDQ, Q for
+// kDKDV) and X1 (V or dO).  kDQ holds K until dQ += dS K is done but V only
+// until dP, and issues the next step's products early, so its K ring is one
+// slot deeper.
+template <int D, bool kDKDV>
+struct BLayout {
+  static constexpr int kTileBytes = kT * D * 2;
+  static constexpr int kPanelBytes = kT * 128;   // 128 rows x 64 bf16 columns
+  static constexpr int kPanels = D / 64;
+  static constexpr int kX0Slots = kDKDV ? 2 : 3;
+  static constexpr int kX1Slots = 2;
+  static constexpr int kF0 = 0;                  // fixed tiles
+  static constexpr int kF1 = kTileBytes;
+  static constexpr int kX0 = 2 * kTileBytes;
+  static constexpr int kX1 = kX0 + kX0Slots * kTileBytes;
+  static constexpr int kVec = kX1 + kX1Slots * kTileBytes;    // kDKDV: [2][-lse2, -D][128] fp32
+  static constexpr int kBar = kVec + (kDKDV ? 2 * 2 * kT * 4 : 0);
+  static constexpr int kRingOff = kBar + 256;  // the item ring
+  static constexpr int kBytes = kRingOff + 256;
+  static constexpr int kAlloc = kBytes + 1024;
+  __host__ __device__ static constexpr int x0(int slot) { return kX0 + slot * kTileBytes; }
+  __host__ __device__ static constexpr int x1(int slot) { return kX1 + slot * kTileBytes; }
+};
+
+enum BBar : int {
+  kFixFull = 0,
+  kFixEmpty = 1,
+  kX0Full = 2,     // + slot (3)
+  kX1Full = 5,     // + slot (2)
+  kX0Empty = 7,    // + slot (3)
+  kX1Empty = 10,   // + slot (2)
+  kSFull = 12,     // + TMEM buffer (kDKDV; kDQ uses +0): S and dP of a step are in TMEM
+  kPReady = 14,    // + step parity: P / dS written by all softmax threads
+  kSConsumed = 16, // kDQ: every softmax thread has read S and dP of the step
+  kAccFull = 17,   // the item's accumulators are final
+  kVecFull = 18,   // + buffer: per-column lse / delta of a query tile written (kDKDV)
+  kVecFree = 20,   // + buffer: every softmax thread is done reading it
+  kPReadyS = 22,   // + TMEM buffer (kDKDV): dS^T written (kPReady + buffer: P^T written)
+  kDrain = 24,
+  kNumBars = 25
+};
+// kDQ keeps packed dS in its own double buffer of TMEM columns (acc0 ends at
+// 256 + D <= 384), so S and dP of the next step can be issued while the
+// softmax still works on the current one.
+constexpr uint32_t kDsBuf = 384;
+constexpr int kTmemSlot = kNumBars * 8;
+constexpr int kAbortSlot = kNumBars * 8 + 4;
+
+struct BParams {
+  int* head;            // the plan's list
+  const int4* items;
+  int T, n_seqs, Hq, Hk, G;
+  int tq;               // tokens of a packed tile
+  int causal;
+  float scale_log2;     // log2(e) / sqrt(d)
+  float scale;          // 1 / sqrt(d)
+  const float* lse;     // [Hq, T], natural log
+  const float* delta;   // [T, Hq]
+  __nv_bfloat16* g0;    // dQ (kDQ) or dV (kDKDV)
+  __nv_bfloat16* g1;    // dK (kDKDV)
+  long long gs0[2], gs1[2];  // their strides: row, head
+  int* err;
+  unsigned long long timeout_ns;
+  int fault_drop;       // test hook: CTA 0 never loads its first streamed X0 tile
+};
+
+// An item: the sequence, the key head, the first token of the fixed tile and its tokens, and
+// the streamed tiles [x_lo, x_hi].
+struct BItem {
+  int row0, len, hk;
+  int t0, tokens;
+  int x_lo, x_hi;
+};
+template <bool kDKDV>
+__device__ __forceinline__ void decode_bitem(const BParams& p, const PackedOrder& order, int w,
+                                             BItem& it) {
+  int x;
+  order.at(w, x, it.hk);
+  const int4 e = p.items[x];
+  it.row0 = e.x;
+  it.len = e.y;
+  const int tile = kDKDV ? kT : p.tq;
+  it.t0 = e.z * tile;
+  it.tokens = min(tile, it.len - it.t0);
+  if (kDKDV) {  // query tiles that see a key of the tile
+    it.x_lo = p.causal ? it.t0 / p.tq : 0;
+    it.x_hi = (it.len - 1) / p.tq;
+  } else {      // key tiles seen by a row of the tile
+    it.x_lo = 0;
+    it.x_hi = ((p.causal ? it.t0 + it.tokens : it.len) - 1) / kT;
+  }
+}
+
+template <int D, bool kDKDV>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_f0,
+                         const __grid_constant__ CUtensorMap tm_f1,
+                         const __grid_constant__ CUtensorMap tm_x0,
+                         const __grid_constant__ CUtensorMap tm_x1, const BParams p) {
+  using Lay = BLayout<D, kDKDV>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = ptx::smem_u32(smem);
+  const uint32_t bars = sbase + Lay::kBar;
+  auto bar = [&](int idx) -> uint32_t { return bars + 8u * static_cast<uint32_t>(idx); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kBar + kTmemSlot);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Lay::kBar + kAbortSlot);
+  float* vec = reinterpret_cast<float*>(smem + Lay::kVec);
+  const ItemRing ring{sbase + Lay::kRingOff,
+                      reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 2 * kRing * 8)};
+  // the item whose fixed tiles the producer is loading (the MMA warp's copy)
+  volatile int* fix_item = reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 128);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(bar(kFixFull), 1);
+    ptx::mbar_init(bar(kFixEmpty), 1);
+    for (int s = 0; s < Lay::kX0Slots; ++s) {
+      ptx::mbar_init(bar(kX0Full + s), 1);
+      ptx::mbar_init(bar(kX0Empty + s), 1);
+    }
+    for (int s = 0; s < Lay::kX1Slots; ++s) {
+      ptx::mbar_init(bar(kX1Full + s), 1);
+      ptx::mbar_init(bar(kX1Empty + s), 1);
+    }
+    ptx::mbar_init(bar(kSFull), 1);
+    ptx::mbar_init(bar(kSFull + 1), 1);
+    ptx::mbar_init(bar(kPReady), kSoftmaxThreads);
+    ptx::mbar_init(bar(kPReady + 1), kSoftmaxThreads);
+    ptx::mbar_init(bar(kSConsumed), kSoftmaxThreads);
+    ptx::mbar_init(bar(kAccFull), 1);
+    for (int b2 = 0; b2 < 2; ++b2) {
+      ptx::mbar_init(bar(kVecFull + b2), kT);
+      ptx::mbar_init(bar(kVecFree + b2), kSoftmaxThreads);
+    }
+    ptx::mbar_init(bar(kPReadyS), kSoftmaxThreads);
+    ptx::mbar_init(bar(kPReadyS + 1), kSoftmaxThreads);
+    ptx::mbar_init(bar(kDrain), 1);
+    ring_init(ring, kSoftmaxThreads / 32);  // the softmax warps read the ring
+    *abort_flag = 0u;
+    ptx::fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  const int packed_rows = p.tq * p.G;
+  if (kDKDV && packed_rows < kT) {  // no load ever writes these rows of the streamed tiles
+    for (int sl = warp; sl < Lay::kX0Slots + Lay::kX1Slots; sl += kThreads / 32)
+      zero_rows<Lay::kPanels>(sbase + Lay::x0(sl), packed_rows, kT);  // (X1 lies behind X0)
+    ptx::fence_proxy_async_shared();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  cudaGridDependencySynchronize();  // the plan and D
+  const PackedOrder order(p.head[0], p.Hk, gridDim.x);
+  const int x_tokens = kDKDV ? p.tq : kT;  // of a streamed tile
+  const uint32_t packed_bytes = static_cast<uint32_t>(packed_rows) * 128u * Lay::kPanels;
+  const uint32_t fix_bytes = kDKDV ? Lay::kTileBytes : packed_bytes;
+  const uint32_t x_bytes = kDKDV ? packed_bytes : Lay::kTileBytes;
+
+  if (warp >= kProducerWarp) {
+   // the third warpgroup gives registers away, then splits into its roles
+   ptx::setmaxnreg_dec<kControlRegs>();
+   if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      ptx::tma_prefetch_desc(&tm_f0);
+      ptx::tma_prefetch_desc(&tm_f1);
+      ptx::tma_prefetch_desc(&tm_x0);
+      ptx::tma_prefetch_desc(&tm_x1);
+      uint32_t x_iter = 0, fix_iter = 0;
+      uint32_t armed0[3] = {0u, 0u, 0u}, armed1[2] = {0u, 0u};  // loads started per slot
+      int ahead = 0;  // the claim of the CTA's next item
+      bool dropped = false;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const int w = k == 0 ? static_cast<int>(blockIdx.x) : ahead;
+        if (!ring_put(ring, static_cast<uint32_t>(k), w, abort_flag, p)) { ok = false; break; }
+        if (w >= order.n) break;
+        ahead = packed_claim(p.head, gridDim.x);  // read when that item starts
+        BItem it;
+        decode_bitem<kDKDV>(p, order, w, it);
+        const int fix_head = kDKDV ? it.hk : it.hk * p.G, x_head = kDKDV ? it.hk * p.G : it.hk;
+        if (!wait1(bar(kFixEmpty), (fix_iter & 1u) ^ 1u, abort_flag, p)) { ok = false; break; }
+        *fix_item = w;  // the MMA warp reads it once this phase of kFixFull completes
+        ptx::mbar_arrive_expect_tx(bar(kFixFull), 2 * fix_bytes);
+        for (int pn = 0; pn < Lay::kPanels; ++pn) {
+          ptx::tma_load_3d(sbase + Lay::kF0 + pn * Lay::kPanelBytes, &tm_f0, bar(kFixFull),
+                           pn * 64, fix_head, it.row0 + it.t0);
+          ptx::tma_load_3d(sbase + Lay::kF1 + pn * Lay::kPanelBytes, &tm_f1, bar(kFixFull),
+                           pn * 64, fix_head, it.row0 + it.t0);
+        }
+        ++fix_iter;
+        for (int f = it.x_lo; f <= it.x_hi; ++f) {
+          const uint32_t s0 = x_iter % Lay::kX0Slots, ph0 = (x_iter / Lay::kX0Slots) & 1u;
+          const uint32_t s1 = x_iter % Lay::kX1Slots, ph1 = (x_iter / Lay::kX1Slots) & 1u;
+          const int xs = it.row0 + f * x_tokens;
+          if (!wait1(bar(kX0Empty + s0), ph0 ^ 1u, abort_flag, p)) { ok = false; break; }
+          if (p.fault_drop && blockIdx.x == 0 && !dropped) {
+            // Test hook: this tile is never loaded, so the MMA warp's
+            // bounded wait for it runs out and the CTA takes its abort path.
+            dropped = true;
+          } else {
+            ptx::mbar_arrive_expect_tx(bar(kX0Full + s0), x_bytes);
+            for (int pn = 0; pn < Lay::kPanels; ++pn)
+              ptx::tma_load_3d(sbase + Lay::x0(s0) + pn * Lay::kPanelBytes, &tm_x0,
+                               bar(kX0Full + s0), pn * 64, x_head, xs);
+            ++armed0[s0];
+          }
+          if (!wait1(bar(kX1Empty + s1), ph1 ^ 1u, abort_flag, p)) { ok = false; break; }
+          ptx::mbar_arrive_expect_tx(bar(kX1Full + s1), x_bytes);
+          for (int pn = 0; pn < Lay::kPanels; ++pn)
+            ptx::tma_load_3d(sbase + Lay::x1(s1) + pn * Lay::kPanelBytes, &tm_x1,
+                             bar(kX1Full + s1), pn * 64, x_head, xs);
+          ++armed1[s1];
+          ++x_iter;
+        }
+      }
+      // No more items: tell the MMA warp through the next phase of kFixFull.
+      if (ok && wait1(bar(kFixEmpty), (fix_iter & 1u) ^ 1u, abort_flag, p)) {
+        *fix_item = INT_MAX;
+        ptx::mbar_arrive(bar(kFixFull));
+        ++fix_iter;
+      }
+      // Let every copy this thread started land before the CTA can exit.
+      if (fix_iter > 0) wait1(bar(kFixFull), (fix_iter - 1) & 1u, abort_flag, p, false);
+      for (int s = 0; s < Lay::kX0Slots; ++s)
+        if (armed0[s] > 0) wait1(bar(kX0Full + s), (armed0[s] - 1) & 1u, abort_flag, p, false);
+      for (int s = 0; s < Lay::kX1Slots; ++s)
+        if (armed1[s] > 0) wait1(bar(kX1Full + s), (armed1[s] - 1) & 1u, abort_flag, p, false);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp runs this loop with warp-uniform values; one lane picked
+    // by elect.sync issues each MMA and commit (the warp-collective forms in
+    // ptx.cuh), and every wait is the warp-uniform one.
+    {
+      constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kT, kT, false);   // N = streamed rows
+      constexpr uint32_t kIdescG = ptx::idesc_bf16_f32(kT, D, true);     // N = d, B MN-major
+      const uint64_t d_k = ptx::smem_desc_sw128(sbase, 16, 1024);                // K-major
+      const uint64_t d_mn = ptx::smem_desc_sw128(sbase, Lay::kPanelBytes, 1024);  // MN-major
+      const uint32_t tS = tmem_base, tdP = tmem_base + 128;
+      const uint32_t tA0 = tmem_base + 256, tA1 = tmem_base + 256 + D;
+      uint32_t x_iter = 0, fix_iter = 0;
+      bool ok = true;
+      // D_t = A B^T over the head dimension, both tiles K-major.
+      auto issue_ss = [&](uint32_t d_tmem, int a_off, int b_off) {
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint64_t step =
+              static_cast<uint64_t>(((s >> 2) * Lay::kPanelBytes + (s & 3) * 32) >> 4);
+          ptx::mma_ss_w(d_tmem, d_k + (a_off >> 4) + step, d_k + (b_off >> 4) + step, kIdescS,
+                      s > 0 ? 1u : 0u);
+        }
+      };
+      // acc (+)= A B: A = packed bf16 columns at a_tmem, in two halves
+      // `half` columns apart (64: the halves of S / dP; 32: contiguous),
+      // B = the streamed tile at b_off read MN-major (rows = K).
+      auto issue_ts = [&](uint32_t acc, uint32_t a_tmem, int b_off, bool first, int half,
+                          int steps) {
+#pragma unroll
+        for (int s = 0; s < kT / 16; ++s) {
+          if (s >= steps) continue;
+          const uint32_t a_col = static_cast<uint32_t>((s >> 2) * half + (s & 3) * 8);
+          ptx::mma_ts_w(acc, a_tmem + a_col, d_mn + (b_off >> 4) + static_cast<uint64_t>(s * 128),
+                      kIdescG, (first && s == 0) ? 0u : 1u);
+        }
+      };
+      uint32_t n = 0;       // kDQ: steps issued so far (all items)
+      uint32_t m_half = 0;  // kDKDV: halves issued so far (all items)
+      constexpr uint32_t kIdescS64 = ptx::idesc_bf16_f32(kT, 64, false);
+      // D = A B^T over the head dimension with B 64 rows (a half tile).
+      auto issue_ss64 = [&](uint32_t d_tmem, int a_off, int b_off) {
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint64_t step =
+              static_cast<uint64_t>(((s >> 2) * Lay::kPanelBytes + (s & 3) * 32) >> 4);
+          ptx::mma_ss_w(d_tmem, d_k + (a_off >> 4) + step, d_k + (b_off >> 4) + step, kIdescS64,
+                      s > 0 ? 1u : 0u);
+        }
+      };
+      // acc (+)= A B over 64 queries: A = the two warpgroups' packed pieces
+      // (32 columns apart), B = the half tile at b_off read MN-major.
+      auto issue_ts64 = [&](uint32_t acc, uint32_t a_tmem, int b_off, bool first, int steps) {
+#pragma unroll
+        for (int s = 0; s < 64 / 16; ++s) {
+          if (s >= steps) continue;
+          const uint32_t a_col = static_cast<uint32_t>((s >> 1) * 32 + (s & 1) * 8);
+          ptx::mma_ts_w(acc, a_tmem + a_col, d_mn + (b_off >> 4) + static_cast<uint64_t>(s * 128),
+                      kIdescG, (first && s == 0) ? 0u : 1u);
+        }
+      };
+      for (;;) {
+        // The producer publishes each item with its fixed tiles' load (and
+        // the end of the work with a plain arrival), so this warp needs no
+        // wait beyond the one for those tiles.
+        if (!wait_warp(bar(kFixFull), fix_iter & 1u, abort_flag, p)) { ok = false; break; }
+        ++fix_iter;
+        const int w = *fix_item;
+        if (w >= order.n) break;
+        BItem it;
+        decode_bitem<kDKDV>(p, order, w, it);
+        ptx::tc_fence_after();
+        // rows of the last streamed tile: keys, or tokens times heads
+        const int x_left = it.len - it.x_hi * x_tokens;
+        const int last_rows = kDKDV ? min(x_left, p.tq) * p.G : min(x_left, kT);
+        // (a tile of all tq tokens ends in rows that are zero: the product may run over them)
+        const bool ragged = kDKDV ? x_left < p.tq : last_rows < kT;
+        const int last_steps = ragged ? (last_rows + 15) / 16 : kT / 16;
+        const int last_zero = min(last_steps * 16, kDKDV ? packed_rows : kT);
+        if constexpr (!kDKDV) {
+          // S, dP of step n + 1 go out once the softmax has read those of
+          // step n; dQ += dS K of step n once its dS is in buffer n % 2.
+          bool have = false;  // S, dP of the current step already issued
+          // S, dP of streamed step x: K from X0 slot x % 3, V from X1 slot
+          // x % 2; V's slot is free once dP is done.
+          auto issue_step = [&](uint32_t x, bool last) -> bool {
+            const uint32_t s0 = x % Lay::kX0Slots, s1 = x % Lay::kX1Slots;
+            if (!wait_warp(bar(kX0Full + s0), (x / Lay::kX0Slots) & 1u, abort_flag, p)) return false;
+            if (!wait_warp(bar(kX1Full + s1), (x / Lay::kX1Slots) & 1u, abort_flag, p)) return false;
+            ptx::tc_fence_after();
+            if (last && ragged && last_rows < last_zero) {
+              zero_rows<Lay::kPanels>(sbase + Lay::x0(s0), last_rows, last_zero);
+              ptx::fence_proxy_async_shared();
+              __syncwarp();
+            }
+            issue_ss(tS, Lay::kF0, Lay::x0(s0));
+            issue_ss(tdP, Lay::kF1, Lay::x1(s1));
+            ptx::mma_commit_w(bar(kSFull));
+            ptx::mma_commit_w(bar(kX1Empty + s1));
+            return true;
+          };
+          for (int f = it.x_lo; f <= it.x_hi; ++f) {
+            if (!have) {
+              if (n > 0 && !wait_warp(bar(kSConsumed), (n - 1u) & 1u, abort_flag, p)) { ok = false; break; }
+              if (!issue_step(x_iter, f == it.x_hi)) { ok = false; break; }
+            }
+            have = false;
+            if (f < it.x_hi) {
+              if (!wait_warp(bar(kSConsumed), n & 1u, abort_flag, p)) { ok = false; break; }
+              if (!issue_step(x_iter + 1, f + 1 == it.x_hi)) { ok = false; break; }
+              have = true;
+            }
+            if (!wait_warp(bar(kPReady + (n & 1u)), (n >> 1) & 1u, abort_flag, p)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const uint32_t s0 = x_iter % Lay::kX0Slots;
+            issue_ts(tA0, tmem_base + kDsBuf + (n & 1u) * 64u, Lay::x0(s0), f == it.x_lo, 32,
+                     f == it.x_hi ? last_steps : kT / 16);
+            ptx::mma_commit_w(bar(kX0Empty + s0));
+            ++n;
+            ++x_iter;
+          }
+          if (!ok) break;
+          ptx::mma_commit_w(bar(kFixEmpty));
+          ptx::mma_commit_w(bar(kAccFull));
+          continue;
+        }
+        // kDKDV: half hh of the item is query rows 64 (hh % 2) .. of its
+        // streamed tile x_iter + hh / 2; m counts halves over all items and
+        // half m uses TMEM buffer m % 2.  S^T, dP^T of half m + 1 are issued
+        // before dV, dK of half m, so they run during the softmax of half m.
+        // (the last tile's second half is left out where no row is in it).
+        const int last_half = 2 * (it.x_hi - it.x_lo);
+        const int nh = last_half + (last_steps > 4 ? 2 : 1);
+        auto issue_half = [&](uint32_t mm, int hh2) -> bool {
+          const uint32_t xi = x_iter + static_cast<uint32_t>(hh2 >> 1);
+          const uint32_t st = xi % Lay::kX0Slots, ph = (xi / Lay::kX0Slots) & 1u;
+          if (!wait_warp(bar(kX0Full + st), ph, abort_flag, p)) return false;
+          if (!wait_warp(bar(kX1Full + st), ph, abort_flag, p)) return false;
+          ptx::tc_fence_after();
+          if (hh2 == last_half && ragged && last_rows < last_zero) {
+            zero_rows<Lay::kPanels>(sbase + Lay::x0(st), last_rows, last_zero);
+            zero_rows<Lay::kPanels>(sbase + Lay::x1(st), last_rows, last_zero);
+            ptx::fence_proxy_async_shared();
+            __syncwarp();
+          }
+          const uint32_t b = mm & 1u;
+          const int rows = (hh2 & 1) * 64 * 128;   // byte offset of query row 64 in a panel
+          issue_ss64(tmem_base + 128u * b, Lay::kF0, Lay::x0(st) + rows);         // S^T = K Q_h^T
+          issue_ss64(tmem_base + 128u * b + 64u, Lay::kF1, Lay::x1(st) + rows);   // dP^T = V dO_h^T
+          ptx::mma_commit_w(bar(kSFull + b));
+          return true;
+        };
+        if (!issue_half(m_half, 0)) { ok = false; break; }
+        for (int hh = 0; hh < nh; ++hh) {
+          const uint32_t b = m_half & 1u;
+          if (hh + 1 < nh && !issue_half(m_half + 1, hh + 1)) { ok = false; break; }
+          // dV += P^T dO_h as soon as P^T is in TMEM, dK += dS^T Q_h once dS^T is
+          if (!wait_warp(bar(kPReady + b), (m_half >> 1) & 1u, abort_flag, p)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t st = (x_iter + static_cast<uint32_t>(hh >> 1)) % Lay::kX0Slots;
+          const int rows = (hh & 1) * 64 * 128;
+          const int steps = hh >= last_half ? last_steps - 4 * (hh & 1) : 4;
+          issue_ts64(tA0, tmem_base + 128u * b, Lay::x1(st) + rows, hh == 0, steps);
+          if (!wait_warp(bar(kPReadyS + b), (m_half >> 1) & 1u, abort_flag, p)) { ok = false; break; }
+          ptx::tc_fence_after();
+          issue_ts64(tA1, tmem_base + 128u * b + 64u, Lay::x0(st) + rows, hh == 0, steps);
+          if ((hh & 1) || hh + 1 == nh) {
+            ptx::mma_commit_w(bar(kX0Empty + st));
+            ptx::mma_commit_w(bar(kX1Empty + st));
+          }
+          ++m_half;
+        }
+        if (!ok) break;
+        x_iter += static_cast<uint32_t>(it.x_hi - it.x_lo + 1);
+        ptx::mma_commit_w(bar(kFixEmpty));
+        ptx::mma_commit_w(bar(kAccFull));
+      }
+      // Wait until every MMA this warp issued has finished.
+      ptx::mma_commit_w(bar(kDrain));
+      wait_warp(bar(kDrain), 0u, abort_flag, p, false);
+    }
+   }
+  } else {
+    ptx::setmaxnreg_inc<kSoftmaxRegs>();
+    // ------------------------------------------------------------ softmax
+    const int wg = warp >> 2;        // column half of this warpgroup
+    const int wq = warp & 3;         // TMEM lane quarter
+    const int row_in_tile = wq * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem_base + lane_off;
+    const uint32_t tdP = tS + 128;
+    const uint32_t tA0 = tS + 256, tA1 = tS + 256 + D;
+    const int col0 = wg * 64;
+    const float sc = p.scale_log2;
+    // token and head of a packed tile's row: this thread's in kDQ; in kDKDV that of the column
+    // whose constants it loads
+    const int packed_row = kDKDV ? static_cast<int>(threadIdx.x) : row_in_tile;
+    const int my_token = packed_row / p.G, my_head = packed_row - my_token * p.G;
+    uint32_t s_cnt = 0, item_cnt = 0, h_cnt = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int w = ring_get(ring, static_cast<uint32_t>(k), abort_flag, p);
+      if (w < 0) { ok = false; break; }
+      if (w >= order.n) break;
+      BItem it;
+      decode_bitem<kDKDV>(p, order, w, it);
+      // This thread's row: a key, or a token and a head.  One that is not stored sees
+      // everything, so that it does not hold its warp to the masked pass.
+      const int row_token = kDKDV ? row_in_tile : my_token;
+      const bool row_valid = row_token < it.tokens;
+      const int token = it.t0 + row_token;
+      const size_t row = static_cast<size_t>(it.row0) + token;
+      const int head = kDKDV ? it.hk : it.hk * p.G + my_head;
+      const int seen = !row_valid ? INT_MAX / 2 : p.causal ? token + 1 : it.len;  // kDQ: keys
+      const int from = kDKDV && row_valid && p.causal ? token : 0;  // kDKDV: the first query
+      float lse2_r = 0.f, d_r = 0.f;     // kDQ: per-row constants
+      if (!kDKDV && row_valid) {
+        lse2_r = __ldg(p.lse + static_cast<size_t>(head) * p.T + row) * kLog2e;
+        d_r = p.delta[row * p.Hq + head];
+      }
+      for (int f = it.x_lo; f <= it.x_hi; ++f) {
+        const int xs = f * x_tokens;  // first streamed token
+        const int tokens = min(x_tokens, it.len - xs);
+        const int buf = static_cast<int>(s_cnt & 1u);
+        const uint32_t use = s_cnt >> 1;  // uses of this buffer before this one
+        if (kDKDV) {
+          // Per-column constants of the streamed query tile, shared by all
+          // rows: warps 0-3 write them once the previous user of the buffer
+          // is done, every softmax warp waits for them (all waits bounded).
+          if (threadIdx.x < kT) {
+            if (use > 0 &&
+                !wait_warp(bar(kVecFree + buf), (use - 1u) & 1u, abort_flag, p)) { ok = false; break; }
+            // Rows behind the tile's last: P = 2^-inf = 0 where the scores are finite.
+            const bool there = my_token < tokens;
+            const size_t q = static_cast<size_t>(it.row0) + xs + my_token;
+            const int h = it.hk * p.G + my_head;
+            vec[(buf * 2 + 0) * kT + threadIdx.x] =
+                there ? -__ldg(p.lse + static_cast<size_t>(h) * p.T + q) * kLog2e : -INFINITY;
+            vec[(buf * 2 + 1) * kT + threadIdx.x] = there ? -p.delta[q * p.Hq + h] : 0.f;
+            ptx::mbar_arrive(bar(kVecFull + buf));
+          }
+          if (!wait_warp(bar(kVecFull + buf), use & 1u, abort_flag, p)) { ok = false; break; }
+        }
+        // The columns that the row sees.  A packed tile of all its tokens ends in zero rows of Q
+        // and dO, which need no mask (their P is 0 by their constant).
+        const int c_lo = kDKDV ? max(from - xs, 0) * p.G : 0;
+        const int c_hi = kDKDV ? (tokens == x_tokens ? kT : tokens * p.G) - 1 : seen - xs - 1;
+        if constexpr (!kDKDV) {
+          const uint32_t n = s_cnt;
+          if (!wait_warp(bar(kSFull), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
+          ++s_cnt;
+          ptx::tc_fence_after();
+          // Read all of this half of S and dP, release them for the next
+          // step's products, then form dS into buffer n % 2.
+          uint32_t sv[2][32], dv[2][32];
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch) {
+            ptx::tmem_ld32(tS + col0 + ch * 32, sv[ch]);
+            ptx::tmem_ld32(tdP + col0 + ch * 32, dv[ch]);
+          }
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch) {
+            ptx::reg_fence(sv[ch]);
+            ptx::reg_fence(dv[ch]);
+          }
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(kSConsumed));
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch) {
+            const int c0 = col0 + ch * 32;
+            uint32_t pk_s[16];
+            if (__all_sync(0xffffffffu, c_lo <= c0 && c_hi >= c0 + 31)) {
+              // every column visible to every row of the warp: paired fp32
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                float e0, e1, g0, g1;
+                ptx::fma_f32x2(e0, e1, __uint_as_float(sv[ch][2 * x]), __uint_as_float(sv[ch][2 * x + 1]),
+                               sc, sc, -lse2_r, -lse2_r);
+                const float p0 = ptx::ex2(e0), p1 = ptx::ex2(e1);
+                ptx::fma_f32x2(g0, g1, __uint_as_float(dv[ch][2 * x]), __uint_as_float(dv[ch][2 * x + 1]),
+                               1.f, 1.f, -d_r, -d_r);
+                ptx::fma_f32x2(g0, g1, p0, p1, g0, g1, 0.f, 0.f);
+                pk_s[x] = ptx::pack_bf16(g0, g1);
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                float dsr[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int cc = c0 + 2 * x + e;
+                  const bool vis = cc >= c_lo && cc <= c_hi;
+                  const float pv =
+                      vis ? ptx::ex2(fmaf(__uint_as_float(sv[ch][2 * x + e]), sc, -lse2_r)) : 0.f;
+                  dsr[e] = vis ? pv * (__uint_as_float(dv[ch][2 * x + e]) - d_r) : 0.f;
+                }
+                pk_s[x] = ptx::pack_bf16(dsr[0], dsr[1]);
+              }
+            }
+            ptx::tmem_st16(tmem_base + lane_off + kDsBuf + (n & 1u) * 64u + c0 / 2, pk_s);
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(kPReady + (n & 1u)));
+          continue;
+        }
+        ++s_cnt;  // query tiles seen: selects the per-column buffer
+        // The two 64-query halves of this tile; half m uses TMEM buffer m % 2.
+        const int halves = f == it.x_hi && tokens < x_tokens && tokens * p.G <= 64 ? 1 : 2;
+        for (int h = 0; h < halves; ++h) {
+          const uint32_t b = h_cnt & 1u;
+          if (!wait_warp(bar(kSFull + b), (h_cnt >> 1) & 1u, abort_flag, p)) { ok = false; break; }
+          ptx::tc_fence_after();
+          // this warpgroup's 32 columns of S^T and dP^T in buffer b
+          const uint32_t tb = tmem_base + lane_off + 128u * b + 32u * static_cast<uint32_t>(wg);
+          uint32_t sv[32], dv[32];
+          ptx::tmem_ld32(tb, sv);
+          ptx::tmem_ld32(tb + 64, dv);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence(sv);
+          ptx::reg_fence(dv);
+          const int c0 = 64 * h + 32 * wg;   // first tile column of this piece
+          uint32_t pk_p[16], pk_s[16];
+          float pf[32];  // this chunk's P in fp32, for dS
+          // per-column -lse2 and -D of this chunk, four columns per load
+          const float4* nl4 = reinterpret_cast<const float4*>(vec + (buf * 2 + 0) * kT + c0);
+          const float4* nd4 = reinterpret_cast<const float4*>(vec + (buf * 2 + 1) * kT + c0);
+          // P^T first: it is stored and announced (kPReady) before dS^T is
+          // formed, so the MMA warp starts dV += P^T dO meanwhile.
+          const bool all_visible = __all_sync(0xffffffffu, c_lo <= c0 && c_hi >= c0 + 31);
+          if (all_visible) {
+            // every column visible to every row of the warp: paired fp32
+#pragma unroll
+            for (int x4 = 0; x4 < 8; ++x4) {
+              const float4 nl = nl4[x4];
+              const float nla[4] = {nl.x, nl.y, nl.z, nl.w};
+#pragma unroll
+              for (int hx = 0; hx < 2; ++hx) {
+                const int x = 2 * x4 + hx;
+                float e0, e1;
+                ptx::fma_f32x2(e0, e1, __uint_as_float(sv[2 * x]), __uint_as_float(sv[2 * x + 1]), sc,
+                               sc, nla[2 * hx], nla[2 * hx + 1]);
+                pf[2 * x] = ptx::ex2(e0);
+                pf[2 * x + 1] = ptx::ex2(e1);
+                pk_p[x] = ptx::pack_bf16(pf[2 * x], pf[2 * x + 1]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int cc = c0 + 2 * x + e;
+                const bool vis = cc >= c_lo && cc <= c_hi;
+                pf[2 * x + e] =
+                    vis ? ptx::ex2(fmaf(__uint_as_float(sv[2 * x + e]), sc, vec[(buf * 2 + 0) * kT + cc]))
+                        : 0.f;
+              }
+              pk_p[x] = ptx::pack_bf16(pf[2 * x], pf[2 * x + 1]);
+            }
+          }
+          ptx::tmem_st16(tb, pk_p);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(kPReady + b));
+          // dS^T = P^T (dP^T - D)
+          if (all_visible) {
+#pragma unroll
+            for (int x4 = 0; x4 < 8; ++x4) {
+              const float4 nd = nd4[x4];
+              const float nda[4] = {nd.x, nd.y, nd.z, nd.w};
+#pragma unroll
+              for (int hx = 0; hx < 2; ++hx) {
+                const int x = 2 * x4 + hx;
+                float g0, g1;
+                ptx::fma_f32x2(g0, g1, __uint_as_float(dv[2 * x]), __uint_as_float(dv[2 * x + 1]), 1.f,
+                               1.f, nda[2 * hx], nda[2 * hx + 1]);
+                ptx::fma_f32x2(g0, g1, pf[2 * x], pf[2 * x + 1], g0, g1, 0.f, 0.f);
+                pk_s[x] = ptx::pack_bf16(g0, g1);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              float dsr[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int cc = c0 + 2 * x + e;
+                const bool vis = cc >= c_lo && cc <= c_hi;
+                dsr[e] = vis ? pf[2 * x + e] *
+                                   (__uint_as_float(dv[2 * x + e]) + vec[(buf * 2 + 1) * kT + cc])
+                             : 0.f;
+              }
+              pk_s[x] = ptx::pack_bf16(dsr[0], dsr[1]);
+            }
+          }
+          ptx::tmem_st16(tb + 64, pk_s);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(kPReadyS + b));
+          ++h_cnt;
+        }
+        if (!ok) break;
+        ptx::mbar_arrive(bar(kVecFree + buf));
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- epilogue
+      if (!wait_warp(bar(kAccFull), item_cnt & 1u, abort_flag, p)) { ok = false; break; }
+      ++item_cnt;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int a = 0; a < (kDKDV ? 2 : 1); ++a) {
+        const uint32_t tacc = a == 0 ? tA0 : tA1;
+        __nv_bfloat16* g = a == 0 ? p.g0 : p.g1;
+        const float fac = (kDKDV && a == 0) ? 1.f : p.scale;  // dV unscaled; dK, dQ / sqrt(d)
+        const long long(&gs)[2] = a == 0 ? p.gs0 : p.gs1;
+        uint4* dst = reinterpret_cast<uint4*>(g + static_cast<long long>(row) * gs[0] + head * gs[1]);
+#pragma unroll
+        for (int ch = 0; ch < D / 64; ++ch) {
+          const int c0 = wg * (D / 2) + ch * 32;
+          uint32_t ov[32];
+          ptx::tmem_ld32(tacc + c0, ov);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence(ov);
+          if (row_valid) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint4 v4;
+              v4.x = ptx::pack_bf16(__uint_as_float(ov[8 * x + 0]) * fac, __uint_as_float(ov[8 * x + 1]) * fac);
+              v4.y = ptx::pack_bf16(__uint_as_float(ov[8 * x + 2]) * fac, __uint_as_float(ov[8 * x + 3]) * fac);
+              v4.z = ptx::pack_bf16(__uint_as_float(ov[8 * x + 4]) * fac, __uint_as_float(ov[8 * x + 5]) * fac);
+              v4.w = ptx::pack_bf16(__uint_as_float(ov[8 * x + 6]) * fac, __uint_as_float(ov[8 * x + 7]) * fac);
+              dst[c0 / 8 + x] = v4;
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    ptx::tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+template <int D, bool kDKDV>
+cudaError_t launch_packed_bwd(const PackedArgs& a, BParams p, const PackedList& list,
+                              const void* dout, bool dependent, cudaStream_t stream) {
+  using Lay = BLayout<D, kDKDV>;
+  static_assert(Lay::kAlloc <= 232448, "shared memory budget");
+  static_assert(Lay::kX0Slots <= 3 && Lay::kX1Slots == 2, "barrier slots");
+  const auto kern = packed_bwd_kernel<D, kDKDV>;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), Lay::kAlloc);
+  if (e != cudaSuccess) return e;
+  // kDQ: fixed (Q, dO), streamed (K, V); kDKDV: fixed (K, V), streamed (Q, dO)
+  CUtensorMap mq, mg, mk, mv;
+  if (!packed_map(&mq, a.q, a.T, a.Hq, D, a.qs[0], a.qs[1], p.G, p.tq) ||
+      !packed_map(&mg, dout, a.T, a.Hq, D, static_cast<long long>(a.Hq) * D, D, p.G, p.tq) ||
+      !packed_map(&mk, a.k, a.T, a.Hk, D, a.ks[0], a.ks[1], 1, kT) ||
+      !packed_map(&mv, a.v, a.T, a.Hk, D, a.vs[0], a.vs[1], 1, kT))
+    return cudaErrorInvalidValue;
+  p.head = list.head;
+  p.items = list.items;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(
+      sm_count(), packed_items(a.T, p.n_seqs, list.tokens) * a.Hk)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Lay::kAlloc;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = dependent ? 1 : 0;
+  count_launch(0);
+  return kDKDV ? cudaLaunchKernelEx(&cfg, kern, mk, mv, mq, mg, p)
+               : cudaLaunchKernelEx(&cfg, kern, mq, mg, mk, mv, p);
+}
+
+// dK/dV on `stream`, dQ beside it on the library's second stream, whose CTAs take the SMs that
+// the last dK/dV items leave idle; both after the plan.
+template <int D>
+cudaError_t launch_packed_pair(const PackedArgs& a, const BParams& dkdv, const BParams& dq,
+                               const PackedPlan& plan, const void* dout, cudaStream_t stream) {
+  const cudaStream_t side = bwd_side_stream();
+  if (!side) return cudaErrorUnknown;
+  cudaEvent_t ready = nullptr, dq_done = nullptr;
+  if (cudaEventCreateWithFlags(&ready, cudaEventDisableTiming) != cudaSuccess)
+    return cudaErrorUnknown;
+  if (cudaEventCreateWithFlags(&dq_done, cudaEventDisableTiming) != cudaSuccess) {
+    cudaEventDestroy(ready);
+    return cudaErrorUnknown;
+  }
+  cudaError_t e = cudaEventRecord(ready, stream);
+  if (e == cudaSuccess) e = launch_packed_bwd<D, true>(a, dkdv, plan.list[0], dout, true, stream);
+  if (e == cudaSuccess) e = cudaStreamWaitEvent(side, ready, 0);
+  if (e == cudaSuccess) e = launch_packed_bwd<D, false>(a, dq, plan.list[1], dout, false, side);
+  if (e == cudaSuccess) e = cudaEventRecord(dq_done, side);
+  if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, dq_done, 0);
+  // (destroying a recorded event releases it once the work it marks is done)
+  cudaEventDestroy(ready);
+  cudaEventDestroy(dq_done);
+  return e;
+}
+
+// Byte offsets of the workspace's parts: the lists of key tiles and of query tiles, and D.
+struct Space {
+  long long keys, queries, delta, total;
+  Space(int T, int n, int Hq, int tq) {
+    const auto up = [](long long x) { return (x + 255) / 256 * 256; };
+    keys = 0;
+    queries = up(packed_list_bytes(T, n, kT));
+    delta = queries + up(packed_list_bytes(T, n, tq));
+    total = delta + up(4LL * T * Hq);
+  }
+};
+
+}  // namespace
+}  // namespace cpring
+
+extern "C" {
+
+int64_t cp_packed_attn_bwd_workspace_bytes(int T, int n_seqs, int Hq, int Hk, int d) {
+  if (cpring::check_packed(T, n_seqs, Hq, Hk, d, 0) != CP_OK) return -1;
+  return cpring::Space(T, n_seqs, Hq, cpring::kTileRows / (Hq / Hk)).total;
+}
+
+cp_status cp_packed_attn_bwd(const void* q, const int64_t* q_strides, const void* k,
+                             const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                             const void* out, const float* lse, const void* dout,
+                             const int32_t* seq_offsets, void* dq, const int64_t* dq_strides,
+                             void* dk, const int64_t* dk_strides, void* dv,
+                             const int64_t* dv_strides, int T, int n_seqs, int Hq, int Hk, int d,
+                             int causal, void* workspace, int64_t workspace_bytes,
+                             cudaStream_t stream) {
+  cpring::TraceRange trace_("cp_packed_attn_bwd");
+  using namespace cpring;
+  if (!q || !k || !v || !out || !lse || !dout || !seq_offsets || !dq || !dk || !dv || !workspace)
+    return CP_ERR_NULL;
+  const cp_status st = check_packed(T, n_seqs, Hq, Hk, d, causal);
+  if (st != CP_OK) return st;
+  PackedArgs a{};
+  a.q = q; a.k = k; a.v = v;
+  a.T = T; a.Hq = Hq; a.Hk = Hk;
+  int64_t dqs[2], dks[2], dvs[2];
+  for (const void* t : {q, k, v, out, dout, static_cast<const void*>(dq),
+                        static_cast<const void*>(dk), static_cast<const void*>(dv)})
+    if (!aligned(t, 16)) return CP_ERR_ALIGN;
+  if (!aligned(lse, 4) || !aligned(seq_offsets, 4) || !aligned(workspace, 256) ||
+      !packed_strides(q_strides, Hq, d, a.qs) || !packed_strides(k_strides, Hk, d, a.ks) ||
+      !packed_strides(v_strides, Hk, d, a.vs) || !packed_strides(dq_strides, Hq, d, dqs) ||
+      !packed_strides(dk_strides, Hk, d, dks) || !packed_strides(dv_strides, Hk, d, dvs))
+    return CP_ERR_ALIGN;
+  const int G = Hq / Hk, tq = kTileRows / G;
+  const Space sp(T, n_seqs, Hq, tq);
+  if (workspace_bytes < sp.total) return CP_ERR_BUFFER;
+  if (device_cc() != 103) return CP_ERR_DEVICE;
+  char* const ws = static_cast<char*>(workspace);
+  PackedPlan plan{};
+  plan.list[0] = packed_list(ws + sp.keys, T, n_seqs, kT, true);
+  plan.list[1] = packed_list(ws + sp.queries, T, n_seqs, tq, false);
+  plan.lists = 2;
+  plan.offsets = seq_offsets;
+  plan.n = n_seqs; plan.T = T; plan.causal = causal;
+  plan.n_buckets = packed_buckets(T);
+  plan.out = out; plan.dout = dout;
+  plan.delta = reinterpret_cast<float*>(ws + sp.delta);
+  plan.rows = static_cast<long long>(T) * Hq;
+  plan.d = d;
+  plan.err = device_error_word();
+  if (!plan.err) return CP_ERR_CUDA;
+  if (launch_packed_plan(plan, stream) != cudaSuccess) return CP_ERR_CUDA;
+  BParams p{};
+  p.T = T; p.n_seqs = n_seqs; p.Hq = Hq; p.Hk = Hk; p.G = G; p.tq = tq; p.causal = causal;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
+  p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
+  p.lse = lse;
+  p.delta = plan.delta;
+  p.err = plan.err;
+  p.timeout_ns = test_wait_limit_ns();
+  p.fault_drop = test_fault_drop();
+  BParams pq = p;
+  p.g0 = static_cast<__nv_bfloat16*>(dv);
+  p.g1 = static_cast<__nv_bfloat16*>(dk);
+  pq.g0 = static_cast<__nv_bfloat16*>(dq);
+  for (int i = 0; i < 2; ++i) {
+    p.gs0[i] = dvs[i];
+    p.gs1[i] = dks[i];
+    pq.gs0[i] = dqs[i];
+  }
+  const cudaError_t e = d == 128 ? launch_packed_pair<128>(a, p, pq, plan, dout, stream)
+                                 : launch_packed_pair<64>(a, p, pq, plan, dout, stream);
+  return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,164 @@
+// The plan of a call over packed prompts: every sequence's tiles in a list, the most
+// expensive first.
+//
+// For the backward the launch's other blocks form D = rowsum(dO * O), which is bound by its
+// two reads.
+//
+// One block per list.  The sequences' tiles are counted and summed, and the tiles are
+// sorted by cost (key tiles that a query tile sees, or the reverse) by counting: each
+// finds its sequence by bisection of the sums.  Ties keep no order, which decides only
+// the CTA that computes an item, never a result.  Bound by the latency of its few passes.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "packed.cuh"
+
+namespace cpring {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kWarps = kPlanThreads / 32;
+constexpr int kSmall = 2048;  // sums and buckets up to this many stay in shared memory
+
+// Exclusive sum over the block; `total` gets the whole.
+__device__ __forceinline__ int block_scan(int x, int* warp_sum, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  __syncthreads();  // an earlier call's sums are read
+  if (lane == 31) warp_sum[warp] = y;
+  __syncthreads();
+  int s = warp_sum[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += z;
+  }
+  total = __shfl_sync(0xffffffffu, s, kWarps - 1);
+  const int before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+  return y - x + (warp > 0 ? before : 0);
+}
+
+// D of rows dealt over `blocks` blocks: 8 entries to a lane, d / 8 lanes to a row.
+__device__ __forceinline__ void row_dots(const PackedPlan& p, int block, int blocks) {
+  const int lanes = p.d / 8;
+  const long long vecs = p.rows * lanes, step = static_cast<long long>(blocks) * kPlanThreads;
+  const uint4* const out = static_cast<const uint4*>(p.out);
+  const uint4* const dout = static_cast<const uint4*>(p.dout);
+  const long long end = (vecs + 31) / 32 * 32;  // whole warps
+  for (long long x = static_cast<long long>(block) * kPlanThreads + threadIdx.x; x < end;
+       x += step) {
+    float s = 0.f;
+    if (x < vecs) {
+      const uint4 a = __ldg(out + x), b = __ldg(dout + x);
+      const uint32_t u[4] = {a.x, a.y, a.z, a.w}, w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(w[i] << 16), s);
+        s = fmaf(__uint_as_float(u[i] & 0xffff0000u), __uint_as_float(w[i] & 0xffff0000u), s);
+      }
+    }
+    for (int o = lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (x < vecs && x % lanes == 0) p.delta[x / lanes] = s;
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedPlan p) {
+  __shared__ int warp_sum[kWarps];
+  __shared__ int near_starts[kSmall], near_buckets[kSmall];
+  cudaTriggerProgrammaticLaunchCompletion();  // the attention's blocks may line up
+  if (blockIdx.x >= p.lists) {
+    row_dots(p, blockIdx.x - p.lists, gridDim.x - p.lists);
+    return;
+  }
+  const PackedList l = p.list[blockIdx.x];
+  int* const starts = p.n <= kSmall ? near_starts : l.starts;
+  int* const buckets = p.n_buckets <= kSmall ? near_buckets : l.buckets;
+  for (int i = threadIdx.x; i < p.n_buckets; i += kPlanThreads) buckets[i] = 0;
+  int items = 0;
+  bool bad = false;
+  for (int base = 0; base < p.n; base += kPlanThreads) {
+    const int i = base + threadIdx.x;
+    int tiles = 0;
+    if (i < p.n) {
+      const int a = __ldg(p.offsets + i), z = __ldg(p.offsets + i + 1);
+      if (a < 0 || z < a || z > p.T)
+        bad = true;
+      else
+        tiles = (z - a + l.tokens - 1) / l.tokens;
+    }
+    int total;
+    const int before = block_scan(tiles, warp_sum, total);
+    if (i < p.n) starts[i] = items + before;
+    items += total;
+  }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) {
+      l.head[0] = l.head[1] = 0;
+      atomicOr(p.err, kErrDocOffsets);
+    }
+    return;
+  }
+  if (threadIdx.x == 0) {
+    l.head[0] = items;
+    l.head[1] = 0;
+  }
+  // Item x: its sequence's rows, its tile, and the bucket of its cost (0: the largest).
+  auto item = [&](int x, int& bucket) {
+    int lo = 0, hi = p.n;  // the last sequence that starts at or before x; empty ones are passed
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= x) lo = mid; else hi = mid;
+    }
+    const int row = __ldg(p.offsets + lo), len = __ldg(p.offsets + lo + 1) - row;
+    const int tile = x - starts[lo];
+    int cost = len;
+    if (p.causal)
+      cost = l.of_keys ? len - tile * l.tokens
+                       : static_cast<int>(min(static_cast<long long>(len),
+                                              (tile + 1LL) * l.tokens));
+    bucket = p.n_buckets - 1 - (cost + kCostUnit - 1) / kCostUnit;
+    return make_int4(row, len, tile, 0);
+  };
+  for (int x = threadIdx.x; x < items; x += kPlanThreads) {
+    int b;
+    item(x, b);
+    atomicAdd(buckets + b, 1);
+  }
+  __syncthreads();
+  int placed = 0;
+  for (int base = 0; base < p.n_buckets; base += kPlanThreads) {
+    const int i = base + threadIdx.x;
+    const int x = i < p.n_buckets ? buckets[i] : 0;
+    int total;
+    const int before = block_scan(x, warp_sum, total);
+    if (i < p.n_buckets) buckets[i] = placed + before;
+    placed += total;
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < items; x += kPlanThreads) {
+    int b;
+    const int4 it = item(x, b);
+    l.items[atomicAdd(buckets + b, 1)] = it;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_packed_plan(const PackedPlan& p, cudaStream_t stream) {
+  unsigned blocks = p.lists;
+  if (p.delta) {
+    const long long want = (p.rows * (p.d / 8) + kPlanThreads - 1) / kPlanThreads;
+    blocks += static_cast<unsigned>(std::min<long long>(want, 2LL * sm_count()));
+  }
+  packed_plan_kernel<<<blocks, kPlanThreads, 0, stream>>>(p);
+  count_launch(2);
+  return cudaGetLastError();
+}
+
+}  // namespace cpring

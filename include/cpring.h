@@ -636,6 +636,67 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
                                cudaStream_t stream);
 
 /*
+ * Attention over packed prompts of different lengths with grouped heads: what a
+ * layer's prefill runs before cp_paged_append and cp_paged_attn_decode, and its training
+ * forward.  (The masks of packed samples: "Context Parallel", 基本机制 and 常见失败模式; the
+ * softmax over key tiles: "上下文並行", 線上 Softmax.)  Sequence s holds the rows
+ * [seq_offsets[s], seq_offsets[s + 1]) of q, k and v; a row sees the keys of its own
+ * sequence (causal: up to its own position); head h reads key head h / (Hq / Hk).
+ *  q, k, v    device, bf16 [T,Hq,d], [T,Hk,d], [T,Hk,d], read.
+ *  q_strides, k_strides, v_strides   host, two strides in elements (row, head; the d
+ *             entries are contiguous), or NULL = contiguous: the three may be views of
+ *             one projection's output.  The head's a multiple of d, the row's a multiple
+ *             of the head's and at least H times it (CP_ERR_ALIGN otherwise).
+ *  seq_offsets  device int32 [n_seqs + 1]: 0 <= o_0 <= o_1 <= ... <= o_n <= T (others:
+ *             nothing is written, and cp_get_last_status reports
+ *             CP_ERR_DOC_OFFSETS).  Sequences may be empty.
+ *  out        device, bf16 [T,Hq,d] contiguous, written.
+ *  lse        device, fp32 [Hq,T], written: natural log.
+ *             Rows of no sequence are left as they were in both.  What q, k and v hold
+ *             there, whatever it is, reaches no output; an infinite or NaN key or value
+ *             may reach every row of its own sequence.
+ *  T >= 1; n_seqs 1 .. 2^20; Hq % Hk == 0, Hq / Hk <= 128 (else CP_ERR_UNSUPPORTED);
+ *  T * Hq < 2^31, (T + n_seqs) * Hk < 2^30;  d 64 or 128.
+ *  workspace  device, >= cp_packed_attn_fwd_workspace_bytes(...) bytes, 256-byte aligned,
+ *             caller-owned, contents undefined afterwards (calls that can overlap, two
+ *             captured graphs' among them, need one each); too small: CP_ERR_BUFFER.
+ * Two launches; nothing is allocated, and the lengths are read on the device, so a
+ * captured call follows them when it is replayed.
+ */
+int64_t cp_packed_attn_fwd_workspace_bytes(int T, int n_seqs, int Hq, int Hk, int d);
+cp_status cp_packed_attn_fwd(const void* q, const int64_t* q_strides, const void* k,
+                             const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                             const int32_t* seq_offsets, void* out, float* lse, int T, int n_seqs,
+                             int Hq, int Hk, int d, int causal, void* workspace,
+                             int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Backward of cp_packed_attn_fwd: the gradients of sum(out * dout) with respect to q, k and v
+ * ("上下文並行", section 反向傳播), those of a key head summed over the query heads that read
+ * it, in fp32 within one block: the result does not change from run to run.
+ *  q, k, v, seq_offsets, causal   as given to the forward, out and lse as it wrote them.
+ *  dout       device, bf16 [T,Hq,d] contiguous, read.
+ *  dq, dk, dv device, bf16 [T,Hq,d], [T,Hk,d], [T,Hk,d], written; their strides as the inputs',
+ *             so that they may be views of one projection's gradient.  Rows of no
+ *             sequence are left as they were; what the inputs hold there reaches no output.
+ *  workspace  device, >= cp_packed_attn_bwd_workspace_bytes(...) bytes, otherwise as the
+ *             forward's.
+ *  Sizes, alignment and errors as cp_packed_attn_fwd (dq, dk, dv 16 bytes).
+ * Three launches: the plan with D = rowsum(dout * out) and the dK/dV kernel on `stream`, and
+ * the dQ kernel on the library's second stream (cp_ring_attn_bwd), which `stream` then waits
+ * for.  Nothing is allocated.
+ */
+int64_t cp_packed_attn_bwd_workspace_bytes(int T, int n_seqs, int Hq, int Hk, int d);
+cp_status cp_packed_attn_bwd(const void* q, const int64_t* q_strides, const void* k,
+                             const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                             const void* out, const float* lse, const void* dout,
+                             const int32_t* seq_offsets, void* dq, const int64_t* dq_strides,
+                             void* dk, const int64_t* dk_strides, void* dv,
+                             const int64_t* dv_strides, int T, int n_seqs, int Hq, int Hk, int d,
+                             int causal, void* workspace, int64_t workspace_bytes,
+                             cudaStream_t stream);
+
+/*
  * TEST HOOK.  Later cp_paged_attn_decode calls (and their workspace sizes)
  * attend the prefix with the 16-row items of the decode kernel (path 0) or with
  * the tcgen05 kernel (path 1), whatever their sizes; -1 returns to the rule.
