@@ -312,12 +312,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // B = the streamed tile at b_off read MN-major (rows = K).
       auto issue_ts = [&](uint32_t acc, uint32_t a_tmem, int b_off, bool first, int half,
                           int steps) {
-#pragma unroll
-        for (int s = 0; s < kT / 16; ++s) {
-          if (s >= steps) continue;
+        auto step = [&](int s) {
           const uint32_t a_col = static_cast<uint32_t>((s >> 2) * half + (s & 3) * 8);
           ptx::mma_ts_w(acc, a_tmem + a_col, d_mn + (b_off >> 4) + static_cast<uint64_t>(s * 128),
                       kIdescG, (first && s == 0) ? 0u : 1u);
+        };
+        if (steps == kT / 16) {  // without a test between the products
+#pragma unroll
+          for (int s = 0; s < kT / 16; ++s) step(s);
+        } else {
+#pragma unroll 1
+          for (int s = 0; s < steps; ++s) step(s);
         }
       };
       uint32_t n = 0;       // kDQ: steps issued so far (all items)
@@ -336,12 +341,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // acc (+)= A B over 64 queries: A = the two warpgroups' packed pieces
       // (32 columns apart), B = the half tile at b_off read MN-major.
       auto issue_ts64 = [&](uint32_t acc, uint32_t a_tmem, int b_off, bool first, int steps) {
-#pragma unroll
-        for (int s = 0; s < 64 / 16; ++s) {
-          if (s >= steps) continue;
+        auto step = [&](int s) {
           const uint32_t a_col = static_cast<uint32_t>((s >> 1) * 32 + (s & 1) * 8);
           ptx::mma_ts_w(acc, a_tmem + a_col, d_mn + (b_off >> 4) + static_cast<uint64_t>(s * 128),
                       kIdescG, (first && s == 0) ? 0u : 1u);
+        };
+        if (steps >= 4) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) step(s);
+        } else {
+#pragma unroll 1
+          for (int s = 0; s < steps; ++s) step(s);
         }
       };
       for (;;) {

@@ -21,6 +21,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "attn_softmax.cuh"
@@ -256,16 +257,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const uint64_t d_qk = ptx::smem_desc_sw128(sbase, 16, 1024);
     const uint64_t d_v = ptx::smem_desc_sw128(sbase, Lay::kPanelBytes, 1024);
-    // O_t (+)= P_t V over the steps [part * 4, part * 4 + 4) that lie below `steps`: keys
-    // 0-63 (part 0) or 64-127 (part 1), whose P the softmax signals separately.
-    auto issue_pv = [&](int t, uint32_t st, bool first, int part, int steps) {
+    // O_t (+)= P_t V over the steps [part * 4, part * 4 + 4): keys 0-63 (part 0) or 64-127 (part
+    // 1), whose P the softmax signals separately.  kWhole: all of them; otherwise those below
+    // `steps`.  (A test between the products would hold this warp's issue up: with one in every
+    // step the kernel took 1769 us instead of 1479 for 32K tokens of 8/2 heads.)
+    auto issue_pv = [&](auto whole, int t, uint32_t st, bool first, int part, int steps) {
       const uint64_t dv = d_v + ((Lay::kVOff + st * Lay::kTileBytes) >> 4);
+      auto step = [&](int s) {
+        ptx::mma_ts_w(tmem_base + 256 + t * D, tmem_base + t * 128 + s * 8,
+                      dv + static_cast<uint64_t>((s * 16 * 128) >> 4), kIdescPV,
+                      (first && s == 0) ? 0u : 1u);
+      };
+      if constexpr (decltype(whole)::value) {
 #pragma unroll
-      for (int s = part * (kSteps / 2); s < (part + 1) * (kSteps / 2); ++s)
-        if (s < steps)
-          ptx::mma_ts_w(tmem_base + 256 + t * D, tmem_base + t * 128 + s * 8,
-                        dv + static_cast<uint64_t>((s * 16 * 128) >> 4), kIdescPV,
-                        (first && s == 0) ? 0u : 1u);
+        for (int s = part * (kSteps / 2); s < (part + 1) * (kSteps / 2); ++s) step(s);
+      } else {
+#pragma unroll 1
+        for (int s = part * (kSteps / 2); s < min(steps, (part + 1) * (kSteps / 2)); ++s) step(s);
+      }
     };
     // S_t = Q_t K^T (both K-major, 128-byte swizzled panels; a K step is
     // 32 bytes, four steps per panel).
@@ -291,39 +300,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool pend0 = false, pend1 = false;    // an S issued whose PV is still owed
       bool first0 = true, first1 = true;    // next PV overwrites O
       uint32_t prev_st = 0, prev_ph = 0;
-      int prev_keys = kBN;                  // keys of the previous tile that exist
       bool have_prev = false, prev_v_ready = false;
-      // Owed PV of tile t on the previous K/V stage: wait for V (its rows behind the last
-      // key zeroed) and P, issue.  After the item's last PV of tile t, O_t is final.
-      auto flush = [&](int t, uint32_t& pc, bool& first, bool last) -> bool {
+      const int last = max(it.last[0], it.last[1]);
+      // keys of the last tile: fewer than 128 where it is the sequence's last
+      const int last_keys = min(kBN, it.len - last * kBN);
+      // Owed PV of tile t on the previous K/V stage: wait for V and P, issue.  After the item's
+      // last PV of tile t, O_t is final.  kWhole: every key of the tile exists; otherwise V's
+      // rows behind the last key are zeroed first.
+      auto flush = [&](auto whole, int t, uint32_t& pc, bool& first, bool final) -> bool {
         if (!prev_v_ready) {
           if (!wait_warp(bar(kVFull + prev_st), prev_ph, abort_flag, p)) return false;
-          if (prev_keys % 16 != 0) {
-            zero_rows<Lay::kPanels>(sbase + Lay::kVOff + prev_st * Lay::kTileBytes, prev_keys,
-                                    (prev_keys + 15) / 16 * 16);
+          if constexpr (!decltype(whole)::value) {
+            zero_rows<Lay::kPanels>(sbase + Lay::kVOff + prev_st * Lay::kTileBytes, last_keys,
+                                    (last_keys + 15) / 16 * 16);
             ptx::fence_proxy_async_shared();
             __syncwarp();
           }
           prev_v_ready = true;
         }
-        const int steps = (prev_keys + 15) / 16;
+        const int steps = (last_keys + 15) / 16;
         if (!wait_warp(bar(kPReady + t), pc & 1u, abort_flag, p)) return false;
         ptx::tc_fence_after();
-        issue_pv(t, prev_st, first, 0, steps);
+        issue_pv(whole, t, prev_st, first, 0, steps);
         if (!wait_warp(bar(kPReadyB + t), pc & 1u, abort_flag, p)) return false;
         ++pc;
         ptx::tc_fence_after();
-        issue_pv(t, prev_st, false, 1, steps);
-        if (last) ptx::mma_commit_w(bar(kOBar + t));
+        issue_pv(whole, t, prev_st, false, 1, steps);
+        if (final) ptx::mma_commit_w(bar(kOBar + t));
         first = false;
         return true;
       };
-      const int last = max(it.last[0], it.last[1]);
       for (int f = 0; f <= last; ++f) {
         const uint32_t st = kv_iter % kStages;
         const uint32_t ph = (kv_iter / kStages) & 1u;
         if (pend0) {
-          if (!flush(0, p_cnt0, first0, f - 1 == it.last[0])) { ok = false; break; }
+          if (!flush(std::true_type(), 0, p_cnt0, first0, f - 1 == it.last[0])) {
+            ok = false;
+            break;
+          }
           pend0 = false;
         }
         if (!wait_warp(bar(kKFull + st), ph, abort_flag, p)) { ok = false; break; }
@@ -333,7 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           pend0 = true;
         }
         if (pend1) {
-          if (!flush(1, p_cnt1, first1, f - 1 == it.last[1])) { ok = false; break; }
+          if (!flush(std::true_type(), 1, p_cnt1, first1, f - 1 == it.last[1])) {
+            ok = false;
+            break;
+          }
           pend1 = false;
         }
         if (f <= it.last[1]) {
@@ -344,19 +361,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (have_prev) ptx::mma_commit_w(bar(kVEmpty + prev_st));  // V(f-1) read by every PV
         prev_st = st;
         prev_ph = ph;
-        prev_keys = min(kBN, it.len - f * kBN);
         have_prev = true;
         prev_v_ready = false;
         ++kv_iter;
       }
       if (!ok) break;
       ptx::mma_commit_w(bar(kQEmpty));  // every S of this item has been issued
-      if (pend0) {
-        if (!flush(0, p_cnt0, first0, true)) { ok = false; break; }
+      if (last_keys == kBN) {
+        ok = (!pend0 || flush(std::true_type(), 0, p_cnt0, first0, true)) &&
+             (!pend1 || flush(std::true_type(), 1, p_cnt1, first1, true));
+      } else {
+        ok = (!pend0 || flush(std::false_type(), 0, p_cnt0, first0, true)) &&
+             (!pend1 || flush(std::false_type(), 1, p_cnt1, first1, true));
       }
-      if (pend1) {
-        if (!flush(1, p_cnt1, first1, true)) { ok = false; break; }
-      }
+      if (!ok) break;
       if (have_prev) ptx::mma_commit_w(bar(kVEmpty + prev_st));
     }
     // Wait until every MMA this warp issued has finished.
