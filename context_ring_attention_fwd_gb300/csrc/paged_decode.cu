@@ -61,6 +61,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "decode_int4.cuh"
 #include "internal.h"
 #include "paged_decode.h"
 #include "ptx.cuh"
@@ -72,9 +73,12 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kWarpKeys = 16;                    // keys of a tile that a warp owns
 constexpr int kTileKeys = kWarps * kWarpKeys;    // 64
+constexpr int kTileKeys4 = 128;                  // over a cache in 4 bits
 constexpr int kRows = 16;                        // rows of an item
 constexpr int kCtasPerSm = 3;
-constexpr int kMaxGrid = 480;                    // bounds the slots of the workspace
+template <int kNT>
+constexpr int kCtas4 = kNT == 1 ? 4 : 3;         // of paged_decode4_kernel
+constexpr int kMaxGrid = 640;                    // bounds the slots of the workspace
 constexpr int kMaxBatch = 4096;
 // From this many rows on a warp joins a row, four below.  Measured, one / four (us in
 // the kernel): 32 rows of 11 parts 5.3 / 4.4; 2048 rows of 21 parts 9.5 / 11.1;
@@ -85,23 +89,17 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 // One warp's part of a pipeline stage: 16 rows of K, then 16 of V, as 16-byte
 // chunks; chunk c of row r at c ^ (r mod 8) (mod 4 for rows of 64 bytes), so
-// that both ldmatrix and the row-wise reads of codes are conflict-free.  Rows in 4 bits
-// (64 or 32 bytes, two or four to a line of the banks) move their chunks every second or
-// fourth row, and the 16 rows' scales of K, then of V, lie behind them.
+// that both ldmatrix and the row-wise reads of codes are conflict-free.
 template <int D, Held kHeld>
 struct Stage {
-  static constexpr int kRowBytes = kHeld == Held::kBf16 ? 2 * D : kHeld == Held::kE4M3 ? D : D / 2;
-  static constexpr int kScaleBytes = D / kBlock;  // of a row in 4 bits
+  static constexpr int kRowBytes = D * (kHeld == Held::kE4M3 ? 1 : 2);
   static constexpr int kChunks = kRowBytes / 16;
-  static constexpr int kV = kWarpKeys * kRowBytes;  // where V starts
-  static constexpr int kScales = 2 * kV;            // and the scales
-  static constexpr int kBytes = kScales + (kHeld == Held::kInt4 ? 2 * kWarpKeys * kScaleBytes : 0);
+  static constexpr int kBytes = 2 * kWarpKeys * kRowBytes;
   static constexpr int kCount = kBytes >= 8192 ? 2 : 4;
   static constexpr int kRing = kCount * kBytes;  // per warp
-  static constexpr int kSwz = kHeld == Held::kInt4 ? kChunks - 1 : kChunks >= 8 ? 7 : 3;
-  static constexpr int kSwzRows = kHeld == Held::kInt4 ? 8 / kChunks : 1;
+  static constexpr int kSwz = kChunks >= 8 ? 7 : 3;
   __device__ static uint32_t at(uint32_t base, int row, int chunk) {
-    return base + row * kRowBytes + ((chunk ^ (row / kSwzRows & kSwz)) << 4);
+    return base + row * kRowBytes + ((chunk ^ (row & kSwz)) << 4);
   }
 };
 
@@ -113,11 +111,17 @@ __device__ __forceinline__ int common_keys(const DecodeParams& p, int len) {
   return max(0, len - (p.n_q - 1) - p.P);
 }
 
+// Keys of a tile of the kernel that attends a cache of this form.
+__host__ __device__ constexpr int tile_keys_of(Held held) {
+  return held == Held::kInt4 ? kTileKeys4 : kTileKeys;
+}
+
 // Units of sequence b's items.
+template <int kKeys>
 __device__ __forceinline__ unsigned own_units(const DecodeParams& p, int b) {
   const int n = common_keys(p, __ldg(p.seq_lens + b));
   return n <= 0 ? 0u
-                : (static_cast<unsigned>((n + kTileKeys - 1) / kTileKeys) + kItemCost) *
+                : (static_cast<unsigned>((n + kKeys - 1) / kKeys) + kItemCost) *
                       static_cast<unsigned>(p.Hk * p.own_tiles_of_rows);
 }
 
@@ -164,45 +168,16 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-// What a head's codes are multiplied by (x: 0 K, 1 V).
-template <Held kHeld>
-__device__ __forceinline__ float head_descale(const DecodeParams& p, int x, int hk) {
-  if (kHeld == Held::kBf16 || (kHeld == Held::kInt4 && p.descale[x] == nullptr)) return 1.f;
-  return __ldg(p.descale[x] + hk);
-}
-
-// kBytes (4 or 8) to shared memory, or zeros.
-template <int kBytes>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src),
-               "r"(there ? kBytes : 0), "n"(kBytes)
-               : "memory");
-}
-
-template <int D, Held kHeld>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const DecodeParams p) {
-  using St = Stage<D, kHeld>;
-  constexpr bool kE4M3 = kHeld == Held::kE4M3, kInt4 = kHeld == Held::kInt4;
-  constexpr int kK = D / 16;   // k-steps of S = Q K^T
-  constexpr int kN = D / 8;    // 8-column tiles of O
-  constexpr bool kF16 = kE4M3 || kInt4;         // both products in fp16
-  constexpr float kShift = kF16 ? 15.f : 0.f;   // P is held times 2^kShift
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ unsigned scan[kWarps];
-  __shared__ float merge_ml[kWarps][kRows][2];
+// The sequences' first units in `starts` (every CTA scans the lengths; CTA 0 keeps the
+// result for the join); returns the units of all.
+template <int kKeys>
+__device__ __forceinline__ unsigned lay_out(const DecodeParams& p, unsigned prefix_all,
+                                            unsigned* starts, unsigned* scan) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quad = lane >> 2, c4 = lane & 3;
-  const uint32_t ring = ptx::smem_u32(smem) + warp * St::kRing;
-
-  cudaTriggerProgrammaticLaunchCompletion();  // the next kernel's blocks may line up
-  // ---- the sequences' first units (every CTA scans the lengths; CTA 0 keeps
-  // the result for the join) and this CTA's stretch
-  const unsigned prefix_all = prefix_units(p);
-  unsigned* const starts = reinterpret_cast<unsigned*>(smem + kWarps * St::kRing);
   unsigned run = prefix_all;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    const unsigned n = b < p.B ? own_units(p, b) : 0u;
+    const unsigned n = b < p.B ? own_units<kKeys>(p, b) : 0u;
     unsigned x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -228,17 +203,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
     if (blockIdx.x == 0) p.starts[p.B] = W;
   }
   __syncthreads();
-  const unsigned g = min(gridDim.x, W);
-  if (blockIdx.x >= g) return;
-  unsigned w = stretch(blockIdx.x, W, g);
-  const unsigned w_end = stretch(blockIdx.x + 1, W, g);
+  return W;
+}
 
-  while (w < w_end) {
-    // ---- the item that holds unit w
-    bool prefix;
-    int b0, hk, row0, rows, n_keys, base_pos;
-    unsigned n_tiles, u0;
-    const int32_t* pages;
+// The item that holds unit w, and the unit's place in it.
+struct Item {
+  bool prefix;
+  int b0, hk, row0, rows, n_keys, base_pos;
+  unsigned n_tiles, u0;
+  const int32_t* pages;
+  __device__ __forceinline__ Item(const DecodeParams& p, const unsigned* starts,
+                                  unsigned prefix_all, unsigned w, int tile_keys) {
     if (w < prefix_all) {
       prefix = true;
       n_tiles = p.prefix_tiles;
@@ -260,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       }
       b0 = lo;
       n_keys = common_keys(p, __ldg(p.seq_lens + b0));
-      n_tiles = (n_keys + kTileKeys - 1) / kTileKeys;
+      n_tiles = (n_keys + tile_keys - 1) / tile_keys;
       const unsigned local = w - starts[b0];
       const unsigned item = local / (n_tiles + kItemCost);
       u0 = local - item * (n_tiles + kItemCost);
@@ -270,6 +245,105 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       base_pos = p.P;
       pages = p.table + b0 * p.table_stride;
     }
+  }
+};
+
+// The item's state, or its part of it over the tiles [t0, t1), from the four warps': sums
+// [warp][16 rows][kPitch] that share a reference, and (m, l) of each; l is NaN for a bad page.
+template <int D>
+constexpr int kPitch = D + 8;  // floats; staggers the rows over the banks
+template <int D, bool kShifted>
+__device__ __forceinline__ void write_item(const DecodeParams& p, const Item& it, int t0, int t1,
+                                           const float* mo, const float (&merge_ml)[kWarps][kRows][2],
+                                           bool any_bad, float vd) {
+  constexpr float kShift = kShifted ? 15.f : 0.f;
+      const bool complete = t0 == 0 && static_cast<unsigned>(t1) == it.n_tiles;
+      const bool direct = complete && !it.prefix && p.P == 0 && p.n_q == 1;
+      constexpr int kVecs = D / 4;  // 4-column vectors of a row
+      for (int x = threadIdx.x; x < it.rows * kVecs; x += kThreads) {
+        const int r = x / kVecs, col = (x % kVecs) * 4;
+        float big = -INFINITY, l = 0.f;
+  #pragma unroll
+        for (int y = 0; y < kWarps; ++y) big = fmaxf(big, merge_ml[y][r][0]);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  #pragma unroll
+        for (int y = 0; y < kWarps; ++y) {
+          const float my = merge_ml[y][r][0];
+          // an empty state's l is 0, or NaN where its scores were
+          l += merge_ml[y][r][1] * (my == -INFINITY ? 1.f : ptx::ex2(my - big));
+          const float4 a = *reinterpret_cast<const float4*>(mo + (y * kRows + r) * kPitch<D> + col);
+          sum.x += a.x;
+          sum.y += a.y;
+          sum.z += a.z;
+          sum.w += a.w;
+        }
+        if (any_bad) l = NAN;
+        const RowOf row(p, it.b0, it.hk, it.row0 + r);
+        if (direct) {
+          const float inv = l == 0.f ? 0.f : vd / l;
+          uint2 v;
+          v.x = ptx::pack_bf16(sum.x * inv, sum.y * inv);
+          v.y = ptx::pack_bf16(sum.z * inv, sum.w * inv);
+          *reinterpret_cast<uint2*>(p.out + row.index(p) * D + col) = v;
+          if (col == 0)
+            p.lse[(static_cast<long long>(row.b) * p.Hq + row.h) * p.n_q + row.i] =
+                (big - kShift + log2f(l)) * kLn2;
+          continue;
+        }
+        float *to, *ml;
+        if (complete) {
+          const long long at = (it.prefix ? static_cast<long long>(p.B) * p.n_q * p.Hq : 0) +
+                               row.index(p);
+          to = p.whole_o + at * D;
+          ml = p.whole_ml + at * 2;
+        } else {
+          const long long at = (static_cast<long long>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0)) * kRows + r;
+          to = p.slot_o + at * D;
+          ml = p.slot_ml + at * 2;
+        }
+        *reinterpret_cast<float4*>(to + col) = make_float4(sum.x * vd, sum.y * vd, sum.z * vd,
+                                                           sum.w * vd);
+        if (col == 0) *reinterpret_cast<float2*>(ml) = make_float2(big - kShift, l);
+      }
+}
+
+// What a head's codes are multiplied by (x: 0 K, 1 V).
+template <Held kHeld>
+__device__ __forceinline__ float head_descale(const DecodeParams& p, int x, int hk) {
+  if (kHeld == Held::kBf16 || (kHeld == Held::kInt4 && p.descale[x] == nullptr)) return 1.f;
+  return __ldg(p.descale[x] + hk);
+}
+
+template <int D, Held kHeld>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(const DecodeParams p) {
+  using St = Stage<D, kHeld>;
+  static_assert(kHeld != Held::kInt4, "paged_decode4_kernel's");
+  constexpr bool kE4M3 = kHeld == Held::kE4M3;
+  constexpr int kK = D / 16;   // k-steps of S = Q K^T
+  constexpr int kN = D / 8;    // 8-column tiles of O
+  constexpr float kShift = kE4M3 ? 15.f : 0.f;  // P is held times 2^kShift
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ unsigned scan[kWarps];
+  __shared__ float merge_ml[kWarps][kRows][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = lane >> 2, c4 = lane & 3;
+  const uint32_t ring = ptx::smem_u32(smem) + warp * St::kRing;
+
+  cudaTriggerProgrammaticLaunchCompletion();  // the next kernel's blocks may line up
+  const unsigned prefix_all = prefix_units(p);
+  unsigned* const starts = reinterpret_cast<unsigned*>(smem + kWarps * St::kRing);
+  const unsigned W = lay_out<kTileKeys>(p, prefix_all, starts, scan);
+  const unsigned g = min(gridDim.x, W);
+  if (blockIdx.x >= g) return;
+  unsigned w = stretch(blockIdx.x, W, g);
+  const unsigned w_end = stretch(blockIdx.x + 1, W, g);
+
+  while (w < w_end) {
+    const Item it(p, starts, prefix_all, w, kTileKeys);
+    const int b0 = it.b0, hk = it.hk, row0 = it.row0, rows = it.rows, n_keys = it.n_keys,
+              base_pos = it.base_pos;
+    const unsigned n_tiles = it.n_tiles, u0 = it.u0;
+    const int32_t* const pages = it.pages;
     const unsigned u1 = min(n_tiles + kItemCost, u0 + (w_end - w));
     const int t0 = tile_of_unit(u0), t1 = tile_of_unit(u1);
     w += u1 - u0;
@@ -312,18 +386,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
           for (int i = 0; i < kWarpKeys / kPerStep; ++i) {
             const int key = i * kPerStep + lane / St::kChunks;
             const long long o = __shfl_sync(0xffffffffu, off[x], key);
-            cp_async16(St::at(dst + x * St::kV, key, chunk),
+            cp_async16(St::at(dst + x * (St::kBytes / 2), key, chunk),
                        p.cache[x] + o + chunk * 16, (held >> key & 1u) ? 16 : 0);
           }
-        }
-        if (kInt4) {  // lane l: the scales of key l % 16, of K or of V
-          const int key = lane % kWarpKeys, x = lane / kWarpKeys;
-          const int page = __shfl_sync(0xffffffffu, at.page, key);
-          const int slot = __shfl_sync(0xffffffffu, at.slot, key);
-          const bool there = held >> key & 1u;
-          const long long o = there ? page * p.ss[x][0] + slot * p.ss[x][1] + hk * p.ss[x][2] : 0;
-          cp_async_small<St::kScaleBytes>(
-              dst + St::kScales + (x * kWarpKeys + key) * St::kScaleBytes, p.scales[x] + o, there);
         }
       }
       cp_commit();
@@ -345,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       const RowOf r1(p, b0, hk, min(row0 + quad + 8, row0 + rows - 1));
       const __nv_bfloat16* const q0 = r0.query(p);
       const __nv_bfloat16* const q1 = r1.query(p);
-      if (!kF16) {
+      if (!kE4M3) {
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
           qf[k][0] = *reinterpret_cast<const uint32_t*>(q0 + k * 16 + c4 * 2);
@@ -380,11 +445,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
           (x ? sc1 : sc0) = p.scale * desc * down;
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
-            // 4 bits: a word's codes i and i + 4 come as a pair
-            const int at = kInt4 ? 8 * (k / 2) + 2 * (k % 2) : 4 * k;
-            constexpr int kNext = kInt4 ? 4 : 1, kSecond = kInt4 ? 1 : 2;
-            qf[k][x] = pack_f16(z[at] * up, z[at + kNext] * up);
-            qf[k][2 + x] = pack_f16(z[at + kSecond] * up, z[at + kSecond + kNext] * up);
+            qf[k][x] = pack_f16(z[4 * k] * up, z[4 * k + 1] * up);
+            qf[k][2 + x] = pack_f16(z[4 * k + 2] * up, z[4 * k + 3] * up);
           }
         }
       }
@@ -401,41 +463,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       load(t + St::kCount - 1, stage == 0 ? St::kCount - 1 : stage - 1, next);
       next = look_up(t + St::kCount);
       const uint32_t ks = ring + stage * St::kBytes;
-      const uint32_t vs = ks + St::kV;
+      const uint32_t vs = ks + St::kBytes / 2;
       if (++stage == St::kCount) stage = 0;
       // ---- S: two 8-key tiles
       float s[2][4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-      if (kInt4) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int row = j * 8 + quad;
-          uint32_t u[D / 32], two;  // the lane's quarter of the row, and its scales
-          if constexpr (D == 128)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                         : "r"(St::at(ks, row, c4)));
-          else
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                         : "=r"(u[0]), "=r"(u[1])
-                         : "r"(St::at(ks, row, c4 / 2) + c4 % 2 * 8));
-          const uint32_t at = ks + St::kScales + row * St::kScaleBytes;
-          if constexpr (D == 128)
-            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(two) : "r"(at + 2 * c4));
-          else
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(two) : "r"(at + c4));
-          two = half2_of_codes(two);
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) {  // two words to a block of 16
-            const uint32_t sc = __byte_perm(two, 0, x < 2 ? 0x1010 : 0x3232);
-            uint32_t v[4];
-            widen4(u[x], sc, scale_offset(sc), v);
-            mma16816<true>(s[j], qf[2 * x], v[0], v[1]);
-            mma16816<true>(s[j], qf[2 * x + 1], v[2], v[3]);
-          }
-        }
-      } else if (!kE4M3) {
+      if (!kE4M3) {
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
           uint32_t b[4];
@@ -502,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       }
       uint32_t pf[4];
       uint32_t pe[4];  // bf16: what the upper half of P leaves
-      if (kF16) {
+      if (kE4M3) {
         pf[0] = pack_f16(pr[0][0], pr[0][1]);
         pf[1] = pack_f16(pr[0][2], pr[0][3]);
         pf[2] = pack_f16(pr[1][0], pr[1][1]);
@@ -520,46 +554,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
         }
       }
       // ---- O += P V
-      uint32_t vsc[kInt4 ? D / 64 : 1][4];  // scales as half pairs of keys: chunks 2 x (lo, hi), 2 x + 1
-      if constexpr (kInt4) {
-        // the words of this lane's keys 2 c4 and 2 c4 + 1 (y = 0), and of the two 8 further (1)
-        constexpr int kWords = D / 64;
-        const uint32_t pick = 0x6240u + 0x1111u * (quad >> 2);  // a chunk's columns 16 on: the odd
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t at = ks + St::kScales + (kWarpKeys + 8 * y + 2 * c4) * St::kScaleBytes;
-          uint32_t r[2 * kWords];
-          if constexpr (D == 128)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                         : "r"(at));
-          else
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at));
-#pragma unroll
-          for (int x = 0; x < kWords; ++x) {
-            const uint32_t c = __byte_perm(r[x], r[kWords + x], pick);
-            vsc[x][y] = half2_of_codes(c & 0xffffu);
-            vsc[x][2 + y] = half2_of_codes(c >> 16);
-          }
-        }
-      }
 #pragma unroll
       for (int ch = 0; ch < St::kChunks; ch += 2) {
         uint32_t b[4];
         ldsm4_t(St::at(vs, ((lane >> 3) & 1) * 8 + (lane & 7), ch + (lane >> 4)), b);
-        if constexpr (kInt4) {
-          // A 16-bit element is four neighbouring columns: code i of each makes an
-          // 8-column tile.
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t lo[4], hi[4];
-            const uint32_t s0 = vsc[ch / 2][2 * x], s1 = vsc[ch / 2][2 * x + 1];
-            widen4(b[2 * x], s0, scale_offset(s0), lo);
-            widen4(b[2 * x + 1], s1, scale_offset(s1), hi);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mma16816<true>(o[4 * (ch + x) + i], pf, lo[i], hi[i]);
-          }
-        } else if (!kE4M3) {
+        if (!kE4M3) {
           mma16816<false>(o[ch], pf, b[0], b[1]);
           mma16816<false>(o[ch + 1], pf, b[2], b[3]);
           mma16816<false>(o[ch], pe, b[0], b[1]);
@@ -592,7 +591,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       merge_ml[warp][quad + 8][1] = l1;
     }
     __syncthreads();
-    constexpr int kPitch = D + 8;  // floats; staggers the rows over the banks
     float* const mo = reinterpret_cast<float*>(smem);
     {
       float big0 = -INFINITY, big1 = -INFINITY;
@@ -603,22 +601,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       }
       const float f0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - big0);
       const float f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - big1);
-      float* const w0 = mo + (warp * kRows + quad) * kPitch;
-      float* const w1 = w0 + 8 * kPitch;
-      if (kInt4) {
-#pragma unroll
-        for (int ch = 0; ch < kN / 4; ++ch)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float(&a)[4] = o[4 * ch], (&b)[4] = o[4 * ch + 1], (&c)[4] = o[4 * ch + 2],
-                       (&d)[4] = o[4 * ch + 3];
-            const int col = ch * 32 + c4 * 8 + e * 4;
-            *reinterpret_cast<float4*>(w0 + col) =
-                make_float4(a[e] * f0, b[e] * f0, c[e] * f0, d[e] * f0);
-            *reinterpret_cast<float4*>(w1 + col) =
-                make_float4(a[2 + e] * f1, b[2 + e] * f1, c[2 + e] * f1, d[2 + e] * f1);
-          }
-      } else if (!kE4M3) {
+      float* const w0 = mo + (warp * kRows + quad) * kPitch<D>;
+      float* const w1 = w0 + 8 * kPitch<D>;
+      if (!kE4M3) {
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
           *reinterpret_cast<float2*>(w0 + n * 8 + c4 * 2) = make_float2(o[n][0] * f0, o[n][1] * f0);
@@ -637,55 +622,149 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       }
     }
     __syncthreads();
-    const bool complete = t0 == 0 && static_cast<unsigned>(t1) == n_tiles;
-    const bool direct = complete && !prefix && p.P == 0 && p.n_q == 1;
-    const float vd = head_descale<kHeld>(p, 1, hk);
-    constexpr int kVecs = D / 4;  // 4-column vectors of a row
-    for (int x = threadIdx.x; x < rows * kVecs; x += kThreads) {
-      const int r = x / kVecs, col = (x % kVecs) * 4;
-      float big = -INFINITY, l = 0.f;
+    write_item<D, kShift == 15.f>(p, it, t0, t1, mo, merge_ml, any_bad,
+                                  kE4M3 ? __ldg(p.descale[1] + hk) : 1.f);
+    if (any_bad && threadIdx.x == 0) atomicOr(p.err, kErrCache);
+    __syncthreads();  // the ring is free again
+  }
+}
+
+// Over a cache in 4 bits (decode_int4.cuh): 128-key tiles, 32 keys to a warp, up to kNT x 8
+// rows of an item.
+template <int D, int kNT>
+__global__ void __launch_bounds__(kThreads, kCtas4<kNT>) paged_decode4_kernel(const DecodeParams p) {
+  using Core = Int4Core<D, kNT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ unsigned scan[kWarps];
+  __shared__ float merge_ml[kWarps][kRows][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = ptx::smem_u32(smem) + warp * Core::kRing;
+
+  cudaTriggerProgrammaticLaunchCompletion();  // the next kernel's blocks may line up
+  const unsigned prefix_all = prefix_units(p);
+  unsigned* const starts = reinterpret_cast<unsigned*>(smem + kWarps * Core::kRing);
+  const unsigned W = lay_out<kTileKeys4>(p, prefix_all, starts, scan);
+  const unsigned g = min(gridDim.x, W);
+  if (blockIdx.x >= g) return;
+  unsigned w = stretch(blockIdx.x, W, g);
+  const unsigned w_end = stretch(blockIdx.x + 1, W, g);
+  const long long v_from_k = p.cache[1] - p.cache[0];
+
+  while (w < w_end) {
+    const Item it(p, starts, prefix_all, w, kTileKeys4);
+    const unsigned u1 = min(it.n_tiles + kItemCost, it.u0 + (w_end - w));
+    const int t0 = tile_of_unit(it.u0), t1 = tile_of_unit(u1);
+    w += u1 - it.u0;
+    if (t0 >= t1) continue;
+
+    // ---- this warp's loads of tile t: a key to a lane, whose page is looked up before
+    struct Place {
+      int page, slot;
+    };
+    bool bad = false;
+    auto look_up = [&](int t) {
+      Place at{-1, 0};
+      const int key = t * kTileKeys4 + warp * Core::kKeys + lane;
+      if (t < t1 && key < it.n_keys) {
+        const int pos = it.base_pos + key;
+        const int x = p.page_of(pos);
+        at.slot = pos - x * p.page_size;
+        at.page = __ldg(it.pages + x);
+        if (at.page < 0 || at.page >= p.n_pages) {
+          at.page = -1;
+          bad = true;
+        }
+      }
+      return at;
+    };
+    auto load = [&](int t, int stage, Place at) {
+      if (t < t1) {
+        const uint32_t dst = ring + stage * Core::kBytes;
+        const bool have = at.page >= 0;
+        const unsigned held = __ballot_sync(0xffffffffu, have);
+        const long long page = have ? at.page : 0;
+        constexpr int kPerStep = 32 / Core::kChunks;  // keys per warp-wide access
+        const int chunk = lane % Core::kChunks, first = lane / Core::kChunks;
+        auto rows = [&](auto both) {  // K's rows, and V's where they lie alike; or V's
+          constexpr int kX = decltype(both)::value;
+          const uint8_t* const row = p.cache[kX] + page * p.cs[kX][0] + at.slot * p.cs[kX][1] +
+                                     it.hk * p.cs[kX][2];
+          const unsigned long long mine = reinterpret_cast<unsigned long long>(row);
 #pragma unroll
-      for (int y = 0; y < kWarps; ++y) big = fmaxf(big, merge_ml[y][r][0]);
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < Core::kKeys / kPerStep; ++i) {
+            const int key = i * kPerStep + first;
+            const uint8_t* const src = reinterpret_cast<const uint8_t*>(
+                                           __shfl_sync(0xffffffffu, mine, key)) + chunk * 16;
+            const int bytes = (held >> key & 1u) ? 16 : 0;
+            cp_async16(Core::at(dst + kX * Core::kV, key, chunk), src, bytes);
+            if (kX == 0 && p.alike)
+              cp_async16(Core::at(dst + Core::kV, key, chunk), src + v_from_k, bytes);
+          }
+        };
+        rows(std::integral_constant<int, 0>());
+        if (!p.alike) rows(std::integral_constant<int, 1>());
 #pragma unroll
-      for (int y = 0; y < kWarps; ++y) {
-        const float my = merge_ml[y][r][0];
-        // an empty state's l is 0, or NaN where its scores were
-        l += merge_ml[y][r][1] * (my == -INFINITY ? 1.f : ptx::ex2(my - big));
-        const float4 a = *reinterpret_cast<const float4*>(mo + (y * kRows + r) * kPitch + col);
-        sum.x += a.x;
-        sum.y += a.y;
-        sum.z += a.z;
-        sum.w += a.w;
+        for (int x = 0; x < 2; ++x)
+          cp_async_small<Core::kScaleBytes>(
+              dst + Core::kScales + (x * Core::kKeys + lane) * Core::kScaleBytes,
+              p.scales[x] + page * p.ss[x][0] + at.slot * p.ss[x][1] + it.hk * p.ss[x][2], have);
       }
-      if (any_bad) l = NAN;
-      const RowOf row(p, b0, hk, row0 + r);
-      if (direct) {
-        const float inv = l == 0.f ? 0.f : vd / l;
-        uint2 v;
-        v.x = ptx::pack_bf16(sum.x * inv, sum.y * inv);
-        v.y = ptx::pack_bf16(sum.z * inv, sum.w * inv);
-        *reinterpret_cast<uint2*>(p.out + row.index(p) * D + col) = v;
-        if (col == 0)
-          p.lse[(static_cast<long long>(row.b) * p.Hq + row.h) * p.n_q + row.i] =
-              (big - kShift + log2f(l)) * kLn2;
-        continue;
-      }
-      float *to, *ml;
-      if (complete) {
-        const long long at = (prefix ? static_cast<long long>(p.B) * p.n_q * p.Hq : 0) +
-                             row.index(p);
-        to = p.whole_o + at * D;
-        ml = p.whole_ml + at * 2;
-      } else {
-        const long long at = (static_cast<long long>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0)) * kRows + r;
-        to = p.slot_o + at * D;
-        ml = p.slot_ml + at * 2;
-      }
-      *reinterpret_cast<float4*>(to + col) = make_float4(sum.x * vd, sum.y * vd, sum.z * vd,
-                                                         sum.w * vd);
-      if (col == 0) *reinterpret_cast<float2*>(ml) = make_float2(big - kShift, l);
+      cp_commit();
+    };
+    Place next;
+    {
+      Place first[Core::kCount];
+#pragma unroll
+      for (int i = 0; i < Core::kCount; ++i) first[i] = look_up(t0 + i);
+#pragma unroll
+      for (int i = 0; i < Core::kCount - 1; ++i) load(t0 + i, i, first[i]);
+      next = first[Core::kCount - 1];
     }
+    Core core;
+    core.load_queries(
+        [&](int r) { return RowOf(p, it.b0, it.hk, it.row0 + r).query(p); }, it.rows,
+        p.scale * head_descale<Held::kInt4>(p, 0, it.hk), lane);
+
+    int stage = 0;
+    for (int t = t0; t < t1; ++t) {
+      cp_wait<Core::kCount - 2>();
+      __syncwarp();
+      load(t + Core::kCount - 1, stage == 0 ? Core::kCount - 1 : stage - 1, next);
+      next = look_up(t + Core::kCount);
+      core.step(ring + stage * Core::kBytes, it.n_keys - t * kTileKeys4 - warp * Core::kKeys, lane);
+      if (++stage == Core::kCount) stage = 0;
+    }
+    cp_wait<0>();
+
+    // ---- join the four warps' states; a bad page makes the item's l NaN
+    core.sum_lanes();
+    const bool any_bad = __syncthreads_or(bad);  // also: every warp is done with its ring
+    const int r0 = 2 * (lane & 3);
+    if (lane < 4) {
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          merge_ml[warp][8 * nt + r0 + e][0] = core.m[nt][e];
+          merge_ml[warp][8 * nt + r0 + e][1] = core.l[nt][e];
+        }
+    }
+    __syncthreads();
+    float* const mo = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * nt + r0 + e;
+        float big = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) big = fmaxf(big, merge_ml[x][row][0]);
+        const float f = core.m[nt][e] == -INFINITY ? 0.f : ptx::ex2(core.m[nt][e] - big);
+        core.store_row(mo + (warp * kRows + row) * kPitch<D>, nt, e, f, lane);
+      }
+    __syncthreads();
+    write_item<D, true>(p, it, t0, t1, mo, merge_ml, any_bad,
+                        Core::kUnit * head_descale<Held::kInt4>(p, 1, it.hk));
     if (any_bad && threadIdx.x == 0) atomicOr(p.err, kErrCache);
     __syncthreads();  // the ring is free again
   }
@@ -786,7 +865,8 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
   const int r_own = i * p.G + h % p.G;
   Parts own{p.slot_o, p.slot_ml, 0, 0, kRows, r_own % kRows};
   if (common > 0) {
-    const unsigned n = static_cast<unsigned>((common + kTileKeys - 1) / kTileKeys);
+    constexpr int kKeys = tile_keys_of(kHeld);
+    const unsigned n = static_cast<unsigned>((common + kKeys - 1) / kKeys);
     own.find(first_own + (hk * p.own_tiles_of_rows + r_own / kRows) * (n + kItemCost), n, W, g);
     if (own.count == 1) {
       if (p.P == 0 && p.n_q == 1) return;  // written by the item's CTA
@@ -1013,15 +1093,26 @@ struct Space {
 
 template <int D, Held kHeld>
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
-  using St = Stage<D, kHeld>;
-  static_assert(kWarps * St::kRing >= kWarps * kRows * (D + 8) * 4, "the join fits the ring");
-  const int smem = kWarps * St::kRing + 4 * (p.B + 1);
-  const int most = kWarps * St::kRing + 4 * (kMaxBatch + 1);
-  cudaError_t e = ensure_smem_limit(
-      reinterpret_cast<const void*>(&paged_decode_kernel<D, kHeld>), most);
+  void (*kern)(DecodeParams);
+  int ring, ctas;
+  if constexpr (kHeld == Held::kInt4) {
+    static_assert(Int4Core<D, 2>::kRing >= kRows * kPitch<D> * 4, "the join fits the ring");
+    // 8 rows where no item has more (measured: see the top)
+    const bool few = p.R <= 8 && (p.P == 0 || p.B * p.R <= 8);
+    kern = few ? paged_decode4_kernel<D, 1> : paged_decode4_kernel<D, 2>;
+    ring = kWarps * Int4Core<D, 1>::kRing;
+    ctas = few ? kCtas4<1> : kCtas4<2>;
+  } else {
+    static_assert(Stage<D, kHeld>::kRing >= kRows * kPitch<D> * 4, "the join fits the ring");
+    kern = paged_decode_kernel<D, kHeld>;
+    ring = kWarps * Stage<D, kHeld>::kRing;
+    ctas = kCtasPerSm;
+  }
+  const int smem = ring + 4 * (p.B + 1);
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), ring + 4 * (kMaxBatch + 1));
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(std::min(kMaxGrid, kCtasPerSm * sm_count()));
-  paged_decode_kernel<D, kHeld><<<grid, kThreads, smem, stream>>>(p);
+  const unsigned grid = static_cast<unsigned>(std::min(kMaxGrid, ctas * sm_count()));
+  kern<<<grid, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   count_launch(2);
@@ -1092,7 +1183,8 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
   const bool wide =  // and never without the space for its parts
       cache->elem_bytes > 0 && sp.pslot_ml > sp.pslot_o &&
       wide_prefix(B * R, prefix_len, Hk, d, cache->elem_bytes, cache->page_size);
-  const int prefix_rows = wide ? kPrefixRows : kRows, prefix_keys = wide ? kPrefixKeys : kTileKeys;
+  const int prefix_rows = wide ? kPrefixRows : kRows,
+            prefix_keys = wide ? kPrefixKeys : tile_keys_of(held_by(cache));
   const long long own_rt = (R + kRows - 1) / kRows;
   const long long prefix_rt = (B * R + prefix_rows - 1) / prefix_rows;
   const long long most_tiles = (capacity + kTileKeys - 1) / kTileKeys;
@@ -1153,7 +1245,9 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
         std::min(kMaxPrefixGrid, sm_count()), prefix_tiles * prefix_rt * Hk));
   p.timeout_ns = test_wait_limit_ns();
   p.fault_drop_k = test_fault_drop();
-  p.n_pages = cache->n_pages; p.page_size = cache->page_size;
+  p.n_pages = cache->n_pages;
+  p.set_page_size(cache->page_size);
+  p.alike = std::equal(p.cs[0], p.cs[0] + 3, p.cs[1]);
   p.capacity = capacity;
   auto launch = [&](auto dim) {
     constexpr int kD = decltype(dim)::value;

@@ -48,7 +48,23 @@ struct DecodeParams {
   // paged_decode_kernel (16 rows, 64 keys).
   int prefix_rows, prefix_row_tiles, prefix_tiles, prefix_grid;
   int n_pages, page_size;
+  uint32_t page_mul;         // pos / page_size = pos * page_mul >> page_shift, below 2^31
+  int page_shift;
+  int alike;                 // K's and V's strides are the same
   long long capacity;        // max_pages * page_size
+
+  // With 2^(s - 1) < n <= 2^s the multiplier 2^(31 + s) / n, rounded up, is below 2^32 and is
+  // off by less than 1, so a product with pos < 2^31 is off by less than 2^(31 + s) / n.
+  void set_page_size(int n) {
+    page_size = n;
+    int s = 0;
+    while ((1LL << s) < n) ++s;
+    page_shift = 31 + s;
+    page_mul = static_cast<uint32_t>(((1ULL << page_shift) + n - 1) / n);
+  }
+  __device__ __forceinline__ int page_of(int pos) const {
+    return static_cast<int>(static_cast<unsigned long long>(pos) * page_mul >> page_shift);
+  }
 };
 
 // 16 bytes to shared memory, the first `bytes` (0 or 16) of them copied, the rest zeros.
@@ -66,26 +82,6 @@ __device__ __forceinline__ uint32_t half2_of_codes(uint32_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
   return h;
-}
-// Entries in 4 bits.  Entry i of a row is code (byte i / 2, the low half for even i) minus 8,
-// times its block's E4M3 scale, times the head's descale.  A code in bits 4 to 7 of a half word
-// below the fp16 exponent of 64 reads 64 + code, so one fused multiply-add, (64 + code) s -
-// 72 s, gives (code - 8) s: the sums and products of a code's 4 and a scale's 4 bits fit
-// fp16's 11, so the value is exact.
-// The four pairs of a word: half2 i holds the codes i and i + 4 (in two half words: code i of
-// each), times the scales of the halves of `s`; ms = scale_offset(s).
-__device__ __forceinline__ uint32_t scale_offset(uint32_t s) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(0xd480d480u));  // -72
-  return r;
-}
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t s, uint32_t ms, uint32_t (&v)[4]) {
-  const uint32_t t[4] = {w << 4, w, w >> 4, w >> 8};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t n = (t[i] & 0x00f000f0u) | 0x54005400u;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(n), "r"(s), "r"(ms));
-  }
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
