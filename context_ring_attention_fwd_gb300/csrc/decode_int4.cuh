@@ -61,20 +61,24 @@ struct Widener {
     m1032 = mul_f16x2(scales, 0xd408d408u);  // -64.5
   }
   // half2 i: the codes i (low half) and i + 4 (high half) of a word.
+  // (lop3 is written out: from the expression (x & mask) | exponent the compiler makes two
+  // operations, 62 us instead of 54 in the kernel for 32 sequences of up to 16K.)
   __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&v)[4]) const {
     const uint32_t t = w >> 8;
     auto low = [&](uint32_t x) {
       uint32_t r;
-      asm("fma.rn.f16x2 %0, %1, %2, %3;"
+      asm("{\n\t.reg .b32 n;\n\tlop3.b32 n, %1, 0x000f000f, %2, 0xea;\n\t"
+          "fma.rn.f16x2 %0, n, %3, %4;\n\t}"
           : "=r"(r)
-          : "r"((x & 0x000f000fu) | 0x64006400u), "r"(s), "r"(m1032));
+          : "r"(x), "r"(0x64006400u), "r"(s), "r"(m1032));
       return r;
     };
     auto high = [&](uint32_t x) {
       uint32_t r;
-      asm("fma.rn.f16x2 %0, %1, %2, %3;"
+      asm("{\n\t.reg .b32 n;\n\tlop3.b32 n, %1, 0x00f000f0, %2, 0xea;\n\t"
+          "fma.rn.f16x2 %0, n, %3, %4;\n\t}"
           : "=r"(r)
-          : "r"((x & 0x00f000f0u) | 0x54005400u), "r"(s), "r"(m72));
+          : "r"(x), "r"(0x54005400u), "r"(s), "r"(m72));
       return r;
     };
     v[0] = low(w);
@@ -93,7 +97,9 @@ struct Int4Core {
   static constexpr int kBytes = kScales + 2 * kKeys * kScaleBytes;
   static constexpr int kCount = D == 128 ? 2 : 4;  // stages
   static constexpr int kRing = kCount * kBytes;
-  static constexpr float kShift = 15.f;         // P is held times 2^kShift
+  // P is held times 2^kShift and at most 2^kSlack, so below 2^15 in fp16, which flushes what
+  // is 2^-34 of the reference.
+  static constexpr float kShift = 10.f, kSlack = 5.f;
   static constexpr float kUnit = 16.f;          // values are held divided by it
 
   uint32_t q[kNT][D / 16][2];
@@ -173,76 +179,103 @@ struct Int4Core {
   __device__ __forceinline__ void step(uint32_t stage, int left, int lane) {
     const int quad = lane >> 2, c4 = lane & 3;
     constexpr int kWords = D / 32;
-    // ---- S^T: keys quad and quad + 8 of each 16, rows 2 c4 and 2 c4 + 1
-    float s[2][kNT][4];
+    // ---- S^T: keys quad and quad + 8 of each 16, rows 2 c4 and 2 c4 + 1; in two sums each, so
+    // that four products are under way at a time
+    float s[2][kNT][4], s2[2][kNT][4];
+    uint32_t u[2][2][kWords], two[2][2];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
-        s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
-      uint32_t u[2][kWords], two[2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][nt][e] = s2[mt][nt][e] = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = mt * 16 + h * 8 + quad;
         load_words<kWords>(D == 128 ? at(stage, row, c4) : at(stage, row, c4 / 2) + c4 % 2 * 8,
-                           u[h]);
+                           u[mt][h]);
         const uint32_t from = stage + kScales + row * kScaleBytes;
         if constexpr (D == 128)
-          asm volatile("ld.shared.u16 %0, [%1];" : "=r"(two[h]) : "r"(from + 2 * c4));
+          asm volatile("ld.shared.u16 %0, [%1];" : "=r"(two[mt][h]) : "r"(from + 2 * c4));
         else
-          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(two[h]) : "r"(from + c4));
-        two[h] = half2_of_codes(two[h]);
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(two[mt][h]) : "r"(from + c4));
+        two[mt][h] = half2_of_codes(two[mt][h]);
       }
+    }
 #pragma unroll
-      for (int b = 0; b < D / 64; ++b) {  // the lane's blocks of 16, two words each
-        const Widener w0(__byte_perm(two[0], 0, b ? 0x3232 : 0x1010));
-        const Widener w1(__byte_perm(two[1], 0, b ? 0x3232 : 0x1010));
+    for (int b = 0; b < D / 64; ++b)  // the lane's blocks of 16, two words each
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const Widener w0(__byte_perm(two[mt][0], 0, b ? 0x3232 : 0x1010));
+        const Widener w1(__byte_perm(two[mt][1], 0, b ? 0x3232 : 0x1010));
 #pragma unroll
         for (int x = 2 * b; x < 2 * b + 2; ++x) {
           uint32_t v0[4], v1[4];
-          w0(u[0][x], v0);
-          w1(u[1][x], v1);
+          w0(u[mt][0][x], v0);
+          w1(u[mt][1][x], v1);
+          const uint32_t a0[4] = {v0[0], v1[0], v0[1], v1[1]}, a1[4] = {v0[2], v1[2], v0[3], v1[3]};
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t a[4] = {v0[2 * y], v1[2 * y], v0[2 * y + 1], v1[2 * y + 1]};
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-              mma(s[mt][nt], a, q[nt][2 * x + y][0], q[nt][2 * x + y][1]);
+          for (int nt = 0; nt < kNT; ++nt) {
+            mma(s[mt][nt], a0, q[nt][2 * x][0], q[nt][2 * x][1]);
+            mma(s2[mt][nt], a1, q[nt][2 * x + 1][0], q[nt][2 * x + 1][1]);
           }
         }
       }
+    // ---- V of the tile, and the scales of keys 2 c4 and 2 c4 + 1 and of the two 8 further,
+    // while the softmax waits for its steps
+    constexpr int kHalf = D / 64;
+    uint32_t v[2][kHalf][4], r4[2][2][2 * kHalf];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        load_words<2 * kHalf>(
+            stage + kScales + (kKeys + mt * 16 + 8 * y + 2 * c4) * kScaleBytes, r4[mt][y]);
+#pragma unroll
+      for (int x = 0; x < kHalf; ++x) {
+        const uint32_t addr = at(stage + kV, mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7),
+                                 2 * x + (lane >> 4));
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[mt][x][0]), "=r"(v[mt][x][1]), "=r"(v[mt][x][2]), "=r"(v[mt][x][3])
+                     : "r"(addr));
+      }
     }
-    if (left < kKeys) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[mt][nt][e] += s2[mt][nt][e];
+          if (left < kKeys && mt * 16 + (e >> 1) * 8 + quad >= left) s[mt][nt][e] = -INFINITY;
+        }
+    // ---- P against a reference that moves only when a score passes it by 2^kSlack
+    auto exponents = [&](int mt, int nt, int e) {
+      const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
+      return fmaf(s[mt][nt][e], sc[nt][e & 1], kShift - ref);
+    };
+    bool over = false;
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      float top = -INFINITY;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (mt * 16 + (e >> 1) * 8 + quad >= left) s[mt][nt][e] = -INFINITY;
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, exponents(mt, nt, e));
+      over |= top > kShift + kSlack || m[nt][0] == -INFINITY || m[nt][1] == -INFINITY;
     }
-    // ---- running maximum, P
-    float top[kNT][2];
-    bool grows = false;
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2])) *
-                  sc[nt][e];
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        top[nt][e] = x;
-        grows |= x > m[nt][e];
-      }
-    if (__any_sync(0xffffffffu, grows)) {
+    if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
         float a[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float n = fmaxf(m[nt][e], top[nt][e]);
+          float x = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]),
+                          fmaxf(s[1][nt][e], s[1][nt][e + 2])) * sc[nt][e];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float n = fmaxf(m[nt][e], x);
           a[e] = m[nt][e] == -INFINITY ? 0.f : ptx::ex2(m[nt][e] - n);
           m[nt][e] = n;
           l[nt][e] *= a[e];
@@ -255,60 +288,42 @@ struct Int4Core {
     }
     uint32_t p[2][kNT][2];  // of 16 keys: the first 8, the others
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      float r[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) r[e] = (m[nt][e] == -INFINITY ? 0.f : m[nt][e]) - kShift;
+    for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[e] = ptx::ex2(fmaf(s[mt][nt][e], sc[nt][e & 1], -r[e & 1]));
+          x[e] = ptx::ex2(exponents(mt, nt, e));
           l[nt][e & 1] += x[e];
         }
         p[mt][nt][0] = transposed8x8(pack_f16(x[0], x[1]));
         p[mt][nt][1] = transposed8x8(pack_f16(x[2], x[3]));
       }
-    }
     // ---- O^T += V^T P^T
     const uint32_t pick = 0x6240u + 0x1111u * (quad >> 2);  // of a chunk's two blocks, this lane's
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      // scale words of keys 2 c4 and 2 c4 + 1, and of the two 8 further
-      constexpr int kHalf = D / 64;
-      uint32_t r[2][2 * kHalf];
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
-        load_words<2 * kHalf>(
-            stage + kScales + (kKeys + mt * 16 + 8 * y + 2 * c4) * kScaleBytes, r[y]);
-#pragma unroll
-      for (int ch = 0; ch < kChunks; ch += 2) {
-        uint32_t v[4];
-        const uint32_t addr =
-            at(stage + kV, mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), ch + (lane >> 4));
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                     : "r"(addr));
-        const uint32_t c0 = __byte_perm(r[0][ch / 2], r[0][kHalf + ch / 2], pick);
-        const uint32_t c1 = __byte_perm(r[1][ch / 2], r[1][kHalf + ch / 2], pick);
+      for (int h = 0; h < kHalf; ++h) {
+        const uint32_t c0 = __byte_perm(r4[mt][0][h], r4[mt][0][kHalf + h], pick);
+        const uint32_t c1 = __byte_perm(r4[mt][1][h], r4[mt][1][kHalf + h], pick);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const Widener w0(half2_of_codes(x ? c0 >> 16 : c0 & 0xffffu));
           const Widener w1(half2_of_codes(x ? c1 >> 16 : c1 & 0xffffu));
           uint32_t lo[4], hi[4];  // column 4 quad + i of the chunk: two keys each
-          w0(v[2 * x], lo);
-          w1(v[2 * x + 1], hi);
+          w0(v[mt][h][2 * x], lo);
+          w1(v[mt][h][2 * x + 1], hi);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t a[4] = {lo[2 * i], lo[2 * i + 1], hi[2 * i], hi[2 * i + 1]};
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
-              mma(o[nt][2 * (ch + x) + i], a, p[mt][nt][0], p[mt][nt][1]);
+              mma(o[nt][2 * (2 * h + x) + i], a, p[mt][nt][0], p[mt][nt][1]);
           }
         }
       }
-    }
   }
 
   // The sums of the rows' exponentials over the lanes that share them.

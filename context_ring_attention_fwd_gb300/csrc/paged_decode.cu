@@ -76,9 +76,7 @@ constexpr int kTileKeys = kWarps * kWarpKeys;    // 64
 constexpr int kTileKeys4 = 128;                  // over a cache in 4 bits
 constexpr int kRows = 16;                        // rows of an item
 constexpr int kCtasPerSm = 3;
-template <int kNT>
-constexpr int kCtas4 = kNT == 1 ? 4 : 3;         // of paged_decode4_kernel
-constexpr int kMaxGrid = 640;                    // bounds the slots of the workspace
+constexpr int kMaxGrid = 480;                    // bounds the slots of the workspace
 constexpr int kMaxBatch = 4096;
 // From this many rows on a warp joins a row, four below.  Measured, one / four (us in
 // the kernel): 32 rows of 11 parts 5.3 / 4.4; 2048 rows of 21 parts 9.5 / 11.1;
@@ -252,11 +250,11 @@ struct Item {
 // [warp][16 rows][kPitch] that share a reference, and (m, l) of each; l is NaN for a bad page.
 template <int D>
 constexpr int kPitch = D + 8;  // floats; staggers the rows over the banks
-template <int D, bool kShifted>
+template <int D, int kShiftLog2>
 __device__ __forceinline__ void write_item(const DecodeParams& p, const Item& it, int t0, int t1,
                                            const float* mo, const float (&merge_ml)[kWarps][kRows][2],
                                            bool any_bad, float vd) {
-  constexpr float kShift = kShifted ? 15.f : 0.f;
+  constexpr float kShift = kShiftLog2;  // P was held times 2^kShift
       const bool complete = t0 == 0 && static_cast<unsigned>(t1) == it.n_tiles;
       const bool direct = complete && !it.prefix && p.P == 0 && p.n_q == 1;
       constexpr int kVecs = D / 4;  // 4-column vectors of a row
@@ -622,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
       }
     }
     __syncthreads();
-    write_item<D, kShift == 15.f>(p, it, t0, t1, mo, merge_ml, any_bad,
+    write_item<D, kE4M3 ? 15 : 0>(p, it, t0, t1, mo, merge_ml, any_bad,
                                   kE4M3 ? __ldg(p.descale[1] + hk) : 1.f);
     if (any_bad && threadIdx.x == 0) atomicOr(p.err, kErrCache);
     __syncthreads();  // the ring is free again
@@ -632,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(cons
 // Over a cache in 4 bits (decode_int4.cuh): 128-key tiles, 32 keys to a warp, up to kNT x 8
 // rows of an item.
 template <int D, int kNT>
-__global__ void __launch_bounds__(kThreads, kCtas4<kNT>) paged_decode4_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode4_kernel(const DecodeParams p) {
   using Core = Int4Core<D, kNT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ unsigned scan[kWarps];
@@ -648,7 +646,6 @@ __global__ void __launch_bounds__(kThreads, kCtas4<kNT>) paged_decode4_kernel(co
   if (blockIdx.x >= g) return;
   unsigned w = stretch(blockIdx.x, W, g);
   const unsigned w_end = stretch(blockIdx.x + 1, W, g);
-  const long long v_from_k = p.cache[1] - p.cache[0];
 
   while (w < w_end) {
     const Item it(p, starts, prefix_all, w, kTileKeys4);
@@ -662,6 +659,9 @@ __global__ void __launch_bounds__(kThreads, kCtas4<kNT>) paged_decode4_kernel(co
       int page, slot;
     };
     bool bad = false;
+    const uint8_t* const head[2] = {p.cache[0] + it.hk * p.cs[0][2], p.cache[1] + it.hk * p.cs[1][2]};
+    const uint8_t* const scale_head[2] = {p.scales[0] + it.hk * p.ss[0][2],
+                                          p.scales[1] + it.hk * p.ss[1][2]};
     auto look_up = [&](int t) {
       Place at{-1, 0};
       const int key = t * kTileKeys4 + warp * Core::kKeys + lane;
@@ -682,32 +682,38 @@ __global__ void __launch_bounds__(kThreads, kCtas4<kNT>) paged_decode4_kernel(co
         const uint32_t dst = ring + stage * Core::kBytes;
         const bool have = at.page >= 0;
         const unsigned held = __ballot_sync(0xffffffffu, have);
-        const long long page = have ? at.page : 0;
+        // unsigned, so that a product with a stride is two instructions
+        const unsigned page = have ? at.page : 0, slot = at.slot;
         constexpr int kPerStep = 32 / Core::kChunks;  // keys per warp-wide access
         const int chunk = lane % Core::kChunks, first = lane / Core::kChunks;
-        auto rows = [&](auto both) {  // K's rows, and V's where they lie alike; or V's
-          constexpr int kX = decltype(both)::value;
-          const uint8_t* const row = p.cache[kX] + page * p.cs[kX][0] + at.slot * p.cs[kX][1] +
-                                     it.hk * p.cs[kX][2];
-          const unsigned long long mine = reinterpret_cast<unsigned long long>(row);
+        // K's rows, and V's where their strides are the same (0); or V's (1)
+        auto rows = [&](auto which, auto whole) {
+          constexpr int kX = decltype(which)::value;
+          const unsigned long long mine = page * static_cast<unsigned long long>(p.cs[kX][0]) +
+                                          slot * static_cast<unsigned long long>(p.cs[kX][1]);
+          const uint8_t* const base = head[kX] + chunk * 16;
 #pragma unroll
           for (int i = 0; i < Core::kKeys / kPerStep; ++i) {
             const int key = i * kPerStep + first;
-            const uint8_t* const src = reinterpret_cast<const uint8_t*>(
-                                           __shfl_sync(0xffffffffu, mine, key)) + chunk * 16;
-            const int bytes = (held >> key & 1u) ? 16 : 0;
-            cp_async16(Core::at(dst + kX * Core::kV, key, chunk), src, bytes);
+            const unsigned long long o = __shfl_sync(0xffffffffu, mine, key);
+            const int bytes = decltype(whole)::value || (held >> key & 1u) ? 16 : 0;
+            cp_async16(Core::at(dst + kX * Core::kV, key, chunk), base + o, bytes);
             if (kX == 0 && p.alike)
-              cp_async16(Core::at(dst + Core::kV, key, chunk), src + v_from_k, bytes);
+              cp_async16(Core::at(dst + Core::kV, key, chunk), head[1] + chunk * 16 + o, bytes);
           }
         };
-        rows(std::integral_constant<int, 0>());
-        if (!p.alike) rows(std::integral_constant<int, 1>());
+        if (held == 0xffffffffu)
+          rows(std::integral_constant<int, 0>(), std::true_type());
+        else
+          rows(std::integral_constant<int, 0>(), std::false_type());
+        if (!p.alike) rows(std::integral_constant<int, 1>(), std::false_type());
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           cp_async_small<Core::kScaleBytes>(
               dst + Core::kScales + (x * Core::kKeys + lane) * Core::kScaleBytes,
-              p.scales[x] + page * p.ss[x][0] + at.slot * p.ss[x][1] + it.hk * p.ss[x][2], have);
+              scale_head[x] + (page * static_cast<unsigned long long>(p.ss[x][0]) +
+                               slot * static_cast<unsigned long long>(p.ss[x][1])),
+              have);
       }
       cp_commit();
     };
@@ -763,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, kCtas4<kNT>) paged_decode4_kernel(co
         core.store_row(mo + (warp * kRows + row) * kPitch<D>, nt, e, f, lane);
       }
     __syncthreads();
-    write_item<D, true>(p, it, t0, t1, mo, merge_ml, any_bad,
+    write_item<D, static_cast<int>(Core::kShift)>(p, it, t0, t1, mo, merge_ml, any_bad,
                         Core::kUnit * head_descale<Held::kInt4>(p, 1, it.hk));
     if (any_bad && threadIdx.x == 0) atomicOr(p.err, kErrCache);
     __syncthreads();  // the ring is free again
@@ -1094,24 +1100,22 @@ struct Space {
 template <int D, Held kHeld>
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   void (*kern)(DecodeParams);
-  int ring, ctas;
+  int ring;
   if constexpr (kHeld == Held::kInt4) {
     static_assert(Int4Core<D, 2>::kRing >= kRows * kPitch<D> * 4, "the join fits the ring");
     // 8 rows where no item has more (measured: see the top)
     const bool few = p.R <= 8 && (p.P == 0 || p.B * p.R <= 8);
     kern = few ? paged_decode4_kernel<D, 1> : paged_decode4_kernel<D, 2>;
     ring = kWarps * Int4Core<D, 1>::kRing;
-    ctas = few ? kCtas4<1> : kCtas4<2>;
   } else {
     static_assert(Stage<D, kHeld>::kRing >= kRows * kPitch<D> * 4, "the join fits the ring");
     kern = paged_decode_kernel<D, kHeld>;
     ring = kWarps * Stage<D, kHeld>::kRing;
-    ctas = kCtasPerSm;
   }
   const int smem = ring + 4 * (p.B + 1);
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), ring + 4 * (kMaxBatch + 1));
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(std::min(kMaxGrid, ctas * sm_count()));
+  const unsigned grid = static_cast<unsigned>(std::min(kMaxGrid, kCtasPerSm * sm_count()));
   kern<<<grid, kThreads, smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
