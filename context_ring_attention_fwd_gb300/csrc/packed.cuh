@@ -32,17 +32,25 @@
 namespace cpring {
 
 constexpr int kCostUnit = 128;  // tokens that an item's cost is counted in
+constexpr int kLeastPart = 4;   // streamed tiles of a part of a key tile
+constexpr int kMaxParts = 512;  // parts of a call over all key heads (the sums' space)
 
 // A list in the caller's workspace.  The attention's kernels, which may start before the plan
 // is done and wait for it, read it (and D) with plain loads: a read-only load (__ldg) promises
 // that nothing writes during the kernel, and the compiler may move it before the wait.
 struct PackedList {
-  int* head;        // [0] items of a key head (0 where the offsets are malformed), [1] next claim
-  int4* items;      // {first row of the sequence, its length, the tile's index, 0}
+  int* head;        // [0] items of a key head (0 where the offsets are malformed), [1] next claim,
+                    // [2] streamed tiles of a part (kSplit)
+  int4* items;      // {first row of the sequence, its length, the tile's index, part}
   int* starts;      // [n] items before each sequence (scratch)
   int* buckets;     // [n_buckets] (scratch)
   int tokens;       // of a tile
   int of_keys;      // tiles of keys: their cost is the queries that see them
+  // Tiles of keys are cut along their queries (packed_plan.cu) into at most this many parts (of a
+  // key head), each with a slot of fp32 sums; part = 1 + slot + (index << 16).  The last
+  // of a tile's parts to end, by `done`, adds them up.
+  int slots;
+  int* done;        // [slots of a key head][Hk]: parts that ended, by the first part's slot
 };
 
 struct PackedPlan {
@@ -50,6 +58,7 @@ struct PackedPlan {
   int lists;
   const int32_t* offsets;
   int n, T, causal, n_buckets;
+  int tq, Hk, grid;  // of the backward's key tiles
   int* err;
   // the backward: delta[row] = sum of out * dout over a row's d entries (rows T * Hq)
   const void* out;
@@ -85,11 +94,12 @@ inline int packed_buckets(int T) { return T / kCostUnit + 2; }
 inline long long packed_list_bytes(int T, int n, int tokens) {
   return 256 + 16 * packed_items(T, n, tokens) + 4LL * n + 4LL * packed_buckets(T);
 }
-inline PackedList packed_list(char* at, int T, int n, int tokens, bool of_keys) {
+inline PackedList packed_list(char* at, int T, int n, int tokens, bool of_keys, int slots = 0) {
   PackedList l{};
   l.head = reinterpret_cast<int*>(at);
   l.items = reinterpret_cast<int4*>(at + 256);
-  l.starts = reinterpret_cast<int*>(at + 256 + 16 * packed_items(T, n, tokens));
+  l.starts = reinterpret_cast<int*>(at + 256 + 16 * (packed_items(T, n, tokens) + slots));
+  l.slots = slots;
   l.buckets = l.starts + n;
   l.tokens = tokens;
   l.of_keys = of_keys;

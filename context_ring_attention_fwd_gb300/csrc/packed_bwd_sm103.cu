@@ -85,7 +85,8 @@ enum BBar : int {
   kVecFree = 20,   // + buffer: every softmax thread is done reading it
   kPReadyS = 22,   // + TMEM buffer (kDKDV): dS^T written (kPReady + buffer: P^T written)
   kDrain = 24,
-  kNumBars = 25
+  kJoin = 25,      // kDKDV: the softmax threads have stored a part's sums; then: know its rank
+  kNumBars = 26
 };
 // kDQ keeps packed dS in its own double buffer of TMEM columns (acc0 ends at
 // 256 + D <= 384), so S and dP of the next step can be issued while the
@@ -93,6 +94,7 @@ enum BBar : int {
 constexpr uint32_t kDsBuf = 384;
 constexpr int kTmemSlot = kNumBars * 8;
 constexpr int kAbortSlot = kNumBars * 8 + 4;
+constexpr int kRankSlot = kNumBars * 8 + 8;
 
 struct BParams {
   int* head;            // the plan's list
@@ -107,6 +109,8 @@ struct BParams {
   __nv_bfloat16* g0;    // dQ (kDQ) or dV (kDKDV)
   __nv_bfloat16* g1;    // dK (kDKDV)
   long long gs0[2], gs1[2];  // their strides: row, head
+  float4* sums;         // kDKDV: [slot][Hk][dV, dK][d / 4][128] of the tiles in parts
+  int* done;
   int* err;
   unsigned long long timeout_ns;
   int fault_drop;       // test hook: CTA 0 never loads its first streamed X0 tile
@@ -118,6 +122,7 @@ struct BItem {
   int row0, len, hk;
   int t0, tokens;
   int x_lo, x_hi;
+  int slot, part, parts;  // kDKDV: of a tile in parts, the part's slot, its index, their number
 };
 template <bool kDKDV>
 __device__ __forceinline__ void decode_bitem(const BParams& p, const PackedOrder& order, int w,
@@ -133,10 +138,30 @@ __device__ __forceinline__ void decode_bitem(const BParams& p, const PackedOrder
   if (kDKDV) {  // query tiles that see a key of the tile
     it.x_lo = p.causal ? it.t0 / p.tq : 0;
     it.x_hi = (it.len - 1) / p.tq;
+    it.slot = (e.w & 0xffff) - 1;
+    it.part = 0;
+    it.parts = 1;
+    if (e.w != 0) {
+      const int chunk = p.head[2];
+      it.part = e.w >> 16;
+      it.parts = (it.x_hi - it.x_lo) / chunk + 1;
+      it.x_lo += it.part * chunk;
+      it.x_hi = min(it.x_hi, it.x_lo + chunk - 1);
+    }
   } else {      // key tiles seen by a row of the tile
     it.x_lo = 0;
     it.x_hi = ((p.causal ? it.t0 + it.tokens : it.len) - 1) / kT;
   }
+}
+
+// What another block wrote during this kernel (past L1).
+__device__ __forceinline__ float4 load_cg(const float4* at) {
+  float4 f;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+               : "l"(at)
+               : "memory");
+  return f;
 }
 
 template <int D, bool kDKDV>
@@ -154,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int idx) -> uint32_t { return bars + 8u * static_cast<uint32_t>(idx); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kBar + kTmemSlot);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Lay::kBar + kAbortSlot);
+  volatile int* rank = reinterpret_cast<volatile int*>(smem + Lay::kBar + kRankSlot);
   float* vec = reinterpret_cast<float*>(smem + Lay::kVec);
   const ItemRing ring{sbase + Lay::kRingOff,
                       reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 2 * kRing * 8)};
@@ -184,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(kVecFull + b2), kT);
       ptx::mbar_init(bar(kVecFree + b2), kSoftmaxThreads);
     }
+    ptx::mbar_init(bar(kJoin), kSoftmaxThreads);
     ptx::mbar_init(bar(kPReadyS), kSoftmaxThreads);
     ptx::mbar_init(bar(kPReadyS + 1), kSoftmaxThreads);
     ptx::mbar_init(bar(kDrain), 1);
@@ -491,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // whose constants it loads
     const int packed_row = kDKDV ? static_cast<int>(threadIdx.x) : row_in_tile;
     const int my_token = packed_row / p.G, my_head = packed_row - my_token * p.G;
-    uint32_t s_cnt = 0, item_cnt = 0, h_cnt = 0;
+    uint32_t s_cnt = 0, item_cnt = 0, h_cnt = 0, join_cnt = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int w = ring_get(ring, static_cast<uint32_t>(k), abort_flag, p);
@@ -704,6 +731,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_warp(bar(kAccFull), item_cnt & 1u, abort_flag, p)) { ok = false; break; }
       ++item_cnt;
       ptx::tc_fence_after();
+      // A part of a tile: its sums go to its slot, and the last of the tile's parts to end adds
+      // them all up, in the parts' order whoever is last.  A thread reads what threads of its
+      // own place wrote.
+      const bool in_parts = kDKDV && it.parts > 1;
+      const float4* first_part = nullptr;
+      if (in_parts) {
+        constexpr int kSlot = 2 * (D / 4) * kT;  // float4 of a slot
+        float4* const to = p.sums + (static_cast<size_t>(it.slot) * p.Hk + it.hk) * kSlot;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int ch = 0; ch < D / 64; ++ch) {
+            const int c0 = wg * (D / 2) + ch * 32;
+            uint32_t ov[32];
+            ptx::tmem_ld32((a == 0 ? tA0 : tA1) + c0, ov);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence(ov);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              to[(a * (D / 4) + c0 / 4 + x) * kT + row_in_tile] =
+                  make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]),
+                              __uint_as_float(ov[4 * x + 2]), __uint_as_float(ov[4 * x + 3]));
+          }
+        __threadfence();
+        ptx::mbar_arrive(bar(kJoin));
+        if (!wait_warp(bar(kJoin), join_cnt & 1u, abort_flag, p)) { ok = false; break; }
+        ++join_cnt;
+        if (threadIdx.x == 0) {
+          *rank = atomicAdd(p.done + (it.slot - it.part) * p.Hk + it.hk, 1);
+          __threadfence();
+        }
+        ptx::mbar_arrive(bar(kJoin));
+        if (!wait_warp(bar(kJoin), join_cnt & 1u, abort_flag, p)) { ok = false; break; }
+        ++join_cnt;
+        if (*rank != it.parts - 1) continue;
+        __threadfence();
+        first_part = p.sums + (static_cast<size_t>(it.slot - it.part) * p.Hk + it.hk) * kSlot;
+      }
 #pragma unroll
       for (int a = 0; a < (kDKDV ? 2 : 1); ++a) {
         const uint32_t tacc = a == 0 ? tA0 : tA1;
@@ -715,9 +780,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ch = 0; ch < D / 64; ++ch) {
           const int c0 = wg * (D / 2) + ch * 32;
           uint32_t ov[32];
-          ptx::tmem_ld32(tacc + c0, ov);
-          ptx::tmem_wait_ld();
-          ptx::reg_fence(ov);
+          if (kDKDV && in_parts) {
+            float sum[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) sum[x] = 0.f;
+            const float4* at = first_part + (a * (D / 4) + c0 / 4) * kT + row_in_tile;
+            for (int j = 0; j < it.parts; ++j, at += static_cast<size_t>(p.Hk) * 2 * (D / 4) * kT) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const float4 f = load_cg(at + x * kT);
+                sum[4 * x] += f.x;
+                sum[4 * x + 1] += f.y;
+                sum[4 * x + 2] += f.z;
+                sum[4 * x + 3] += f.w;
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(sum[x]);
+          } else {
+            ptx::tmem_ld32(tacc + c0, ov);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence(ov);
+          }
           if (row_valid) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -767,7 +851,7 @@ cudaError_t launch_packed_bwd(const PackedArgs& a, BParams p, const PackedList& 
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(
-      sm_count(), packed_items(a.T, p.n_seqs, list.tokens) * a.Hk)));
+      sm_count(), (packed_items(a.T, p.n_seqs, list.tokens) + list.slots) * a.Hk)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Lay::kAlloc;
   cfg.stream = stream;
@@ -804,15 +888,24 @@ cudaError_t launch_packed_pair(const PackedArgs& a, const BParams& dkdv, const B
   return e;
 }
 
-// Byte offsets of the workspace's parts: the lists of key tiles and of query tiles, and D.
+// Byte offsets of the workspace's parts: the lists of key tiles (with its parts) and of query
+// tiles, D, and the sums of key tiles in parts.
 struct Space {
-  long long keys, queries, delta, total;
-  Space(int T, int n, int Hq, int tq) {
+  int slots;  // of a key head
+  long long keys, queries, delta, done, sums, total;
+  Space(int T, int n, int Hq, int Hk, int d) {
+    const int tq = kT / (Hq / Hk);
+    // All parts of a call, none shorter than the shortest, and as many as the plan cuts (its
+    // share of a CTA's work makes 2 / 0.6 of the grid's at most).
+    const long long most = packed_items(T, n, kT) * (T / tq / kLeastPart + 1);
+    slots = static_cast<int>(std::min<long long>(most, (kMaxParts + Hk - 1) / Hk));
     const auto up = [](long long x) { return (x + 255) / 256 * 256; };
     keys = 0;
-    queries = up(packed_list_bytes(T, n, kT));
+    queries = up(packed_list_bytes(T, n, kT) + 16LL * slots);
     delta = queries + up(packed_list_bytes(T, n, tq));
-    total = delta + up(4LL * T * Hq);
+    done = delta + up(4LL * T * Hq);
+    sums = done + up(4LL * slots * Hk);
+    total = sums + 8LL * slots * Hk * kT * d;
   }
 };
 
@@ -823,7 +916,7 @@ extern "C" {
 
 int64_t cp_packed_attn_bwd_workspace_bytes(int T, int n_seqs, int Hq, int Hk, int d) {
   if (cpring::check_packed(T, n_seqs, Hq, Hk, d, 0) != CP_OK) return -1;
-  return cpring::Space(T, n_seqs, Hq, cpring::kTileRows / (Hq / Hk)).total;
+  return cpring::Space(T, n_seqs, Hq, Hk, d).total;
 }
 
 cp_status cp_packed_attn_bwd(const void* q, const int64_t* q_strides, const void* k,
@@ -853,12 +946,14 @@ cp_status cp_packed_attn_bwd(const void* q, const int64_t* q_strides, const void
       !packed_strides(dk_strides, Hk, d, dks) || !packed_strides(dv_strides, Hk, d, dvs))
     return CP_ERR_ALIGN;
   const int G = Hq / Hk, tq = kTileRows / G;
-  const Space sp(T, n_seqs, Hq, tq);
+  const Space sp(T, n_seqs, Hq, Hk, d);
   if (workspace_bytes < sp.total) return CP_ERR_BUFFER;
   if (device_cc() != 103) return CP_ERR_DEVICE;
   char* const ws = static_cast<char*>(workspace);
   PackedPlan plan{};
-  plan.list[0] = packed_list(ws + sp.keys, T, n_seqs, kT, true);
+  plan.list[0] = packed_list(ws + sp.keys, T, n_seqs, kT, true, sp.slots);
+  plan.list[0].done = reinterpret_cast<int*>(ws + sp.done);
+  plan.tq = tq; plan.Hk = Hk; plan.grid = sm_count();
   plan.list[1] = packed_list(ws + sp.queries, T, n_seqs, tq, false);
   plan.lists = 2;
   plan.offsets = seq_offsets;
@@ -880,6 +975,8 @@ cp_status cp_packed_attn_bwd(const void* q, const int64_t* q_strides, const void
   p.err = plan.err;
   p.timeout_ns = test_wait_limit_ns();
   p.fault_drop = test_fault_drop();
+  p.sums = reinterpret_cast<float4*>(ws + sp.sums);
+  p.done = plan.list[0].done;
   BParams pq = p;
   p.g0 = static_cast<__nv_bfloat16*>(dv);
   p.g1 = static_cast<__nv_bfloat16*>(dk);

@@ -10,6 +10,7 @@
 // the CTA that computes an item, never a result.  Bound by the latency of its few passes.
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "packed.cuh"
@@ -44,6 +45,31 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sum, int& total) {
   return y - x + (warp > 0 ? before : 0);
 }
 
+__device__ __forceinline__ long long block_sum(long long x, long long* warp_sum) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  __syncthreads();  // an earlier call's sums are read
+  if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0;
+  for (int w = 0; w < kWarps; ++w) x += warp_sum[w];
+  return x;
+}
+
+constexpr float kShare = 0.6f;
+
+// Packed query tiles that see a key of an item's tile, and the bucket of part j of `chunk` of them.
+__device__ __forceinline__ int first_streamed(const PackedPlan& p, const int4& it) {
+  return p.causal ? it.z * kTileRows / p.tq : 0;
+}
+__device__ __forceinline__ int streamed_tiles(const PackedPlan& p, const int4& it) {
+  return (it.y - 1) / p.tq - first_streamed(p, it) + 1;
+}
+__device__ __forceinline__ int part_bucket(const PackedPlan& p, const int4& it, int j, int chunk) {
+  const int tiles = min(chunk, streamed_tiles(p, it) - j * chunk);
+  return max(0, p.n_buckets - 1 - (tiles * p.tq + kCostUnit - 1) / kCostUnit);
+}
+
 // D of rows dealt over `blocks` blocks: 8 entries to a lane, d / 8 lanes to a row.
 __device__ __forceinline__ void row_dots(const PackedPlan& p, int block, int blocks) {
   const int lanes = p.d / 8;
@@ -69,7 +95,8 @@ __device__ __forceinline__ void row_dots(const PackedPlan& p, int block, int blo
 }
 
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedPlan p) {
-  __shared__ int warp_sum[kWarps];
+  __shared__ int warp_sum[kWarps], next_slot;
+  __shared__ long long wide_sum[kWarps];
   __shared__ int near_starts[kSmall], near_buckets[kSmall];
   cudaTriggerProgrammaticLaunchCompletion();  // the attention's blocks may line up
   if (blockIdx.x >= p.lists) {
@@ -104,10 +131,6 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     }
     return;
   }
-  if (threadIdx.x == 0) {
-    l.head[0] = items;
-    l.head[1] = 0;
-  }
   // Item x: its sequence's rows, its tile, and the bucket of its cost (0: the largest).
   auto item = [&](int x, int& bucket) {
     int lo = 0, hi = p.n;  // the last sequence that starts at or before x; empty ones are passed
@@ -125,10 +148,45 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     bucket = p.n_buckets - 1 - (cost + kCostUnit - 1) / kCostUnit;
     return make_int4(row, len, tile, 0);
   };
+  // Tiles of keys are cut where the largest is more than its share of a CTA's work: into parts of
+  // kShare of that share, so that a call of few tiles fills the GPU and ends at one time.  (A
+  // part costs its start, its sums' way through memory and their addition; measured in
+  // packed_bwd_sm103.cu.)
+  int chunk = INT_MAX;
+  auto parts_of = [&](const int4& it) {
+    return (streamed_tiles(p, it) - 1) / chunk + 1;
+  };
+  if (l.slots > 0) {
+    long long all = 0;
+    for (int x = threadIdx.x; x < items; x += kPlanThreads) {
+      int b;
+      all += streamed_tiles(p, item(x, b));
+    }
+    all = block_sum(all, wide_sum);
+    const long long share = static_cast<long long>(kShare * static_cast<float>(all) * p.Hk / p.grid);
+    chunk = static_cast<int>(min(max(share, static_cast<long long>(kLeastPart)), 1LL << 30));
+    for (;;) {  // as many parts as there are slots
+      int parts = 0;
+      for (int x = threadIdx.x; x < items; x += kPlanThreads) {
+        int b;
+        const int n = parts_of(item(x, b));
+        parts += n > 1 ? n : 0;
+      }
+      if (block_sum(static_cast<long long>(parts), wide_sum) <= l.slots) break;
+      chunk *= 2;
+    }
+    for (int i = threadIdx.x; i < l.slots * p.Hk; i += kPlanThreads) l.done[i] = 0;
+    if (threadIdx.x == 0) l.head[2] = chunk;
+  }
   for (int x = threadIdx.x; x < items; x += kPlanThreads) {
     int b;
-    item(x, b);
-    atomicAdd(buckets + b, 1);
+    const int4 it = item(x, b);
+    const int n = l.slots > 0 ? parts_of(it) : 1;
+    if (n == 1) {
+      atomicAdd(buckets + b, 1);
+    } else {
+      for (int j = 0; j < n; ++j) atomicAdd(buckets + part_bucket(p, it, j, chunk), 1);
+    }
   }
   __syncthreads();
   int placed = 0;
@@ -140,11 +198,25 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     if (i < p.n_buckets) buckets[i] = placed + before;
     placed += total;
   }
+  if (threadIdx.x == 0) {
+    l.head[0] = placed;
+    l.head[1] = 0;
+    next_slot = 0;
+  }
   __syncthreads();
   for (int x = threadIdx.x; x < items; x += kPlanThreads) {
     int b;
-    const int4 it = item(x, b);
-    l.items[atomicAdd(buckets + b, 1)] = it;
+    int4 it = item(x, b);
+    const int n = l.slots > 0 ? parts_of(it) : 1;
+    if (n == 1) {
+      l.items[atomicAdd(buckets + b, 1)] = it;
+      continue;
+    }
+    const int slot = atomicAdd(&next_slot, n);
+    for (int j = 0; j < n; ++j) {
+      const int at = atomicAdd(buckets + part_bucket(p, it, j, chunk), 1);
+      l.items[at] = make_int4(it.x, it.y, it.z, 1 + slot + j + (j << 16));
+    }
   }
 }
 

@@ -349,3 +349,19 @@ def test_a_wait_that_runs_out_is_reported():
     finally:
         pkg.test_set_wait_fault(False)
     p.check(*p.forward())
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,Hq,Hk,d", [
+    ([1500], 2, 1, 128),             # few key tiles of many queries: cut into parts
+    ([900, 40, 7], 14, 2, 64),       # beside tiles that are not
+    ([400, 1100], 8, 1, 128),
+])
+def test_gradients_of_key_tiles_in_parts(lens, Hq, Hk, d, causal):
+    """The parts are added up in one order, whichever ends last."""
+    p = Prompts(lens, Hq, Hk, d, seed=21)
+    out, lse = p.forward(causal)
+    grads = p.backward(out, lse, causal)
+    p.check_gradients(out, lse, grads, causal)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(grads, p.backward(out, lse, causal)))
