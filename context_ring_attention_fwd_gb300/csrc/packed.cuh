@@ -108,6 +108,64 @@ inline PackedList packed_list(char* at, int T, int n, int tokens, bool of_keys, 
 
 namespace {
 
+// One CTA's claims of a list: its first item is its own index, later ones come from the
+// list's counter (which the plan clears at every call, so a replayed graph starts afresh).
+__device__ __forceinline__ int packed_claim(int* head, int grid) {
+  return grid + atomicAdd(head + 1, 1);
+}
+
+// The CTA's ring of items, as the list has them and with their key heads: the producer reads
+// an item once, ahead of its use, and the other roles from shared memory.  (Each reading the
+// list waited for L2 at every item's start.)  Full barriers take the producer's arrival, empty
+// ones one of each softmax warp; the MMA warp reads a slot with its item's Q (or fixed tiles),
+// before its softmax can be done.
+struct PackedEntry {
+  int4 e;
+  int hk;  // -1: no more items
+};
+struct PackedRing {
+  uint32_t bars;             // shared address: kRing full barriers, then kRing empty ones
+  volatile int (*slots)[8];  // e.x .. e.w, hk
+  __device__ uint32_t full(uint32_t k) const { return bars + 8u * (k % kRing); }
+  __device__ uint32_t empty(uint32_t k) const { return bars + 8u * (kRing + k % kRing); }
+  __device__ void init(int readers) const {
+    for (int s = 0; s < kRing; ++s) {
+      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(empty(s), readers);
+    }
+  }
+  // Producer (one thread): the CTA's k-th item.
+  template <class P>
+  __device__ bool put(uint32_t k, const PackedEntry& x, volatile uint32_t* abort_flag,
+                      const P& p) const {
+    if (k >= kRing && !wait1(empty(k), (k / kRing - 1) & 1u, abort_flag, p)) return false;
+    volatile int* const to = slots[k % kRing];
+    to[0] = x.e.x;
+    to[1] = x.e.y;
+    to[2] = x.e.z;
+    to[3] = x.e.w;
+    to[4] = x.hk;
+    ptx::mbar_arrive(full(k));
+    return true;
+  }
+  __device__ PackedEntry read(uint32_t k) const {
+    const volatile int* const from = slots[k % kRing];
+    return PackedEntry{make_int4(from[0], from[1], from[2], from[3]), from[4]};
+  }
+  // A softmax warp (every lane): the k-th item; false if the wait gave up.
+  template <class P>
+  __device__ bool get(uint32_t k, PackedEntry& x, volatile uint32_t* abort_flag,
+                      const P& p) const {
+    if (!wait_warp(full(k), (k / kRing) & 1u, abort_flag, p)) return false;
+    x = read(k);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(empty(k));
+    return true;
+  }
+};
+constexpr int kPackedRingBytes = 2 * kRing * 8 + kRing * 32 + 16;  // barriers, slots, the MMA warp's word
+static_assert(kPackedRingBytes <= 256, "the item ring's shared-memory block");
+
 // The (tile, key head) pair of item w: groups of `hg` heads, in a group the list's order.
 // A long list walks few heads at a time, whose keys then come from L2: the smallest group
 // whose items fill the grid once; a short one (under 16 rounds of the grid) is one pool, so
@@ -119,18 +177,39 @@ struct PackedOrder {
     group = heads;
     if (n >= 16LL * grid) group = max(1, min(heads, (grid + items - 1) / items));
   }
-  __device__ void at(int w, int& tile, int& head) const {
+  // Item w of the list at `list`, whose key head is -1 behind the last.
+  __device__ PackedEntry at(const int4* list, int w) const {
+    if (w >= n) return PackedEntry{make_int4(0, 0, 0, 0), -1};
     const int g = w / (group * items), r = w - g * group * items;
     const int in_group = min(group, heads - g * group);
-    tile = r / in_group;
-    head = g * group + r - tile * in_group;
+    const int tile = r / in_group;
+    return PackedEntry{list[tile], g * group + r - tile * in_group};
   }
 };
 
-// One CTA's claims of a list: its first item is its own index, later ones come from the
-// list's counter (which the plan clears at every call, so a replayed graph starts afresh).
-__device__ __forceinline__ int packed_claim(int* head, int grid) {
-  return grid + atomicAdd(head + 1, 1);
+// A warp's 32 rows of 128 bytes in shared memory, 16-byte chunk c of row r at c ^ (r mod 8), from
+// which rows are written to memory by whole lines: a thread that stores its own row writes half
+// sectors of 32 lines at a time.
+constexpr int kRowStage = 32 * 128;
+__device__ __forceinline__ void stage_chunk(uint32_t base, int row, int chunk, uint32_t a,
+                                            uint32_t b, uint32_t c, uint32_t d) {
+  ptx::st_shared_v4(base + row * 128 + ((chunk ^ (row & 7)) << 4), a, b, c, d);
+}
+// `to`: where this lane's row starts (null: it is not written).
+__device__ __forceinline__ void write_rows(uint32_t base, __nv_bfloat16* to, int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = i * 4 + lane / 8, chunk = lane % 8;
+    const unsigned long long at =
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), row);
+    uint4 u;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "r"(base + row * 128 + ((chunk ^ (row & 7)) << 4)));
+    if (at != 0) reinterpret_cast<uint4*>(at)[chunk] = u;
+  }
+  __syncwarp();
 }
 
 // Zeroes the bytes [from, to) of shared memory (multiples of 16) with the lanes of a warp.

@@ -125,11 +125,9 @@ struct BItem {
   int slot, part, parts;  // kDKDV: of a tile in parts, the part's slot, its index, their number
 };
 template <bool kDKDV>
-__device__ __forceinline__ void decode_bitem(const BParams& p, const PackedOrder& order, int w,
-                                             BItem& it) {
-  int x;
-  order.at(w, x, it.hk);
-  const int4 e = p.items[x];
+__device__ __forceinline__ void decode_bitem(const BParams& p, const PackedEntry& x, BItem& it) {
+  const int4 e = x.e;
+  it.hk = x.hk;
   it.row0 = e.x;
   it.len = e.y;
   const int tile = kDKDV ? kT : p.tq;
@@ -151,6 +149,20 @@ __device__ __forceinline__ void decode_bitem(const BParams& p, const PackedOrder
   } else {      // key tiles seen by a row of the tile
     it.x_lo = 0;
     it.x_hi = ((p.causal ? it.t0 + it.tokens : it.len) - 1) / kT;
+  }
+}
+
+// The columns [lo, hi] of 32 as bits, and packed bf16 pairs of 32 columns with the others
+// zeroed: what masked pairs of a query and a key hold is replaced, whatever it is.
+__device__ __forceinline__ uint32_t seen_columns(int lo, int hi) {
+  const uint32_t below = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
+  return lo <= 0 ? below : lo > 31 ? 0u : below & (0xffffffffu << lo);
+}
+__device__ __forceinline__ void keep_pairs(uint32_t (&pk)[16], uint32_t columns) {
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    const uint32_t two = columns >> (2 * x);
+    pk[x] &= (two & 1u ? 0x0000ffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
   }
 }
 
@@ -181,10 +193,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Lay::kBar + kAbortSlot);
   volatile int* rank = reinterpret_cast<volatile int*>(smem + Lay::kBar + kRankSlot);
   float* vec = reinterpret_cast<float*>(smem + Lay::kVec);
-  const ItemRing ring{sbase + Lay::kRingOff,
-                      reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 2 * kRing * 8)};
-  // the item whose fixed tiles the producer is loading (the MMA warp's copy)
-  volatile int* fix_item = reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 128);
+  const PackedRing ring{
+      sbase + Lay::kRingOff,
+      reinterpret_cast<volatile int(*)[8]>(smem + Lay::kRingOff + 2 * kRing * 8)};
+  // the ring's index of the item whose fixed tiles the producer is loading, for the MMA warp
+  volatile int* fix_item =
+      reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 2 * kRing * 8 + kRing * 32);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -214,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(bar(kPReadyS), kSoftmaxThreads);
     ptx::mbar_init(bar(kPReadyS + 1), kSoftmaxThreads);
     ptx::mbar_init(bar(kDrain), 1);
-    ring_init(ring, kSoftmaxThreads / 32);  // the softmax warps read the ring
+    ring.init(kSoftmaxThreads / 32);
     *abort_flag = 0u;
     ptx::fence_barrier_init();
   }
@@ -233,7 +247,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   cudaGridDependencySynchronize();  // the plan and D
-  const PackedOrder order(p.head[0], p.Hk, gridDim.x);
   const int x_tokens = kDKDV ? p.tq : kT;  // of a streamed tile
   const uint32_t packed_bytes = static_cast<uint32_t>(packed_rows) * 128u * Lay::kPanels;
   const uint32_t fix_bytes = kDKDV ? Lay::kTileBytes : packed_bytes;
@@ -249,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tma_prefetch_desc(&tm_f1);
       ptx::tma_prefetch_desc(&tm_x0);
       ptx::tma_prefetch_desc(&tm_x1);
+      const PackedOrder order(p.head[0], p.Hk, gridDim.x);
       uint32_t x_iter = 0, fix_iter = 0;
       uint32_t armed0[3] = {0u, 0u, 0u}, armed1[2] = {0u, 0u};  // loads started per slot
       int ahead = 0;  // the claim of the CTA's next item
@@ -256,14 +270,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int w = k == 0 ? static_cast<int>(blockIdx.x) : ahead;
-        if (!ring_put(ring, static_cast<uint32_t>(k), w, abort_flag, p)) { ok = false; break; }
-        if (w >= order.n) break;
-        ahead = packed_claim(p.head, gridDim.x);  // read when that item starts
+        const PackedEntry entry = order.at(p.items, w);
+        if (entry.hk >= 0) ahead = packed_claim(p.head, gridDim.x);  // read when that item starts
+        if (!ring.put(static_cast<uint32_t>(k), entry, abort_flag, p)) { ok = false; break; }
+        if (entry.hk < 0) break;
         BItem it;
-        decode_bitem<kDKDV>(p, order, w, it);
+        decode_bitem<kDKDV>(p, entry, it);
         const int fix_head = kDKDV ? it.hk : it.hk * p.G, x_head = kDKDV ? it.hk * p.G : it.hk;
         if (!wait1(bar(kFixEmpty), (fix_iter & 1u) ^ 1u, abort_flag, p)) { ok = false; break; }
-        *fix_item = w;  // the MMA warp reads it once this phase of kFixFull completes
+        *fix_item = k;  // the MMA warp reads it once this phase of kFixFull completes
         ptx::mbar_arrive_expect_tx(bar(kFixFull), 2 * fix_bytes);
         for (int pn = 0; pn < Lay::kPanels; ++pn) {
           ptx::tma_load_3d(sbase + Lay::kF0 + pn * Lay::kPanelBytes, &tm_f0, bar(kFixFull),
@@ -299,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // No more items: tell the MMA warp through the next phase of kFixFull.
       if (ok && wait1(bar(kFixEmpty), (fix_iter & 1u) ^ 1u, abort_flag, p)) {
-        *fix_item = INT_MAX;
+        *fix_item = -1;
         ptx::mbar_arrive(bar(kFixFull));
         ++fix_iter;
       }
@@ -387,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // wait beyond the one for those tiles.
         if (!wait_warp(bar(kFixFull), fix_iter & 1u, abort_flag, p)) { ok = false; break; }
         ++fix_iter;
-        const int w = *fix_item;
-        if (w >= order.n) break;
+        const int k = *fix_item;
+        if (k < 0) break;
         BItem it;
-        decode_bitem<kDKDV>(p, order, w, it);
+        decode_bitem<kDKDV>(p, ring.read(static_cast<uint32_t>(k)), it);
         ptx::tc_fence_after();
         // rows of the last streamed tile: keys, or tokens times heads
         const int x_left = it.len - it.x_hi * x_tokens;
@@ -521,11 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s_cnt = 0, item_cnt = 0, h_cnt = 0, join_cnt = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      const int w = ring_get(ring, static_cast<uint32_t>(k), abort_flag, p);
-      if (w < 0) { ok = false; break; }
-      if (w >= order.n) break;
+      PackedEntry entry;
+      if (!ring.get(static_cast<uint32_t>(k), entry, abort_flag, p)) { ok = false; break; }
+      if (entry.hk < 0) break;
       BItem it;
-      decode_bitem<kDKDV>(p, order, w, it);
+      decode_bitem<kDKDV>(p, entry, it);
       // This thread's row: a key, or a token and a head.  One that is not stored sees
       // everything, so that it does not hold its warp to the masked pass.
       const int row_token = kDKDV ? row_in_tile : my_token;
@@ -592,34 +607,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int ch = 0; ch < 2; ++ch) {
             const int c0 = col0 + ch * 32;
             uint32_t pk_s[16];
-            if (__all_sync(0xffffffffu, c_lo <= c0 && c_hi >= c0 + 31)) {
-              // every column visible to every row of the warp: paired fp32
 #pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                float e0, e1, g0, g1;
-                ptx::fma_f32x2(e0, e1, __uint_as_float(sv[ch][2 * x]), __uint_as_float(sv[ch][2 * x + 1]),
-                               sc, sc, -lse2_r, -lse2_r);
-                const float p0 = ptx::ex2(e0), p1 = ptx::ex2(e1);
-                ptx::fma_f32x2(g0, g1, __uint_as_float(dv[ch][2 * x]), __uint_as_float(dv[ch][2 * x + 1]),
-                               1.f, 1.f, -d_r, -d_r);
-                ptx::fma_f32x2(g0, g1, p0, p1, g0, g1, 0.f, 0.f);
-                pk_s[x] = ptx::pack_bf16(g0, g1);
-              }
-            } else {
-#pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                float dsr[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int cc = c0 + 2 * x + e;
-                  const bool vis = cc >= c_lo && cc <= c_hi;
-                  const float pv =
-                      vis ? ptx::ex2(fmaf(__uint_as_float(sv[ch][2 * x + e]), sc, -lse2_r)) : 0.f;
-                  dsr[e] = vis ? pv * (__uint_as_float(dv[ch][2 * x + e]) - d_r) : 0.f;
-                }
-                pk_s[x] = ptx::pack_bf16(dsr[0], dsr[1]);
-              }
+            for (int x = 0; x < 16; ++x) {  // paired fp32
+              float e0, e1, g0, g1;
+              ptx::fma_f32x2(e0, e1, __uint_as_float(sv[ch][2 * x]), __uint_as_float(sv[ch][2 * x + 1]),
+                             sc, sc, -lse2_r, -lse2_r);
+              const float p0 = ptx::ex2(e0), p1 = ptx::ex2(e1);
+              ptx::fma_f32x2(g0, g1, __uint_as_float(dv[ch][2 * x]), __uint_as_float(dv[ch][2 * x + 1]),
+                             1.f, 1.f, -d_r, -d_r);
+              ptx::fma_f32x2(g0, g1, p0, p1, g0, g1, 0.f, 0.f);
+              pk_s[x] = ptx::pack_bf16(g0, g1);
             }
+            if (__any_sync(0xffffffffu, c_lo > c0 || c_hi < c0 + 31))
+              keep_pairs(pk_s, seen_columns(c_lo - c0, c_hi - c0));
             ptx::tmem_st16(tmem_base + lane_off + kDsBuf + (n & 1u) * 64u + c0 / 2, pk_s);
           }
           ptx::tmem_wait_st();
@@ -650,11 +650,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float4* nd4 = reinterpret_cast<const float4*>(vec + (buf * 2 + 1) * kT + c0);
           // P^T first: it is stored and announced (kPReady) before dS^T is
           // formed, so the MMA warp starts dV += P^T dO meanwhile.
-          const bool all_visible = __all_sync(0xffffffffu, c_lo <= c0 && c_hi >= c0 + 31);
-          if (all_visible) {
-            // every column visible to every row of the warp: paired fp32
+          const bool masked = __any_sync(0xffffffffu, c_lo > c0 || c_hi < c0 + 31);
+          const uint32_t columns = seen_columns(c_lo - c0, c_hi - c0);
+          {
 #pragma unroll
-            for (int x4 = 0; x4 < 8; ++x4) {
+            for (int x4 = 0; x4 < 8; ++x4) {  // paired fp32
               const float4 nl = nl4[x4];
               const float nla[4] = {nl.x, nl.y, nl.z, nl.w};
 #pragma unroll
@@ -668,26 +668,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pk_p[x] = ptx::pack_bf16(pf[2 * x], pf[2 * x + 1]);
               }
             }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int cc = c0 + 2 * x + e;
-                const bool vis = cc >= c_lo && cc <= c_hi;
-                pf[2 * x + e] =
-                    vis ? ptx::ex2(fmaf(__uint_as_float(sv[2 * x + e]), sc, vec[(buf * 2 + 0) * kT + cc]))
-                        : 0.f;
-              }
-              pk_p[x] = ptx::pack_bf16(pf[2 * x], pf[2 * x + 1]);
-            }
           }
+          if (masked) keep_pairs(pk_p, columns);
           ptx::tmem_st16(tb, pk_p);
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
           ptx::mbar_arrive(bar(kPReady + b));
           // dS^T = P^T (dP^T - D)
-          if (all_visible) {
+          {
 #pragma unroll
             for (int x4 = 0; x4 < 8; ++x4) {
               const float4 nd = nd4[x4];
@@ -702,21 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pk_s[x] = ptx::pack_bf16(g0, g1);
               }
             }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              float dsr[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int cc = c0 + 2 * x + e;
-                const bool vis = cc >= c_lo && cc <= c_hi;
-                dsr[e] = vis ? pf[2 * x + e] *
-                                   (__uint_as_float(dv[2 * x + e]) + vec[(buf * 2 + 1) * kT + cc])
-                             : 0.f;
-              }
-              pk_s[x] = ptx::pack_bf16(dsr[0], dsr[1]);
-            }
           }
+          if (masked) keep_pairs(pk_s, columns);
           ptx::tmem_st16(tb + 64, pk_s);
           ptx::tmem_wait_st();
           ptx::tc_fence_before();

@@ -46,7 +46,6 @@ constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kTmemCols = 512;
-constexpr float kRescaleLog2 = 8.0f;
 constexpr float kOverflowGuard = 18446744073709551616.0f;  // 2^64
 constexpr float kOverflowGuardLog2 = 64.0f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -61,7 +60,8 @@ struct Layout {
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
   static constexpr int kBarOff = kVOff + kStages * kTileBytes;
   static constexpr int kRingOff = kBarOff + 256;  // the item ring
-  static constexpr int kBytes = kRingOff + 256;
+  static constexpr int kStageOff = kRingOff + 256;  // the softmax warps' rows on their way out
+  static constexpr int kBytes = kStageOff + kSoftmaxWarps * kRowStage;
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024 B
 };
 
@@ -102,11 +102,9 @@ struct FwdItem {
   int row0, len, hk;
   int token[kQTiles], tokens[kQTiles], last[kQTiles];
 };
-__device__ __forceinline__ void fwd_item(const FwdParams& p, const PackedOrder& order, int w,
-                                         FwdItem& it) {
-  int x;
-  order.at(w, x, it.hk);
-  const int4 e = p.items[x];
+__device__ __forceinline__ void fwd_item(const FwdParams& p, const PackedEntry& x, FwdItem& it) {
+  const int4 e = x.e;
+  it.hk = x.hk;
   it.row0 = e.x;
   it.len = e.y;
 #pragma unroll
@@ -115,6 +113,26 @@ __device__ __forceinline__ void fwd_item(const FwdParams& p, const PackedOrder& 
     it.tokens[t] = max(0, min(p.tq, it.len - it.token[t]));
     const int seen = p.causal ? it.token[t] + it.tokens[t] : it.len;
     it.last[t] = it.tokens[t] > 0 ? (seen - 1) / kBN : -1;
+  }
+}
+
+// This thread's 128 scores of the S tile, with columns behind c_hi set to -inf (chunk by
+// chunk: one that the whole warp sees whole costs a test).
+__device__ __forceinline__ void load_seen(uint32_t tS, int c_hi, uint32_t (&sv)[4][32]) {
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tS + ch * 32, sv[ch]);
+  ptx::tmem_wait_ld();
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) ptx::reg_fence(sv[ch]);
+  if (__all_sync(0xffffffffu, c_hi >= kBN - 1)) return;
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    const int hi = c_hi - ch * 32;
+    if (__all_sync(0xffffffffu, hi >= 31)) continue;
+    const uint32_t seen = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
+#pragma unroll
+    for (int x = 0; x < 32; ++x)
+      if (!(seen >> x & 1u)) sv[ch][x] = __float_as_uint(-INFINITY);
   }
 }
 
@@ -133,10 +151,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kBarOff + kTmemSlot);
   volatile uint32_t* abort_flag =
       reinterpret_cast<volatile uint32_t*>(smem + Lay::kBarOff + kAbortSlot);
-  const ItemRing ring{sbase + Lay::kRingOff,
-                      reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 2 * kRing * 8)};
-  // the item whose Q the producer is loading (the MMA warp's copy of the work)
-  volatile int* q_item = reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 128);
+  const PackedRing ring{
+      sbase + Lay::kRingOff,
+      reinterpret_cast<volatile int(*)[8]>(smem + Lay::kRingOff + 2 * kRing * 8)};
+  // the ring's index of the item whose Q the producer is loading, for the MMA warp
+  volatile int* q_item =
+      reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 2 * kRing * 8 + kRing * 32);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -157,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(kOBar + t), 1);
     }
     ptx::mbar_init(bar(kDrain), 1);
-    ring_init(ring, kSoftmaxWarps);
+    ring.init(kSoftmaxWarps);
     *abort_flag = 0u;
     ptx::fence_barrier_init();
   }
@@ -170,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   cudaGridDependencySynchronize();  // the plan
-  const PackedOrder order(p.head[0], p.Hk, gridDim.x);
 
   if (warp >= kProducerWarp) {
    ptx::setmaxnreg_dec<kControlRegs>();
@@ -181,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tma_prefetch_desc(&tmap_k);
       ptx::tma_prefetch_desc(&tmap_v);
       const uint32_t q_bytes = static_cast<uint32_t>(p.tq * p.G) * 128u * Lay::kPanels;
+      const PackedOrder order(p.head[0], p.Hk, gridDim.x);
       uint32_t kv_iter = 0, q_iter = 0;
       int ahead = 0;  // the claim of the CTA's next item
       // Loads started into each stage: the n-th one completes phase n - 1.
@@ -189,13 +209,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int w = k == 0 ? static_cast<int>(blockIdx.x) : ahead;
-        if (!ring_put(ring, static_cast<uint32_t>(k), w, abort_flag, p)) { ok = false; break; }
-        if (w >= order.n) break;
-        ahead = packed_claim(p.head, gridDim.x);  // read when that item starts
+        const PackedEntry x = order.at(p.items, w);
+        if (x.hk >= 0) ahead = packed_claim(p.head, gridDim.x);  // read when that item starts
+        if (!ring.put(static_cast<uint32_t>(k), x, abort_flag, p)) { ok = false; break; }
+        if (x.hk < 0) break;
         FwdItem it;
-        fwd_item(p, order, w, it);
+        fwd_item(p, x, it);
         if (!wait1(bar(kQEmpty), (q_iter & 1u) ^ 1u, abort_flag, p)) { ok = false; break; }
-        *q_item = w;  // the MMA warp reads it with this phase of kQFull
+        *q_item = k;  // the MMA warp reads it with this phase of kQFull
         const int tiles = it.tokens[1] > 0 ? 2 : 1;
         ptx::mbar_arrive_expect_tx(bar(kQFull), tiles * q_bytes);
         for (int t = 0; t < tiles; ++t)
@@ -235,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // No more items: tell the MMA warp through the next phase of kQFull.
       if (ok && wait1(bar(kQEmpty), (q_iter & 1u) ^ 1u, abort_flag, p)) {
-        *q_item = INT_MAX;
+        *q_item = -1;
         ptx::mbar_arrive(bar(kQFull));
         ++q_iter;
       }
@@ -292,10 +313,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (;;) {
       if (!wait_warp(bar(kQFull), q_iter & 1u, abort_flag, p)) { ok = false; break; }
       ++q_iter;
-      const int w = *q_item;
-      if (w >= order.n) break;
+      const int k = *q_item;
+      if (k < 0) break;
       FwdItem it;
-      fwd_item(p, order, w, it);
+      fwd_item(p, ring.read(static_cast<uint32_t>(k)), it);
       ptx::tc_fence_after();
       bool pend0 = false, pend1 = false;    // an S issued whose PV is still owed
       bool first0 = true, first1 = true;    // next PV overwrites O
@@ -395,11 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s_cnt = 0, o_cnt = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      const int w = ring_get(ring, static_cast<uint32_t>(k), abort_flag, p);
-      if (w < 0) { ok = false; break; }
-      if (w >= order.n) break;
+      PackedEntry entry;
+      if (!ring.get(static_cast<uint32_t>(k), entry, abort_flag, p)) { ok = false; break; }
+      if (entry.hk < 0) break;
       FwdItem it;
-      fwd_item(p, order, w, it);
+      fwd_item(p, entry, it);
       // this warpgroup's tile (selects keep the item in registers)
       const int tokens = t ? it.tokens[1] : it.tokens[0];
       const int last = t ? it.last[1] : it.last[0];
@@ -420,8 +441,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         float lsum, mx;
         float alpha = 1.f;
         bool rescale_o = false;
-        load_scores(tS, 0, c_hi, sv);
-        if (!__any_sync(0xffffffffu, m_used == -INFINITY)) {
+        load_seen(tS, c_hi, sv);
+        if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
+          // The first tile: its row max is the reference.  (The rest is the code of every tile,
+          // so that a short prompt waits for little code to be fetched.)
+          const float m_tile = row_max(sv) * sc;
+          if (m_used == -INFINITY) m_used = m_tile;
+        }
+        {
           // P in two halves of 64 keys against the current reference, each signalled once
           // stored; checked first against the guard (see attn_sm103.cu).
           const float lsum1 = exp_half(sv, 0, sc, m_used, pk);
@@ -451,17 +478,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             m_used = m_tile;
           }
           exponentials<false, false>(sv, sc, m_used, pk, lsum, mx);
-        } else {
-          // Some row of this warp has no reference yet: row max first.
-          mx = row_max(sv);
-          const float m_tile = mx * sc;
-          if (m_tile > m_used + kRescaleLog2) {
-            rescale_o = (m_used != -INFINITY);
-            alpha = rescale_o ? ptx::ex2(m_used - m_tile) : 0.f;
-            l_run *= alpha;
-            m_used = m_tile;
-          }
-          exponentials<false, false>(sv, sc, (m_used == -INFINITY) ? 0.f : m_used, pk, lsum, mx);
         }
         l_run += lsum;
         ptx::tmem_st32(tS, pk[0]);
@@ -494,28 +510,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv_l = 1.f / l_run;
       const size_t row = static_cast<size_t>(it.row0) + token;
       const int h = it.hk * p.G + row_head;
-      uint4* dst = reinterpret_cast<uint4*>(p.out + (row * p.Hq + h) * D);
+      __nv_bfloat16* const dst = row_valid ? p.out + (row * p.Hq + h) * D : nullptr;
+      const uint32_t rows = sbase + Lay::kStageOff + warp * kRowStage;
+#pragma unroll 1
+      for (int half = 0; half < D / 64; ++half) {  // 64 columns, 128 bytes of a row
 #pragma unroll
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t ov[32];
-        ptx::tmem_ld32(tO + ch * 32, ov);
-        ptx::tmem_wait_ld();
-        ptx::reg_fence(ov);
-        if (row_valid) {
+        for (int ch = 0; ch < 2; ++ch) {
+          uint32_t ov[32];
+          ptx::tmem_ld32(tO + half * 64 + ch * 32, ov);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence(ov);
+          uint32_t b[16];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint4 v4;
-            v4.x = ptx::pack_bf16(__uint_as_float(ov[8 * x + 0]) * inv_l,
-                                  __uint_as_float(ov[8 * x + 1]) * inv_l);
-            v4.y = ptx::pack_bf16(__uint_as_float(ov[8 * x + 2]) * inv_l,
-                                  __uint_as_float(ov[8 * x + 3]) * inv_l);
-            v4.z = ptx::pack_bf16(__uint_as_float(ov[8 * x + 4]) * inv_l,
-                                  __uint_as_float(ov[8 * x + 5]) * inv_l);
-            v4.w = ptx::pack_bf16(__uint_as_float(ov[8 * x + 6]) * inv_l,
-                                  __uint_as_float(ov[8 * x + 7]) * inv_l);
-            dst[ch * 4 + x] = v4;
-          }
+          for (int x = 0; x < 16; ++x)
+            b[x] = ptx::pack_bf16(__uint_as_float(ov[2 * x]) * inv_l,
+                                  __uint_as_float(ov[2 * x + 1]) * inv_l);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            stage_chunk(rows, lane, ch * 4 + x, b[4 * x], b[4 * x + 1], b[4 * x + 2], b[4 * x + 3]);
         }
+        write_rows(rows, dst ? dst + half * 64 : nullptr, lane);
       }
       if (row_valid) p.lse[static_cast<size_t>(h) * p.T + row] = (m_used + log2f(l_run)) * kLn2;
     }

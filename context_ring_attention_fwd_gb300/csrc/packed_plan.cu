@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   int* const buckets = p.n_buckets <= kSmall ? near_buckets : l.buckets;
   for (int i = threadIdx.x; i < p.n_buckets; i += kPlanThreads) buckets[i] = 0;
   int items = 0;
+  long long streamed = 0;  // tiles that the key tiles of a key head stream, or a little more
   bool bad = false;
   for (int base = 0; base < p.n; base += kPlanThreads) {
     const int i = base + threadIdx.x;
@@ -118,6 +119,14 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
         bad = true;
       else
         tiles = (z - a + l.tokens - 1) / l.tokens;
+      if (l.slots > 0 && tiles > 0) {
+        const long long queries = (z - a - 1) / p.tq + 1;
+        // the k-th tile's first query tile is k kTileRows / tq, rounded down
+        streamed += tiles * queries;
+        if (p.causal)
+          streamed -= max(0LL, static_cast<long long>(tiles) * (tiles - 1) / 2 * kTileRows / p.tq -
+                                   tiles);
+      }
     }
     int total;
     const int before = block_scan(tiles, warp_sum, total);
@@ -157,24 +166,13 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     return (streamed_tiles(p, it) - 1) / chunk + 1;
   };
   if (l.slots > 0) {
-    long long all = 0;
-    for (int x = threadIdx.x; x < items; x += kPlanThreads) {
-      int b;
-      all += streamed_tiles(p, item(x, b));
-    }
-    all = block_sum(all, wide_sum);
+    // A tile of n > chunk streamed tiles is cut into at most 2 n / chunk parts, so with a chunk of
+    // 2 / slots of all streamed tiles at least there are no more parts than slots.
+    const long long all = block_sum(streamed, wide_sum);
     const long long share = static_cast<long long>(kShare * static_cast<float>(all) * p.Hk / p.grid);
-    chunk = static_cast<int>(min(max(share, static_cast<long long>(kLeastPart)), 1LL << 30));
-    for (;;) {  // as many parts as there are slots
-      int parts = 0;
-      for (int x = threadIdx.x; x < items; x += kPlanThreads) {
-        int b;
-        const int n = parts_of(item(x, b));
-        parts += n > 1 ? n : 0;
-      }
-      if (block_sum(static_cast<long long>(parts), wide_sum) <= l.slots) break;
-      chunk *= 2;
-    }
+    const long long least = (2 * all + l.slots - 1) / l.slots;
+    chunk = static_cast<int>(min(max(max(share, least), static_cast<long long>(kLeastPart)),
+                                 1LL << 30));
     for (int i = threadIdx.x; i < l.slots * p.Hk; i += kPlanThreads) l.done[i] = 0;
     if (threadIdx.x == 0) l.head[2] = chunk;
   }

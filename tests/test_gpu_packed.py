@@ -285,12 +285,14 @@ def test_scores_that_grow_along_the_keys():
 
 
 def test_forward_equals_the_ring_attentions():
-    """Equal heads and documents: the same rows to the same tolerance, bit for bit where the
-    tiles are the same (one sequence)."""
+    """Equal heads and one sequence: P of the same scores against the same references.  The rows'
+    sums of up to 512 of them are added in another order, which makes 2 * 512 * 2^-24 of each at
+    most: lse differs by that, out by that and so by one step of bf16, 2^-7 of itself."""
     p = Prompts([512], 4, 4, 128, seed=5, pad=0, fused=False)
     out, lse = p.forward()
     want, wantl = pkg.ring_attn_fwd(p.q[None], p.k[None], p.v[None], 1, True)
-    assert torch.equal(out, want[0]) and torch.equal(lse, wantl[0])
+    assert (lse - wantl[0]).abs().max() <= 2.0 ** -14
+    assert ((out.float() - want[0].float()).abs() <= 2.0 ** -7 * want[0].float().abs()).all()
 
 
 def test_many_sequences():
