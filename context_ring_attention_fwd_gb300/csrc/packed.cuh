@@ -33,6 +33,7 @@ namespace cpring {
 
 constexpr int kCostUnit = 128;  // tokens that an item's cost is counted in
 constexpr int kLeastPart = 4;   // streamed tiles of a part of a key tile
+constexpr int kLeastCut = 8;    // key tiles with up to this many stay whole
 constexpr int kMaxParts = 512;  // parts of a call over all key heads (the sums' space)
 
 // A list in the caller's workspace.  The attention's kernels, which may start before the plan

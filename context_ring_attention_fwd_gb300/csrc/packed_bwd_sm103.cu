@@ -176,6 +176,45 @@ __device__ __forceinline__ float4 load_cg(const float4* at) {
   return f;
 }
 
+// The 32 columns at `at` of `parts` parts, `step` apart, added in their order.  Bound by latency:
+// the loads of kAtOnce parts are under way at a time.
+__device__ __forceinline__ void sum_parts(uint32_t (&sum)[32], const float4* at, int parts,
+                                          size_t step) {
+  constexpr int kAtOnce = 6;
+#pragma unroll
+  for (int c = 0; c < 8; c += 4) {
+    float4 s[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) s[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int j = 0; j < parts; j += kAtOnce) {
+      float4 f[kAtOnce][4];
+#pragma unroll
+      for (int y = 0; y < kAtOnce; ++y)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          f[y][x] = j + y < parts ? load_cg(at + (j + y) * step + (c + x) * kT)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < kAtOnce; ++y)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s[x].x += f[y][x].x;
+          s[x].y += f[y][x].y;
+          s[x].z += f[y][x].z;
+          s[x].w += f[y][x].w;
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      sum[4 * (c + x)] = __float_as_uint(s[x].x);
+      sum[4 * (c + x) + 1] = __float_as_uint(s[x].y);
+      sum[4 * (c + x) + 2] = __float_as_uint(s[x].z);
+      sum[4 * (c + x) + 3] = __float_as_uint(s[x].w);
+    }
+  }
+}
+
 template <int D, bool kDKDV>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_f0,
@@ -756,22 +795,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c0 = wg * (D / 2) + ch * 32;
           uint32_t ov[32];
           if (kDKDV && in_parts) {
-            float sum[32];
-#pragma unroll
-            for (int x = 0; x < 32; ++x) sum[x] = 0.f;
-            const float4* at = first_part + (a * (D / 4) + c0 / 4) * kT + row_in_tile;
-            for (int j = 0; j < it.parts; ++j, at += static_cast<size_t>(p.Hk) * 2 * (D / 4) * kT) {
-#pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const float4 f = load_cg(at + x * kT);
-                sum[4 * x] += f.x;
-                sum[4 * x + 1] += f.y;
-                sum[4 * x + 2] += f.z;
-                sum[4 * x + 3] += f.w;
-              }
-            }
-#pragma unroll
-            for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(sum[x]);
+            sum_parts(ov, first_part + (a * (D / 4) + c0 / 4) * kT + row_in_tile, it.parts,
+                      static_cast<size_t>(p.Hk) * 2 * (D / 4) * kT);
           } else {
             ptx::tmem_ld32(tacc + c0, ov);
             ptx::tmem_wait_ld();

@@ -442,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         bool rescale_o = false;
         load_seen(tS, c_hi, sv);
-        if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
-          // The first tile: its row max is the reference.  (The rest is the code of every tile,
+        if (f == 0) {
+          // The first tile, of which every row sees a key: its row max is the reference.  (The rest is the code of every tile,
           // so that a short prompt waits for little code to be fetched.)
           const float m_tile = row_max(sv) * sc;
           if (m_used == -INFINITY) m_used = m_tile;

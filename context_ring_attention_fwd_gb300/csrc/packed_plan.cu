@@ -56,7 +56,6 @@ __device__ __forceinline__ long long block_sum(long long x, long long* warp_sum)
   return x;
 }
 
-constexpr float kShare = 0.6f;
 
 // Packed query tiles that see a key of an item's tile, and the bucket of part j of `chunk` of them.
 __device__ __forceinline__ int first_streamed(const PackedPlan& p, const int4& it) {
@@ -157,19 +156,24 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     bucket = p.n_buckets - 1 - (cost + kCostUnit - 1) / kCostUnit;
     return make_int4(row, len, tile, 0);
   };
-  // Tiles of keys are cut where the largest is more than its share of a CTA's work: into parts of
-  // kShare of that share, so that a call of few tiles fills the GPU and ends at one time.  (A
-  // part costs its start, its sums' way through memory and their addition; measured in
-  // packed_bwd_sm103.cu.)
+  // Tiles of keys that stream more than a CTA's share of the work are cut, so that a call of few
+  // tiles fills the GPU and ends at one time.  A part costs about 5 streamed tiles besides its own
+  // (its start, its sums' way through memory, their addition), so parts are as many as CTAs
+  // where the share is small, 1.3 of it, and down to 0.6 of it where it is large; they are no
+  // shorter than kLeastPart, and tiles of up to kLeastCut stay whole.  Measured, whole / cut (us a
+  // call): 4096 tokens of 8/1 heads 524 / 137, 8192 of 8/2 557 / 403, 1500 of 2/1 65 / 37; 200 of
+  // 16/4 (7 streamed tiles) 31 / 39, which stays whole.
   int chunk = INT_MAX;
   auto parts_of = [&](const int4& it) {
-    return (streamed_tiles(p, it) - 1) / chunk + 1;
+    const int n = streamed_tiles(p, it);
+    return n <= kLeastCut ? 1 : (n - 1) / chunk + 1;
   };
   if (l.slots > 0) {
     // A tile of n > chunk streamed tiles is cut into at most 2 n / chunk parts, so with a chunk of
     // 2 / slots of all streamed tiles at least there are no more parts than slots.
     const long long all = block_sum(streamed, wide_sum);
-    const long long share = static_cast<long long>(kShare * static_cast<float>(all) * p.Hk / p.grid);
+    const float mean = static_cast<float>(all) * p.Hk / p.grid;
+    const long long share = static_cast<long long>(0.6f * mean + fminf(0.7f * mean, 20.f));
     const long long least = (2 * all + l.slots - 1) / l.slots;
     chunk = static_cast<int>(min(max(max(share, least), static_cast<long long>(kLeastPart)),
                                  1LL << 30));
