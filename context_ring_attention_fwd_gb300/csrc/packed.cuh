@@ -188,6 +188,45 @@ struct PackedOrder {
   }
 };
 
+// Item w of a call of few sequences without a plan: the sequences' tiles in their order, the key
+// heads of a tile side by side (every lane of the warp calls it).  Malformed offsets: no item.
+__device__ __forceinline__ PackedEntry packed_direct(const int32_t* offsets, int n, int T,
+                                                     int tokens, int heads, int w, bool& bad) {
+  const int lane = threadIdx.x & 31, tile = w / heads;
+  PackedEntry found{make_int4(0, 0, 0, 0), -1};
+  bad = false;
+  int before = 0;
+  for (int base = 0; base < n; base += 32) {
+    const int i = base + lane;
+    int a = 0, len = 0;
+    if (i < n) {
+      a = __ldg(offsets + i);
+      const int z = __ldg(offsets + i + 1);
+      bad |= a < 0 || z < a || z > T;
+      len = z - a;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad) return PackedEntry{make_int4(0, 0, 0, 0), -1};
+    const int tiles = (len + tokens - 1) / tokens;
+    int x = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int start = before + x - tiles;
+    const unsigned has = __ballot_sync(0xffffffffu, tile >= start && tile < start + tiles);
+    if (has) {
+      const int from = __ffs(has) - 1;
+      found.e = make_int4(__shfl_sync(0xffffffffu, a, from), __shfl_sync(0xffffffffu, len, from),
+                          tile - __shfl_sync(0xffffffffu, start, from), 0);
+      found.hk = w - tile * heads;
+    }
+    before += __shfl_sync(0xffffffffu, x, 31);
+  }
+  return found;
+}
+
 // A warp's 32 rows of 128 bytes in shared memory, 16-byte chunk c of row r at c ^ (r mod 8), from
 // which rows are written to memory by whole lines: a thread that stores its own row writes half
 // sectors of 32 lines at a time.

@@ -18,7 +18,8 @@
 namespace cpring {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;  // or, where one pass of so few is enough:
+constexpr int kFewThreads = 256;
 constexpr int kWarps = kPlanThreads / 32;
 constexpr int kSmall = 2048;  // sums and buckets up to this many stay in shared memory
 
@@ -34,7 +35,7 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sum, int& total) {
   __syncthreads();  // an earlier call's sums are read
   if (lane == 31) warp_sum[warp] = y;
   __syncthreads();
-  int s = warp_sum[lane];
+  int s = lane < blockDim.x / 32 ? warp_sum[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int z = __shfl_up_sync(0xffffffffu, s, o);
@@ -45,17 +46,15 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sum, int& total) {
   return y - x + (warp > 0 ? before : 0);
 }
 
-__device__ __forceinline__ long long block_sum(long long x, long long* warp_sum) {
+__device__ __forceinline__ float block_sum(float x, float* warp_sum) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  __syncthreads();  // an earlier call's sums are read
   if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = x;
   __syncthreads();
-  x = 0;
-  for (int w = 0; w < kWarps; ++w) x += warp_sum[w];
+  x = 0.f;
+  for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) x += warp_sum[w];
   return x;
 }
-
 
 // Packed query tiles that see a key of an item's tile, and the bucket of part j of `chunk` of them.
 __device__ __forceinline__ int first_streamed(const PackedPlan& p, const int4& it) {
@@ -71,12 +70,12 @@ __device__ __forceinline__ int part_bucket(const PackedPlan& p, const int4& it, 
 
 // D of rows dealt over `blocks` blocks: 8 entries to a lane, d / 8 lanes to a row.
 __device__ __forceinline__ void row_dots(const PackedPlan& p, int block, int blocks) {
-  const int lanes = p.d / 8;
-  const long long vecs = p.rows * lanes, step = static_cast<long long>(blocks) * kPlanThreads;
+  const int shift = p.d == 128 ? 4 : 3, lanes = 1 << shift;
+  const long long vecs = p.rows << shift, step = static_cast<long long>(blocks) * blockDim.x;
   const uint4* const out = static_cast<const uint4*>(p.out);
   const uint4* const dout = static_cast<const uint4*>(p.dout);
   const long long end = (vecs + 31) / 32 * 32;  // whole warps
-  for (long long x = static_cast<long long>(block) * kPlanThreads + threadIdx.x; x < end;
+  for (long long x = static_cast<long long>(block) * blockDim.x + threadIdx.x; x < end;
        x += step) {
     float s = 0.f;
     if (x < vecs) {
@@ -89,13 +88,13 @@ __device__ __forceinline__ void row_dots(const PackedPlan& p, int block, int blo
       }
     }
     for (int o = lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (x < vecs && x % lanes == 0) p.delta[x / lanes] = s;
+    if (x < vecs && (x & (lanes - 1)) == 0) p.delta[x >> shift] = s;
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedPlan p) {
   __shared__ int warp_sum[kWarps], next_slot;
-  __shared__ long long wide_sum[kWarps];
+  __shared__ float streamed_sum[kWarps];
   __shared__ int near_starts[kSmall], near_buckets[kSmall];
   cudaTriggerProgrammaticLaunchCompletion();  // the attention's blocks may line up
   if (blockIdx.x >= p.lists) {
@@ -105,11 +104,11 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   const PackedList l = p.list[blockIdx.x];
   int* const starts = p.n <= kSmall ? near_starts : l.starts;
   int* const buckets = p.n_buckets <= kSmall ? near_buckets : l.buckets;
-  for (int i = threadIdx.x; i < p.n_buckets; i += kPlanThreads) buckets[i] = 0;
+  for (int i = threadIdx.x; i < p.n_buckets; i += blockDim.x) buckets[i] = 0;
   int items = 0;
-  long long streamed = 0;  // tiles that the key tiles of a key head stream, or a little more
+  float streamed = 0.f;  // tiles that the key tiles of a key head stream, or a little more
   bool bad = false;
-  for (int base = 0; base < p.n; base += kPlanThreads) {
+  for (int base = 0; base < p.n; base += blockDim.x) {
     const int i = base + threadIdx.x;
     int tiles = 0;
     if (i < p.n) {
@@ -119,12 +118,10 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
       else
         tiles = (z - a + l.tokens - 1) / l.tokens;
       if (l.slots > 0 && tiles > 0) {
-        const long long queries = (z - a - 1) / p.tq + 1;
+        const float t = tiles, queries = (z - a - 1) / p.tq + 1;
+        streamed += t * queries;
         // the k-th tile's first query tile is k kTileRows / tq, rounded down
-        streamed += tiles * queries;
-        if (p.causal)
-          streamed -= max(0LL, static_cast<long long>(tiles) * (tiles - 1) / 2 * kTileRows / p.tq -
-                                   tiles);
+        if (p.causal) streamed -= fmaxf(0.f, t * (t - 1.f) * (0.5f * kTileRows) / p.tq - t);
       }
     }
     int total;
@@ -171,16 +168,14 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   if (l.slots > 0) {
     // A tile of n > chunk streamed tiles is cut into at most 2 n / chunk parts, so with a chunk of
     // 2 / slots of all streamed tiles at least there are no more parts than slots.
-    const long long all = block_sum(streamed, wide_sum);
-    const float mean = static_cast<float>(all) * p.Hk / p.grid;
-    const long long share = static_cast<long long>(0.6f * mean + fminf(0.7f * mean, 20.f));
-    const long long least = (2 * all + l.slots - 1) / l.slots;
-    chunk = static_cast<int>(min(max(max(share, least), static_cast<long long>(kLeastPart)),
-                                 1LL << 30));
-    for (int i = threadIdx.x; i < l.slots * p.Hk; i += kPlanThreads) l.done[i] = 0;
+    const float all = 1.001f * block_sum(streamed, streamed_sum);  // (whatever was rounded)
+    const float mean = all * p.Hk / p.grid;
+    const float share = 0.6f * mean + fminf(0.7f * mean, 20.f);
+    chunk = max(kLeastPart, static_cast<int>(fminf(fmaxf(share, 2.f * all / l.slots) + 1.f, 1e9f)));
+    for (int i = threadIdx.x; i < l.slots * p.Hk; i += blockDim.x) l.done[i] = 0;
     if (threadIdx.x == 0) l.head[2] = chunk;
   }
-  for (int x = threadIdx.x; x < items; x += kPlanThreads) {
+  for (int x = threadIdx.x; x < items; x += blockDim.x) {
     int b;
     const int4 it = item(x, b);
     const int n = l.slots > 0 ? parts_of(it) : 1;
@@ -192,7 +187,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   }
   __syncthreads();
   int placed = 0;
-  for (int base = 0; base < p.n_buckets; base += kPlanThreads) {
+  for (int base = 0; base < p.n_buckets; base += blockDim.x) {
     const int i = base + threadIdx.x;
     const int x = i < p.n_buckets ? buckets[i] : 0;
     int total;
@@ -206,7 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     next_slot = 0;
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < items; x += kPlanThreads) {
+  for (int x = threadIdx.x; x < items; x += blockDim.x) {
     int b;
     int4 it = item(x, b);
     const int n = l.slots > 0 ? parts_of(it) : 1;
@@ -226,11 +221,14 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
 
 cudaError_t launch_packed_plan(const PackedPlan& p, cudaStream_t stream) {
   unsigned blocks = p.lists;
+  const bool few = p.n <= kFewThreads && p.T / p.list[0].tokens <= kFewThreads;
+  const int threads = few ? kFewThreads : kPlanThreads;
   if (p.delta) {
-    const long long want = (p.rows * (p.d / 8) + kPlanThreads - 1) / kPlanThreads;
-    blocks += static_cast<unsigned>(std::min<long long>(want, 2LL * sm_count()));
+    const long long want = (p.rows * (p.d / 8) + threads - 1) / threads;
+    const long long most = (few ? 6LL : 2LL) * sm_count();
+    blocks += static_cast<unsigned>(std::min<long long>(want, most));
   }
-  packed_plan_kernel<<<blocks, kPlanThreads, 0, stream>>>(p);
+  packed_plan_kernel<<<blocks, threads, 0, stream>>>(p);
   count_launch(2);
   return cudaGetLastError();
 }

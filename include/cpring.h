@@ -660,7 +660,8 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
  *  workspace  device, >= cp_packed_attn_fwd_workspace_bytes(...) bytes, 256-byte aligned,
  *             caller-owned, contents undefined afterwards (calls that can overlap, two
  *             captured graphs' among them, need one each); too small: CP_ERR_BUFFER.
- * Two launches; nothing is allocated, and the lengths are read on the device, so a
+ * One launch, or two (a plan of the work first, where there are more tiles than
+ * multiprocessors); nothing is allocated, and the lengths are read on the device, so a
  * captured call follows them when it is replayed.
  */
 int64_t cp_packed_attn_fwd_workspace_bytes(int T, int n_seqs, int Hq, int Hk, int d);
