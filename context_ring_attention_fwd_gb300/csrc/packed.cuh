@@ -32,26 +32,28 @@
 namespace cpring {
 
 constexpr int kCostUnit = 128;  // tokens that an item's cost is counted in
-constexpr int kLeastPart = 4;   // streamed tiles of a part of a key tile
-constexpr int kLeastCut = 8;    // key tiles with up to this many stay whole
-constexpr int kMaxParts = 512;  // parts of a call over all key heads (the sums' space)
+constexpr int kLeastPart = 4;   // streamed tiles of a part of an item
+constexpr int kLeastCut = 8;    // items with up to this many stay whole
+constexpr int kMaxParts = 512;  // parts of a call over all key heads (the sums' space): the
+constexpr int kMaxFwdParts = 320;  // backward's, the forward's
 
 // A list in the caller's workspace.  The attention's kernels, which may start before the plan
 // is done and wait for it, read it (and D) with plain loads: a read-only load (__ldg) promises
 // that nothing writes during the kernel, and the compiler may move it before the wait.
 struct PackedList {
   int* head;        // [0] items of a key head (0 where the offsets are malformed), [1] next claim,
-                    // [2] streamed tiles of a part (kSplit)
+                    // [2] streamed tiles of a part
   int4* items;      // {first row of the sequence, its length, the tile's index, part}
   int* starts;      // [n] items before each sequence (scratch)
   int* buckets;     // [n_buckets] (scratch)
   int tokens;       // of a tile
   int of_keys;      // tiles of keys: their cost is the queries that see them
-  // Tiles of keys are cut along their queries (packed_plan.cu) into at most this many parts (of a
-  // key head), each with a slot of fp32 sums; part = 1 + slot + (index << 16).  The last
-  // of a tile's parts to end, by `done`, adds them up.
+  // Items are cut along the tiles that they stream (packed_plan.cu) into at most this many parts
+  // (of a key head; 0: they are not), each with a slot of fp32 sums; part = 1 + slot + (index <<
+  // 16).  The last of an item's parts to end, by `done`, joins them.
   int slots;
-  int* done;        // [slots of a key head][Hk]: parts that ended, by the first part's slot
+  int* done;        // counters of parts that ended, cleared by the plan
+  int n_done;
 };
 
 struct PackedPlan {
@@ -250,6 +252,16 @@ __device__ __forceinline__ void write_rows(uint32_t base, __nv_bfloat16* to, int
     if (at != 0) reinterpret_cast<uint4*>(at)[chunk] = u;
   }
   __syncwarp();
+}
+
+// What another block wrote during this kernel (past L1).
+__device__ __forceinline__ float4 load_cg(const float4* at) {
+  float4 f;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+               : "l"(at)
+               : "memory");
+  return f;
 }
 
 // Zeroes the bytes [from, to) of shared memory (multiples of 16) with the lanes of a warp.

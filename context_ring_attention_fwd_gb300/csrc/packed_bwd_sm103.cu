@@ -166,16 +166,6 @@ __device__ __forceinline__ void keep_pairs(uint32_t (&pk)[16], uint32_t columns)
   }
 }
 
-// What another block wrote during this kernel (past L1).
-__device__ __forceinline__ float4 load_cg(const float4* at) {
-  float4 f;
-  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-               : "l"(at)
-               : "memory");
-  return f;
-}
-
 // The 32 columns at `at` of `parts` parts, `step` apart, added in their order.  Bound by latency:
 // the loads of kAtOnce parts are under way at a time.
 __device__ __forceinline__ void sum_parts(uint32_t (&sum)[32], const float4* at, int parts,
@@ -310,7 +300,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok; ++k) {
         const int w = k == 0 ? static_cast<int>(blockIdx.x) : ahead;
         const PackedEntry entry = order.at(p.items, w);
-        if (entry.hk >= 0) ahead = packed_claim(p.head, gridDim.x);  // read when that item starts
         if (!ring.put(static_cast<uint32_t>(k), entry, abort_flag, p)) { ok = false; break; }
         if (entry.hk < 0) break;
         BItem it;
@@ -350,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++armed1[s1];
           ++x_iter;
         }
+        ahead = packed_claim(p.head, gridDim.x);  // (not before: see packed_fwd_sm103.cu)
       }
       // No more items: tell the MMA warp through the next phase of kFixFull.
       if (ok && wait1(bar(kFixEmpty), (fix_iter & 1u) ^ 1u, abort_flag, p)) {
@@ -953,6 +943,7 @@ cp_status cp_packed_attn_bwd(const void* q, const int64_t* q_strides, const void
   PackedPlan plan{};
   plan.list[0] = packed_list(ws + sp.keys, T, n_seqs, kT, true, sp.slots);
   plan.list[0].done = reinterpret_cast<int*>(ws + sp.done);
+  plan.list[0].n_done = sp.slots * Hk;
   plan.tq = tq; plan.Hk = Hk; plan.grid = sm_count();
   plan.list[1] = packed_list(ws + sp.queries, T, n_seqs, tq, false);
   plan.lists = 2;

@@ -13,6 +13,10 @@
 // padding), and 0 times infinity is NaN, so the PV product of a ragged tile ends at the next
 // multiple of 16 keys, and the up to 15 rows of V beyond the last key are zeroed in
 // shared memory first.  K needs none: its rows are columns of S, which the mask replaces.
+//
+// Items that see many keys in a call of few are cut along them (packed_plan.cu): a part leaves its
+// (O, m, l) in a slot, and the last to end of a query tile's parts joins them by the online
+// merge of cp_lse_merge, in the parts' order.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -77,10 +81,13 @@ enum Bar : int {
   kPReadyB = 14,  // + tile: the last 64 keys' P of tile t stored (and O rescaled)
   kOBar = 16,     // + tile: every PV of tile t in the item done (once per item)
   kDrain = 18,
-  kNumBars = 19
+  kJoin = 19,     // + tile: its threads have stored a part's state; then: know its rank
+  kNumBars = 21
 };
 constexpr int kTmemSlot = kNumBars * 8;
 constexpr int kAbortSlot = kNumBars * 8 + 4;
+constexpr int kRankSlot = kNumBars * 8 + 8;  // two
+static_assert(kRankSlot + 8 <= 256, "the barriers' shared-memory block");
 
 struct FwdParams {
   int* head;           // the plan's list
@@ -93,17 +100,22 @@ struct FwdParams {
   float scale_log2;    // log2(e) / sqrt(d)
   __nv_bfloat16* out;  // [T, Hq, d]
   float* lse;          // [Hq, T]
+  float4* parts;       // [slot][Hk][query tile]: O [d / 4][128] float4, then (m, l) [128]
+  int* done;           // [slot][Hk][query tile]
   int* err;
   unsigned long long timeout_ns;
   int fault_drop_k;    // test hook: CTA 0 never loads its first K tile
 };
 
-// An item: two packed tiles of one sequence for one key head, and the last key tile that each
-// sees (-1: the tile is empty).
+// An item: two packed tiles of one sequence for one key head, the first key tile, and the last
+// that each tile sees (before the first: none), of an item in parts the part's own.
 struct FwdItem {
   int row0, len, hk;
   int token[kQTiles], tokens[kQTiles], last[kQTiles];
+  int first;
+  int slot, part, parts[kQTiles];  // the part's slot, its index, and the parts of each tile
 };
+template <bool kParts>
 __device__ __forceinline__ void fwd_item(const FwdParams& p, const PackedEntry& x, FwdItem& it) {
   const int4 e = x.e;
   it.hk = x.hk;
@@ -115,7 +127,76 @@ __device__ __forceinline__ void fwd_item(const FwdParams& p, const PackedEntry& 
     it.tokens[t] = max(0, min(p.tq, it.len - it.token[t]));
     const int seen = p.causal ? it.token[t] + it.tokens[t] : it.len;
     it.last[t] = it.tokens[t] > 0 ? (seen - 1) / kBN : -1;
+    it.parts[t] = 1;
   }
+  it.first = it.slot = it.part = 0;
+  if (kParts && e.w != 0) {
+    const int chunk = p.head[2];
+    it.slot = (e.w & 0xffff) - 1;
+    it.part = e.w >> 16;
+    it.first = it.part * chunk;
+#pragma unroll
+    for (int t = 0; t < kQTiles; ++t) {
+      it.parts[t] = it.last[t] / chunk + 1;
+      it.last[t] = min(it.last[t], it.first + chunk - 1);
+    }
+  }
+}
+
+// float4 of a query tile's state in a slot.
+template <int D>
+constexpr int kPartSize = (D / 4) * kBM + kBM / 2;
+
+// (m, l) of this thread's row in part j of the parts from `first` on (its row's first float4).
+template <int D>
+__device__ __forceinline__ float2 part_ml(const FwdParams& p, const float4* first, int j,
+                                          int row_in_tile) {
+  const float4* const base = first - row_in_tile +
+                             static_cast<size_t>(j) * p.Hk * kQTiles * kPartSize<D> +
+                             (D / 4) * kBM;
+  float2 ml;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];"
+               : "=f"(ml.x), "=f"(ml.y)
+               : "l"(reinterpret_cast<const float2*>(base) + row_in_tile)
+               : "memory");
+  return ml;
+}
+// Columns [32 ch, 32 ch + 32) of the row: the parts' O, each against its own reference, to the
+// reference m.  Bound by latency: two parts' loads are under way at a time.
+template <int D>
+__device__ __forceinline__ void join_parts(const FwdParams& p, const float4* first, int ch,
+                                           int parts, float m, int row_in_tile,
+                                           uint32_t (&sum)[32]) {
+  float s[32];
+#pragma unroll
+  for (int x = 0; x < 32; ++x) s[x] = 0.f;
+  const size_t step = static_cast<size_t>(p.Hk) * kQTiles * kPartSize<D>;
+#pragma unroll 1
+  for (int j = 0; j < parts; j += 2) {
+    float4 f[2][8];
+    float w[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const bool there = j + y < parts;
+      const float2 ml = there ? part_ml<D>(p, first, j + y, row_in_tile) : make_float2(0.f, 0.f);
+      w[y] = ml.y == 0.f ? 0.f : ptx::ex2(ml.x - m);
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        f[y][x] = there ? load_cg(first + (j + y) * step + (ch * 8 + x) * kBM)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        s[4 * x] = fmaf(f[y][x].x, w[y], s[4 * x]);
+        s[4 * x + 1] = fmaf(f[y][x].y, w[y], s[4 * x + 1]);
+        s[4 * x + 2] = fmaf(f[y][x].z, w[y], s[4 * x + 2]);
+        s[4 * x + 3] = fmaf(f[y][x].w, w[y], s[4 * x + 3]);
+      }
+  }
+#pragma unroll
+  for (int x = 0; x < 32; ++x) sum[x] = __float_as_uint(s[x]);
 }
 
 // This thread's 128 scores of the S tile, with columns behind c_hi set to -inf (chunk by
@@ -138,7 +219,8 @@ __device__ __forceinline__ void load_seen(uint32_t tS, int c_hi, uint32_t (&sv)[
   }
 }
 
-template <int D>
+// kParts: for calls whose items may be in parts.
+template <int D, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
                       const __grid_constant__ CUtensorMap tmap_k,
@@ -156,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PackedRing ring{
       sbase + Lay::kRingOff,
       reinterpret_cast<volatile int(*)[8]>(smem + Lay::kRingOff + 2 * kRing * 8)};
+  volatile int* rank = reinterpret_cast<volatile int*>(smem + Lay::kBarOff + kRankSlot);
   // the ring's index of the item whose Q the producer is loading, for the MMA warp
   volatile int* q_item =
       reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 2 * kRing * 8 + kRing * 32);
@@ -177,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(kPReady + t), 128);
       ptx::mbar_init(bar(kPReadyB + t), 128);
       ptx::mbar_init(bar(kOBar + t), 1);
+      ptx::mbar_init(bar(kJoin + t), 128);
     }
     ptx::mbar_init(bar(kDrain), 1);
     ring.init(kSoftmaxWarps);
@@ -211,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_bytes = static_cast<uint32_t>(p.tq * p.G) * 128u * Lay::kPanels;
       const PackedOrder order(p.offsets ? 0 : p.head[0], p.Hk, gridDim.x);
       uint32_t kv_iter = 0, q_iter = 0;
-      int ahead = 0;  // the claim of the CTA's next item
+      int ahead = INT_MAX;  // the claim of the CTA's next item
       // Loads started into each stage: the n-th one completes phase n - 1.
       uint32_t k_armed0 = 0, k_armed1 = 0, v_armed0 = 0, v_armed1 = 0;
       bool dropped = false;
@@ -219,12 +303,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok; ++k) {
         const int w = k == 0 ? static_cast<int>(blockIdx.x) : ahead;
         const PackedEntry x = p.offsets && k == 0 ? only : order.at(p.items, w);
-        if (x.hk >= 0 && !p.offsets)
-          ahead = packed_claim(p.head, gridDim.x);  // read when that item starts
         if (!ring.put(static_cast<uint32_t>(k), x, abort_flag, p)) { ok = false; break; }
         if (x.hk < 0) break;
         FwdItem it;
-        fwd_item(p, x, it);
+        fwd_item<kParts>(p, x, it);
         if (!wait1(bar(kQEmpty), (q_iter & 1u) ^ 1u, abort_flag, p)) { ok = false; break; }
         *q_item = k;  // the MMA warp reads it with this phase of kQFull
         const int tiles = it.tokens[1] > 0 ? 2 : 1;
@@ -237,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              it.row0 + (t ? it.token[1] : it.token[0]));
         ++q_iter;
         const int last = max(it.last[0], it.last[1]);
-        for (int f = 0; f <= last; ++f) {
+        for (int f = it.first; f <= last; ++f) {
           const uint32_t st = kv_iter % kStages;
           const uint32_t ph = (kv_iter / kStages) & 1u;
           const int row = it.row0 + f * kBN;
@@ -263,6 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (st == 0) ++v_armed0; else ++v_armed1;
           ++kv_iter;
         }
+        // The next item is claimed once this one's loads are under way, not before: a CTA at its
+        // start would take one that another is free for sooner.
+        if (!p.offsets) ahead = packed_claim(p.head, gridDim.x);
       }
       // No more items: tell the MMA warp through the next phase of kQFull.
       if (ok && wait1(bar(kQEmpty), (q_iter & 1u) ^ 1u, abort_flag, p)) {
@@ -326,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int k = *q_item;
       if (k < 0) break;
       FwdItem it;
-      fwd_item(p, ring.read(static_cast<uint32_t>(k)), it);
+      fwd_item<kParts>(p, ring.read(static_cast<uint32_t>(k)), it);
       ptx::tc_fence_after();
       bool pend0 = false, pend1 = false;    // an S issued whose PV is still owed
       bool first0 = true, first1 = true;    // next PV overwrites O
@@ -361,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = false;
         return true;
       };
-      for (int f = 0; f <= last; ++f) {
+      for (int f = it.first; f <= last; ++f) {
         const uint32_t st = kv_iter % kStages;
         const uint32_t ph = (kv_iter / kStages) & 1u;
         if (pend0) {
@@ -423,25 +508,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem_base + lane_off + static_cast<uint32_t>(t * 128);
     const uint32_t tO = tmem_base + lane_off + 256u + static_cast<uint32_t>(t * D);
     const float sc = p.scale_log2;
-    uint32_t s_cnt = 0, o_cnt = 0;
+    uint32_t s_cnt = 0, o_cnt = 0, join_cnt = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       PackedEntry entry;
       if (!ring.get(static_cast<uint32_t>(k), entry, abort_flag, p)) { ok = false; break; }
       if (entry.hk < 0) break;
       FwdItem it;
-      fwd_item(p, entry, it);
+      fwd_item<kParts>(p, entry, it);
       // this warpgroup's tile (selects keep the item in registers)
       const int tokens = t ? it.tokens[1] : it.tokens[0];
       const int last = t ? it.last[1] : it.last[0];
-      if (tokens == 0) continue;
+      const int parts = t ? it.parts[1] : it.parts[0];
+      if (tokens == 0 || last < it.first) continue;
       const bool row_valid = row_token < tokens;
       const int token = (t ? it.token[1] : it.token[0]) + row_token;
       const int seen = !row_valid ? 0 : p.causal ? token + 1 : it.len;  // keys
       // A row that is not stored has a reference from the start, so that it does not hold
       // its warp to the careful pass; all of its columns are masked.
       float m_used = row_valid ? -INFINITY : 0.f, l_run = 0.f;
-      for (int f = 0; f <= last; ++f) {
+      for (int f = it.first; f <= last; ++f) {
         if (!wait_warp(bar(kSFull + t), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
         ++s_cnt;
         ptx::tc_fence_after();
@@ -452,11 +538,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         bool rescale_o = false;
         load_seen(tS, c_hi, sv);
-        if (f == 0) {
-          // The first tile, of which every row sees a key: its row max is the reference.  (The rest is the code of every tile,
-          // so that a short prompt waits for little code to be fetched.)
+        if (f == it.first) {
+          // Its row max is the reference; a row that sees none of a part's first tile sees
+          // none of the part.  (The rest is the code of every tile, so that a short prompt waits
+          // for little code to be fetched.)
           const float m_tile = row_max(sv) * sc;
-          if (m_used == -INFINITY) m_used = m_tile;
+          if (row_valid) m_used = kParts && m_tile == -INFINITY && it.part > 0 ? 0.f : m_tile;
         }
         {
           // P in two halves of 64 keys against the current reference, each signalled once
@@ -517,6 +604,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_warp(bar(kOBar + t), o_cnt & 1u, abort_flag, p)) { ok = false; break; }
       ++o_cnt;
       ptx::tc_fence_after();
+      const float4* first_part = nullptr;
+      if (kParts && parts > 1) {
+        const size_t at = (static_cast<size_t>(it.slot) * p.Hk + it.hk) * kQTiles + t;
+        float4* const to = p.parts + at * kPartSize<D> + row_in_tile;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t ov[32];
+          ptx::tmem_ld32(tO + ch * 32, ov);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence(ov);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            to[(ch * 8 + x) * kBM] =
+                make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]),
+                            __uint_as_float(ov[4 * x + 2]), __uint_as_float(ov[4 * x + 3]));
+        }
+        reinterpret_cast<float2*>(to - row_in_tile + (D / 4) * kBM)[row_in_tile] =
+            make_float2(m_used, l_run);
+        __threadfence();
+        ptx::mbar_arrive(bar(kJoin + t));
+        if (!wait_warp(bar(kJoin + t), join_cnt & 1u, abort_flag, p)) { ok = false; break; }
+        ++join_cnt;
+        const size_t at0 = (static_cast<size_t>(it.slot - it.part) * p.Hk + it.hk) * kQTiles + t;
+        if (row_in_tile == 0) {
+          rank[t] = atomicAdd(p.done + at0, 1);
+          __threadfence();
+        }
+        ptx::mbar_arrive(bar(kJoin + t));
+        if (!wait_warp(bar(kJoin + t), join_cnt & 1u, abort_flag, p)) { ok = false; break; }
+        ++join_cnt;
+        if (rank[t] != parts - 1) continue;
+        __threadfence();
+        first_part = p.parts + at0 * kPartSize<D> + row_in_tile;
+        // the row's reference and sum over all parts
+        m_used = -INFINITY;
+        l_run = 0.f;
+        for (int j = 0; j < parts; ++j) {
+          const float2 ml = part_ml<D>(p, first_part, j, row_in_tile);
+          if (ml.y == 0.f) continue;  // the part saw nothing of the row
+          const float big = fmaxf(m_used, ml.x);
+          l_run = (m_used == -INFINITY ? 0.f : l_run * ptx::ex2(m_used - big)) +
+                  ml.y * ptx::ex2(ml.x - big);
+          m_used = big;
+        }
+      }
       const float inv_l = 1.f / l_run;
       const size_t row = static_cast<size_t>(it.row0) + token;
       const int h = it.hk * p.G + row_head;
@@ -527,9 +659,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
           uint32_t ov[32];
-          ptx::tmem_ld32(tO + half * 64 + ch * 32, ov);
-          ptx::tmem_wait_ld();
-          ptx::reg_fence(ov);
+          if (kParts && first_part != nullptr) {
+            join_parts<D>(p, first_part, half * 2 + ch, parts, m_used, row_in_tile, ov);
+          } else {
+            ptx::tmem_ld32(tO + half * 64 + ch * 32, ov);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence(ov);
+          }
           uint32_t b[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x)
@@ -555,12 +691,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool kParts>
 cudaError_t launch_packed_fwd(const PackedArgs& a, const FwdParams& p, int grid,
                               cudaStream_t stream) {
   using Lay = Layout<D>;
   static_assert(Lay::kAlloc <= 232448, "shared memory budget");
-  const auto kern = packed_fwd_kernel<D>;
+  const auto kern = packed_fwd_kernel<D, kParts>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), Lay::kAlloc);
   if (e != cudaSuccess) return e;
   CUtensorMap mq, mk, mv;
@@ -581,6 +717,28 @@ cudaError_t launch_packed_fwd(const PackedArgs& a, const FwdParams& p, int grid,
   count_launch(0);
   return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p);
 }
+
+// A call that may have this many items has enough of them, whatever the lengths, and its
+// kernel is the one that knows no parts.
+constexpr int kManyItems = 1024;
+
+// Byte offsets of the workspace's parts: the list, and the states of items in parts.
+struct Space {
+  int slots;  // of a key head
+  long long list, done, parts, total;
+  Space(int T, int n, int Hk, int d, int tokens) {
+    const auto up = [](long long x) { return (x + 255) / 256 * 256; };
+    const long long items = packed_items(T, n, tokens);
+    const long long most = T <= kBN * kLeastCut || items * Hk >= kManyItems
+                               ? 0
+                               : items * (T / kBN / kLeastPart + 1);
+    slots = static_cast<int>(std::min<long long>(most, (kMaxFwdParts + Hk - 1) / Hk));
+    list = 0;
+    done = up(packed_list_bytes(T, n, tokens) + 16LL * slots);
+    parts = done + up(4LL * slots * Hk * kQTiles);
+    total = parts + 16LL * slots * Hk * kQTiles * (d == 128 ? kPartSize<128> : kPartSize<64>);
+  }
+};
 
 }  // namespace
 
@@ -612,7 +770,7 @@ extern "C" {
 
 int64_t cp_packed_attn_fwd_workspace_bytes(int T, int n_seqs, int Hq, int Hk, int d) {
   if (cpring::check_packed(T, n_seqs, Hq, Hk, d, 0) != CP_OK) return -1;
-  return cpring::packed_list_bytes(T, n_seqs, 2 * (cpring::kTileRows / (Hq / Hk)));
+  return cpring::Space(T, n_seqs, Hk, d, cpring::kQTiles * (cpring::kTileRows / (Hq / Hk))).total;
 }
 
 cp_status cp_packed_attn_fwd(const void* q, const int64_t* q_strides, const void* k,
@@ -634,14 +792,19 @@ cp_status cp_packed_attn_fwd(const void* q, const int64_t* q_strides, const void
       !packed_strides(v_strides, Hk, d, a.vs))
     return CP_ERR_ALIGN;
   const int G = Hq / Hk, tq = kTileRows / G, tokens = kQTiles * tq;
-  if (workspace_bytes < packed_list_bytes(T, n_seqs, tokens)) return CP_ERR_BUFFER;
+  const Space sp(T, n_seqs, Hk, d, tokens);
+  if (workspace_bytes < sp.total) return CP_ERR_BUFFER;
   if (device_cc() != 103) return CP_ERR_DEVICE;
-  // A call whose every item, whatever the lengths, has a CTA to itself needs no order of them.
-  // (12 prompts of up to 90 tokens, 32/8 heads: 14.0 us a call with a plan, 11 without.)
+  // A call whose every item, whatever the lengths, has a CTA to itself and stays whole needs no
+  // plan.  (12 prompts of up to 90 tokens, 32/8 heads: 14.0 us a call with one, 10.5 without.)
   const long long most_items = packed_items(T, n_seqs, tokens) * Hk;
-  const bool direct = most_items <= sm_count();
+  const bool direct = most_items <= sm_count() && sp.slots == 0;
+  char* const ws = static_cast<char*>(workspace);
   PackedPlan plan{};
-  plan.list[0] = packed_list(static_cast<char*>(workspace), T, n_seqs, tokens, false);
+  plan.list[0] = packed_list(ws + sp.list, T, n_seqs, tokens, false, sp.slots);
+  plan.list[0].done = reinterpret_cast<int*>(ws + sp.done);
+  plan.list[0].n_done = sp.slots * Hk * kQTiles;
+  plan.tq = tq; plan.Hk = Hk; plan.grid = sm_count();
   plan.lists = 1;
   plan.offsets = seq_offsets;
   plan.n = n_seqs; plan.T = T; plan.causal = causal;
@@ -657,12 +820,18 @@ cp_status cp_packed_attn_fwd(const void* q, const int64_t* q_strides, const void
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
+  p.parts = reinterpret_cast<float4*>(ws + sp.parts);
+  p.done = plan.list[0].done;
   p.err = plan.err;
   p.timeout_ns = test_wait_limit_ns();
   p.fault_drop_k = test_fault_drop();
-  const int grid = static_cast<int>(std::min<long long>(sm_count(), most_items));
-  const cudaError_t e = d == 128 ? launch_packed_fwd<128>(a, p, grid, stream)
-                                 : launch_packed_fwd<64>(a, p, grid, stream);
+  const int grid = static_cast<int>(std::min<long long>(sm_count(), most_items + sp.slots * Hk));
+  auto launch = [&](auto parts) {
+    constexpr bool kParts = decltype(parts)::value;
+    return d == 128 ? launch_packed_fwd<128, kParts>(a, p, grid, stream)
+                    : launch_packed_fwd<64, kParts>(a, p, grid, stream);
+  };
+  const cudaError_t e = sp.slots > 0 ? launch(std::true_type()) : launch(std::false_type());
   return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 

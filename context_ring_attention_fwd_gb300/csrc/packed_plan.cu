@@ -56,16 +56,19 @@ __device__ __forceinline__ float block_sum(float x, float* warp_sum) {
   return x;
 }
 
-// Packed query tiles that see a key of an item's tile, and the bucket of part j of `chunk` of them.
-__device__ __forceinline__ int first_streamed(const PackedPlan& p, const int4& it) {
-  return p.causal ? it.z * kTileRows / p.tq : 0;
+// The tiles that an item streams: key tiles that its queries see, or packed query tiles that
+// see its keys; and the bucket of part j of `chunk` of them.
+__device__ __forceinline__ int streamed_tiles(const PackedPlan& p, const PackedList& l,
+                                              const int4& it) {
+  if (l.of_keys) return (it.y - 1) / p.tq - (p.causal ? it.z * kTileRows / p.tq : 0) + 1;
+  const long long seen = p.causal ? (it.z + 1LL) * l.tokens : it.y;
+  return (static_cast<int>(min(seen, static_cast<long long>(it.y))) - 1) / kTileRows + 1;
 }
-__device__ __forceinline__ int streamed_tiles(const PackedPlan& p, const int4& it) {
-  return (it.y - 1) / p.tq - first_streamed(p, it) + 1;
-}
-__device__ __forceinline__ int part_bucket(const PackedPlan& p, const int4& it, int j, int chunk) {
-  const int tiles = min(chunk, streamed_tiles(p, it) - j * chunk);
-  return max(0, p.n_buckets - 1 - (tiles * p.tq + kCostUnit - 1) / kCostUnit);
+__device__ __forceinline__ int part_bucket(const PackedPlan& p, const PackedList& l,
+                                           const int4& it, int j, int chunk) {
+  const int tiles = min(chunk, streamed_tiles(p, l, it) - j * chunk);
+  const int tokens = tiles * (l.of_keys ? p.tq : kTileRows);
+  return max(0, p.n_buckets - 1 - (tokens + kCostUnit - 1) / kCostUnit);
 }
 
 // D of rows dealt over `blocks` blocks: 8 entries to a lane, d / 8 lanes to a row.
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   int* const buckets = p.n_buckets <= kSmall ? near_buckets : l.buckets;
   for (int i = threadIdx.x; i < p.n_buckets; i += blockDim.x) buckets[i] = 0;
   int items = 0;
-  float streamed = 0.f;  // tiles that the key tiles of a key head stream, or a little more
+  float streamed = 0.f;  // tiles that the items of a key head stream, or a little more
   bool bad = false;
   for (int base = 0; base < p.n; base += blockDim.x) {
     const int i = base + threadIdx.x;
@@ -118,10 +121,15 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
       else
         tiles = (z - a + l.tokens - 1) / l.tokens;
       if (l.slots > 0 && tiles > 0) {
-        const float t = tiles, queries = (z - a - 1) / p.tq + 1;
-        streamed += t * queries;
-        // the k-th tile's first query tile is k kTileRows / tq, rounded down
-        if (p.causal) streamed -= fmaxf(0.f, t * (t - 1.f) * (0.5f * kTileRows) / p.tq - t);
+        const float t = tiles, all = (z - a - 1) / (l.of_keys ? p.tq : kTileRows) + 1;
+        // Causal: the k-th of the key tiles does not stream the first k kTileRows / tq (rounded
+        // down), the k-th of the query tiles streams (k + 1) tokens / kTileRows (rounded up).
+        float some = t * all;
+        if (p.causal && l.of_keys)
+          some -= fmaxf(0.f, t * (t - 1.f) * (0.5f * kTileRows) / p.tq - t);
+        else if (p.causal)
+          some = fminf(some, t * (t + 1.f) * (0.5f / kTileRows) * l.tokens + t);
+        streamed += some;
       }
     }
     int total;
@@ -153,16 +161,16 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     bucket = p.n_buckets - 1 - (cost + kCostUnit - 1) / kCostUnit;
     return make_int4(row, len, tile, 0);
   };
-  // Tiles of keys that stream more than a CTA's share of the work are cut, so that a call of few
-  // tiles fills the GPU and ends at one time.  A part costs about 5 streamed tiles besides its own
-  // (its start, its sums' way through memory, their addition), so parts are as many as CTAs
-  // where the share is small, 1.3 of it, and down to 0.6 of it where it is large; they are no
-  // shorter than kLeastPart, and tiles of up to kLeastCut stay whole.  Measured, whole / cut (us a
-  // call): 4096 tokens of 8/1 heads 524 / 137, 8192 of 8/2 557 / 403, 1500 of 2/1 65 / 37; 200 of
-  // 16/4 (7 streamed tiles) 31 / 39, which stays whole.
+  // Items that stream more than a CTA's share of the work are cut, so that a call of few items
+  // fills the GPU and ends at one time.  A part costs about 5 streamed tiles besides its own (its
+  // start, its sums' way through memory, their addition), so parts are as many as CTAs where
+  // the share is small, 1.3 of it, and down to 0.6 of it where it is large; they are no
+  // shorter than kLeastPart, and items of up to kLeastCut stay whole.  Measured for the backward's
+  // key tiles, whole / cut (us a call): 4096 tokens of 8/1 heads 524 / 137, 8192 of 8/2 557 /
+  // 403, 1500 of 2/1 65 / 37; 200 of 16/4 (7 streamed tiles) 31 / 39, which stays whole.
   int chunk = INT_MAX;
   auto parts_of = [&](const int4& it) {
-    const int n = streamed_tiles(p, it);
+    const int n = streamed_tiles(p, l, it);
     return n <= kLeastCut ? 1 : (n - 1) / chunk + 1;
   };
   if (l.slots > 0) {
@@ -172,7 +180,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     const float mean = all * p.Hk / p.grid;
     const float share = 0.6f * mean + fminf(0.7f * mean, 20.f);
     chunk = max(kLeastPart, static_cast<int>(fminf(fmaxf(share, 2.f * all / l.slots) + 1.f, 1e9f)));
-    for (int i = threadIdx.x; i < l.slots * p.Hk; i += blockDim.x) l.done[i] = 0;
+    for (int i = threadIdx.x; i < l.n_done; i += blockDim.x) l.done[i] = 0;
     if (threadIdx.x == 0) l.head[2] = chunk;
   }
   for (int x = threadIdx.x; x < items; x += blockDim.x) {
@@ -182,7 +190,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     if (n == 1) {
       atomicAdd(buckets + b, 1);
     } else {
-      for (int j = 0; j < n; ++j) atomicAdd(buckets + part_bucket(p, it, j, chunk), 1);
+      for (int j = 0; j < n; ++j) atomicAdd(buckets + part_bucket(p, l, it, j, chunk), 1);
     }
   }
   __syncthreads();
@@ -211,7 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     }
     const int slot = atomicAdd(&next_slot, n);
     for (int j = 0; j < n; ++j) {
-      const int at = atomicAdd(buckets + part_bucket(p, it, j, chunk), 1);
+      const int at = atomicAdd(buckets + part_bucket(p, l, it, j, chunk), 1);
       l.items[at] = make_int4(it.x, it.y, it.z, 1 + slot + j + (j << 16));
     }
   }

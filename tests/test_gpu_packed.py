@@ -367,3 +367,20 @@ def test_gradients_of_key_tiles_in_parts(lens, Hq, Hk, d, causal):
     p.check_gradients(out, lse, grads, causal)
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(grads, p.backward(out, lse, causal)))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,Hq,Hk,d", [
+    ([3000], 2, 1, 128),             # few items of many keys: cut into parts
+    ([2500, 40, 7], 3, 1, 64),       # tiles whose first rows see nothing of a part's keys
+    ([1300, 1700], 8, 1, 128),
+    ([1200] * 4, 2, 2, 64),
+])
+def test_forward_of_items_in_parts(lens, Hq, Hk, d, causal):
+    """The parts are joined in one order, whichever ends last."""
+    p = Prompts(lens, Hq, Hk, d, seed=22, scale=2.0)
+    out, lse = p.forward(causal)
+    p.check(out, lse, causal)
+    for _ in range(3):
+        again, lse2 = p.forward(causal)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
