@@ -295,11 +295,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t x_iter = 0, fix_iter = 0;
       uint32_t armed0[3] = {0u, 0u, 0u}, armed1[2] = {0u, 0u};  // loads started per slot
       int ahead = 0;  // the claim of the CTA's next item
+      // kDQ claims it when this item's loads are under way (see packed_fwd_sm103.cu), kDKDV when
+      // this item starts: its CTAs then end one by one and make room for dQ's, which start with
+      // the most expensive items.  Measured for kDKDV, at the start / late (us a call): 8192
+      // tokens of 8/2 heads 413 / 447, 20000 of 1/1 272 / 295, 5000 + 2500 of 16/2 389 / 426; but
+      // 3000 + 200 + 100 of 32/8 268 / 250, 9000 of 4/4 (d = 64) 225 / 213.
+      constexpr bool early = kDKDV;
       bool dropped = false;
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int w = k == 0 ? static_cast<int>(blockIdx.x) : ahead;
         const PackedEntry entry = order.at(p.items, w);
+        if (early && entry.hk >= 0) ahead = packed_claim(p.head, gridDim.x);
         if (!ring.put(static_cast<uint32_t>(k), entry, abort_flag, p)) { ok = false; break; }
         if (entry.hk < 0) break;
         BItem it;
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++armed1[s1];
           ++x_iter;
         }
-        ahead = packed_claim(p.head, gridDim.x);  // (not before: see packed_fwd_sm103.cu)
+        if (!early) ahead = packed_claim(p.head, gridDim.x);
       }
       // No more items: tell the MMA warp through the next phase of kFixFull.
       if (ok && wait1(bar(kFixEmpty), (fix_iter & 1u) ^ 1u, abort_flag, p)) {
