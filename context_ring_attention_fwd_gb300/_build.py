@@ -26,7 +26,8 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 SOURCES = ["attn_sm103.cu", "attn_f32.cu", "merge.cu", "noalloc.cu", "ring_emulation.cpp",
            "ulysses.cu", "fp8.cu", "attn_bwd_sm103.cu", "norm_rope.cu", "paged_append.cu",
            "paged_decode.cu", "prefix_sm103.cu", "packed_plan.cu", "packed_fwd_sm103.cu",
-           "packed_bwd_sm103.cu", "api.cpp", "scratch.cpp", "host_path.cpp"]
+           "packed_bwd_sm103.cu", "api.cpp", "scratch.cpp", "beside.cpp",
+           "host_path.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -45,7 +45,6 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <mutex>
 
 #include "attn_common.cuh"
 #include "internal.h"
@@ -828,57 +827,22 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// The dQ launch reads nothing that the dK/dV launch writes, so it can run on
-// a second stream of the library's (one per device, created on first use
-// and kept for the process's life): its CTAs then take the SMs that the
-// dK/dV launch's last items leave idle instead of waiting for all of them.
-// The caller's stream waits for it before anything enqueued later.
+// dK/dV on `stream`, dQ beside it: it reads nothing that the dK/dV launch writes, and its CTAs take
+// the SMs that the last dK/dV items leave idle.
 #ifndef CPRING_BWD_OVERLAP
 #define CPRING_BWD_OVERLAP 1
 #endif
-struct BwdSideStream {
-  std::mutex mu;
-  cudaStream_t s = nullptr;
-};
-constexpr int kMaxBwdDevices = 64;
-BwdSideStream g_bwd_side[kMaxBwdDevices];
-
-// dK/dV on `stream`, dQ beside it; both after everything already on `stream`.
 template <int D>
 cudaError_t launch_bwd_pair(const BwdArgs& a, cudaStream_t stream) {
-  cudaStream_t side = CPRING_BWD_OVERLAP ? bwd_side_stream() : nullptr;
-  if (!side) {
-    cudaError_t e = launch_bwd_t<D, true>(a, stream);
+  if (!CPRING_BWD_OVERLAP) {
+    const cudaError_t e = launch_bwd_t<D, true>(a, stream);
     return e == cudaSuccess ? launch_bwd_t<D, false>(a, stream) : e;
   }
-  cudaEvent_t ready = nullptr, dq_done = nullptr;
-  if (cudaEventCreateWithFlags(&ready, cudaEventDisableTiming) != cudaSuccess) return cudaErrorUnknown;
-  if (cudaEventCreateWithFlags(&dq_done, cudaEventDisableTiming) != cudaSuccess) {
-    cudaEventDestroy(ready);
-    return cudaErrorUnknown;
-  }
-  cudaError_t e = cudaEventRecord(ready, stream);
-  if (e == cudaSuccess) e = launch_bwd_t<D, true>(a, stream);
-  if (e == cudaSuccess) e = cudaStreamWaitEvent(side, ready, 0);
-  if (e == cudaSuccess) e = launch_bwd_t<D, false>(a, side);
-  if (e == cudaSuccess) e = cudaEventRecord(dq_done, side);
-  if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, dq_done, 0);
-  // (destroying a recorded event releases it once the work it marks is done)
-  cudaEventDestroy(ready);
-  cudaEventDestroy(dq_done);
-  return e;
+  return launch_beside(stream, [&](cudaStream_t s) { return launch_bwd_t<D, true>(a, s); },
+                       [&](cudaStream_t s) { return launch_bwd_t<D, false>(a, s); });
 }
 
 }  // namespace
-
-cudaStream_t bwd_side_stream() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxBwdDevices) return nullptr;
-  BwdSideStream& b = g_bwd_side[dev];
-  std::lock_guard<std::mutex> lock(b.mu);
-  if (!b.s && cudaStreamCreateWithFlags(&b.s, cudaStreamNonBlocking) != cudaSuccess) b.s = nullptr;
-  return b.s;
-}
 
 cudaError_t launch_attn_bwd(const BwdArgs& a, cudaStream_t stream) {
   {

@@ -145,9 +145,17 @@ cudaError_t launch_schedule_probe(const AttnArgs& a, int32_t* ranges, cudaStream
 // Backward: the row sums D, then the dK/dV kernel and the dQ kernel (bf16,
 // d in {64, 128}).
 cudaError_t launch_attn_bwd(const BwdArgs& a, cudaStream_t stream);
-// The library's second stream for the backward's dQ on the current device (null: none could
-// be made).
-cudaStream_t bwd_side_stream();
+// Two launches side by side behind `stream`'s work, both before its later work (beside.cpp): each
+// is called with the stream that it goes to.
+using LaunchFn = cudaError_t (*)(void* what, cudaStream_t stream);
+cudaError_t launch_beside(cudaStream_t stream, LaunchFn first, void* what1, LaunchFn second,
+                          void* what2);
+template <class F1, class F2>
+cudaError_t launch_beside(cudaStream_t stream, F1 first, F2 second) {
+  return launch_beside(
+      stream, [](void* f, cudaStream_t s) { return (*static_cast<F1*>(f))(s); }, &first,
+      [](void* f, cudaStream_t s) { return (*static_cast<F2*>(f))(s); }, &second);
+}
 cudaError_t launch_doc_scan(const int32_t* doc_offsets, int S, int32_t* doc_info,
                             cudaStream_t stream);
 cudaError_t launch_merge(float* o_acc, float* m_acc, float* l_acc, const float* o_part,

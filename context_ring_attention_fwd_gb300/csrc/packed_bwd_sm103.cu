@@ -859,30 +859,23 @@ cudaError_t launch_packed_bwd(const PackedArgs& a, BParams p, const PackedList& 
                : cudaLaunchKernelEx(&cfg, kern, mq, mg, mk, mv, p);
 }
 
-// dK/dV on `stream`, dQ beside it on the library's second stream, whose CTAs take the SMs that
-// the last dK/dV items leave idle; both after the plan.
+// dK/dV on `stream`, dQ beside it, whose CTAs take the SMs that the last dK/dV items leave idle;
+// both after the plan.  (A captured dK/dV waits for the whole plan before it starts.)
 template <int D>
 cudaError_t launch_packed_pair(const PackedArgs& a, const BParams& dkdv, const BParams& dq,
                                const PackedPlan& plan, const void* dout, cudaStream_t stream) {
-  const cudaStream_t side = bwd_side_stream();
-  if (!side) return cudaErrorUnknown;
-  cudaEvent_t ready = nullptr, dq_done = nullptr;
-  if (cudaEventCreateWithFlags(&ready, cudaEventDisableTiming) != cudaSuccess)
-    return cudaErrorUnknown;
-  if (cudaEventCreateWithFlags(&dq_done, cudaEventDisableTiming) != cudaSuccess) {
-    cudaEventDestroy(ready);
-    return cudaErrorUnknown;
-  }
-  cudaError_t e = cudaEventRecord(ready, stream);
-  if (e == cudaSuccess) e = launch_packed_bwd<D, true>(a, dkdv, plan.list[0], dout, true, stream);
-  if (e == cudaSuccess) e = cudaStreamWaitEvent(side, ready, 0);
-  if (e == cudaSuccess) e = launch_packed_bwd<D, false>(a, dq, plan.list[1], dout, false, side);
-  if (e == cudaSuccess) e = cudaEventRecord(dq_done, side);
-  if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, dq_done, 0);
-  // (destroying a recorded event releases it once the work it marks is done)
-  cudaEventDestroy(ready);
-  cudaEventDestroy(dq_done);
-  return e;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(stream, &status);
+  if (e != cudaSuccess) return e;
+  const bool early = status == cudaStreamCaptureStatusNone;
+  return launch_beside(
+      stream,
+      [&](cudaStream_t s) {
+        return launch_packed_bwd<D, true>(a, dkdv, plan.list[0], dout, early, s);
+      },
+      [&](cudaStream_t s) {
+        return launch_packed_bwd<D, false>(a, dq, plan.list[1], dout, false, s);
+      });
 }
 
 // Byte offsets of the workspace's parts: the lists of key tiles (with its parts) and of query
