@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* fix_item =
       reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 2 * kRing * 8 + kRing * 32);
 
-  const int warp = threadIdx.x >> 5;
+  // (by a shuffle: the compiler then knows it, and what follows from it, as the warp's)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {

@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* q_item =
       reinterpret_cast<volatile int*>(smem + Lay::kRingOff + 2 * kRing * 8 + kRing * 32);
 
-  const int warp = threadIdx.x >> 5;
+  // (by a shuffle: the compiler then knows it, and what follows from it, as the warp's)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -656,21 +657,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t rows = sbase + Lay::kStageOff + warp * kRowStage;
 #pragma unroll 1
       for (int half = 0; half < D / 64; ++half) {  // 64 columns, 128 bytes of a row
+        uint32_t ov[2][32];
+        if (kParts && first_part != nullptr) {
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch)
+            join_parts<D>(p, first_part, half * 2 + ch, parts, m_used, row_in_tile, ov[ch]);
+        } else {
+          ptx::tmem_ld32(tO + half * 64, ov[0]);
+          ptx::tmem_ld32(tO + half * 64 + 32, ov[1]);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence(ov[0]);
+          ptx::reg_fence(ov[1]);
+        }
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
-          uint32_t ov[32];
-          if (kParts && first_part != nullptr) {
-            join_parts<D>(p, first_part, half * 2 + ch, parts, m_used, row_in_tile, ov);
-          } else {
-            ptx::tmem_ld32(tO + half * 64 + ch * 32, ov);
-            ptx::tmem_wait_ld();
-            ptx::reg_fence(ov);
-          }
           uint32_t b[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x)
-            b[x] = ptx::pack_bf16(__uint_as_float(ov[2 * x]) * inv_l,
-                                  __uint_as_float(ov[2 * x + 1]) * inv_l);
+            b[x] = ptx::pack_bf16(__uint_as_float(ov[ch][2 * x]) * inv_l,
+                                  __uint_as_float(ov[ch][2 * x + 1]) * inv_l);
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             stage_chunk(rows, lane, ch * 4 + x, b[4 * x], b[4 * x + 1], b[4 * x + 2], b[4 * x + 3]);
