@@ -17,7 +17,10 @@
 //    ldmatrix.trans, which moves 16 bits, four neighbouring columns, of two keys to a lane.
 //  - P^T leaves the first product with a key to a lane and enters the second with a row to a
 //    lane: movmatrix turns its 8 x 8 pieces.
-// Measured in paged_decode.cu.
+//  - A row's reference moves only when a score passes it by 2^5 (all but a few of the first tiles
+//    of an item go without the maximum's shuffles), and V is read while the softmax waits.
+// 660 instructions for 32 keys and 8 rows; issue slots are 63 % used in the long case, where the
+// whole call runs at 76 % of the copy rate (paged_decode.cu).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -103,8 +106,9 @@ struct Int4Core {
   static constexpr float kUnit = 16.f;          // values are held divided by it
 
   uint32_t q[kNT][D / 16][2];
-  float sc[kNT][2];  // of rows 2 c4 and 2 c4 + 1
-  float m[kNT][2], l[kNT][2];
+  float sc[kNT][2];    // of rows 2 c4 and 2 c4 + 1
+  float lift[kNT][2];  // kShift less the rows' references (infinity: no key yet)
+  float l[kNT][2];
   float o[kNT][D / 16][4];
 
   // Chunk c of row r at c ^ (r / 2 mod 4), for rows of 32 bytes c ^ (r / 4 mod 2): free of bank
@@ -142,7 +146,7 @@ struct Int4Core {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         sc[nt][e] = __shfl_sync(0xffffffffu, mine, (2 * c4 + e) * 4);
-        m[nt][e] = -INFINITY;
+        lift[nt][e] = INFINITY;
         l[nt][e] = 0.f;
       }
 #pragma unroll
@@ -179,16 +183,15 @@ struct Int4Core {
   __device__ __forceinline__ void step(uint32_t stage, int left, int lane) {
     const int quad = lane >> 2, c4 = lane & 3;
     constexpr int kWords = D / 32;
-    // ---- S^T: keys quad and quad + 8 of each 16, rows 2 c4 and 2 c4 + 1; in two sums each, so
-    // that four products are under way at a time
-    float s[2][kNT][4], s2[2][kNT][4];
+    // ---- S^T: keys quad and quad + 8 of each 16, rows 2 c4 and 2 c4 + 1
+    float s[2][kNT][4];
     uint32_t u[2][2][kWords], two[2][2];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] = s2[mt][nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = mt * 16 + h * 8 + quad;
@@ -217,7 +220,7 @@ struct Int4Core {
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt) {
             mma(s[mt][nt], a0, q[nt][2 * x][0], q[nt][2 * x][1]);
-            mma(s2[mt][nt], a1, q[nt][2 * x + 1][0], q[nt][2 * x + 1][1]);
+            mma(s[mt][nt], a1, q[nt][2 * x + 1][0], q[nt][2 * x + 1][1]);
           }
         }
       }
@@ -245,39 +248,46 @@ struct Int4Core {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[mt][nt][e] += s2[mt][nt][e];
+        for (int e = 0; e < 4; ++e)
           if (left < kKeys && mt * 16 + (e >> 1) * 8 + quad >= left) s[mt][nt][e] = -INFINITY;
-        }
     // ---- P against a reference that moves only when a score passes it by 2^kSlack
-    auto exponents = [&](int mt, int nt, int e) {
-      const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-      return fmaf(s[mt][nt][e], sc[nt][e & 1], kShift - ref);
+    float x[2][kNT][4];  // the exponents
+    auto against = [&](const float (&from)[kNT][2]) {
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[mt][nt][e] = fmaf(s[mt][nt][e], sc[nt][e & 1], from[nt][e & 1]);
     };
+    against(lift);
     bool over = false;
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
-      float top = -INFINITY;
+      float top = lift[nt][0] == INFINITY || lift[nt][1] == INFINITY ? INFINITY : -INFINITY;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, exponents(mt, nt, e));
-      over |= top > kShift + kSlack || m[nt][0] == -INFINITY || m[nt][1] == -INFINITY;
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, x[mt][nt][e]);
+      over |= top > kShift + kSlack;
     }
     if (__any_sync(0xffffffffu, over)) {
+      float from[kNT][2];
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
         float a[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]),
+          float y = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]),
                           fmaxf(s[1][nt][e], s[1][nt][e + 2])) * sc[nt][e];
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          const float n = fmaxf(m[nt][e], x);
-          a[e] = m[nt][e] == -INFINITY ? 0.f : ptx::ex2(m[nt][e] - n);
-          m[nt][e] = n;
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+          const float old = lift[nt][e];
+          lift[nt][e] = fminf(old, kShift - y);
+          a[e] = old == INFINITY ? 0.f : ptx::ex2(lift[nt][e] - old);
+          from[nt][e] = lift[nt][e] == INFINITY ? kShift : lift[nt][e];  // no key yet
           l[nt][e] *= a[e];
         }
 #pragma unroll
@@ -285,20 +295,21 @@ struct Int4Core {
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[nt][k][e] *= a[e & 1];
       }
+      against(from);
     }
     uint32_t p[2][kNT][2];  // of 16 keys: the first 8, the others
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        float x[4];
+        float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[e] = ptx::ex2(exponents(mt, nt, e));
-          l[nt][e & 1] += x[e];
+          y[e] = ptx::ex2(x[mt][nt][e]);
+          l[nt][e & 1] += y[e];
         }
-        p[mt][nt][0] = transposed8x8(pack_f16(x[0], x[1]));
-        p[mt][nt][1] = transposed8x8(pack_f16(x[2], x[3]));
+        p[mt][nt][0] = transposed8x8(pack_f16(y[0], y[1]));
+        p[mt][nt][1] = transposed8x8(pack_f16(y[2], y[3]));
       }
     // ---- O^T += V^T P^T
     const uint32_t pick = 0x6240u + 0x1111u * (quad >> 2);  // of a chunk's two blocks, this lane's
@@ -325,6 +336,8 @@ struct Int4Core {
         }
       }
   }
+
+  __device__ __forceinline__ float m(int nt, int e) const { return kShift - lift[nt][e]; }
 
   // The sums of the rows' exponentials over the lanes that share them.
   __device__ __forceinline__ void sum_lanes() {
