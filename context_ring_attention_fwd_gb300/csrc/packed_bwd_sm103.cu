@@ -47,22 +47,21 @@ constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Streamed tiles run in two rings of single-tile slots: X0 (K for kDQ, Q for
-// kDKDV) and X1 (V or dO).  kDQ holds K until dQ += dS K is done but V only
-// until dP, and issues the next step's products early, so its K ring is one
-// slot deeper.
+// kDKDV) and X1 (V or dO).  A step's K or Q is held until its dQ or dK is done, behind the next
+// step's first product, V only until dP and dO until dV, so the first ring is one slot deeper.
 template <int D, bool kDKDV>
 struct BLayout {
   static constexpr int kTileBytes = kT * D * 2;
   static constexpr int kPanelBytes = kT * 128;   // 128 rows x 64 bf16 columns
   static constexpr int kPanels = D / 64;
-  static constexpr int kX0Slots = kDKDV ? 2 : 3;
+  static constexpr int kX0Slots = 3;
   static constexpr int kX1Slots = 2;
   static constexpr int kF0 = 0;                  // fixed tiles
   static constexpr int kF1 = kTileBytes;
   static constexpr int kX0 = 2 * kTileBytes;
   static constexpr int kX1 = kX0 + kX0Slots * kTileBytes;
-  static constexpr int kVec = kX1 + kX1Slots * kTileBytes;    // kDKDV: [2][-lse2, -D][128] fp32
-  static constexpr int kBar = kVec + (kDKDV ? 2 * 2 * kT * 4 : 0);
+  static constexpr int kVec = kX1 + kX1Slots * kTileBytes;    // kDKDV: fp32 [128], -lse2 of two tiles, -D
+  static constexpr int kBar = kVec + (kDKDV ? 3 * kT * 4 : 0);
   static constexpr int kRingOff = kBar + 256;  // the item ring
   static constexpr int kBytes = kRingOff + 256;
   static constexpr int kAlloc = kBytes + 1024;
@@ -77,13 +76,13 @@ enum BBar : int {
   kX1Full = 5,     // + slot (2)
   kX0Empty = 7,    // + slot (3)
   kX1Empty = 10,   // + slot (2)
-  kSFull = 12,     // + TMEM buffer (kDKDV; kDQ uses +0): S and dP of a step are in TMEM
-  kPReady = 14,    // + step parity: P / dS written by all softmax threads
+  kSFull = 12,     // S and dP of a step are in TMEM (kDKDV: S^T, and with + 1 dP^T)
+  kPReady = 14,    // kDQ: + step parity: dS written; kDKDV: + half: P^T of 64 queries written
   kSConsumed = 16, // kDQ: every softmax thread has read S and dP of the step
   kAccFull = 17,   // the item's accumulators are final
-  kVecFull = 18,   // + buffer: per-column lse / delta of a query tile written (kDKDV)
-  kVecFree = 20,   // + buffer: every softmax thread is done reading it
-  kPReadyS = 22,   // + TMEM buffer (kDKDV): dS^T written (kPReady + buffer: P^T written)
+  kVecFull = 18,   // + buffer: per-column lse of a query tile written (kDKDV)
+  kDFull = 20,     // the same of D
+  kPReadyS = 22,   // + half (kDKDV): dS^T of 64 queries written
   kDrain = 24,
   kJoin = 25,      // kDKDV: the softmax threads have stored a part's sums; then: know its rank
   kNumBars = 26
@@ -252,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(bar(kAccFull), 1);
     for (int b2 = 0; b2 < 2; ++b2) {
       ptx::mbar_init(bar(kVecFull + b2), kT);
-      ptx::mbar_init(bar(kVecFree + b2), kSoftmaxThreads);
     }
+    ptx::mbar_init(bar(kDFull), kT);
     ptx::mbar_init(bar(kJoin), kSoftmaxThreads);
     ptx::mbar_init(bar(kPReadyS), kSoftmaxThreads);
     ptx::mbar_init(bar(kPReadyS + 1), kSoftmaxThreads);
@@ -404,19 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int s = 0; s < steps; ++s) step(s);
         }
       };
-      uint32_t n = 0;       // kDQ: steps issued so far (all items)
-      uint32_t m_half = 0;  // kDKDV: halves issued so far (all items)
-      constexpr uint32_t kIdescS64 = ptx::idesc_bf16_f32(kT, 64, false);
-      // D = A B^T over the head dimension with B 64 rows (a half tile).
-      auto issue_ss64 = [&](uint32_t d_tmem, int a_off, int b_off) {
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint64_t step =
-              static_cast<uint64_t>(((s >> 2) * Lay::kPanelBytes + (s & 3) * 32) >> 4);
-          ptx::mma_ss_w(d_tmem, d_k + (a_off >> 4) + step, d_k + (b_off >> 4) + step, kIdescS64,
-                      s > 0 ? 1u : 0u);
-        }
-      };
+      uint32_t n = 0;  // steps issued so far (all items), and (kDKDV) those of two halves
+      uint32_t n_two = 0;
       // acc (+)= A B over 64 queries: A = the two warpgroups' packed pieces
       // (32 columns apart), B = the half tile at b_off read MN-major.
       auto issue_ts64 = [&](uint32_t acc, uint32_t a_tmem, int b_off, bool first, int steps) {
@@ -498,54 +486,67 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mma_commit_w(bar(kAccFull));
           continue;
         }
-        // kDKDV: half hh of the item is query rows 64 (hh % 2) .. of its
-        // streamed tile x_iter + hh / 2; m counts halves over all items and
-        // half m uses TMEM buffer m % 2.  S^T, dP^T of half m + 1 are issued
-        // before dV, dK of half m, so they run during the softmax of half m.
-        // (the last tile's second half is left out where no row is in it).
-        const int last_half = 2 * (it.x_hi - it.x_lo);
-        const int nh = last_half + (last_steps > 4 ? 2 : 1);
-        auto issue_half = [&](uint32_t mm, int hh2) -> bool {
-          const uint32_t xi = x_iter + static_cast<uint32_t>(hh2 >> 1);
-          const uint32_t st = xi % Lay::kX0Slots, ph = (xi / Lay::kX0Slots) & 1u;
-          if (!wait_warp(bar(kX0Full + st), ph, abort_flag, p)) return false;
-          if (!wait_warp(bar(kX1Full + st), ph, abort_flag, p)) return false;
+        // kDKDV: dV += P^T dO of a step and S^T of the next go out when its P^T is written, in two
+        // halves of 64 queries, dK += dS^T Q and the next dP^T when its dS^T is.  So the softmax
+        // forms dS^T during the first pair of products and the next P^T during the second.  P^T
+        // and dS^T lie where S^T and dP^T were, which the products' order keeps apart.
+        // (The last tile's second half is left out where no row is in it.)
+        auto issue_s = [&](uint32_t x, bool last) -> bool {  // S^T = K Q^T
+          const uint32_t s0 = x % Lay::kX0Slots;
+          if (!wait_warp(bar(kX0Full + s0), (x / Lay::kX0Slots) & 1u, abort_flag, p)) return false;
           ptx::tc_fence_after();
-          if (hh2 == last_half && ragged && last_rows < last_zero) {
-            zero_rows<Lay::kPanels>(sbase + Lay::x0(st), last_rows, last_zero);
-            zero_rows<Lay::kPanels>(sbase + Lay::x1(st), last_rows, last_zero);
+          if (last && ragged && last_rows < last_zero) {
+            zero_rows<Lay::kPanels>(sbase + Lay::x0(s0), last_rows, last_zero);
             ptx::fence_proxy_async_shared();
             __syncwarp();
           }
-          const uint32_t b = mm & 1u;
-          const int rows = (hh2 & 1) * 64 * 128;   // byte offset of query row 64 in a panel
-          issue_ss64(tmem_base + 128u * b, Lay::kF0, Lay::x0(st) + rows);         // S^T = K Q_h^T
-          issue_ss64(tmem_base + 128u * b + 64u, Lay::kF1, Lay::x1(st) + rows);   // dP^T = V dO_h^T
-          ptx::mma_commit_w(bar(kSFull + b));
+          issue_ss(tS, Lay::kF0, Lay::x0(s0));
+          ptx::mma_commit_w(bar(kSFull));
           return true;
         };
-        if (!issue_half(m_half, 0)) { ok = false; break; }
-        for (int hh = 0; hh < nh; ++hh) {
-          const uint32_t b = m_half & 1u;
-          if (hh + 1 < nh && !issue_half(m_half + 1, hh + 1)) { ok = false; break; }
-          // dV += P^T dO_h as soon as P^T is in TMEM, dK += dS^T Q_h once dS^T is
-          if (!wait_warp(bar(kPReady + b), (m_half >> 1) & 1u, abort_flag, p)) { ok = false; break; }
+        auto issue_dp = [&](uint32_t x, bool last) -> bool {  // dP^T = V dO^T
+          const uint32_t s1 = x % Lay::kX1Slots;
+          if (!wait_warp(bar(kX1Full + s1), (x / Lay::kX1Slots) & 1u, abort_flag, p)) return false;
           ptx::tc_fence_after();
-          const uint32_t st = (x_iter + static_cast<uint32_t>(hh >> 1)) % Lay::kX0Slots;
-          const int rows = (hh & 1) * 64 * 128;
-          const int steps = hh >= last_half ? last_steps - 4 * (hh & 1) : 4;
-          issue_ts64(tA0, tmem_base + 128u * b, Lay::x1(st) + rows, hh == 0, steps);
-          if (!wait_warp(bar(kPReadyS + b), (m_half >> 1) & 1u, abort_flag, p)) { ok = false; break; }
-          ptx::tc_fence_after();
-          issue_ts64(tA1, tmem_base + 128u * b + 64u, Lay::x0(st) + rows, hh == 0, steps);
-          if ((hh & 1) || hh + 1 == nh) {
-            ptx::mma_commit_w(bar(kX0Empty + st));
-            ptx::mma_commit_w(bar(kX1Empty + st));
+          if (last && ragged && last_rows < last_zero) {
+            zero_rows<Lay::kPanels>(sbase + Lay::x1(s1), last_rows, last_zero);
+            ptx::fence_proxy_async_shared();
+            __syncwarp();
           }
-          ++m_half;
+          issue_ss(tdP, Lay::kF1, Lay::x1(s1));
+          ptx::mma_commit_w(bar(kSFull + 1));
+          return true;
+        };
+        if (!issue_s(x_iter, it.x_lo == it.x_hi) || !issue_dp(x_iter, it.x_lo == it.x_hi)) {
+          ok = false;
+          break;
+        }
+        for (int f = it.x_lo; f <= it.x_hi; ++f) {
+          const bool first = f == it.x_lo, last = f == it.x_hi;
+          const int steps = last ? last_steps : kT / 16;
+          // acc += A B, A in the halves' order as they are written
+          auto issue_g = [&](uint32_t acc, uint32_t a_tmem, int b_off, int ready) -> bool {
+            if (!wait_warp(bar(ready), n & 1u, abort_flag, p)) return false;
+            ptx::tc_fence_after();
+            issue_ts64(acc, a_tmem, b_off, first, steps);
+            if (steps <= 4) return true;
+            if (!wait_warp(bar(ready + 1), n_two & 1u, abort_flag, p)) return false;
+            ptx::tc_fence_after();
+            issue_ts64(acc, a_tmem + 64u, b_off + 64 * 128, false, steps - 4);
+            return true;
+          };
+          const uint32_t s0 = x_iter % Lay::kX0Slots, s1 = x_iter % Lay::kX1Slots;
+          if (!issue_g(tA0, tS, Lay::x1(s1), kPReady)) { ok = false; break; }
+          ptx::mma_commit_w(bar(kX1Empty + s1));
+          if (!last && !issue_s(x_iter + 1, f + 1 == it.x_hi)) { ok = false; break; }
+          if (!issue_g(tA1, tdP, Lay::x0(s0), kPReadyS)) { ok = false; break; }
+          ptx::mma_commit_w(bar(kX0Empty + s0));
+          if (!last && !issue_dp(x_iter + 1, f + 1 == it.x_hi)) { ok = false; break; }
+          ++n;
+          if (steps > 4) ++n_two;
+          ++x_iter;
         }
         if (!ok) break;
-        x_iter += static_cast<uint32_t>(it.x_hi - it.x_lo + 1);
         ptx::mma_commit_w(bar(kFixEmpty));
         ptx::mma_commit_w(bar(kAccFull));
       }
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // whose constants it loads
     const int packed_row = kDKDV ? static_cast<int>(threadIdx.x) : row_in_tile;
     const int my_token = packed_row / p.G, my_head = packed_row - my_token * p.G;
-    uint32_t s_cnt = 0, item_cnt = 0, h_cnt = 0, join_cnt = 0;
+    uint32_t s_cnt = 0, item_cnt = 0, join_cnt = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       PackedEntry entry;
@@ -592,29 +593,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         lse2_r = __ldg(p.lse + static_cast<size_t>(head) * p.T + row) * kLog2e;
         d_r = p.delta[row * p.Hq + head];
       }
+      // kDKDV: -lse2 and -D of this thread's row of a streamed tile.  Rows behind the tile's last:
+      // P = 2^-inf = 0 where the scores are finite.
+      float nl_next = 0.f, nd_next = 0.f;
+      auto load_constants = [&](int f) {
+        nl_next = -INFINITY;
+        nd_next = 0.f;
+        const int t = f * x_tokens + my_token;
+        if (threadIdx.x < kT && f <= it.x_hi && my_token < p.tq && t < it.len) {
+          const size_t q = static_cast<size_t>(it.row0) + t;
+          const int h = it.hk * p.G + my_head;
+          nl_next = -__ldg(p.lse + static_cast<size_t>(h) * p.T + q) * kLog2e;
+          nd_next = -p.delta[q * p.Hq + h];
+        }
+      };
+      if (kDKDV) load_constants(it.x_lo);
       for (int f = it.x_lo; f <= it.x_hi; ++f) {
         const int xs = f * x_tokens;  // first streamed token
         const int tokens = min(x_tokens, it.len - xs);
-        const int buf = static_cast<int>(s_cnt & 1u);
-        const uint32_t use = s_cnt >> 1;  // uses of this buffer before this one
-        if (kDKDV) {
-          // Per-column constants of the streamed query tile, shared by all
-          // rows: warps 0-3 write them once the previous user of the buffer
-          // is done, every softmax warp waits for them (all waits bounded).
-          if (threadIdx.x < kT) {
-            if (use > 0 &&
-                !wait_warp(bar(kVecFree + buf), (use - 1u) & 1u, abort_flag, p)) { ok = false; break; }
-            // Rows behind the tile's last: P = 2^-inf = 0 where the scores are finite.
-            const bool there = my_token < tokens;
-            const size_t q = static_cast<size_t>(it.row0) + xs + my_token;
-            const int h = it.hk * p.G + my_head;
-            vec[(buf * 2 + 0) * kT + threadIdx.x] =
-                there ? -__ldg(p.lse + static_cast<size_t>(h) * p.T + q) * kLog2e : -INFINITY;
-            vec[(buf * 2 + 1) * kT + threadIdx.x] = there ? -p.delta[q * p.Hq + h] : 0.f;
-            ptx::mbar_arrive(bar(kVecFull + buf));
-          }
-          if (!wait_warp(bar(kVecFull + buf), use & 1u, abort_flag, p)) { ok = false; break; }
-        }
         // The columns that the row sees.  A packed tile of all its tokens ends in zero rows of Q
         // and dO, which need no mask (their P is 0 by their constant).
         const int c_lo = kDKDV ? max(from - xs, 0) * p.G : 0;
@@ -664,79 +660,107 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(bar(kPReady + (n & 1u)));
           continue;
         }
-        ++s_cnt;  // query tiles seen: selects the per-column buffer
-        // The two 64-query halves of this tile; half m uses TMEM buffer m % 2.
-        const int halves = f == it.x_hi && tokens < x_tokens && tokens * p.G <= 64 ? 1 : 2;
-        for (int h = 0; h < halves; ++h) {
-          const uint32_t b = h_cnt & 1u;
-          if (!wait_warp(bar(kSFull + b), (h_cnt >> 1) & 1u, abort_flag, p)) { ok = false; break; }
-          ptx::tc_fence_after();
-          // this warpgroup's 32 columns of S^T and dP^T in buffer b
-          const uint32_t tb = tmem_base + lane_off + 128u * b + 32u * static_cast<uint32_t>(wg);
-          uint32_t sv[32], dv[32];
-          ptx::tmem_ld32(tb, sv);
-          ptx::tmem_ld32(tb + 64, dv);
-          ptx::tmem_wait_ld();
-          ptx::reg_fence(sv);
-          ptx::reg_fence(dv);
-          const int c0 = 64 * h + 32 * wg;   // first tile column of this piece
-          uint32_t pk_p[16], pk_s[16];
-          float pf[32];  // this chunk's P in fp32, for dS
-          // per-column -lse2 and -D of this chunk, four columns per load
-          const float4* nl4 = reinterpret_cast<const float4*>(vec + (buf * 2 + 0) * kT + c0);
-          const float4* nd4 = reinterpret_cast<const float4*>(vec + (buf * 2 + 1) * kT + c0);
-          // P^T first: it is stored and announced (kPReady) before dS^T is
-          // formed, so the MMA warp starts dV += P^T dO meanwhile.
-          const bool masked = __any_sync(0xffffffffu, c_lo > c0 || c_hi < c0 + 31);
-          const uint32_t columns = seen_columns(c_lo - c0, c_hi - c0);
-          {
-#pragma unroll
-            for (int x4 = 0; x4 < 8; ++x4) {  // paired fp32
-              const float4 nl = nl4[x4];
-              const float nla[4] = {nl.x, nl.y, nl.z, nl.w};
-#pragma unroll
-              for (int hx = 0; hx < 2; ++hx) {
-                const int x = 2 * x4 + hx;
-                float e0, e1;
-                ptx::fma_f32x2(e0, e1, __uint_as_float(sv[2 * x]), __uint_as_float(sv[2 * x + 1]), sc,
-                               sc, nla[2 * hx], nla[2 * hx + 1]);
-                pf[2 * x] = ptx::ex2(e0);
-                pf[2 * x + 1] = ptx::ex2(e1);
-                pk_p[x] = ptx::pack_bf16(pf[2 * x], pf[2 * x + 1]);
-              }
-            }
-          }
-          if (masked) keep_pairs(pk_p, columns);
-          ptx::tmem_st16(tb, pk_p);
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(bar(kPReady + b));
-          // dS^T = P^T (dP^T - D)
-          {
-#pragma unroll
-            for (int x4 = 0; x4 < 8; ++x4) {
-              const float4 nd = nd4[x4];
-              const float nda[4] = {nd.x, nd.y, nd.z, nd.w};
-#pragma unroll
-              for (int hx = 0; hx < 2; ++hx) {
-                const int x = 2 * x4 + hx;
-                float g0, g1;
-                ptx::fma_f32x2(g0, g1, __uint_as_float(dv[2 * x]), __uint_as_float(dv[2 * x + 1]), 1.f,
-                               1.f, nda[2 * hx], nda[2 * hx + 1]);
-                ptx::fma_f32x2(g0, g1, pf[2 * x], pf[2 * x + 1], g0, g1, 0.f, 0.f);
-                pk_s[x] = ptx::pack_bf16(g0, g1);
-              }
-            }
-          }
-          if (masked) keep_pairs(pk_s, columns);
-          ptx::tmem_st16(tb + 64, pk_s);
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(bar(kPReadyS + b));
-          ++h_cnt;
+        // Per-column constants of the streamed query tile, shared by all rows: warps 0-3 write
+        // them, having loaded them a tile ahead.  Nobody still reads the buffers: a thread that
+        // has seen S^T of step n - 1 (this loop's last turn) knows that all have formed P^T of
+        // step n - 2, one that has seen dP^T of step n that all have formed dS^T of step n - 1.
+        const float nd = nd_next;
+        float* const lse_vec = vec + (s_cnt & 1u) * kT;
+        if (threadIdx.x < kT) {
+          lse_vec[threadIdx.x] = nl_next;
+          ptx::mbar_arrive(bar(kVecFull + (s_cnt & 1u)));
+          load_constants(f + 1);
         }
-        if (!ok) break;
-        ptx::mbar_arrive(bar(kVecFree + buf));
+        const bool two = f != it.x_hi || tokens == x_tokens || tokens * p.G > 64;  // halves
+        if (!wait_warp(bar(kVecFull + (s_cnt & 1u)), (s_cnt >> 1) & 1u, abort_flag, p)) {
+          ok = false;
+          break;
+        }
+        if (!wait_warp(bar(kSFull), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
+        ptx::tc_fence_after();
+        // This warpgroup's 32 columns of each half.  P stays in fp32 for dS.
+        uint32_t pv[2][32];
+        ptx::tmem_ld32(tS + 32 * wg, pv[0]);
+        ptx::tmem_ld32(tS + 32 * wg + 64, pv[1]);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence(pv[0]);
+        ptx::reg_fence(pv[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !two) break;
+          const int c0 = 64 * h + 32 * wg;
+          const float4* const nl4 = reinterpret_cast<const float4*>(lse_vec + c0);
+          uint32_t pk[16];
+#pragma unroll
+          for (int x4 = 0; x4 < 8; ++x4) {  // paired fp32
+            const float4 nl = nl4[x4];
+            const float nla[4] = {nl.x, nl.y, nl.z, nl.w};
+#pragma unroll
+            for (int hx = 0; hx < 2; ++hx) {
+              const int x = 2 * x4 + hx;
+              float e0, e1;
+              ptx::fma_f32x2(e0, e1, __uint_as_float(pv[h][2 * x]),
+                             __uint_as_float(pv[h][2 * x + 1]), sc, sc, nla[2 * hx],
+                             nla[2 * hx + 1]);
+              e0 = ptx::ex2(e0);
+              e1 = ptx::ex2(e1);
+              pv[h][2 * x] = __float_as_uint(e0);
+              pv[h][2 * x + 1] = __float_as_uint(e1);
+              pk[x] = ptx::pack_bf16(e0, e1);
+            }
+          }
+          if (__any_sync(0xffffffffu, c_lo > c0 || c_hi < c0 + 31))
+            keep_pairs(pk, seen_columns(c_lo - c0, c_hi - c0));
+          ptx::tmem_st16(tS + c0, pk);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(kPReady + h));
+        }
+        // dS^T = P^T (dP^T - D)
+        float* const d_vec = vec + 2 * kT;
+        if (!wait_warp(bar(kSFull + 1), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
+        ptx::tc_fence_after();
+        if (threadIdx.x < kT) {
+          d_vec[threadIdx.x] = nd;
+          ptx::mbar_arrive(bar(kDFull));
+        }
+        uint32_t dv[2][32];
+        ptx::tmem_ld32(tdP + 32 * wg, dv[0]);
+        ptx::tmem_ld32(tdP + 32 * wg + 64, dv[1]);
+        if (!wait_warp(bar(kDFull), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
+        ptx::tmem_wait_ld();
+        ptx::reg_fence(dv[0]);
+        ptx::reg_fence(dv[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !two) break;
+          const int c0 = 64 * h + 32 * wg;
+          const float4* const nd4 = reinterpret_cast<const float4*>(d_vec + c0);
+          uint32_t pk[16];
+#pragma unroll
+          for (int x4 = 0; x4 < 8; ++x4) {
+            const float4 nd_c = nd4[x4];
+            const float nda[4] = {nd_c.x, nd_c.y, nd_c.z, nd_c.w};
+#pragma unroll
+            for (int hx = 0; hx < 2; ++hx) {
+              const int x = 2 * x4 + hx;
+              float g0, g1;
+              ptx::fma_f32x2(g0, g1, __uint_as_float(dv[h][2 * x]),
+                             __uint_as_float(dv[h][2 * x + 1]), 1.f, 1.f, nda[2 * hx],
+                             nda[2 * hx + 1]);
+              ptx::fma_f32x2(g0, g1, __uint_as_float(pv[h][2 * x]),
+                             __uint_as_float(pv[h][2 * x + 1]), g0, g1, 0.f, 0.f);
+              pk[x] = ptx::pack_bf16(g0, g1);
+            }
+          }
+          if (__any_sync(0xffffffffu, c_lo > c0 || c_hi < c0 + 31))
+            keep_pairs(pk, seen_columns(c_lo - c0, c_hi - c0));
+          ptx::tmem_st16(tdP + c0, pk);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(kPReadyS + h));
+        }
+        ++s_cnt;
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
