@@ -71,26 +71,26 @@ struct BLayout {
 
 enum BBar : int {
   kFixFull = 0,
-  kFixEmpty = 1,
+  kFixEmpty = 1,   // (kDQ: every softmax thread and the MMA warp have read the item's)
   kX0Full = 2,     // + slot (3)
   kX1Full = 5,     // + slot (2)
   kX0Empty = 7,    // + slot (3)
   kX1Empty = 10,   // + slot (2)
-  kSFull = 12,     // S and dP of a step are in TMEM (kDKDV: S^T, and with + 1 dP^T)
-  kPReady = 14,    // kDQ: + step parity: dS written; kDKDV: + half: P^T of 64 queries written
-  kSConsumed = 16, // kDQ: every softmax thread has read S and dP of the step
-  kAccFull = 17,   // the item's accumulators are final
-  kVecFull = 18,   // + buffer: per-column lse of a query tile written (kDKDV)
-  kDFull = 20,     // the same of D
-  kPReadyS = 22,   // + half (kDKDV): dS^T of 64 queries written
+  kSFull = 12,     // S of a step is in TMEM
+  kDPFull = 13,    // dP
+  kPReady = 14,    // kDKDV: + half: P^T of 64 queries written by all softmax threads
+  kDSReady = 16,   // + half: dS of 64 streamed rows written
+  kSRead = 18,     // kDQ: every softmax thread has read S of the step
+  kAccFull = 19,   // the item's accumulators are final
+  kVecFull = 20,   // kDKDV: + buffer: per-column lse of a query tile written
+  kDFull = 22,     // the same of D
+  kFixHeld = 23,   // kDQ: Q and dO of the item are in TMEM
   kDrain = 24,
   kJoin = 25,      // kDKDV: the softmax threads have stored a part's sums; then: know its rank
   kNumBars = 26
 };
-// kDQ keeps packed dS in its own double buffer of TMEM columns (acc0 ends at
-// 256 + D <= 384), so S and dP of the next step can be issued while the
-// softmax still works on the current one.
-constexpr uint32_t kDsBuf = 384;
+// TMEM: S, dP, the accumulators from 256 on; of kDQ also the fixed tiles, packed, from here on.
+constexpr uint32_t kHeldQ = 384, kHeldG = 448;
 constexpr int kTmemSlot = kNumBars * 8;
 constexpr int kAbortSlot = kNumBars * 8 + 4;
 constexpr int kRankSlot = kNumBars * 8 + 8;
@@ -151,18 +151,20 @@ __device__ __forceinline__ void decode_bitem(const BParams& p, const PackedEntry
   }
 }
 
-// The columns [lo, hi] of 32 as bits, and packed bf16 pairs of 32 columns with the others
+// The columns [lo, hi] of 32 as bits, and 32 columns (fp32, and packed in bf16) with the others
 // zeroed: what masked pairs of a query and a key hold is replaced, whatever it is.
 __device__ __forceinline__ uint32_t seen_columns(int lo, int hi) {
   const uint32_t below = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
   return lo <= 0 ? below : lo > 31 ? 0u : below & (0xffffffffu << lo);
 }
-__device__ __forceinline__ void keep_pairs(uint32_t (&pk)[16], uint32_t columns) {
+__device__ __forceinline__ void keep_columns(uint32_t (&v)[32], uint32_t (&pk)[16],
+                                             uint32_t columns) {
 #pragma unroll
-  for (int x = 0; x < 16; ++x) {
-    const uint32_t two = columns >> (2 * x);
-    pk[x] &= (two & 1u ? 0x0000ffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
-  }
+  for (int x = 0; x < 32; ++x)
+    if (!(columns >> x & 1u)) v[x] = 0u;
+#pragma unroll
+  for (int x = 0; x < 16; ++x)
+    pk[x] = ptx::pack_bf16(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
 }
 
 // The 32 columns at `at` of `parts` parts, `step` apart, added in their order.  Bound by latency:
@@ -204,6 +206,19 @@ __device__ __forceinline__ void sum_parts(uint32_t (&sum)[32], const float4* at,
   }
 }
 
+// Shared memory by its address: through a pointer that was aligned as an integer these would be
+// generic, which take more of the bandwidth that the products' operands need.
+__device__ __forceinline__ float4 load_floats(uint32_t at) {
+  float4 f;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+               : "r"(at));
+  return f;
+}
+__device__ __forceinline__ void store_float(uint32_t at, float x) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
+
 template <int D, bool kDKDV>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_f0,
@@ -220,7 +235,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kBar + kTmemSlot);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Lay::kBar + kAbortSlot);
   volatile int* rank = reinterpret_cast<volatile int*>(smem + Lay::kBar + kRankSlot);
-  float* vec = reinterpret_cast<float*>(smem + Lay::kVec);
   const PackedRing ring{
       sbase + Lay::kRingOff,
       reinterpret_cast<volatile int(*)[8]>(smem + Lay::kRingOff + 2 * kRing * 8)};
@@ -234,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(bar(kFixFull), 1);
-    ptx::mbar_init(bar(kFixEmpty), 1);
+    ptx::mbar_init(bar(kFixEmpty), kDKDV ? 1 : kSoftmaxThreads + 1);
     for (int s = 0; s < Lay::kX0Slots; ++s) {
       ptx::mbar_init(bar(kX0Full + s), 1);
       ptx::mbar_init(bar(kX0Empty + s), 1);
@@ -244,18 +258,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(kX1Empty + s), 1);
     }
     ptx::mbar_init(bar(kSFull), 1);
-    ptx::mbar_init(bar(kSFull + 1), 1);
-    ptx::mbar_init(bar(kPReady), kSoftmaxThreads);
-    ptx::mbar_init(bar(kPReady + 1), kSoftmaxThreads);
-    ptx::mbar_init(bar(kSConsumed), kSoftmaxThreads);
-    ptx::mbar_init(bar(kAccFull), 1);
-    for (int b2 = 0; b2 < 2; ++b2) {
-      ptx::mbar_init(bar(kVecFull + b2), kT);
+    ptx::mbar_init(bar(kDPFull), 1);
+    for (int h = 0; h < 2; ++h) {
+      ptx::mbar_init(bar(kPReady + h), kSoftmaxThreads);
+      ptx::mbar_init(bar(kDSReady + h), kSoftmaxThreads);
+      ptx::mbar_init(bar(kVecFull + h), kT);
     }
     ptx::mbar_init(bar(kDFull), kT);
+    ptx::mbar_init(bar(kSRead), kSoftmaxThreads);
+    ptx::mbar_init(bar(kFixHeld), kSoftmaxThreads);
+    ptx::mbar_init(bar(kAccFull), 1);
     ptx::mbar_init(bar(kJoin), kSoftmaxThreads);
-    ptx::mbar_init(bar(kPReadyS), kSoftmaxThreads);
-    ptx::mbar_init(bar(kPReadyS + 1), kSoftmaxThreads);
     ptx::mbar_init(bar(kDrain), 1);
     ring.init(kSoftmaxThreads / 32);
     *abort_flag = 0u;
@@ -375,45 +388,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tA0 = tmem_base + 256, tA1 = tmem_base + 256 + D;
       uint32_t x_iter = 0, fix_iter = 0;
       bool ok = true;
-      // D_t = A B^T over the head dimension, both tiles K-major.
-      auto issue_ss = [&](uint32_t d_tmem, int a_off, int b_off) {
+      // d = A B^T over the head dimension.  kDKDV: both tiles K-major in shared memory (a_off its
+      // offset); kDQ: A's packed columns in TMEM from a_tmem on.
+      auto issue_scores = [&](uint32_t d_tmem, int a_off, uint32_t a_tmem, int b_off) {
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           const uint64_t step =
               static_cast<uint64_t>(((s >> 2) * Lay::kPanelBytes + (s & 3) * 32) >> 4);
-          ptx::mma_ss_w(d_tmem, d_k + (a_off >> 4) + step, d_k + (b_off >> 4) + step, kIdescS,
-                      s > 0 ? 1u : 0u);
+          if constexpr (kDKDV)
+            ptx::mma_ss_w(d_tmem, d_k + (a_off >> 4) + step, d_k + (b_off >> 4) + step, kIdescS,
+                          s > 0 ? 1u : 0u);
+          else
+            ptx::mma_ts_w(d_tmem, tmem_base + a_tmem + s * 8u, d_k + (b_off >> 4) + step, kIdescS,
+                          s > 0 ? 1u : 0u);
         }
       };
-      // acc (+)= A B: A = packed bf16 columns at a_tmem, in two halves
-      // `half` columns apart (64: the halves of S / dP; 32: contiguous),
-      // B = the streamed tile at b_off read MN-major (rows = K).
-      auto issue_ts = [&](uint32_t acc, uint32_t a_tmem, int b_off, bool first, int half,
-                          int steps) {
-        auto step = [&](int s) {
-          const uint32_t a_col = static_cast<uint32_t>((s >> 2) * half + (s & 3) * 8);
-          ptx::mma_ts_w(acc, a_tmem + a_col, d_mn + (b_off >> 4) + static_cast<uint64_t>(s * 128),
-                      kIdescG, (first && s == 0) ? 0u : 1u);
-        };
-        if (steps == kT / 16) {  // without a test between the products
-#pragma unroll
-          for (int s = 0; s < kT / 16; ++s) step(s);
-        } else {
-#pragma unroll 1
-          for (int s = 0; s < steps; ++s) step(s);
-        }
-      };
-      uint32_t n = 0;  // steps issued so far (all items), and (kDKDV) those of two halves
-      uint32_t n_two = 0;
-      // acc (+)= A B over 64 queries: A = the two warpgroups' packed pieces
-      // (32 columns apart), B = the half tile at b_off read MN-major.
-      auto issue_ts64 = [&](uint32_t acc, uint32_t a_tmem, int b_off, bool first, int steps) {
+      // acc (+)= A B over 64 streamed rows: A = the two warpgroups' packed pieces (32 columns
+      // apart), B = half of the streamed tile, at b_off, read MN-major (rows = K).
+      auto issue_half = [&](uint32_t acc, uint32_t a_tmem, int b_off, bool first, int steps) {
         auto step = [&](int s) {
           const uint32_t a_col = static_cast<uint32_t>((s >> 1) * 32 + (s & 1) * 8);
           ptx::mma_ts_w(acc, a_tmem + a_col, d_mn + (b_off >> 4) + static_cast<uint64_t>(s * 128),
                       kIdescG, (first && s == 0) ? 0u : 1u);
         };
-        if (steps >= 4) {
+        if (steps >= 4) {  // without a test between the products
 #pragma unroll
           for (int s = 0; s < 4; ++s) step(s);
         } else {
@@ -421,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int s = 0; s < steps; ++s) step(s);
         }
       };
+      uint32_t n = 0, n_two = 0;  // steps issued so far (all items), those of two halves
       for (;;) {
         // The producer publishes each item with its fixed tiles' load (and
         // the end of the work with a plain arrival), so this warp needs no
@@ -429,6 +428,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++fix_iter;
         const int k = *fix_item;
         if (k < 0) break;
+        if (!kDKDV) {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(kFixEmpty));
+          if (!wait_warp(bar(kFixHeld), (fix_iter - 1) & 1u, abort_flag, p)) { ok = false; break; }
+        }
         BItem it;
         decode_bitem<kDKDV>(p, ring.read(static_cast<uint32_t>(k)), it);
         ptx::tc_fence_after();
@@ -439,84 +443,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool ragged = kDKDV ? x_left < p.tq : last_rows < kT;
         const int last_steps = ragged ? (last_rows + 15) / 16 : kT / 16;
         const int last_zero = min(last_steps * 16, kDKDV ? packed_rows : kT);
-        if constexpr (!kDKDV) {
-          // S, dP of step n + 1 go out once the softmax has read those of
-          // step n; dQ += dS K of step n once its dS is in buffer n % 2.
-          bool have = false;  // S, dP of the current step already issued
-          // S, dP of streamed step x: K from X0 slot x % 3, V from X1 slot
-          // x % 2; V's slot is free once dP is done.
-          auto issue_step = [&](uint32_t x, bool last) -> bool {
-            const uint32_t s0 = x % Lay::kX0Slots, s1 = x % Lay::kX1Slots;
-            if (!wait_warp(bar(kX0Full + s0), (x / Lay::kX0Slots) & 1u, abort_flag, p)) return false;
-            if (!wait_warp(bar(kX1Full + s1), (x / Lay::kX1Slots) & 1u, abort_flag, p)) return false;
-            ptx::tc_fence_after();
-            if (last && ragged && last_rows < last_zero) {
-              zero_rows<Lay::kPanels>(sbase + Lay::x0(s0), last_rows, last_zero);
-              ptx::fence_proxy_async_shared();
-              __syncwarp();
-            }
-            issue_ss(tS, Lay::kF0, Lay::x0(s0));
-            issue_ss(tdP, Lay::kF1, Lay::x1(s1));
-            ptx::mma_commit_w(bar(kSFull));
-            ptx::mma_commit_w(bar(kX1Empty + s1));
-            return true;
-          };
-          for (int f = it.x_lo; f <= it.x_hi; ++f) {
-            if (!have) {
-              if (n > 0 && !wait_warp(bar(kSConsumed), (n - 1u) & 1u, abort_flag, p)) { ok = false; break; }
-              if (!issue_step(x_iter, f == it.x_hi)) { ok = false; break; }
-            }
-            have = false;
-            if (f < it.x_hi) {
-              if (!wait_warp(bar(kSConsumed), n & 1u, abort_flag, p)) { ok = false; break; }
-              if (!issue_step(x_iter + 1, f + 1 == it.x_hi)) { ok = false; break; }
-              have = true;
-            }
-            if (!wait_warp(bar(kPReady + (n & 1u)), (n >> 1) & 1u, abort_flag, p)) { ok = false; break; }
-            ptx::tc_fence_after();
-            const uint32_t s0 = x_iter % Lay::kX0Slots;
-            issue_ts(tA0, tmem_base + kDsBuf + (n & 1u) * 64u, Lay::x0(s0), f == it.x_lo, 32,
-                     f == it.x_hi ? last_steps : kT / 16);
-            ptx::mma_commit_w(bar(kX0Empty + s0));
-            ++n;
-            ++x_iter;
-          }
-          if (!ok) break;
-          ptx::mma_commit_w(bar(kFixEmpty));
-          ptx::mma_commit_w(bar(kAccFull));
-          continue;
-        }
-        // kDKDV: dV += P^T dO of a step and S^T of the next go out when its P^T is written, in two
-        // halves of 64 queries, dK += dS^T Q and the next dP^T when its dS^T is.  So the softmax
-        // forms dS^T during the first pair of products and the next P^T during the second.  P^T
-        // and dS^T lie where S^T and dP^T were, which the products' order keeps apart.
+        // A step's first product S; dV += P^T dO, when P^T is written; dQ += dS K or
+        // dK += dS^T Q, when dS is.  S of the next step goes out when S has been read and, where
+        // P^T lies in its place, dV is under way; dP of the next step behind dQ or dK, as dS lies in
+        // dP's place.  So the softmax forms dS during S (and dV) and the next P during dQ or dK and
+        // the next dP.  What is written in halves of 64 streamed rows enters its product so.
         // (The last tile's second half is left out where no row is in it.)
-        auto issue_s = [&](uint32_t x, bool last) -> bool {  // S^T = K Q^T
-          const uint32_t s0 = x % Lay::kX0Slots;
-          if (!wait_warp(bar(kX0Full + s0), (x / Lay::kX0Slots) & 1u, abort_flag, p)) return false;
+        auto loaded = [&](int full, int at, uint32_t round, bool zero) -> bool {
+          if (!wait_warp(bar(full), round & 1u, abort_flag, p)) return false;
           ptx::tc_fence_after();
-          if (last && ragged && last_rows < last_zero) {
-            zero_rows<Lay::kPanels>(sbase + Lay::x0(s0), last_rows, last_zero);
+          if (zero) {
+            zero_rows<Lay::kPanels>(sbase + at, last_rows, last_zero);
             ptx::fence_proxy_async_shared();
             __syncwarp();
           }
-          issue_ss(tS, Lay::kF0, Lay::x0(s0));
+          return true;
+        };
+        const bool zero_last = ragged && last_rows < last_zero;
+        auto issue_s = [&](uint32_t x, bool last) -> bool {
+          const uint32_t s0 = x % Lay::kX0Slots;
+          if (!loaded(kX0Full + s0, Lay::x0(s0), x / Lay::kX0Slots, last && zero_last)) return false;
+          issue_scores(tS, Lay::kF0, kHeldQ, Lay::x0(s0));
           ptx::mma_commit_w(bar(kSFull));
           return true;
         };
-        auto issue_dp = [&](uint32_t x, bool last) -> bool {  // dP^T = V dO^T
+        auto issue_dp = [&](uint32_t x, bool last) -> bool {
           const uint32_t s1 = x % Lay::kX1Slots;
-          if (!wait_warp(bar(kX1Full + s1), (x / Lay::kX1Slots) & 1u, abort_flag, p)) return false;
-          ptx::tc_fence_after();
-          if (last && ragged && last_rows < last_zero) {
-            zero_rows<Lay::kPanels>(sbase + Lay::x1(s1), last_rows, last_zero);
-            ptx::fence_proxy_async_shared();
-            __syncwarp();
-          }
-          issue_ss(tdP, Lay::kF1, Lay::x1(s1));
-          ptx::mma_commit_w(bar(kSFull + 1));
+          if (!loaded(kX1Full + s1, Lay::x1(s1), x / Lay::kX1Slots, kDKDV && last && zero_last))
+            return false;
+          issue_scores(tdP, Lay::kF1, kHeldG, Lay::x1(s1));
+          ptx::mma_commit_w(bar(kDPFull));
+          if (!kDKDV) ptx::mma_commit_w(bar(kX1Empty + s1));
           return true;
         };
+        if (!kDKDV && n > 0 && !wait_warp(bar(kSRead), (n - 1u) & 1u, abort_flag, p)) {
+          ok = false;
+          break;
+        }
         if (!issue_s(x_iter, it.x_lo == it.x_hi) || !issue_dp(x_iter, it.x_lo == it.x_hi)) {
           ok = false;
           break;
@@ -524,22 +487,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int f = it.x_lo; f <= it.x_hi; ++f) {
           const bool first = f == it.x_lo, last = f == it.x_hi;
           const int steps = last ? last_steps : kT / 16;
-          // acc += A B, A in the halves' order as they are written
           auto issue_g = [&](uint32_t acc, uint32_t a_tmem, int b_off, int ready) -> bool {
             if (!wait_warp(bar(ready), n & 1u, abort_flag, p)) return false;
             ptx::tc_fence_after();
-            issue_ts64(acc, a_tmem, b_off, first, steps);
+            issue_half(acc, a_tmem, b_off, first, steps);
             if (steps <= 4) return true;
             if (!wait_warp(bar(ready + 1), n_two & 1u, abort_flag, p)) return false;
             ptx::tc_fence_after();
-            issue_ts64(acc, a_tmem + 64u, b_off + 64 * 128, false, steps - 4);
+            issue_half(acc, a_tmem + 64u, b_off + 64 * 128, false, steps - 4);
             return true;
           };
           const uint32_t s0 = x_iter % Lay::kX0Slots, s1 = x_iter % Lay::kX1Slots;
-          if (!issue_g(tA0, tS, Lay::x1(s1), kPReady)) { ok = false; break; }
-          ptx::mma_commit_w(bar(kX1Empty + s1));
+          if constexpr (kDKDV) {
+            if (!issue_g(tA0, tS, Lay::x1(s1), kPReady)) { ok = false; break; }
+            ptx::mma_commit_w(bar(kX1Empty + s1));
+          } else {
+            if (!last && !wait_warp(bar(kSRead), n & 1u, abort_flag, p)) { ok = false; break; }
+          }
           if (!last && !issue_s(x_iter + 1, f + 1 == it.x_hi)) { ok = false; break; }
-          if (!issue_g(tA1, tdP, Lay::x0(s0), kPReadyS)) { ok = false; break; }
+          if (!issue_g(kDKDV ? tA1 : tA0, tdP, Lay::x0(s0), kDSReady)) { ok = false; break; }
           ptx::mma_commit_w(bar(kX0Empty + s0));
           if (!last && !issue_dp(x_iter + 1, f + 1 == it.x_hi)) { ok = false; break; }
           ++n;
@@ -547,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++x_iter;
         }
         if (!ok) break;
-        ptx::mma_commit_w(bar(kFixEmpty));
+        if (kDKDV) ptx::mma_commit_w(bar(kFixEmpty));
         ptx::mma_commit_w(bar(kAccFull));
       }
       // Wait until every MMA this warp issued has finished.
@@ -558,14 +524,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     ptx::setmaxnreg_inc<kSoftmaxRegs>();
     // ------------------------------------------------------------ softmax
-    const int wg = warp >> 2;        // column half of this warpgroup
+    const int wg = warp >> 2;        // this warpgroup has 32 columns of each half
     const int wq = warp & 3;         // TMEM lane quarter
     const int row_in_tile = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem_base + lane_off;
     const uint32_t tdP = tS + 128;
     const uint32_t tA0 = tS + 256, tA1 = tS + 256 + D;
-    const int col0 = wg * 64;
     const float sc = p.scale_log2;
     // token and head of a packed tile's row: this thread's in kDQ; in kDKDV that of the column
     // whose constants it loads
@@ -589,22 +554,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seen = !row_valid ? INT_MAX / 2 : p.causal ? token + 1 : it.len;  // kDQ: keys
       const int from = kDKDV && row_valid && p.causal ? token : 0;  // kDKDV: the first query
       float lse2_r = 0.f, d_r = 0.f;     // kDQ: per-row constants
+      if (!kDKDV) {
+        // Q (the first warpgroup) and dO (the second) to TMEM, from where the products take them
+        // without reading shared memory again.
+        if (!wait_warp(bar(kFixFull), item_cnt & 1u, abort_flag, p)) { ok = false; break; }
+        const uint32_t from = sbase + (wg ? Lay::kF1 : Lay::kF0) + row_in_tile * 128;
+#pragma unroll
+        for (int pn = 0; pn < Lay::kPanels; ++pn) {
+          uint32_t x[32];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[4 * c]), "=r"(x[4 * c + 1]), "=r"(x[4 * c + 2]),
+                           "=r"(x[4 * c + 3])
+                         : "r"(from + pn * Lay::kPanelBytes + ((c ^ (row_in_tile & 7)) << 4)));
+          ptx::tmem_st32(tS + (wg ? kHeldG : kHeldQ) + pn * 32, x);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(kFixHeld));
+        ptx::mbar_arrive(bar(kFixEmpty));
+      }
       if (!kDKDV && row_valid) {
         lse2_r = __ldg(p.lse + static_cast<size_t>(head) * p.T + row) * kLog2e;
         d_r = p.delta[row * p.Hq + head];
       }
-      // kDKDV: -lse2 and -D of this thread's row of a streamed tile.  Rows behind the tile's last:
-      // P = 2^-inf = 0 where the scores are finite.
-      float nl_next = 0.f, nd_next = 0.f;
+      // kDKDV: lse and D of this thread's row of the next streamed tile, as loaded: arithmetic
+      // here would wait for them.  Rows behind the tile's last: P = 2^-inf = 0 where the scores
+      // are finite.
+      float lse_next = INFINITY, d_next = 0.f;
       auto load_constants = [&](int f) {
-        nl_next = -INFINITY;
-        nd_next = 0.f;
+        lse_next = INFINITY;
+        d_next = 0.f;
         const int t = f * x_tokens + my_token;
         if (threadIdx.x < kT && f <= it.x_hi && my_token < p.tq && t < it.len) {
           const size_t q = static_cast<size_t>(it.row0) + t;
           const int h = it.hk * p.G + my_head;
-          nl_next = -__ldg(p.lse + static_cast<size_t>(h) * p.T + q) * kLog2e;
-          nd_next = -p.delta[q * p.Hq + h];
+          lse_next = __ldg(p.lse + static_cast<size_t>(h) * p.T + q);
+          d_next = p.delta[q * p.Hq + h];
         }
       };
       if (kDKDV) load_constants(it.x_lo);
@@ -615,85 +602,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         // and dO, which need no mask (their P is 0 by their constant).
         const int c_lo = kDKDV ? max(from - xs, 0) * p.G : 0;
         const int c_hi = kDKDV ? (tokens == x_tokens ? kT : tokens * p.G) - 1 : seen - xs - 1;
-        if constexpr (!kDKDV) {
-          const uint32_t n = s_cnt;
-          if (!wait_warp(bar(kSFull), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
-          ++s_cnt;
-          ptx::tc_fence_after();
-          // Read all of this half of S and dP, release them for the next
-          // step's products, then form dS into buffer n % 2.
-          uint32_t sv[2][32], dv[2][32];
+        const bool two = kDKDV ? f != it.x_hi || tokens == x_tokens || tokens * p.G > 64
+                               : tokens > 64;  // halves
+        uint32_t columns[2];
+        bool masked[2];
 #pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            ptx::tmem_ld32(tS + col0 + ch * 32, sv[ch]);
-            ptx::tmem_ld32(tdP + col0 + ch * 32, dv[ch]);
-          }
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            ptx::reg_fence(sv[ch]);
-            ptx::reg_fence(dv[ch]);
-          }
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(bar(kSConsumed));
-#pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            const int c0 = col0 + ch * 32;
-            uint32_t pk_s[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {  // paired fp32
-              float e0, e1, g0, g1;
-              ptx::fma_f32x2(e0, e1, __uint_as_float(sv[ch][2 * x]), __uint_as_float(sv[ch][2 * x + 1]),
-                             sc, sc, -lse2_r, -lse2_r);
-              const float p0 = ptx::ex2(e0), p1 = ptx::ex2(e1);
-              ptx::fma_f32x2(g0, g1, __uint_as_float(dv[ch][2 * x]), __uint_as_float(dv[ch][2 * x + 1]),
-                             1.f, 1.f, -d_r, -d_r);
-              ptx::fma_f32x2(g0, g1, p0, p1, g0, g1, 0.f, 0.f);
-              pk_s[x] = ptx::pack_bf16(g0, g1);
-            }
-            if (__any_sync(0xffffffffu, c_lo > c0 || c_hi < c0 + 31))
-              keep_pairs(pk_s, seen_columns(c_lo - c0, c_hi - c0));
-            ptx::tmem_st16(tmem_base + lane_off + kDsBuf + (n & 1u) * 64u + c0 / 2, pk_s);
-          }
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(bar(kPReady + (n & 1u)));
-          continue;
+        for (int h = 0; h < 2; ++h) {
+          const int c0 = 64 * h + 32 * wg;
+          masked[h] = __any_sync(0xffffffffu, c_lo > c0 || c_hi < c0 + 31);
+          columns[h] = seen_columns(c_lo - c0, c_hi - c0);
         }
-        // Per-column constants of the streamed query tile, shared by all rows: warps 0-3 write
+        // Per-column constants of a streamed query tile, shared by all rows: warps 0-3 write
         // them, having loaded them a tile ahead.  Nobody still reads the buffers: a thread that
-        // has seen S^T of step n - 1 (this loop's last turn) knows that all have formed P^T of
-        // step n - 2, one that has seen dP^T of step n that all have formed dS^T of step n - 1.
-        const float nd = nd_next;
-        float* const lse_vec = vec + (s_cnt & 1u) * kT;
-        if (threadIdx.x < kT) {
-          lse_vec[threadIdx.x] = nl_next;
-          ptx::mbar_arrive(bar(kVecFull + (s_cnt & 1u)));
-          load_constants(f + 1);
-        }
-        const bool two = f != it.x_hi || tokens == x_tokens || tokens * p.G > 64;  // halves
-        if (!wait_warp(bar(kVecFull + (s_cnt & 1u)), (s_cnt >> 1) & 1u, abort_flag, p)) {
-          ok = false;
-          break;
+        // has seen S of step n - 1 (this loop's last turn) knows that all have formed P of
+        // step n - 2, one that has seen dP of step n that all have formed dS of step n - 1.
+        const uint32_t lse_vec = sbase + Lay::kVec + (s_cnt & 1u) * kT * 4;
+        const uint32_t d_vec = sbase + Lay::kVec + 2 * kT * 4;
+        float d_of_row = 0.f;
+        if (kDKDV) {
+          d_of_row = -d_next;
+          if (threadIdx.x < kT) {
+            store_float(lse_vec + threadIdx.x * 4, -lse_next * kLog2e);
+            ptx::mbar_arrive(bar(kVecFull + (s_cnt & 1u)));
+            load_constants(f + 1);
+          }
+          if (!wait_warp(bar(kVecFull + (s_cnt & 1u)), (s_cnt >> 1) & 1u, abort_flag, p)) {
+            ok = false;
+            break;
+          }
         }
         if (!wait_warp(bar(kSFull), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
         ptx::tc_fence_after();
-        // This warpgroup's 32 columns of each half.  P stays in fp32 for dS.
-        uint32_t pv[2][32];
+        uint32_t pv[2][32];  // S, then P, which stays in fp32 for dS
         ptx::tmem_ld32(tS + 32 * wg, pv[0]);
         ptx::tmem_ld32(tS + 32 * wg + 64, pv[1]);
         ptx::tmem_wait_ld();
         ptx::reg_fence(pv[0]);
         ptx::reg_fence(pv[1]);
+        if (!kDKDV) {
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(kSRead));
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h == 1 && !two) break;
           const int c0 = 64 * h + 32 * wg;
-          const float4* const nl4 = reinterpret_cast<const float4*>(lse_vec + c0);
           uint32_t pk[16];
 #pragma unroll
           for (int x4 = 0; x4 < 8; ++x4) {  // paired fp32
-            const float4 nl = nl4[x4];
+            const float4 nl =
+                kDKDV ? load_floats(lse_vec + (c0 + 4 * x4) * 4) : make_float4(-lse2_r, -lse2_r, -lse2_r, -lse2_r);
             const float nla[4] = {nl.x, nl.y, nl.z, nl.w};
 #pragma unroll
             for (int hx = 0; hx < 2; ++hx) {
@@ -706,28 +664,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               e1 = ptx::ex2(e1);
               pv[h][2 * x] = __float_as_uint(e0);
               pv[h][2 * x + 1] = __float_as_uint(e1);
-              pk[x] = ptx::pack_bf16(e0, e1);
+              if (kDKDV) pk[x] = ptx::pack_bf16(e0, e1);
             }
           }
-          if (__any_sync(0xffffffffu, c_lo > c0 || c_hi < c0 + 31))
-            keep_pairs(pk, seen_columns(c_lo - c0, c_hi - c0));
-          ptx::tmem_st16(tS + c0, pk);
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(bar(kPReady + h));
+          if constexpr (kDKDV) {
+            if (masked[h]) keep_columns(pv[h], pk, columns[h]);
+            ptx::tmem_st16(tS + c0, pk);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(kPReady + h));
+          }
         }
-        // dS^T = P^T (dP^T - D)
-        float* const d_vec = vec + 2 * kT;
-        if (!wait_warp(bar(kSFull + 1), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
+        // dS = P (dP - D)
+        if (!wait_warp(bar(kDPFull), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
         ptx::tc_fence_after();
-        if (threadIdx.x < kT) {
-          d_vec[threadIdx.x] = nd;
+        if (kDKDV && threadIdx.x < kT) {
+          store_float(d_vec + threadIdx.x * 4, d_of_row);
           ptx::mbar_arrive(bar(kDFull));
         }
         uint32_t dv[2][32];
         ptx::tmem_ld32(tdP + 32 * wg, dv[0]);
         ptx::tmem_ld32(tdP + 32 * wg + 64, dv[1]);
-        if (!wait_warp(bar(kDFull), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
+        if (kDKDV && !wait_warp(bar(kDFull), s_cnt & 1u, abort_flag, p)) { ok = false; break; }
         ptx::tmem_wait_ld();
         ptx::reg_fence(dv[0]);
         ptx::reg_fence(dv[1]);
@@ -735,12 +693,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 2; ++h) {
           if (h == 1 && !two) break;
           const int c0 = 64 * h + 32 * wg;
-          const float4* const nd4 = reinterpret_cast<const float4*>(d_vec + c0);
           uint32_t pk[16];
 #pragma unroll
           for (int x4 = 0; x4 < 8; ++x4) {
-            const float4 nd_c = nd4[x4];
-            const float nda[4] = {nd_c.x, nd_c.y, nd_c.z, nd_c.w};
+            const float4 nd = kDKDV ? load_floats(d_vec + (c0 + 4 * x4) * 4)
+                                    : make_float4(-d_r, -d_r, -d_r, -d_r);
+            const float nda[4] = {nd.x, nd.y, nd.z, nd.w};
 #pragma unroll
             for (int hx = 0; hx < 2; ++hx) {
               const int x = 2 * x4 + hx;
@@ -750,15 +708,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                              nda[2 * hx + 1]);
               ptx::fma_f32x2(g0, g1, __uint_as_float(pv[h][2 * x]),
                              __uint_as_float(pv[h][2 * x + 1]), g0, g1, 0.f, 0.f);
+              dv[h][2 * x] = __float_as_uint(g0);
+              dv[h][2 * x + 1] = __float_as_uint(g1);
               pk[x] = ptx::pack_bf16(g0, g1);
             }
           }
-          if (__any_sync(0xffffffffu, c_lo > c0 || c_hi < c0 + 31))
-            keep_pairs(pk, seen_columns(c_lo - c0, c_hi - c0));
+          if (masked[h]) keep_columns(dv[h], pk, columns[h]);
           ptx::tmem_st16(tdP + c0, pk);
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
-          ptx::mbar_arrive(bar(kPReadyS + h));
+          ptx::mbar_arrive(bar(kDSReady + h));
         }
         ++s_cnt;
       }
