@@ -153,12 +153,13 @@ struct PackedRing {
   }
   // (Every lane of a warp.  The shuffle tells the compiler that the item is one for the warp, so
   // that the loops over its tiles are the warp's and not each lane's.)
+  __device__ static PackedEntry uniform(const PackedEntry& x) {
+    auto all = [](int y) { return __shfl_sync(0xffffffffu, y, 0); };
+    return PackedEntry{make_int4(all(x.e.x), all(x.e.y), all(x.e.z), all(x.e.w)), all(x.hk)};
+  }
   __device__ PackedEntry read(uint32_t k) const {
     const volatile int* const from = slots[k % kRing];
-    int x[5];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) x[i] = __shfl_sync(0xffffffffu, from[i], 0);
-    return PackedEntry{make_int4(x[0], x[1], x[2], x[3]), x[4]};
+    return uniform(PackedEntry{make_int4(from[0], from[1], from[2], from[3]), from[4]});
   }
   // A softmax warp (every lane): the k-th item; false if the wait gave up.
   template <class P>

@@ -71,7 +71,7 @@ struct BLayout {
 
 enum BBar : int {
   kFixFull = 0,
-  kFixEmpty = 1,   // (kDQ: every softmax thread and the MMA warp have read the item's)
+  kFixEmpty = 1,   // kDKDV: their last products are done; kDQ: they are in TMEM
   kX0Full = 2,     // + slot (3)
   kX1Full = 5,     // + slot (2)
   kX0Empty = 7,    // + slot (3)
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(bar(kFixFull), 1);
-    ptx::mbar_init(bar(kFixEmpty), kDKDV ? 1 : kSoftmaxThreads + 1);
+    ptx::mbar_init(bar(kFixEmpty), kDKDV ? 1 : kSoftmaxThreads + 1);  // and the MMA warp
     for (int s = 0; s < Lay::kX0Slots; ++s) {
       ptx::mbar_init(bar(kX0Full + s), 1);
       ptx::mbar_init(bar(kX0Empty + s), 1);
@@ -448,6 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P^T lies in its place, dV is under way; dP of the next step behind dQ or dK, as dS lies in
         // dP's place.  So the softmax forms dS during S (and dV) and the next P during dQ or dK and
         // the next dP.  What is written in halves of 64 streamed rows enters its product so.
+        // (Measured for kDQ, 16K tokens of 16/4 heads, in the kernel: 962 us, 73 % of the tensor
+        // pipe; dS in a place of its own, so that dP need not wait for dQ, and dO for that in
+        // shared memory: 1044.)
         // (The last tile's second half is left out where no row is in it.)
         auto loaded = [&](int full, int at, uint32_t round, bool zero) -> bool {
           if (!wait_warp(bar(full), round & 1u, abort_flag, p)) return false;
@@ -499,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           const uint32_t s0 = x_iter % Lay::kX0Slots, s1 = x_iter % Lay::kX1Slots;
           if constexpr (kDKDV) {
+            if (last) ptx::mma_commit_w(bar(kFixEmpty));  // every S^T and dP^T is under way
             if (!issue_g(tA0, tS, Lay::x1(s1), kPReady)) { ok = false; break; }
             ptx::mma_commit_w(bar(kX1Empty + s1));
           } else {
@@ -513,7 +517,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++x_iter;
         }
         if (!ok) break;
-        if (kDKDV) ptx::mma_commit_w(bar(kFixEmpty));
         ptx::mma_commit_w(bar(kAccFull));
       }
       // Wait until every MMA this warp issued has finished.
@@ -538,9 +541,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_token = packed_row / p.G, my_head = packed_row - my_token * p.G;
     uint32_t s_cnt = 0, item_cnt = 0, join_cnt = 0;
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      PackedEntry entry;
-      if (!ring.get(static_cast<uint32_t>(k), entry, abort_flag, p)) { ok = false; break; }
+    // lse and D as loaded (arithmetic on them would wait for them): kDQ: of this thread's row;
+    // kDKDV: of its row of the next streamed tile.  Rows behind that tile's last: P = 2^-inf = 0
+    // where the scores are finite.
+    float lse_next = 0.f, d_next = 0.f;
+    auto load_constants = [&](const BItem& it, int token, bool there, float lse_else) {
+      lse_next = lse_else;
+      d_next = 0.f;
+      if (there) {
+        const size_t q = static_cast<size_t>(it.row0) + token;
+        const int h = it.hk * p.G + my_head;
+        lse_next = __ldg(p.lse + static_cast<size_t>(h) * p.T + q);
+        d_next = p.delta[q * p.Hq + h];
+      }
+    };
+    auto load_columns = [&](const BItem& it, int f) {
+      const int t = f * x_tokens + my_token;
+      load_constants(it, t, threadIdx.x < kT && f <= it.x_hi && my_token < p.tq && t < it.len,
+                     INFINITY);
+    };
+    // kDQ: the k-th item, and what its start waits for: its rows' constants, and Q (by the first
+    // warpgroup) and dO (by the second) in TMEM, from where the products take them without
+    // reading shared memory again.  Of the item before every product but its last dQ is done.
+    PackedEntry entry{make_int4(0, 0, 0, 0), -1};
+    auto prepare = [&](uint32_t k) -> bool {
+      if (!ring.get(k, entry, abort_flag, p)) return false;
+      if (entry.hk < 0) return true;
+      BItem it;
+      decode_bitem<kDKDV>(p, entry, it);
+      load_constants(it, it.t0 + my_token, my_token < it.tokens, 0.f);
+      if (!wait_warp(bar(kFixFull), k & 1u, abort_flag, p)) return false;
+      const uint32_t row = sbase + (wg ? Lay::kF1 : Lay::kF0) + row_in_tile * 128;
+#pragma unroll
+      for (int pn = 0; pn < Lay::kPanels; ++pn) {
+        uint32_t x[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[4 * c]), "=r"(x[4 * c + 1]), "=r"(x[4 * c + 2]),
+                         "=r"(x[4 * c + 3])
+                       : "r"(row + pn * Lay::kPanelBytes + ((c ^ (row_in_tile & 7)) << 4)));
+        ptx::tmem_st32(tS + (wg ? kHeldG : kHeldQ) + pn * 32, x);
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(bar(kFixHeld));
+      ptx::mbar_arrive(bar(kFixEmpty));
+      return true;
+    };
+    if constexpr (!kDKDV) ok = prepare(0);
+    for (uint32_t k = 0; ok; ++k) {
+      if constexpr (kDKDV) {
+        if (!ring.get(k, entry, abort_flag, p)) { ok = false; break; }
+      } else {
+        entry = PackedRing::uniform(entry);
+      }
       if (entry.hk < 0) break;
       BItem it;
       decode_bitem<kDKDV>(p, entry, it);
@@ -553,48 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int head = kDKDV ? it.hk : it.hk * p.G + my_head;
       const int seen = !row_valid ? INT_MAX / 2 : p.causal ? token + 1 : it.len;  // kDQ: keys
       const int from = kDKDV && row_valid && p.causal ? token : 0;  // kDKDV: the first query
-      float lse2_r = 0.f, d_r = 0.f;     // kDQ: per-row constants
-      if (!kDKDV) {
-        // Q (the first warpgroup) and dO (the second) to TMEM, from where the products take them
-        // without reading shared memory again.
-        if (!wait_warp(bar(kFixFull), item_cnt & 1u, abort_flag, p)) { ok = false; break; }
-        const uint32_t from = sbase + (wg ? Lay::kF1 : Lay::kF0) + row_in_tile * 128;
-#pragma unroll
-        for (int pn = 0; pn < Lay::kPanels; ++pn) {
-          uint32_t x[32];
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x[4 * c]), "=r"(x[4 * c + 1]), "=r"(x[4 * c + 2]),
-                           "=r"(x[4 * c + 3])
-                         : "r"(from + pn * Lay::kPanelBytes + ((c ^ (row_in_tile & 7)) << 4)));
-          ptx::tmem_st32(tS + (wg ? kHeldG : kHeldQ) + pn * 32, x);
-        }
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(bar(kFixHeld));
-        ptx::mbar_arrive(bar(kFixEmpty));
-      }
-      if (!kDKDV && row_valid) {
-        lse2_r = __ldg(p.lse + static_cast<size_t>(head) * p.T + row) * kLog2e;
-        d_r = p.delta[row * p.Hq + head];
-      }
-      // kDKDV: lse and D of this thread's row of the next streamed tile, as loaded: arithmetic
-      // here would wait for them.  Rows behind the tile's last: P = 2^-inf = 0 where the scores
-      // are finite.
-      float lse_next = INFINITY, d_next = 0.f;
-      auto load_constants = [&](int f) {
-        lse_next = INFINITY;
-        d_next = 0.f;
-        const int t = f * x_tokens + my_token;
-        if (threadIdx.x < kT && f <= it.x_hi && my_token < p.tq && t < it.len) {
-          const size_t q = static_cast<size_t>(it.row0) + t;
-          const int h = it.hk * p.G + my_head;
-          lse_next = __ldg(p.lse + static_cast<size_t>(h) * p.T + q);
-          d_next = p.delta[q * p.Hq + h];
-        }
-      };
-      if (kDKDV) load_constants(it.x_lo);
+      const float lse2_r = lse_next * kLog2e, d_r = d_next;  // kDQ
+      if (kDKDV) load_columns(it, it.x_lo);
       for (int f = it.x_lo; f <= it.x_hi; ++f) {
         const int xs = f * x_tokens;  // first streamed token
         const int tokens = min(x_tokens, it.len - xs);
@@ -624,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (threadIdx.x < kT) {
             store_float(lse_vec + threadIdx.x * 4, -lse_next * kLog2e);
             ptx::mbar_arrive(bar(kVecFull + (s_cnt & 1u)));
-            load_constants(f + 1);
+            load_columns(it, f + 1);
           }
           if (!wait_warp(bar(kVecFull + (s_cnt & 1u)), (s_cnt >> 1) & 1u, abort_flag, p)) {
             ok = false;
@@ -723,6 +738,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
+      if constexpr (!kDKDV) {  // before the wait, so that the next item's first products start
+        if (!prepare(k + 1)) { ok = false; break; }
+      }
       if (!wait_warp(bar(kAccFull), item_cnt & 1u, abort_flag, p)) { ok = false; break; }
       ++item_cnt;
       ptx::tc_fence_after();
