@@ -5,13 +5,24 @@
 //   D = rowsum(dO * O);  dP = dO V^T;  dS = P * (dP - D);
 //   dV = P^T dO;  dK = dS^T Q / sqrt(d);  dQ = dS K / sqrt(d)
 // ("上下文並行（Context Parallelism, CP）", compassingai.com, section 反向傳播), the sums of a key
-// head's dK and dV running over the G query heads that read it.  Two kernels as in
-// attn_bwd_sm103.cu, where the CTA's roles and its use of TMEM are described:
+// head's dK and dV running over the G query heads that read it.  Two kernels, with the CTA's roles as
+// attn_bwd_sm103.cu describes them:
 //   kDKDV  a CTA owns a 128-key tile of one key head and walks the packed query tiles
 //          (packed.cuh) that see it: G heads' rows are neighbours in the products' inner
 //          dimension, so a shared head's gradients are summed in the accumulators.
 //   kDQ    a CTA owns a packed query tile and walks the key tiles it sees.
 // Every output is finished by one CTA: no atomics.
+//
+// The seven products of a tile pair (two of them twice) are 7 / 5 of the formulas' operations:
+// one kernel for all five would add dQ up over CTAs, by atomics in the order of arrival or through
+// memory.  Bound by shared memory beside the tensor pipe: S^T and dP^T read both operands there at
+// its full rate (128 bytes a clock), and the copies, dV's and dK's tiles and the constants come on
+// top, 2560 clocks a tile pair for 2048 of products in kDKDV.  kDQ's fixed operands are therefore
+// in TMEM; kDKDV has no columns left for its.  Measured (16K tokens of 16/4 heads, d = 128, in the
+// kernels): kDKDV 1470 us, 68 % of the tensor pipe, kDQ 970, 73 %; with S^T and dP^T in halves of
+// 64 queries, two in flight, kDKDV took 1830, and with constants read by generic loads 1570.
+// P and dS are rounded to bf16 for their products, as the ring's backward rounds them: 2.5e-3 to
+// 3.0e-3 of the gradients against 64 bits (relative in the norm), 1.7e-3 of it the outputs' own.
 //
 // Rows that are not there (behind a sequence, behind tq G) may hold anything.  Where they are
 // summed over - Q and dO in kDKDV, K in kDQ - they are zeroed in shared memory up to the next
@@ -308,18 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t x_iter = 0, fix_iter = 0;
       uint32_t armed0[3] = {0u, 0u, 0u}, armed1[2] = {0u, 0u};  // loads started per slot
       int ahead = 0;  // the claim of the CTA's next item
-      // kDQ claims it when this item's loads are under way (see packed_fwd_sm103.cu), kDKDV when
-      // this item starts: its CTAs then end one by one and make room for dQ's, which start with
-      // the most expensive items.  Measured for kDKDV, at the start / late (us a call): 8192
-      // tokens of 8/2 heads 413 / 447, 20000 of 1/1 272 / 295, 5000 + 2500 of 16/2 389 / 426; but
-      // 3000 + 200 + 100 of 32/8 268 / 250, 9000 of 4/4 (d = 64) 225 / 213.
-      constexpr bool early = kDKDV;
       bool dropped = false;
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int w = k == 0 ? static_cast<int>(blockIdx.x) : ahead;
         const PackedEntry entry = order.at(p.items, w);
-        if (early && entry.hk >= 0) ahead = packed_claim(p.head, gridDim.x);
         if (!ring.put(static_cast<uint32_t>(k), entry, abort_flag, p)) { ok = false; break; }
         if (entry.hk < 0) break;
         BItem it;
@@ -359,7 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++armed1[s1];
           ++x_iter;
         }
-        if (!early) ahead = packed_claim(p.head, gridDim.x);
+        // The next item is claimed once this one's loads are under way (see packed_fwd_sm103.cu).
+        // Measured for kDKDV, so / when this item starts (us a call): 3000 + 200 + 100 tokens of
+        // 32/8 heads 219 / 252, 6000 of 16/2 359 / 374, 8 x 2048 of 32/8 781 / 790, 9000 of 4/4
+        // (d = 64) 179 / 186; but 8192 of 8/2 375 / 342, 20000 of 1/1 (d = 64) 257 / 237.
+        ahead = packed_claim(p.head, gridDim.x);
       }
       // No more items: tell the MMA warp through the next phase of kFixFull.
       if (ok && wait1(bar(kFixEmpty), (fix_iter & 1u) ^ 1u, abort_flag, p)) {
@@ -448,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P^T lies in its place, dV is under way; dP of the next step behind dQ or dK, as dS lies in
         // dP's place.  So the softmax forms dS during S (and dV) and the next P during dQ or dK and
         // the next dP.  What is written in halves of 64 streamed rows enters its product so.
-        // (Measured for kDQ, 16K tokens of 16/4 heads, in the kernel: 962 us, 73 % of the tensor
+        // (Measured for kDQ, 16K tokens of 16/4 heads, in the kernel: 970 us, 73 % of the tensor
         // pipe; dS in a place of its own, so that dP need not wait for dQ, and dO for that in
         // shared memory: 1044.)
         // (The last tile's second half is left out where no row is in it.)

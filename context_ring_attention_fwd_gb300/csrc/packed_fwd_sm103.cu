@@ -14,6 +14,14 @@
 // multiple of 16 keys, and the up to 15 rows of V beyond the last key are zeroed in
 // shared memory first.  K needs none: its rows are columns of S, which the mask replaces.
 //
+// Bound by the tensor pipe where sequences are long: 32K tokens of 8/2 heads, 2.2 TFLOP, 1210 us, 95 %
+// of the cuBLAS rate (80 % of the pipe's cycles); a run of seconds, at the clock that the power cap
+// leaves, 1410.  In short ones by what an item costs besides its tiles, about 2.5 us (its first S,
+// its rows' way out): 14
+// prompts of up to 2000 tokens, 32/8 heads, 109 GFLOP: 100 us, 54 % of the pipe's cycles.  P is rounded to
+// bf16 for its product, as in the ring's forward, which costs about as much as the output's own
+// rounding (2.0e-3 to 2.2e-3 against 64 bits, relative in the norm, where that alone makes 1.7e-3).
+//
 // Items that see many keys in a call of few are cut along them (packed_plan.cu): a part leaves its
 // (O, m, l) in a slot, and the last to end of a query tile's parts joins them by the online
 // merge of cp_lse_merge, in the parts' order.
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // O_t (+)= P_t V over the steps [part * 4, part * 4 + 4): keys 0-63 (part 0) or 64-127 (part
     // 1), whose P the softmax signals separately.  kWhole: all of them; otherwise those below
     // `steps`.  (A test between the products would hold this warp's issue up: with one in every
-    // step the kernel took 1769 us instead of 1479 for 32K tokens of 8/2 heads.)
+    // step the kernel took 1769 us instead of 1287 for 32K tokens of 8/2 heads.)
     auto issue_pv = [&](auto whole, int t, uint32_t st, bool first, int part, int steps) {
       const uint64_t dv = d_v + ((Lay::kVOff + st * Lay::kTileBytes) >> 4);
       auto step = [&](int s) {

@@ -166,8 +166,9 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   // start, its sums' way through memory, their addition), so parts are as many as CTAs where
   // the share is small, 1.3 of it, and down to 0.6 of it where it is large; they are no
   // shorter than kLeastPart, and items of up to kLeastCut stay whole.  Measured for the backward's
-  // key tiles, whole / cut (us a call): 4096 tokens of 8/1 heads 524 / 137, 8192 of 8/2 557 /
-  // 403, 1500 of 2/1 65 / 37; 200 of 16/4 (7 streamed tiles) 31 / 39, which stays whole.
+  // key tiles, whole / cut (us a call): 4096 tokens of 8/1 heads 409 / 131, 8192 of 8/2 622 /
+  // 342, 5000 + 2500 of 16/2 720 / 339, 1500 of 2/1 50 / 35, 20000 of 1/1 (d = 64) 236 / 237; 200
+  // of 16/4 (7 streamed tiles) 25 / 25, which stays whole.
   int chunk = INT_MAX;
   auto parts_of = [&](const int4& it) {
     const int n = streamed_tiles(p, l, it);

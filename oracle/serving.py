@@ -1,7 +1,7 @@
 """fp64 numpy oracle of the operators around the attention: the per-head norm
 and rotation of queries and keys with its gradient, the append to a paged
-cache, decode attention over such a cache, and what a cache in 4 bits holds.  Written row by row from the
-definitions; shares no code with the CUDA library."""
+cache, decode attention over such a cache, and what a cache in 4 bits holds.
+Written row by row from the definitions; shares no code with the CUDA library."""
 from __future__ import annotations
 
 import numpy as np
@@ -114,7 +114,8 @@ def quantise4(x, descale=None):
     scales = e4m3_codes((np.abs(y).max(-1) * (f(1) / f(7))).astype(np.float64))
     s = e4m3_values()[scales][..., None]
     q = np.divide(y, s.astype(f), out=np.zeros_like(y), where=s > 0)
-    n = (np.clip(np.rint(np.nan_to_num(q, nan=0.0, posinf=7, neginf=-7)), -7, 7) + 8).astype(np.uint8).reshape(*y.shape[:-2], -1)
+    n = np.clip(np.rint(np.nan_to_num(q, nan=0.0, posinf=7, neginf=-7)), -7, 7) + 8
+    n = n.astype(np.uint8).reshape(*y.shape[:-2], -1)
     return n[..., ::2] | n[..., 1::2] << 4, scales
 
 
