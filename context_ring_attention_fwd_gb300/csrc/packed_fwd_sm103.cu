@@ -70,10 +70,10 @@ struct Layout {
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + kQTiles * kTileBytes;
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
-  static constexpr int kBarOff = kVOff + kStages * kTileBytes;
+  static constexpr int kStageOff = kVOff + kStages * kTileBytes;  // the softmax warps' rows on
+  static constexpr int kBarOff = kStageOff + kSoftmaxWarps * kRowStage;  // their way out
   static constexpr int kRingOff = kBarOff + 256;  // the item ring
-  static constexpr int kStageOff = kRingOff + 256;  // the softmax warps' rows on their way out
-  static constexpr int kBytes = kStageOff + kSoftmaxWarps * kRowStage;
+  static constexpr int kBytes = kRingOff + 256;
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024 B
 };
 
@@ -104,6 +104,7 @@ struct FwdParams {
   int n_seqs;
   int T, Hq, Hk, G;
   int tq;              // tokens of a packed tile
+  int warp_tokens;     // of a warp's 32 rows; 0: they hold a part of a token
   int causal;
   float scale_log2;    // log2(e) / sqrt(d)
   __nv_bfloat16* out;  // [T, Hq, d]
@@ -232,7 +233,8 @@ template <int D, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
                       const __grid_constant__ CUtensorMap tmap_k,
-                      const __grid_constant__ CUtensorMap tmap_v, const FwdParams p) {
+                      const __grid_constant__ CUtensorMap tmap_v,
+                      const __grid_constant__ CUtensorMap tmap_o, const FwdParams p) {
   using Lay = Layout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -332,6 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t st = kv_iter % kStages;
           const uint32_t ph = (kv_iter / kStages) & 1u;
           const int row = it.row0 + f * kBN;
+          // The next item is claimed when the last loads but one are under way, not before: a CTA
+          // at its start would take one that another is free for sooner; and not behind the last,
+          // where the answer would be waited for.
+          if (f == max(it.first, last - 1) && !p.offsets) ahead = packed_claim(p.head, gridDim.x);
           if (!wait1(bar(kKEmpty + st), ph ^ 1u, abort_flag, p)) { ok = false; break; }
           if (p.fault_drop_k && blockIdx.x == 0 && !dropped) {
             // Test hook: this K tile is never loaded, so the MMA warp's
@@ -354,9 +360,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (st == 0) ++v_armed0; else ++v_armed1;
           ++kv_iter;
         }
-        // The next item is claimed once this one's loads are under way, not before: a CTA at its
-        // start would take one that another is free for sooner.
-        if (!p.offsets) ahead = packed_claim(p.head, gridDim.x);
       }
       // No more items: tell the MMA warp through the next phase of kQFull.
       if (ok && wait1(bar(kQEmpty), (q_iter & 1u) ^ 1u, abort_flag, p)) {
@@ -663,6 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int h = it.hk * p.G + row_head;
       __nv_bfloat16* const dst = row_valid ? p.out + (row * p.Hq + h) * D : nullptr;
       const uint32_t rows = sbase + Lay::kStageOff + warp * kRowStage;
+      // Whole tokens of all its rows go out by TMA, which the warp does not wait for.  (Rows
+      // written by the lanes held it up for 2700 - 3100 clocks an item.)
+      const bool by_tma = p.warp_tokens > 0 && (wq + 1) * p.warp_tokens <= tokens;
 #pragma unroll 1
       for (int half = 0; half < D / 64; ++half) {  // 64 columns, 128 bytes of a row
         uint32_t ov[2][32];
@@ -677,6 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::reg_fence(ov[0]);
           ptx::reg_fence(ov[1]);
         }
+        if (lane == 0) ptx::tma_store_wait_read();  // the stage is free again
+        __syncwarp();
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
           uint32_t b[16];
@@ -688,10 +696,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 4; ++x)
             stage_chunk(rows, lane, ch * 4 + x, b[4 * x], b[4 * x + 1], b[4 * x + 2], b[4 * x + 3]);
         }
-        write_rows(rows, dst ? dst + half * 64 : nullptr, lane);
+        if (by_tma) {
+          ptx::fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0)
+            ptx::tma_store_3d(rows, &tmap_o, half * 64, it.hk * p.G,
+                              it.row0 + (t ? it.token[1] : it.token[0]) + wq * p.warp_tokens);
+        } else {
+          write_rows(rows, dst ? dst + half * 64 : nullptr, lane);
+        }
       }
       if (row_valid) p.lse[static_cast<size_t>(h) * p.T + row] = (m_used + log2f(l_run)) * kLn2;
     }
+    if (lane == 0) ptx::tma_store_wait();
   }
 
   // ---------------------------------------------------------------- teardown
@@ -712,10 +729,12 @@ cudaError_t launch_packed_fwd(const PackedArgs& a, const FwdParams& p, int grid,
   const auto kern = packed_fwd_kernel<D, kParts>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), Lay::kAlloc);
   if (e != cudaSuccess) return e;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   if (!packed_map(&mq, a.q, a.T, a.Hq, D, a.qs[0], a.qs[1], p.G, p.tq) ||
       !packed_map(&mk, a.k, a.T, a.Hk, D, a.ks[0], a.ks[1], 1, kBN) ||
-      !packed_map(&mv, a.v, a.T, a.Hk, D, a.vs[0], a.vs[1], 1, kBN))
+      !packed_map(&mv, a.v, a.T, a.Hk, D, a.vs[0], a.vs[1], 1, kBN) ||
+      !packed_map(&mo, p.out, a.T, a.Hq, D, static_cast<long long>(a.Hq) * D, D, p.G,
+                  std::max(1, p.warp_tokens)))
     return cudaErrorInvalidValue;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -728,7 +747,7 @@ cudaError_t launch_packed_fwd(const PackedArgs& a, const FwdParams& p, int grid,
   cfg.attrs = &at;
   cfg.numAttrs = p.offsets ? 0 : 1;
   count_launch(0);
-  return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p);
+  return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mo, p);
 }
 
 // A call that may have this many items has enough of them, whatever the lengths, and its
@@ -830,6 +849,7 @@ cp_status cp_packed_attn_fwd(const void* q, const int64_t* q_strides, const void
   p.offsets = direct ? seq_offsets : nullptr;
   p.n_seqs = n_seqs;
   p.T = T; p.Hq = Hq; p.Hk = Hk; p.G = G; p.tq = tq; p.causal = causal;
+  p.warp_tokens = 32 % G == 0 ? 32 / G : 0;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
