@@ -522,9 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = p.scale_log2;
     uint32_t s_cnt = 0, o_cnt = 0, join_cnt = 0;
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      PackedEntry entry;
-      if (!ring.get(static_cast<uint32_t>(k), entry, abort_flag, p)) { ok = false; break; }
+    PackedEntry entry;
+    ok = ring.get(0, entry, abort_flag, p);
+    for (uint32_t k = 0; ok; ++k) {
+      entry = PackedRing::uniform(entry);
       if (entry.hk < 0) break;
       FwdItem it;
       fwd_item<kParts>(p, entry, it);
@@ -532,7 +533,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tokens = t ? it.tokens[1] : it.tokens[0];
       const int last = t ? it.last[1] : it.last[0];
       const int parts = t ? it.parts[1] : it.parts[0];
-      if (tokens == 0 || last < it.first) continue;
+      if (tokens == 0 || last < it.first) {
+        ok = ring.get(k + 1, entry, abort_flag, p);
+        continue;
+      }
       const bool row_valid = row_token < tokens;
       const int token = (t ? it.token[1] : it.token[0]) + row_token;
       const int seen = !row_valid ? 0 : p.causal ? token + 1 : it.len;  // keys
@@ -613,6 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
+      if (!ring.get(k + 1, entry, abort_flag, p)) { ok = false; break; }  // while O is formed
       if (!wait_warp(bar(kOBar + t), o_cnt & 1u, abort_flag, p)) { ok = false; break; }
       ++o_cnt;
       ptx::tc_fence_after();
