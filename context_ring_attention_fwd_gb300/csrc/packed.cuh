@@ -172,7 +172,8 @@ struct PackedRing {
     return true;
   }
 };
-constexpr int kPackedRingBytes = 2 * kRing * 8 + kRing * 32 + 16;  // barriers, slots, the MMA warp's word
+// barriers, slots, the MMA warp's word
+constexpr int kPackedRingBytes = 2 * kRing * 8 + kRing * 32 + 16;
 static_assert(kPackedRingBytes <= 256, "the item ring's shared-memory block");
 
 // The (tile, key head) pair of item w: groups of `hg` heads, in a group the list's order.

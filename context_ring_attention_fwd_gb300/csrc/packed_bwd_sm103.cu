@@ -5,8 +5,8 @@
 //   D = rowsum(dO * O);  dP = dO V^T;  dS = P * (dP - D);
 //   dV = P^T dO;  dK = dS^T Q / sqrt(d);  dQ = dS K / sqrt(d)
 // ("上下文並行（Context Parallelism, CP）", compassingai.com, section 反向傳播), the sums of a key
-// head's dK and dV running over the G query heads that read it.  Two kernels, with the CTA's roles as
-// attn_bwd_sm103.cu describes them:
+// head's dK and dV running over the G query heads that read it.  Two kernels, with the CTA's
+// roles as attn_bwd_sm103.cu describes them:
 //   kDKDV  a CTA owns a 128-key tile of one key head and walks the packed query tiles
 //          (packed.cuh) that see it: G heads' rows are neighbours in the products' inner
 //          dimension, so a shared head's gradients are summed in the accumulators.
@@ -71,7 +71,8 @@ struct BLayout {
   static constexpr int kF1 = kTileBytes;
   static constexpr int kX0 = 2 * kTileBytes;
   static constexpr int kX1 = kX0 + kX0Slots * kTileBytes;
-  static constexpr int kVec = kX1 + kX1Slots * kTileBytes;    // kDKDV: fp32 [128], -lse2 of two tiles, -D
+  // kDKDV: fp32 [128], -lse2 of two tiles, -D
+  static constexpr int kVec = kX1 + kX1Slots * kTileBytes;
   static constexpr int kBar = kVec + (kDKDV ? 3 * kT * 4 : 0);
   static constexpr int kRingOff = kBar + 256;  // the item ring
   static constexpr int kBytes = kRingOff + 256;
@@ -453,9 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int last_zero = min(last_steps * 16, kDKDV ? packed_rows : kT);
         // A step's first product S; dV += P^T dO, when P^T is written; dQ += dS K or
         // dK += dS^T Q, when dS is.  S of the next step goes out when S has been read and, where
-        // P^T lies in its place, dV is under way; dP of the next step behind dQ or dK, as dS lies in
-        // dP's place.  So the softmax forms dS during S (and dV) and the next P during dQ or dK and
-        // the next dP.  What is written in halves of 64 streamed rows enters its product so.
+        // P^T lies in its place, dV is under way; dP of the next step behind dQ or dK, as dS lies
+        // in dP's place.  So the softmax forms dS during S (and dV) and the next P during dQ or dK
+        // and the next dP.  What is written in halves of 64 streamed rows enters its product so.
         // (Measured for kDQ, 16K tokens of 16/4 heads, in the kernel: 970 us, 73 % of the tensor
         // pipe; dS in a place of its own, so that dP need not wait for dQ, and dO for that in
         // shared memory: 1044.)
@@ -473,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool zero_last = ragged && last_rows < last_zero;
         auto issue_s = [&](uint32_t x, bool last) -> bool {
           const uint32_t s0 = x % Lay::kX0Slots;
-          if (!loaded(kX0Full + s0, Lay::x0(s0), x / Lay::kX0Slots, last && zero_last)) return false;
+          if (!loaded(kX0Full + s0, Lay::x0(s0), x / Lay::kX0Slots, last && zero_last))
+            return false;
           issue_scores(tS, Lay::kF0, kHeldQ, Lay::x0(s0));
           ptx::mma_commit_w(bar(kSFull));
           return true;
@@ -674,7 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x4 = 0; x4 < 8; ++x4) {  // paired fp32
             const float4 nl =
-                kDKDV ? load_floats(lse_vec + (c0 + 4 * x4) * 4) : make_float4(-lse2_r, -lse2_r, -lse2_r, -lse2_r);
+                kDKDV ? load_floats(lse_vec + (c0 + 4 * x4) * 4)
+                      : make_float4(-lse2_r, -lse2_r, -lse2_r, -lse2_r);
             const float nla[4] = {nl.x, nl.y, nl.z, nl.w};
 #pragma unroll
             for (int hx = 0; hx < 2; ++hx) {

@@ -259,57 +259,58 @@ template <int D>
 constexpr int kPitch = D + 8;  // floats; staggers the rows over the banks
 template <int D, int kShiftLog2>
 __device__ __forceinline__ void write_item(const DecodeParams& p, const Item& it, int t0, int t1,
-                                           const float* mo, const float (&merge_ml)[kWarps][kRows][2],
-                                           bool any_bad, float vd) {
+                                           const float* mo,
+                                           const float (&merge_ml)[kWarps][kRows][2], bool any_bad,
+                                           float vd) {
   constexpr float kShift = kShiftLog2;  // P was held times 2^kShift
-      const bool complete = t0 == 0 && static_cast<unsigned>(t1) == it.n_tiles;
-      const bool direct = complete && !it.prefix && p.P == 0 && p.n_q == 1;
-      constexpr int kVecs = D / 4;  // 4-column vectors of a row
-      for (int x = threadIdx.x; x < it.rows * kVecs; x += kThreads) {
-        const int r = x / kVecs, col = (x % kVecs) * 4;
-        float big = -INFINITY, l = 0.f;
-  #pragma unroll
-        for (int y = 0; y < kWarps; ++y) big = fmaxf(big, merge_ml[y][r][0]);
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  #pragma unroll
-        for (int y = 0; y < kWarps; ++y) {
-          const float my = merge_ml[y][r][0];
-          // an empty state's l is 0, or NaN where its scores were
-          l += merge_ml[y][r][1] * (my == -INFINITY ? 1.f : ptx::ex2(my - big));
-          const float4 a = *reinterpret_cast<const float4*>(mo + (y * kRows + r) * kPitch<D> + col);
-          sum.x += a.x;
-          sum.y += a.y;
-          sum.z += a.z;
-          sum.w += a.w;
-        }
-        if (any_bad) l = NAN;
-        const RowOf row(p, it.b0, it.hk, it.row0 + r);
-        if (direct) {
-          const float inv = l == 0.f ? 0.f : vd / l;
-          uint2 v;
-          v.x = ptx::pack_bf16(sum.x * inv, sum.y * inv);
-          v.y = ptx::pack_bf16(sum.z * inv, sum.w * inv);
-          *reinterpret_cast<uint2*>(p.out + row.index(p) * D + col) = v;
-          if (col == 0)
-            p.lse[(static_cast<long long>(row.b) * p.Hq + row.h) * p.n_q + row.i] =
-                (big - kShift + log2f(l)) * kLn2;
-          continue;
-        }
-        float *to, *ml;
-        if (complete) {
-          const long long at = (it.prefix ? static_cast<long long>(p.B) * p.n_q * p.Hq : 0) +
-                               row.index(p);
-          to = p.whole_o + at * D;
-          ml = p.whole_ml + at * 2;
-        } else {
-          const long long at = (static_cast<long long>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0)) * kRows + r;
-          to = p.slot_o + at * D;
-          ml = p.slot_ml + at * 2;
-        }
-        *reinterpret_cast<float4*>(to + col) = make_float4(sum.x * vd, sum.y * vd, sum.z * vd,
-                                                           sum.w * vd);
-        if (col == 0) *reinterpret_cast<float2*>(ml) = make_float2(big - kShift, l);
-      }
+  const bool complete = t0 == 0 && static_cast<unsigned>(t1) == it.n_tiles;
+  const bool direct = complete && !it.prefix && p.P == 0 && p.n_q == 1;
+  constexpr int kVecs = D / 4;  // 4-column vectors of a row
+  for (int x = threadIdx.x; x < it.rows * kVecs; x += kThreads) {
+    const int r = x / kVecs, col = (x % kVecs) * 4;
+    float big = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int y = 0; y < kWarps; ++y) big = fmaxf(big, merge_ml[y][r][0]);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int y = 0; y < kWarps; ++y) {
+      const float my = merge_ml[y][r][0];
+      // an empty state's l is 0, or NaN where its scores were
+      l += merge_ml[y][r][1] * (my == -INFINITY ? 1.f : ptx::ex2(my - big));
+      const float4 a = *reinterpret_cast<const float4*>(mo + (y * kRows + r) * kPitch<D> + col);
+      sum.x += a.x;
+      sum.y += a.y;
+      sum.z += a.z;
+      sum.w += a.w;
+    }
+    if (any_bad) l = NAN;
+    const RowOf row(p, it.b0, it.hk, it.row0 + r);
+    if (direct) {
+      const float inv = l == 0.f ? 0.f : vd / l;
+      uint2 v;
+      v.x = ptx::pack_bf16(sum.x * inv, sum.y * inv);
+      v.y = ptx::pack_bf16(sum.z * inv, sum.w * inv);
+      *reinterpret_cast<uint2*>(p.out + row.index(p) * D + col) = v;
+      if (col == 0)
+        p.lse[(static_cast<long long>(row.b) * p.Hq + row.h) * p.n_q + row.i] =
+            (big - kShift + log2f(l)) * kLn2;
+      continue;
+    }
+    float *to, *ml;
+    if (complete) {
+      const long long at = (it.prefix ? static_cast<long long>(p.B) * p.n_q * p.Hq : 0) +
+                           row.index(p);
+      to = p.whole_o + at * D;
+      ml = p.whole_ml + at * 2;
+    } else {
+      const long long at = (static_cast<long long>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0)) * kRows + r;
+      to = p.slot_o + at * D;
+      ml = p.slot_ml + at * 2;
+    }
+    *reinterpret_cast<float4*>(to + col) = make_float4(sum.x * vd, sum.y * vd, sum.z * vd,
+                                                       sum.w * vd);
+    if (col == 0) *reinterpret_cast<float2*>(ml) = make_float2(big - kShift, l);
+  }
 }
 
 // What a head's codes are multiplied by (x: 0 K, 1 V).
@@ -666,7 +667,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode4_kernel(con
       int page, slot;
     };
     bool bad = false;
-    const uint8_t* const head[2] = {p.cache[0] + it.hk * p.cs[0][2], p.cache[1] + it.hk * p.cs[1][2]};
+    const uint8_t* const head[2] = {p.cache[0] + it.hk * p.cs[0][2],
+                                    p.cache[1] + it.hk * p.cs[1][2]};
     const uint8_t* const scale_head[2] = {p.scales[0] + it.hk * p.ss[0][2],
                                           p.scales[1] + it.hk * p.ss[1][2]};
     auto look_up = [&](int t) {
@@ -776,8 +778,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode4_kernel(con
         core.store_row(mo + (warp * kRows + row) * kPitch<D>, nt, e, f, lane);
       }
     __syncthreads();
-    write_item<D, static_cast<int>(Core::kShift)>(p, it, t0, t1, mo, merge_ml, any_bad,
-                        Core::kUnit * head_descale<Held::kInt4>(p, 1, it.hk));
+    write_item<D, static_cast<int>(Core::kShift)>(
+        p, it, t0, t1, mo, merge_ml, any_bad,
+        Core::kUnit * head_descale<Held::kInt4>(p, 1, it.hk));
     if (any_bad && threadIdx.x == 0) atomicOr(p.err, kErrCache);
     __syncthreads();  // the ring is free again
   }
@@ -897,7 +900,8 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeParam
     }
     pre.r = row % p.prefix_rows;
     const int tile = row / p.prefix_rows;
-    const int item = wide ? prefix_item<kHeld == Held::kE4M3>(p, hk, tile) : hk * p.prefix_row_tiles + tile;
+    const int item = wide ? prefix_item<kHeld == Held::kE4M3>(p, hk, tile)
+                          : hk * p.prefix_row_tiles + tile;
     pre.find(item * units, n,
              wide ? units * static_cast<unsigned>(p.Hk * p.prefix_row_tiles) : W,
              wide ? static_cast<unsigned>(p.prefix_grid) : g);
@@ -1120,7 +1124,8 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
     ring = kWarps * Stage<D, kHeld>::kRing;
   }
   const int smem = ring + 4 * (p.B + 1);
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), ring + 4 * (kMaxBatch + 1));
+  cudaError_t e =
+      ensure_smem_limit(reinterpret_cast<const void*>(kern), ring + 4 * (kMaxBatch + 1));
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(std::min(kMaxGrid, kCtasPerSm * sm_count()));
   kern<<<grid, kThreads, smem, stream>>>(p);
