@@ -14,11 +14,11 @@
 // multiple of 16 keys, and the up to 15 rows of V beyond the last key are zeroed in
 // shared memory first.  K needs none: its rows are columns of S, which the mask replaces.
 //
-// Bound by the tensor pipe where sequences are long: 32K tokens of 8/2 heads, 2.2 TFLOP, 1210 us, 95 %
+// Bound by the tensor pipe where sequences are long: 32K tokens of 8/2 heads, 2.2 TFLOP, 1200 us, 95 %
 // of the cuBLAS rate (80 % of the pipe's cycles); a run of seconds, at the clock that the power cap
-// leaves, 1350 - 1410.  In short ones by what an item costs besides its tiles, about 2.3 us (its
+// leaves, 1330 - 1410.  In short ones by what an item costs besides its tiles, about 2.3 us (its
 // first S, the drain behind its last P, its rows' way out): 14 prompts of up to 2000 tokens, 32/8
-// heads, 109 GFLOP, 97 us, 54 % of the pipe's cycles.  (The next item's first S issued between the
+// heads, 109 GFLOP, 97 us, 56 % of the pipe's cycles.  (The next item's first S issued between the
 // last two PVs, which the drain would hide, made the MMA warp's loop slower: 110 us there, 1280 for
 // the 32K.)  P is rounded to bf16 for its product, as in the ring's forward, which costs about as
 // much as the output's own rounding (2.0e-3 to 2.2e-3 against 64 bits, relative in the norm, where
