@@ -237,6 +237,23 @@ def test_decode_of_small_and_large_scores(d, scale):
     b.check(*b.run())
 
 
+@pytest.mark.parametrize("Hq", [4, 12])
+@pytest.mark.parametrize("fall", [False, True])
+def test_decode_of_scores_that_rise_or_fall_along_the_keys(Hq, fall):
+    """Scales from 2^-6 to 2^5 along the keys, all entries of one sign: scores that pass a row's
+    reference again and again, or leave it behind by more than fp16 holds."""
+    d, page, n = 64, 16, 900
+    b = Batch4([n, 3], 1, Hq, 1, d, page, seed=21)
+    b.q.abs_()
+    t = b.table.cpu().numpy()[0]
+    pos = np.arange(n)
+    code = (8 + 88 * pos // n).astype(np.uint8)
+    at = torch.tensor(t[pos // page], device=DEV).long(), torch.tensor(pos % page, device=DEV)
+    b.k[at[0], at[1]] = 0xFF
+    b.ks[at[0], at[1]] = torch.tensor(code[::-1].copy() if fall else code, device=DEV)[:, None, None]
+    b.check(*b.run())
+
+
 @pytest.mark.parametrize("n_q,P", [(1, 0), (3, 70)])
 def test_the_split_and_its_join(n_q, P):
     """Sequences cut over many blocks, and short ones beside them."""

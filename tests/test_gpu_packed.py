@@ -159,6 +159,20 @@ def test_gradients(lens, Hq, Hk, d, causal):
     p.check_gradients(out, lse, p.backward(out, lse, causal, fused=Hq % 4 == 0), causal)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,Hq,Hk,d", [
+    ([70, 9, 1], 16, 1, 64),      # two tokens to a warp's rows
+    ([5, 40, 33], 32, 1, 128),    # one
+    ([20, 3], 64, 1, 64),         # half a one
+    ([17, 130, 64], 2, 1, 128),   # sixteen
+])
+def test_tokens_that_fill_a_warps_rows_or_do_not(lens, Hq, Hk, d, causal):
+    p = Prompts(lens, Hq, Hk, d, seed=Hq, lead=2, pad=5, fused=True)
+    out, lse = p.forward(causal)
+    p.check(out, lse, causal)
+    p.check_gradients(out, lse, p.backward(out, lse, causal, fused=True), causal)
+
+
 def test_gradients_are_differences():
     """Along a random direction in q, k and v the loss's slope, from the oracle's forward in 64
     bits, is the gradients' product with it: each gradient entry is known to 2^-7 of its size
