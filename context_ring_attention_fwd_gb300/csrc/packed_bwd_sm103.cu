@@ -120,6 +120,7 @@ struct BParams {
   __nv_bfloat16* g0;    // dQ (kDQ) or dV (kDKDV)
   __nv_bfloat16* g1;    // dK (kDKDV)
   long long gs0[2], gs1[2];  // their strides: row, head
+  int wide;             // the outputs start at multiples of 32 bytes
   float4* sums;         // kDKDV: [slot][Hk][dV, dK][d / 4][128] of the tiles in parts
   int* done;
   int* err;
@@ -229,6 +230,20 @@ __device__ __forceinline__ float4 load_floats(uint32_t at) {
 }
 __device__ __forceinline__ void store_float(uint32_t at, float x) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
+
+// 32 bytes of a row, whole sectors where the outputs lie so.  (Measured, in two halves of 16 /
+// whole, us a call: 14 prompts of up to 2000 tokens, 32/8 heads, 288 / 279; 6 of up to 200, 16/4,
+// 26.3 / 25.1.  Wider rows by way of shared memory would need some, and there is none left.)
+__device__ __forceinline__ void store_32(uint4* to, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 template <int D, bool kDKDV>
@@ -814,13 +829,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (row_valid) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint4 v4;
-              v4.x = ptx::pack_bf16(__uint_as_float(ov[8 * x + 0]) * fac, __uint_as_float(ov[8 * x + 1]) * fac);
-              v4.y = ptx::pack_bf16(__uint_as_float(ov[8 * x + 2]) * fac, __uint_as_float(ov[8 * x + 3]) * fac);
-              v4.z = ptx::pack_bf16(__uint_as_float(ov[8 * x + 4]) * fac, __uint_as_float(ov[8 * x + 5]) * fac);
-              v4.w = ptx::pack_bf16(__uint_as_float(ov[8 * x + 6]) * fac, __uint_as_float(ov[8 * x + 7]) * fac);
-              dst[c0 / 8 + x] = v4;
+            for (int x = 0; x < 2; ++x) {
+              uint32_t w[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y)
+                w[y] = ptx::pack_bf16(__uint_as_float(ov[16 * x + 2 * y]) * fac,
+                                      __uint_as_float(ov[16 * x + 2 * y + 1]) * fac);
+              store_32(dst + c0 / 8 + 2 * x, w, p.wide);
             }
           }
         }
@@ -981,7 +996,9 @@ cp_status cp_packed_attn_bwd(const void* q, const int64_t* q_strides, const void
   p.fault_drop = test_fault_drop();
   p.sums = reinterpret_cast<float4*>(ws + sp.sums);
   p.done = plan.list[0].done;
+  p.wide = aligned(dk, 32) && aligned(dv, 32);
   BParams pq = p;
+  pq.wide = aligned(dq, 32);
   p.g0 = static_cast<__nv_bfloat16*>(dv);
   p.g1 = static_cast<__nv_bfloat16*>(dk);
   pq.g0 = static_cast<__nv_bfloat16*>(dq);

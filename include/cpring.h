@@ -674,7 +674,7 @@ cp_status cp_packed_attn_fwd(const void* q, const int64_t* q_strides, const void
 /*
  * Backward of cp_packed_attn_fwd: the gradients of sum(out * dout) with respect to q, k and v
  * ("上下文並行", section 反向傳播), those of a key head summed over the query heads that read
- * it, in fp32 within one block: the result does not change from run to run.
+ * it, in fp32 and in one order: the result does not change from run to run.
  *  q, k, v, seq_offsets, causal   as given to the forward, out and lse as it wrote them.
  *  dout       device, bf16 [T,Hq,d] contiguous, read.
  *  dq, dk, dv device, bf16 [T,Hq,d], [T,Hk,d], [T,Hk,d], written; their strides as the inputs',
@@ -685,7 +685,7 @@ cp_status cp_packed_attn_fwd(const void* q, const int64_t* q_strides, const void
  *  Sizes, alignment and errors as cp_packed_attn_fwd (dq, dk, dv 16 bytes).
  * Three launches: the plan with D = rowsum(dout * out) and the dK/dV kernel on `stream`, and
  * the dQ kernel on the library's second stream (cp_ring_attn_bwd), which `stream` then waits
- * for.  Nothing is allocated.
+ * for; in a capture, two branches of its graph.  Nothing is allocated.
  */
 int64_t cp_packed_attn_bwd_workspace_bytes(int T, int n_seqs, int Hq, int Hk, int d);
 cp_status cp_packed_attn_bwd(const void* q, const int64_t* q_strides, const void* k,

@@ -173,6 +173,17 @@ def test_tokens_that_fill_a_warps_rows_or_do_not(lens, Hq, Hk, d, causal):
     p.check_gradients(out, lse, p.backward(out, lse, causal, fused=True), causal)
 
 
+def test_outputs_that_start_16_bytes_into_a_sector():
+    p = Prompts([150, 40], 4, 2, 64, seed=5, pad=3)
+    out, lse = p.forward()
+    want = p.backward(out, lse)
+    to = [torch.full((t.numel() + 8,), -7.0, dtype=BF16, device=DEV)[8:].view(t.shape)
+          for t in want]
+    assert all(t.data_ptr() % 32 == 16 for t in to)
+    pkg.packed_attn_bwd(p.q, p.k, p.v, out, lse, p.dout, p.offsets, dq=to[0], dk=to[1], dv=to[2])
+    assert all(torch.equal(a, b) for a, b in zip(to, want))
+
+
 def test_gradients_are_differences():
     """Along a random direction in q, k and v the loss's slope, from the oracle's forward in 64
     bits, is the gradients' product with it: each gradient entry is known to 2^-7 of its size
