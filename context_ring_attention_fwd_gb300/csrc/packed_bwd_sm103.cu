@@ -19,7 +19,7 @@
 // its full rate (128 bytes a clock), and the copies, dV's and dK's tiles and the constants come on
 // top, 2560 clocks a tile pair for 2048 of products in kDKDV.  kDQ's fixed operands are therefore
 // in TMEM; kDKDV has no columns left for its.  Measured (16K tokens of 16/4 heads, d = 128, in the
-// kernels): kDKDV 1470 us, 68 % of the tensor pipe, kDQ 970, 73 %; with S^T and dP^T in halves of
+// kernels): kDKDV 1450 us, 67 % of the tensor pipe, kDQ 970, 73 %; with S^T and dP^T in halves of
 // 64 queries, two in flight, kDKDV took 1830, and with constants read by generic loads 1570.
 // P and dS are rounded to bf16 for their products, as the ring's backward rounds them: 2.5e-3 to
 // 3.0e-3 of the gradients against 64 bits (relative in the norm), 1.7e-3 of it the outputs' own.
