@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The next item is claimed once this one's loads are under way (see packed_fwd_sm103.cu).
         // Measured for kDKDV, so / when this item starts (us a call): 3000 + 200 + 100 tokens of
         // 32/8 heads 219 / 252, 6000 of 16/2 359 / 374, 8 x 2048 of 32/8 781 / 790, 9000 of 4/4
-        // (d = 64) 179 / 186; but 8192 of 8/2 375 / 342, 20000 of 1/1 (d = 64) 257 / 237.
+        // (d = 64) 179 / 186; but 20000 of 1/1 (d = 64) 257 / 237.
         ahead = packed_claim(p.head, gridDim.x);
       }
       // No more items: tell the MMA warp through the next phase of kFixFull.
@@ -913,8 +913,8 @@ struct Space {
   long long keys, queries, delta, done, sums, total;
   Space(int T, int n, int Hq, int Hk, int d) {
     const int tq = kT / (Hq / Hk);
-    // All parts of a call, none shorter than the shortest, and as many as the plan cuts (its
-    // share of a CTA's work makes 2 / 0.6 of the grid's at most).
+    // All parts of a call, none shorter than the shortest, and no more than kMaxParts, which the
+    // plan keeps to.
     const long long most = packed_items(T, n, kT) * (T / tq / kLeastPart + 1);
     slots = static_cast<int>(std::min<long long>(most, (kMaxParts + Hk - 1) / Hk));
     const auto up = [](long long x) { return (x + 255) / 256 * 256; };

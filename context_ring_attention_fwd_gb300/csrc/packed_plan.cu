@@ -181,21 +181,28 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   // start, its sums' way through memory, their addition), so parts are as many as CTAs where
   // the share is small, 1.3 of it, and down to 0.6 of it where it is large; they are no
   // shorter than kLeastPart, and items of up to kLeastCut stay whole.  Measured for the backward's
-  // key tiles, whole / cut (us a call): 4096 tokens of 8/1 heads 409 / 131, 8192 of 8/2 622 /
-  // 342, 5000 + 2500 of 16/2 720 / 339, 1500 of 2/1 50 / 35, 20000 of 1/1 (d = 64) 236 / 237; 200
-  // of 16/4 (7 streamed tiles) 25 / 25, which stays whole.
+  // key tiles, whole / cut (us a call): 4096 tokens of 8/1 heads 409 / 130, 8192 of 8/2 622 /
+  // 331, 5000 + 2500 of 16/2 720 / 329, 1500 of 2/1 50 / 35; 200 of 16/4 (7 streamed tiles) 25 /
+  // 25, which stays whole.
+  // Key tiles that are no more than the CTAs are cut down to 0.45 of the share: so / to 0.6, 8192
+  // tokens of 8/2 heads 331 / 377, 5000 + 2500 of 16/2 329 / 359.  More of them balance
+  // themselves: 9000 of 4/4 (d = 64) 183 / 177, 3000 + 200 + 100 of 32/8 222 / 215, 14 prompts of
+  // 32/8 281 / 278.  (Nor does the forward gain: 20000 of 1/1, d = 64, 82 / 78.)
   int chunk = INT_MAX;
   auto parts_of = [&](const int4& it) {
     const int n = streamed_tiles(p, l, it);
     return n <= kLeastCut ? 1 : (n - 1) / chunk + 1;
   };
   if (l.slots > 0) {
-    // A tile of n > chunk streamed tiles is cut into at most 2 n / chunk parts, so with a chunk of
-    // 2 / slots of all streamed tiles at least there are no more parts than slots.
+    // An item of n > chunk streamed tiles is cut into less than n / chunk + 1 parts, and into at
+    // most 2 n / chunk, so there are no more parts than slots with a chunk of at least
+    // 1 / (slots - items) of all streamed tiles, or of 2 / slots.
     const float all = 1.001f * block_sum(streamed, streamed_sum);  // (whatever was rounded)
     const float mean = all * p.Hk / p.grid;
-    const float share = 0.6f * mean + fminf(0.7f * mean, 20.f);
-    chunk = max(kLeastPart, static_cast<int>(fminf(fmaxf(share, 2.f * all / l.slots) + 1.f, 1e9f)));
+    const float down = l.of_keys && static_cast<long long>(items) * p.Hk <= p.grid ? 0.45f : 0.6f;
+    const float share = down * mean + fminf((1.3f - down) * mean, 20.f);
+    const float least = 2 * items < l.slots ? all / (l.slots - items) : 2.f * all / l.slots;
+    chunk = max(kLeastPart, static_cast<int>(fminf(fmaxf(share, least) + 1.f, 1e9f)));
     for (int i = threadIdx.x; i < l.n_done; i += blockDim.x) l.done[i] = 0;
     if (threadIdx.x == 0) l.head[2] = chunk;
   }
