@@ -135,7 +135,7 @@ struct BParams {
   int* err;
   unsigned long long timeout_ns;
   int fault_drop;       // test hook: CTA 0 never loads its first streamed X0 tile
-  unsigned long long* work_slot;  // this launch's claim counter (see claim_first)
+  unsigned long long* work_slot;  // this launch's claim counter (see claim_first), or null
   uint32_t epoch;                 // this launch's tag in that counter
 };
 
@@ -261,12 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool dropped = false;
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        const int w = !CPRING_DYNAMIC ? item_of(k, c, G)
-                      : (k == 0) ? c : G + claimed_index(ahead, p.epoch, p.err);
+        const int w = item_at(p, k, c, G, ahead);
         if (!ring_put(ring, static_cast<uint32_t>(k), w, abort_flag, p)) { ok = false; break; }
         if (w >= p.n_items) break;
-        if (CPRING_DYNAMIC)  // claim the CTA's next item now; it is read when that item starts
-          ahead = (k == 0) ? claim_first(p.work_slot, p.epoch) : claim_next(p.work_slot);
+        // claim the CTA's next item now; it is read when that item starts
+        ahead = claim_ahead(p, k);
         BItem it;
         decode_bitem<kDKDV>(p, n_docs, w, it);
         if (!wait1(bar(kFixEmpty), (fix_iter & 1u) ^ 1u, abort_flag, p)) { ok = false; break; }
@@ -801,12 +800,10 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
   if (!p.err) return cudaErrorInvalidValue;
   p.timeout_ns = test_wait_limit_ns();
   p.fault_drop = test_fault_drop();
-  unsigned long long* slots = work_slots_address();
-  if (!slots) return cudaErrorInvalidValue;
-  const uint32_t epoch = next_epoch(slots);
-  if (epoch == 0) return cudaErrorInvalidValue;
-  p.epoch = epoch;
-  p.work_slot = slots + epoch % kWorkSlots;
+  if (CPRING_DYNAMIC) {
+    const cudaError_t e = take_counter(p, stream);
+    if (e != cudaSuccess) return e;
+  }
   const int grid = static_cast<int>(std::min<long long>(items, sm_count()));
   // Head groups as in the forward: a launch with at least 16 rounds of the
   // grid and no document layout takes the smallest group whose items fill

@@ -119,6 +119,9 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity,
 // (launch epoch << 32 | next index), and epochs only grow, so no launch
 // clears it and none allocates it.  At most kWorkSlots launches can run at
 // once on a device before one would reuse the slot of another still running.
+// A captured launch has no counter: its parameters are the same in every replay,
+// which would find a counter where the last replay, or a later launch that uses the
+// slot, left it.  Its CTAs take the fixed order of item_of.
 constexpr int kWorkSlots = 256;
 __device__ unsigned long long g_work_slots[kWorkSlots];
 // Tuning switch of the backward kernels: CTAs claim items from the launch's
@@ -154,6 +157,19 @@ __device__ __forceinline__ int claimed_index(unsigned long long v, uint32_t epoc
     return INT_MAX / 2;
   }
   return static_cast<int>(v & 0xffffffffull);
+}
+
+// The k-th item of CTA c of G, given its latest claim; and, once that item is known,
+// the claim of its next one.
+template <class P>
+__device__ __forceinline__ int item_at(const P& p, int k, int c, int G, unsigned long long ahead) {
+  if (k == 0 || p.work_slot == nullptr) return item_of(k, c, G);
+  return G + claimed_index(ahead, p.epoch, p.err);
+}
+template <class P>
+__device__ __forceinline__ unsigned long long claim_ahead(const P& p, int k) {
+  if (p.work_slot == nullptr) return 0;
+  return k == 0 ? claim_first(p.work_slot, p.epoch) : claim_next(p.work_slot);
 }
 
 // The CTA's ring of claimed item indices: the producer publishes each item
@@ -282,6 +298,22 @@ uint32_t next_epoch(unsigned long long* slots) {
     e = ++g_epoch[dev];
   }
   return e;
+}
+
+// The claim counter of a launch on `stream` and the launch's tag; none in a capture.
+template <class P>
+cudaError_t take_counter(P& p, cudaStream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(stream, &status);
+  if (e != cudaSuccess) return e;
+  p.work_slot = nullptr;
+  if (status != cudaStreamCaptureStatusNone) return cudaSuccess;
+  unsigned long long* const slots = work_slots_address();
+  if (!slots) return cudaErrorInvalidValue;
+  p.epoch = next_epoch(slots);
+  if (p.epoch == 0) return cudaErrorInvalidValue;
+  p.work_slot = slots + p.epoch % kWorkSlots;
+  return cudaSuccess;
 }
 
 }  // namespace

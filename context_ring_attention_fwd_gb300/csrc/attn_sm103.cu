@@ -196,7 +196,7 @@ struct KParams {
   int kv_row0;       // key index of row 0 of the K/V tensors (0 unless a block)
   int head_group;    // (b, h) heads whose items are dealt out together
   const int32_t* slot_perm;  // or null: slots heaviest first by measured cost
-  unsigned long long* work_slot;  // this launch's claim counter (see claim_first)
+  unsigned long long* work_slot;  // this launch's claim counter (see claim_first), or null
   uint32_t epoch;                 // this launch's tag in that counter
   const float* q_descale;  // FP8 form: [B * H] each
   const float* k_descale;
@@ -353,14 +353,13 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tmap_q, const CUten
       bool dropped = false;
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        const int w = !kDynamic ? item_of(k, c, G)
-                      : (k == 0) ? c : G + claimed_index(ahead, p.epoch, p.err);
+        const int w = kDynamic ? item_at(p, k, c, G, ahead) : item_of(k, c, G);
         if constexpr (kDynamic) {
           if (!ring_put(ring, static_cast<uint32_t>(k), w, abort_flag, p)) { ok = false; break; }
         }
         if (w >= p.n_items) break;
         if constexpr (kDynamic)  // claim the CTA's next item now; it is read when that item starts
-          ahead = (k == 0) ? claim_first(p.work_slot, p.epoch) : claim_next(p.work_slot);
+          ahead = claim_ahead(p, k);
         Item it;
         decode_item(p, n_docs, w, it);
         if (it.F_lo > it.F_hi) continue;
@@ -940,11 +939,11 @@ __device__ __forceinline__ void attn_body_fp8(const CUtensorMap& tmap_q, const C
       bool dropped = false;
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        const int w = (k == 0) ? c : G + claimed_index(ahead, p.epoch, p.err);
+        const int w = item_at(p, k, c, G, ahead);
         if (!ring_put(ring, static_cast<uint32_t>(k), w, abort_flag, p)) { ok = false; break; }
         if (w >= p.n_items) break;
         // claim the CTA's next item now; it is read when that item starts
-        ahead = (k == 0) ? claim_first(p.work_slot, p.epoch) : claim_next(p.work_slot);
+        ahead = claim_ahead(p, k);
         Item it;
         decode_item(p, n_docs, w, it);
         if (it.F_lo > it.F_hi) continue;
@@ -1426,12 +1425,10 @@ cudaError_t launch_t(const AttnArgs& a, cudaStream_t stream) {
   if (!p.err) return cudaErrorInvalidValue;
   p.timeout_ns = g_wait_limit_ns.load();
   p.fault_drop_k = g_fault_drop_k.load();
-  unsigned long long* slots = work_slots_address();
-  if (!slots) return cudaErrorInvalidValue;
-  const uint32_t epoch = next_epoch(slots);
-  if (epoch == 0) return cudaErrorInvalidValue;
-  p.epoch = epoch;
-  p.work_slot = slots + epoch % kWorkSlots;
+  if (kDynamic) {
+    const cudaError_t e = take_counter(p, stream);
+    if (e != cudaSuccess) return e;
+  }
   const int grid = static_cast<int>(std::min<long long>(items, sm_count()));
   // Head groups: fewer heads in flight reuse each K/V tile from L2.  A long
   // launch (many rounds of the grid) takes the smallest group whose items
