@@ -82,7 +82,8 @@ inline cp_status check_shape(int B, int S, int H, int d, int n_shards) {
 // threads take turns; its constructor orders `stream` after the work of the
 // previous lease when that ran on another stream, and its destructor records
 // the point after which the next lease may reuse the buffer.  Every launch
-// that reads the buffer must be enqueued on `stream` while the lease lives.
+// that reads the buffer must be enqueued on `stream` while the lease lives.  On a
+// stream that is being captured the lease is memory of the graph's own.
 class ScratchLease {
  public:
   ScratchLease(size_t bytes, cudaStream_t stream);
@@ -96,6 +97,7 @@ class ScratchLease {
   int dev_ = -1;
   void* ptr_ = nullptr;
   bool ok_ = false;
+  bool of_graph_ = false;
   cudaStream_t stream_ = nullptr;
 };
 

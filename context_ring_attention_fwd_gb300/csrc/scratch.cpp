@@ -8,6 +8,11 @@
 // a call on another stream first waits for an event recorded after the
 // previous user's work, so two launches never use the buffer at once.  The
 // per-device lock is held only while a call enqueues its work.
+//
+// A captured call has nothing of that buffer: memory that is allocated in a capture
+// exists while the graph runs and no longer, an event recorded in a capture orders no
+// other call, and a replay is not ordered behind the calls between it and the last one.
+// Its scratch is allocated and released by nodes of the graph.
 #include <cuda_runtime_api.h>
 
 #include <algorithm>
@@ -33,6 +38,12 @@ DeviceScratch g_scratch[kMaxDevices];
 }  // namespace
 
 ScratchLease::ScratchLease(size_t bytes, cudaStream_t stream) : stream_(stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &status) != cudaSuccess) return;
+  if (status != cudaStreamCaptureStatusNone) {
+    ok_ = of_graph_ = cudaMallocAsync(&ptr_, bytes, stream) == cudaSuccess;
+    return;
+  }
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return;
   DeviceScratch& s = g_scratch[dev];
@@ -62,6 +73,7 @@ ScratchLease::ScratchLease(size_t bytes, cudaStream_t stream) : stream_(stream) 
 }
 
 ScratchLease::~ScratchLease() {
+  if (of_graph_) cudaFreeAsync(ptr_, stream_);
   if (dev_ < 0) return;
   DeviceScratch& s = g_scratch[dev_];
   if (s.released && cudaEventRecord(s.released, stream_) == cudaSuccess) {

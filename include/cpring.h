@@ -124,7 +124,8 @@ cp_status cp_ring_attn_fwd_rank(const void* q, const void* k, const void* v, voi
  *
  * cp_ring_attn_fwd allocates its small per-device scratch (stream-ordered
  * cudaMallocAsync) the first time a call passes doc_offsets and whenever a call
- * needs more than it holds.  Processes that give nearly all GPU memory to their
+ * needs more than it holds; a captured call's is allocated and released by nodes of
+ * its graph.  Processes that give nearly all GPU memory to their
  * own pool at start-up and forbid later cudaMalloc/cudaMallocAsync, and loops
  * that must never enter the driver's allocator, call this entry point instead:
  * it allocates nothing and keeps its scratch in a fixed device array built into

@@ -148,3 +148,66 @@ def test_replays_among_many_single_calls():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got_g, want_g))
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def documents_call(d, docs, fp8=False):
+    docs_t = offsets(docs)
+    out, lse = torch.empty((B, S, H, d), dtype=BF16, device=DEV), torch.empty((B, H, S), device=DEV)
+
+    def call(q, k, v, g):
+        if fp8:
+            pkg.cp_ring_attn_fwd_fp8(*pkg.fp8_quantize_qkv(q, k, v), out, lse, 2, True, docs_t)
+        else:
+            pkg.cp_ring_attn_fwd(q, k, v, out, lse, 2, True, docs_t)
+        return out, lse
+    return call
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_captured_call_has_scratch_of_its_own(fp8):
+    """Calls whose scratch for documents is cached are captured, the cache grows, and replays run
+    beside single calls with other documents."""
+    d = 128
+    x, fresh = rows(6, d), rows(7, d)
+    call = documents_call(d, DOCS, fp8)
+    graph, got = captured(call, x)
+    # a longer sequence: more scratch than any call here before
+    T = 65536
+    y = [torch.randn((1, T, 1, 64), device=DEV).to(BF16) for _ in range(3)]
+    pkg.ring_attn_fwd(*y, 64, True, [0, 5, T])
+    for to, t in zip(x, fresh):
+        to.copy_(t)
+    other = documents_call(d, [0, 1024, 1500, 2048], fp8)
+    want = [t.clone() for t in documents_call(d, DOCS, fp8)(*fresh)]
+    want_other = [t.clone() for t in other(*fresh)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        with torch.cuda.stream(side):
+            for t in got:
+                t.fill_(7)
+            graph.replay()
+        got_other = other(*fresh)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(torch.equal(a, b) for a, b in zip(got_other, want_other))
+
+
+def test_calls_with_documents_after_a_capture():
+    """A capture in between leaves the other streams' calls as they were."""
+    d = 64
+    x = rows(8, d)
+    call = documents_call(d, DOCS)
+    want = [t.clone() for t in call(*x)]
+    kept = documents_call(d, DOCS)  # its tensors are the graph's
+    graph, got = captured(kept, x)
+    for s in (torch.cuda.Stream(), torch.cuda.Stream()):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            again = call(*x)
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(again, want))
+    for t in got:
+        t.fill_(7)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
