@@ -89,6 +89,13 @@ bool packed_strides(const int64_t* given, int H, int d, int64_t (&to)[2]);
 
 cudaError_t launch_packed_plan(const PackedPlan& p, cudaStream_t stream);
 
+// Slots of a key head for a call of `most` parts a key head, `parts` over all.  With one or two
+// the plan's chunk is all that is streamed, which cuts nothing: none then.
+inline int packed_slots(long long most, int parts, int Hk) {
+  const long long slots = std::min<long long>(most, (parts + Hk - 1) / Hk);
+  return slots < 3 ? 0 : static_cast<int>(slots);
+}
+
 // Byte sizes and places of a list of tiles of `tokens` tokens.
 inline long long packed_items(int T, int n, int tokens) {
   return static_cast<long long>(T) / tokens + n;

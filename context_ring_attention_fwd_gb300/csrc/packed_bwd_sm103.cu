@@ -914,9 +914,11 @@ struct Space {
   Space(int T, int n, int Hq, int Hk, int d) {
     const int tq = kT / (Hq / Hk);
     // All parts of a call, none shorter than the shortest, and no more than kMaxParts, which the
-    // plan keeps to.
-    const long long most = packed_items(T, n, kT) * (T / tq / kLeastPart + 1);
-    slots = static_cast<int>(std::min<long long>(most, (kMaxParts + Hk - 1) / Hk));
+    // plan keeps to; none where every tile stays whole.
+    const long long most = (T - 1) / tq + 1 <= kLeastCut
+                               ? 0
+                               : packed_items(T, n, kT) * (T / tq / kLeastPart + 1);
+    slots = packed_slots(most, kMaxParts, Hk);
     const auto up = [](long long x) { return (x + 255) / 256 * 256; };
     keys = 0;
     queries = up(packed_list_bytes(T, n, kT) + 16LL * slots);

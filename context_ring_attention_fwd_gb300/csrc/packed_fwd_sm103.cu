@@ -771,7 +771,7 @@ struct Space {
     const long long most = T <= kBN * kLeastCut || items * Hk >= kManyItems
                                ? 0
                                : items * (T / kBN / kLeastPart + 1);
-    slots = static_cast<int>(std::min<long long>(most, (kMaxFwdParts + Hk - 1) / Hk));
+    slots = packed_slots(most, kMaxFwdParts, Hk);
     list = 0;
     done = up(packed_list_bytes(T, n, tokens) + 16LL * slots);
     parts = done + up(4LL * slots * Hk * kQTiles);

@@ -409,3 +409,15 @@ def test_forward_of_items_in_parts(lens, Hq, Hk, d, causal):
     for _ in range(3):
         again, lse2 = p.forward(causal)
         assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,Hq,Hk,d", [
+    ([300, 30], 1040, 260, 64),  # 10 streamed tiles, but two slots a key head
+    ([200, 100], 16, 4, 128),    # 7
+])
+def test_gradients_where_no_tile_is_cut(lens, Hq, Hk, d, causal):
+    p = Prompts(lens, Hq, Hk, d, seed=23)
+    out, lse = p.forward(causal)
+    p.check(out, lse, causal)
+    p.check_gradients(out, lse, p.backward(out, lse, causal), causal)

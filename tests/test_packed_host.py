@@ -139,6 +139,19 @@ def test_workspace_sizes():
             assert f(*bad) == -1
 
 
+def test_no_workspace_for_parts_where_nothing_is_cut():
+    """Sums of parts take 128 KB a slot and key head at d = 128; what else there is (D, lists) is
+    below 8 bytes a row and head and 1 KB."""
+    bwd = pkg.cp_packed_attn_bwd_workspace_bytes
+    for T, n, Hq, Hk in [(200, 6, 16, 4),      # 7 streamed tiles: they stay whole
+                         (1000, 3, 1024, 1024),  # a slot for each key head: too few for a cut
+                         (2000, 1, 600, 300)]:  # two
+        assert bwd(T, n, Hq, Hk, 128) <= 8 * T * Hq + 1024
+    assert bwd(2000, 1, 2, 1, 128) > 1 << 20   # where tiles are cut there is
+    # the forward's, with two slots a key head
+    assert pkg.cp_packed_attn_fwd_workspace_bytes(1200, 1, 170, 170, 128) <= 1 << 16
+
+
 def test_host_tensors_are_refused():
     q = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
