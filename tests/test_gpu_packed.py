@@ -19,6 +19,7 @@ import torch
 
 import context_ring_attention_fwd_gb300 as pkg
 from oracle import packed
+import packed_plan
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -421,3 +422,71 @@ def test_gradients_where_no_tile_is_cut(lens, Hq, Hk, d, causal):
     out, lse = p.forward(causal)
     p.check(out, lse, causal)
     p.check_gradients(out, lse, p.backward(out, lse, causal), causal)
+
+
+PARTS = [
+    # lens, Hq, Hk, d, of the forward: items, slots, causal or not
+    ([1500] + [9] * 30, 21, 3, 64),     # seven heads; 72 items for 107 slots
+    ([3000] + [20] * 25, 12, 4, 64),    # 61 for 80
+    ([1600] + [5] * 60, 8, 8, 128),     # 67 for 40
+    ([1091] + [13] * 5, 1, 1, 64),      # 10 for 126: parts are as short as they may be
+    # of the backward
+    ([2560] + [30] * 20, 32, 8, 64),    # 40 items for 64 slots
+    ([2000] + [3] * 60, 28, 4, 128),    # seven heads; 76 for 128
+    ([773], 2, 1, 128),                 # 7 for 28
+]
+
+
+class Guarded:
+    """A workspace of exactly the stated size between two guards."""
+
+    def __init__(self, need):
+        self.all = torch.full((need + 3 * 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+        self.at = 4096 + -self.all.data_ptr() % 256
+        self.need = need
+        self.ws = self.all[self.at:self.at + need]
+
+    def kept(self):
+        return bool((self.all[:self.at] == 0xA5).all()
+                    and (self.all[self.at + self.need:] == 0xA5).all())
+
+
+def test_parts_take_every_branch_of_the_plan():
+    for which in ("fwd", "bwd"):
+        reached = set()
+        for lens, Hq, Hk, d in PARTS:
+            for causal in (True, False):
+                slots, items, streamed, chunk, bound = packed_plan.cut(
+                    which, lens, sum(lens) + 3, Hq, Hk, causal, torch.cuda.get_device_properties(
+                        0).multi_processor_count)
+                if chunk and packed_plan.parts(streamed, chunk):
+                    reached.add(2 * items < slots)
+        assert reached == {True, False}
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,Hq,Hk,d", PARTS)
+def test_parts_stay_in_the_workspace(lens, Hq, Hk, d, causal):
+    p = Prompts(lens, Hq, Hk, d, seed=24, pad=3)
+    args = (p.T, len(lens), Hq, Hk, d)
+    fwd, bwd = (Guarded(f(*args)) for f in (pkg.cp_packed_attn_fwd_workspace_bytes,
+                                            pkg.cp_packed_attn_bwd_workspace_bytes))
+    out, lse = p.forward(causal, workspace=fwd.ws)
+    assert fwd.kept()
+    p.check(out, lse, causal)
+    grads = p.backward(out, lse, causal, workspace=bwd.ws)
+    assert bwd.kept()
+    p.check_gradients(out, lse, grads, causal)
+
+
+def test_parts_as_long_as_the_bound_has_them():
+    """So much is streamed for so many items that the bound on the parts' number, not a block's
+    share, sets their length."""
+    lens, Hq, Hk, d = [10603, 10065, 7897] + [13] * 150, 1, 1, 64
+    _, _, streamed, chunk, bound = packed_plan.cut("fwd", lens, sum(lens) + 3, Hq, Hk, False)
+    assert bound and packed_plan.parts(streamed, chunk) > 200
+    p = Prompts(lens, Hq, Hk, d, seed=25, pad=3)
+    fwd = Guarded(pkg.cp_packed_attn_fwd_workspace_bytes(p.T, len(lens), Hq, Hk, d))
+    out, lse = p.forward(False, workspace=fwd.ws)
+    assert fwd.kept()
+    p.check(out, lse, False)

@@ -9,6 +9,7 @@ import torch
 
 import context_ring_attention_fwd_gb300 as pkg
 from oracle import packed, ref
+import packed_plan
 
 V = ctypes.c_void_p
 FAKE, ODD = V(0x10000), V(0x10002)
@@ -150,6 +151,39 @@ def test_no_workspace_for_parts_where_nothing_is_cut():
     assert bwd(2000, 1, 2, 1, 128) > 1 << 20   # where tiles are cut there is
     # the forward's, with two slots a key head
     assert pkg.cp_packed_attn_fwd_workspace_bytes(1200, 1, 170, 170, 128) <= 1 << 16
+
+
+@pytest.mark.parametrize("which", ["fwd", "bwd"])
+def test_the_plan_cuts_no_more_parts_than_there_are_slots(which):
+    """By the plan's own rule, over random calls.  (The kernel sums its estimate of the streamed
+    tiles in fp32: at most 2^10 terms to a thread and 2^5 + 5 additions behind them, each off by
+    2^-24, and a term by a few: below 2^-13, where the rule adds 2^-10.)"""
+    rng = np.random.default_rng(30)
+    cut_calls = fullest = 0
+    reached = set()
+    for _ in range(4000):
+        Hk = int(rng.choice([1, 2, 3, 4, 5, 8, 16, 24, 100]))
+        Hq = Hk * int(rng.choice([1, 2, 3, 4, 7, 8, 16, 64, 128]))
+        lens = np.concatenate([rng.integers(0, int(10 ** rng.uniform(1, 4.5)), rng.integers(1, 6)),
+                               rng.integers(0, 40, rng.choice([0, 0, 5, 60, 400]))])
+        T = int(lens.sum()) + int(rng.choice([0, 5, 3000]))
+        if T == 0:
+            continue
+        causal = bool(rng.integers(2))
+        slots, items, streamed, chunk, bound = packed_plan.cut(which, lens, T, Hq, Hk, causal)
+        if chunk is None:
+            continue
+        n = packed_plan.parts(streamed, chunk)
+        assert n <= slots, (lens, T, Hq, Hk, causal)
+        if n:
+            cut_calls += 1
+            fullest = max(fullest, n / slots)
+            reached.add((2 * items < slots, bound))
+    assert cut_calls > 150 and fullest > 0.6
+    # few items for the slots and many, the share and the bound (a backward of many items has
+    # a share above its bound: 0.6 / 152 of what is streamed, the bound 2 / 512)
+    want = {(True, True), (True, False), (False, False)} | ({(False, True)} if which == "fwd" else set())
+    assert want <= reached
 
 
 def test_host_tensors_are_refused():
