@@ -160,7 +160,7 @@ __device__ __forceinline__ int claimed_index(unsigned long long v, uint32_t epoc
 }
 
 // The k-th item of CTA c of G, given its latest claim; and, once that item is known,
-// the claim of its next one.
+// the claim of its next one.  (For the kernels that run with a counter and without.)
 template <class P>
 __device__ __forceinline__ int item_at(const P& p, int k, int c, int G, unsigned long long ahead) {
   if (k == 0 || p.work_slot == nullptr) return item_of(k, c, G);
@@ -300,14 +300,21 @@ uint32_t next_epoch(unsigned long long* slots) {
   return e;
 }
 
+cudaError_t is_captured(cudaStream_t stream, bool& captured) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(stream, &status);
+  captured = status != cudaStreamCaptureStatusNone;
+  return e;
+}
+
 // The claim counter of a launch on `stream` and the launch's tag; none in a capture.
 template <class P>
 cudaError_t take_counter(P& p, cudaStream_t stream) {
-  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
-  const cudaError_t e = cudaStreamIsCapturing(stream, &status);
+  bool captured;
+  const cudaError_t e = is_captured(stream, captured);
   if (e != cudaSuccess) return e;
   p.work_slot = nullptr;
-  if (status != cudaStreamCaptureStatusNone) return cudaSuccess;
+  if (captured) return cudaSuccess;
   unsigned long long* const slots = work_slots_address();
   if (!slots) return cudaErrorInvalidValue;
   p.epoch = next_epoch(slots);

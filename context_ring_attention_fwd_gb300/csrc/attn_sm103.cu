@@ -353,13 +353,14 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tmap_q, const CUten
       bool dropped = false;
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        const int w = kDynamic ? item_at(p, k, c, G, ahead) : item_of(k, c, G);
+        const int w = !kDynamic ? item_of(k, c, G)
+                      : (k == 0) ? c : G + claimed_index(ahead, p.epoch, p.err);
         if constexpr (kDynamic) {
           if (!ring_put(ring, static_cast<uint32_t>(k), w, abort_flag, p)) { ok = false; break; }
         }
         if (w >= p.n_items) break;
         if constexpr (kDynamic)  // claim the CTA's next item now; it is read when that item starts
-          ahead = claim_ahead(p, k);
+          ahead = (k == 0) ? claim_first(p.work_slot, p.epoch) : claim_next(p.work_slot);
         Item it;
         decode_item(p, n_docs, w, it);
         if (it.F_lo > it.F_hi) continue;
@@ -1467,19 +1468,24 @@ cudaError_t launch_attn_bf16(const AttnArgs& a, cudaStream_t stream) {
   // and one step's launch.  A launch without documents over whole key ranges
   // (all ranks, or one rank's query shard) takes the fixed snake deal, which
   // measured faster there (81.4 against 85.7 ms for all ranks at 128K, and
-  // 87.2 against 89.5 ms for the four rank launches of the same shape).
-  const bool dynamic = CPRING_DYNAMIC_ALWAYS || a.doc_offsets != nullptr ||
-                       (CPRING_RANK_DYNAMIC && a.q_shard >= 0) || partial;
-  if (a.d == 128) {
-    if (partial) return launch_t<128, true, false, true>(a, stream);
-    return dynamic ? launch_t<128, false, false, true>(a, stream)
-                   : launch_t<128, false, false, false>(a, stream);
-  }
-  if (a.d == 64) {
-    if (partial) return launch_t<64, true, false, true>(a, stream);
-    return dynamic ? launch_t<64, false, false, true>(a, stream)
-                   : launch_t<64, false, false, false>(a, stream);
-  }
+  // 87.2 against 89.5 ms for the four rank launches of the same shape).  So does
+  // every captured launch, which has no counter; by a kernel of its own, since a test for
+  // the counter in the claiming one cost a step's launch 1 % (8K, 16 heads).
+  bool captured;
+  const cudaError_t e = is_captured(stream, captured);
+  if (e != cudaSuccess) return e;
+  const bool dynamic = !captured && (CPRING_DYNAMIC_ALWAYS || a.doc_offsets != nullptr ||
+                                     (CPRING_RANK_DYNAMIC && a.q_shard >= 0) || partial);
+  auto launch = [&](auto dim) {
+    constexpr int kD = decltype(dim)::value;
+    if (partial)
+      return dynamic ? launch_t<kD, true, false, true>(a, stream)
+                     : launch_t<kD, true, false, false>(a, stream);
+    return dynamic ? launch_t<kD, false, false, true>(a, stream)
+                   : launch_t<kD, false, false, false>(a, stream);
+  };
+  if (a.d == 128) return launch(std::integral_constant<int, 128>());
+  if (a.d == 64) return launch(std::integral_constant<int, 64>());
   return cudaErrorInvalidValue;
 }
 
