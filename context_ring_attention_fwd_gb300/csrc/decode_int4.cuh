@@ -19,7 +19,7 @@
 //    lane: movmatrix turns its 8 x 8 pieces.
 //  - A row's reference moves only when a score passes it by 2^5 (all but a few of the first tiles
 //    of an item go without the maximum's shuffles), and V is read while the softmax waits.
-// 660 instructions for 32 keys and 8 rows; issue slots are 63 % used in the long case, where the
+// 660 instructions for 32 keys and 8 rows; issue slots are 66 % used in the long case, where the
 // whole call runs at 76 % of the copy rate (paged_decode.cu).
 #pragma once
 

@@ -11,7 +11,10 @@
 //          (packed.cuh) that see it: G heads' rows are neighbours in the products' inner
 //          dimension, so a shared head's gradients are summed in the accumulators.
 //   kDQ    a CTA owns a packed query tile and walks the key tiles it sees.
-// Every output is finished by one CTA: no atomics.
+// No gradient is summed by atomics.  A CTA that has all of a tile stores its gradients.  Key
+// tiles of many queries may be cut into parts (packed_plan.cu): each leaves its fp32 sums of dV and
+// dK in a slot (1024 d bytes, written and read again), counts itself by an atomic, and the last to
+// end adds the tile's slots up in the parts' order.
 //
 // The seven products of a tile pair (two of them twice) are 7 / 5 of the formulas' operations:
 // one kernel for all five would add dQ up over CTAs, by atomics in the order of arrival or through
@@ -22,7 +25,7 @@
 // kernels): kDKDV 1450 us, 67 % of the tensor pipe, kDQ 970, 73 %; with S^T and dP^T in halves of
 // 64 queries, two in flight, kDKDV took 1830, and with constants read by generic loads 1570.
 // P and dS are rounded to bf16 for their products, as the ring's backward rounds them: 2.5e-3 to
-// 3.0e-3 of the gradients against 64 bits (relative in the norm), 1.7e-3 of it the outputs' own.
+// 3.0e-3 of the gradients against 64 bits (relative in the norm), 1.65e-3 of it the outputs' own.
 //
 // Rows that are not there (behind a sequence, behind tq G) may hold anything.  Where they are
 // summed over - Q and dO in kDKDV, K in kDQ - they are zeroed in shared memory up to the next
@@ -233,7 +236,7 @@ __device__ __forceinline__ void store_float(uint32_t at, float x) {
 }
 
 // 32 bytes of a row, whole sectors where the outputs lie so.  (Measured, in two halves of 16 /
-// whole, us a call: 14 prompts of up to 2000 tokens, 32/8 heads, 288 / 279; 6 of up to 200, 16/4,
+// whole, us a call: 10 prompts of up to 2000 tokens, 32/8 heads, 288 / 279; 6 of up to 200, 16/4,
 // 26.3 / 25.1.  Wider rows by way of shared memory would need some, and there is none left.)
 __device__ __forceinline__ void store_32(uint4* to, const uint32_t (&w)[8], bool wide) {
   if (wide) {

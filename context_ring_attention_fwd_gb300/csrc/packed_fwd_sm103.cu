@@ -22,7 +22,7 @@
 // last two PVs, which the drain would hide, made the MMA warp's loop slower: 110 us there, 1280 for
 // the 32K.)  P is rounded to bf16 for its product, as in the ring's forward, which costs about as
 // much as the output's own rounding (2.0e-3 to 2.2e-3 against 64 bits, relative in the norm, where
-// that alone makes 1.7e-3).
+// that alone makes 1.65e-3).
 //
 // Items that see many keys in a call of few are cut along them (packed_plan.cu): a part leaves its
 // (O, m, l) in a slot, and the last to end of a query tile's parts joins them by the online

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   // 25, which stays whole.
   // Key tiles that are no more than the CTAs are cut down to 0.45 of the share: so / to 0.6, 8192
   // tokens of 8/2 heads 331 / 377, 5000 + 2500 of 16/2 329 / 359.  More of them balance
-  // themselves: 9000 of 4/4 (d = 64) 183 / 177, 3000 + 200 + 100 of 32/8 222 / 215, 14 prompts of
+  // themselves: 9000 of 4/4 (d = 64) 183 / 177, 3000 + 200 + 100 of 32/8 222 / 215, 10 prompts of
   // 32/8 281 / 278.  (Nor does the forward gain: 20000 of 1/1, d = 64, 82 / 78.)
   int chunk = INT_MAX;
   auto parts_of = [&](const int4& it) {

@@ -403,8 +403,8 @@ void cp_launch_counts(int64_t* counts4);
  * dK/dV kernel (one CTA per 128-key tile) on `stream`, and the dQ kernel (one
  * CTA per 128-query tile), which reads nothing the dK/dV kernel writes, on a
  * second stream owned by the library (one per device, kept for the
- * process's life) after D; `stream` then waits for it, so work enqueued
- * later on `stream` sees every gradient.  Both kernels run on tcgen05 with
+ * process's life; in a capture, as a branch of its graph) after D; `stream`
+ * then waits for it, so work enqueued later on `stream` sees every gradient.  Both kernels run on tcgen05 with
  * fp32 accumulation and bf16 P / dS operands.
  */
 int64_t cp_ring_attn_bwd_workspace_bytes(int B, int S, int H, int d, int n_shards);
@@ -553,12 +553,15 @@ typedef struct cp_paged_cache {
  * A cache in 4 bits.  A row (one head of one token) is d / 2 bytes of codes, entry i
  * in byte i / 2 (the low half for even i), and d / 16 scales:
  *   value[i] = (code[i] - 8) * scale[i / 16] * descale[head],  code in 0 .. 15.
- * k_strides and v_strides are in bytes, each a multiple of 16.  A row x is written as
+ * k_strides and v_strides are in bytes, each a multiple of 16; a head's rows of a page
+ * are read fastest where they lie side by side (16 sequences of 32K tokens, 8 key heads:
+ * 119 us, and 232 where a token's heads do).  A row x is written as
  *   y = x * (1 / descale[head]);  scale = E4M3(max |y| over its 16 entries * (1 / 7));
  *   code = round(y / scale) clamped to +-7, plus 8
  * (each an fp32 operation rounded to nearest, ties to even; scale saturated at 448,
  * and where it is 0 the code is 8), so that while max |y| < 3328 an entry y is off by
- * scale / 2 or, where that is more, 7 / 1024.  A NaN makes its 16 entries NaN.
+ * scale / 2 or, where that is more, 7 / 1024; beyond, entries are cut off at 3136.  A
+ * NaN makes its 16 entries NaN.
  */
 
 /*
@@ -595,7 +598,9 @@ cp_status cp_paged_append(const cp_paged_cache* cache, const void* q, const int6
  * Decode attention over a paged cache for a batch whose sequences share a
  * prefix, which is attended once for the whole batch: every sequence's
  * partial state over the prefix and over its own keys are joined by the
- * online merge of cp_lse_merge ("上下文並行", section 線上 Softmax).
+ * online merge of cp_lse_merge ("上下文並行", section 線上 Softmax).  (A prefix is read
+ * once for every 256 rows, n_q (Hq / Hk) of each sequence, or, where those are few or the
+ * cache is in 4 bits, for every 16.)
  * Sequence b has seq_lens[b] tokens in the cache, the n_q last of them its
  * queries: query i is at position seq_lens[b] - n_q + i.  It sees the keys of
  * positions [0, prefix_len), read through prefix_pages, and those of positions
@@ -618,6 +623,8 @@ cp_status cp_paged_append(const cp_paged_cache* cache, const void* q, const int6
  *             256-byte aligned, caller-owned, contents undefined afterwards
  *             (calls that can overlap, two captured graphs' among them, need
  *             one each); too small: CP_ERR_BUFFER.
+ * Over 8 and 4 bits a key's weight in a row is held in 16 bits relative to the row's
+ * largest: one below 2^-34 of it may count as 0.
  * Rows that see no key (an unused batch row, a query before its sequence's
  * start) get out = 0, lse = -inf.  What the cache holds in slots that no query
  * sees is never used, whatever it is.  A sequence with a length outside its
@@ -661,9 +668,10 @@ cp_status cp_paged_attn_decode(const cp_paged_cache* cache, const void* q,
  *  workspace  device, >= cp_packed_attn_fwd_workspace_bytes(...) bytes, 256-byte aligned,
  *             caller-owned, contents undefined afterwards (calls that can overlap, two
  *             captured graphs' among them, need one each); too small: CP_ERR_BUFFER.
- * One launch, or two (a plan of the work first, where there are more tiles than
- * multiprocessors); nothing is allocated, and the lengths are read on the device, so a
- * captured call follows them when it is replayed.
+ * One launch where T <= 1024 and the items that there may be, (T / (2 floor(128 / (Hq /
+ * Hk))) + n_seqs) * Hk, are no more than the multiprocessors; otherwise two, a plan of the
+ * work first.  Nothing is allocated, and the lengths are read on the device, so a captured
+ * call follows them when it is replayed.
  */
 int64_t cp_packed_attn_fwd_workspace_bytes(int T, int n_seqs, int Hq, int Hk, int d);
 cp_status cp_packed_attn_fwd(const void* q, const int64_t* q_strides, const void* k,
@@ -701,7 +709,8 @@ cp_status cp_packed_attn_bwd(const void* q, const int64_t* q_strides, const void
 /*
  * TEST HOOK.  Later cp_paged_attn_decode calls (and their workspace sizes)
  * attend the prefix with the 16-row items of the decode kernel (path 0) or with
- * the tcgen05 kernel (path 1), whatever their sizes; -1 returns to the rule.
+ * the tcgen05 kernel (path 1), whatever their sizes; -1 returns to the rule.  A cache
+ * in 4 bits has the first path only, and ignores this.
  * Process-wide; for tests only.
  */
 void cp_test_set_prefix_path(int path);
