@@ -263,10 +263,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // dw[tensor][column] = sum over blocks, 32 columns a block of this kernel,
-// 32 threads a column; the order is fixed by the block count alone.
+// 32 threads a column; the order is fixed by the block count alone.  (The sums are
+// written while this kernel waits: no __restrict__, which with const would promise that
+// they do not change, and let their loads go before the wait.)
 __global__ void __launch_bounds__(1024)
-    gain_grad_kernel(const float* __restrict__ partial, int blocks, int d, float* dqw,
-                     float* dkw) {
+    gain_grad_kernel(const float* partial, int blocks, int d, float* dqw, float* dkw) {
   __shared__ float part[32][33];
   cudaGridDependencySynchronize();
   const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 d

@@ -285,3 +285,37 @@ def test_cosines_and_sines_are_those_of_the_exact_angle(il):
     c, s = (y[:, 0], y[:, 1]) if il else (y[:, 0], y[:, d // 2])
     assert np.abs(c - np.array([1, 0, -1, 0, 1, 0, -1, 0, 1])).max() <= 2e-7
     assert np.abs(s - np.array([0, 1, 0, -1, 0, 1, 0, -1, 0])).max() <= 2e-7
+
+
+@pytest.mark.parametrize("S,Hq,Hk,d", [(64, 8, 2, 128), (1500, 16, 4, 64)])
+def test_calls_in_a_row_share_a_workspace(S, Hq, Hk, d):
+    """The gains' gradients are summed from the workspace that the call before used: each is of its
+    own inputs, in single calls and in replays."""
+    f = freqs(d).to(DEV)
+    need = pkg.cp_qk_norm_rope_bwd_workspace_bytes(1, S, Hq, Hk, d)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    sets, outs, want = [], [], []
+    for seed in range(8):
+        q, k, qw, kw, g = make(1, S, Hq, Hk, d, torch.bfloat16, 100 + seed)
+        dqo, dko = (torch.randn(t.shape, generator=g).to(t.dtype).to(DEV) for t in (q, k))
+        sets.append((dqo, dko, q.contiguous(), k.contiguous(), qw, kw, f, None))
+        outs.append([torch.empty_like(dqo), torch.empty_like(dko)]
+                    + [torch.empty(d, device=DEV) for _ in range(2)])
+        pkg.cp_qk_norm_rope_bwd(*sets[-1], *outs[-1], workspace=ws)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs[-1]])
+
+    def all_of_them():
+        for s, o in zip(sets, outs):
+            pkg.cp_qk_norm_rope_bwd(*s, *o, workspace=ws)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        all_of_them()
+    for once in [all_of_them] * 20 + [graph.replay] * 20:
+        for o in outs:
+            for t in o:
+                t.zero_()
+        once()
+        for o, x in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, x))
