@@ -7,10 +7,9 @@
 // capture ends.
 #include <cuda_runtime_api.h>
 
-#include <algorithm>
 #include <mutex>
-#include <new>
 
+#include "capture.h"
 #include "internal.h"
 
 namespace cpring {
@@ -32,37 +31,6 @@ cudaStream_t side_stream() {
   return b.s;
 }
 
-// What the stream's next launch would depend on.
-struct Tail {
-  cudaGraphNode_t* nodes = nullptr;
-  cudaGraphEdgeData* edges = nullptr;
-  size_t count = 0;
-  Tail() = default;
-  Tail(const Tail&) = delete;
-  Tail& operator=(const Tail&) = delete;
-  ~Tail() {
-    delete[] nodes;
-    delete[] edges;
-  }
-  cudaError_t read(cudaStream_t stream) {
-    cudaStreamCaptureStatus status;
-    const cudaGraphNode_t* n = nullptr;
-    const cudaGraphEdgeData* e = nullptr;
-    const cudaError_t err =
-        cudaStreamGetCaptureInfo(stream, &status, nullptr, nullptr, &n, &e, &count);
-    if (err != cudaSuccess) return err;
-    nodes = new (std::nothrow) cudaGraphNode_t[count + 1];
-    edges = new (std::nothrow) cudaGraphEdgeData[count + 1]();
-    if (!nodes || !edges) return cudaErrorMemoryAllocation;
-    std::copy(n, n + count, nodes);
-    if (e) std::copy(e, e + count, edges);
-    return cudaSuccess;
-  }
-  cudaError_t put(cudaStream_t stream, unsigned flags) {
-    return cudaStreamUpdateCaptureDependencies(stream, nodes, edges, count, flags);
-  }
-};
-
 }  // namespace
 
 cudaError_t launch_beside(cudaStream_t stream, LaunchFn first, void* what1, LaunchFn second,
@@ -71,7 +39,7 @@ cudaError_t launch_beside(cudaStream_t stream, LaunchFn first, void* what1, Laun
   cudaError_t e = cudaStreamIsCapturing(stream, &status);
   if (e != cudaSuccess) return e;
   if (status != cudaStreamCaptureStatusNone) {
-    Tail before, after;
+    CaptureTail before, after;
     if ((e = before.read(stream)) != cudaSuccess) return e;
     if ((e = first(what1, stream)) != cudaSuccess) return e;
     if ((e = after.read(stream)) != cudaSuccess) return e;

@@ -16,13 +16,15 @@
 // (one set per device, created on first use and kept for the process's
 // life); a per-device lock is held while a call enqueues its work, so host
 // threads take turns.  The caller's stream ends up waiting for every copy,
-// so synchronising it means the host outputs are complete.
+// so synchronising it means the host outputs are complete.  A captured call
+// takes neither: its copies are branches of the graph (capture.h).
 #include <cuda_runtime_api.h>
 
 #include <mutex>
 #include <optional>
 #include <vector>
 
+#include "capture.h"
 #include "internal.h"
 
 namespace cpring {
@@ -78,6 +80,47 @@ bool ensure_resources(HostPathDevice& h, int n_events) {
   return true;
 }
 
+// The three lines of work of a call, each in its own order, and the marks that
+// order them: streams and events, or in a capture branches of the graph.
+class Lanes {
+ public:
+  enum Lane { kIn, kCompute, kOut };
+  Lanes(HostPathDevice& h, cudaStream_t stream, bool captured, int marks)
+      : h_(h), stream_(stream), captured_(captured), marks_(captured ? marks : 0) {}
+  // The stream that takes the lane's next work.
+  cudaStream_t on(Lane lane) {
+    if (!captured_) return lane == kIn ? h_.h2d : lane == kOut ? h_.d2h : stream_;
+    if (lane != now_) {
+      check(tails_[now_].read(stream_));
+      check(tails_[lane].put(stream_, cudaStreamSetCaptureDependencies));
+      now_ = lane;
+    }
+    return stream_;
+  }
+  void mark(Lane lane, int i) {
+    const cudaStream_t s = on(lane);
+    check(captured_ ? marks_[i].read(s) : cudaEventRecord(h_.events[i], s));
+  }
+  void wait(Lane lane, int i) {
+    const cudaStream_t s = on(lane);
+    check(captured_ ? marks_[i].put(s, cudaStreamAddCaptureDependencies)
+                    : cudaStreamWaitEvent(s, h_.events[i], 0));
+  }
+  void check(cudaError_t e) {
+    if (err_ == cudaSuccess && e != cudaSuccess) err_ = e;
+  }
+  bool ok() const { return err_ == cudaSuccess; }
+
+ private:
+  HostPathDevice& h_;
+  const cudaStream_t stream_;
+  const bool captured_;
+  std::vector<CaptureTail> marks_;
+  CaptureTail tails_[3];
+  Lane now_ = kCompute;
+  cudaError_t err_ = cudaSuccess;
+};
+
 cp_status host_forward(const void* q_host, const void* k_host, const void* v_host, void* out_host,
                        float* lse_host, int B, int S, int H, int d, int n_shards, int causal,
                        const int32_t* doc_offsets, void* workspace, int64_t workspace_bytes,
@@ -96,12 +139,17 @@ cp_status host_forward(const void* q_host, const void* k_host, const void* v_hos
   const int N = n_shards;
   HostPathDevice* hp = host_path_device();
   if (!hp) return CP_ERR_CUDA;
-  std::lock_guard<std::mutex> lock(hp->mu);
-  if (!ensure_resources(*hp, 2 * N + 2)) return CP_ERR_CUDA;
-  cudaEvent_t ev_start = hp->events[0];
-  cudaEvent_t ev_end = hp->events[1];
-  cudaEvent_t* landed = hp->events.data() + 2;
-  cudaEvent_t* done = hp->events.data() + 2 + N;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &status) != cudaSuccess) return CP_ERR_CUDA;
+  const bool captured = status != cudaStreamCaptureStatusNone;
+  std::unique_lock<std::mutex> lock(hp->mu, std::defer_lock);
+  if (!captured) {
+    lock.lock();
+    if (!ensure_resources(*hp, 2 * N + 2)) return CP_ERR_CUDA;
+  }
+  Lanes lanes(*hp, stream, captured, 2 * N + 2);
+  constexpr int kStart = 0, kEnd = 1, kLanded = 2;  // marks; + shard
+  const int kDone = 2 + N;                          // + rank
 
   char* ws = static_cast<char*>(workspace);
   char* qd = ws;
@@ -118,39 +166,36 @@ cp_status host_forward(const void* q_host, const void* k_host, const void* v_hos
            static_cast<size_t>(i) * shard_bytes;
   };
 
-  cudaError_t err = cudaSuccess;
-  auto chk = [&](cudaError_t e) {
-    if (err == cudaSuccess && e != cudaSuccess) err = e;
-  };
   // Everything the caller enqueued before (including an earlier call's
   // kernels on these device buffers) comes first.
-  chk(cudaEventRecord(ev_start, stream));
-  chk(cudaStreamWaitEvent(hp->h2d, ev_start, 0));
+  lanes.mark(Lanes::kCompute, kStart);
+  lanes.wait(Lanes::kIn, kStart);
 
   // Documents: the doc-scan word and each rank's slot order live in the
   // library's cached scratch for the rest of the call.
   std::optional<ScratchLease> lease;
   int32_t* info = nullptr;
   if (doc_offsets) {
-    lease.emplace(doc_scratch_bytes(S, N, 0, !f32), stream);
+    lease.emplace(doc_scratch_bytes(S, N, 0, !f32), lanes.on(Lanes::kCompute));
     if (!lease->ok()) return CP_ERR_CUDA;
     info = static_cast<int32_t*>(lease->get());
-    chk(launch_doc_scan(doc_offsets, S, info, stream));
+    lanes.check(launch_doc_scan(doc_offsets, S, info, stream));
   }
 
   // shard i of Q, K, V to the device, in rank order
-  for (int i = 0; i < N && err == cudaSuccess; ++i) {
+  for (int i = 0; i < N && lanes.ok(); ++i) {
+    const cudaStream_t in = lanes.on(Lanes::kIn);
     for (int b = 0; b < B; ++b) {
       const size_t off = static_cast<size_t>(b) * seq_bytes + static_cast<size_t>(i) * shard_bytes;
-      chk(cudaMemcpyAsync(qd + off, at(q_host, b, i), shard_bytes, cudaMemcpyHostToDevice, hp->h2d));
-      chk(cudaMemcpyAsync(kd + off, at(k_host, b, i), shard_bytes, cudaMemcpyHostToDevice, hp->h2d));
-      chk(cudaMemcpyAsync(vd + off, at(v_host, b, i), shard_bytes, cudaMemcpyHostToDevice, hp->h2d));
+      lanes.check(cudaMemcpyAsync(qd + off, at(q_host, b, i), shard_bytes, cudaMemcpyHostToDevice, in));
+      lanes.check(cudaMemcpyAsync(kd + off, at(k_host, b, i), shard_bytes, cudaMemcpyHostToDevice, in));
+      lanes.check(cudaMemcpyAsync(vd + off, at(v_host, b, i), shard_bytes, cudaMemcpyHostToDevice, in));
     }
-    chk(cudaEventRecord(landed[i], hp->h2d));
+    lanes.mark(Lanes::kIn, kLanded + i);
   }
   // rank i once the shards it reads have landed; its rows go back at once
-  for (int i = 0; i < N && err == cudaSuccess; ++i) {
-    chk(cudaStreamWaitEvent(stream, landed[causal ? i : N - 1], 0));
+  for (int i = 0; i < N && lanes.ok(); ++i) {
+    lanes.wait(Lanes::kCompute, kLanded + (causal ? i : N - 1));
     AttnArgs a{};
     a.q = qd; a.k = kd; a.v = vd;
     a.B = B; a.S = S; a.H = H; a.d = d; a.n_shards = N;
@@ -160,24 +205,25 @@ cp_status host_forward(const void* q_host, const void* k_host, const void* v_hos
     a.doc_info = info;
     a.slot_perm = (info && !f32) ? info + 4 : nullptr;
     a.out = od; a.lse = ld;
-    chk(f32 ? launch_attn_f32(a, stream) : launch_attn_bf16(a, stream));
-    chk(cudaEventRecord(done[i], stream));
-    chk(cudaStreamWaitEvent(hp->d2h, done[i], 0));
+    lanes.check(f32 ? launch_attn_f32(a, stream) : launch_attn_bf16(a, stream));
+    lanes.mark(Lanes::kCompute, kDone + i);
+    lanes.wait(Lanes::kOut, kDone + i);
+    const cudaStream_t back = lanes.on(Lanes::kOut);
     for (int b = 0; b < B; ++b) {
       const size_t off = static_cast<size_t>(b) * seq_bytes + static_cast<size_t>(i) * shard_bytes;
-      chk(cudaMemcpyAsync(static_cast<char*>(out_host) + off, od + off, shard_bytes,
-                          cudaMemcpyDeviceToHost, hp->d2h));
+      lanes.check(cudaMemcpyAsync(static_cast<char*>(out_host) + off, od + off, shard_bytes,
+                                  cudaMemcpyDeviceToHost, back));
     }
     // lse [B, H, S]: rank i's L entries of each of the B*H rows
-    chk(cudaMemcpy2DAsync(lse_host + static_cast<size_t>(i) * L, static_cast<size_t>(S) * 4,
-                          ld + static_cast<size_t>(i) * L, static_cast<size_t>(S) * 4,
-                          static_cast<size_t>(L) * 4, static_cast<size_t>(B) * H,
-                          cudaMemcpyDeviceToHost, hp->d2h));
+    lanes.check(cudaMemcpy2DAsync(lse_host + static_cast<size_t>(i) * L, static_cast<size_t>(S) * 4,
+                                  ld + static_cast<size_t>(i) * L, static_cast<size_t>(S) * 4,
+                                  static_cast<size_t>(L) * 4, static_cast<size_t>(B) * H,
+                                  cudaMemcpyDeviceToHost, back));
   }
   // the caller's stream waits for the last copy back
-  chk(cudaEventRecord(ev_end, hp->d2h));
-  chk(cudaStreamWaitEvent(stream, ev_end, 0));
-  return err == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+  lanes.mark(Lanes::kOut, kEnd);
+  lanes.wait(Lanes::kCompute, kEnd);
+  return lanes.ok() ? CP_OK : CP_ERR_CUDA;
 }
 
 }  // namespace

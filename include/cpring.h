@@ -180,7 +180,8 @@ cp_status cp_ring_attn_fwd_noalloc(const void* q, const void* k, const void* v, 
  *  CP_ERR_BUFFER.  With doc_offsets the call uses the cached scratch that
  *  cp_ring_attn_fwd uses.  The copy streams and their events are created on
  *  the first call on each device and kept; a per-device lock is held while a
- *  call enqueues, so concurrent host threads take turns.
+ *  call enqueues, so concurrent host threads take turns.  In a captured call the
+ *  copies are branches of its graph.
  */
 int64_t cp_ring_attn_fwd_host_workspace_bytes(int B, int S, int H, int d, int n_shards,
                                               int elem_bytes /* 2 bf16, 4 fp32 */);

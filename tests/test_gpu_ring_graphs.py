@@ -211,3 +211,47 @@ def test_calls_with_documents_after_a_capture():
         t.fill_(7)
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("docs", [None, DOCS])
+def test_a_host_call_while_another_is_being_captured(docs):
+    """The call from host buffers captured on one stream, and made on another while that capture is
+    open: both give the single call's result, and the other stream is not drawn into the capture."""
+    d, N = 64, 4
+    x = [t.cpu().pin_memory() for t in rows(9, d, 3)]
+    need = pkg.lib().cp_ring_attn_fwd_host_workspace_bytes(B, S, H, d, N, 2)
+    docs_t = None if docs is None else offsets(docs)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+
+    def buffers():
+        return (torch.empty(need, dtype=torch.uint8, device=DEV),
+                torch.zeros((B, S, H, d), dtype=BF16).pin_memory(),
+                torch.zeros((B, H, S)).pin_memory())
+
+    def call(ws, out, lse, stream):
+        return pkg.lib().cp_ring_attn_fwd_host(*(p(t) for t in x), p(out), p(lse), B, S, H, d, N, 1,
+                                               None if docs is None else p(docs_t), p(ws), need,
+                                               ctypes.c_void_p(stream.cuda_stream))
+
+    single, caught, beside = buffers(), buffers(), buffers()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    assert call(*single, s1) == 0
+    s1.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s1):
+        graph.capture_begin(capture_error_mode="thread_local")
+        captured_status = call(*caught, s1)
+        status = call(*beside, s2)
+        graph.capture_end()
+    assert captured_status == 0 and status == 0
+    s2.synchronize()
+    for a, b in zip(beside[1:], single[1:]):
+        assert torch.equal(a, b)
+    assert not caught[1].any()
+    with torch.cuda.stream(s1):
+        for _ in range(2):
+            caught[1].zero_()
+            graph.replay()
+            s1.synchronize()
+            for a, b in zip(caught[1:], single[1:]):
+                assert torch.equal(a, b)
