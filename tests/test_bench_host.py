@@ -89,3 +89,17 @@ def test_recorded_traffic_holds_only_for_its_kernel_sources(monkeypatch):
     real = bench.kernel_sources_digest()
     assert len(real) == 16 and real != bench.kernel_sources_digest(bench.BWD_KERNEL_SOURCES)
 
+
+
+def test_the_recorded_traffics_digest_covers_the_headers_of_the_kernels():
+    """What a kernel's source includes of device code is among the files that its figure holds for."""
+    import re
+    csrc = "context_ring_attention_fwd_gb300/csrc/"
+
+    def headers(rel):
+        with open(os.path.join(ROOT, rel)) as f:
+            found = {csrc + h for h in re.findall(r'#include "([a-z0-9_]+\.cuh)"', f.read())}
+        return found.union(*(headers(h) for h in found))
+
+    for files in (bench.KERNEL_SOURCES, bench.BWD_KERNEL_SOURCES):
+        assert files[0].endswith(".cu") and headers(files[0]) == set(files[1:])
