@@ -405,8 +405,8 @@ void cp_launch_counts(int64_t* counts4);
  * CTA per 128-query tile), which reads nothing the dK/dV kernel writes, on a
  * second stream owned by the library (one per device, kept for the
  * process's life; in a capture, as a branch of its graph) after D; `stream`
- * then waits for it, so work enqueued later on `stream` sees every gradient.  Both kernels run on tcgen05 with
- * fp32 accumulation and bf16 P / dS operands.
+ * then waits for it, so work enqueued later on `stream` sees every gradient.
+ * Both kernels run on tcgen05 with fp32 accumulation and bf16 P / dS operands.
  */
 int64_t cp_ring_attn_bwd_workspace_bytes(int B, int S, int H, int d, int n_shards);
 cp_status cp_ring_attn_bwd(const void* q, const void* k, const void* v, const void* out,
